@@ -48,7 +48,10 @@
  *     synchronises its stream and is not capturable.
  *
  * Also here: a dense trellis-coded linear layer on the same kernels
- * (trellis_linear_*, at the end of this file).
+ * (trellis_linear_*), and, at the end of this file, what tuning the router of
+ * a layer with frozen 4-bit experts needs: a router with load statistics,
+ * losses and their gradient, MXFP4 quantisation and products (dense, and by
+ * expert), and the combine of the routes' rows with its gradient.
  */
 #ifndef TRELLIS_MOE_H_
 #define TRELLIS_MOE_H_
@@ -353,6 +356,119 @@ tm_status trellis_linear_forward(tm_linear* lin, const uint16_t* x, int32_t T, f
 tm_status trellis_linear_poll_error(tm_linear* lin, void* workspace, uint32_t* flags, void* stream);
 
 void trellis_linear_destroy(tm_linear* lin);
+
+/* ------------------------------------------------------------------------
+ * Element types of the entry points below. All of them compute in fp32 and
+ * round once where they store. */
+typedef enum { TM_F32 = 0, TM_BF16 = 1, TM_F16 = 2 } tm_dtype;
+
+/* ------------------------------------------------------------------------
+ * Router with load statistics and losses.
+ *   ids  [T, k]  the k largest logits of a token, descending, ties to the lowest id
+ *   w    [T, k]  softmax over the selected
+ *   lse  [T]     log sum exp of the token's logits
+ * A token is valid if mask[t] != 0 (mask NULL: all are) and one of its logits
+ * is above -inf. Over the n valid tokens:
+ *   tokens [1]     n
+ *   counts [E]     routes to e whose logit is above -inf
+ *   prob   [E]     mean probability of e, p = softmax(logits)
+ *   losses [2]     balance: E sum_e (counts_e / (n k)) prob_e  (1 when even);
+ *                  z: mean of lse^2.  Both 0 when n = 0.
+ * The mask keeps padding out of the statistics and losses; it does not change
+ * the token's own ids, w and lse. A token whose logits are all -inf gets ids
+ * 0..k-1, w 0 and lse -inf. logits: row t at logits + t * ld elements, ld >= E;
+ * 1 <= E <= 256, 1 <= k <= min(E, 32). Nothing is summed by atomics: equal
+ * inputs give equal bits. workspace: trellis_moe_router_workspace_size bytes,
+ * 16-byte aligned, contents ignored. T = 0 writes the statistics of no tokens. */
+size_t trellis_moe_router_workspace_size(int32_t T, int32_t E);
+tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t ld, const uint8_t* mask, int32_t T,
+                                     int32_t E, int32_t k, int32_t* ids, float* w, float* lse, int32_t* counts,
+                                     float* prob, float* losses, int32_t* tokens, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* grad_logits [T, E] (contiguous, of the logits' type, written) from the
+ * forward call's inputs and outputs, grad_w [T, k] (NULL: none) and
+ * grad_losses [2] on the device (NULL: none). counts are constants of the
+ * balance loss. A masked token has no gradient from the losses. */
+tm_status trellis_moe_router_backward(const void* logits, int32_t dtype, int64_t ld, const uint8_t* mask, int32_t T,
+                                      int32_t E, int32_t k, const int32_t* ids, const float* w, const float* lse,
+                                      const int32_t* counts, const int32_t* tokens, const float* grad_w,
+                                      const float* grad_losses, void* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Weighted combine of rows in route order (r = t * k + j, as
+ * trellis_moe_mxfp4_forward_experts writes them): out[t] = sum_j w[t, j]
+ * rows[t * k + j], fp32, in order j; a route of weight 0 is left out. 1 <= k <= 32. */
+tm_status trellis_moe_combine_forward(const void* rows, int32_t dtype, const float* w, int32_t T, int32_t k,
+                                      int32_t H, float* out, void* stream);
+
+/* grad_rows[t * k + j] = w[t, j] grad_out[t] (of the rows' type; NULL: not
+ * wanted), grad_w[t, j] = <grad_out[t], rows[t * k + j]> (NULL: not wanted). */
+tm_status trellis_moe_combine_backward(const void* rows, int32_t dtype, const float* w, const float* grad_out,
+                                       int32_t T, int32_t k, int32_t H, void* grad_rows, float* grad_w, void* stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4 (micro-scaled 4-bit floating point): blocks of 32 values along a row
+ * share a power of two 2^(byte - 127) (E8M0; 255 stands for NaN); a value is a
+ * 4-bit E2M1 code s|ee|m of magnitude 0, .5, 1, 1.5, 2, 3, 4, 6. A row of K
+ * values has B = ceil(K / 32) blocks: 16 B code bytes (value 2i in the low
+ * half of byte i; values past K are 0) and B scale bytes.
+ * Quantisation: exponent e = ceil(log2(fp32(amax / 6))) clamped to [-127, 127]
+ * (amax = 0: -127), the smallest power of two at which nothing saturates;
+ * codes round to nearest even. A block with an infinity or a NaN: byte 255,
+ * codes 0. x: row r at x + r * ld elements; codes [rows, 16 B] 16-byte aligned. */
+tm_status trellis_moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t K,
+                                     uint8_t* codes, uint8_t* scales, void* stream);
+
+/* out [rows, K] = the values that codes and scales stand for, rounded to dtype. */
+tm_status trellis_moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K,
+                                       void* out, int32_t dtype, void* stream);
+
+/* Products with MXFP4 weights. Rows of x are quantised to MXFP4 by the rule
+ * above, products are summed in fp32:
+ *   y_r = W_e q(x_r)            W_e [N, K], e = 0 or the route's expert
+ * gated: W_e has 2N rows, gate rows 0..N-1 then up rows, and
+ *   y_r = silu(W_gate q(x_r)) * (W_up q(x_r))      silu(g) = g / (1 + exp(-g)) */
+typedef struct tm_mxfp4 tm_mxfp4;
+
+typedef struct {
+  int32_t E;        /* experts, 1..256 (1 for a dense matrix) */
+  int32_t N;        /* output channels, >= 1 */
+  int32_t K;        /* input channels, >= 1 */
+  int32_t gated;    /* 0 or 1 */
+  int32_t max_rows; /* largest number of output rows of a call (T, or T * topk) */
+  /* DEVICE pointers, caller-owned, outliving the handle. R = N, or 2N if gated. */
+  const uint8_t* codes;   /* [E, R, 16 B], 16-byte aligned */
+  const uint8_t* scales;  /* [E, R, B] */
+} tm_mxfp4_desc;
+
+/* *workspace_bytes = the workspace of a call of max_rows rows. Errors:
+ * TM_EINVAL, TM_EUNSUPPORTED, TM_ECUDA. */
+tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, size_t* workspace_bytes);
+
+/* Workspace bytes for a call of `rows` output rows (0 for a NULL handle). */
+size_t trellis_moe_mxfp4_workspace_size(const tm_mxfp4* h, int32_t rows);
+
+/* Dense form (E = 1): x [T, K], row t at x + t * ld elements; out [T, N],
+ * written. workspace 256-byte aligned, contents on entry ignored; its first
+ * 4 bytes are the device error word. T = 0 is a no-op. */
+tm_status trellis_moe_mxfp4_forward(tm_mxfp4* h, const void* x, int32_t x_dtype, int64_t ld, int32_t T, void* out,
+                                    int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* By expert: route r = t * topk + j goes to expert ids[r] (int32 [T, topk])
+ * and reads row t of x (per_route 0) or row r (per_route 1); out [T * topk, N]
+ * in route order. An id outside 0..E-1 gives a row of zeros and sets bit 0 of
+ * the error word. */
+tm_status trellis_moe_mxfp4_forward_experts(tm_mxfp4* h, const void* x, int32_t x_dtype, int64_t ld,
+                                            int32_t per_route, const int32_t* ids, int32_t T, int32_t topk, void* out,
+                                            int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Read and clear the error word of `workspace` (synchronises `stream`). Returns
+ * TM_EDEVICE if any flag was set (bit 0: expert id out of range; bit 1: a
+ * pipeline wait gave up). */
+tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* flags, void* stream);
+
+void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
 
 #ifdef __cplusplus
 }

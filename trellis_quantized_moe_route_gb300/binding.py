@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import Any, NamedTuple, Optional
 
 import numpy as np
 
@@ -34,6 +34,11 @@ EXPORTED = [
     "trellis_moe_last_error", "trellis_moe_destroy", "trellis_moe_route_map_static",
     "trellis_linear_prepare", "trellis_linear_workspace_size", "trellis_linear_forward",
     "trellis_linear_poll_error", "trellis_linear_destroy",
+    "trellis_moe_router_workspace_size", "trellis_moe_router_forward", "trellis_moe_router_backward",
+    "trellis_moe_combine_forward", "trellis_moe_combine_backward",
+    "trellis_moe_mxfp4_quantize", "trellis_moe_mxfp4_dequantize", "trellis_moe_mxfp4_prepare",
+    "trellis_moe_mxfp4_workspace_size", "trellis_moe_mxfp4_forward", "trellis_moe_mxfp4_forward_experts",
+    "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_destroy",
 ]
 
 
@@ -59,6 +64,12 @@ class LinearDesc(ctypes.Structure):
                 ("svh", ctypes.c_void_p)]
 
 
+class MxFp4Desc(ctypes.Structure):
+    """tm_mxfp4_desc (include/trellis_moe.h)."""
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 class TrellisMoEError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__("%s: %s" % (STATUS.get(status, status), msg))
@@ -76,7 +87,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError("libtrellis_moe.so is not built (%s); run __graft_entry__.build()" % path)
     lib = ctypes.CDLL(path)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "trellis_moe_prepare": (I32, [ctypes.POINTER(LayerDesc), ctypes.POINTER(P), ctypes.POINTER(SZ)]),
         "trellis_moe_workspace_size": (SZ, [P, I32]),
@@ -100,6 +111,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "trellis_linear_forward": (I32, [P, P, I32, P, P, SZ, P]),
         "trellis_linear_poll_error": (I32, [P, P, ctypes.POINTER(ctypes.c_uint32), P]),
         "trellis_linear_destroy": (None, [P]),
+        "trellis_moe_router_workspace_size": (SZ, [I32, I32]),
+        "trellis_moe_router_forward": (I32, [P, I32, I64, P, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P]),
+        "trellis_moe_router_backward": (I32, [P, I32, I64, P, I32, I32, I32, P, P, P, P, P, P, P, P, P]),
+        "trellis_moe_combine_forward": (I32, [P, I32, P, I32, I32, I32, P, P]),
+        "trellis_moe_combine_backward": (I32, [P, I32, P, P, I32, I32, I32, P, P, P]),
+        "trellis_moe_mxfp4_quantize": (I32, [P, I32, I64, I64, I32, P, P, P]),
+        "trellis_moe_mxfp4_dequantize": (I32, [P, P, I64, I32, P, I32, P]),
+        "trellis_moe_mxfp4_prepare": (I32, [ctypes.POINTER(MxFp4Desc), ctypes.POINTER(P), ctypes.POINTER(SZ)]),
+        "trellis_moe_mxfp4_workspace_size": (SZ, [P, I32]),
+        "trellis_moe_mxfp4_forward": (I32, [P, P, I32, I64, I32, P, I32, P, SZ, P]),
+        "trellis_moe_mxfp4_forward_experts": (I32, [P, P, I32, I64, I32, P, I32, I32, P, I32, P, SZ, P]),
+        "trellis_moe_mxfp4_poll_error": (I32, [P, P, ctypes.POINTER(ctypes.c_uint32), P]),
+        "trellis_moe_mxfp4_destroy": (None, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -429,3 +453,307 @@ class TrellisLinear:
         if st not in (TM_OK, -5):
             _check(st)
         return int(flags.value)
+
+
+# ---------------------------------------------------------------------------
+# Router losses, route combine and MXFP4 (device tensors in, device tensors out)
+# ---------------------------------------------------------------------------
+def _dtype_code(dtype) -> int:
+    torch = _torch()
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if dtype not in codes:
+        raise ValueError("dtype must be torch.float32, torch.bfloat16 or torch.float16, not %s" % dtype)
+    return codes[dtype]
+
+
+def _on_device(name, t, dtype=None, shape=None, contiguous=True):
+    """Checks one tensor argument; returns it (None passes)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _rows_2d(name, t):
+    """A matrix whose rows may lie apart (last dimension contiguous); returns its row stride."""
+    _on_device(name, t, contiguous=False)
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, not %d" % (name, t.dim()))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: the last dimension must be contiguous" % name)
+    ld = int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
+    if ld < t.shape[1]:
+        raise ValueError("%s: rows overlap (stride %d for %d columns)" % (name, ld, t.shape[1]))
+    return ld
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+class RouterOut(NamedTuple):
+    """Results of router_forward (see trellis_moe_router_forward)."""
+    ids: Any      # int32 [T, k]
+    w: Any        # float32 [T, k]
+    lse: Any      # float32 [T]
+    counts: Any   # int32 [E]
+    prob: Any     # float32 [E]
+    losses: Any   # float32 [2]: balance, z
+    tokens: Any   # int32 [1]
+
+
+def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
+    """Router with load statistics and losses on device logits [T, E] (float32,
+    bfloat16 or float16; rows may lie apart); mask: bool or uint8 [T], false
+    for padding."""
+    torch = _torch()
+    lib = load_library()
+    ld = _rows_2d("logits", logits)
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    if mask is not None:
+        _on_device("mask", mask, shape=(T,))
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
+    dev, k = logits.device, int(k)
+    kk = max(k, 0)
+    # one allocation: ids | w | lse | counts | prob | losses | tokens, then the workspace
+    wsb = int(lib.trellis_moe_router_workspace_size(T, E))
+    head = 2 * T * kk + T + 2 * E + 3
+    head = (head + 3) // 4 * 4
+    buf = torch.empty(head + (wsb + 3) // 4, dtype=torch.int32, device=dev)
+    fb = buf.view(torch.float32)
+    o = T * kk
+    out = RouterOut(ids=buf[:o].view(T, kk), w=fb[o:2 * o].view(T, kk), lse=fb[2 * o:2 * o + T],
+                    counts=buf[2 * o + T:2 * o + T + E], prob=fb[2 * o + T + E:2 * o + T + 2 * E],
+                    losses=fb[2 * o + T + 2 * E:2 * o + T + 2 * E + 2],
+                    tokens=buf[2 * o + T + 2 * E + 2:2 * o + T + 2 * E + 3])
+    with torch.cuda.device(dev):
+        _check(lib.trellis_moe_router_forward(
+            logits.data_ptr(), _dtype_code(logits.dtype), ld, _opt(mask), T, E, k, out.ids.data_ptr(),
+            out.w.data_ptr(), out.lse.data_ptr(), out.counts.data_ptr(), out.prob.data_ptr(), out.losses.data_ptr(),
+            out.tokens.data_ptr(), buf.data_ptr() + 4 * head, wsb, _raw_stream(stream)))
+    return out
+
+
+def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=None, out=None, stream=None):
+    """Gradient of the logits from grad_w [T, k] and grad_losses [2] (float32,
+    on the device, either may be None); fwd and mask as in the forward call."""
+    torch = _torch()
+    lib = load_library()
+    ld = _rows_2d("logits", logits)
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    k = int(fwd.ids.shape[1])
+    _on_device("ids", fwd.ids, torch.int32, (T, k))
+    _on_device("w", fwd.w, torch.float32, (T, k))
+    _on_device("lse", fwd.lse, torch.float32, (T,))
+    _on_device("counts", fwd.counts, torch.int32, (E,))
+    _on_device("tokens", fwd.tokens, torch.int32, (1,))
+    _on_device("grad_w", grad_w, torch.float32, (T, k))
+    _on_device("grad_losses", grad_losses, torch.float32, (2,))
+    if mask is not None:
+        _on_device("mask", mask, shape=(T,))
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    else:
+        _on_device("out", out, logits.dtype, (T, E))
+    with torch.cuda.device(logits.device):
+        _check(lib.trellis_moe_router_backward(
+            logits.data_ptr(), _dtype_code(logits.dtype), ld, _opt(mask), T, E, k, fwd.ids.data_ptr(),
+            fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(), fwd.tokens.data_ptr(), _opt(grad_w),
+            _opt(grad_losses), out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def combine(rows, w, out=None, stream=None):
+    """out [T, H] float32 = sum_j w[t, j] rows[t * k + j] for rows [T * k, H] in
+    route order and w float32 [T, k]."""
+    torch = _torch()
+    lib = load_library()
+    _on_device("w", w, torch.float32)
+    T, k = int(w.shape[0]), int(w.shape[1])
+    _on_device("rows", rows)
+    if rows.dim() != 2 or rows.shape[0] != T * k:
+        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
+    H = int(rows.shape[1])
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.float32, device=rows.device)
+    else:
+        _on_device("out", out, torch.float32, (T, H))
+    with torch.cuda.device(rows.device):
+        _check(lib.trellis_moe_combine_forward(rows.data_ptr(), _dtype_code(rows.dtype), w.data_ptr(), T, k, H,
+                                               out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = True, stream=None):
+    """(grad_rows of the rows' type, grad_w float32) of combine; None where not wanted."""
+    torch = _torch()
+    lib = load_library()
+    _on_device("w", w, torch.float32)
+    T, k = int(w.shape[0]), int(w.shape[1])
+    _on_device("rows", rows)
+    if rows.dim() != 2 or rows.shape[0] != T * k:
+        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
+    H = int(rows.shape[1])
+    _on_device("grad_out", grad_out, torch.float32, (T, H))
+    grows = torch.empty_like(rows) if want_rows else None
+    gw = torch.empty_like(w) if want_w else None
+    with torch.cuda.device(rows.device):
+        _check(lib.trellis_moe_combine_backward(rows.data_ptr(), _dtype_code(rows.dtype), w.data_ptr(),
+                                                grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw),
+                                                _raw_stream(stream)))
+    return grows, gw
+
+
+def mxfp4_quantize(x, stream=None):
+    """Rows of x [rows, K] (float32, bfloat16 or float16; rows may lie apart) ->
+    (codes uint8 [rows, 16 B], scales uint8 [rows, B]), B = ceil(K / 32)."""
+    torch = _torch()
+    lib = load_library()
+    ld = _rows_2d("x", x)
+    rows, K = int(x.shape[0]), int(x.shape[1])
+    B = (K + 31) // 32
+    codes = torch.empty((rows, 16 * B), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, B), dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(lib.trellis_moe_mxfp4_quantize(x.data_ptr(), _dtype_code(x.dtype), ld, rows, K, codes.data_ptr(),
+                                              scales.data_ptr(), _raw_stream(stream)))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
+    """Values [rows, K] of MXFP4 codes [rows, 16 B] and scales [rows, B]."""
+    torch = _torch()
+    lib = load_library()
+    B = (int(K) + 31) // 32
+    if codes.dim() != 2:
+        raise ValueError("codes must have two dimensions, not %d" % codes.dim())
+    rows = int(codes.shape[0])
+    _on_device("codes", codes, torch.uint8, (rows, 16 * B))
+    _on_device("scales", scales, torch.uint8, (rows, B))
+    dtype = torch.float32 if dtype is None else dtype
+    if out is None:
+        out = torch.empty((rows, int(K)), dtype=dtype, device=codes.device)
+    else:
+        _on_device("out", out, dtype, (rows, int(K)))
+    with torch.cuda.device(codes.device):
+        _check(lib.trellis_moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, int(K), out.data_ptr(),
+                                                _dtype_code(dtype), _raw_stream(stream)))
+    return out
+
+
+class _MxFp4:
+    """One prepared set of MXFP4 matrices: codes uint8 [E, R, 16 B] and scales
+    uint8 [E, R, B] on the device (kept alive here)."""
+
+    def __init__(self, codes, scales, K: int, max_rows: int, gated: bool):
+        torch = _torch()
+        self.lib = load_library()
+        B = (int(K) + 31) // 32
+        E, R = int(codes.shape[0]), int(codes.shape[1])
+        _on_device("codes", codes, torch.uint8, (E, R, 16 * B))
+        _on_device("scales", scales, torch.uint8, (E, R, B))
+        if gated and R % 2:
+            raise ValueError("a gated matrix has gate and up rows: %d rows are odd" % R)
+        self.device = codes.device
+        self.codes, self.scales = codes, scales
+        self.E, self.N, self.K, self.gated = E, R // 2 if gated else R, int(K), bool(gated)
+        d = MxFp4Desc(E, self.N, self.K, 1 if gated else 0, int(max_rows), codes.data_ptr(), scales.data_ptr())
+        handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+        with torch.cuda.device(self.device):
+            _check(self.lib.trellis_moe_mxfp4_prepare(ctypes.byref(d), ctypes.byref(handle), ctypes.byref(ws)))
+        self.handle = handle
+        self.workspace_bytes = int(ws.value)
+        self.workspace = torch.empty(self.workspace_bytes + 256, dtype=torch.uint8, device=self.device)
+        off = (-self.workspace.data_ptr()) % 256
+        self.workspace = self.workspace[off:off + self.workspace_bytes]
+
+    def close(self):
+        if getattr(self, "handle", None):
+            self.lib.trellis_moe_mxfp4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def poll_error(self, stream=None) -> int:
+        flags = ctypes.c_uint32(0)
+        with _torch().cuda.device(self.device):
+            st = self.lib.trellis_moe_mxfp4_poll_error(self.handle, _ptr(self.workspace), ctypes.byref(flags),
+                                                       _raw_stream(stream))
+        if st not in (TM_OK, -5):
+            _check(st)
+        return int(flags.value)
+
+    def _output(self, rows, x, out, out_dtype):
+        torch = _torch()
+        dtype = out.dtype if out is not None else (torch.float32 if out_dtype is None else out_dtype)
+        if out_dtype is not None and dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype %s" % (dtype, out_dtype))
+        if x.device != self.device:
+            raise ValueError("x is on %s, the weights on %s" % (x.device, self.device))
+        if x.shape[1] != self.K:
+            raise ValueError("x must have %d columns, not %d" % (self.K, x.shape[1]))
+        if out is None:
+            return torch.empty((rows, self.N), dtype=dtype, device=self.device)
+        return _on_device("out", out, dtype, (rows, self.N))
+
+
+class MxFp4Linear(_MxFp4):
+    """Dense product with MXFP4 weights: codes [R, 16 B], scales [R, B]; gated:
+    R = 2N, gate rows then up rows."""
+
+    def __init__(self, codes, scales, K: int, max_tokens: int, gated: bool = False):
+        super().__init__(codes[None], scales[None], K, max_tokens, gated)
+
+    def forward(self, x, out=None, out_dtype=None, stream=None):
+        """x [T, K] (float32, bfloat16 or float16; rows may lie apart) -> [T, N]
+        of out_dtype (default float32)."""
+        torch = _torch()
+        ld = _rows_2d("x", x)
+        T = int(x.shape[0])
+        out = self._output(T, x, out, out_dtype)
+        with torch.cuda.device(self.device):
+            _check(self.lib.trellis_moe_mxfp4_forward(
+                self.handle, x.data_ptr(), _dtype_code(x.dtype), ld, T, out.data_ptr(), _dtype_code(out.dtype),
+                self.workspace.data_ptr(), self.workspace_bytes, _raw_stream(stream)))
+        return out
+
+
+class MxFp4Experts(_MxFp4):
+    """Products by expert with MXFP4 weights: codes [E, R, 16 B], scales
+    [E, R, B]; gated: R = 2N, gate rows then up rows."""
+
+    def __init__(self, codes, scales, K: int, topk: int, max_tokens: int, gated: bool = False):
+        super().__init__(codes, scales, K, int(max_tokens) * int(topk), gated)
+        self.topk = int(topk)
+
+    def forward(self, x, ids, per_route: bool = False, out=None, out_dtype=None, stream=None):
+        """x [T, K] (per_route: [T * topk, K]) and ids int32 [T, topk] -> rows
+        [T * topk, N] in route order, of out_dtype (default float32)."""
+        torch = _torch()
+        ld = _rows_2d("x", x)
+        T = int(ids.shape[0])
+        _on_device("ids", ids, torch.int32, (T, self.topk))
+        need = T * self.topk if per_route else T
+        if x.shape[0] != need:
+            raise ValueError("x must have %d rows, not %d" % (need, x.shape[0]))
+        out = self._output(T * self.topk, x, out, out_dtype)
+        with torch.cuda.device(self.device):
+            _check(self.lib.trellis_moe_mxfp4_forward_experts(
+                self.handle, x.data_ptr(), _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T,
+                self.topk, out.data_ptr(), _dtype_code(out.dtype), self.workspace.data_ptr(), self.workspace_bytes,
+                _raw_stream(stream)))
+        return out
