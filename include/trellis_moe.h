@@ -38,8 +38,9 @@
  *     returns an error has launched nothing and written nothing.
  *   - Errors: a negative tm_status; trellis_moe_last_error() gives a message
  *     for the calling thread.
- *   - Only trellis_moe_prepare and trellis_linear_prepare allocate device
- *     memory (small descriptor tables), and trellis_moe_forward_host builds
+ *   - Only trellis_moe_prepare, trellis_linear_prepare (small descriptor
+ *     tables) and trellis_moe_mxfp4_prepare (the weights' scales) allocate
+ *     device memory, and trellis_moe_forward_host builds
  *     the CUDA graphs it caches on the handle (see there).
  *     trellis_moe_forward, trellis_moe_forward_logits and
  *     trellis_linear_forward use only the caller's workspace, launch only on
@@ -442,7 +443,10 @@ typedef struct {
   const uint8_t* scales;  /* [E, R, B] */
 } tm_mxfp4_desc;
 
-/* *workspace_bytes = the workspace of a call of max_rows rows. Errors:
+/* Lays the scales out for the tensor cores (device memory of E * R * B bytes,
+ * R and B rounded up to 128 rows and 8 blocks; synchronises): codes and scales
+ * must be complete when it is called, and later changes of the scales are not
+ * seen. *workspace_bytes = the workspace of a call of max_rows rows. Errors:
  * TM_EINVAL, TM_EUNSUPPORTED, TM_ECUDA. */
 tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, size_t* workspace_bytes);
 

@@ -670,6 +670,7 @@ class _MxFp4:
         d = MxFp4Desc(E, self.N, self.K, 1 if gated else 0, int(max_rows), codes.data_ptr(), scales.data_ptr())
         handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
         with torch.cuda.device(self.device):
+            torch.cuda.current_stream().synchronize()  # prepare reads the scales on a stream of its own
             _check(self.lib.trellis_moe_mxfp4_prepare(ctypes.byref(d), ctypes.byref(handle), ctypes.byref(ws)))
         self.handle = handle
         self.workspace_bytes = int(ws.value)

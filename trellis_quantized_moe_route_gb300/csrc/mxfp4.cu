@@ -1,18 +1,17 @@
 // Products with MXFP4 weights (sm_103a): y = deq(q(x)) deq(W)^T for a dense
 // matrix or for each route's expert, with the rows of x quantised to MXFP4 in
-// the call. A product of two codes is a multiple of 1/4 of at most 36, so a
-// block's 32 products add up exactly in fp32; the blocks' sums, each times its
-// two powers of two, are added in fp32.
+// the call. Entry points, workspace and the order of the kernels; the products
+// themselves are in mxfp4_tc.cu.
 #include <algorithm>
 #include <new>
 
-#include "elem.cuh"
 #include "mxfp4.h"
-#include "mxfp4.cuh"
 #include "status.h"
 
 struct tm_mxfp4 {
   tm_mxfp4_desc desc;
+  uint8_t* d_scales;  // the weights' scales as the tensor cores read them
+  CUtensorMap wmap;
 };
 
 namespace tmoe {
@@ -21,61 +20,8 @@ namespace {
 
 constexpr size_t kMxAlign = 256;
 size_t mx_align(size_t v) { return (v + kMxAlign - 1) / kMxAlign * kMxAlign; }
-int mx_blocks(int K) { return (K + 31) / 32; }
 
-// Error word | codes of x | scales of x
-struct MxLayout {
-  size_t codes, scales, total;
-};
-
-MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
-  MxLayout L;
-  L.codes = kMxAlign;
-  L.scales = L.codes + mx_align((size_t)rows * mx_blocks(d.K) * 16);
-  L.total = L.scales + mx_align((size_t)rows * mx_blocks(d.K));
-  return L;
-}
-
-// One warp: one row of y, 32 output channels (one a lane).
-template <typename T>
-__global__ void __launch_bounds__(128) k_mx_rows(const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                                                 const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
-                                                 const int32_t* __restrict__ ids, int rows, int x_div, int E, int N,
-                                                 int nb, int gated, T* __restrict__ out, uint32_t* __restrict__ err) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.y * 4 + warp;
-  const int n = blockIdx.x * 32 + lane;
-  if (r >= rows || n >= N) return;
-  const int e = ids ? ids[r] : 0;
-  if (e < 0 || e >= E) {
-    if (n == 0) atomicOr(err, 1u);
-    out[(size_t)r * N + n] = from_f32<T>(0.0f);
-    return;
-  }
-  const size_t xr = (size_t)(r / x_div) * nb;
-  const size_t wr0 = ((size_t)e * (gated ? 2 * N : N) + n) * nb;
-  float y[2] = {0.0f, 0.0f};
-  for (int half = 0; half <= gated; ++half) {
-    const size_t wr = wr0 + (size_t)half * N * nb;
-    float acc = 0.0f;
-    for (int b = 0; b < nb; ++b) {
-      float s = 0.0f;
-      for (int c = 0; c < 4; ++c) {
-        float a[8], w[8];
-        e2m1x8_to_f32(__ldg(reinterpret_cast<const uint32_t*>(xc) + (xr + b) * 4 + c), a);
-        e2m1x8_to_f32(__ldg(reinterpret_cast<const uint32_t*>(wc) + (wr + b) * 4 + c), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(a[i], w[i], s);
-      }
-      acc += s * mxfp4_power(xs[xr + b]) * mxfp4_power(ws[wr + b]);
-    }
-    y[half] = acc;
-  }
-  const float v = gated ? y[0] / (1.0f + expf(-y[0])) * y[1] : y[0];
-  out[(size_t)r * N + n] = from_f32<T>(v);
-}
-
-__global__ void k_mx_clear(uint32_t* err) { *err = 0; }
+constexpr int kMxRowsMax = 240, kMxRowsMaxGated = 112;  // rows of a block (mxfp4_tc.cu)
 
 struct MxCall {
   const void* x;
@@ -84,27 +30,98 @@ struct MxCall {
   const int32_t* ids;
   int rows;    // rows of y
   int x_rows;
-  int x_div;   // row r of y reads row r / x_div of x
+  int topk;    // rows of y that read one row of x
   void* out;
   int out_dtype;
   void* ws;
 };
 
-cudaError_t mx_run(const tm_mxfp4_desc& d, const MxCall& c, cudaStream_t st) {
+// Rows of a block. Dense: as few blocks as the limit allows, evenly filled.
+// By expert: the limit, or less where experts average fewer routes.
+int mx_block_rows(const tm_mxfp4_desc& d, bool dense, long rows) {
+  const int most = d.gated ? kMxRowsMaxGated : kMxRowsMax;
+  long want = rows;
+  if (dense) {
+    const long blocks = (rows + most - 1) / most;
+    want = (rows + blocks - 1) / blocks;
+  } else {
+    want = std::max<long>(16, 2 * rows / d.E);
+  }
+  return (int)std::min<long>(most, (want + 15) / 16 * 16);
+}
+
+long mx_max_blocks(const tm_mxfp4_desc& d, long rows, int bn) { return rows / bn + std::min<long>(d.E, rows) + 1; }
+
+// Error word | route map | codes of x in block order | their scales. Sized for
+// the largest block and for the most blocks, so that a workspace for more rows
+// fits fewer.
+struct MxLayout {
+  size_t rank, tile_counts, counts, offsets, block_expert, nblocks, route_of_slot, slot_of_route, codes, scales, total;
+};
+
+MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
+  MxLayout L;
+  const long ex = std::min<long>(d.E, rows) + 1;
+  const size_t slots = (size_t)(rows + ex * kMxRowsMax), blocks = (size_t)(rows / 16 + ex);
+  const size_t B = mx_blocks(d.K), S = mx_stages(d.K);
+  size_t o = kMxAlign;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += mx_align(bytes);
+    return at;
+  };
+  const size_t R = (size_t)rows;
+  L.rank = take(R * 4);
+  L.tile_counts = take((R + 1023) / 1024 * d.E * 4);
+  L.counts = take((size_t)d.E * 4);
+  L.offsets = take(((size_t)d.E + 1) * 4);
+  L.block_expert = take(blocks * 4);
+  L.nblocks = take(4);
+  L.route_of_slot = take(slots * 4);
+  L.slot_of_route = take(R * 4);
+  L.codes = take(slots * B * 16);
+  L.scales = take(blocks * S * 1024 + slots / 128 * S * 1024);
+  L.total = o;
+  return L;
+}
+
+cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
+  const tm_mxfp4_desc& d = h->desc;
   const MxLayout L = mx_layout(d, c.rows);
   uint8_t* base = static_cast<uint8_t*>(c.ws);
   uint32_t* err = reinterpret_cast<uint32_t*>(base);
-  k_mx_clear<<<1, 1, 0, st>>>(err);
-  cudaError_t e = launch_mxfp4_quantize(c.x, c.x_dtype, c.ld, c.x_rows, d.K, base + L.codes, base + L.scales, st);
+  auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(base + off); };
+  cudaError_t e = cudaMemsetAsync(err, 0, 4, st);
   if (e != cudaSuccess) return e;
-  auto go = [&](auto elem) {
-    using T = decltype(elem);
-    k_mx_rows<T><<<dim3((d.N + 31) / 32, (c.rows + 3) / 4), 128, 0, st>>>(
-        base + L.codes, base + L.scales, d.codes, d.scales, c.ids, c.rows, c.x_div, d.E, d.N, mx_blocks(d.K), d.gated,
-        static_cast<T*>(c.out), err);
-    return cudaGetLastError();
-  };
-  return TM_BY_DTYPE(c.out_dtype, go);
+  MxTcArgs a{};
+  a.E = d.E;
+  a.N = d.N;
+  a.K = d.K;
+  a.gated = d.gated;
+  a.rows = c.rows;
+  a.bn = mx_block_rows(d, c.ids == nullptr, c.rows);
+  a.nrb = (a.bn + 127) / 128;
+  a.wscale = h->d_scales;
+  a.xscale = base + L.scales;
+  a.out = c.out;
+  a.err = err;
+  a.wmap = h->wmap;
+  a.max_blocks = (c.rows + a.bn - 1) / a.bn;
+  if (c.ids) {
+    a.max_blocks = (int)mx_max_blocks(d, c.rows, a.bn);
+    a.block_expert = i32(L.block_expert);
+    a.nblocks = i32(L.nblocks);
+    a.counts = i32(L.counts);
+    a.offsets = i32(L.offsets);
+    a.route_of_slot = i32(L.route_of_slot);
+    RouteMapArgs rm{c.ids, c.rows, d.E, a.bn, i32(L.rank), i32(L.tile_counts), i32(L.counts), i32(L.offsets),
+                    i32(L.block_expert), i32(L.nblocks), i32(L.route_of_slot), i32(L.slot_of_route), err};
+    if ((e = launch_route_map(rm, st)) != cudaSuccess) return e;
+  }
+  MxQuantArgs q{c.x, c.ld, c.x_rows, d.K, c.topk, c.ids ? i32(L.slot_of_route) : nullptr, a.bn, a.nrb, base + L.codes,
+                base + L.scales, c.out, d.N * dtype_bytes(c.out_dtype)};
+  if ((e = launch_mx_rows_quantize(q, c.x_dtype, st)) != cudaSuccess) return e;
+  return launch_mx_tc(a, base + L.codes, (long)a.max_blocks * a.bn, c.out_dtype, st);
 }
 
 tm_status mx_check(const tm_mxfp4* h, const MxCall& c, size_t ws_bytes) {
@@ -149,6 +166,17 @@ tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, s
   tm_mxfp4* h = new (std::nothrow) tm_mxfp4();
   if (!h) return status_fail(TM_EINVAL, "out of host memory");
   h->desc = d;
+  h->d_scales = nullptr;
+  const int halves = d.gated ? 2 : 1;
+  cudaError_t e;
+  if ((e = cudaMalloc(&h->d_scales, mx_weight_scale_bytes(d.E, halves, d.N, d.K))) != cudaSuccess ||
+      (e = launch_mx_weight_scales(d.scales, d.E, halves, d.N, d.K, h->d_scales, nullptr)) != cudaSuccess ||
+      (e = mx_weight_map(&h->wmap, d.codes, (long)d.E * halves * d.N, d.K)) != cudaSuccess ||
+      (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {
+    cudaFree(h->d_scales);
+    delete h;
+    return status_cuda(e, "lay out the scales");
+  }
   *out = h;
   if (workspace_bytes) *workspace_bytes = mx_layout(d, d.max_rows).total;
   return TM_OK;
@@ -169,7 +197,7 @@ tm_status trellis_moe_mxfp4_forward(tm_mxfp4* h, const void* x, int32_t x_dtype,
   const MxCall c{x, x_dtype, ld, nullptr, T, T, 1, out, out_dtype, workspace};
   const tm_status s = mx_check(h, c, workspace_bytes);
   if (s != TM_OK) return s;
-  const cudaError_t e = mx_run(h->desc, c, (cudaStream_t)stream);
+  const cudaError_t e = mx_run(h, c, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "MXFP4 product");
 }
 
@@ -185,10 +213,11 @@ tm_status trellis_moe_mxfp4_forward_experts(tm_mxfp4* h, const void* x, int32_t 
   if ((long)T * topk > h->desc.max_rows)
     return status_fail(TM_EINVAL, "T*topk=%ld exceeds the prepared max_rows=%d", (long)T * topk, h->desc.max_rows);
   if (!ids) return status_fail(TM_EINVAL, "ids is NULL");
-  const MxCall c{x, x_dtype, ld, ids, T * topk, per_route ? T * topk : T, per_route ? 1 : topk, out, out_dtype, workspace};
+  const MxCall c{x, x_dtype, ld, ids, T * topk, per_route ? T * topk : T, per_route ? 1 : topk,
+                 out, out_dtype, workspace};
   const tm_status s = mx_check(h, c, workspace_bytes);
   if (s != TM_OK) return s;
-  const cudaError_t e = mx_run(h->desc, c, (cudaStream_t)stream);
+  const cudaError_t e = mx_run(h, c, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "MXFP4 expert products");
 }
 
@@ -207,6 +236,10 @@ tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* f
   return TM_OK;
 }
 
-void trellis_moe_mxfp4_destroy(tm_mxfp4* h) { delete h; }
+void trellis_moe_mxfp4_destroy(tm_mxfp4* h) {
+  if (!h) return;
+  cudaFree(h->d_scales);
+  delete h;
+}
 
 }  // extern "C"

@@ -1,0 +1,446 @@
+// Products with MXFP4 weights on the tensor cores (sm_103a).
+//
+// D[n, r] = sum_k W[n, k] x[r, k], both operands E2M1 codes with one E8M0 scale
+// per 32 columns, as `tcgen05.mma.kind::mxf4.block_scale`: the 128 rows of a
+// tile of W are the M side (TMEM lanes), the rows of x the N side (TMEM
+// columns), so that a block of x may have any multiple of 16 rows up to 240
+// and an expert with few routes wastes little. A thread of the epilogue then
+// holds one output channel, and a warp stores 32 neighbouring channels of a
+// row. Gated products keep two accumulators, gate and up rows of the same 128
+// channels against one x operand, and the same thread holds both.
+//
+// Persistent, one CTA per SM: a loader thread (TMA boxes of 256 columns = one
+// 128-byte swizzle span of codes, bulk copies of the scale chunks), an issuer
+// thread (scales to tensor memory with tcgen05.cp, then one MMA per 64
+// columns), and eight epilogue warps that drain one accumulator buffer while
+// the next unit fills the other. 240 columns twice, plus 24 columns of scales,
+// is what 512 columns of tensor memory hold; that is why a block ends at 240.
+//
+// Every wait is bounded (2 s): one that runs out raises bit 1 of the error
+// word, lets the copies and MMAs in flight finish, frees the tensor memory and
+// returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "elem.cuh"
+#include "mxfp4.cuh"
+#include "mxfp4.h"
+#include "status.h"
+#include "tc.cuh"
+
+namespace tmoe {
+
+namespace {
+
+constexpr int kMxEpiWarps = 8;
+constexpr int kMxThreads = (kMxEpiWarps + 2) * 32;
+constexpr uint64_t kMxWaitNs = 2000000000ull;
+constexpr uint64_t kMxDrainNs = 500000000ull;
+constexpr int kMxMaxStages = 8;
+constexpr int kMxSfCol = 480;       // first tensor-memory column of the scales
+constexpr int kMxTileBytes = 128 * 128;
+constexpr uint32_t kMxSmem = 220 * 1024;
+
+__device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar)) : "memory");
+}
+
+// 512 bytes of scales (32 rows of 16 bytes, rows 16 bytes apart) to four
+// columns of tensor memory, repeated in each quarter of the lanes.
+__device__ __forceinline__ void mx_copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = smem_desc(saddr, 128, 128);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D (+)= A B^T over 64 columns with one scale per 32.
+__device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc));
+}
+
+// Instruction descriptor: E2M1 x E2M1, E8M0 scales, fp32 accumulator, both
+// operands K-major, M = 128; `id` is the first of the two scale bytes used
+// (0 or 2 of the chunk's four).
+__device__ __forceinline__ uint32_t mx_idesc(int n, int id) {
+  return ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(128 >> 4) << 24) | ((uint32_t)id << 29);
+}
+
+struct MxBars {
+  uint64_t full[kMxMaxStages], empty[kMxMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+};
+
+// One unit: a block of rows times 128 output channels.
+struct MxUnit {
+  int expert, tile, slot0, rows;
+};
+
+__device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int tiles) {
+  MxUnit m;
+  const int b = u / tiles;
+  m.tile = u - b * tiles;
+  m.slot0 = b * a.bn;
+  if (a.block_expert) {
+    m.expert = a.block_expert[b];
+    m.rows = min(a.bn, a.counts[m.expert] - (m.slot0 - a.offsets[m.expert]));
+  } else {
+    m.expert = 0;
+    m.rows = min(a.bn, a.rows - m.slot0);
+  }
+  return m;
+}
+
+struct MxGeom {
+  int tiles, units, stages, ring, ksteps;
+  uint32_t a_bytes, b_bytes, sfa_bytes, sfb_bytes, stage_bytes;
+};
+
+template <bool GATED>
+__device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring) {
+  MxGeom g;
+  g.tiles = (a.N + 127) / 128;
+  const int blocks = a.block_expert ? *a.nblocks : (a.rows + a.bn - 1) / a.bn;
+  g.units = blocks * g.tiles;
+  g.stages = mx_stages(a.K);
+  g.ksteps = (mx_blocks(a.K) + 1) / 2;
+  g.ring = ring;
+  g.a_bytes = (GATED ? 2 : 1) * kMxTileBytes;
+  g.b_bytes = (uint32_t)a.bn * 128;
+  g.sfa_bytes = (GATED ? 2 : 1) * 1024;
+  g.sfb_bytes = (uint32_t)a.nrb * 1024;
+  g.stage_bytes = (g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes + 1023) / 1024 * 1024;
+  return g;
+}
+
+template <bool GATED>
+__device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
+                          uint64_t limit) {
+  int it = 0;
+  bool ok = true;
+  for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
+    const MxUnit m = mx_unit(a, u, g.tiles);
+    const int wrow = m.expert * (GATED ? 2 * a.N : a.N) + m.tile * 128;
+    const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles + m.tile) * g.stages * 1024;
+    const size_t xsf = (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
+    for (int s = 0; s < g.stages; ++s, ++it) {
+      const int slot = it % g.ring;
+      if (it >= g.ring && !mbar_wait_abort(&B.empty[slot], ((it / g.ring) - 1) & 1, abort, limit)) {
+        ok = false;
+        break;
+      }
+      unsigned char* st = smem + (size_t)slot * g.stage_bytes;
+      uint64_t* bar = &B.full[slot];
+      mbar_arrive_expect_tx(bar, g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes);
+      mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
+      if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
+      mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
+      unsigned char* sf = st + g.a_bytes + g.b_bytes;
+      bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
+      if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)g.tiles * g.stages + s) * 1024, 1024, bar);
+      bulk_g2s(sf + g.sfa_bytes, a.xscale + xsf + (size_t)s * g.sfb_bytes, g.sfb_bytes, bar);
+    }
+  }
+  if (*abort) {  // let the copies in flight land before the CTA goes
+    int never = 0;
+    for (int i = max(0, it - g.ring); i < it; ++i) mbar_wait_abort(&B.full[i % g.ring], (i / g.ring) & 1, &never, kMxDrainNs);
+  }
+}
+
+template <bool GATED>
+__device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
+                          volatile int* abort, uint64_t limit) {
+  int it = 0, nu = 0;
+  bool ok = true;
+  const int halves = GATED ? 2 : 1;
+  for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
+    const MxUnit m = mx_unit(a, u, g.tiles);
+    const int n16 = (m.rows + 15) / 16 * 16;
+    const int buf = nu & 1;
+    if (nu >= 2 && !mbar_wait_abort(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, limit)) break;
+    tc_fence_after();
+    const uint32_t d = tmem + (uint32_t)(buf * halves * a.bn);
+    for (int s = 0; s < g.stages; ++s, ++it) {
+      const int slot = it % g.ring;
+      if (!mbar_wait_abort(&B.full[slot], (it / g.ring) & 1, abort, limit)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = smem_u32(smem) + (uint32_t)slot * g.stage_bytes;
+      const uint32_t sf = st + g.a_bytes + g.b_bytes;
+      const int steps = min(4, g.ksteps - s * 4);
+      const uint32_t tsfa = tmem + kMxSfCol, tsfb = tsfa + 8u * halves;
+      for (int c = 0; c < 2 && c * 2 < steps; ++c) {
+        for (int h = 0; h < halves; ++h) mx_copy_scales(tsfa + (uint32_t)(c * halves + h) * 4, sf + h * 1024 + c * 512);
+        for (int r = 0; r < a.nrb; ++r)
+          mx_copy_scales(tsfb + (uint32_t)(c * a.nrb + r) * 4, sf + g.sfa_bytes + (uint32_t)(c * a.nrb + r) * 512);
+      }
+      const uint64_t bdesc = smem_desc_sw128(st + g.a_bytes);
+      for (int k = 0; k < steps; ++k) {
+        const uint32_t idesc = mx_idesc(n16, (k & 1) * 2);
+        const uint32_t c = (uint32_t)(k >> 1);
+        for (int h = 0; h < halves; ++h) {
+          const uint64_t adesc = smem_desc_sw128(st + h * kMxTileBytes);
+          mx_mma(d + (uint32_t)(h * a.bn), adesc + (uint64_t)(k * 2), bdesc + (uint64_t)(k * 2), idesc,
+                 tsfa + (c * halves + h) * 4, tsfb + c * a.nrb * 4, s > 0 || k > 0 ? 1u : 0u);
+        }
+      }
+      tc_commit(&B.empty[slot]);
+    }
+    if (ok) tc_commit(&B.acc_full[buf]);
+  }
+  if (*abort && it > 0) {
+    int never = 0;
+    mbar_wait_abort(&B.empty[(it - 1) % g.ring], ((it - 1) / g.ring) & 1, &never, kMxDrainNs);
+  }
+}
+
+template <bool GATED, typename T>
+__device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, volatile int* abort,
+                            uint64_t limit) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quarter = warp & 3, part = warp >> 2;
+  const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+  T* out = static_cast<T*>(a.out);
+  int nu = 0;
+  for (int u = blockIdx.x; u < g.units; u += gridDim.x, ++nu) {
+    const MxUnit m = mx_unit(a, u, g.tiles);
+    const int buf = nu & 1;
+    const int n = m.tile * 128 + quarter * 32 + lane;
+    const bool ok = mbar_wait_abort(&B.acc_full[buf], (nu >> 1) & 1, abort, limit);
+    if (!__all_sync(0xFFFFFFFFu, ok)) return;
+    tc_fence_after();
+    const uint32_t d = tmem + lane_base + (uint32_t)(buf * (GATED ? 2 : 1) * a.bn);
+    for (int c0 = part * 32; c0 < m.rows; c0 += 64) {
+      uint32_t v[32], w[32];
+      tmem_ld32(d + c0, v);
+      if (GATED) tmem_ld32(d + a.bn + c0, w);
+      int row = m.slot0 + c0 + lane;
+      if (a.route_of_slot) row = c0 + lane < m.rows ? a.route_of_slot[row] : -1;
+      tmem_ld_wait();
+      reg_fence32(v);
+      if (GATED) reg_fence32(w);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const int r = __shfl_sync(0xFFFFFFFFu, row, c);
+        float y = __uint_as_float(v[c]);
+        if (GATED) y = y / (1.0f + __expf(-y)) * __uint_as_float(w[c]);
+        if (c0 + c < m.rows && n < a.N) out[(size_t)r * a.N + n] = from_f32<T>(y);
+      }
+    }
+    tc_fence_before();
+    if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
+    __syncwarp();
+  }
+}
+
+template <bool GATED, typename T>
+__global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__ MxTcArgs a, int ring) {
+  extern __shared__ unsigned char mx_smem_raw[];
+  __shared__ __align__(8) MxBars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort;
+  unsigned char* smem = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ring; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], kMxEpiWarps);
+    }
+    s_abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort = &s_abort;
+  const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
+  const MxGeom g = mx_geom<GATED>(a, ring);
+  if (warp < kMxEpiWarps) {
+    mx_epilogue<GATED, T>(a, g, bars, tmem, abort, limit);
+  } else if (threadIdx.x == kMxEpiWarps * 32) {
+    mx_loader<GATED>(a, g, bars, smem, abort, limit);
+  } else if (threadIdx.x == (kMxEpiWarps + 1) * 32) {
+    mx_issuer<GATED>(a, g, bars, smem, tmem, abort, limit);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort) atomicOr(a.err, 2u);
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+PFN_cuTensorMapEncodeTiled_v12000 mx_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Rows of codes as bytes, boxes of 128 bytes (256 values) x `box` rows. Box
+// starts are multiples of 128 bytes, rows of 16; what lies past a row or the
+// last row reads as 0.
+cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t bytes = (cuuint64_t)mx_blocks(K) * 16;
+  cuuint64_t dims[2] = {bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {bytes};
+  cuuint32_t boxes[2] = {128, (cuuint32_t)box};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, boxes, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool GATED, typename T>
+cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
+  auto kern = k_mx_tc<GATED, T>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
+  if (attr != cudaSuccess) return attr;
+  const uint32_t stage = (uint32_t)(GATED ? 2 : 1) * (kMxTileBytes + 1024) + (uint32_t)a.bn * 128 + (uint32_t)a.nrb * 1024;
+  const uint32_t stage_bytes = (stage + 1023) / 1024 * 1024;
+  const int ring = (int)std::min<uint32_t>(kMxMaxStages, (kMxSmem - 1024) / stage_bytes);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long units = (long)a.max_blocks * ((a.N + 127) / 128);
+  const int grid = (int)std::max<long>(1, std::min<long>(units, sms));
+  kern<<<grid, kMxThreads, 1024 + ring * stage_bytes, st>>>(a, ring);
+  return cudaGetLastError();
+}
+
+// One thread a 4-byte word of the laid-out scales; absent rows and blocks get 0.
+__global__ void __launch_bounds__(256) k_mx_weight_scales(const uint8_t* __restrict__ s, int halves, int N, int nb,
+                                                          int tiles, int chunks, long words, uint32_t* __restrict__ out) {
+  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (long)gridDim.x * blockDim.x) {
+    const int w = (int)(i & 127);
+    long j = i >> 7;
+    const int c = (int)(j % chunks);
+    j /= chunks;
+    const int tile = (int)(j % tiles);
+    const long eh = j / tiles;  // expert * halves + half
+    const int n = tile * 128 + (w & 3) * 32 + (w >> 2);
+    uint32_t v = 0;
+    if (n < N)
+      for (int b = 0; b < 4; ++b)
+        if (c * 4 + b < nb) v |= (uint32_t)s[((size_t)eh * N + n) * nb + c * 4 + b] << (8 * b);
+    out[i] = v;
+  }
+}
+
+// A warp takes 256 columns (eight blocks, four lanes each) of one row of x.
+template <typename T>
+__global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, bool vec) {
+  const int lane = threadIdx.x & 31;
+  const int nb = mx_blocks(a.K), stages = mx_stages(a.K);
+  const long warps = (long)gridDim.x * 8, items = (long)a.x_rows * stages;
+  const T* x = static_cast<const T*>(a.x);
+  for (long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5); i < items; i += warps) {
+    const int row = (int)(i / stages), s = (int)(i - (long)row * stages);
+    const int blk = s * 8 + (lane >> 2), col = blk * 32 + (lane & 3) * 8;
+    const T* p = x + (size_t)row * a.ld + col;
+    float v[8];
+    if (col + 8 <= a.K) {
+      load_f32<8>(p, vec, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = col + c < a.K ? to_f32(p[c]) : 0.0f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t byte = mxfp4_scale_byte(m);
+    const float inv = mxfp4_inverse(byte);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] *= inv;
+    const uint32_t q = byte == 255u ? 0u : e2m1x8(v);
+    // the four bytes of a chunk (128 columns, 16 lanes) in its first lane
+    const int base = lane & 16;
+    uint32_t word = byte;
+    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 4) << 8;
+    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 8) << 16;
+    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 12) << 24;
+    for (int j = 0; j < a.topk; ++j) {
+      const int r = row * a.topk + j;
+      const int slot = a.slot_of_route ? a.slot_of_route[r] : r;
+      if (slot < 0) {
+        if (s == 0) {
+          char* o = static_cast<char*>(a.out) + (size_t)r * a.out_row_bytes;
+          for (int b = lane * 2; b < a.out_row_bytes; b += 64) *reinterpret_cast<uint16_t*>(o + b) = 0;
+        }
+        continue;
+      }
+      if (blk < nb) *reinterpret_cast<uint32_t*>(a.codes + ((size_t)slot * nb + blk) * 16 + (lane & 3) * 4) = q;
+      if ((lane & 15) == 0) {
+        const int b = slot / a.bn, t = slot - b * a.bn;
+        const size_t chunk = ((size_t)b * stages * 2 + s * 2 + (lane >> 4)) * a.nrb + (t >> 7);
+        *reinterpret_cast<uint32_t*>(a.scales + chunk * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4) = word;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+size_t mx_weight_scale_bytes(int E, int halves, int N, int K) {
+  return (size_t)E * halves * ((N + 127) / 128) * mx_stages(K) * 1024;
+}
+
+cudaError_t launch_mx_weight_scales(const uint8_t* scales, int E, int halves, int N, int K, uint8_t* out,
+                                    cudaStream_t st) {
+  const long words = (long)(mx_weight_scale_bytes(E, halves, N, K) / 4);
+  const int ctas = (int)std::min<long>(152 * 16, (words + 255) / 256);
+  k_mx_weight_scales<<<ctas, 256, 0, st>>>(scales, halves, N, mx_blocks(K), (N + 127) / 128, 2 * mx_stages(K), words,
+                                           reinterpret_cast<uint32_t*>(out));
+  return cudaGetLastError();
+}
+
+cudaError_t mx_weight_map(CUtensorMap* m, const uint8_t* codes, long rows, int K) {
+  return mx_code_map(m, codes, rows, K, 128);
+}
+
+cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int out_dtype, cudaStream_t st) {
+  const cudaError_t e = mx_code_map(&a.xmap, codes_x, slots, a.K, a.bn);
+  if (e != cudaSuccess) return e;
+  auto go = [&](auto elem) {
+    using T = decltype(elem);
+    return a.gated ? mx_launch<true, T>(a, st) : mx_launch<false, T>(a, st);
+  };
+  return TM_BY_DTYPE(out_dtype, go);
+}
+
+cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_t st) {
+  const int es = dtype_bytes(dtype);
+  const bool vec = ((uintptr_t)a.x) % 16 == 0 && (a.ld * es) % 16 == 0;
+  const long items = (long)a.x_rows * mx_stages(a.K);
+  const int ctas = (int)std::min<long>(152 * 16, (items + 7) / 8);
+  auto go = [&](auto elem) {
+    k_mx_rows_quantize<decltype(elem)><<<ctas, 256, 0, st>>>(a, vec);
+    return cudaGetLastError();
+  };
+  return TM_BY_DTYPE(dtype, go);
+}
+
+}  // namespace tmoe
