@@ -64,12 +64,35 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 
 // Instruction descriptor: E2M1 x E2M1, E8M0 scales, fp32 accumulator, both
-// operands K-major, M = 128; `id` is the first of the two scale bytes used
-// (0 or 2 of the chunk's four).
-__device__ __forceinline__ uint32_t mx_idesc(int n, int id) {
-  return ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(128 >> 4) << 24) | ((uint32_t)id << 29);
+// operands K-major, M = 128. Bits 4 and 29 take the first of the two scale
+// bytes used (0 or 2 of the chunk's four).
+__device__ __forceinline__ uint32_t mx_idesc(int n) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
 }
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool mx_elect() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait_abort by a whole warp, with one answer for it.
+__device__ __forceinline__ bool mx_wait_warp(uint64_t* mbar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_abort(mbar, parity, abort, limit));
+}
+
+// Position in the ring of stages: slot and the parity of its use.
+struct MxRing {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int ring) {
+    if (++slot == ring) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 struct MxBars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
@@ -121,6 +144,7 @@ __device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring) {
 template <bool GATED>
 __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
                           uint64_t limit) {
+  MxRing r;
   int it = 0;
   bool ok = true;
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
@@ -128,14 +152,13 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
     const int wrow = m.expert * (GATED ? 2 * a.N : a.N) + m.tile * 128;
     const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles + m.tile) * g.stages * 1024;
     const size_t xsf = (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
-    for (int s = 0; s < g.stages; ++s, ++it) {
-      const int slot = it % g.ring;
-      if (it >= g.ring && !mbar_wait_abort(&B.empty[slot], ((it / g.ring) - 1) & 1, abort, limit)) {
+    for (int s = 0; s < g.stages; ++s, ++it, r.next(g.ring)) {
+      if (it >= g.ring && !mbar_wait_abort(&B.empty[r.slot], r.phase ^ 1, abort, limit)) {
         ok = false;
         break;
       }
-      unsigned char* st = smem + (size_t)slot * g.stage_bytes;
-      uint64_t* bar = &B.full[slot];
+      unsigned char* st = smem + (size_t)r.slot * g.stage_bytes;
+      uint64_t* bar = &B.full[r.slot];
       mbar_arrive_expect_tx(bar, g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes);
       mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
       if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
@@ -152,48 +175,74 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   }
 }
 
-template <bool GATED>
+// The MMAs of one stage: the chunks' scales to tensor memory, then one MMA per
+// 64 columns (`steps` of them) and half. Run by a whole warp, of which `lead`
+// is one thread: the operands are then the same for the warp, which keeps them
+// in uniform registers; issued from a single thread's branch, each
+// instruction cost 110-120 cycles of moving its operands there.
+template <bool GATED, int NRB>
+__device__ __forceinline__ void mx_issue_stage(uint32_t st, uint32_t b_bytes, uint32_t tmem, uint32_t d, uint32_t dup,
+                                               uint32_t idesc, int steps, bool first, bool lead) {
+  constexpr int H = GATED ? 2 : 1;
+  const uint32_t sfa = st + H * kMxTileBytes + b_bytes, sfb = sfa + H * 1024;
+  const uint32_t tsfa = tmem + kMxSfCol, tsfb = tsfa + 8u * H;
+  const uint64_t adesc = smem_desc_sw128(st), bdesc = smem_desc_sw128(st + H * kMxTileBytes);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if (c * 2 < steps) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (lead) mx_copy_scales(tsfa + (uint32_t)(c * H + h) * 4, sfa + h * 1024 + c * 512);
+#pragma unroll
+      for (int r = 0; r < NRB; ++r)
+        if (lead) mx_copy_scales(tsfb + (uint32_t)(c * NRB + r) * 4, sfb + (uint32_t)(c * NRB + r) * 512);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < steps) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (lead)
+          mx_mma(d + (h ? dup : 0u), adesc + (uint64_t)(h * (kMxTileBytes >> 4) + k * 2), bdesc + (uint64_t)(k * 2),
+                 idesc | ((uint32_t)((k & 1) * 2) << 4) | ((uint32_t)((k & 1) * 2) << 29),
+                 tsfa + (uint32_t)((k >> 1) * H + h) * 4, tsfb + (uint32_t)((k >> 1) * NRB) * 4,
+                 !first || k > 0 ? 1u : 0u);
+    }
+  }
+}
+
+template <bool GATED, int NRB>
 __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
                           volatile int* abort, uint64_t limit) {
+  MxRing r;
   int it = 0, nu = 0;
   bool ok = true;
-  const int halves = GATED ? 2 : 1;
+  constexpr int H = GATED ? 2 : 1;
+  const bool lead = mx_elect();
+  const uint32_t base = smem_u32(smem);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
     const MxUnit m = mx_unit(a, u, g.tiles);
-    const int n16 = (m.rows + 15) / 16 * 16;
+    const uint32_t idesc = mx_idesc((m.rows + 15) / 16 * 16);
     const int buf = nu & 1;
-    if (nu >= 2 && !mbar_wait_abort(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, limit)) break;
+    if (nu >= 2 && !mx_wait_warp(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, limit)) break;
     tc_fence_after();
-    const uint32_t d = tmem + (uint32_t)(buf * halves * a.bn);
-    for (int s = 0; s < g.stages; ++s, ++it) {
-      const int slot = it % g.ring;
-      if (!mbar_wait_abort(&B.full[slot], (it / g.ring) & 1, abort, limit)) {
+    const uint32_t d = tmem + (uint32_t)(buf * H * a.bn);
+    for (int s = 0; s < g.stages; ++s, ++it, r.next(g.ring)) {
+      if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, limit)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t st = smem_u32(smem) + (uint32_t)slot * g.stage_bytes;
-      const uint32_t sf = st + g.a_bytes + g.b_bytes;
-      const int steps = min(4, g.ksteps - s * 4);
-      const uint32_t tsfa = tmem + kMxSfCol, tsfb = tsfa + 8u * halves;
-      for (int c = 0; c < 2 && c * 2 < steps; ++c) {
-        for (int h = 0; h < halves; ++h) mx_copy_scales(tsfa + (uint32_t)(c * halves + h) * 4, sf + h * 1024 + c * 512);
-        for (int r = 0; r < a.nrb; ++r)
-          mx_copy_scales(tsfb + (uint32_t)(c * a.nrb + r) * 4, sf + g.sfa_bytes + (uint32_t)(c * a.nrb + r) * 512);
-      }
-      const uint64_t bdesc = smem_desc_sw128(st + g.a_bytes);
-      for (int k = 0; k < steps; ++k) {
-        const uint32_t idesc = mx_idesc(n16, (k & 1) * 2);
-        const uint32_t c = (uint32_t)(k >> 1);
-        for (int h = 0; h < halves; ++h) {
-          const uint64_t adesc = smem_desc_sw128(st + h * kMxTileBytes);
-          mx_mma(d + (uint32_t)(h * a.bn), adesc + (uint64_t)(k * 2), bdesc + (uint64_t)(k * 2), idesc,
-                 tsfa + (c * halves + h) * 4, tsfb + c * a.nrb * 4, s > 0 || k > 0 ? 1u : 0u);
-        }
-      }
-      tc_commit(&B.empty[slot]);
+      const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes;
+      const int steps = g.ksteps - s * 4;
+      if (steps >= 4)
+        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem, d, (uint32_t)a.bn, idesc, 4, s == 0, lead);
+      else
+        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem, d, (uint32_t)a.bn, idesc, steps, s == 0, lead);
+      if (lead) tc_commit(&B.empty[r.slot]);
     }
-    if (ok) tc_commit(&B.acc_full[buf]);
+    if (ok && lead) tc_commit(&B.acc_full[buf]);
   }
   if (*abort && it > 0) {
     int never = 0;
@@ -213,8 +262,7 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
     const MxUnit m = mx_unit(a, u, g.tiles);
     const int buf = nu & 1;
     const int n = m.tile * 128 + quarter * 32 + lane;
-    const bool ok = mbar_wait_abort(&B.acc_full[buf], (nu >> 1) & 1, abort, limit);
-    if (!__all_sync(0xFFFFFFFFu, ok)) return;
+    if (!mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, limit)) return;
     tc_fence_after();
     const uint32_t d = tmem + lane_base + (uint32_t)(buf * (GATED ? 2 : 1) * a.bn);
     for (int c0 = part * 32; c0 < m.rows; c0 += 64) {
@@ -247,7 +295,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   unsigned char* smem = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // (the same for the warp, and known to be)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ring; ++i) {
       mbar_init(&bars.full[i], 1);
@@ -272,8 +320,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
     mx_epilogue<GATED, T>(a, g, bars, tmem, abort, limit);
   } else if (threadIdx.x == kMxEpiWarps * 32) {
     mx_loader<GATED>(a, g, bars, smem, abort, limit);
-  } else if (threadIdx.x == (kMxEpiWarps + 1) * 32) {
-    mx_issuer<GATED>(a, g, bars, smem, tmem, abort, limit);
+  } else if (warp == kMxEpiWarps + 1) {
+    if (a.nrb == 1)
+      mx_issuer<GATED, 1>(a, g, bars, smem, tmem, abort, limit);
+    else
+      mx_issuer<GATED, 2>(a, g, bars, smem, tmem, abort, limit);
   }
   tc_fence_before();
   __syncthreads();
