@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace tmoe {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -21,49 +23,80 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements as fp32. `vec`: p is aligned to 16 bytes and N
-// elements are whole 16-byte words; else one element at a time.
-template <int N, typename T>
-__device__ __forceinline__ void load_f32(const T* __restrict__ p, bool vec, float (&v)[N]) {
-  constexpr int PER = 16 / (int)sizeof(T);
-  static_assert(N % PER == 0, "whole 16-byte words");
-  if (vec) {
+// Eight consecutive elements, of which the first n (0..8) exist. VEC: the
+// elements are whole 16-byte words at an aligned address and n is 0 or 8; the
+// words are then loaded without a branch, and converted where they are used,
+// so that a thread's loads can all be in flight at once.
+template <typename T, bool VEC>
+struct Eight {
+  static constexpr int kWords = 8 * (int)sizeof(T) / 16;
+  uint4 q[kWords];
+
+  __device__ __forceinline__ void load(const T* __restrict__ p, int n) {
+    if (VEC) {
 #pragma unroll
-    for (int c = 0; c < N / PER; ++c) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + c);
-      const T* t = reinterpret_cast<const T*>(&q);
+      for (int w = 0; w < kWords; ++w)
+        q[w] = n == 8 ? __ldg(reinterpret_cast<const uint4*>(p) + w) : make_uint4(0, 0, 0, 0);
+    } else {
+      T* t = reinterpret_cast<T*>(q);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[c * PER + i] = to_f32(t[i]);
+      for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : from_f32<T>(0.0f);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32(p[i]);
   }
+  __device__ __forceinline__ void to(float (&v)[8]) const {
+    const T* t = reinterpret_cast<const T*>(q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+  }
+  __device__ __forceinline__ void from(const float (&v)[8]) {
+    T* t = reinterpret_cast<T*>(q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+  }
+  __device__ __forceinline__ void store(T* __restrict__ p, int n) const {
+    if (VEC) {
+      if (n == 8) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) reinterpret_cast<uint4*>(p)[w] = q[w];
+      }
+    } else {
+      const T* t = reinterpret_cast<const T*>(q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = t[i];
+    }
+  }
+};
+
+// Whether rows of `cols` elements of `es` bytes, `ld` elements apart, can be
+// read as Eight<T, true>.
+inline bool eights(const void* p, int64_t ld, int64_t cols, int es) {
+  return ((uintptr_t)p) % 16 == 0 && (ld * es) % 16 == 0 && cols % 8 == 0;
 }
 
-template <int N, typename T>
-__device__ __forceinline__ void store_f32(T* __restrict__ p, bool vec, const float (&v)[N]) {
-  constexpr int PER = 16 / (int)sizeof(T);
-  static_assert(N % PER == 0, "whole 16-byte words");
-  if (vec) {
-#pragma unroll
-    for (int c = 0; c < N / PER; ++c) {
-      uint4 q;
-      T* t = reinterpret_cast<T*>(&q);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(v[c * PER + i]);
-      reinterpret_cast<uint4*>(p)[c] = q;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = from_f32<T>(v[i]);
+// n / d for 0 <= n < 2^31 by one multiplication: m = floor(2^(31+L) / d) + 1
+// with L = ceil(log2 d) is at most 2^(31+L)/d + 1, and the excess times n stays
+// below 2^(31+L), so the quotient is exact.
+struct FastDiv {
+  uint32_t d, m, shift;
+  explicit FastDiv(uint32_t div) : d(div) {
+    uint32_t l = 0;
+    while ((1ull << l) < div) ++l;
+    shift = 31 + l;
+    m = (uint32_t)((1ull << shift) / div + 1);
   }
-}
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> shift); }
+};
 
 }  // namespace tmoe
 
-// Calls F with a value of the element type of tm_dtype `d`.
+// Calls F with a value of the element type of tm_dtype `d` (and with whether
+// its rows are whole eights).
 #define TM_BY_DTYPE(d, F)                     \
   ((d) == TM_F32    ? F(float())              \
    : (d) == TM_BF16 ? F(__nv_bfloat16())      \
                     : F(__half()))
+#define TM_BY_DTYPE_VEC(d, vec, F)                                                                              \
+  ((d) == TM_F32 ? ((vec) ? F(float(), std::true_type()) : F(float(), std::false_type()))                       \
+   : (d) == TM_BF16 ? ((vec) ? F(__nv_bfloat16(), std::true_type()) : F(__nv_bfloat16(), std::false_type()))    \
+                    : ((vec) ? F(__half(), std::true_type()) : F(__half(), std::false_type())))

@@ -134,6 +134,8 @@ tm_status mx_check(const tm_mxfp4* h, const MxCall& c, size_t ws_bytes) {
   if (((uintptr_t)c.out) % dtype_bytes(c.out_dtype))
     return status_fail(TM_EINVAL, "out must be aligned to its elements");
   if (c.rows > d.max_rows) return status_fail(TM_EINVAL, "%d rows exceed the prepared max_rows=%d", c.rows, d.max_rows);
+  if ((long)c.x_rows * mx_stages(d.K) > (1L << 30))
+    return status_fail(TM_EUNSUPPORTED, "%d rows of K=%d are too large", c.x_rows, d.K);
   if (!c.ws) return status_fail(TM_EWORKSPACE, "workspace is NULL");
   if (((uintptr_t)c.ws) % kMxAlign) return status_fail(TM_EWORKSPACE, "workspace must be %zu-byte aligned", kMxAlign);
   const size_t need = mx_layout(d, c.rows).total;

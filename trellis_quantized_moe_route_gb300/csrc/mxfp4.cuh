@@ -13,14 +13,16 @@ namespace tmoe {
 // layer's UE8M0 rule with E2M1's largest value, e = ceil(log2(fp32(amax / 6)))
 // clamped to [-127, 127], so that nothing saturates; amax = 0 gives -127. A
 // block that holds an infinity or a NaN has no finite scale: 255 (NaN).
+// Without the division: amax = m 2^k, 1 <= m < 2, and amax / 6 = (m / 1.5)
+// 2^(k - 2), whose exponent rounds up to k - 2 while m <= 1.5 and to k - 1
+// above, where m / 1.5 lies at least 2/3 of an ulp above 1 and so rounds above
+// 1, except at k = -125: there the quotient is subnormal with half the
+// precision, and one ulp above 1.5 still rounds to 1. (Checked against the
+// division at every exponent.)
 __device__ __forceinline__ uint32_t mxfp4_scale_byte(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F800000u) return 255u;
-  const uint32_t b = __float_as_uint(__fdiv_rn(__uint_as_float(amax_bits), 6.0f));
-  if (b == 0) return 0u;
-  const uint32_t man = b & 0x7FFFFFu;
-  // (a subnormal quotient is below 2^-126: its exponent clamps to -127 or, above 2^-127, is -126)
-  if ((b >> 23) == 0) return man > 0x400000u ? 1u : 0u;
-  return (b >> 23) + (man != 0 ? 1u : 0u);
+  const uint32_t f = amax_bits >> 23, man = amax_bits & 0x7FFFFFu;
+  const uint32_t byte = (uint32_t)max((int)f - 2 + (man > 0x400000u + (f == 2u ? 1u : 0u) ? 1 : 0), 0);
+  return f == 255u ? 255u : byte;
 }
 
 // 2^-(e) for the scale byte e + 127 of a finite block.
@@ -46,6 +48,22 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       : "=r"(r)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
+}
+
+// Quantises a block spread over four neighbouring lanes, eight values each:
+// returns the lane's eight codes, `byte` the block's scale. All 32 lanes take
+// part. |v| compares as bits like the values, a NaN above every number.
+__device__ __forceinline__ uint32_t mxfp4_block(float (&v)[8], uint32_t& byte) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  byte = mxfp4_scale_byte(m);
+  const float inv = mxfp4_inverse(byte);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] *= inv;
+  return byte == 255u ? 0u : e2m1x8(v);
 }
 
 // Eight codes -> four fp16 pairs (exact).

@@ -7,10 +7,6 @@
 
 namespace tmoe {
 
-// rows of x (stride ld elements) -> codes and scales in row order.
-cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t ld, long rows, int K, uint8_t* codes,
-                                  uint8_t* scales, cudaStream_t st);
-
 // Blocks of 32 along K, and the pieces the tensor-core kernels walk: a scale
 // chunk covers 128 columns, a pipeline stage 256 (the last one filled up).
 __host__ __device__ inline int mx_blocks(int K) { return (K + 31) / 32; }

@@ -16,84 +16,113 @@ namespace {
 
 // Four lanes take a block, eight values each: the block's maximum is two
 // shuffles away, and a warp reads eight blocks (512 or 1024 bytes) in one or
-// two loads of 16 bytes a lane.
-template <typename T>
-__global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ x, int64_t ld, long rows, int K, bool vec,
-                                                        uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int nb = (K + 31) / 32;
-  const long total = rows * nb * 4;
-  const long stride = (long)gridDim.x * blockDim.x;
-  const long padded = (total + 31) / 32 * 32;  // whole warps take part in the shuffles
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < padded; i += stride) {
+// two loads of 16 bytes a lane. A CTA takes kQuTile such eighths, four of a
+// thread in flight at once. The row of an eighth comes from one
+// multiplication: with a 64-bit division a tile, the same kernels took twice
+// as long (163840 x 1536 bf16: 193 and 187 us).
+constexpr int kQuUnroll = 4;
+constexpr int kQuTile = 256 * kQuUnroll;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ x, int64_t ld, uint32_t total, FastDiv per,
+                                                        int K, uint32_t* __restrict__ codes,
+                                                        uint8_t* __restrict__ scales) {
+  const uint32_t tile = blockIdx.x * kQuTile + threadIdx.x;
+  Eight<T, VEC> e[kQuUnroll];
+#pragma unroll
+  for (int u = 0; u < kQuUnroll; ++u) {
+    const uint32_t i = tile + u * 256, r = per.div(i);
+    const int col = (int)(i - r * per.d) * 8;
+    e[u].load(x + (int64_t)r * ld + col, i < total ? max(0, min(8, K - col)) : 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kQuUnroll; ++u) {
+    const uint32_t i = tile + u * 256;
     float v[8];
-    const long blk = i >> 2;
-    const long row = blk / nb;
-    const int col = (int)(blk - row * nb) * 32 + (int)(i & 3) * 8;
-    const T* p = x + row * ld + col;
-    if (i < total && col + 8 <= K) {
-      load_f32<8>(p, vec, v);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = i < total && col + c < K ? to_f32(p[c]) : 0.0f;
-    }
-    uint32_t m = 0;  // |v| as bits: ordered like the values, a NaN above every number
-#pragma unroll
-    for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t byte = mxfp4_scale_byte(m);
-    const float inv = mxfp4_inverse(byte);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] *= inv;
-    const uint32_t q = byte == 255u ? 0u : e2m1x8(v);
+    e[u].to(v);
+    uint32_t byte;
+    const uint32_t q = mxfp4_block(v, byte);
     if (i < total) {
       codes[i] = q;
-      if ((i & 3) == 0) scales[blk] = (uint8_t)byte;
+      if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
     }
   }
 }
 
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_mxfp4_dequantize(const uint32_t* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales, long rows, int K,
-                                                          bool vec, T* __restrict__ out) {
-  const int nb = (K + 31) / 32;
-  const long total = rows * nb * 4;
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
-    const long blk = i >> 2;
-    const long row = blk / nb;
-    const int col = (int)(blk - row * nb) * 32 + (int)(i & 3) * 8;
-    float v[8];
-    e2m1x8_to_f32(__ldg(codes + i), v);
-    const float s = mxfp4_power(__ldg(scales + blk));
+                                                          const uint8_t* __restrict__ scales, uint32_t total,
+                                                          FastDiv per, int K, T* __restrict__ out) {
+  const uint32_t tile = blockIdx.x * kQuTile + threadIdx.x;
+  uint32_t c[kQuUnroll], b[kQuUnroll];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] *= s;
-    T* o = out + row * K + col;
-    if (col + 8 <= K) {
-      store_f32<8>(o, vec, v);
-    } else {
-      for (int c = 0; col + c < K; ++c) o[c] = from_f32<T>(v[c]);
-    }
+  for (int u = 0; u < kQuUnroll; ++u) {
+    const uint32_t i = tile + u * 256;
+    c[u] = i < total ? __ldg(codes + i) : 0u;
+    b[u] = i < total ? __ldg(scales + (i >> 2)) : 0u;
+  }
+#pragma unroll
+  for (int u = 0; u < kQuUnroll; ++u) {
+    const uint32_t i = tile + u * 256, r = per.div(i);
+    const int col = (int)(i - r * per.d) * 8;
+    float v[8];
+    e2m1x8_to_f32(c[u], v);
+    const float s = mxfp4_power(b[u]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= s;
+    Eight<T, VEC> e;
+    e.from(v);
+    e.store(out + (int64_t)r * K + col, i < total ? max(0, min(8, K - col)) : 0);
   }
 }
 
-int quant_ctas(long items) { return (int)std::min<long>(152 * 16, (items + 255) / 256); }
+// Calls f(first row, rows) over pieces of less than 2^30 eighths each, so that
+// the kernels' indexes stay in 32 bits.
+template <typename F>
+cudaError_t by_rows(long rows, int per, F f) {
+  const long most = std::max(1L, (1L << 30) / per);
+  for (long r = 0; r < rows; r += most) {
+    const cudaError_t e = f(r, std::min(most, rows - r));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+unsigned quant_ctas(uint32_t items) { return (items + kQuTile - 1) / kQuTile; }
+
+cudaError_t mxfp4_quantize(const void* x, int dtype, int64_t ld, long rows, int K, uint8_t* codes, uint8_t* scales,
+                           cudaStream_t st) {
+  const int es = dtype_bytes(dtype), nb = (K + 31) / 32, per = nb * 4;
+  auto go = [&](auto elem, auto vec) {
+    using T = decltype(elem);
+    return by_rows(rows, per, [&](long r, long n) {
+      const uint32_t total = (uint32_t)(n * per);
+      k_mxfp4_quantize<T, decltype(vec)::value><<<quant_ctas(total), 256, 0, st>>>(
+          static_cast<const T*>(x) + r * ld, ld, total, FastDiv(per), K, reinterpret_cast<uint32_t*>(codes) + r * per,
+          scales + r * nb);
+      return cudaGetLastError();
+    });
+  };
+  return TM_BY_DTYPE_VEC(dtype, eights(x, ld, K, es), go);
+}
+
+cudaError_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long rows, int K, void* out, int dtype,
+                             cudaStream_t st) {
+  const int es = dtype_bytes(dtype), nb = (K + 31) / 32, per = nb * 4;
+  auto go = [&](auto elem, auto vec) {
+    using T = decltype(elem);
+    return by_rows(rows, per, [&](long r, long n) {
+      const uint32_t total = (uint32_t)(n * per);
+      k_mxfp4_dequantize<T, decltype(vec)::value><<<quant_ctas(total), 256, 0, st>>>(
+          reinterpret_cast<const uint32_t*>(codes) + r * per, scales + r * nb, total, FastDiv(per), K,
+          static_cast<T*>(out) + r * K);
+      return cudaGetLastError();
+    });
+  };
+  return TM_BY_DTYPE_VEC(dtype, eights(out, K, K, es), go);
+}
 
 }  // namespace
-
-cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t ld, long rows, int K, uint8_t* codes,
-                                  uint8_t* scales, cudaStream_t st) {
-  if (rows == 0) return cudaSuccess;
-  const int es = dtype_bytes(dtype);
-  const bool vec = ((uintptr_t)x) % 16 == 0 && (ld * es) % 16 == 0;
-  auto go = [&](auto elem) {
-    using T = decltype(elem);
-    k_mxfp4_quantize<T><<<quant_ctas(rows * ((K + 31) / 32) * 4), 256, 0, st>>>(
-        static_cast<const T*>(x), ld, rows, K, vec, reinterpret_cast<uint32_t*>(codes), scales);
-    return cudaGetLastError();
-  };
-  return TM_BY_DTYPE(dtype, go);
-}
 
 }  // namespace tmoe
 
@@ -106,13 +135,13 @@ tm_status trellis_moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t ld, i
   set_last_error("");
   if (!dtype_ok(dtype)) return status_fail(TM_EINVAL, "dtype=%d is not a tm_dtype", dtype);
   if (rows < 0) return status_fail(TM_EINVAL, "rows=%lld < 0", (long long)rows);
-  if (K < 1) return status_fail(TM_EINVAL, "K=%d must be >= 1", K);
+  if (K < 1 || K > (1 << 30)) return status_fail(TM_EINVAL, "K=%d outside 1..%d", K, 1 << 30);
   if (ld < K) return status_fail(TM_EINVAL, "ld=%lld is less than K=%d", (long long)ld, K);
   if (rows == 0) return TM_OK;
   if (!x || !codes || !scales) return status_fail(TM_EINVAL, "x, codes and scales must be non-NULL");
   if (((uintptr_t)x) % dtype_bytes(dtype)) return status_fail(TM_EINVAL, "x must be aligned to its elements");
   if (((uintptr_t)codes) % 16) return status_fail(TM_EINVAL, "codes must be 16-byte aligned");
-  const cudaError_t e = launch_mxfp4_quantize(x, dtype, ld, (long)rows, K, codes, scales, (cudaStream_t)stream);
+  const cudaError_t e = mxfp4_quantize(x, dtype, ld, (long)rows, K, codes, scales, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "MXFP4 quantise");
 }
 
@@ -121,20 +150,12 @@ tm_status trellis_moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scal
   set_last_error("");
   if (!dtype_ok(dtype)) return status_fail(TM_EINVAL, "dtype=%d is not a tm_dtype", dtype);
   if (rows < 0) return status_fail(TM_EINVAL, "rows=%lld < 0", (long long)rows);
-  if (K < 1) return status_fail(TM_EINVAL, "K=%d must be >= 1", K);
+  if (K < 1 || K > (1 << 30)) return status_fail(TM_EINVAL, "K=%d outside 1..%d", K, 1 << 30);
   if (rows == 0) return TM_OK;
   if (!codes || !scales || !out) return status_fail(TM_EINVAL, "codes, scales and out must be non-NULL");
   if (((uintptr_t)codes) % 16) return status_fail(TM_EINVAL, "codes must be 16-byte aligned");
-  const int es = dtype_bytes(dtype);
-  if (((uintptr_t)out) % es) return status_fail(TM_EINVAL, "out must be aligned to its elements");
-  const bool vec = ((uintptr_t)out) % 16 == 0 && ((size_t)K * es) % 16 == 0;
-  auto go = [&](auto elem) {
-    using T = decltype(elem);
-    k_mxfp4_dequantize<T><<<quant_ctas(rows * ((K + 31) / 32) * 4), 256, 0, (cudaStream_t)stream>>>(
-        reinterpret_cast<const uint32_t*>(codes), scales, (long)rows, K, vec, static_cast<T*>(out));
-    return cudaGetLastError();
-  };
-  const cudaError_t e = TM_BY_DTYPE(dtype, go);
+  if (((uintptr_t)out) % dtype_bytes(dtype)) return status_fail(TM_EINVAL, "out must be aligned to its elements");
+  const cudaError_t e = mxfp4_dequantize(codes, scales, (long)rows, K, out, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "MXFP4 dequantise");
 }
 

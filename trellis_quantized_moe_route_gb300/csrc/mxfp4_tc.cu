@@ -399,55 +399,56 @@ __global__ void __launch_bounds__(256) k_mx_weight_scales(const uint8_t* __restr
   }
 }
 
-// A warp takes 256 columns (eight blocks, four lanes each) of one row of x.
-template <typename T>
-__global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, bool vec) {
+// A warp takes 512 columns of one row of x, 256 (eight blocks, four lanes each)
+// at a time, both loads in flight at once.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, int stages, FastDiv pairs, FastDiv bn,
+                                                          int items) {
   const int lane = threadIdx.x & 31;
-  const int nb = mx_blocks(a.K), stages = mx_stages(a.K);
-  const long warps = (long)gridDim.x * 8, items = (long)a.x_rows * stages;
-  const T* x = static_cast<const T*>(a.x);
-  for (long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5); i < items; i += warps) {
-    const int row = (int)(i / stages), s = (int)(i - (long)row * stages);
-    const int blk = s * 8 + (lane >> 2), col = blk * 32 + (lane & 3) * 8;
-    const T* p = x + (size_t)row * a.ld + col;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= items) return;
+  const int nb = mx_blocks(a.K);
+  const int row = (int)pairs.div(i), s0 = (i - row * (int)pairs.d) * 2;
+  const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ld;
+  const int first = a.slot_of_route ? a.slot_of_route[row * a.topk] : row;
+  Eight<T, VEC> e[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int col = (s0 + u) * 256 + lane * 8;
+    e[u].load(x + col, max(0, min(8, a.K - col)));
+  }
+  uint32_t q[2], word[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
     float v[8];
-    if (col + 8 <= a.K) {
-      load_f32<8>(p, vec, v);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = col + c < a.K ? to_f32(p[c]) : 0.0f;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t byte = mxfp4_scale_byte(m);
-    const float inv = mxfp4_inverse(byte);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] *= inv;
-    const uint32_t q = byte == 255u ? 0u : e2m1x8(v);
+    e[u].to(v);
+    uint32_t byte;
+    q[u] = mxfp4_block(v, byte);
     // the four bytes of a chunk (128 columns, 16 lanes) in its first lane
     const int base = lane & 16;
-    uint32_t word = byte;
-    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 4) << 8;
-    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 8) << 16;
-    word |= __shfl_sync(0xFFFFFFFFu, byte, base + 12) << 24;
-    for (int j = 0; j < a.topk; ++j) {
-      const int r = row * a.topk + j;
-      const int slot = a.slot_of_route ? a.slot_of_route[r] : r;
-      if (slot < 0) {
-        if (s == 0) {
-          char* o = static_cast<char*>(a.out) + (size_t)r * a.out_row_bytes;
-          for (int b = lane * 2; b < a.out_row_bytes; b += 64) *reinterpret_cast<uint16_t*>(o + b) = 0;
-        }
-        continue;
+    word[u] = byte;
+    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 4) << 8;
+    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 8) << 16;
+    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 12) << 24;
+  }
+  for (int j = 0; j < a.topk; ++j) {
+    const int r = row * a.topk + j;
+    const int slot = j == 0 ? first : a.slot_of_route[r];
+    if (slot < 0) {
+      if (s0 == 0) {
+        char* o = static_cast<char*>(a.out) + (size_t)r * a.out_row_bytes;
+        for (int b = lane * 2; b < a.out_row_bytes; b += 64) *reinterpret_cast<uint16_t*>(o + b) = 0;
       }
-      if (blk < nb) *reinterpret_cast<uint32_t*>(a.codes + ((size_t)slot * nb + blk) * 16 + (lane & 3) * 4) = q;
-      if ((lane & 15) == 0) {
-        const int b = slot / a.bn, t = slot - b * a.bn;
+      continue;
+    }
+    const int b = (int)bn.div(slot), t = slot - b * (int)bn.d;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int s = s0 + u, blk = s * 8 + (lane >> 2);
+      if (blk < nb) *reinterpret_cast<uint32_t*>(a.codes + ((size_t)slot * nb + blk) * 16 + (lane & 3) * 4) = q[u];
+      if ((lane & 15) == 0 && s < stages) {
         const size_t chunk = ((size_t)b * stages * 2 + s * 2 + (lane >> 4)) * a.nrb + (t >> 7);
-        *reinterpret_cast<uint32_t*>(a.scales + chunk * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4) = word;
+        *reinterpret_cast<uint32_t*>(a.scales + chunk * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4) = word[u];
       }
     }
   }
@@ -484,14 +485,14 @@ cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int ou
 
 cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_t st) {
   const int es = dtype_bytes(dtype);
-  const bool vec = ((uintptr_t)a.x) % 16 == 0 && (a.ld * es) % 16 == 0;
-  const long items = (long)a.x_rows * mx_stages(a.K);
-  const int ctas = (int)std::min<long>(152 * 16, (items + 7) / 8);
-  auto go = [&](auto elem) {
-    k_mx_rows_quantize<decltype(elem)><<<ctas, 256, 0, st>>>(a, vec);
+  const int stages = mx_stages(a.K), pairs = (stages + 1) / 2;
+  const int items = a.x_rows * pairs;
+  auto go = [&](auto elem, auto vec) {
+    k_mx_rows_quantize<decltype(elem), decltype(vec)::value><<<(items + 7) / 8, 256, 0, st>>>(a, stages, FastDiv(pairs),
+                                                                                             FastDiv(a.bn), items);
     return cudaGetLastError();
   };
-  return TM_BY_DTYPE(dtype, go);
+  return TM_BY_DTYPE_VEC(dtype, eights(a.x, a.ld, a.K, es), go);
 }
 
 }  // namespace tmoe

@@ -13,104 +13,101 @@ namespace tmoe {
 
 namespace {
 
-constexpr int kCbVec = 8;  // elements of a thread
-
-template <typename T>
-__global__ void __launch_bounds__(256) k_combine_routes(const T* __restrict__ rows, const float* __restrict__ w, int T_,
-                                                        int k, int H, bool vec, float* __restrict__ out) {
-  const int per = (H + kCbVec - 1) / kCbVec;
-  const long total = (long)T_ * per;
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
-    const long t = i / per;
-    const int h = (int)(i - t * per) * kCbVec;
-    float acc[kCbVec] = {};
-    const bool whole = h + kCbVec <= H;
-    for (int j = 0; j < k; ++j) {
-      const float wj = __ldg(w + t * k + j);
-      const T* row = rows + ((size_t)t * k + j) * H + h;
-      if (wj == 0.0f) continue;
-      if (whole) {
-        float v[kCbVec];
-        load_f32<kCbVec>(row, vec, v);
+// A thread takes eight columns of a token; four routes' loads are in flight at
+// once.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_combine_routes(const T* __restrict__ rows, const float* __restrict__ w,
+                                                        uint32_t total, FastDiv per, int k, int H,
+                                                        float* __restrict__ out) {
+  const uint32_t n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= total) return;
+  const size_t t = per.div(n);
+  const int h = (int)(n - (uint32_t)t * per.d) * 8, len = min(8, H - h);
+  float acc[8] = {};
+  const T* row = rows + t * k * H + h;
+  const float* wt = w + t * k;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    Eight<T, VEC> e[4];
+    float wj[4];
 #pragma unroll
-        for (int x = 0; x < kCbVec; ++x) acc[x] = fmaf(wj, v[x], acc[x]);
-      } else {
-        for (int x = 0; h + x < H; ++x) acc[x] = fmaf(wj, to_f32(row[x]), acc[x]);
-      }
+    for (int u = 0; u < 4; ++u) {
+      e[u].load(row + (size_t)(j0 + u) * H, j0 + u < k ? len : 0);
+      wj[u] = j0 + u < k ? __ldg(wt + j0 + u) : 0.0f;
     }
-    float* o = out + (size_t)t * H + h;
-    if (whole) {
-      store_f32<kCbVec>(o, vec, acc);
-    } else {
-      for (int x = 0; h + x < H; ++x) o[x] = acc[x];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float v[8];
+      e[u].to(v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = wj[u] != 0.0f ? fmaf(wj[u], v[x], acc[x]) : acc[x];
     }
   }
+  Eight<float, VEC> o;
+  o.from(acc);
+  o.store(out + t * H + h, len);
 }
 
 constexpr int kCbChunk = 8;  // routes whose dot products a block holds at once
 
-// One block per token.
-template <typename T>
+// One block per token; a thread takes eight columns at a time, the chunk's
+// loads all in flight.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_combine_routes_bwd(const T* __restrict__ rows, const float* __restrict__ w,
-                                                            const float* __restrict__ gout, int T_, int k, int H,
-                                                            bool vec, T* __restrict__ grows, float* __restrict__ gw) {
+                                                            const float* __restrict__ gout, int k, int H,
+                                                            T* __restrict__ grows, float* __restrict__ gw) {
   __shared__ float s_dot[8][kCbChunk];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = blockDim.x >> 5;
-  for (int t = blockIdx.x; t < T_; t += gridDim.x) {
-    for (int j0 = 0; j0 < k; j0 += kCbChunk) {
-      const int nj = min(kCbChunk, k - j0);
-      float dot[kCbChunk] = {};
-      for (int h = threadIdx.x * kCbVec; h < H; h += blockDim.x * kCbVec) {
-        float g[kCbVec];
-        const bool whole = h + kCbVec <= H;
-        if (whole) {
-          load_f32<kCbVec>(gout + (size_t)t * H + h, vec, g);
-        } else {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const size_t t = blockIdx.x;
+  for (int j0 = 0; j0 < k; j0 += kCbChunk) {
+    float dot[kCbChunk] = {}, wj[kCbChunk];
 #pragma unroll
-          for (int x = 0; x < kCbVec; ++x) g[x] = h + x < H ? gout[(size_t)t * H + h + x] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kCbChunk; ++j) {
-          if (j >= nj) break;
-          const size_t r = ((size_t)t * k + j0 + j) * H + h;
-          const float wj = w[(size_t)t * k + j0 + j];
-          float v[kCbVec];
-          if (whole) {
-            load_f32<kCbVec>(rows + r, vec, v);
-          } else {
-#pragma unroll
-            for (int x = 0; x < kCbVec; ++x) v[x] = h + x < H ? to_f32(rows[r + x]) : 0.0f;
-          }
-#pragma unroll
-          for (int x = 0; x < kCbVec; ++x) {
-            dot[j] = fmaf(g[x], v[x], dot[j]);
-            v[x] = wj * g[x];
-          }
-          if (grows) {
-            if (whole) {
-              store_f32<kCbVec>(grows + r, vec, v);
-            } else {
-              for (int x = 0; h + x < H; ++x) grows[r + x] = from_f32<T>(v[x]);
-            }
-          }
-        }
-      }
+    for (int j = 0; j < kCbChunk; ++j) wj[j] = j0 + j < k ? __ldg(w + t * k + j0 + j) : 0.0f;
+    for (int h = threadIdx.x * 8; h < H; h += blockDim.x * 8) {
+      const int len = min(8, H - h);
+      Eight<float, VEC> ge;
+      ge.load(gout + t * H + h, len);
+      float g[8];
+      const size_t base = (t * k + j0) * H + h;
       if (gw) {
+        Eight<T, VEC> e[kCbChunk];
+#pragma unroll
+        for (int j = 0; j < kCbChunk; ++j) e[j].load(rows + base + (size_t)j * H, j0 + j < k ? len : 0);
+        ge.to(g);
 #pragma unroll
         for (int j = 0; j < kCbChunk; ++j) {
+          float v[8];
+          e[j].to(v);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-          if (lane == 0) s_dot[warp][j] = dot[j];
+          for (int x = 0; x < 8; ++x) dot[j] = fmaf(g[x], v[x], dot[j]);
         }
-        __syncthreads();
-        if (threadIdx.x < nj) {
-          float s = 0.0f;
-          for (int u = 0; u < warps; ++u) s += s_dot[u][threadIdx.x];
-          gw[(size_t)t * k + j0 + threadIdx.x] = s;
-        }
-        __syncthreads();
       }
+      if (grows) {
+        ge.to(g);
+#pragma unroll
+        for (int j = 0; j < kCbChunk; ++j) {
+          float v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = wj[j] * g[x];
+          Eight<T, VEC> o;
+          o.from(v);
+          o.store(grows + base + (size_t)j * H, j0 + j < k ? len : 0);
+        }
+      }
+    }
+    if (gw) {
+#pragma unroll
+      for (int j = 0; j < kCbChunk; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
+        if (lane == 0) s_dot[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < kCbChunk && j0 + threadIdx.x < k) {
+        float s = 0.0f;
+        for (int u = 0; u < warps; ++u) s += s_dot[u][threadIdx.x];
+        gw[t * k + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
     }
   }
 }
@@ -124,8 +121,6 @@ tm_status combine_check(const void* rows, int32_t dtype, const float* w, int32_t
   if (((uintptr_t)rows) % dtype_bytes(dtype)) return status_fail(TM_EINVAL, "rows must be aligned to its elements");
   return TM_OK;
 }
-
-bool aligned16(const void* p, size_t row_bytes) { return ((uintptr_t)p) % 16 == 0 && row_bytes % 16 == 0; }
 
 }  // namespace
 
@@ -142,15 +137,17 @@ tm_status trellis_moe_combine_forward(const void* rows, int32_t dtype, const flo
   if (s != TM_OK) return s;
   if (T == 0) return TM_OK;
   if (!out || ((uintptr_t)out) % 4) return status_fail(TM_EINVAL, "out must be non-NULL and 4-byte aligned");
-  const bool vec = aligned16(rows, (size_t)H * dtype_bytes(dtype)) && aligned16(out, (size_t)H * 4);
-  const long items = (long)T * ((H + kCbVec - 1) / kCbVec);
-  const int ctas = (int)std::min<long>(152 * 16, (items + 255) / 256);
-  auto go = [&](auto elem) {
+  const int per = (H + 7) / 8;
+  if ((long)T * per > (1L << 30)) return status_fail(TM_EUNSUPPORTED, "T=%d rows of H=%d are too large", T, H);
+  const uint32_t items = (uint32_t)T * per;
+  auto go = [&](auto elem, auto vec) {
     using E = decltype(elem);
-    k_combine_routes<E><<<ctas, 256, 0, (cudaStream_t)stream>>>(static_cast<const E*>(rows), w, T, k, H, vec, out);
+    k_combine_routes<E, decltype(vec)::value><<<(items + 255) / 256, 256, 0, (cudaStream_t)stream>>>(
+        static_cast<const E*>(rows), w, items, FastDiv(per), k, H, out);
     return cudaGetLastError();
   };
-  const cudaError_t e = TM_BY_DTYPE(dtype, go);
+  const bool vec = eights(rows, H, H, dtype_bytes(dtype)) && eights(out, H, H, 4);
+  const cudaError_t e = TM_BY_DTYPE_VEC(dtype, vec, go);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "combine");
 }
 
@@ -166,16 +163,17 @@ tm_status trellis_moe_combine_backward(const void* rows, int32_t dtype, const fl
   if (!grad_rows && !grad_w) return status_fail(TM_EINVAL, "grad_rows and grad_w are both NULL");
   if (((uintptr_t)grad_rows) % dtype_bytes(dtype))
     return status_fail(TM_EINVAL, "grad_rows must be aligned to its elements");
-  const size_t row = (size_t)H * dtype_bytes(dtype);
-  const bool vec = aligned16(rows, row) && aligned16(grad_out, (size_t)H * 4) && aligned16(grad_rows, row);
-  const int ctas = std::min(T, 152 * 16);
-  auto go = [&](auto elem) {
+  const int es = dtype_bytes(dtype);
+  const bool vec = eights(rows, H, H, es) && eights(grad_out, H, H, 4) && eights(grad_rows, H, H, es);
+  // (as many threads as have a column group, whole warps)
+  const int threads = std::min(256, (H + 255) / 256 * 32);
+  auto go = [&](auto elem, auto v) {
     using E = decltype(elem);
-    k_combine_routes_bwd<E><<<ctas, 256, 0, (cudaStream_t)stream>>>(static_cast<const E*>(rows), w, grad_out, T, k, H,
-                                                                    vec, static_cast<E*>(grad_rows), grad_w);
+    k_combine_routes_bwd<E, decltype(v)::value><<<T, threads, 0, (cudaStream_t)stream>>>(
+        static_cast<const E*>(rows), w, grad_out, k, H, static_cast<E*>(grad_rows), grad_w);
     return cudaGetLastError();
   };
-  const cudaError_t e = TM_BY_DTYPE(dtype, go);
+  const cudaError_t e = TM_BY_DTYPE_VEC(dtype, vec, go);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "combine backward");
 }
 

@@ -65,19 +65,46 @@ struct RouterFwd {
   int32_t* part_n;
 };
 
-// Adds up `parts` CTAs' statistics and writes the results. Thread e of the
-// block owns expert e; every sum runs in CTA order.
-__device__ void router_finish(const RouterFwd& a, const float* __restrict__ pp, const int32_t* __restrict__ pc,
-                              const float* __restrict__ pz, const int32_t* __restrict__ pn, int parts) {
+// Adds up `parts` CTAs' statistics and writes the results: a warp adds every
+// (warps)-th part in order, then one thread an expert adds the warps' sums.
+template <int V>
+__device__ void router_finish(const RouterFwd& a, int parts, float (*s_acc)[V * 32], int (*s_cnt)[V * 32]) {
   __shared__ float s_dot[32];
   __shared__ int s_n;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  float acc[V] = {};
+  int cnt[V] = {};
+  for (int c0 = warp; c0 < parts; c0 += warps * 4) {
+    float p[4][V];
+    int n[4][V];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + u * warps, e = lane + 32 * i;
+        const bool in = c < parts && e < a.E;
+        p[u][i] = in ? a.part_prob[(size_t)c * a.E + e] : 0.0f;
+        n[u][i] = in ? a.part_counts[(size_t)c * a.E + e] : 0;
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc[i] += p[u][i];
+        cnt[i] += n[u][i];
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s_acc[warp][lane + 32 * i] = acc[i];
+    s_cnt[warp][lane + 32 * i] = cnt[i];
+  }
   if (warp == 0) {
     int n = 0;
     float z = 0.0f;
     for (int c = lane; c < parts; c += 32) {
-      n += pn[c];
-      z += pz[c];
+      n += a.part_n[c];
+      z += a.part_z[c];
     }
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     z = warp_sum(z);
@@ -92,74 +119,101 @@ __device__ void router_finish(const RouterFwd& a, const float* __restrict__ pp, 
   float dot = 0.0f;
   if (tid < a.E) {
     float p = 0.0f;
-    int cnt = 0;
-    for (int c = 0; c < parts; ++c) {
-      p += pp[(size_t)c * a.E + tid];
-      cnt += pc[(size_t)c * a.E + tid];
+    int c = 0;
+    for (int u = 0; u < warps; ++u) {
+      p += s_acc[u][tid];
+      c += s_cnt[u][tid];
     }
     p *= inv_n;
     a.prob[tid] = p;
-    a.counts[tid] = cnt;
-    dot = (float)cnt * inv_n / (float)a.k * p;
+    a.counts[tid] = c;
+    dot = (float)c * inv_n / (float)a.k * p;
   }
   dot = warp_sum(dot);
   if (lane == 0) s_dot[warp] = dot;
   __syncthreads();
   if (warp == 0) {
-    dot = lane < (int)(blockDim.x >> 5) ? s_dot[lane] : 0.0f;
+    dot = lane < warps ? s_dot[lane] : 0.0f;
     dot = warp_sum(dot);
     if (lane == 0) a.losses[0] = (float)a.E * dot;
   }
 }
 
-// One token by one warp. l[i]: the logit of expert lane + 32 i (absent: key 0,
-// below every float's). Adds the token's statistics to the lane's sums.
+// Keys of one token, expert lane + 32 i in place i (absent: 0, below every
+// float's), sorted descending within the lane; `perm` holds the places they
+// came from, four bits each, equal keys in order of place.
+template <int V>
+__device__ __forceinline__ void router_sort(uint32_t (&key)[V], uint32_t& perm) {
+  uint32_t id[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) id[i] = i;
+  // odd-even transposition: neighbours swap only when out of order, so it is stable
+#pragma unroll
+  for (int r = 0; r < V; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < V; i += 2) {
+      const bool sw = key[i + 1] > key[i];
+      const uint32_t k0 = key[i], k1 = key[i + 1], d0 = id[i], d1 = id[i + 1];
+      key[i] = sw ? k1 : k0;
+      key[i + 1] = sw ? k0 : k1;
+      id[i] = sw ? d1 : d0;
+      id[i + 1] = sw ? d0 : d1;
+    }
+  perm = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) perm |= id[i] << (4 * i);
+}
+
+// One token by one warp: l[i] is the logit of expert lane + 32 i. The k rounds
+// take the largest of the lanes' first keys; the lane it came from moves its
+// keys up by one. Adds the token's statistics to the lane's sums.
 template <int V>
 __device__ __forceinline__ void router_token(const RouterFwd& a, int t, const float (&l)[V], bool on,
                                              float (&acc)[V], int (&cnt)[V], float& z, int& n) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[V];
+  uint32_t key[V], perm;
 #pragma unroll
   for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < a.E ? order_key(l[i]) : 0u;
+  router_sort<V>(key, perm);
   uint32_t sel = 0;  // bit i: expert lane + 32 i was selected
-  int my_id = 0;
-  float my_l = 0.0f, m = 0.0f;
+  uint32_t my_key = 0, my_id = 0, first = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t lm = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) lm = max(lm, key[i]);
-    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, lm);
-    uint32_t id = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] == best) id = lane + 32 * i;
-    id = __reduce_min_sync(0xFFFFFFFFu, id);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i == (int)id) {
-        key[i] = 0u;
-        sel |= 1u << i;
-      }
-    const float v = order_unkey(best);
-    if (j == 0) m = v;
+    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+    const uint32_t id = lane + 32 * (perm & 15u);
+    uint32_t who = __ballot_sync(0xFFFFFFFFu, key[0] == best);
+    uint32_t winner = __ffs(who) - 1;
+    uint32_t wid = __shfl_sync(0xFFFFFFFFu, id, winner);
+    if (who & (who - 1)) {  // equal logits: the lowest expert
+      wid = __reduce_min_sync(0xFFFFFFFFu, key[0] == best ? id : 0xFFFFFFFFu);
+      winner = wid & 31u;
+    }
+    if (j == 0) first = best;
     if (lane == j) {
-      my_id = (int)id;
-      my_l = v;
+      my_key = best;
+      my_id = wid;
+    }
+    if (lane == (int)winner) {
+      sel |= 1u << (perm & 15u);
+      perm >>= 4;
+#pragma unroll
+      for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+      key[V - 1] = 0u;
     }
   }
+  const float m = order_unkey(first);
   const bool some = m != -INFINITY;
   float p[V], total = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    p[i] = lane + 32 * i < a.E ? expf(l[i] - m) : 0.0f;
+    p[i] = lane + 32 * i < a.E ? __expf(l[i] - m) : 0.0f;
     total += p[i];
   }
   total = warp_sum(total);
-  const float we = lane < a.k ? expf(my_l - m) : 0.0f;
+  const float we = lane < a.k ? __expf(order_unkey(my_key) - m) : 0.0f;
   const float wsum = warp_sum(we);
   const float lse = m + logf(total);
   if (lane < a.k) {
-    a.ids[(size_t)t * a.k + lane] = my_id;
+    a.ids[(size_t)t * a.k + lane] = (int)my_id;
     a.w[(size_t)t * a.k + lane] = some ? we / wsum : 0.0f;
   }
   if (lane == 0) a.lse[t] = some ? lse : -INFINITY;
@@ -228,12 +282,15 @@ __global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a) {
   }
   if (gridDim.x == 1) {
     __syncthreads();
-    router_finish(a, a.part_prob, a.part_counts, a.part_z, a.part_n, 1);
+    router_finish<V>(a, 1, s_acc, s_cnt);
   }
 }
 
-__global__ void __launch_bounds__(256) k_router_finish(RouterFwd a, int parts) {
-  router_finish(a, a.part_prob, a.part_counts, a.part_z, a.part_n, parts);
+template <int V>
+__global__ void __launch_bounds__(kRtWarps * 32) k_router_finish(RouterFwd a, int parts) {
+  __shared__ float s_acc[kRtWarps][V * 32];
+  __shared__ int s_cnt[kRtWarps][V * 32];
+  router_finish<V>(a, parts, s_acc, s_cnt);
 }
 
 struct RouterBwd {
@@ -275,7 +332,7 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a) {
     float p[V], s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = on && lane + 32 * i < a.E ? expf(to_f32(row[lane + 32 * i]) - lse) : 0.0f;
+      p[i] = on && lane + 32 * i < a.E ? __expf(to_f32(row[lane + 32 * i]) - lse) : 0.0f;
       s += f[i] * p[i];
     }
     s = warp_sum(s);
@@ -380,15 +437,13 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   auto go = [&](auto elem) {
     using T_ = decltype(elem);
     return by_width<T_>(E, [&](auto v) {
-      k_router_fwd<decltype(v)::value, T_><<<ctas, threads, 0, st>>>(a);
+      constexpr int V = decltype(v)::value;
+      k_router_fwd<V, T_><<<ctas, threads, 0, st>>>(a);
+      if (ctas > 1) k_router_finish<V><<<1, threads, 0, st>>>(a, ctas);
       return cudaGetLastError();
     });
   };
-  cudaError_t e = TM_BY_DTYPE(dtype, go);
-  if (e == cudaSuccess && ctas > 1) {
-    k_router_finish<<<1, 256, 0, st>>>(a, ctas);
-    e = cudaGetLastError();
-  }
+  const cudaError_t e = TM_BY_DTYPE(dtype, go);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "router with losses");
 }
 
