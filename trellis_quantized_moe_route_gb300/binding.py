@@ -139,11 +139,17 @@ def _check(status: int):
         raise TrellisMoEError(status, msg)
 
 
+_torch_mod = None
+
+
 def _torch():
-    import torch
-    if not torch.cuda.is_available():
-        raise RuntimeError("trellis_moe needs a CUDA device; no CPU fallback exists")
-    return torch
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise RuntimeError("trellis_moe needs a CUDA device; no CPU fallback exists")
+        _torch_mod = torch
+    return _torch_mod
 
 
 def _stream_ptr(stream=None):
@@ -458,12 +464,33 @@ class TrellisLinear:
 # ---------------------------------------------------------------------------
 # Router losses, route combine and MXFP4 (device tensors in, device tensors out)
 # ---------------------------------------------------------------------------
+_dtype_codes: dict = {}
+
+
 def _dtype_code(dtype) -> int:
-    torch = _torch()
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if dtype not in codes:
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _dtype_codes.get(dtype)
+    if code is None:
         raise ValueError("dtype must be torch.float32, torch.bfloat16 or torch.float16, not %s" % dtype)
-    return codes[dtype]
+    return code
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; raises on an error status. The
+    marshalling of the small calls costs more than their kernels, so the guard
+    is entered only when another device is current."""
+    torch = _torch()
+    index = device.index
+    if index == torch.cuda.current_device():
+        raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(stream))
+    if status != TM_OK:
+        _check(status)
 
 
 def _on_device(name, t, dtype=None, shape=None, contiguous=True):
@@ -472,9 +499,9 @@ def _on_device(name, t, dtype=None, shape=None, contiguous=True):
         return None
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -482,16 +509,32 @@ def _on_device(name, t, dtype=None, shape=None, contiguous=True):
 
 
 def _rows_2d(name, t):
-    """A matrix whose rows may lie apart (last dimension contiguous); returns its row stride."""
-    _on_device(name, t, contiguous=False)
+    """A matrix whose rows may lie apart (last dimension contiguous); returns
+    its rows, columns and row stride."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions, not %d" % (name, t.dim()))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    if t.is_contiguous():
+        return rows, cols, cols
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("%s: the last dimension must be contiguous" % name)
-    ld = int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
-    if ld < t.shape[1]:
-        raise ValueError("%s: rows overlap (stride %d for %d columns)" % (name, ld, t.shape[1]))
-    return ld
+    if rows <= 1:
+        ld = cols
+    if ld < cols:
+        raise ValueError("%s: rows overlap (stride %d for %d columns)" % (name, ld, cols))
+    return rows, cols, ld
+
+
+def _mask(mask, T):
+    if mask is None:
+        return None
+    _on_device("mask", mask, shape=(T,))
+    if mask.dtype not in (_torch_mod.bool, _torch_mod.uint8):
+        raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
+    return mask.data_ptr()
 
 
 def _opt(t):
@@ -515,30 +558,24 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
     for padding."""
     torch = _torch()
     lib = load_library()
-    ld = _rows_2d("logits", logits)
-    T, E = int(logits.shape[0]), int(logits.shape[1])
-    if mask is not None:
-        _on_device("mask", mask, shape=(T,))
-        if mask.dtype not in (torch.bool, torch.uint8):
-            raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
+    T, E, ld = _rows_2d("logits", logits)
+    mp = _mask(mask, T)
     dev, k = logits.device, int(k)
     kk = max(k, 0)
-    # one allocation: ids | w | lse | counts | prob | losses | tokens, then the workspace
-    wsb = int(lib.trellis_moe_router_workspace_size(T, E))
-    head = 2 * T * kk + T + 2 * E + 3
-    head = (head + 3) // 4 * 4
-    buf = torch.empty(head + (wsb + 3) // 4, dtype=torch.int32, device=dev)
-    fb = buf.view(torch.float32)
     o = T * kk
-    out = RouterOut(ids=buf[:o].view(T, kk), w=fb[o:2 * o].view(T, kk), lse=fb[2 * o:2 * o + T],
-                    counts=buf[2 * o + T:2 * o + T + E], prob=fb[2 * o + T + E:2 * o + T + 2 * E],
-                    losses=fb[2 * o + T + 2 * E:2 * o + T + 2 * E + 2],
-                    tokens=buf[2 * o + T + 2 * E + 2:2 * o + T + 2 * E + 3])
-    with torch.cuda.device(dev):
-        _check(lib.trellis_moe_router_forward(
-            logits.data_ptr(), _dtype_code(logits.dtype), ld, _opt(mask), T, E, k, out.ids.data_ptr(),
-            out.w.data_ptr(), out.lse.data_ptr(), out.counts.data_ptr(), out.prob.data_ptr(), out.losses.data_ptr(),
-            out.tokens.data_ptr(), buf.data_ptr() + 4 * head, wsb, _raw_stream(stream)))
+    # one allocation a type, the workspace after the float32 results; strided
+    # views of them cost less than an allocation each, and much less than split()
+    wsb = lib.trellis_moe_router_workspace_size(T, E)
+    head = (o + T + E + 5) // 4 * 4
+    f = torch.empty(head + (wsb + 3) // 4, dtype=torch.float32, device=dev)
+    i = torch.empty(o + E + 1, dtype=torch.int32, device=dev)
+    sf, si, row, one = f.as_strided, i.as_strided, (kk, 1), (1,)
+    ids = si((T, kk), row, 0)
+    out = RouterOut(ids, sf((T, kk), row, 0), sf((T,), one, o), si((E,), one, o), sf((E,), one, o + T),
+                    sf((2,), one, o + T + E), si(one, one, o + E))
+    wp, ip = f.data_ptr(), i.data_ptr()
+    _launch(lib.trellis_moe_router_forward, dev, stream, logits.data_ptr(), _dtype_code(logits.dtype), ld, mp, T, E, k,
+            ip, wp, wp + 4 * o, ip + 4 * o, wp + 4 * (o + T), wp + 4 * (o + T + E), ip + 4 * (o + E), wp + 4 * head, wsb)
     return out
 
 
@@ -547,70 +584,61 @@ def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=
     on the device, either may be None); fwd and mask as in the forward call."""
     torch = _torch()
     lib = load_library()
-    ld = _rows_2d("logits", logits)
-    T, E = int(logits.shape[0]), int(logits.shape[1])
-    k = int(fwd.ids.shape[1])
-    _on_device("ids", fwd.ids, torch.int32, (T, k))
-    _on_device("w", fwd.w, torch.float32, (T, k))
-    _on_device("lse", fwd.lse, torch.float32, (T,))
-    _on_device("counts", fwd.counts, torch.int32, (E,))
-    _on_device("tokens", fwd.tokens, torch.int32, (1,))
-    _on_device("grad_w", grad_w, torch.float32, (T, k))
-    _on_device("grad_losses", grad_losses, torch.float32, (2,))
-    if mask is not None:
-        _on_device("mask", mask, shape=(T,))
-        if mask.dtype not in (torch.bool, torch.uint8):
-            raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
+    T, E, ld = _rows_2d("logits", logits)
+    k = fwd.ids.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    _on_device("ids", fwd.ids, i32, (T, k))
+    _on_device("w", fwd.w, f32, (T, k))
+    _on_device("lse", fwd.lse, f32, (T,))
+    _on_device("counts", fwd.counts, i32, (E,))
+    _on_device("tokens", fwd.tokens, i32, (1,))
+    _on_device("grad_w", grad_w, f32, (T, k))
+    _on_device("grad_losses", grad_losses, f32, (2,))
+    mp = _mask(mask, T)
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     else:
         _on_device("out", out, logits.dtype, (T, E))
-    with torch.cuda.device(logits.device):
-        _check(lib.trellis_moe_router_backward(
-            logits.data_ptr(), _dtype_code(logits.dtype), ld, _opt(mask), T, E, k, fwd.ids.data_ptr(),
-            fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(), fwd.tokens.data_ptr(), _opt(grad_w),
-            _opt(grad_losses), out.data_ptr(), _raw_stream(stream)))
+    _launch(lib.trellis_moe_router_backward, logits.device, stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+            mp, T, E, k, fwd.ids.data_ptr(), fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(),
+            fwd.tokens.data_ptr(), _opt(grad_w), _opt(grad_losses), out.data_ptr())
     return out
+
+
+def _route_rows(rows, w):
+    _on_device("w", w, _torch().float32)
+    if w.dim() != 2:
+        raise ValueError("w must have two dimensions, not %d" % w.dim())
+    T, k = w.shape
+    _on_device("rows", rows)
+    if rows.dim() != 2 or rows.shape[0] != T * k:
+        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
+    return T, k, rows.shape[1]
 
 
 def combine(rows, w, out=None, stream=None):
     """out [T, H] float32 = sum_j w[t, j] rows[t * k + j] for rows [T * k, H] in
     route order and w float32 [T, k]."""
     torch = _torch()
-    lib = load_library()
-    _on_device("w", w, torch.float32)
-    T, k = int(w.shape[0]), int(w.shape[1])
-    _on_device("rows", rows)
-    if rows.dim() != 2 or rows.shape[0] != T * k:
-        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
-    H = int(rows.shape[1])
+    T, k, H = _route_rows(rows, w)
     if out is None:
         out = torch.empty((T, H), dtype=torch.float32, device=rows.device)
     else:
         _on_device("out", out, torch.float32, (T, H))
-    with torch.cuda.device(rows.device):
-        _check(lib.trellis_moe_combine_forward(rows.data_ptr(), _dtype_code(rows.dtype), w.data_ptr(), T, k, H,
-                                               out.data_ptr(), _raw_stream(stream)))
+    _launch(load_library().trellis_moe_combine_forward, rows.device, stream, rows.data_ptr(), _dtype_code(rows.dtype),
+            w.data_ptr(), T, k, H, out.data_ptr())
     return out
 
 
 def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = True, stream=None):
     """(grad_rows of the rows' type, grad_w float32) of combine; None where not wanted."""
     torch = _torch()
-    lib = load_library()
-    _on_device("w", w, torch.float32)
-    T, k = int(w.shape[0]), int(w.shape[1])
-    _on_device("rows", rows)
-    if rows.dim() != 2 or rows.shape[0] != T * k:
-        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
-    H = int(rows.shape[1])
+    T, k, H = _route_rows(rows, w)
     _on_device("grad_out", grad_out, torch.float32, (T, H))
     grows = torch.empty_like(rows) if want_rows else None
     gw = torch.empty_like(w) if want_w else None
-    with torch.cuda.device(rows.device):
-        _check(lib.trellis_moe_combine_backward(rows.data_ptr(), _dtype_code(rows.dtype), w.data_ptr(),
-                                                grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw),
-                                                _raw_stream(stream)))
+    _launch(load_library().trellis_moe_combine_backward, rows.device, stream, rows.data_ptr(),
+            _dtype_code(rows.dtype), w.data_ptr(), grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw))
     return grows, gw
 
 
@@ -618,26 +646,22 @@ def mxfp4_quantize(x, stream=None):
     """Rows of x [rows, K] (float32, bfloat16 or float16; rows may lie apart) ->
     (codes uint8 [rows, 16 B], scales uint8 [rows, B]), B = ceil(K / 32)."""
     torch = _torch()
-    lib = load_library()
-    ld = _rows_2d("x", x)
-    rows, K = int(x.shape[0]), int(x.shape[1])
+    rows, K, ld = _rows_2d("x", x)
     B = (K + 31) // 32
     codes = torch.empty((rows, 16 * B), dtype=torch.uint8, device=x.device)
     scales = torch.empty((rows, B), dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(lib.trellis_moe_mxfp4_quantize(x.data_ptr(), _dtype_code(x.dtype), ld, rows, K, codes.data_ptr(),
-                                              scales.data_ptr(), _raw_stream(stream)))
+    _launch(load_library().trellis_moe_mxfp4_quantize, x.device, stream, x.data_ptr(), _dtype_code(x.dtype), ld, rows,
+            K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
     """Values [rows, K] of MXFP4 codes [rows, 16 B] and scales [rows, B]."""
     torch = _torch()
-    lib = load_library()
     B = (int(K) + 31) // 32
     if codes.dim() != 2:
         raise ValueError("codes must have two dimensions, not %d" % codes.dim())
-    rows = int(codes.shape[0])
+    rows = codes.shape[0]
     _on_device("codes", codes, torch.uint8, (rows, 16 * B))
     _on_device("scales", scales, torch.uint8, (rows, B))
     dtype = torch.float32 if dtype is None else dtype
@@ -645,9 +669,8 @@ def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
         out = torch.empty((rows, int(K)), dtype=dtype, device=codes.device)
     else:
         _on_device("out", out, dtype, (rows, int(K)))
-    with torch.cuda.device(codes.device):
-        _check(lib.trellis_moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, int(K), out.data_ptr(),
-                                                _dtype_code(dtype), _raw_stream(stream)))
+    _launch(load_library().trellis_moe_mxfp4_dequantize, codes.device, stream, codes.data_ptr(), scales.data_ptr(),
+            rows, int(K), out.data_ptr(), _dtype_code(dtype))
     return out
 
 
@@ -677,6 +700,7 @@ class _MxFp4:
         self.workspace = torch.empty(self.workspace_bytes + 256, dtype=torch.uint8, device=self.device)
         off = (-self.workspace.data_ptr()) % 256
         self.workspace = self.workspace[off:off + self.workspace_bytes]
+        self.workspace_ptr = self.workspace.data_ptr()
 
     def close(self):
         if getattr(self, "handle", None):
@@ -722,14 +746,11 @@ class MxFp4Linear(_MxFp4):
     def forward(self, x, out=None, out_dtype=None, stream=None):
         """x [T, K] (float32, bfloat16 or float16; rows may lie apart) -> [T, N]
         of out_dtype (default float32)."""
-        torch = _torch()
-        ld = _rows_2d("x", x)
-        T = int(x.shape[0])
+        T, _, ld = _rows_2d("x", x)
         out = self._output(T, x, out, out_dtype)
-        with torch.cuda.device(self.device):
-            _check(self.lib.trellis_moe_mxfp4_forward(
-                self.handle, x.data_ptr(), _dtype_code(x.dtype), ld, T, out.data_ptr(), _dtype_code(out.dtype),
-                self.workspace.data_ptr(), self.workspace_bytes, _raw_stream(stream)))
+        _launch(self.lib.trellis_moe_mxfp4_forward, self.device, stream, self.handle, x.data_ptr(),
+                _dtype_code(x.dtype), ld, T, out.data_ptr(), _dtype_code(out.dtype), self.workspace_ptr,
+                self.workspace_bytes)
         return out
 
 
@@ -744,17 +765,14 @@ class MxFp4Experts(_MxFp4):
     def forward(self, x, ids, per_route: bool = False, out=None, out_dtype=None, stream=None):
         """x [T, K] (per_route: [T * topk, K]) and ids int32 [T, topk] -> rows
         [T * topk, N] in route order, of out_dtype (default float32)."""
-        torch = _torch()
-        ld = _rows_2d("x", x)
-        T = int(ids.shape[0])
-        _on_device("ids", ids, torch.int32, (T, self.topk))
+        rows, _, ld = _rows_2d("x", x)
+        T = ids.shape[0]
+        _on_device("ids", ids, _torch().int32, (T, self.topk))
         need = T * self.topk if per_route else T
-        if x.shape[0] != need:
-            raise ValueError("x must have %d rows, not %d" % (need, x.shape[0]))
+        if rows != need:
+            raise ValueError("x must have %d rows, not %d" % (need, rows))
         out = self._output(T * self.topk, x, out, out_dtype)
-        with torch.cuda.device(self.device):
-            _check(self.lib.trellis_moe_mxfp4_forward_experts(
-                self.handle, x.data_ptr(), _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T,
-                self.topk, out.data_ptr(), _dtype_code(out.dtype), self.workspace.data_ptr(), self.workspace_bytes,
-                _raw_stream(stream)))
+        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.device, stream, self.handle, x.data_ptr(),
+                _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T, self.topk, out.data_ptr(),
+                _dtype_code(out.dtype), self.workspace_ptr, self.workspace_bytes)
         return out

@@ -11,6 +11,7 @@
 struct tm_mxfp4 {
   tm_mxfp4_desc desc;
   uint8_t* d_scales;  // the weights' scales as the tensor cores read them
+  int sms;
   CUtensorMap wmap;
 };
 
@@ -85,8 +86,43 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
   return L;
 }
 
+// Rows of a chunk of the few-rows kernel, or 0 where the block kernel runs.
+int mx_dec_rows(const tm_mxfp4_desc& d, const MxCall& c) {
+  const long most = c.ids ? 1024 : kMxDecRows;
+  if (c.rows > most) return 0;
+  const long each = c.ids ? std::min<long>(c.rows, std::max<long>(4, 2L * c.rows / d.E)) : c.rows;
+  if (each > kMxDecRows) return 0;
+  int bn = 16;
+  while (bn < each) bn *= 2;
+  return bn;
+}
+
 cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   const tm_mxfp4_desc& d = h->desc;
+  if (const int bn = mx_dec_rows(d, c)) {
+    MxDecArgs a{};
+    a.E = d.E;
+    a.N = d.N;
+    a.K = d.K;
+    a.gated = d.gated;
+    a.rows = c.rows;
+    a.bn = bn;
+    a.sms = h->sms;
+    a.x = c.x;
+    a.x_dtype = c.x_dtype;
+    a.ld = c.ld;
+    const int es = dtype_bytes(c.x_dtype);
+    a.vec = ((uintptr_t)c.x) % 16 == 0 && (c.ld * es) % 16 == 0 && d.K % 8 == 0;  // (as eights())
+    a.ids = c.ids;
+    a.topk = c.topk;
+    a.wscale = h->d_scales;
+    a.out = c.out;
+    a.out_dtype = c.out_dtype;
+    a.err = static_cast<uint32_t*>(c.ws);
+    a.wmap = h->wmap;
+    const int chunks = c.ids ? c.rows / bn + std::min(d.E, c.rows) : (c.rows + bn - 1) / bn;
+    return launch_mx_dec(a, chunks, st);
+  }
   const MxLayout L = mx_layout(d, c.rows);
   uint8_t* base = static_cast<uint8_t*>(c.ws);
   uint32_t* err = reinterpret_cast<uint32_t*>(base);
@@ -171,7 +207,10 @@ tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, s
   h->d_scales = nullptr;
   const int halves = d.gated ? 2 : 1;
   cudaError_t e;
-  if ((e = cudaMalloc(&h->d_scales, mx_weight_scale_bytes(d.E, halves, d.N, d.K))) != cudaSuccess ||
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+      (e = cudaMalloc(&h->d_scales, mx_weight_scale_bytes(d.E, halves, d.N, d.K))) != cudaSuccess ||
       (e = launch_mx_weight_scales(d.scales, d.E, halves, d.N, d.K, h->d_scales, nullptr)) != cudaSuccess ||
       (e = mx_weight_map(&h->wmap, d.codes, (long)d.E * halves * d.N, d.K)) != cudaSuccess ||
       (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {

@@ -42,6 +42,29 @@ struct MxTcArgs {
 cudaError_t mx_weight_map(CUtensorMap* m, const uint8_t* codes, long rows, int K);
 cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int out_dtype, cudaStream_t st);
 
+// The product for few rows in one launch (mxfp4_dec.cu): x is quantised inside
+// and routes are found from the ids.
+constexpr int kMxDecRows = 128;  // most rows of a chunk
+struct MxDecArgs {
+  int E, N, K, gated;
+  int rows;             // rows of y
+  int bn;               // rows of a chunk: 16, 32, 64 or 128
+  int sms;
+  const void* x;
+  int x_dtype;
+  int64_t ld;
+  int vec;              // rows of x are whole eights
+  const int32_t* ids;   // NULL: dense
+  int topk;             // rows of y that read one row of x
+  const uint8_t* wscale;
+  void* out;
+  int out_dtype;
+  uint32_t* err;
+  uint64_t wait_ns;
+  CUtensorMap wmap;
+};
+cudaError_t launch_mx_dec(const MxDecArgs& a, int chunks, cudaStream_t st);
+
 // Rows of x to MXFP4 in block order: row r's codes at slot s, its scales at
 // [s / bn][...][(s % bn) / 128]. dense: s = r; by expert: slot_of_route of its
 // topk routes (per_route: of route r), and a route without a slot gets its row

@@ -1,0 +1,360 @@
+// Products with MXFP4 weights for few rows (sm_103a): one launch that reads the
+// touched weights once, split along K over the CTAs of a cluster.
+//
+// A unit is 128 output channels (gated: the 128 gate and the 128 up rows) and a
+// chunk of up to `bn` rows of one expert; each CTA of the unit's cluster takes
+// a contiguous part of the 256-column stages. The W tile and its scales come by
+// TMA; the rows of x are quantised by four warps straight into the swizzled
+// operand and scale layout in shared memory, so there is no pass over x before
+// and no row map: every CTA counts the routes of each expert in shared memory
+// and finds its own. The MMA is the block-scaled one of mxfp4_mma.cuh with the
+// rows of x as N = 16, 32, ... columns; tensor cores have time to spare here,
+// what bounds the call is the weights' bytes and the latency of one load, MMA
+// and drain chain, which the split shortens and spreads over the SMs.
+//
+// The partial sums of a unit meet in the cluster's shared memory and are added
+// in rank order: the same bits every time. A CTA frees its tensor memory before
+// it waits for its cluster, so that a CTA that waits holds nothing that another
+// one needs.
+#include <algorithm>
+
+#include "elem.cuh"
+#include "mxfp4.cuh"
+#include "mxfp4.h"
+#include "mxfp4_mma.cuh"
+#include "status.h"
+
+namespace tmoe {
+
+namespace {
+
+constexpr int kMdThreads = 192;  // four warps quantise and drain, one loads, one issues
+constexpr int kMdMaxRing = 8;
+
+struct MdBars {
+  uint64_t full[kMdMaxRing], empty[kMdMaxRing];
+  uint64_t acc;
+};
+
+__device__ __forceinline__ uint32_t md_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void md_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float md_peer_f32(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Eight values of a row of x in any of the element types (n of them exist).
+__device__ __forceinline__ void md_load(const MxDecArgs& a, size_t off, int n, float (&v)[8]) {
+  auto get = [&](auto elem) {
+    using T = decltype(elem);
+    const T* p = static_cast<const T*>(a.x) + off;
+    if (a.vec) {
+      Eight<T, true> e;
+      e.load(p, n);
+      e.to(v);
+    } else {
+      Eight<T, false> e;
+      e.load(p, n);
+      e.to(v);
+    }
+    return 0;
+  };
+  TM_BY_DTYPE(a.x_dtype, get);
+}
+
+__device__ __forceinline__ void md_store(const MxDecArgs& a, size_t i, float y) {
+  if (a.out_dtype == TM_F32)
+    static_cast<float*>(a.out)[i] = y;
+  else if (a.out_dtype == TM_BF16)
+    static_cast<__nv_bfloat16*>(a.out)[i] = from_f32<__nv_bfloat16>(y);
+  else
+    static_cast<__half*>(a.out)[i] = from_f32<__half>(y);
+}
+
+struct MdUnit {
+  int expert, first, rows;  // `rows` rows of the expert from its `first`-th on (rows 0: nothing to do)
+};
+
+// The u-th chunk of bn rows over the experts in order. s_cnt: routes of each.
+__device__ __forceinline__ MdUnit md_find(const MxDecArgs& a, const int* s_cnt, int u) {
+  const int lane = threadIdx.x & 31;
+  MdUnit m{0, 0, 0};
+  int before = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int c = e0 + lane < a.E ? s_cnt[e0 + lane] : 0;
+    const int n = (c + a.bn - 1) / a.bn;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int lo = before + incl - n;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, u >= lo && u < lo + n);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      m.expert = e0 + src;
+      m.first = (u - __shfl_sync(0xFFFFFFFFu, lo, src)) * a.bn;
+      m.rows = min(a.bn, __shfl_sync(0xFFFFFFFFu, c, src) - m.first);
+      return m;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return m;
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ MxDecArgs a, int split, int per, int ring,
+                                                       uint32_t cols) {
+  constexpr int H = GATED ? 2 : 1;
+  extern __shared__ unsigned char md_smem_raw[];
+  __shared__ __align__(8) MdBars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort;
+  __shared__ int s_cnt[kMaxExperts];
+  __shared__ int s_row[kMxDecRows];
+  __shared__ MdUnit s_unit;
+  unsigned char* smem = md_smem_raw + ((1024u - (smem_u32(md_smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int rank = split > 1 ? (int)md_cluster_rank() : 0;
+  const int unit = blockIdx.x / split;
+  const int tiles = (a.N + 127) / 128;
+  const int chunk = unit / tiles, tile = unit - chunk * tiles;
+  const int stages = mx_stages(a.K);
+  const int s_lo = rank * per, s_hi = min(stages, s_lo + per), mine = max(0, s_hi - s_lo);
+  const uint32_t b_bytes = (uint32_t)a.bn * 128;
+  const uint32_t stage_bytes = (H * (kMxTileBytes + 1024) + b_bytes + 1024 + 1023) / 1024 * 1024;
+  float* part = reinterpret_cast<float*>(smem + (size_t)ring * stage_bytes);  // [H][bn][128]
+
+  if (tid == 0) {
+    for (int i = 0; i < ring; ++i) {
+      mbar_init(&bars.full[i], 5);  // the loader's expect_tx and four quantising warps
+      mbar_init(&bars.empty[i], 1);
+    }
+    mbar_init(&bars.acc, 1);
+    s_abort = 0;
+    mbar_fence_init();
+  }
+  MdUnit m{0, chunk * a.bn, min(a.bn, a.rows - chunk * a.bn)};
+  if (a.ids) {
+    for (int e = tid; e < a.E; e += kMdThreads) s_cnt[e] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int r = tid; r < a.rows; r += kMdThreads) {
+      const int e = a.ids[r];
+      if (e >= 0 && e < a.E)
+        atomicAdd(&s_cnt[e], 1);
+      else
+        bad = true;
+    }
+    // (every CTA sees all ids; the first one writes the error word, long
+    // before a wait of any CTA can run out and set its bit)
+    const int any = __syncthreads_or(bad);
+    if (blockIdx.x == 0 && tid == 0) *a.err = any ? 1u : 0u;
+    if (any) {  // a route without an expert gets a row of zeros, from one CTA
+      for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const int e = a.ids[r];
+        if (e >= 0 && e < a.E) continue;
+        for (int n = tid; n < a.N; n += kMdThreads) md_store(a, (size_t)r * a.N + n, 0.0f);
+      }
+    }
+    if (warp == 0) {
+      m = md_find(a, s_cnt, chunk);
+      // its routes, ascending
+      int seen = 0;
+      for (int r0 = 0; r0 < a.rows && seen < m.first + m.rows; r0 += 32) {
+        const bool is = r0 + lane < a.rows && a.ids[r0 + lane] == m.expert;
+        const uint32_t b = __ballot_sync(0xFFFFFFFFu, is);
+        const int at = seen + __popc(b & ((1u << lane) - 1u)) - m.first;
+        if (is && at >= 0 && at < m.rows) s_row[at] = r0 + lane;
+        seen += __popc(b);
+      }
+      if (lane == 0) s_unit = m;
+    }
+  } else if (blockIdx.x == 0 && tid == 0) {
+    *a.err = 0u;
+  }
+  __syncthreads();
+  if (a.ids) m = s_unit;
+  if (m.rows <= 0) return;  // (the same for the whole cluster)
+  if (warp == 0) tmem_alloc(&tmem_slot, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t tsfa = tmem + (uint32_t)(H * a.bn);
+  volatile int* abort = &s_abort;
+  const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
+  const int n16 = (m.rows + 15) / 16 * 16;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const int wrow = m.expert * H * a.N + tile * 128;
+      const size_t wsf = ((size_t)m.expert * H * tiles + tile) * stages * 1024;
+      MxRing r;
+      int it = 0;
+      for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
+        if (it >= ring && !mbar_wait_abort(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
+        unsigned char* st = smem + (size_t)r.slot * stage_bytes;
+        uint64_t* bar = &bars.full[r.slot];
+        mbar_arrive_expect_tx(bar, H * (kMxTileBytes + 1024));
+        mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
+        if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
+        unsigned char* sf = st + H * kMxTileBytes + b_bytes;
+        bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
+        if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)tiles * stages + s) * 1024, 1024, bar);
+      }
+      // (after an abort, full[] also counts the quantisers' arrivals; they
+      // arrive for every stage they reach, and a copy in flight lands within
+      // the limit)
+      if (*abort) {
+        int never = 0;
+        for (int i = max(0, it - ring); i < it; ++i)
+          mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs / kMdMaxRing);
+      }
+    }
+  } else if (warp == 5) {
+    const bool lead = mx_elect();
+    const uint32_t base = smem_u32(smem), idesc = mx_idesc(n16);
+    const int ksteps = (mx_blocks(a.K) + 1) / 2;
+    MxRing r;
+    for (int s = s_lo; s < s_hi; ++s, r.next(ring)) {
+      if (!mx_wait_warp(&bars.full[r.slot], r.phase, abort, limit)) break;
+      tc_fence_after();
+      mx_issue_stage<GATED, 1>(base + (uint32_t)r.slot * stage_bytes, b_bytes, tsfa, tmem, (uint32_t)a.bn, idesc,
+                               min(4, ksteps - s * 4), s == s_lo, lead);
+      if (lead) tc_commit(&bars.empty[r.slot]);
+    }
+    if (lead) tc_commit(&bars.acc);
+    if (*abort) {  // what was issued ends before the tensor memory goes
+      int never = 0;
+      mx_wait_warp(&bars.acc, 0, &never, kMxDrainNs);
+    }
+  } else {
+    MxRing r;
+    int it = 0, item = 0;
+    for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
+      if (it >= ring && !mx_wait_warp(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
+      unsigned char* st = smem + (size_t)r.slot * stage_bytes;
+      unsigned char* bt = st + H * kMxTileBytes;
+      unsigned char* sf = bt + b_bytes + H * 1024;
+      for (int i = 0; i < m.rows; ++i, ++item) {
+        if ((item & 3) != warp) continue;
+        const int row = a.ids ? s_row[i] : m.first + i;
+        const int xr = row / a.topk, col = s * 256 + lane * 8;
+        float v[8];
+        md_load(a, (size_t)xr * a.ld + col, max(0, min(8, a.K - col)), v);
+        uint32_t byte;
+        const uint32_t q = mxfp4_block(v, byte);
+        const int g = lane & 16;
+        uint32_t word = byte;
+        word |= __shfl_sync(0xFFFFFFFFu, byte, g + 4) << 8;
+        word |= __shfl_sync(0xFFFFFFFFu, byte, g + 8) << 16;
+        word |= __shfl_sync(0xFFFFFFFFu, byte, g + 12) << 24;
+        *reinterpret_cast<uint32_t*>(bt + sw128_off(i, lane >> 2) + (lane & 3) * 4) = q;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(sf + (lane >> 4) * 512 + (i & 31) * 16 + (i >> 5) * 4) = word;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.full[r.slot]);
+    }
+    if (mine > 0) {
+      const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
+      tc_fence_after();
+      if (ok) {
+        const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          for (int c0 = 0; c0 < n16; c0 += 16) {
+            float v[16];
+            tmem_ld16(lb + (uint32_t)(h * a.bn + c0), v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) part[(size_t)(h * a.bn + c0 + c) * 128 + warp * 32 + lane] = v[c];
+          }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) atomicOr(a.err, 2u);
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, cols);
+  if (split > 1) md_cluster_sync();
+  // ranks that had stages, added in order; rank r writes every split-th row
+  const int active = (stages + per - 1) / per;
+  const uint32_t pbase = smem_u32(part);
+  for (int i = tid; i < 128 * ((m.rows - rank + split - 1) / split); i += kMdThreads) {
+    const int n = i & 127, c = (i >> 7) * split + rank;
+    float y[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const uint32_t at = pbase + (uint32_t)((h * a.bn + c) * 128 + n) * 4;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < active) v[k] = split > 1 ? md_peer_f32(at, (uint32_t)k) : part[(size_t)(h * a.bn + c) * 128 + n];
+      y[h] = v[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k)
+        if (k < active) y[h] += v[k];
+    }
+    const float o = GATED ? y[0] / (1.0f + __expf(-y[0])) * y[H - 1] : y[0];
+    const int ch = tile * 128 + n;
+    if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : m.first + c) * a.N + ch, o);
+  }
+  if (split > 1) md_cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+template <bool GATED>
+cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
+  constexpr int H = GATED ? 2 : 1;
+  auto kern = k_mx_dec<GATED>;
+  constexpr int kSmem = 220 * 1024;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr != cudaSuccess) return attr;
+  const int stages = mx_stages(a.K), tiles = (a.N + 127) / 128;
+  const int units = chunks * tiles;
+  // as many parts as there are stages and idle SMs (two CTAs each), at most a portable cluster
+  int split = 1;
+  while (split < 8 && split * 2 <= stages && units * split * 2 <= 2 * a.sms) split *= 2;
+  const int per = (stages + split - 1) / split;
+  const int stage = (H * (kMxTileBytes + 1024) + a.bn * 128 + 1024 + 1023) / 1024 * 1024;
+  const int part = H * a.bn * 128 * 4;
+  const int ring = std::max(1, std::min(std::min(kMdMaxRing, per), (100 * 1024 - part) / stage));
+  uint32_t cols = 32;
+  while (cols < (uint32_t)(H * a.bn + 8 * H + 8)) cols *= 2;
+  // no more CTAs on an SM than its tensor memory has columns for
+  int smem = 1024 + ring * stage + part;
+  smem = std::max(smem, (int)(227 * 1024 / (512 / cols + 1)));
+  if (smem > kSmem) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * split));
+  cfg.blockDim = dim3(kMdThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, split, per, ring, cols);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_dec(const MxDecArgs& a, int chunks, cudaStream_t st) {
+  return a.gated ? md_launch<true>(a, chunks, st) : md_launch<false>(a, chunks, st);
+}
+
+}  // namespace tmoe

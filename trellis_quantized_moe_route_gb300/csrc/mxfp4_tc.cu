@@ -26,8 +26,8 @@
 #include "elem.cuh"
 #include "mxfp4.cuh"
 #include "mxfp4.h"
+#include "mxfp4_mma.cuh"
 #include "status.h"
-#include "tc.cuh"
 
 namespace tmoe {
 
@@ -35,64 +35,9 @@ namespace {
 
 constexpr int kMxEpiWarps = 8;
 constexpr int kMxThreads = (kMxEpiWarps + 2) * 32;
-constexpr uint64_t kMxWaitNs = 2000000000ull;
-constexpr uint64_t kMxDrainNs = 500000000ull;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxSfCol = 480;       // first tensor-memory column of the scales
-constexpr int kMxTileBytes = 128 * 128;
 constexpr uint32_t kMxSmem = 220 * 1024;
-
-__device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
-               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar)) : "memory");
-}
-
-// 512 bytes of scales (32 rows of 16 bytes, rows 16 bytes apart) to four
-// columns of tensor memory, repeated in each quarter of the lanes.
-__device__ __forceinline__ void mx_copy_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t desc = smem_desc(saddr, 128, 128);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// D (+)= A B^T over 64 columns with one scale per 32.
-__device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc));
-}
-
-// Instruction descriptor: E2M1 x E2M1, E8M0 scales, fp32 accumulator, both
-// operands K-major, M = 128. Bits 4 and 29 take the first of the two scale
-// bytes used (0 or 2 of the chunk's four).
-__device__ __forceinline__ uint32_t mx_idesc(int n) {
-  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
-}
-
-// One thread of a converged warp.
-__device__ __forceinline__ bool mx_elect() {
-  uint32_t p;
-  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
-  return p != 0;
-}
-
-// mbar_wait_abort by a whole warp, with one answer for it.
-__device__ __forceinline__ bool mx_wait_warp(uint64_t* mbar, uint32_t parity, volatile int* abort, uint64_t limit) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_abort(mbar, parity, abort, limit));
-}
-
-// Position in the ring of stages: slot and the parity of its use.
-struct MxRing {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int ring) {
-    if (++slot == ring) {
-      slot = 0;
-      phase ^= 1;
-    }
-  }
-};
 
 struct MxBars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
@@ -175,43 +120,6 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   }
 }
 
-// The MMAs of one stage: the chunks' scales to tensor memory, then one MMA per
-// 64 columns (`steps` of them) and half. Run by a whole warp, of which `lead`
-// is one thread: the operands are then the same for the warp, which keeps them
-// in uniform registers; issued from a single thread's branch, each
-// instruction cost 110-120 cycles of moving its operands there.
-template <bool GATED, int NRB>
-__device__ __forceinline__ void mx_issue_stage(uint32_t st, uint32_t b_bytes, uint32_t tmem, uint32_t d, uint32_t dup,
-                                               uint32_t idesc, int steps, bool first, bool lead) {
-  constexpr int H = GATED ? 2 : 1;
-  const uint32_t sfa = st + H * kMxTileBytes + b_bytes, sfb = sfa + H * 1024;
-  const uint32_t tsfa = tmem + kMxSfCol, tsfb = tsfa + 8u * H;
-  const uint64_t adesc = smem_desc_sw128(st), bdesc = smem_desc_sw128(st + H * kMxTileBytes);
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if (c * 2 < steps) {
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (lead) mx_copy_scales(tsfa + (uint32_t)(c * H + h) * 4, sfa + h * 1024 + c * 512);
-#pragma unroll
-      for (int r = 0; r < NRB; ++r)
-        if (lead) mx_copy_scales(tsfb + (uint32_t)(c * NRB + r) * 4, sfb + (uint32_t)(c * NRB + r) * 512);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (k < steps) {
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (lead)
-          mx_mma(d + (h ? dup : 0u), adesc + (uint64_t)(h * (kMxTileBytes >> 4) + k * 2), bdesc + (uint64_t)(k * 2),
-                 idesc | ((uint32_t)((k & 1) * 2) << 4) | ((uint32_t)((k & 1) * 2) << 29),
-                 tsfa + (uint32_t)((k >> 1) * H + h) * 4, tsfb + (uint32_t)((k >> 1) * NRB) * 4,
-                 !first || k > 0 ? 1u : 0u);
-    }
-  }
-}
-
 template <bool GATED, int NRB>
 __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
                           volatile int* abort, uint64_t limit) {
@@ -237,9 +145,9 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
       const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes;
       const int steps = g.ksteps - s * 4;
       if (steps >= 4)
-        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem, d, (uint32_t)a.bn, idesc, 4, s == 0, lead);
+        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem + kMxSfCol, d, (uint32_t)a.bn, idesc, 4, s == 0, lead);
       else
-        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem, d, (uint32_t)a.bn, idesc, steps, s == 0, lead);
+        mx_issue_stage<GATED, NRB>(st, g.b_bytes, tmem + kMxSfCol, d, (uint32_t)a.bn, idesc, steps, s == 0, lead);
       if (lead) tc_commit(&B.empty[r.slot]);
     }
     if (ok && lead) tc_commit(&B.acc_full[buf]);
