@@ -87,13 +87,12 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
 }
 
 // Rows of a chunk of the few-rows kernel, or 0 where the block kernel runs.
+constexpr int kMxDecRoutes = 256;
 int mx_dec_rows(const tm_mxfp4_desc& d, const MxCall& c) {
-  const long most = c.ids ? 1024 : kMxDecRows;
-  if (c.rows > most) return 0;
-  const long each = c.ids ? std::min<long>(c.rows, std::max<long>(4, 2L * c.rows / d.E)) : c.rows;
-  if (each > kMxDecRows) return 0;
+  if (c.rows > (c.ids ? kMxDecRoutes : kMxDecRows)) return 0;
+  const int each = c.ids ? std::min(c.rows, std::max(4, 2 * c.rows / d.E)) : c.rows;
   int bn = 16;
-  while (bn < each) bn *= 2;
+  while (bn < each && bn < kMxDecRows) bn *= 2;
   return bn;
 }
 
@@ -120,7 +119,7 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
     a.out_dtype = c.out_dtype;
     a.err = static_cast<uint32_t*>(c.ws);
     a.wmap = h->wmap;
-    const int chunks = c.ids ? c.rows / bn + std::min(d.E, c.rows) : (c.rows + bn - 1) / bn;
+    const int chunks = c.ids ? c.rows : (c.rows + bn - 1) / bn;
     return launch_mx_dec(a, chunks, st);
   }
   const MxLayout L = mx_layout(d, c.rows);

@@ -5,17 +5,20 @@
 // chunk of up to `bn` rows of one expert; each CTA of the unit's cluster takes
 // a contiguous part of the 256-column stages. The W tile and its scales come by
 // TMA; the rows of x are quantised by four warps straight into the swizzled
-// operand and scale layout in shared memory, so there is no pass over x before
-// and no row map: every CTA counts the routes of each expert in shared memory
-// and finds its own. The MMA is the block-scaled one of mxfp4_mma.cuh with the
-// rows of x as N = 16, 32, ... columns; tensor cores have time to spare here,
-// what bounds the call is the weights' bytes and the latency of one load, MMA
-// and drain chain, which the split shortens and spreads over the SMs.
+// operand and scale layout in shared memory, so there is no pass over x before.
+// Nor is there a row map: the chunk with index r starts at route r, and exists
+// if the number of earlier routes of the same expert is a multiple of bn; its
+// rows are that route and the next ones of the expert. Each warp finds that by
+// itself with a ballot for every 32 ids, and the CTAs without a chunk leave.
+// The MMA is the block-scaled one of mxfp4_mma.cuh with the rows of x as
+// N = 16, 32, ... columns; tensor cores have time to spare here, what bounds
+// the call is the weights' bytes and the latency of one load, MMA and drain
+// chain, which the split shortens and spreads over the SMs.
 //
-// The partial sums of a unit meet in the cluster's shared memory and are added
-// in rank order: the same bits every time. A CTA frees its tensor memory before
-// it waits for its cluster, so that a CTA that waits holds nothing that another
-// one needs.
+// The partial sums of a unit are sent to the CTA of the cluster that owns their
+// row, which adds them in rank order: the same bits every time. A CTA frees its
+// tensor memory before it waits for its cluster, so that a CTA that waits holds
+// nothing that another one needs.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -41,15 +44,15 @@ __device__ __forceinline__ uint32_t md_cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void md_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ float md_peer_f32(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ void md_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void md_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ uint32_t md_peer(uint32_t saddr, uint32_t rank) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
-  return v;
+  return a;
+}
+__device__ __forceinline__ void md_peer_store(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(a), "f"(v) : "memory");
 }
 
 // Eight values of a row of x in any of the element types (n of them exist).
@@ -80,35 +83,37 @@ __device__ __forceinline__ void md_store(const MxDecArgs& a, size_t i, float y) 
     static_cast<__half*>(a.out)[i] = from_f32<__half>(y);
 }
 
-struct MdUnit {
-  int expert, first, rows;  // `rows` rows of the expert from its `first`-th on (rows 0: nothing to do)
+// The rows of the chunk that starts at route r0: `expert` (out of range: none),
+// `rows` of them (0: no chunk starts here). Called by each warp; `list` (one
+// warp's) gets the routes.
+struct MdChunk {
+  int expert, rows;
+  bool bad;  // some id is out of range
 };
 
-// The u-th chunk of bn rows over the experts in order. s_cnt: routes of each.
-__device__ __forceinline__ MdUnit md_find(const MxDecArgs& a, const int* s_cnt, int u) {
+__device__ __forceinline__ MdChunk md_find(const MxDecArgs& a, int r0, int* list) {
   const int lane = threadIdx.x & 31;
-  MdUnit m{0, 0, 0};
-  int before = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int c = e0 + lane < a.E ? s_cnt[e0 + lane] : 0;
-    const int n = (c + a.bn - 1) / a.bn;
-    int incl = n;
+  MdChunk m;
+  m.expert = a.ids[r0];
+  m.bad = false;
+  int before = 0, from = 0;
+  for (int i = 0; i < a.rows; i += 128) {
+    int id[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
+    for (int u = 0; u < 4; ++u) id[u] = i + u * 32 + lane < a.rows ? a.ids[i + u * 32 + lane] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = i + u * 32 + lane;
+      m.bad |= id[u] < 0 || id[u] >= a.E;
+      const bool is = r < a.rows && id[u] == m.expert;
+      const uint32_t lo = __ballot_sync(0xFFFFFFFFu, is && r < r0), hi = __ballot_sync(0xFFFFFFFFu, is && r >= r0);
+      const int at = from + __popc(hi & ((1u << lane) - 1u));
+      if (list && is && r >= r0 && at < a.bn) list[at] = r;
+      before += __popc(lo);
+      from += __popc(hi);
     }
-    const int lo = before + incl - n;
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, u >= lo && u < lo + n);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      m.expert = e0 + src;
-      m.first = (u - __shfl_sync(0xFFFFFFFFu, lo, src)) * a.bn;
-      m.rows = min(a.bn, __shfl_sync(0xFFFFFFFFu, c, src) - m.first);
-      return m;
-    }
-    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
+  m.rows = before % a.bn == 0 ? min(a.bn, from) : 0;
   return m;
 }
 
@@ -120,9 +125,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   __shared__ __align__(8) MdBars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
-  __shared__ int s_cnt[kMaxExperts];
   __shared__ int s_row[kMxDecRows];
-  __shared__ MdUnit s_unit;
   unsigned char* smem = md_smem_raw + ((1024u - (smem_u32(md_smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -131,12 +134,15 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   const int tiles = (a.N + 127) / 128;
   const int chunk = unit / tiles, tile = unit - chunk * tiles;
   const int stages = mx_stages(a.K);
-  const int s_lo = rank * per, s_hi = min(stages, s_lo + per), mine = max(0, s_hi - s_lo);
+  const int s_lo = rank * per, s_hi = min(stages, s_lo + per);
   const uint32_t b_bytes = (uint32_t)a.bn * 128;
   const uint32_t stage_bytes = (H * (kMxTileBytes + 1024) + b_bytes + 1024 + 1023) / 1024 * 1024;
-  float* part = reinterpret_cast<float*>(smem + (size_t)ring * stage_bytes);  // [H][bn][128]
+  float* part = reinterpret_cast<float*>(smem + (size_t)ring * stage_bytes);  // [split][H][bn / split][128]
 
-  if (tid == 0) {
+  if (split > 1) md_cluster_arrive();  // (waited for before the first store to a peer)
+  mx_grid_wait();
+  mx_grid_launch();
+  if (tid == 128) {
     for (int i = 0; i < ring; ++i) {
       mbar_init(&bars.full[i], 5);  // the loader's expect_tx and four quantising warps
       mbar_init(&bars.empty[i], 1);
@@ -145,49 +151,26 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     s_abort = 0;
     mbar_fence_init();
   }
-  MdUnit m{0, chunk * a.bn, min(a.bn, a.rows - chunk * a.bn)};
+  MdChunk m{0, min(a.bn, a.rows - chunk * a.bn), false};
   if (a.ids) {
-    for (int e = tid; e < a.E; e += kMdThreads) s_cnt[e] = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int r = tid; r < a.rows; r += kMdThreads) {
-      const int e = a.ids[r];
-      if (e >= 0 && e < a.E)
-        atomicAdd(&s_cnt[e], 1);
-      else
-        bad = true;
-    }
+    m = md_find(a, chunk, warp == 0 ? s_row : nullptr);
     // (every CTA sees all ids; the first one writes the error word, long
     // before a wait of any CTA can run out and set its bit)
-    const int any = __syncthreads_or(bad);
-    if (blockIdx.x == 0 && tid == 0) *a.err = any ? 1u : 0u;
-    if (any) {  // a route without an expert gets a row of zeros, from one CTA
-      for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const int e = a.ids[r];
-        if (e >= 0 && e < a.E) continue;
-        for (int n = tid; n < a.N; n += kMdThreads) md_store(a, (size_t)r * a.N + n, 0.0f);
-      }
+    if (blockIdx.x == 0 && warp == 0) {
+      const bool any = __any_sync(0xFFFFFFFFu, m.bad);
+      if (lane == 0) *a.err = any ? 1u : 0u;
     }
-    if (warp == 0) {
-      m = md_find(a, s_cnt, chunk);
-      // its routes, ascending
-      int seen = 0;
-      for (int r0 = 0; r0 < a.rows && seen < m.first + m.rows; r0 += 32) {
-        const bool is = r0 + lane < a.rows && a.ids[r0 + lane] == m.expert;
-        const uint32_t b = __ballot_sync(0xFFFFFFFFu, is);
-        const int at = seen + __popc(b & ((1u << lane) - 1u)) - m.first;
-        if (is && at >= 0 && at < m.rows) s_row[at] = r0 + lane;
-        seen += __popc(b);
-      }
-      if (lane == 0) s_unit = m;
+    if (m.expert < 0 || m.expert >= a.E) {  // a route without an expert gets a row of zeros
+      if (rank == 0)
+        for (int n = tile * 128 + tid; n < min(a.N, tile * 128 + 128); n += kMdThreads)
+          md_store(a, (size_t)chunk * a.N + n, 0.0f);
+      return;
     }
   } else if (blockIdx.x == 0 && tid == 0) {
     *a.err = 0u;
   }
-  __syncthreads();
-  if (a.ids) m = s_unit;
-  if (m.rows <= 0) return;  // (the same for the whole cluster)
-  if (warp == 0) tmem_alloc(&tmem_slot, cols);
+  if (m.rows <= 0) return;  // (here and above: the same for the whole cluster)
+  if (warp == 5) tmem_alloc(&tmem_slot, cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -250,7 +233,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       unsigned char* sf = bt + b_bytes + H * 1024;
       for (int i = 0; i < m.rows; ++i, ++item) {
         if ((item & 3) != warp) continue;
-        const int row = a.ids ? s_row[i] : m.first + i;
+        const int row = a.ids ? s_row[i] : chunk * a.bn + i;
         const int xr = row / a.topk, col = s * 256 + lane * 8;
         float v[8];
         md_load(a, (size_t)xr * a.ld + col, max(0, min(8, a.K - col)), v);
@@ -269,51 +252,55 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.full[r.slot]);
     }
-    if (mine > 0) {
-      const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
-      tc_fence_after();
-      if (ok) {
-        const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
+  }
+  if (split > 1) md_cluster_wait();  // every CTA of the cluster has started
+  const int own = a.bn / split;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
+  if (warp < 4 && s_hi > s_lo) {
+    const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
+    tc_fence_after();
+    if (ok) {
+      const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
+      const uint32_t to = smem_u32(part) + (uint32_t)(rank * H * own * 128 + warp * 32 + lane) * 4;
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-          for (int c0 = 0; c0 < n16; c0 += 16) {
-            float v[16];
-            tmem_ld16(lb + (uint32_t)(h * a.bn + c0), v);
+      for (int h = 0; h < H; ++h)
+        for (int c0 = 0; c0 < n16; c0 += 16) {
+          float v[16];
+          tmem_ld16(lb + (uint32_t)(h * a.bn + c0), v);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) part[(size_t)(h * a.bn + c0 + c) * 128 + warp * 32 + lane] = v[c];
+          for (int c = 0; c < 16; ++c) {
+            if (c0 + c >= m.rows) break;
+            const uint32_t at = to + (uint32_t)(h * own + (c0 + c) / split) * 512;
+            if (split > 1)
+              md_peer_store(md_peer(at, (uint32_t)((c0 + c) % split)), v[c]);
+            else
+              part[(size_t)(h * own + c0 + c) * 128 + warp * 32 + lane] = v[c];
           }
-      }
+        }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) atomicOr(a.err, 2u);
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, cols);
-  if (split > 1) md_cluster_sync();
-  // ranks that had stages, added in order; rank r writes every split-th row
+  if (warp == 5) tmem_dealloc(tmem, cols);
+  if (split > 1) {
+    md_cluster_arrive();
+    md_cluster_wait();
+  }
+  // the sums of the ranks that had stages, in order
   const int active = (stages + per - 1) / per;
-  const uint32_t pbase = smem_u32(part);
   for (int i = tid; i < 128 * ((m.rows - rank + split - 1) / split); i += kMdThreads) {
-    const int n = i & 127, c = (i >> 7) * split + rank;
+    const int n = i & 127, o = i >> 7, c = o * split + rank;
     float y[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const uint32_t at = pbase + (uint32_t)((h * a.bn + c) * 128 + n) * 4;
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < active) v[k] = split > 1 ? md_peer_f32(at, (uint32_t)k) : part[(size_t)(h * a.bn + c) * 128 + n];
-      y[h] = v[0];
-#pragma unroll
-      for (int k = 1; k < 8; ++k)
-        if (k < active) y[h] += v[k];
+      y[h] = part[(h * own + o) * 128 + n];
+      for (int k = 1; k < active; ++k) y[h] += part[((k * H + h) * own + o) * 128 + n];
     }
-    const float o = GATED ? y[0] / (1.0f + __expf(-y[0])) * y[H - 1] : y[0];
+    const float v = GATED ? y[0] / (1.0f + __expf(-y[0])) * y[H - 1] : y[0];
     const int ch = tile * 128 + n;
-    if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : m.first + c) * a.N + ch, o);
+    if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : chunk * a.bn + c) * a.N + ch, v);
   }
-  if (split > 1) md_cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 template <bool GATED>
@@ -343,11 +330,13 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   cfg.blockDim = dim3(kMdThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, a, split, per, ring, cols);
 }
 

@@ -13,6 +13,12 @@ constexpr uint64_t kMxWaitNs = 2000000000ull;   // limit of a pipeline wait
 constexpr uint64_t kMxDrainNs = 500000000ull;   // of a wait for copies in flight after one gave up
 constexpr int kMxTileBytes = 128 * 128;         // 128 rows of W, 256 columns
 
+// Programmatic dependent launch: a kernel may start while the one before it in
+// the stream still runs; before it touches global memory it waits for that one
+// to end, and it lets the next one start as soon as all its own CTAs run.
+__device__ __forceinline__ void mx_grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void mx_grid_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 __device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar)) : "memory");
