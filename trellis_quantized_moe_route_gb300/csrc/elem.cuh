@@ -48,6 +48,28 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
   }
+  // The largest |v| of the eight and of the three neighbouring lanes' (four
+  // lanes from a multiple of four), as the bits of an fp32: these compare like
+  // the values, with infinities and then NaN above all numbers. 16-bit types
+  // compare two at a time. All 32 lanes take part.
+  __device__ __forceinline__ uint32_t block_amax_bits() const {
+    if (sizeof(T) == 2) {
+      const uint32_t a = 0x7FFF7FFFu;
+      uint32_t m = __vmaxu2(__vmaxu2(q[0].x & a, q[0].y & a), __vmaxu2(q[0].z & a, q[0].w & a));
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const uint16_t h = (uint16_t)max(m >> 16, m & 0xFFFFu);
+      return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&h)));
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t a = 0x7FFFFFFFu;
+      m = max(max(m, max(q[w].x & a, q[w].y & a)), max(q[w].z & a, q[w].w & a));
+    }
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  }
   __device__ __forceinline__ void from(const float (&v)[8]) {
     T* t = reinterpret_cast<T*>(q);
 #pragma unroll

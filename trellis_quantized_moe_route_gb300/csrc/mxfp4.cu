@@ -57,7 +57,7 @@ long mx_max_blocks(const tm_mxfp4_desc& d, long rows, int bn) { return rows / bn
 // the largest block and for the most blocks, so that a workspace for more rows
 // fits fewer.
 struct MxLayout {
-  size_t rank, tile_counts, counts, offsets, block_expert, nblocks, route_of_slot, slot_of_route, codes, scales, total;
+  size_t counts, offsets, block_expert, nblocks, route_of_slot, slot_of_route, codes, scales, total;
 };
 
 MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
@@ -72,10 +72,8 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
     return at;
   };
   const size_t R = (size_t)rows;
-  L.rank = take(R * 4);
-  L.tile_counts = take((R + 1023) / 1024 * d.E * 4);
   L.counts = take((size_t)d.E * 4);
-  L.offsets = take(((size_t)d.E + 1) * 4);
+  L.offsets = take((size_t)d.E * 4);
   L.block_expert = take(blocks * 4);
   L.nblocks = take(4);
   L.route_of_slot = take(slots * 4);
@@ -126,8 +124,7 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   uint8_t* base = static_cast<uint8_t*>(c.ws);
   uint32_t* err = reinterpret_cast<uint32_t*>(base);
   auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(base + off); };
-  cudaError_t e = cudaMemsetAsync(err, 0, 4, st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   MxTcArgs a{};
   a.E = d.E;
   a.N = d.N;
@@ -140,6 +137,7 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   a.xscale = base + L.scales;
   a.out = c.out;
   a.err = err;
+  a.sms = h->sms;
   a.wmap = h->wmap;
   a.max_blocks = (c.rows + a.bn - 1) / a.bn;
   if (c.ids) {
@@ -149,12 +147,12 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
     a.counts = i32(L.counts);
     a.offsets = i32(L.offsets);
     a.route_of_slot = i32(L.route_of_slot);
-    RouteMapArgs rm{c.ids, c.rows, d.E, a.bn, i32(L.rank), i32(L.tile_counts), i32(L.counts), i32(L.offsets),
-                    i32(L.block_expert), i32(L.nblocks), i32(L.route_of_slot), i32(L.slot_of_route), err};
-    if ((e = launch_route_map(rm, st)) != cudaSuccess) return e;
+    const MxMapArgs rm{c.ids, c.rows, d.E, a.bn, i32(L.counts), i32(L.offsets), i32(L.block_expert), i32(L.nblocks),
+                       i32(L.route_of_slot), i32(L.slot_of_route), err};
+    if ((e = launch_mx_map(rm, st)) != cudaSuccess) return e;
   }
   MxQuantArgs q{c.x, c.ld, c.x_rows, d.K, c.topk, c.ids ? i32(L.slot_of_route) : nullptr, a.bn, a.nrb, base + L.codes,
-                base + L.scales, c.out, d.N * dtype_bytes(c.out_dtype)};
+                base + L.scales, c.out, d.N * dtype_bytes(c.out_dtype), err};
   if ((e = launch_mx_rows_quantize(q, c.x_dtype, st)) != cudaSuccess) return e;
   return launch_mx_tc(a, base + L.codes, (long)a.max_blocks * a.bn, c.out_dtype, st);
 }

@@ -50,16 +50,10 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// Quantises a block spread over four neighbouring lanes, eight values each:
-// returns the lane's eight codes, `byte` the block's scale. All 32 lanes take
-// part. |v| compares as bits like the values, a NaN above every number.
-__device__ __forceinline__ uint32_t mxfp4_block(float (&v)[8], uint32_t& byte) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(v[c]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  byte = mxfp4_scale_byte(m);
+// Eight values of a block whose largest |v| has the bits amax_bits: returns
+// their codes, `byte` the block's scale.
+__device__ __forceinline__ uint32_t mxfp4_codes(float (&v)[8], uint32_t amax_bits, uint32_t& byte) {
+  byte = mxfp4_scale_byte(amax_bits);
   const float inv = mxfp4_inverse(byte);
 #pragma unroll
   for (int c = 0; c < 8; ++c) v[c] *= inv;

@@ -35,12 +35,28 @@ struct MxTcArgs {
   const uint8_t* xscale;         // [blocks][2 * stages][nrb][512]
   void* out;
   uint32_t* err;
+  int sms;
   uint64_t wait_ns;              // limit of a pipeline wait (0: 2 s)
   CUtensorMap wmap;              // codes of W as [E * R][16 B] bytes, box 128 x 128 bytes
   CUtensorMap xmap;              // codes of x as [blocks * bn][16 B] bytes, box bn x 128 bytes
 };
 cudaError_t mx_weight_map(CUtensorMap* m, const uint8_t* codes, long rows, int K);
 cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int out_dtype, cudaStream_t st);
+
+// Route map of the block kernel: as the layer's, but with the routes of an
+// expert in no fixed order.
+struct MxMapArgs {
+  const int32_t* ids;
+  int R, E, bn;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* block_expert;
+  int32_t* nblocks;
+  int32_t* route_of_slot;
+  int32_t* slot_of_route;
+  uint32_t* err;
+};
+cudaError_t launch_mx_map(const MxMapArgs& a, cudaStream_t st);
 
 // The product for few rows in one launch (mxfp4_dec.cu): x is quantised inside
 // and routes are found from the ids.
@@ -79,6 +95,7 @@ struct MxQuantArgs {
   uint8_t* scales;
   void* out;
   int out_row_bytes;
+  uint32_t* err;
 };
 cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_t st);
 

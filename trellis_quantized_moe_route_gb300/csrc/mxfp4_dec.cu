@@ -55,23 +55,18 @@ __device__ __forceinline__ void md_peer_store(uint32_t a, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(a), "f"(v) : "memory");
 }
 
-// Eight values of a row of x in any of the element types (n of them exist).
-__device__ __forceinline__ void md_load(const MxDecArgs& a, size_t off, int n, float (&v)[8]) {
-  auto get = [&](auto elem) {
+// Quantises eight values of a row of x in any of the element types (n of them
+// exist; the four lanes of a block together).
+__device__ __forceinline__ uint32_t md_quantize(const MxDecArgs& a, size_t off, int n, uint32_t& byte) {
+  auto get = [&](auto elem, auto vec) {
     using T = decltype(elem);
-    const T* p = static_cast<const T*>(a.x) + off;
-    if (a.vec) {
-      Eight<T, true> e;
-      e.load(p, n);
-      e.to(v);
-    } else {
-      Eight<T, false> e;
-      e.load(p, n);
-      e.to(v);
-    }
-    return 0;
+    Eight<T, decltype(vec)::value> e;
+    e.load(static_cast<const T*>(a.x) + off, n);
+    float v[8];
+    e.to(v);
+    return mxfp4_codes(v, e.block_amax_bits(), byte);
   };
-  TM_BY_DTYPE(a.x_dtype, get);
+  return TM_BY_DTYPE_VEC(a.x_dtype, a.vec, get);
 }
 
 __device__ __forceinline__ void md_store(const MxDecArgs& a, size_t i, float y) {
@@ -235,10 +230,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
         if ((item & 3) != warp) continue;
         const int row = a.ids ? s_row[i] : chunk * a.bn + i;
         const int xr = row / a.topk, col = s * 256 + lane * 8;
-        float v[8];
-        md_load(a, (size_t)xr * a.ld + col, max(0, min(8, a.K - col)), v);
         uint32_t byte;
-        const uint32_t q = mxfp4_block(v, byte);
+        const uint32_t q = md_quantize(a, (size_t)xr * a.ld + col, max(0, min(8, a.K - col)), byte);
         const int g = lane & 16;
         uint32_t word = byte;
         word |= __shfl_sync(0xFFFFFFFFu, byte, g + 4) << 8;
@@ -297,7 +290,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       y[h] = part[(h * own + o) * 128 + n];
       for (int k = 1; k < active; ++k) y[h] += part[((k * H + h) * own + o) * 128 + n];
     }
-    const float v = GATED ? y[0] / (1.0f + __expf(-y[0])) * y[H - 1] : y[0];
+    const float v = GATED ? mx_silu(y[0]) * y[H - 1] : y[0];
     const int ch = tile * 128 + n;
     if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : chunk * a.bn + c) * a.N + ch, v);
   }

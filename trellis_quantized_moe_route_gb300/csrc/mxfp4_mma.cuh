@@ -19,6 +19,10 @@ constexpr int kMxTileBytes = 128 * 128;         // 128 rows of W, 256 columns
 __device__ __forceinline__ void mx_grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void mx_grid_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// silu(g) = g / (1 + exp(-g)) with the hardware's exp2 and reciprocal (each a
+// few ulp): where exp(-g) overflows the quotient is -0, as it should be.
+__device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
 __device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar)) : "memory");

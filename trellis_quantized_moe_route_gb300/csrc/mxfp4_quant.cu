@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ x,
     float v[8];
     e[u].to(v);
     uint32_t byte;
-    const uint32_t q = mxfp4_block(v, byte);
+    const uint32_t q = mxfp4_codes(v, e[u].block_amax_bits(), byte);
     if (i < total) {
       codes[i] = q;
       if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;

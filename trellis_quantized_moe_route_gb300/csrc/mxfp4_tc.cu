@@ -158,6 +158,39 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   }
 }
 
+// 32 columns (rows of y) of a thread's channel, as T: y[c] for row `row` of
+// lane c, `rows` of them. 16-bit types with `pair` (an even number of channels,
+// 4-byte aligned): neighbouring lanes swap halves, so that the even one stores
+// both channels of column c and the odd one those of column c + 1.
+template <typename T>
+__device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__ out, int row, int rows, int n, int N,
+                                           bool pair) {
+  const int lane = threadIdx.x & 31;
+  if (sizeof(T) == 2 && pair) {
+    const int odd = lane & 1;
+    T* o = out + (n - odd);
+    const bool in = n - odd < N;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      uint32_t p;
+      T* t = reinterpret_cast<T*>(&p);
+      t[0] = from_f32<T>(y[c]);
+      t[1] = from_f32<T>(y[c + 1]);
+      const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
+      const uint32_t word = odd ? __byte_perm(q, p, 0x7632) : __byte_perm(p, q, 0x5410);
+      const int r = __shfl_sync(0xFFFFFFFFu, row, c + odd);
+      if (in && c + odd < rows) *reinterpret_cast<uint32_t*>(o + (size_t)r * N) = word;
+    }
+  } else {
+    T* o = out + n;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const int r = __shfl_sync(0xFFFFFFFFu, row, c);
+      if (n < N && c < rows) o[(size_t)r * N] = from_f32<T>(y[c]);
+    }
+  }
+}
+
 template <bool GATED, typename T>
 __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, volatile int* abort,
                             uint64_t limit) {
@@ -165,6 +198,7 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
   const int quarter = warp & 3, part = warp >> 2;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   T* out = static_cast<T*>(a.out);
+  const bool pair = a.N % 2 == 0 && ((uintptr_t)out) % 4 == 0;
   int nu = 0;
   for (int u = blockIdx.x; u < g.units; u += gridDim.x, ++nu) {
     const MxUnit m = mx_unit(a, u, g.tiles);
@@ -182,13 +216,11 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
       tmem_ld_wait();
       reg_fence32(v);
       if (GATED) reg_fence32(w);
+      float y[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int r = __shfl_sync(0xFFFFFFFFu, row, c);
-        float y = __uint_as_float(v[c]);
-        if (GATED) y = y / (1.0f + __expf(-y)) * __uint_as_float(w[c]);
-        if (c0 + c < m.rows && n < a.N) out[(size_t)r * a.N + n] = from_f32<T>(y);
-      }
+      for (int c = 0; c < 32; ++c)
+        y[c] = GATED ? mx_silu(__uint_as_float(v[c])) * __uint_as_float(w[c]) : __uint_as_float(v[c]);
+      mx_store32<T>(y, out, row, m.rows - c0, n, a.N, pair);
     }
     tc_fence_before();
     if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
@@ -220,6 +252,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  mx_grid_wait();
+  mx_grid_launch();
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
@@ -270,6 +304,22 @@ cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A launch that may start while the kernel before it ends.
+template <typename... P, typename... A>
+cudaError_t mx_launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <bool GATED, typename T>
 cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
   auto kern = k_mx_tc<GATED, T>;
@@ -278,14 +328,9 @@ cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
   const uint32_t stage = (uint32_t)(GATED ? 2 : 1) * (kMxTileBytes + 1024) + (uint32_t)a.bn * 128 + (uint32_t)a.nrb * 1024;
   const uint32_t stage_bytes = (stage + 1023) / 1024 * 1024;
   const int ring = (int)std::min<uint32_t>(kMxMaxStages, (kMxSmem - 1024) / stage_bytes);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const long units = (long)a.max_blocks * ((a.N + 127) / 128);
-  const int grid = (int)std::max<long>(1, std::min<long>(units, sms));
-  kern<<<grid, kMxThreads, 1024 + ring * stage_bytes, st>>>(a, ring);
-  return cudaGetLastError();
+  const int grid = (int)std::max<long>(1, std::min<long>(units, a.sms));
+  return mx_launch_after(kern, dim3(grid), kMxThreads, 1024 + ring * stage_bytes, st, a, ring);
 }
 
 // One thread a 4-byte word of the laid-out scales; absent rows and blocks get 0.
@@ -307,37 +352,34 @@ __global__ void __launch_bounds__(256) k_mx_weight_scales(const uint8_t* __restr
   }
 }
 
-// A warp takes 512 columns of one row of x, 256 (eight blocks, four lanes each)
-// at a time, both loads in flight at once.
+// A warp takes up to kRqUnroll times 256 columns (eight blocks, four lanes
+// each) of a row of x, all loads in flight at once. Dense (no slots): the first
+// thread clears the error word.
+constexpr int kRqUnroll = 4;
+
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, int stages, FastDiv pairs, FastDiv bn,
-                                                          int items) {
+__global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, int stages, int per, FastDiv segs,
+                                                          FastDiv bn, int items) {
+  mx_grid_wait();
+  mx_grid_launch();
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int i = blockIdx.x * 8 + __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
+  if (!a.slot_of_route && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
   if (i >= items) return;
   const int nb = mx_blocks(a.K);
-  const int row = (int)pairs.div(i), s0 = (i - row * (int)pairs.d) * 2;
-  const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ld;
+  const int row = (int)segs.div(i), s0 = (i - row * (int)segs.d) * per, n = min(per, stages - s0);
+  const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ld + s0 * 256 + lane * 8;
+  const int left = a.K - s0 * 256 - lane * 8;
+  Eight<T, VEC> e[kRqUnroll];
+#pragma unroll
+  for (int u = 0; u < kRqUnroll; ++u) e[u].load(x + u * 256, u < n ? max(0, min(8, left - u * 256)) : 0);
   const int first = a.slot_of_route ? a.slot_of_route[row * a.topk] : row;
-  Eight<T, VEC> e[2];
+  uint32_t q[kRqUnroll], byte[kRqUnroll];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int col = (s0 + u) * 256 + lane * 8;
-    e[u].load(x + col, max(0, min(8, a.K - col)));
-  }
-  uint32_t q[2], word[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < kRqUnroll; ++u) {
     float v[8];
     e[u].to(v);
-    uint32_t byte;
-    q[u] = mxfp4_block(v, byte);
-    // the four bytes of a chunk (128 columns, 16 lanes) in its first lane
-    const int base = lane & 16;
-    word[u] = byte;
-    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 4) << 8;
-    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 8) << 16;
-    word[u] |= __shfl_sync(0xFFFFFFFFu, byte, base + 12) << 24;
+    q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
   }
   for (int j = 0; j < a.topk; ++j) {
     const int r = row * a.topk + j;
@@ -350,16 +392,124 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
       continue;
     }
     const int b = (int)bn.div(slot), t = slot - b * (int)bn.d;
+    uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes) + ((size_t)slot * nb + s0 * 8) * 4 + lane;
+    uint8_t* scales = a.scales + (((size_t)b * stages + s0) * 2 * a.nrb + (lane >> 4) * a.nrb + (t >> 7)) * 512 +
+                      (t & 31) * 16 + ((t & 127) >> 5) * 4 + ((lane >> 2) & 3);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int s = s0 + u, blk = s * 8 + (lane >> 2);
-      if (blk < nb) *reinterpret_cast<uint32_t*>(a.codes + ((size_t)slot * nb + blk) * 16 + (lane & 3) * 4) = q[u];
-      if ((lane & 15) == 0 && s < stages) {
-        const size_t chunk = ((size_t)b * stages * 2 + s * 2 + (lane >> 4)) * a.nrb + (t >> 7);
-        *reinterpret_cast<uint32_t*>(a.scales + chunk * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4) = word[u];
+    for (int u = 0; u < kRqUnroll; ++u) {
+      if (u < n) {
+        if ((s0 + u) * 8 + (lane >> 2) < nb) codes[u * 32] = q[u];
+        if ((lane & 3) == 0) scales[u * 1024 * a.nrb] = (uint8_t)byte[u];
       }
     }
   }
+}
+
+// Route map for the block kernel, by one cluster of kMapCtas CTAs: every CTA
+// counts its part of the routes by expert in shared memory, reads the others'
+// counts, and places its routes. Their order within an expert is that of the
+// atomics, which no result depends on: a row's product is the same in any
+// place of any block. Writes counts, offsets (multiples of bn), the blocks'
+// experts and their number, slot_of_route (-1: no such expert) and
+// route_of_slot (only for slots with a route), and the error word.
+constexpr int kMapCtas = 8;
+constexpr int kMapThreads = 1024;
+
+__global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) k_mx_map(const MxMapArgs a) {
+  __shared__ int s_cnt[kMaxExperts];    // this CTA's routes by expert
+  __shared__ int s_base[kMaxExperts];   // slot of this CTA's first route of the expert
+  __shared__ int s_warp[kMaxExperts / 32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  mx_grid_wait();
+  mx_grid_launch();
+  for (int e = tid; e < kMaxExperts; e += kMapThreads) s_cnt[e] = 0;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  const int part = (a.R + kMapCtas - 1) / kMapCtas, lo = (int)rank * part, hi = min(a.R, lo + part);
+  for (int r0 = lo; r0 < hi; r0 += kMapThreads * 4) {
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * kMapThreads + tid;
+      e[u] = r < hi ? a.ids[r] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * kMapThreads + tid;
+      const bool in = r < hi, ok = in && e[u] >= 0 && e[u] < a.E;
+      if (in && !ok) s_bad = 1;
+      const int key = ok ? e[u] : -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, key);
+      const int leader = __ffs(same) - 1;
+      int at = 0;
+      if (lane == leader && ok) at = atomicAdd(&s_cnt[key], __popc(same));
+      at = __shfl_sync(0xFFFFFFFFu, at, leader) + __popc(same & ((1u << lane) - 1u));
+      if (in) a.slot_of_route[r] = ok ? at : -1;  // the place among this CTA's, for now
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  // thread e: this CTA's base within expert e, and the expert's total
+  int before = 0, total = 0, blocks = 0;
+  if (tid < a.E) {
+#pragma unroll
+    for (int c = 0; c < kMapCtas; ++c) {
+      uint32_t at;
+      int v;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(&s_cnt[tid])), "r"(c));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+      if (c < (int)rank) before += v;
+      total += v;
+    }
+    blocks = (total + a.bn - 1) / a.bn;
+  }
+  int incl = blocks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31 && warp < kMaxExperts / 32) s_warp[warp] = incl;
+  int bad = 0;
+  if (rank == 0 && tid < kMapCtas) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(&s_bad)), "r"(tid));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(bad) : "r"(at) : "memory");
+  }
+  bad = __syncthreads_or(bad);
+  if (tid < a.E) {
+    int first = incl - blocks;
+    for (int w = 0; w < warp; ++w) first += s_warp[w];
+    s_base[tid] = first * a.bn + before;
+    if (rank == 0) {
+      a.counts[tid] = total;
+      a.offsets[tid] = first * a.bn;
+      for (int b = 0; b < blocks; ++b) a.block_expert[first + b] = tid;
+      if (tid == a.E - 1) *a.nblocks = first + blocks;
+    }
+  }
+  if (rank == 0 && tid == 0) *a.err = bad ? 1u : 0u;
+  __syncthreads();
+  for (int r0 = lo + tid; r0 < hi; r0 += kMapThreads * 4) {
+    int at[4], e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * kMapThreads;
+      at[u] = r < hi ? a.slot_of_route[r] : -1;
+      e[u] = r < hi ? a.ids[r] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (at[u] < 0) continue;
+      const int r = r0 + u * kMapThreads, slot = s_base[e[u]] + at[u];
+      a.slot_of_route[r] = slot;
+      a.route_of_slot[slot] = r;
+    }
+  }
+  // no CTA leaves while another may read its counts
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 }  // namespace
@@ -391,14 +541,17 @@ cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int ou
   return TM_BY_DTYPE(out_dtype, go);
 }
 
+cudaError_t launch_mx_map(const MxMapArgs& a, cudaStream_t st) {
+  return mx_launch_after(k_mx_map, dim3(kMapCtas), kMapThreads, 0, st, a);
+}
+
 cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_t st) {
   const int es = dtype_bytes(dtype);
-  const int stages = mx_stages(a.K), pairs = (stages + 1) / 2;
-  const int items = a.x_rows * pairs;
+  const int stages = mx_stages(a.K), segs = (stages + kRqUnroll - 1) / kRqUnroll, per = (stages + segs - 1) / segs;
+  const int items = a.x_rows * segs;
   auto go = [&](auto elem, auto vec) {
-    k_mx_rows_quantize<decltype(elem), decltype(vec)::value><<<(items + 7) / 8, 256, 0, st>>>(a, stages, FastDiv(pairs),
-                                                                                             FastDiv(a.bn), items);
-    return cudaGetLastError();
+    return mx_launch_after(k_mx_rows_quantize<decltype(elem), decltype(vec)::value>, dim3((items + 7) / 8), 256, 0, st, a,
+                           stages, per, FastDiv(segs), FastDiv(a.bn), items);
   };
   return TM_BY_DTYPE_VEC(dtype, eights(a.x, a.ld, a.K, es), go);
 }
