@@ -57,7 +57,7 @@ long mx_max_blocks(const tm_mxfp4_desc& d, long rows, int bn) { return rows / bn
 // the largest block and for the most blocks, so that a workspace for more rows
 // fits fewer.
 struct MxLayout {
-  size_t counts, offsets, block_expert, nblocks, route_of_slot, slot_of_route, codes, scales, total;
+  size_t block_info, nblocks, route_of_slot, slot_of_route, codes, scales, total;
 };
 
 MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
@@ -72,9 +72,7 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
     return at;
   };
   const size_t R = (size_t)rows;
-  L.counts = take((size_t)d.E * 4);
-  L.offsets = take((size_t)d.E * 4);
-  L.block_expert = take(blocks * 4);
+  L.block_info = take(blocks * 8);
   L.nblocks = take(4);
   L.route_of_slot = take(slots * 4);
   L.slot_of_route = take(R * 4);
@@ -142,13 +140,11 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   a.max_blocks = (c.rows + a.bn - 1) / a.bn;
   if (c.ids) {
     a.max_blocks = (int)mx_max_blocks(d, c.rows, a.bn);
-    a.block_expert = i32(L.block_expert);
+    int2* info = reinterpret_cast<int2*>(base + L.block_info);
+    a.block_info = info;
     a.nblocks = i32(L.nblocks);
-    a.counts = i32(L.counts);
-    a.offsets = i32(L.offsets);
     a.route_of_slot = i32(L.route_of_slot);
-    const MxMapArgs rm{c.ids, c.rows, d.E, a.bn, i32(L.counts), i32(L.offsets), i32(L.block_expert), i32(L.nblocks),
-                       i32(L.route_of_slot), i32(L.slot_of_route), err};
+    const MxMapArgs rm{c.ids, c.rows, d.E, a.bn, info, i32(L.nblocks), i32(L.route_of_slot), i32(L.slot_of_route), err};
     if ((e = launch_mx_map(rm, st)) != cudaSuccess) return e;
   }
   MxQuantArgs q{c.x, c.ld, c.x_rows, d.K, c.topk, c.ids ? i32(L.slot_of_route) : nullptr, a.bn, a.nrb, base + L.codes,

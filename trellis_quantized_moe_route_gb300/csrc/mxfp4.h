@@ -26,10 +26,8 @@ struct MxTcArgs {
   int bn;                        // rows of a block: a multiple of 16, <= 240 (gated: <= 112)
   int nrb;                       // 128-row scale chunks of a block: ceil(bn / 128)
   int max_blocks;                // blocks the launch may find
-  const int32_t* block_expert;   // by expert: the route map; NULL: dense, block b = rows b * bn ...
+  const int2* block_info;        // by expert: the map's (expert, rows); NULL: dense, block b = rows b * bn ...
   const int32_t* nblocks;
-  const int32_t* counts;
-  const int32_t* offsets;
   const int32_t* route_of_slot;
   const uint8_t* wscale;         // launch_mx_weight_scales
   const uint8_t* xscale;         // [blocks][2 * stages][nrb][512]
@@ -43,14 +41,12 @@ struct MxTcArgs {
 cudaError_t mx_weight_map(CUtensorMap* m, const uint8_t* codes, long rows, int K);
 cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int out_dtype, cudaStream_t st);
 
-// Route map of the block kernel: as the layer's, but with the routes of an
-// expert in no fixed order.
+// Route map of the block kernel: every expert's routes in blocks of bn slots,
+// in no fixed order within the expert.
 struct MxMapArgs {
   const int32_t* ids;
   int R, E, bn;
-  int32_t* counts;
-  int32_t* offsets;
-  int32_t* block_expert;
+  int2* block_info;        // (expert, rows) of block b, slots b * bn ...
   int32_t* nblocks;
   int32_t* route_of_slot;
   int32_t* slot_of_route;

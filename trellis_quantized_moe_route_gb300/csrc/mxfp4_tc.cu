@@ -12,7 +12,7 @@
 // Persistent, one CTA per SM: a loader thread (TMA boxes of 256 columns = one
 // 128-byte swizzle span of codes, bulk copies of the scale chunks), an issuer
 // thread (scales to tensor memory with tcgen05.cp, then one MMA per 64
-// columns), and eight epilogue warps that drain one accumulator buffer while
+// columns), and sixteen epilogue warps that drain one accumulator buffer while
 // the next unit fills the other. 240 columns twice, plus 24 columns of scales,
 // is what 512 columns of tensor memory hold; that is why a block ends at 240.
 //
@@ -33,7 +33,7 @@ namespace tmoe {
 
 namespace {
 
-constexpr int kMxEpiWarps = 8;
+constexpr int kMxEpiWarps = 16;
 constexpr int kMxThreads = (kMxEpiWarps + 2) * 32;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxSfCol = 480;       // first tensor-memory column of the scales
@@ -49,16 +49,17 @@ struct MxUnit {
   int expert, tile, slot0, rows;
 };
 
-__device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int tiles) {
-  MxUnit m;
+__device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int units, int tiles) {
+  MxUnit m{0, 0, 0, 0};
+  if (u >= units) return m;
   const int b = u / tiles;
   m.tile = u - b * tiles;
   m.slot0 = b * a.bn;
-  if (a.block_expert) {
-    m.expert = a.block_expert[b];
-    m.rows = min(a.bn, a.counts[m.expert] - (m.slot0 - a.offsets[m.expert]));
+  if (a.block_info) {
+    const int2 i = a.block_info[b];
+    m.expert = i.x;
+    m.rows = i.y;
   } else {
-    m.expert = 0;
     m.rows = min(a.bn, a.rows - m.slot0);
   }
   return m;
@@ -73,7 +74,7 @@ template <bool GATED>
 __device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring) {
   MxGeom g;
   g.tiles = (a.N + 127) / 128;
-  const int blocks = a.block_expert ? *a.nblocks : (a.rows + a.bn - 1) / a.bn;
+  const int blocks = a.block_info ? *a.nblocks : (a.rows + a.bn - 1) / a.bn;
   g.units = blocks * g.tiles;
   g.stages = mx_stages(a.K);
   g.ksteps = (mx_blocks(a.K) + 1) / 2;
@@ -92,8 +93,10 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   MxRing r;
   int it = 0;
   bool ok = true;
+  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
-    const MxUnit m = mx_unit(a, u, g.tiles);
+    const MxUnit m = next;
+    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
     const int wrow = m.expert * (GATED ? 2 * a.N : a.N) + m.tile * 128;
     const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles + m.tile) * g.stages * 1024;
     const size_t xsf = (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
@@ -129,8 +132,10 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   constexpr int H = GATED ? 2 : 1;
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem);
+  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
-    const MxUnit m = mx_unit(a, u, g.tiles);
+    const MxUnit m = next;
+    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
     const uint32_t idesc = mx_idesc((m.rows + 15) / 16 * 16);
     const int buf = nu & 1;
     if (nu >= 2 && !mx_wait_warp(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, limit)) break;
@@ -199,20 +204,35 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   T* out = static_cast<T*>(a.out);
   const bool pair = a.N % 2 == 0 && ((uintptr_t)out) % 4 == 0;
-  int nu = 0;
+  // the next unit and its rows' places are read while this one is stored: a
+  // chain of global loads between two units cost about as much as storing one
+  constexpr int kStep = kMxEpiWarps / 4 * 32;  // columns between a warp's pieces of 32
+  constexpr int kPieces = (240 + kStep - 1) / kStep;
+  int nu = 0, row[kPieces];
+  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
+  auto rows_of = [&](const MxUnit& m) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = part * 32 + k * kStep + lane;
+      row[k] = c >= m.rows ? 0 : a.block_info ? a.route_of_slot[m.slot0 + c] : m.slot0 + c;
+    }
+  };
+  rows_of(next);
   for (int u = blockIdx.x; u < g.units; u += gridDim.x, ++nu) {
-    const MxUnit m = mx_unit(a, u, g.tiles);
+    const MxUnit m = next;
+    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
     const int buf = nu & 1;
     const int n = m.tile * 128 + quarter * 32 + lane;
     if (!mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, limit)) return;
     tc_fence_after();
     const uint32_t d = tmem + lane_base + (uint32_t)(buf * (GATED ? 2 : 1) * a.bn);
-    for (int c0 = part * 32; c0 < m.rows; c0 += 64) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c0 = part * 32 + k * kStep;
+      if (c0 >= m.rows) break;
       uint32_t v[32], w[32];
       tmem_ld32(d + c0, v);
       if (GATED) tmem_ld32(d + a.bn + c0, w);
-      int row = m.slot0 + c0 + lane;
-      if (a.route_of_slot) row = c0 + lane < m.rows ? a.route_of_slot[row] : -1;
       tmem_ld_wait();
       reg_fence32(v);
       if (GATED) reg_fence32(w);
@@ -220,8 +240,9 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         y[c] = GATED ? mx_silu(__uint_as_float(v[c])) * __uint_as_float(w[c]) : __uint_as_float(v[c]);
-      mx_store32<T>(y, out, row, m.rows - c0, n, a.N, pair);
+      mx_store32<T>(y, out, row[k], m.rows - c0, n, a.N, pair);
     }
+    rows_of(next);
     tc_fence_before();
     if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
     __syncwarp();
@@ -409,9 +430,9 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
 // counts its part of the routes by expert in shared memory, reads the others'
 // counts, and places its routes. Their order within an expert is that of the
 // atomics, which no result depends on: a row's product is the same in any
-// place of any block. Writes counts, offsets (multiples of bn), the blocks'
-// experts and their number, slot_of_route (-1: no such expert) and
-// route_of_slot (only for slots with a route), and the error word.
+// place of any block. Writes the blocks' experts and rows and the number of
+// blocks, slot_of_route (-1: no such expert), route_of_slot (only for slots
+// with a route) and the error word.
 constexpr int kMapCtas = 8;
 constexpr int kMapThreads = 1024;
 
@@ -484,9 +505,7 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
     for (int w = 0; w < warp; ++w) first += s_warp[w];
     s_base[tid] = first * a.bn + before;
     if (rank == 0) {
-      a.counts[tid] = total;
-      a.offsets[tid] = first * a.bn;
-      for (int b = 0; b < blocks; ++b) a.block_expert[first + b] = tid;
+      for (int b = 0; b < blocks; ++b) a.block_info[first + b] = make_int2(tid, min(a.bn, total - b * a.bn));
       if (tid == a.E - 1) *a.nblocks = first + blocks;
     }
   }
