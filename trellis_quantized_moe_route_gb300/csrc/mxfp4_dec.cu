@@ -113,9 +113,10 @@ __device__ __forceinline__ MdChunk md_find(const MxDecArgs& a, int r0, int* list
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ MxDecArgs a, int split, int per, int ring,
+__global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ MxDecArgs a, int lsplit, int per, int ring,
                                                        uint32_t cols) {
   constexpr int H = GATED ? 2 : 1;
+  const int split = 1 << lsplit;
   extern __shared__ unsigned char md_smem_raw[];
   __shared__ __align__(8) MdBars bars;
   __shared__ uint32_t tmem_slot;
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int rank = split > 1 ? (int)md_cluster_rank() : 0;
-  const int unit = blockIdx.x / split;
+  const int unit = blockIdx.x >> lsplit;
   const int tiles = (a.N + 127) / 128;
   const int chunk = unit / tiles, tile = unit - chunk * tiles;
   const int stages = mx_stages(a.K);
@@ -135,9 +136,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   float* part = reinterpret_cast<float*>(smem + (size_t)ring * stage_bytes);  // [split][H][bn / split][128]
 
   if (split > 1) md_cluster_arrive();  // (waited for before the first store to a peer)
-  mx_grid_wait();
-  mx_grid_launch();
   if (tid == 128) {
+    mx_prefetch_map(&a.wmap);
     for (int i = 0; i < ring; ++i) {
       mbar_init(&bars.full[i], 5);  // the loader's expect_tx and four quantising warps
       mbar_init(&bars.empty[i], 1);
@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     s_abort = 0;
     mbar_fence_init();
   }
+  mx_grid_wait();
+  mx_grid_launch();
   MdChunk m{0, min(a.bn, a.rows - chunk * a.bn), false};
   if (a.ids) {
     m = md_find(a, chunk, warp == 0 ? s_row : nullptr);
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     }
   }
   if (split > 1) md_cluster_wait();  // every CTA of the cluster has started
-  const int own = a.bn / split;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
+  const int own = a.bn >> lsplit;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
   if (warp < 4 && s_hi > s_lo) {
     const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
     tc_fence_after();
@@ -262,9 +264,9 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             if (c0 + c >= m.rows) break;
-            const uint32_t at = to + (uint32_t)(h * own + (c0 + c) / split) * 512;
+            const uint32_t at = to + (uint32_t)(h * own + ((c0 + c) >> lsplit)) * 512;
             if (split > 1)
-              md_peer_store(md_peer(at, (uint32_t)((c0 + c) % split)), v[c]);
+              md_peer_store(md_peer(at, (uint32_t)((c0 + c) & (split - 1))), v[c]);
             else
               part[(size_t)(h * own + c0 + c) * 128 + warp * 32 + lane] = v[c];
           }
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   }
   // the sums of the ranks that had stages, in order
   const int active = (stages + per - 1) / per;
-  for (int i = tid; i < 128 * ((m.rows - rank + split - 1) / split); i += kMdThreads) {
-    const int n = i & 127, o = i >> 7, c = o * split + rank;
+  for (int i = tid; i < 128 * ((m.rows - rank + split - 1) >> lsplit); i += kMdThreads) {
+    const int n = i & 127, o = i >> 7, c = (o << lsplit) + rank;
     float y[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -306,8 +308,9 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   const int stages = mx_stages(a.K), tiles = (a.N + 127) / 128;
   const int units = chunks * tiles;
   // as many parts as there are stages and idle SMs (two CTAs each), at most a portable cluster
-  int split = 1;
-  while (split < 8 && split * 2 <= stages && units * split * 2 <= 2 * a.sms) split *= 2;
+  int lsplit = 0;
+  while (lsplit < 3 && (2 << lsplit) <= stages && (units << lsplit) <= a.sms) ++lsplit;
+  const int split = 1 << lsplit;
   const int per = (stages + split - 1) / split;
   const int stage = (H * (kMxTileBytes + 1024) + a.bn * 128 + 1024 + 1023) / 1024 * 1024;
   const int part = H * a.bn * 128 * 4;
@@ -330,7 +333,7 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   at[1].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, split, per, ring, cols);
+  return cudaLaunchKernelEx(&cfg, kern, a, lsplit, per, ring, cols);
 }
 
 }  // namespace

@@ -20,8 +20,20 @@ __device__ __forceinline__ void mx_grid_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void mx_grid_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // silu(g) = g / (1 + exp(-g)) with the hardware's exp2 and reciprocal (each a
-// few ulp): where exp(-g) overflows the quotient is -0, as it should be.
-__device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// few ulp). Subnormals flush: an exp(-g) that small leaves 1, and a reciprocal
+// that small (g below -87) makes the result 0. Written out because the same
+// through __expf and __fdividef also scales subnormals, and the epilogue of a
+// gated block of 112 rows is bound by its instructions.
+__device__ __forceinline__ float mx_silu(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r;
+}
+
+__device__ __forceinline__ void mx_prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
+}
 
 __device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"

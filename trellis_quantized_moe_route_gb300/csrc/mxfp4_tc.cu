@@ -173,6 +173,7 @@ __device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__
   const int lane = threadIdx.x & 31;
   if (sizeof(T) == 2 && pair) {
     const int odd = lane & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     T* o = out + (n - odd);
     const bool in = n - odd < N;
 #pragma unroll
@@ -182,7 +183,7 @@ __device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__
       t[0] = from_f32<T>(y[c]);
       t[1] = from_f32<T>(y[c + 1]);
       const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
-      const uint32_t word = odd ? __byte_perm(q, p, 0x7632) : __byte_perm(p, q, 0x5410);
+      const uint32_t word = __byte_perm(p, q, pick);
       const int r = __shfl_sync(0xFFFFFFFFu, row, c + odd);
       if (in && c + odd < rows) *reinterpret_cast<uint32_t*>(o + (size_t)r * N) = word;
     }
@@ -268,6 +269,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
     }
     s_abort = 0;
     mbar_fence_init();
+  }
+  if (threadIdx.x == kMxEpiWarps * 32) {
+    mx_prefetch_map(&a.wmap);
+    mx_prefetch_map(&a.xmap);
   }
   if (warp == 0) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
@@ -375,18 +380,26 @@ __global__ void __launch_bounds__(256) k_mx_weight_scales(const uint8_t* __restr
 
 // A warp takes up to kRqUnroll times 256 columns (eight blocks, four lanes
 // each) of a row of x, all loads in flight at once. Dense (no slots): the first
-// thread clears the error word.
+// thread clears the error word. By expert: the route map is the kernel before
+// this one in the stream, and it lets this one start only after it has itself
+// waited for all that came before it, so x may be read, and quantised, while
+// the map is being made; only the slots wait for it.
 constexpr int kRqUnroll = 4;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, int stages, int per, FastDiv segs,
                                                           FastDiv bn, int items) {
-  mx_grid_wait();
-  mx_grid_launch();
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
-  if (!a.slot_of_route && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
-  if (i >= items) return;
+  if (!a.slot_of_route) {
+    mx_grid_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
+  }
+  mx_grid_launch();
+  if (i >= items) {
+    if (a.slot_of_route) mx_grid_wait();
+    return;
+  }
   const int nb = mx_blocks(a.K);
   const int row = (int)segs.div(i), s0 = (i - row * (int)segs.d) * per, n = min(per, stages - s0);
   const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ld + s0 * 256 + lane * 8;
@@ -394,7 +407,6 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
   Eight<T, VEC> e[kRqUnroll];
 #pragma unroll
   for (int u = 0; u < kRqUnroll; ++u) e[u].load(x + u * 256, u < n ? max(0, min(8, left - u * 256)) : 0);
-  const int first = a.slot_of_route ? a.slot_of_route[row * a.topk] : row;
   uint32_t q[kRqUnroll], byte[kRqUnroll];
 #pragma unroll
   for (int u = 0; u < kRqUnroll; ++u) {
@@ -402,9 +414,10 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
     e[u].to(v);
     q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
   }
+  if (a.slot_of_route) mx_grid_wait();
   for (int j = 0; j < a.topk; ++j) {
     const int r = row * a.topk + j;
-    const int slot = j == 0 ? first : a.slot_of_route[r];
+    const int slot = a.slot_of_route ? a.slot_of_route[r] : r;
     if (slot < 0) {
       if (s0 == 0) {
         char* o = static_cast<char*>(a.out) + (size_t)r * a.out_row_bytes;
