@@ -37,7 +37,8 @@ constexpr int kMxEpiWarps = 16;
 constexpr int kMxThreads = (kMxEpiWarps + 2) * 32;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxSfCol = 480;       // first tensor-memory column of the scales
-constexpr uint32_t kMxSmem = 220 * 1024;
+constexpr uint32_t kMxSmem = 226 * 1024;
+constexpr int kMxStoreBytes = 16 * 256;  // 16 rows of 128 16-bit channels, for each four epilogue warps
 
 struct MxBars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
@@ -49,33 +50,37 @@ struct MxUnit {
   int expert, tile, slot0, rows;
 };
 
-__device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int units, int tiles) {
-  MxUnit m{0, 0, 0, 0};
-  if (u >= units) return m;
-  const int b = u / tiles;
-  m.tile = u - b * tiles;
+// Unit u (past the last one: the last, whose values are not used). Without a
+// branch, so that a unit can be read ahead: the load is waited for where its
+// values are used.
+template <bool EXPERTS>
+__device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int units, FastDiv tiles) {
+  MxUnit m;
+  const int v = min(u, units - 1), b = (int)tiles.div((uint32_t)v);
+  m.tile = v - b * (int)tiles.d;
   m.slot0 = b * a.bn;
-  if (a.block_info) {
-    const int2 i = a.block_info[b];
+  if (EXPERTS) {
+    const int2 i = __ldg(a.block_info + b);  // (of an earlier kernel: complete before mx_grid_wait returns)
     m.expert = i.x;
     m.rows = i.y;
   } else {
+    m.expert = 0;
     m.rows = min(a.bn, a.rows - m.slot0);
   }
   return m;
 }
 
 struct MxGeom {
-  int tiles, units, stages, ring, ksteps;
+  FastDiv tiles;
+  int units, stages, ring, ksteps;
   uint32_t a_bytes, b_bytes, sfa_bytes, sfb_bytes, stage_bytes;
 };
 
-template <bool GATED>
-__device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring) {
-  MxGeom g;
-  g.tiles = (a.N + 127) / 128;
-  const int blocks = a.block_info ? *a.nblocks : (a.rows + a.bn - 1) / a.bn;
-  g.units = blocks * g.tiles;
+template <bool GATED, bool EXPERTS>
+__device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring, FastDiv tiles) {
+  MxGeom g{tiles};
+  const int blocks = EXPERTS ? *a.nblocks : (a.rows + a.bn - 1) / a.bn;
+  g.units = blocks * (int)tiles.d;
   g.stages = mx_stages(a.K);
   g.ksteps = (mx_blocks(a.K) + 1) / 2;
   g.ring = ring;
@@ -87,18 +92,18 @@ __device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring) {
   return g;
 }
 
-template <bool GATED>
+template <bool GATED, bool EXPERTS>
 __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
                           uint64_t limit) {
   MxRing r;
   int it = 0;
   bool ok = true;
-  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
+  MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
     const MxUnit m = next;
-    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
+    next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
     const int wrow = m.expert * (GATED ? 2 * a.N : a.N) + m.tile * 128;
-    const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles + m.tile) * g.stages * 1024;
+    const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles.d + m.tile) * g.stages * 1024;
     const size_t xsf = (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
     for (int s = 0; s < g.stages; ++s, ++it, r.next(g.ring)) {
       if (it >= g.ring && !mbar_wait_abort(&B.empty[r.slot], r.phase ^ 1, abort, limit)) {
@@ -113,7 +118,7 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
       mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
       unsigned char* sf = st + g.a_bytes + g.b_bytes;
       bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
-      if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)g.tiles * g.stages + s) * 1024, 1024, bar);
+      if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)g.tiles.d * g.stages + s) * 1024, 1024, bar);
       bulk_g2s(sf + g.sfa_bytes, a.xscale + xsf + (size_t)s * g.sfb_bytes, g.sfb_bytes, bar);
     }
   }
@@ -123,7 +128,7 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   }
 }
 
-template <bool GATED, int NRB>
+template <bool GATED, bool EXPERTS, int NRB>
 __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
                           volatile int* abort, uint64_t limit) {
   MxRing r;
@@ -132,10 +137,10 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   constexpr int H = GATED ? 2 : 1;
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem);
-  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
+  MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
     const MxUnit m = next;
-    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
+    next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
     const uint32_t idesc = mx_idesc((m.rows + 15) / 16 * 16);
     const int buf = nu & 1;
     if (nu >= 2 && !mx_wait_warp(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, limit)) break;
@@ -164,64 +169,82 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
 }
 
 // 32 columns (rows of y) of a thread's channel, as T: y[c] for row `row` of
-// lane c, `rows` of them. 16-bit types with `pair` (an even number of channels,
-// 4-byte aligned): neighbouring lanes swap halves, so that the even one stores
-// both channels of column c and the odd one those of column c + 1.
+// lane c, `rows` of them.
 template <typename T>
-__device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__ out, int row, int rows, int n, int N,
-                                           bool pair) {
-  const int lane = threadIdx.x & 31;
-  if (sizeof(T) == 2 && pair) {
-    const int odd = lane & 1;
-    const uint32_t pick = odd ? 0x3276u : 0x5410u;
-    T* o = out + (n - odd);
-    const bool in = n - odd < N;
+__device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__ out, int row, int rows, int n, int N) {
+  T* o = out + n;
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      uint32_t p;
-      T* t = reinterpret_cast<T*>(&p);
-      t[0] = from_f32<T>(y[c]);
-      t[1] = from_f32<T>(y[c + 1]);
-      const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
-      const uint32_t word = __byte_perm(p, q, pick);
-      const int r = __shfl_sync(0xFFFFFFFFu, row, c + odd);
-      if (in && c + odd < rows) *reinterpret_cast<uint32_t*>(o + (size_t)r * N) = word;
-    }
-  } else {
-    T* o = out + n;
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const int r = __shfl_sync(0xFFFFFFFFu, row, c);
-      if (n < N && c < rows) o[(size_t)r * N] = from_f32<T>(y[c]);
-    }
+  for (int c = 0; c < 32; ++c) {
+    const int r = __shfl_sync(0xFFFFFFFFu, row, c);
+    if (n < N && c < rows) o[(size_t)r * N] = from_f32<T>(y[c]);
   }
 }
 
-template <bool GATED, typename T>
-__device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, volatile int* abort,
-                            uint64_t limit) {
+// The same for 16-bit types where rows of y are whole 16-byte words: the four
+// warps of a piece (128 channels) put 16 rows at a time into shared memory and
+// store them from there in 16-byte words, a whole row's 256 bytes by 16 lanes
+// (as single elements a warp's store covered 64 bytes, and storing a piece of
+// 32 rows took 1400 cycles). Neighbouring lanes first swap halves, so that the
+// even one holds both channels of an even row and the odd one of the next; the
+// 64-byte halves of odd rows change places, which keeps the two apart in banks.
+template <typename T>
+__device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __restrict__ out, int row, int rows, int tile,
+                                                 int N, unsigned char* stage, int bar) {
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, odd = lane & 1;
+  const uint32_t pick = odd ? 0x3276u : 0x5410u;
+  const int t = quarter * 32 + lane, chunk = t & 15;
+  const bool in = tile * 128 + chunk * 8 < N;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h * 16 >= rows) break;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      uint32_t p;
+      T* e = reinterpret_cast<T*>(&p);
+      e[0] = from_f32<T>(y[h * 16 + c]);
+      e[1] = from_f32<T>(y[h * 16 + c + 1]);
+      const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
+      const int word = (quarter * 16 + (lane >> 1)) ^ (odd << 4);
+      *reinterpret_cast<uint32_t*>(stage + (c + odd) * 256 + word * 4) = __byte_perm(p, q, pick);
+    }
+    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = k * 8 + (t >> 4);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((chunk * 16) ^ ((r & 1) << 6)));
+      const int to = __shfl_sync(0xFFFFFFFFu, row, h * 16 + r);
+      if (in && h * 16 + r < rows)
+        *reinterpret_cast<uint4*>(out + (size_t)to * N + tile * 128 + chunk * 8) = v;
+    }
+    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
+  }
+}
+
+template <bool GATED, bool EXPERTS, typename T>
+__device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, unsigned char* stage,
+                            volatile int* abort, uint64_t limit) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quarter = warp & 3, part = warp >> 2;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   T* out = static_cast<T*>(a.out);
-  const bool pair = a.N % 2 == 0 && ((uintptr_t)out) % 4 == 0;
+  const bool words = sizeof(T) == 2 && a.N % 8 == 0 && ((uintptr_t)out) % 16 == 0;
   // the next unit and its rows' places are read while this one is stored: a
   // chain of global loads between two units cost about as much as storing one
   constexpr int kStep = kMxEpiWarps / 4 * 32;  // columns between a warp's pieces of 32
   constexpr int kPieces = (240 + kStep - 1) / kStep;
   int nu = 0, row[kPieces];
-  MxUnit next = mx_unit(a, blockIdx.x, g.units, g.tiles);
+  MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
   auto rows_of = [&](const MxUnit& m) {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       const int c = part * 32 + k * kStep + lane;
-      row[k] = c >= m.rows ? 0 : a.block_info ? a.route_of_slot[m.slot0 + c] : m.slot0 + c;
+      row[k] = EXPERTS ? (c < m.rows ? a.route_of_slot[m.slot0 + c] : 0) : m.slot0 + c;
     }
   };
   rows_of(next);
   for (int u = blockIdx.x; u < g.units; u += gridDim.x, ++nu) {
     const MxUnit m = next;
-    next = mx_unit(a, u + gridDim.x, g.units, g.tiles);
+    next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
     const int buf = nu & 1;
     const int n = m.tile * 128 + quarter * 32 + lane;
     if (!mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, limit)) return;
@@ -241,7 +264,10 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         y[c] = GATED ? mx_silu(__uint_as_float(v[c])) * __uint_as_float(w[c]) : __uint_as_float(v[c]);
-      mx_store32<T>(y, out, row[k], m.rows - c0, n, a.N, pair);
+      if (words)
+        mx_store32_words<T>(y, out, row[k], m.rows - c0, m.tile, a.N, stage + part * kMxStoreBytes, 1 + part);
+      else
+        mx_store32<T>(y, out, row[k], m.rows - c0, n, a.N);
     }
     rows_of(next);
     tc_fence_before();
@@ -250,8 +276,8 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
   }
 }
 
-template <bool GATED, typename T>
-__global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__ MxTcArgs a, int ring) {
+template <bool GATED, bool EXPERTS, typename T>
+__global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__ MxTcArgs a, int ring, FastDiv tiles) {
   extern __shared__ unsigned char mx_smem_raw[];
   __shared__ __align__(8) MxBars bars;
   __shared__ uint32_t tmem_slot;
@@ -283,16 +309,18 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
-  const MxGeom g = mx_geom<GATED>(a, ring);
-  if (warp < kMxEpiWarps) {
-    mx_epilogue<GATED, T>(a, g, bars, tmem, abort, limit);
+  const MxGeom g = mx_geom<GATED, EXPERTS>(a, ring, tiles);
+  if (g.units == 0) {
+    // (every route was dropped)
+  } else if (warp < kMxEpiWarps) {
+    mx_epilogue<GATED, EXPERTS, T>(a, g, bars, tmem, smem + (size_t)ring * g.stage_bytes, abort, limit);
   } else if (threadIdx.x == kMxEpiWarps * 32) {
-    mx_loader<GATED>(a, g, bars, smem, abort, limit);
+    mx_loader<GATED, EXPERTS>(a, g, bars, smem, abort, limit);
   } else if (warp == kMxEpiWarps + 1) {
     if (a.nrb == 1)
-      mx_issuer<GATED, 1>(a, g, bars, smem, tmem, abort, limit);
+      mx_issuer<GATED, EXPERTS, 1>(a, g, bars, smem, tmem, abort, limit);
     else
-      mx_issuer<GATED, 2>(a, g, bars, smem, tmem, abort, limit);
+      mx_issuer<GATED, EXPERTS, 2>(a, g, bars, smem, tmem, abort, limit);
   }
   tc_fence_before();
   __syncthreads();
@@ -346,17 +374,19 @@ cudaError_t mx_launch_after(void (*kern)(P...), dim3 grid, int threads, size_t s
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <bool GATED, typename T>
+template <bool GATED, bool EXPERTS, typename T>
 cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
-  auto kern = k_mx_tc<GATED, T>;
+  auto kern = k_mx_tc<GATED, EXPERTS, T>;
   static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
   if (attr != cudaSuccess) return attr;
   const uint32_t stage = (uint32_t)(GATED ? 2 : 1) * (kMxTileBytes + 1024) + (uint32_t)a.bn * 128 + (uint32_t)a.nrb * 1024;
   const uint32_t stage_bytes = (stage + 1023) / 1024 * 1024;
-  const int ring = (int)std::min<uint32_t>(kMxMaxStages, (kMxSmem - 1024) / stage_bytes);
+  const uint32_t store = kMxEpiWarps / 4 * kMxStoreBytes;
+  const int ring = (int)std::min<uint32_t>(kMxMaxStages, (kMxSmem - 1024 - store) / stage_bytes);
   const long units = (long)a.max_blocks * ((a.N + 127) / 128);
   const int grid = (int)std::max<long>(1, std::min<long>(units, a.sms));
-  return mx_launch_after(kern, dim3(grid), kMxThreads, 1024 + ring * stage_bytes, st, a, ring);
+  return mx_launch_after(kern, dim3(grid), kMxThreads, 1024 + ring * stage_bytes + store, st, a, ring,
+                         FastDiv((a.N + 127) / 128));
 }
 
 // One thread a 4-byte word of the laid-out scales; absent rows and blocks get 0.
@@ -410,9 +440,11 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
   uint32_t q[kRqUnroll], byte[kRqUnroll];
 #pragma unroll
   for (int u = 0; u < kRqUnroll; ++u) {
-    float v[8];
-    e[u].to(v);
-    q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
+    if (u < n) {
+      float v[8];
+      e[u].to(v);
+      q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
+    }
   }
   if (a.slot_of_route) mx_grid_wait();
   for (int j = 0; j < a.topk; ++j) {
@@ -449,6 +481,18 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
 constexpr int kMapCtas = 8;
 constexpr int kMapThreads = 1024;
 
+// Up to kMapHeld routes of a thread stay in registers between the two passes;
+// more go through slot_of_route.
+constexpr int kMapHeld = 4;
+
+__device__ __forceinline__ int map_peer_int(const int* p, int rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) k_mx_map(const MxMapArgs a) {
   __shared__ int s_cnt[kMaxExperts];    // this CTA's routes by expert
   __shared__ int s_base[kMaxExperts];   // slot of this CTA's first route of the expert
@@ -457,48 +501,44 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  mx_grid_wait();
-  mx_grid_launch();
   for (int e = tid; e < kMaxExperts; e += kMapThreads) s_cnt[e] = 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
+  mx_grid_wait();
+  mx_grid_launch();
   const int part = (a.R + kMapCtas - 1) / kMapCtas, lo = (int)rank * part, hi = min(a.R, lo + part);
-  for (int r0 = lo; r0 < hi; r0 += kMapThreads * 4) {
-    int e[4];
+  const bool held = part <= kMapHeld * kMapThreads;
+  int e[kMapHeld], at[kMapHeld];
+  for (int r0 = lo + tid; r0 < hi; r0 += kMapThreads * kMapHeld) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * kMapThreads + tid;
-      e[u] = r < hi ? a.ids[r] : 0;
-    }
+    for (int u = 0; u < kMapHeld; ++u) e[u] = r0 + u * kMapThreads < hi ? a.ids[r0 + u * kMapThreads] : 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * kMapThreads + tid;
-      const bool in = r < hi, ok = in && e[u] >= 0 && e[u] < a.E;
-      if (in && !ok) s_bad = 1;
-      const int key = ok ? e[u] : -1;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, key);
-      const int leader = __ffs(same) - 1;
-      int at = 0;
-      if (lane == leader && ok) at = atomicAdd(&s_cnt[key], __popc(same));
-      at = __shfl_sync(0xFFFFFFFFu, at, leader) + __popc(same & ((1u << lane) - 1u));
-      if (in) a.slot_of_route[r] = ok ? at : -1;  // the place among this CTA's, for now
+    for (int u = 0; u < kMapHeld; ++u) {
+      const int r = r0 + u * kMapThreads;
+      at[u] = -1;
+      if (r < hi) {
+        if (e[u] >= 0 && e[u] < a.E)
+          at[u] = atomicAdd(&s_cnt[e[u]], 1);
+        else
+          s_bad = 1;
+        if (!held) a.slot_of_route[r] = at[u];  // the place among this CTA's, for now
+      }
     }
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-  // thread e: this CTA's base within expert e, and the expert's total
+  // thread x: this CTA's base within expert x, and the expert's total
   int before = 0, total = 0, blocks = 0;
   if (tid < a.E) {
 #pragma unroll
     for (int c = 0; c < kMapCtas; ++c) {
-      uint32_t at;
-      int v;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(&s_cnt[tid])), "r"(c));
-      asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+      const int v = map_peer_int(&s_cnt[tid], c);
       if (c < (int)rank) before += v;
       total += v;
     }
     blocks = (total + a.bn - 1) / a.bn;
   }
+  const int bad = __syncthreads_or(rank == 0 && tid < kMapCtas ? map_peer_int(&s_bad, tid) : 0);
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");  // (done with the peers' counts)
   int incl = blocks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -506,13 +546,7 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
     if (lane >= o) incl += v;
   }
   if (lane == 31 && warp < kMaxExperts / 32) s_warp[warp] = incl;
-  int bad = 0;
-  if (rank == 0 && tid < kMapCtas) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(&s_bad)), "r"(tid));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(bad) : "r"(at) : "memory");
-  }
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   if (tid < a.E) {
     int first = incl - blocks;
     for (int w = 0; w < warp; ++w) first += s_warp[w];
@@ -524,24 +558,25 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
   }
   if (rank == 0 && tid == 0) *a.err = bad ? 1u : 0u;
   __syncthreads();
-  for (int r0 = lo + tid; r0 < hi; r0 += kMapThreads * 4) {
-    int at[4], e[4];
+  for (int r0 = lo + tid; r0 < hi; r0 += kMapThreads * kMapHeld) {
+    if (!held) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * kMapThreads;
-      at[u] = r < hi ? a.slot_of_route[r] : -1;
-      e[u] = r < hi ? a.ids[r] : 0;
+      for (int u = 0; u < kMapHeld; ++u) {
+        const int r = r0 + u * kMapThreads;
+        e[u] = r < hi ? a.ids[r] : 0;
+        at[u] = r < hi ? a.slot_of_route[r] : -1;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (at[u] < 0) continue;
-      const int r = r0 + u * kMapThreads, slot = s_base[e[u]] + at[u];
+    for (int u = 0; u < kMapHeld; ++u) {
+      const int r = r0 + u * kMapThreads;
+      if (r >= hi) break;
+      const int slot = at[u] < 0 ? -1 : s_base[e[u]] + at[u];
       a.slot_of_route[r] = slot;
-      a.route_of_slot[slot] = r;
+      if (slot >= 0) a.route_of_slot[slot] = r;
     }
   }
-  // no CTA leaves while another may read its counts
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no CTA leaves while another reads its counts
 }
 
 }  // namespace
@@ -568,7 +603,8 @@ cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int ou
   if (e != cudaSuccess) return e;
   auto go = [&](auto elem) {
     using T = decltype(elem);
-    return a.gated ? mx_launch<true, T>(a, st) : mx_launch<false, T>(a, st);
+    if (a.block_info) return a.gated ? mx_launch<true, true, T>(a, st) : mx_launch<false, true, T>(a, st);
+    return a.gated ? mx_launch<true, false, T>(a, st) : mx_launch<false, false, T>(a, st);
   };
   return TM_BY_DTYPE(out_dtype, go);
 }
