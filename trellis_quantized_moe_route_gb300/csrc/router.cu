@@ -13,13 +13,21 @@
 //         + w_tj (dw_tj - sum_i w_ti dw_ti)                              e = id_j
 // All of it in fp32 whatever the logits' type; only dl is rounded to it.
 //
-// One warp takes a token: expert e = lane + 32 i sits in register i of its
-// lane, so a row is read once, coalesced, with no alignment asked for. The
-// statistics stay in registers over all of a warp's tokens, are added over the
-// CTA's warps in shared memory and over the CTAs by a second kernel, always in
-// the same order: no atomics, the same bits every time. The backward pass
-// reads the logits again and rebuilds p from lse, which costs less than
-// storing p (T E fp32).
+// One warp takes a token, V logits a lane, and reads the next token's row while
+// it works on this one. What bounds it is the selection's instructions, not the
+// bytes. Each logit becomes a 32-bit key that is unique in the row and orders
+// like (logit, then lower expert): 16-bit logits have their expert in the low
+// half; fp32 logits give up their lowest 8 bits for it, and a token in which two
+// of the k + 1 largest agree in the other 24 (one in some hundred, or equal
+// logits) is selected again on the whole values. A lane sorts its keys once
+// (min / max only, nothing carried along); each of the k rounds is then one
+// warp-wide maximum of the lanes' first keys, and the lane that held it moves up.
+//
+// Probability sums stay in registers over all of a warp's tokens, are added over
+// the CTA's warps in shared memory and over the CTAs by a second kernel, always
+// in the same order; counts are integers. So the same bits every time. The
+// backward pass reads the logits again and rebuilds p from lse, which costs less
+// than storing p (T E fp32).
 #include <algorithm>
 
 #include "elem.cuh"
@@ -32,19 +40,133 @@ namespace {
 constexpr int kRtWarps = 16;      // warps of a CTA with many tokens
 constexpr int kRtMaxCtas = 304;   // two CTAs of 512 threads on each of 152 SMs
 
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t b = __float_as_uint(f + 0.0f);  // -0 as +0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float order_unkey(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
+// Orderable bits of a logit (larger value, larger bits; -0 as +0), in the upper
+// kBits of a word, and back. kNone: the largest such word for -inf.
+template <typename T>
+struct Order;
+template <>
+struct Order<float> {
+  static constexpr uint32_t kMask = 0xFFFFFF00u, kNone = 0x007FFFFFu;
+  static __device__ __forceinline__ uint32_t key(float f) {
+    const uint32_t b = __float_as_uint(f + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+  }
+};
+// (16-bit types: `bits` has the logit in its upper half, zeros below)
+struct Order16 {
+  static constexpr uint32_t kMask = 0xFFFF0000u;
+  static __device__ __forceinline__ uint32_t key(uint32_t bits) {
+    return bits ^ (((uint32_t)((int32_t)bits >> 31) & 0x7FFF0000u) | 0x80000000u);
+  }
+};
+template <>
+struct Order<__nv_bfloat16> : Order16 {
+  static constexpr uint32_t kNone = 0x007FFFFFu;  // -inf is 0xFF80
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFF0000u));
+  }
+};
+template <>
+struct Order<__half> : Order16 {
+  static constexpr uint32_t kNone = 0x03FFFFFFu;  // -inf is 0xFC00
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __half2float(__ushort_as_half((unsigned short)((k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFF0000u)) >> 16)));
+  }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+
+// exp(x) for x <= 0 or NaN by the hardware's exp2 (the product's rounding is
+// |x| 2^-24, as the subtraction's before it).
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
+// The sum over the first k lanes' values in all of them (others hold 0); a
+// warp-wide sum where k > 8.
+__device__ __forceinline__ float first_sum(float v, int k) {
+  if (k > 8) {
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// A row of logits over a warp: V of them a lane (V even). 16-bit types take
+// neighbours in pairs, one 4-byte load each where `pair` allows it. Past the
+// last expert stands -inf: with a higher number than any expert, it comes after
+// an expert's own -inf, and its probability is 0.
+template <int V, typename T>
+struct RowRegs {
+  uint32_t raw[sizeof(T) == 2 ? V / 2 : V];
+
+  static __device__ __forceinline__ int expert(int i) {
+    const int lane = threadIdx.x & 31;
+    return sizeof(T) == 2 ? 2 * lane + 64 * (i >> 1) + (i & 1) : lane + 32 * i;
+  }
+  static constexpr uint32_t kInf16 = sizeof(T) == 2 ? Order<T>::kNone >> 16 : 0;  // ~ of -inf's bits
+  __device__ __forceinline__ void load(const T* __restrict__ row, int E, bool pair) {
+    if (sizeof(T) == 2) {
+      const uint32_t none = 0xFFFFu & ~kInf16;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const int e = expert(2 * i);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + e;
+        raw[i] = none | none << 16;
+        if (pair && e + 1 < E)
+          raw[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        else if (e < E)
+          raw[i] = __ldg(p) | (e + 1 < E ? (uint32_t)__ldg(p + 1) : none) << 16;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        raw[i] = 0xFF800000u;
+        if (expert(i) < E) raw[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + expert(i));
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(raw[i]);
+    const uint16_t h = (uint16_t)(raw[i >> 1] >> (16 * (i & 1)));
+    return to_f32(*reinterpret_cast<const T*>(&h));
+  }
+  // Unique keys: the logit's order, then the lower expert.
+  __device__ __forceinline__ void keys(uint32_t (&key)[V]) const {
+    if (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        key[i] = (Order<float>::key(__uint_as_float(raw[i])) & Order<T>::kMask) | (0xFFu - (uint32_t)expert(i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const uint32_t w = add_zero(raw[i]);
+        key[2 * i] = Order16::key(w << 16) | (0xFFFFu - (uint32_t)expert(2 * i));
+        key[2 * i + 1] = Order16::key(w & 0xFFFF0000u) | (0xFFFFu - (uint32_t)expert(2 * i + 1));
+      }
+    }
+  }
+  // -0 becomes +0
+  static __device__ __forceinline__ uint32_t add_zero(uint32_t w) {
+    if (std::is_same<T, __nv_bfloat16>::value) {
+      const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.0f));
+      return *reinterpret_cast<const uint32_t*>(&s);
+    }
+    const __half2 s = __hadd2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(0.0f));
+    return *reinterpret_cast<const uint32_t*>(&s);
+  }
+};
 
 struct RouterFwd {
   const void* logits;
@@ -139,122 +261,130 @@ __device__ void router_finish(const RouterFwd& a, int parts, float (*s_acc)[V * 
   }
 }
 
-// Keys of one token, expert lane + 32 i in place i (absent: 0, below every
-// float's), sorted descending within the lane; `perm` holds the places they
-// came from, four bits each, equal keys in order of place.
-template <int V>
-__device__ __forceinline__ void router_sort(uint32_t (&key)[V], uint32_t& perm) {
-  uint32_t id[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) id[i] = i;
-  // odd-even transposition: neighbours swap only when out of order, so it is stable
+// The k largest of a row: lane j < k returns the j-th expert. `key`: the unique
+// keys (0: absent), consumed. Returns whether the order is certain.
+template <int V, typename T>
+__device__ __forceinline__ bool router_select(uint32_t (&key)[V], int k, int E, uint32_t& mine, uint32_t& first) {
+  const int lane = threadIdx.x & 31;
+  // odd-even transposition, largest first
 #pragma unroll
   for (int r = 0; r < V; ++r)
 #pragma unroll
     for (int i = r & 1; i + 1 < V; i += 2) {
-      const bool sw = key[i + 1] > key[i];
-      const uint32_t k0 = key[i], k1 = key[i + 1], d0 = id[i], d1 = id[i + 1];
-      key[i] = sw ? k1 : k0;
-      key[i + 1] = sw ? k0 : k1;
-      id[i] = sw ? d1 : d0;
-      id[i + 1] = sw ? d0 : d1;
+      const uint32_t hi = max(key[i], key[i + 1]);
+      key[i + 1] = min(key[i], key[i + 1]);
+      key[i] = hi;
     }
-  perm = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) perm |= id[i] << (4 * i);
-}
-
-// One token by one warp: l[i] is the logit of expert lane + 32 i. The k rounds
-// take the largest of the lanes' first keys; the lane it came from moves its
-// keys up by one. Adds the token's statistics to the lane's sums.
-template <int V>
-__device__ __forceinline__ void router_token(const RouterFwd& a, int t, const float (&l)[V], bool on,
-                                             float (&acc)[V], int (&cnt)[V], float& z, int& n) {
-  const int lane = threadIdx.x & 31;
-  uint32_t key[V], perm;
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < a.E ? order_key(l[i]) : 0u;
-  router_sort<V>(key, perm);
-  uint32_t sel = 0;  // bit i: expert lane + 32 i was selected
-  uint32_t my_key = 0, my_id = 0, first = 0;
-  for (int j = 0; j < a.k; ++j) {
+  const int rounds = sizeof(T) == 4 && k < E ? k + 1 : k;  // (fp32: the first one left out, too)
+  uint32_t extra = 0;
+  auto round = [&] {
     const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key[0]);
-    const uint32_t id = lane + 32 * (perm & 15u);
-    uint32_t who = __ballot_sync(0xFFFFFFFFu, key[0] == best);
-    uint32_t winner = __ffs(who) - 1;
-    uint32_t wid = __shfl_sync(0xFFFFFFFFu, id, winner);
-    if (who & (who - 1)) {  // equal logits: the lowest expert
-      wid = __reduce_min_sync(0xFFFFFFFFu, key[0] == best ? id : 0xFFFFFFFFu);
-      winner = wid & 31u;
-    }
-    if (j == 0) first = best;
-    if (lane == j) {
-      my_key = best;
-      my_id = wid;
-    }
-    if (lane == (int)winner) {
-      sel |= 1u << (perm & 15u);
-      perm >>= 4;
+    if (key[0] == best) {
 #pragma unroll
       for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
       key[V - 1] = 0u;
     }
+    return best;
+  };
+  mine = first = round();
+#pragma unroll 4
+  for (int j = 1; j < rounds; ++j) {
+    extra = round();  // (k = 32: the last one is in no lane)
+    if (lane == j) mine = extra;
   }
-  const float m = order_unkey(first);
-  const bool some = m != -INFINITY;
-  float p[V], total = 0.0f;
+  if (sizeof(T) == 2) return true;
+  uint32_t next = __shfl_down_sync(0xFFFFFFFFu, mine, 1);
+  if (lane == 31) next = extra;
+  const bool same = lane + 1 < rounds && ((mine ^ next) & Order<T>::kMask) == 0;
+  return !__any_sync(0xFFFFFFFFu, same);
+}
+
+// The same on the whole fp32 values, equal ones by the lower expert.
+template <int V>
+__device__ __noinline__ uint32_t router_select_exact(const float* __restrict__ row, int k, int E) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[V], mine = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    p[i] = lane + 32 * i < a.E ? __expf(l[i] - m) : 0.0f;
-    total += p[i];
-  }
-  total = warp_sum(total);
-  const float we = lane < a.k ? __expf(order_unkey(my_key) - m) : 0.0f;
-  const float wsum = warp_sum(we);
-  const float lse = m + logf(total);
-  if (lane < a.k) {
-    a.ids[(size_t)t * a.k + lane] = (int)my_id;
-    a.w[(size_t)t * a.k + lane] = some ? we / wsum : 0.0f;
-  }
-  if (lane == 0) a.lse[t] = some ? lse : -INFINITY;
-  if (on && some) {
-    const float inv = 1.0f / total;
+  for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < E ? Order<float>::key(row[lane + 32 * i]) : 0u;
+  for (int j = 0; j < k; ++j) {
+    uint32_t m = key[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      acc[i] += p[i] * inv;
-      if ((sel >> i & 1u) && l[i] != -INFINITY) ++cnt[i];
-    }
-    z += lse * lse;
-    ++n;
+    for (int i = 1; i < V; ++i) m = max(m, key[i]);
+    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, m);
+    uint32_t id = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == best) id = lane + 32 * i;
+    id = __reduce_min_sync(0xFFFFFFFFu, id);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane + 32 * i == (int)id) key[i] = 0u;
+    if (lane == j) mine = id;
   }
+  return mine;
 }
 
 // A warp's tokens are warp, warp + W, ... (W: warps of the grid). With one CTA
 // the statistics are finished here.
 template <int V, typename T>
-__global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a) {
+__global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a, bool pair) {
+  using Row = RowRegs<V, T>;
   __shared__ float s_acc[kRtWarps][V * 32];
-  __shared__ int s_cnt[kRtWarps][V * 32];
+  __shared__ int s_cnt[kRtWarps][V * 32];  // (the finishing sums use it by warp; the first row counts here)
   __shared__ float s_z[kRtWarps];
   __shared__ int s_nv[kRtWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  for (int e = threadIdx.x; e < V * 32; e += blockDim.x) s_cnt[0][e] = 0;
+  __syncthreads();
   const T* logits = static_cast<const T*>(a.logits);
   float acc[V] = {};
-  int cnt[V] = {};
   float z = 0.0f;
   int n = 0;
-  for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) {
-    const T* row = logits + (size_t)t * a.ld;
-    float l[V];
+  const int step = gridDim.x * warps;
+  int t = blockIdx.x * warps + warp;
+  Row row;
+  if (t < a.T) row.load(logits + (size_t)t * a.ld, a.E, pair);
+  for (; t < a.T; t += step) {
+    const Row now = row;
+    if (t + step < a.T) row.load(logits + (size_t)(t + step) * a.ld, a.E, pair);
+    const bool on = a.mask == nullptr || a.mask[t] != 0;
+    uint32_t key[V], mine, first;
+    now.keys(key);
+    const bool sure = router_select<V, T>(key, a.k, a.E, mine, first);
+    uint32_t id = ~Order<T>::kMask - (mine & ~Order<T>::kMask);
+    const T* src = logits + (size_t)t * a.ld;
+    if (sizeof(T) == 4 && !sure) id = router_select_exact<V>(reinterpret_cast<const float*>(src), a.k, a.E);
+    // any value near the largest serves as the softmax's offset: fp32's lacks its low bits
+    const bool some = first > Order<T>::kNone;
+    const float m = Order<T>::value(first & Order<T>::kMask);
+    float my_l = 0.0f;
+    if (lane < a.k) my_l = sizeof(T) == 4 ? to_f32(src[id]) : Order<T>::value(mine & Order<T>::kMask);
+    float p[V], total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : 0.0f;
-    router_token<V>(a, t, l, a.mask == nullptr || a.mask[t] != 0, acc, cnt, z, n);
+    for (int i = 0; i < V; ++i) {
+      p[i] = exp_fast(now.get(i) - m);
+      total += p[i];
+    }
+    total = warp_sum(total);
+    const float we = lane < a.k ? exp_fast(my_l - m) : 0.0f;
+    const float wsum = first_sum(we, a.k);
+    const float lse = m + __logf(total);
+    if (lane < a.k) {
+      a.ids[(size_t)t * a.k + lane] = (int)id;
+      a.w[(size_t)t * a.k + lane] = some ? __fdividef(we, wsum) : 0.0f;
+      if (on && some && my_l != -INFINITY) atomicAdd(&s_cnt[0][id], 1);
+    }
+    if (lane == 0) a.lse[t] = some ? lse : -INFINITY;
+    if (on && some) {
+      const float inv = __fdividef(1.0f, total);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += p[i] * inv;
+      z += lse * lse;
+      ++n;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    s_acc[warp][lane + 32 * i] = acc[i];
-    s_cnt[warp][lane + 32 * i] = cnt[i];
-  }
+  for (int i = 0; i < V; ++i) s_acc[warp][Row::expert(i)] = acc[i];
   if (lane == 0) {
     s_z[warp] = z;
     s_nv[warp] = n;
@@ -262,13 +392,9 @@ __global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a) {
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float p = 0.0f;
-    int c = 0;
-    for (int u = 0; u < warps; ++u) {
-      p += s_acc[u][e];
-      c += s_cnt[u][e];
-    }
+    for (int u = 0; u < warps; ++u) p += s_acc[u][e];
     a.part_prob[(size_t)blockIdx.x * a.E + e] = p;
-    a.part_counts[(size_t)blockIdx.x * a.E + e] = c;
+    a.part_counts[(size_t)blockIdx.x * a.E + e] = s_cnt[0][e];
   }
   if (threadIdx.x == 0) {
     float zs = 0.0f;
@@ -309,7 +435,8 @@ struct RouterBwd {
 };
 
 template <int V, typename T>
-__global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a) {
+__global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a, bool pair) {
+  using Row = RowRegs<V, T>;
   __shared__ float s_sel[8][V * 32];  // each warp's selected experts' gradients, zero between tokens
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* logits = static_cast<const T*>(a.logits);
@@ -321,42 +448,71 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a) {
   float f[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    f[i] = lane + 32 * i < a.E ? (float)a.counts[lane + 32 * i] * inv_n / (float)a.k : 0.0f;
+    const int e = Row::expert(i);
+    f[i] = e < a.E ? (float)a.counts[e] * inv_n / (float)a.k : 0.0f;
     s_sel[warp][lane + 32 * i] = 0.0f;
   }
   __syncwarp();
-  for (int t = blockIdx.x * 8 + warp; t < a.T; t += gridDim.x * 8) {
-    const T* row = logits + (size_t)t * a.ld;
-    const float lse = a.lse[t];
-    const bool on = lse != -INFINITY && (a.mask == nullptr || a.mask[t] != 0);
+  // a token's inputs, read while the one before it is worked on
+  struct In {
+    Row row;
+    float lse, w, g;
+    int id;
+    bool on;
+  };
+  auto read = [&](int t, In& in) {
+    in.row.load(logits + (size_t)t * a.ld, a.E, pair);
+    in.lse = a.lse[t];
+    in.on = a.mask == nullptr || a.mask[t] != 0;
+    in.id = -1;
+    in.w = in.g = 0.0f;
+    if (a.grad_w && lane < a.k) {
+      in.id = a.ids[(size_t)t * a.k + lane];
+      in.w = a.w[(size_t)t * a.k + lane];
+      in.g = a.grad_w[(size_t)t * a.k + lane];
+    }
+  };
+  const int step = gridDim.x * 8;
+  int t = blockIdx.x * 8 + warp;
+  In next;
+  if (t < a.T) read(t, next);
+  for (; t < a.T; t += step) {
+    const In in = next;
+    if (t + step < a.T) read(t + step, next);
+    const bool on = in.on && in.lse != -INFINITY;
     float p[V], s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = on && lane + 32 * i < a.E ? __expf(to_f32(row[lane + 32 * i]) - lse) : 0.0f;
+      p[i] = on ? exp_fast(in.row.get(i) - in.lse) : 0.0f;
       s += f[i] * p[i];
     }
     s = warp_sum(s);
-    int id = -1;
+    const int id = in.id >= 0 && in.id < a.E ? in.id : -1;
     if (a.grad_w) {
-      float w = 0.0f, g = 0.0f;
-      if (lane < a.k) {
-        id = a.ids[(size_t)t * a.k + lane];
-        w = a.w[(size_t)t * a.k + lane];
-        g = a.grad_w[(size_t)t * a.k + lane];
-      }
       // (a weight of zero gets no gradient whatever comes from above, and a
       // zero from above gives none whatever the weight: padding may hold NaN)
-      const float wg = w != 0.0f && g != 0.0f ? w * g : 0.0f;
-      const float dot = warp_sum(wg);
-      if (id < 0 || id >= a.E) id = -1;
-      if (id >= 0) s_sel[warp][id] = w != 0.0f && dot != 0.0f ? wg - w * dot : wg;
+      const float wg = in.w != 0.0f && in.g != 0.0f ? in.w * in.g : 0.0f;
+      const float dot = first_sum(wg, a.k);
+      if (id >= 0) s_sel[warp][id] = in.w != 0.0f && dot != 0.0f ? wg - in.w * dot : wg;
       __syncwarp();
     }
-    const float c = gz * (on ? lse : 0.0f);
+    const float c = gz * (on ? in.lse : 0.0f);
+    T* out = grad + (size_t)t * a.E;
+    float d[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E) grad[(size_t)t * a.E + e] = from_f32<T>(p[i] * (gb * (f[i] - s) + c) + s_sel[warp][e]);
+    for (int i = 0; i < V; ++i) d[i] = p[i] * (gb * (f[i] - s) + c) + s_sel[warp][Row::expert(i)];
+    if (sizeof(T) == 2 && a.E % 2 == 0 && ((uintptr_t)grad) % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        uint32_t w;
+        reinterpret_cast<T*>(&w)[0] = from_f32<T>(d[i]);
+        reinterpret_cast<T*>(&w)[1] = from_f32<T>(d[i + 1]);
+        if (Row::expert(i) < a.E) *reinterpret_cast<uint32_t*>(out + Row::expert(i)) = w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (Row::expert(i) < a.E) out[Row::expert(i)] = from_f32<T>(d[i]);
     }
     if (a.grad_w) {
       __syncwarp();
@@ -366,20 +522,19 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a) {
   }
 }
 
-// Launches the instantiation of kernel K for E experts and element type T.
+// Calls f with the number of logits a lane holds.
 template <typename T, typename F>
 cudaError_t by_width(int E, F f) {
-  switch ((E + 31) / 32) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 3: return f(std::integral_constant<int, 3>());
-    case 4: return f(std::integral_constant<int, 4>());
-    case 5: return f(std::integral_constant<int, 5>());
-    case 6: return f(std::integral_constant<int, 6>());
-    case 7: return f(std::integral_constant<int, 7>());
+  switch ((E + 63) / 64) {
+    case 1: return f(std::integral_constant<int, 2>());
+    case 2: return f(std::integral_constant<int, 4>());
+    case 3: return f(std::integral_constant<int, 6>());
     default: return f(std::integral_constant<int, 8>());
   }
 }
+
+// Whether neighbouring 16-bit logits can be read as one 4-byte word.
+bool router_pairs(const void* p, int64_t ld) { return ((uintptr_t)p) % 4 == 0 && ld % 2 == 0; }
 
 int router_ctas(int T) { return std::min(kRtMaxCtas, (T + kRtWarps - 1) / kRtWarps); }
 
@@ -434,11 +589,12 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)ctas * E);
   a.part_n = reinterpret_cast<int32_t*>(a.part_z + ctas);
   const int threads = 32 * kRtWarps;
+  const bool pair = router_pairs(logits, ld);
   auto go = [&](auto elem) {
     using T_ = decltype(elem);
     return by_width<T_>(E, [&](auto v) {
       constexpr int V = decltype(v)::value;
-      k_router_fwd<V, T_><<<ctas, threads, 0, st>>>(a);
+      k_router_fwd<V, T_><<<ctas, threads, 0, st>>>(a, pair);
       if (ctas > 1) k_router_finish<V><<<1, threads, 0, st>>>(a, ctas);
       return cudaGetLastError();
     });
@@ -463,10 +619,11 @@ tm_status trellis_moe_router_backward(const void* logits, int32_t dtype, int64_t
   RouterBwd a{logits, ld, mask, T, E, k, ids, w, lse, counts, tokens, grad_w, grad_losses, grad_logits};
   cudaStream_t st = (cudaStream_t)stream;
   const int ctas = std::min(152 * 8, (T + 7) / 8);
+  const bool pair = router_pairs(logits, ld);
   auto go = [&](auto elem) {
     using T_ = decltype(elem);
     return by_width<T_>(E, [&](auto v) {
-      k_router_bwd<decltype(v)::value, T_><<<ctas, 256, 0, st>>>(a);
+      k_router_bwd<decltype(v)::value, T_><<<ctas, 256, 0, st>>>(a, pair);
       return cudaGetLastError();
     });
   };
