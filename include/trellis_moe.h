@@ -379,8 +379,8 @@ typedef enum { TM_F32 = 0, TM_BF16 = 1, TM_F16 = 2 } tm_dtype;
  * the token's own ids, w and lse. A token whose logits are all -inf gets ids
  * 0..k-1, w 0 and lse -inf. logits: row t at logits + t * ld elements, ld >= E;
  * 1 <= E <= 256, 1 <= k <= min(E, 32). Nothing is summed by atomics: equal
- * inputs give equal bits. workspace: trellis_moe_router_workspace_size bytes,
- * 16-byte aligned, contents ignored. T = 0 writes the statistics of no tokens. */
+ * inputs give equal bits. workspace: trellis_moe_router_workspace_size bytes
+ * (0 for few tokens: then NULL will do), 16-byte aligned, contents ignored. T = 0 writes the statistics of no tokens. */
 size_t trellis_moe_router_workspace_size(int32_t T, int32_t E);
 tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t ld, const uint8_t* mask, int32_t T,
                                      int32_t E, int32_t k, int32_t* ids, float* w, float* lse, int32_t* counts,

@@ -562,20 +562,16 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
     mp = _mask(mask, T)
     dev, k = logits.device, int(k)
     kk = max(k, 0)
-    o = T * kk
-    # one allocation a type, the workspace after the float32 results; strided
-    # views of them cost less than an allocation each, and much less than split()
+    f32, i32, empty = torch.float32, torch.int32, torch.empty
+    out = RouterOut(empty((T, kk), dtype=i32, device=dev), empty((T, kk), dtype=f32, device=dev),
+                    empty(T, dtype=f32, device=dev), empty(E, dtype=i32, device=dev), empty(E, dtype=f32, device=dev),
+                    empty(2, dtype=f32, device=dev), empty(1, dtype=i32, device=dev))
     wsb = lib.trellis_moe_router_workspace_size(T, E)
-    head = (o + T + E + 5) // 4 * 4
-    f = torch.empty(head + (wsb + 3) // 4, dtype=torch.float32, device=dev)
-    i = torch.empty(o + E + 1, dtype=torch.int32, device=dev)
-    sf, si, row, one = f.as_strided, i.as_strided, (kk, 1), (1,)
-    ids = si((T, kk), row, 0)
-    out = RouterOut(ids, sf((T, kk), row, 0), sf((T,), one, o), si((E,), one, o), sf((E,), one, o + T),
-                    sf((2,), one, o + T + E), si(one, one, o + E))
-    wp, ip = f.data_ptr(), i.data_ptr()
+    ws = empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    ids, w, lse, counts, prob, losses, tokens = out
     _launch(lib.trellis_moe_router_forward, dev, stream, logits.data_ptr(), _dtype_code(logits.dtype), ld, mp, T, E, k,
-            ip, wp, wp + 4 * o, ip + 4 * o, wp + 4 * (o + T), wp + 4 * (o + T + E), ip + 4 * (o + E), wp + 4 * head, wsb)
+            ids.data_ptr(), w.data_ptr(), lse.data_ptr(), counts.data_ptr(), prob.data_ptr(), losses.data_ptr(),
+            tokens.data_ptr(), _opt(ws), wsb)
     return out
 
 

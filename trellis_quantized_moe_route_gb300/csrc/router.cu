@@ -24,8 +24,10 @@
 // warp-wide maximum of the lanes' first keys, and the lane that held it moves up.
 //
 // Probability sums stay in registers over all of a warp's tokens, are added over
-// the CTA's warps in shared memory and over the CTAs by a second kernel, always
-// in the same order; counts are integers. So the same bits every time. The
+// the CTA's warps and the cluster's CTAs in shared memory and over the clusters
+// by a second kernel (with up to 128 tokens there is one cluster and no second
+// kernel), always in the same order; counts are integers. So the same bits every
+// time. The
 // backward pass reads the logits again and rebuilds p from lse, which costs less
 // than storing p (T E fp32).
 #include <algorithm>
@@ -38,7 +40,7 @@ namespace tmoe {
 namespace {
 
 constexpr int kRtWarps = 16;      // warps of a CTA with many tokens
-constexpr int kRtMaxCtas = 304;   // two CTAs of 512 threads on each of 152 SMs
+constexpr int kRtMaxClusters = 152;  // of two CTAs each: two CTAs of 512 threads on each of 152 SMs
 
 // Orderable bits of a logit (larger value, larger bits; -0 as +0), in the upper
 // kBits of a word, and back. kNone: the largest such word for -inf.
@@ -76,6 +78,24 @@ struct Order<__half> : Order16 {
     return __half2float(__ushort_as_half((unsigned short)((k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFF0000u)) >> 16)));
   }
 };
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ int cluster_peer(const int* p, int rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -180,72 +200,21 @@ struct RouterFwd {
   float* prob;
   float* losses;
   int32_t* tokens;
-  // per CTA: [E] probability sums, [E] counts, then sum lse^2 and valid tokens
+  // per cluster: [E] probability sums, [E] counts, then sum lse^2 and valid tokens
   float* part_prob;
   int32_t* part_counts;
   float* part_z;
   int32_t* part_n;
 };
 
-// Adds up `parts` CTAs' statistics and writes the results: a warp adds every
-// (warps)-th part in order, then one thread an expert adds the warps' sums.
-template <int V>
-__device__ void router_finish(const RouterFwd& a, int parts, float (*s_acc)[V * 32], int (*s_cnt)[V * 32]) {
+// Writes the results from sums over all tokens: thread e < E brings its
+// expert's, every thread z and n.
+__device__ __forceinline__ void router_write(const RouterFwd& a, float p, int c, float z, int n) {
   __shared__ float s_dot[32];
-  __shared__ int s_n;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  float acc[V] = {};
-  int cnt[V] = {};
-  for (int c0 = warp; c0 < parts; c0 += warps * 4) {
-    float p[4][V];
-    int n[4][V];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = c0 + u * warps, e = lane + 32 * i;
-        const bool in = c < parts && e < a.E;
-        p[u][i] = in ? a.part_prob[(size_t)c * a.E + e] : 0.0f;
-        n[u][i] = in ? a.part_counts[(size_t)c * a.E + e] : 0;
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        acc[i] += p[u][i];
-        cnt[i] += n[u][i];
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    s_acc[warp][lane + 32 * i] = acc[i];
-    s_cnt[warp][lane + 32 * i] = cnt[i];
-  }
-  if (warp == 0) {
-    int n = 0;
-    float z = 0.0f;
-    for (int c = lane; c < parts; c += 32) {
-      n += a.part_n[c];
-      z += a.part_z[c];
-    }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    z = warp_sum(z);
-    if (lane == 0) {
-      s_n = n;
-      *a.tokens = n;
-      a.losses[1] = n > 0 ? z / (float)n : 0.0f;
-    }
-  }
-  __syncthreads();
-  const float inv_n = s_n > 0 ? 1.0f / (float)s_n : 0.0f;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   float dot = 0.0f;
   if (tid < a.E) {
-    float p = 0.0f;
-    int c = 0;
-    for (int u = 0; u < warps; ++u) {
-      p += s_acc[u][tid];
-      c += s_cnt[u][tid];
-    }
     p *= inv_n;
     a.prob[tid] = p;
     a.counts[tid] = c;
@@ -255,10 +224,65 @@ __device__ void router_finish(const RouterFwd& a, int parts, float (*s_acc)[V * 
   if (lane == 0) s_dot[warp] = dot;
   __syncthreads();
   if (warp == 0) {
-    dot = lane < warps ? s_dot[lane] : 0.0f;
-    dot = warp_sum(dot);
-    if (lane == 0) a.losses[0] = (float)a.E * dot;
+    dot = warp_sum(lane < (int)(blockDim.x >> 5) ? s_dot[lane] : 0.0f);
+    if (lane == 0) {
+      a.losses[0] = (float)a.E * dot;
+      a.losses[1] = z * inv_n;
+      *a.tokens = n;
+    }
   }
+}
+
+// Adds up the clusters' statistics: thread (q, e) every fourth cluster's from
+// the q-th on, then thread e the four sums, both in order.
+__global__ void __launch_bounds__(1024) k_router_finish(RouterFwd a, int parts) {
+  __shared__ float s_p[4][kMaxExperts];
+  __shared__ int s_c[4][kMaxExperts];
+  __shared__ float s_z;
+  __shared__ int s_n;
+  griddep_wait();
+  const int e = threadIdx.x & (kMaxExperts - 1), q = threadIdx.x / kMaxExperts;
+  if (e < a.E) {
+    constexpr int kStep = 19;  // loads in flight
+    float p = 0.0f;
+    int c = 0;
+    for (int u0 = q; u0 < parts; u0 += 4 * kStep) {
+      float pu[kStep];
+      int cu[kStep];
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const int u = u0 + 4 * i;
+        pu[i] = u < parts ? a.part_prob[u * a.E + e] : 0.0f;
+        cu[i] = u < parts ? a.part_counts[u * a.E + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        p += pu[i];
+        c += cu[i];
+      }
+    }
+    s_p[q][e] = p;
+    s_c[q][e] = c;
+  }
+  if (threadIdx.x < 32) {
+    float z = 0.0f;
+    int n = 0;
+    for (int u = threadIdx.x; u < parts; u += 32) {
+      z += a.part_z[u];
+      n += a.part_n[u];
+    }
+    z = warp_sum(z);
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (threadIdx.x == 0) {
+      s_z = z;
+      s_n = n;
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  const bool in = t < a.E;
+  router_write(a, in ? s_p[0][t] + s_p[1][t] + s_p[2][t] + s_p[3][t] : 0.0f,
+               in ? s_c[0][t] + s_c[1][t] + s_c[2][t] + s_c[3][t] : 0, s_z, s_n);
 }
 
 // The k largest of a row: lane j < k returns the j-th expert. `key`: the unique
@@ -324,17 +348,19 @@ __device__ __noinline__ uint32_t router_select_exact(const float* __restrict__ r
   return mine;
 }
 
-// A warp's tokens are warp, warp + W, ... (W: warps of the grid). With one CTA
-// the statistics are finished here.
+// A warp's tokens are warp, warp + W, ... (W: warps of the grid). With one
+// cluster (of csize CTAs) the statistics are finished here.
 template <int V, typename T>
-__global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a, bool pair) {
+__global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, bool pair, int csize) {
   using Row = RowRegs<V, T>;
   __shared__ float s_acc[kRtWarps][V * 32];
-  __shared__ int s_cnt[kRtWarps][V * 32];  // (the finishing sums use it by warp; the first row counts here)
+  __shared__ int s_cnt[V * 32];
   __shared__ float s_z[kRtWarps];
   __shared__ int s_nv[kRtWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  for (int e = threadIdx.x; e < V * 32; e += blockDim.x) s_cnt[0][e] = 0;
+  const int rank = csize > 1 ? (int)cluster_rank() : 0;
+  griddep_launch();
+  for (int e = threadIdx.x; e < V * 32; e += blockDim.x) s_cnt[e] = 0;
   __syncthreads();
   const T* logits = static_cast<const T*>(a.logits);
   float acc[V] = {};
@@ -372,7 +398,7 @@ __global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a, bool 
     if (lane < a.k) {
       a.ids[(size_t)t * a.k + lane] = (int)id;
       a.w[(size_t)t * a.k + lane] = some ? __fdividef(we, wsum) : 0.0f;
-      if (on && some && my_l != -INFINITY) atomicAdd(&s_cnt[0][id], 1);
+      if (on && some && my_l != -INFINITY) atomicAdd(&s_cnt[id], 1);
     }
     if (lane == 0) a.lse[t] = some ? lse : -INFINITY;
     if (on && some) {
@@ -390,33 +416,58 @@ __global__ void __launch_bounds__(kRtWarps * 32) k_router_fwd(RouterFwd a, bool 
     s_nv[warp] = n;
   }
   __syncthreads();
+  // the CTA's sums, in warp order
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float p = 0.0f;
     for (int u = 0; u < warps; ++u) p += s_acc[u][e];
-    a.part_prob[(size_t)blockIdx.x * a.E + e] = p;
-    a.part_counts[(size_t)blockIdx.x * a.E + e] = s_cnt[0][e];
+    s_acc[0][e] = p;
   }
   if (threadIdx.x == 0) {
-    float zs = 0.0f;
-    int ns = 0;
-    for (int u = 0; u < warps; ++u) {
-      zs += s_z[u];
-      ns += s_nv[u];
+    for (int u = 1; u < warps; ++u) {
+      s_z[0] += s_z[u];
+      s_nv[0] += s_nv[u];
     }
-    a.part_z[blockIdx.x] = zs;
-    a.part_n[blockIdx.x] = ns;
   }
-  if (gridDim.x == 1) {
+  // the cluster's, in rank order, by its first CTA
+  float p = 0.0f, zs = 0.0f;
+  int c = 0, ns = 0;
+  const int e = threadIdx.x;
+  if (csize > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      for (int u = 0; u < csize; ++u) {
+        if (e < a.E) {
+          p += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_acc[0][e]), u));
+          c += cluster_peer(&s_cnt[e], u);
+        }
+        zs += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_z[0]), u));
+        ns += cluster_peer(&s_nv[0], u);
+      }
+    }
+    cluster_sync();  // no CTA leaves while its sums are read
+    if (rank != 0) return;
+  } else {
     __syncthreads();
-    router_finish<V>(a, 1, s_acc, s_cnt);
+    if (e < a.E) {
+      p = s_acc[0][e];
+      c = s_cnt[e];
+    }
+    zs = s_z[0];
+    ns = s_nv[0];
   }
-}
-
-template <int V>
-__global__ void __launch_bounds__(kRtWarps * 32) k_router_finish(RouterFwd a, int parts) {
-  __shared__ float s_acc[kRtWarps][V * 32];
-  __shared__ int s_cnt[kRtWarps][V * 32];
-  router_finish<V>(a, parts, s_acc, s_cnt);
+  if ((int)gridDim.x == csize) {
+    router_write(a, p, c, zs, ns);
+  } else {
+    const int part = blockIdx.x / csize;
+    if (e < a.E) {
+      a.part_prob[part * a.E + e] = p;
+      a.part_counts[part * a.E + e] = c;
+    }
+    if (e == 0) {
+      a.part_z[part] = zs;
+      a.part_n[part] = ns;
+    }
+  }
 }
 
 struct RouterBwd {
@@ -536,9 +587,27 @@ cudaError_t by_width(int E, F f) {
 // Whether neighbouring 16-bit logits can be read as one 4-byte word.
 bool router_pairs(const void* p, int64_t ld) { return ((uintptr_t)p) % 4 == 0 && ld % 2 == 0; }
 
-int router_ctas(int T) { return std::min(kRtMaxCtas, (T + kRtWarps - 1) / kRtWarps); }
+// CTAs of a cluster and clusters of a call: up to 128 tokens one cluster, which
+// writes the results itself (one launch), then pairs (clusters of four do not
+// fill the SMs: 64k tokens took 66 us forward and backward, with pairs 54 us).
+struct RouterGrid {
+  int csize, clusters;
+};
 
-size_t router_ws_bytes(int T, int E) { return (size_t)std::max(1, router_ctas(T)) * ((size_t)E * 8 + 8); }
+RouterGrid router_grid(int T) {
+  const int ctas = std::max(1, (T + kRtWarps - 1) / kRtWarps);
+  if (ctas <= 8) {
+    int c = 1;
+    while (c < ctas) c *= 2;
+    return {c, 1};
+  }
+  return {2, std::min(kRtMaxClusters, (ctas + 1) / 2)};
+}
+
+size_t router_ws_bytes(int T, int E) {
+  const int n = router_grid(T).clusters;
+  return n > 1 ? (size_t)n * ((size_t)E * 8 + 8) : 0;
+}
 
 tm_status router_check(const char* what, const void* logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
                        int32_t k) {
@@ -577,29 +646,42 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
     return status_fail(TM_EINVAL, "counts, prob, losses and tokens must be non-NULL");
   if (T > 0 && (!ids || !w || !lse)) return status_fail(TM_EINVAL, "ids, w and lse must be non-NULL");
   const size_t need = router_ws_bytes(T, E);
-  if (!workspace) return status_fail(TM_EWORKSPACE, "workspace is NULL");
-  if (((uintptr_t)workspace) % 16) return status_fail(TM_EWORKSPACE, "workspace must be 16-byte aligned");
-  if (workspace_bytes < need)
-    return status_fail(TM_EWORKSPACE, "workspace has %zu bytes, %zu needed for T=%d E=%d", workspace_bytes, need, T, E);
+  if (need > 0) {
+    if (!workspace) return status_fail(TM_EWORKSPACE, "workspace is NULL");
+    if (((uintptr_t)workspace) % 16) return status_fail(TM_EWORKSPACE, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+      return status_fail(TM_EWORKSPACE, "workspace has %zu bytes, %zu needed for T=%d E=%d", workspace_bytes, need, T, E);
+  }
   cudaStream_t st = (cudaStream_t)stream;
   RouterFwd a{logits, ld, mask, T, E, k, ids, w, lse, counts, prob, losses, tokens, nullptr, nullptr, nullptr, nullptr};
-  const int ctas = std::max(1, router_ctas(T));
+  const int clusters = router_grid(T).clusters, csize = router_grid(T).csize;
   a.part_prob = static_cast<float*>(workspace);
-  a.part_counts = reinterpret_cast<int32_t*>(a.part_prob + (size_t)ctas * E);
-  a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)ctas * E);
-  a.part_n = reinterpret_cast<int32_t*>(a.part_z + ctas);
-  const int threads = 32 * kRtWarps;
+  a.part_counts = reinterpret_cast<int32_t*>(a.part_prob + (size_t)clusters * E);
+  a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)clusters * E);
+  a.part_n = reinterpret_cast<int32_t*>(a.part_z + clusters);
   const bool pair = router_pairs(logits, ld);
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * csize));
+  cfg.blockDim = dim3(32 * kRtWarps);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = csize > 1 ? 1 : 0;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)csize, 1, 1};
   auto go = [&](auto elem) {
     using T_ = decltype(elem);
-    return by_width<T_>(E, [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      k_router_fwd<V, T_><<<ctas, threads, 0, st>>>(a, pair);
-      if (ctas > 1) k_router_finish<V><<<1, threads, 0, st>>>(a, ctas);
-      return cudaGetLastError();
-    });
+    return by_width<T_>(E, [&](auto v) { return cudaLaunchKernelEx(&cfg, k_router_fwd<decltype(v)::value, T_>, a, pair, csize); });
   };
-  const cudaError_t e = TM_BY_DTYPE(dtype, go);
+  cudaError_t e = TM_BY_DTYPE(dtype, go);
+  if (e == cudaSuccess && clusters > 1) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.numAttrs = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    e = cudaLaunchKernelEx(&cfg, k_router_finish, a, clusters);
+  }
   return e == cudaSuccess ? TM_OK : status_cuda(e, "router with losses");
 }
 
