@@ -89,3 +89,48 @@ def test_host_validation_without_gpu(lib):
     lib.trellis_linear_destroy(None)
     lib.trellis_moe_destroy(None)
 
+
+
+def test_tuning_entry_points_validate_without_gpu(lib):
+    from trellis_quantized_moe_route_gb300 import binding
+    P = ctypes.c_void_p
+    err = lib.trellis_moe_last_error
+
+    def router(dtype=0, ld=8, T=4, E=8, k=2, ws=P(16), logits=P(16)):
+        return lib.trellis_moe_router_forward(logits, dtype, ld, None, T, E, k, P(16), P(16), P(16), P(16), P(16), P(16),
+                                              P(16), ws, 1 << 20, None)
+    assert router(dtype=3) == -1 and b"tm_dtype" in err()
+    assert router(ld=7) == -1 and b"ld=7" in err()
+    assert router(E=257, ld=257) == -2
+    assert router(k=9) == -1 and b"k=9" in err()
+    assert router(T=-1) == -1
+    assert router(logits=None) == -1
+    assert router(logits=P(18)) == -1 and b"aligned" in err()
+    assert router(T=1000, ws=None) == -3
+    assert lib.trellis_moe_router_workspace_size(8, 8) == 0
+    assert lib.trellis_moe_router_workspace_size(4096, 8) > 0
+    assert lib.trellis_moe_router_workspace_size(8, 0) == 0
+    assert lib.trellis_moe_router_backward(P(16), 0, 8, None, 4, 8, 2, None, None, P(16), P(16), P(16), P(16), None,
+                                           P(16), None) == -1 and b"grad_w" in err()
+    # combine
+    assert lib.trellis_moe_combine_forward(P(16), 0, P(16), 4, 33, 8, P(16), None) == -1 and b"k=33" in err()
+    assert lib.trellis_moe_combine_forward(P(16), 0, P(16), 4, 2, 0, P(16), None) == -1
+    assert lib.trellis_moe_combine_backward(P(16), 0, P(16), P(16), 4, 2, 8, None, None, None) == -1
+    # MXFP4
+    assert lib.trellis_moe_mxfp4_quantize(P(16), 0, 31, 4, 32, P(16), P(16), None) == -1 and b"ld=31" in err()
+    assert lib.trellis_moe_mxfp4_quantize(P(16), 0, 32, 4, 32, P(8), P(16), None) == -1 and b"codes" in err()
+    assert lib.trellis_moe_mxfp4_quantize(P(16), 0, 32, 0, 32, None, None, None) == 0
+    assert lib.trellis_moe_mxfp4_dequantize(P(16), P(16), 4, 0, P(16), 0, None) == -1
+    h, d = ctypes.c_void_p(), binding.MxFp4Desc(1, 64, 64, 0, 4, 16, 16)
+    assert lib.trellis_moe_mxfp4_prepare(None, ctypes.byref(h), None) == -1
+    for field, bad, status in (("E", 257, -2), ("N", 0, -2), ("K", 0, -2), ("gated", 2, -1), ("max_rows", 0, -1),
+                               ("codes", 8, -1), ("scales", 0, -1)):
+        good = getattr(d, field)
+        setattr(d, field, bad)
+        assert lib.trellis_moe_mxfp4_prepare(ctypes.byref(d), ctypes.byref(h), None) == status, field
+        setattr(d, field, good)
+    assert lib.trellis_moe_mxfp4_forward(None, P(16), 0, 64, 1, P(16), 0, P(256), 1 << 20, None) == -1
+    assert lib.trellis_moe_mxfp4_forward_experts(None, P(16), 0, 64, 0, P(16), 1, 1, P(16), 0, P(256), 1 << 20, None) == -1
+    assert lib.trellis_moe_mxfp4_set_wait_test(None, 0, 0) == -1
+    assert lib.trellis_moe_mxfp4_workspace_size(None, 4) == 0
+    lib.trellis_moe_mxfp4_destroy(None)

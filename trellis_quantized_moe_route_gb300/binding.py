@@ -38,7 +38,7 @@ EXPORTED = [
     "trellis_moe_combine_forward", "trellis_moe_combine_backward",
     "trellis_moe_mxfp4_quantize", "trellis_moe_mxfp4_dequantize", "trellis_moe_mxfp4_prepare",
     "trellis_moe_mxfp4_workspace_size", "trellis_moe_mxfp4_forward", "trellis_moe_mxfp4_forward_experts",
-    "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_destroy",
+    "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_set_wait_test", "trellis_moe_mxfp4_destroy",
 ]
 
 
@@ -123,6 +123,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "trellis_moe_mxfp4_forward": (I32, [P, P, I32, I64, I32, P, I32, P, SZ, P]),
         "trellis_moe_mxfp4_forward_experts": (I32, [P, P, I32, I64, I32, P, I32, I32, P, I32, P, SZ, P]),
         "trellis_moe_mxfp4_poll_error": (I32, [P, P, ctypes.POINTER(ctypes.c_uint32), P]),
+        "trellis_moe_mxfp4_set_wait_test": (I32, [P, ctypes.c_uint64, I32]),
         "trellis_moe_mxfp4_destroy": (None, [P]),
     }
     for name, (res, args) in sig.items():
@@ -717,6 +718,11 @@ class _MxFp4:
         if st not in (TM_OK, -5):
             _check(st)
         return int(flags.value)
+
+    def set_wait_test(self, wait_limit_ns: int = 0, stall_issuer: bool = False):
+        """Limit of the kernels' pipeline waits, and the stalled issuer used to
+        test that they give up (see the C header)."""
+        _check(self.lib.trellis_moe_mxfp4_set_wait_test(self.handle, int(wait_limit_ns), 1 if stall_issuer else 0))
 
     def _output(self, rows, x, out, out_dtype):
         torch = _torch()

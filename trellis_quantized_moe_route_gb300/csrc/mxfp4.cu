@@ -12,6 +12,8 @@ struct tm_mxfp4 {
   tm_mxfp4_desc desc;
   uint8_t* d_scales;  // the weights' scales as the tensor cores read them
   int sms;
+  uint64_t wait_ns;   // trellis_moe_mxfp4_set_wait_test
+  int stall_issuer;
   CUtensorMap wmap;
 };
 
@@ -114,6 +116,8 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
     a.out = c.out;
     a.out_dtype = c.out_dtype;
     a.err = static_cast<uint32_t*>(c.ws);
+    a.wait_ns = h->wait_ns;
+    a.stall_issuer = h->stall_issuer;
     a.wmap = h->wmap;
     const int chunks = c.ids ? c.rows : (c.rows + bn - 1) / bn;
     return launch_mx_dec(a, chunks, st);
@@ -136,6 +140,8 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   a.out = c.out;
   a.err = err;
   a.sms = h->sms;
+  a.wait_ns = h->wait_ns;
+  a.stall_issuer = h->stall_issuer;
   a.wmap = h->wmap;
   a.max_blocks = (c.rows + a.bn - 1) / a.bn;
   if (c.ids) {
@@ -198,6 +204,8 @@ tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, s
   if (!h) return status_fail(TM_EINVAL, "out of host memory");
   h->desc = d;
   h->d_scales = nullptr;
+  h->wait_ns = 0;
+  h->stall_issuer = 0;
   const int halves = d.gated ? 2 : 1;
   cudaError_t e;
   int dev = 0;
@@ -267,6 +275,15 @@ tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* f
   *flags = v;
   if (v != 0)
     return status_fail(TM_EDEVICE, "device error flags 0x%x (bit 0: expert id out of range; bit 1: a pipeline wait gave up)", v);
+  return TM_OK;
+}
+
+tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, int32_t stall_issuer) {
+  set_last_error("");
+  if (!h) return status_fail(TM_EINVAL, "handle is NULL");
+  if (stall_issuer != 0 && stall_issuer != 1) return status_fail(TM_EINVAL, "stall_issuer=%d must be 0 or 1", stall_issuer);
+  h->wait_ns = wait_limit_ns;
+  h->stall_issuer = stall_issuer;
   return TM_OK;
 }
 

@@ -37,6 +37,7 @@ constexpr int kMdMaxRing = 8;
 struct MdBars {
   uint64_t full[kMdMaxRing], empty[kMdMaxRing];
   uint64_t acc;
+  uint64_t never;  // nothing arrives on it (test of the bounded waits)
 };
 
 __device__ __forceinline__ uint32_t md_cluster_rank() {
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       mbar_init(&bars.empty[i], 1);
     }
     mbar_init(&bars.acc, 1);
+    mbar_init(&bars.never, 1);
     s_abort = 0;
     mbar_fence_init();
   }
@@ -208,7 +210,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     const uint32_t base = smem_u32(smem), idesc = mx_idesc(n16);
     const int ksteps = (mx_blocks(a.K) + 1) / 2;
     MxRing r;
-    for (int s = s_lo; s < s_hi; ++s, r.next(ring)) {
+    if (a.stall_issuer) mx_wait_warp(&bars.never, 0, abort, limit);
+    for (int s = s_lo; s < s_hi && !*abort; ++s, r.next(ring)) {
       if (!mx_wait_warp(&bars.full[r.slot], r.phase, abort, limit)) break;
       tc_fence_after();
       mx_issue_stage<GATED, 1>(base + (uint32_t)r.slot * stage_bytes, b_bytes, tsfa, tmem, (uint32_t)a.bn, idesc,

@@ -43,6 +43,7 @@ constexpr int kMxStoreBytes = 16 * 256;  // 16 rows of 128 16-bit channels, for 
 struct MxBars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t never;  // nothing arrives on it (test of the bounded waits)
 };
 
 // One unit: a block of rows times 128 output channels.
@@ -137,6 +138,7 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   constexpr int H = GATED ? 2 : 1;
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem);
+  if (a.stall_issuer && !mx_wait_warp(&B.never, 0, abort, limit)) return;
   MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
     const MxUnit m = next;
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], kMxEpiWarps);
     }
+    mbar_init(&bars.never, 1);
     s_abort = 0;
     mbar_fence_init();
   }
