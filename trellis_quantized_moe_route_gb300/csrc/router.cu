@@ -40,6 +40,7 @@ namespace tmoe {
 namespace {
 
 constexpr int kRtWarps = 16;      // warps of a CTA with many tokens
+constexpr int kRtBwdCtas = 5;         // CTAs of 256 threads that an SM holds of the backward kernel
 constexpr int kRtMaxClusters = 152;  // of two CTAs each: two CTAs of 512 threads on each of 152 SMs
 
 // Orderable bits of a logit (larger value, larger bits; -0 as +0), in the upper
@@ -124,10 +125,11 @@ __device__ __forceinline__ float first_sum(float v, int k) {
 }
 
 // A row of logits over a warp: V of them a lane (V even). 16-bit types take
-// neighbours in pairs, one 4-byte load each where `pair` allows it. Past the
+// neighbours in pairs, one 4-byte load each with PAIR (an even number of experts,
+// rows 4 bytes aligned). Past the
 // last expert stands -inf: with a higher number than any expert, it comes after
 // an expert's own -inf, and its probability is 0.
-template <int V, typename T>
+template <int V, typename T, bool PAIR>
 struct RowRegs {
   uint32_t raw[sizeof(T) == 2 ? V / 2 : V];
 
@@ -136,7 +138,7 @@ struct RowRegs {
     return sizeof(T) == 2 ? 2 * lane + 64 * (i >> 1) + (i & 1) : lane + 32 * i;
   }
   static constexpr uint32_t kInf16 = sizeof(T) == 2 ? Order<T>::kNone >> 16 : 0;  // ~ of -inf's bits
-  __device__ __forceinline__ void load(const T* __restrict__ row, int E, bool pair) {
+  __device__ __forceinline__ void load(const T* __restrict__ row, int E) {
     if (sizeof(T) == 2) {
       const uint32_t none = 0xFFFFu & ~kInf16;
 #pragma unroll
@@ -144,10 +146,11 @@ struct RowRegs {
         const int e = expert(2 * i);
         const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + e;
         raw[i] = none | none << 16;
-        if (pair && e + 1 < E)
-          raw[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
-        else if (e < E)
+        if (PAIR) {
+          if (e < E) raw[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else if (e < E) {
           raw[i] = __ldg(p) | (e + 1 < E ? (uint32_t)__ldg(p + 1) : none) << 16;
+        }
       }
     } else {
 #pragma unroll
@@ -159,6 +162,8 @@ struct RowRegs {
   }
   __device__ __forceinline__ float get(int i) const {
     if (sizeof(T) == 4) return __uint_as_float(raw[i]);
+    if (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(i & 1 ? raw[i >> 1] & 0xFFFF0000u : raw[i >> 1] << 16);
     const uint16_t h = (uint16_t)(raw[i >> 1] >> (16 * (i & 1)));
     return to_f32(*reinterpret_cast<const T*>(&h));
   }
@@ -267,9 +272,11 @@ __global__ void __launch_bounds__(1024) k_router_finish(RouterFwd a, int parts) 
   if (threadIdx.x < 32) {
     float z = 0.0f;
     int n = 0;
-    for (int u = threadIdx.x; u < parts; u += 32) {
-      z += a.part_z[u];
-      n += a.part_n[u];
+#pragma unroll
+    for (int i = 0; i < (kRtMaxClusters + 31) / 32; ++i) {
+      const int u = threadIdx.x + 32 * i;
+      z += u < parts ? a.part_z[u] : 0.0f;
+      n += u < parts ? a.part_n[u] : 0;
     }
     z = warp_sum(z);
     n = __reduce_add_sync(0xFFFFFFFFu, n);
@@ -350,9 +357,9 @@ __device__ __noinline__ uint32_t router_select_exact(const float* __restrict__ r
 
 // A warp's tokens are warp, warp + W, ... (W: warps of the grid). With one
 // cluster (of csize CTAs) the statistics are finished here.
-template <int V, typename T>
-__global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, bool pair, int csize) {
-  using Row = RowRegs<V, T>;
+template <int V, typename T, bool PAIR>
+__global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, int csize) {
+  using Row = RowRegs<V, T, PAIR>;
   __shared__ float s_acc[kRtWarps][V * 32];
   __shared__ int s_cnt[V * 32];
   __shared__ float s_z[kRtWarps];
@@ -369,10 +376,10 @@ __global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, bo
   const int step = gridDim.x * warps;
   int t = blockIdx.x * warps + warp;
   Row row;
-  if (t < a.T) row.load(logits + (size_t)t * a.ld, a.E, pair);
+  if (t < a.T) row.load(logits + (size_t)t * a.ld, a.E);
   for (; t < a.T; t += step) {
     const Row now = row;
-    if (t + step < a.T) row.load(logits + (size_t)(t + step) * a.ld, a.E, pair);
+    if (t + step < a.T) row.load(logits + (size_t)(t + step) * a.ld, a.E);
     const bool on = a.mask == nullptr || a.mask[t] != 0;
     uint32_t key[V], mine, first;
     now.keys(key);
@@ -485,9 +492,9 @@ struct RouterBwd {
   void* grad_logits;         // [T, E]
 };
 
-template <int V, typename T>
-__global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a, bool pair) {
-  using Row = RowRegs<V, T>;
+template <int V, typename T, bool PAIR>
+__global__ void __launch_bounds__(256, kRtBwdCtas) k_router_bwd(RouterBwd a) {
+  using Row = RowRegs<V, T, PAIR>;
   __shared__ float s_sel[8][V * 32];  // each warp's selected experts' gradients, zero between tokens
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* logits = static_cast<const T*>(a.logits);
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a, bool pair) {
     bool on;
   };
   auto read = [&](int t, In& in) {
-    in.row.load(logits + (size_t)t * a.ld, a.E, pair);
+    in.row.load(logits + (size_t)t * a.ld, a.E);
     in.lse = a.lse[t];
     in.on = a.mask == nullptr || a.mask[t] != 0;
     in.id = -1;
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a, bool pair) {
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = p[i] * (gb * (f[i] - s) + c) + s_sel[warp][Row::expert(i)];
-    if (sizeof(T) == 2 && a.E % 2 == 0 && ((uintptr_t)grad) % 4 == 0) {
+    if (PAIR) {
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
         uint32_t w;
@@ -574,7 +581,7 @@ __global__ void __launch_bounds__(256) k_router_bwd(RouterBwd a, bool pair) {
 }
 
 // Calls f with the number of logits a lane holds.
-template <typename T, typename F>
+template <typename F>
 cudaError_t by_width(int E, F f) {
   switch ((E + 63) / 64) {
     case 1: return f(std::integral_constant<int, 2>());
@@ -584,8 +591,14 @@ cudaError_t by_width(int E, F f) {
   }
 }
 
-// Whether neighbouring 16-bit logits can be read as one 4-byte word.
-bool router_pairs(const void* p, int64_t ld) { return ((uintptr_t)p) % 4 == 0 && ld % 2 == 0; }
+// Calls f with the logits' type and whether they can be taken in pairs.
+template <typename F>
+cudaError_t by_pairs(int32_t dtype, int E, const void* p, int64_t ld, const void* q, F f) {
+  const bool pair = E % 2 == 0 && ((uintptr_t)p) % 4 == 0 && ld % 2 == 0 && ((uintptr_t)q) % 4 == 0;
+  if (dtype == TM_F32) return f(float(), std::false_type());
+  if (dtype == TM_BF16) return pair ? f(__nv_bfloat16(), std::true_type()) : f(__nv_bfloat16(), std::false_type());
+  return pair ? f(__half(), std::true_type()) : f(__half(), std::false_type());
+}
 
 // CTAs of a cluster and clusters of a call: up to 128 tokens one cluster, which
 // writes the results itself (one launch), then pairs (clusters of four do not
@@ -659,7 +672,6 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   a.part_counts = reinterpret_cast<int32_t*>(a.part_prob + (size_t)clusters * E);
   a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)clusters * E);
   a.part_n = reinterpret_cast<int32_t*>(a.part_z + clusters);
-  const bool pair = router_pairs(logits, ld);
   cudaLaunchAttribute at[1];
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * csize));
@@ -669,11 +681,11 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   cfg.numAttrs = csize > 1 ? 1 : 0;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {(unsigned)csize, 1, 1};
-  auto go = [&](auto elem) {
-    using T_ = decltype(elem);
-    return by_width<T_>(E, [&](auto v) { return cudaLaunchKernelEx(&cfg, k_router_fwd<decltype(v)::value, T_>, a, pair, csize); });
-  };
-  cudaError_t e = TM_BY_DTYPE(dtype, go);
+  cudaError_t e = by_pairs(dtype, E, logits, ld, nullptr, [&](auto elem, auto pair) {
+    return by_width(E, [&](auto v) {
+      return cudaLaunchKernelEx(&cfg, k_router_fwd<decltype(v)::value, decltype(elem), decltype(pair)::value>, a, csize);
+    });
+  });
   if (e == cudaSuccess && clusters > 1) {
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(1024);
@@ -700,16 +712,13 @@ tm_status trellis_moe_router_backward(const void* logits, int32_t dtype, int64_t
     return status_fail(TM_EINVAL, "grad_logits must be aligned to its elements");
   RouterBwd a{logits, ld, mask, T, E, k, ids, w, lse, counts, tokens, grad_w, grad_losses, grad_logits};
   cudaStream_t st = (cudaStream_t)stream;
-  const int ctas = std::min(152 * 8, (T + 7) / 8);
-  const bool pair = router_pairs(logits, ld);
-  auto go = [&](auto elem) {
-    using T_ = decltype(elem);
-    return by_width<T_>(E, [&](auto v) {
-      k_router_bwd<decltype(v)::value, T_><<<ctas, 256, 0, st>>>(a, pair);
+  const int ctas = std::min(152 * kRtBwdCtas, (T + 7) / 8);
+  const cudaError_t e = by_pairs(dtype, E, logits, ld, grad_logits, [&](auto elem, auto pair) {
+    return by_width(E, [&](auto v) {
+      k_router_bwd<decltype(v)::value, decltype(elem), decltype(pair)::value><<<ctas, 256, 0, st>>>(a);
       return cudaGetLastError();
     });
-  };
-  const cudaError_t e = TM_BY_DTYPE(dtype, go);
+  });
   return e == cudaSuccess ? TM_OK : status_cuda(e, "router backward");
 }
 
