@@ -238,58 +238,54 @@ __device__ __forceinline__ void router_write(const RouterFwd& a, float p, int c,
   }
 }
 
-// Adds up the clusters' statistics: thread (q, e) every fourth cluster's from
-// the q-th on, then thread e the four sums, both in order.
-__global__ void __launch_bounds__(1024) k_router_finish(RouterFwd a, int parts) {
-  __shared__ float s_p[4][kMaxExperts];
-  __shared__ int s_c[4][kMaxExperts];
-  __shared__ float s_z;
-  __shared__ int s_n;
+// Adds up the clusters' statistics, by one cluster of kFinCtas CTAs: CTA q the
+// parts q, q + kFinCtas, ... in order (its loads all in flight), then the first
+// CTA the CTAs' sums in rank order.
+constexpr int kFinCtas = 8;
+
+__global__ void __cluster_dims__(kFinCtas, 1, 1) __launch_bounds__(kMaxExperts) k_router_finish(RouterFwd a, int parts) {
+  constexpr int kEach = (kRtMaxClusters + kFinCtas - 1) / kFinCtas;
+  __shared__ float s_p[kMaxExperts], s_z;
+  __shared__ int s_c[kMaxExperts], s_n;
+  const int e = threadIdx.x, q = (int)cluster_rank();
   griddep_wait();
-  const int e = threadIdx.x & (kMaxExperts - 1), q = threadIdx.x / kMaxExperts;
-  if (e < a.E) {
-    constexpr int kStep = 19;  // loads in flight
-    float p = 0.0f;
-    int c = 0;
-    for (int u0 = q; u0 < parts; u0 += 4 * kStep) {
-      float pu[kStep];
-      int cu[kStep];
+  float p[kEach], z[kEach];
+  int c[kEach], n[kEach];
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const int u = u0 + 4 * i;
-        pu[i] = u < parts ? a.part_prob[u * a.E + e] : 0.0f;
-        cu[i] = u < parts ? a.part_counts[u * a.E + e] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        p += pu[i];
-        c += cu[i];
-      }
-    }
-    s_p[q][e] = p;
-    s_c[q][e] = c;
+  for (int i = 0; i < kEach; ++i) {
+    const int u = q + kFinCtas * i;
+    p[i] = u < parts && e < a.E ? a.part_prob[u * a.E + e] : 0.0f;
+    c[i] = u < parts && e < a.E ? a.part_counts[u * a.E + e] : 0;
+    z[i] = u < parts ? a.part_z[u] : 0.0f;
+    n[i] = u < parts ? a.part_n[u] : 0;
   }
-  if (threadIdx.x < 32) {
-    float z = 0.0f;
-    int n = 0;
 #pragma unroll
-    for (int i = 0; i < (kRtMaxClusters + 31) / 32; ++i) {
-      const int u = threadIdx.x + 32 * i;
-      z += u < parts ? a.part_z[u] : 0.0f;
-      n += u < parts ? a.part_n[u] : 0;
-    }
-    z = warp_sum(z);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (threadIdx.x == 0) {
-      s_z = z;
-      s_n = n;
-    }
+  for (int i = 1; i < kEach; ++i) {
+    p[0] += p[i];
+    c[0] += c[i];
+    z[0] += z[i];
+    n[0] += n[i];
   }
-  __syncthreads();
-  const int t = threadIdx.x;
-  const bool in = t < a.E;
-  router_write(a, in ? s_p[0][t] + s_p[1][t] + s_p[2][t] + s_p[3][t] : 0.0f,
-               in ? s_c[0][t] + s_c[1][t] + s_c[2][t] + s_c[3][t] : 0, s_z, s_n);
+  s_p[e] = p[0];
+  s_c[e] = c[0];
+  if (e == 0) {
+    s_z = z[0];
+    s_n = n[0];
+  }
+  cluster_sync();
+  if (q == 0) {
+    float pp = 0.0f, zz = 0.0f;
+    int cc = 0, nn = 0;
+#pragma unroll
+    for (int u = 0; u < kFinCtas; ++u) {
+      pp += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_p[e]), u));
+      cc += cluster_peer(&s_c[e], u);
+      zz += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_z), u));
+      nn += cluster_peer(&s_n, u);
+    }
+    router_write(a, pp, cc, zz, nn);
+  }
+  cluster_sync();  // no CTA leaves while its sums are read
 }
 
 // The k largest of a row: lane j < k returns the j-th expert. `key`: the unique
@@ -687,8 +683,8 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
     });
   });
   if (e == cudaSuccess && clusters > 1) {
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
+    cfg.gridDim = dim3(kFinCtas);
+    cfg.blockDim = dim3(kMaxExperts);
     cfg.numAttrs = 1;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
