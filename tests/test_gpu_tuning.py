@@ -315,6 +315,29 @@ def test_mxfp4_experts_all_on_one_and_dropped_ids(binding, T):
     check_experts(binding, T, 2, 6, 96, 64, False, True, np.full((T, 2), -1))
 
 
+def test_mxfp4_few_rows_in_several_chunks(binding):
+    """32 routes of one expert, and 20 + 12: more than a chunk of the few-rows kernel holds."""
+    check_experts(binding, 16, 2, 30, 200, 300, True, False, np.full((16, 2), 29))
+    ids = np.full(32, 3)
+    ids[[1, 4, 5, 7, 8, 11, 15, 18, 20, 21, 25, 30]] = 17
+    check_experts(binding, 32, 1, 30, 72, 1100, False, True, ids.reshape(32, 1), od="f16")
+
+
+@pytest.mark.parametrize("T,gated", [(3, False), (4, True), (40, False), (40, True)])
+def test_mxfp4_long_rows(binding, T, gated):
+    """More stages than any ring holds, and a last stage that is part full."""
+    N, K = 70, 20010
+    codes, scales, W = weights(1, 2 * N if gated else N, K, 5)
+    x = torch.from_numpy(gen(T).standard_normal((T, K)).astype(np.float32))
+    xq = mxfp4.dequantize(*mxfp4.quantize(host(x)), K)
+    y, mag = mxfp4.product(xq, W[0], gated)
+    lin = binding.MxFp4Linear(torch.from_numpy(codes[0]).cuda(), torch.from_numpy(scales[0]).cuda(), K, max_tokens=T, gated=gated)
+    got = lin.forward(x.cuda())
+    assert lin.poll_error() == 0
+    assert (np.abs(host(got) - y) <= bound(y, mag, K, gated, "f32")).all()
+    lin.close()
+
+
 @pytest.mark.parametrize("T", [2, 300])
 def test_mxfp4_product_of_a_bad_row_is_nan_there_only(binding, T):
     codes, scales, W = weights(1, 160, 128, 1)

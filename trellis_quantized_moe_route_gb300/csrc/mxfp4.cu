@@ -84,26 +84,34 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
   return L;
 }
 
-// Rows of a chunk of the few-rows kernel, or 0 where the block kernel runs.
-constexpr int kMxDecRoutes = 256;
-int mx_dec_rows(const tm_mxfp4_desc& d, const MxCall& c) {
-  if (c.rows > (c.ids ? kMxDecRoutes : kMxDecRows)) return 0;
-  const int each = c.ids ? std::min(c.rows, std::max(4, 2 * c.rows / d.E)) : c.rows;
-  int bn = 16;
-  while (bn < each && bn < kMxDecRows) bn *= 2;
-  return bn;
+// Whether a call runs in the few-rows kernel (one launch, weights read once for
+// each chunk of 16 rows, rows quantised in every CTA) rather than in the block
+// kernel (quantisation and, by expert, a route map before it). us a call, few
+// rows / blocks, bf16:
+//   dense 4096 x 4096   T = 1: 6.8 / 9.4   4: 7.6 / 9.3   8: 9.4 / 9.3   16: 12.4 / 9.3
+//   dense 1024 x 1024   T = 1: 4.2 / 5.8   4: 4.2 / 5.8   8: 5.3 / 6.2   16: 6.8 / 5.8
+//   dense 5120 x 1536   T = 1: 5.7 / 6.3   4: 6.3 / 6.5   8: 8.2 / 6.3
+//   128 experts, gated 1024 -> 512    64 routes: 7.7 / 12.5   128: 10.9 / 14.4   192: 13.9 / 14.4   256: 17.0 / 14.5
+//   128 experts, 512 -> 1024          64 routes: 7.3 / 10.8   128: 11.2 / 12.4   192: 17.0 / 13.4
+//   8 experts, gated 1024 -> 1024     16 routes: 7.3 / 8.8    32: 10.3 / 8.8
+//   160 experts, 1536 -> 5120         16 routes: 13.9 / 18.0  32: 26.1 / 26.0    64: 47.8 / 40.7
+// Hence few rows an expert on average, and no more CTAs than a few waves.
+bool mx_few_rows(const tm_mxfp4* h, const MxCall& c) {
+  const tm_mxfp4_desc& d = h->desc;
+  if (!c.ids) return c.rows <= 4;
+  const long tiles = (d.N + 127) / 128;
+  return c.rows <= d.E + 8 && c.rows * tiles <= 8L * h->sms;
 }
 
 cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   const tm_mxfp4_desc& d = h->desc;
-  if (const int bn = mx_dec_rows(d, c)) {
+  if (mx_few_rows(h, c)) {
     MxDecArgs a{};
     a.E = d.E;
     a.N = d.N;
     a.K = d.K;
     a.gated = d.gated;
     a.rows = c.rows;
-    a.bn = bn;
     a.sms = h->sms;
     a.x = c.x;
     a.x_dtype = c.x_dtype;
@@ -119,7 +127,7 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
     a.wait_ns = h->wait_ns;
     a.stall_issuer = h->stall_issuer;
     a.wmap = h->wmap;
-    const int chunks = c.ids ? c.rows : (c.rows + bn - 1) / bn;
+    const int chunks = c.ids ? c.rows : 1;
     return launch_mx_dec(a, chunks, st);
   }
   const MxLayout L = mx_layout(d, c.rows);

@@ -57,11 +57,10 @@ cudaError_t launch_mx_map(const MxMapArgs& a, cudaStream_t st);
 
 // The product for few rows in one launch (mxfp4_dec.cu): x is quantised inside
 // and routes are found from the ids.
-constexpr int kMxDecRows = 128;  // most rows of a chunk
+constexpr int kMxDecRows = 16;  // most rows of a chunk
 struct MxDecArgs {
   int E, N, K, gated;
   int rows;             // rows of y
-  int bn;               // rows of a chunk: 16, 32, 64 or 128
   int sms;
   const void* x;
   int x_dtype;

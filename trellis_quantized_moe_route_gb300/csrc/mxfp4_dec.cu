@@ -2,18 +2,18 @@
 // touched weights once, split along K over the CTAs of a cluster.
 //
 // A unit is 128 output channels (gated: the 128 gate and the 128 up rows) and a
-// chunk of up to `bn` rows of one expert; each CTA of the unit's cluster takes
+// chunk of up to 16 rows of one expert; each CTA of the unit's cluster takes
 // a contiguous part of the 256-column stages. The W tile and its scales come by
 // TMA; the rows of x are quantised by four warps straight into the swizzled
 // operand and scale layout in shared memory, so there is no pass over x before.
 // Nor is there a row map: the chunk with index r starts at route r, and exists
-// if the number of earlier routes of the same expert is a multiple of bn; its
+// if the number of earlier routes of the same expert is a multiple of 16; its
 // rows are that route and the next ones of the expert. Each warp finds that by
 // itself with a ballot for every 32 ids, and the CTAs without a chunk leave.
 // The MMA is the block-scaled one of mxfp4_mma.cuh with the rows of x as
-// N = 16, 32, ... columns; tensor cores have time to spare here, what bounds
-// the call is the weights' bytes and the latency of one load, MMA and drain
-// chain, which the split shortens and spreads over the SMs.
+// N = 16 columns; tensor cores have time to spare here, what bounds the call is
+// the weights' bytes and the latency of one load, MMA and drain chain, which
+// the split shortens and spreads over the SMs.
 //
 // The partial sums of a unit are sent to the CTA of the cluster that owns their
 // row, which adds them in rank order: the same bits every time. A CTA frees its
@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kMdThreads = 192;  // four warps quantise and drain, one loads, one issues
 constexpr int kMdMaxRing = 8;
+constexpr int kMdXBytes = kMxDecRows * 128;  // the x tile of a stage
 
 struct MdBars {
   uint64_t full[kMdMaxRing], empty[kMdMaxRing];
@@ -104,12 +105,12 @@ __device__ __forceinline__ MdChunk md_find(const MxDecArgs& a, int r0, int* list
       const bool is = r < a.rows && id[u] == m.expert;
       const uint32_t lo = __ballot_sync(0xFFFFFFFFu, is && r < r0), hi = __ballot_sync(0xFFFFFFFFu, is && r >= r0);
       const int at = from + __popc(hi & ((1u << lane) - 1u));
-      if (list && is && r >= r0 && at < a.bn) list[at] = r;
+      if (list && is && r >= r0 && at < kMxDecRows) list[at] = r;
       before += __popc(lo);
       from += __popc(hi);
     }
   }
-  m.rows = before % a.bn == 0 ? min(a.bn, from) : 0;
+  m.rows = before % kMxDecRows == 0 ? min(kMxDecRows, from) : 0;
   return m;
 }
 
@@ -132,9 +133,9 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   const int chunk = unit / tiles, tile = unit - chunk * tiles;
   const int stages = mx_stages(a.K);
   const int s_lo = rank * per, s_hi = min(stages, s_lo + per);
-  const uint32_t b_bytes = (uint32_t)a.bn * 128;
-  const uint32_t stage_bytes = (H * (kMxTileBytes + 1024) + b_bytes + 1024 + 1023) / 1024 * 1024;
-  float* part = reinterpret_cast<float*>(smem + (size_t)ring * stage_bytes);  // [split][H][bn / split][128]
+  constexpr uint32_t kStage = H * (kMxTileBytes + 1024) + kMdXBytes + 1024;
+  static_assert(kStage % 1024 == 0, "operands at multiples of the swizzle atom");
+  float* part = reinterpret_cast<float*>(smem + (size_t)ring * kStage);  // [split][H][16 / split][128]
 
   if (split > 1) md_cluster_arrive();  // (waited for before the first store to a peer)
   if (tid == 128) {
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   }
   mx_grid_wait();
   mx_grid_launch();
-  MdChunk m{0, min(a.bn, a.rows - chunk * a.bn), false};
+  MdChunk m{0, min(kMxDecRows, a.rows - chunk * kMxDecRows), false};
   if (a.ids) {
     m = md_find(a, chunk, warp == 0 ? s_row : nullptr);
     // (every CTA sees all ids; the first one writes the error word, long
@@ -174,10 +175,9 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const uint32_t tsfa = tmem + (uint32_t)(H * a.bn);
+  const uint32_t tsfa = tmem + (uint32_t)(H * kMxDecRows);
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
-  const int n16 = (m.rows + 15) / 16 * 16;
 
   if (warp == 4) {
     if (lane == 0) {
@@ -187,12 +187,12 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       int it = 0;
       for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
         if (it >= ring && !mbar_wait_abort(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
-        unsigned char* st = smem + (size_t)r.slot * stage_bytes;
+        unsigned char* st = smem + (size_t)r.slot * kStage;
         uint64_t* bar = &bars.full[r.slot];
         mbar_arrive_expect_tx(bar, H * (kMxTileBytes + 1024));
         mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
         if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
-        unsigned char* sf = st + H * kMxTileBytes + b_bytes;
+        unsigned char* sf = st + H * kMxTileBytes + kMdXBytes;
         bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
         if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)tiles * stages + s) * 1024, 1024, bar);
       }
@@ -207,14 +207,14 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     }
   } else if (warp == 5) {
     const bool lead = mx_elect();
-    const uint32_t base = smem_u32(smem), idesc = mx_idesc(n16);
+    const uint32_t base = smem_u32(smem), idesc = mx_idesc(kMxDecRows);
     const int ksteps = (mx_blocks(a.K) + 1) / 2;
     MxRing r;
     if (a.stall_issuer) mx_wait_warp(&bars.never, 0, abort, limit);
     for (int s = s_lo; s < s_hi && !*abort; ++s, r.next(ring)) {
       if (!mx_wait_warp(&bars.full[r.slot], r.phase, abort, limit)) break;
       tc_fence_after();
-      mx_issue_stage<GATED, 1>(base + (uint32_t)r.slot * stage_bytes, b_bytes, tsfa, tmem, (uint32_t)a.bn, idesc,
+      mx_issue_stage<GATED, 1>(base + (uint32_t)r.slot * kStage, kMdXBytes, tsfa, tmem, (uint32_t)kMxDecRows, idesc,
                                min(4, ksteps - s * 4), s == s_lo, lead);
       if (lead) tc_commit(&bars.empty[r.slot]);
     }
@@ -228,12 +228,12 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     int it = 0, item = 0;
     for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
       if (it >= ring && !mx_wait_warp(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
-      unsigned char* st = smem + (size_t)r.slot * stage_bytes;
+      unsigned char* st = smem + (size_t)r.slot * kStage;
       unsigned char* bt = st + H * kMxTileBytes;
-      unsigned char* sf = bt + b_bytes + H * 1024;
+      unsigned char* sf = bt + kMdXBytes + H * 1024;
       for (int i = 0; i < m.rows; ++i, ++item) {
         if ((item & 3) != warp) continue;
-        const int row = a.ids ? s_row[i] : chunk * a.bn + i;
+        const int row = a.ids ? s_row[i] : chunk * kMxDecRows + i;
         const int xr = row / a.topk, col = s * 256 + lane * 8;
         uint32_t byte;
         const uint32_t q = md_quantize(a, (size_t)xr * a.ld + col, max(0, min(8, a.K - col)), byte);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
         word |= __shfl_sync(0xFFFFFFFFu, byte, g + 12) << 24;
         *reinterpret_cast<uint32_t*>(bt + sw128_off(i, lane >> 2) + (lane & 3) * 4) = q;
         if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(sf + (lane >> 4) * 512 + (i & 31) * 16 + (i >> 5) * 4) = word;
+          *reinterpret_cast<uint32_t*>(sf + (lane >> 4) * 512 + i * 16) = word;
       }
       fence_proxy_async();
       __syncwarp();
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     }
   }
   if (split > 1) md_cluster_wait();  // every CTA of the cluster has started
-  const int own = a.bn >> lsplit;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
+  const int own = kMxDecRows >> lsplit;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
   if (warp < 4 && s_hi > s_lo) {
     const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
     tc_fence_after();
@@ -260,20 +260,19 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
       const uint32_t to = smem_u32(part) + (uint32_t)(rank * H * own * 128 + warp * 32 + lane) * 4;
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-        for (int c0 = 0; c0 < n16; c0 += 16) {
-          float v[16];
-          tmem_ld16(lb + (uint32_t)(h * a.bn + c0), v);
+      for (int h = 0; h < H; ++h) {
+        float v[16];
+        tmem_ld16(lb + (uint32_t)(h * kMxDecRows), v);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= m.rows) break;
-            const uint32_t at = to + (uint32_t)(h * own + ((c0 + c) >> lsplit)) * 512;
-            if (split > 1)
-              md_peer_store(md_peer(at, (uint32_t)((c0 + c) & (split - 1))), v[c]);
-            else
-              part[(size_t)(h * own + c0 + c) * 128 + warp * 32 + lane] = v[c];
-          }
+        for (int c = 0; c < kMxDecRows; ++c) {
+          if (c >= m.rows) break;
+          const uint32_t at = to + (uint32_t)(h * own + (c >> lsplit)) * 512;
+          if (split > 1)
+            md_peer_store(md_peer(at, (uint32_t)(c & (split - 1))), v[c]);
+          else
+            part[(size_t)(h * own + c) * 128 + warp * 32 + lane] = v[c];
         }
+      }
     }
   }
   tc_fence_before();
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     }
     const float v = GATED ? mx_silu(y[0]) * y[H - 1] : y[0];
     const int ch = tile * 128 + n;
-    if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : chunk * a.bn + c) * a.N + ch, v);
+    if (ch < a.N) md_store(a, (size_t)(a.ids ? s_row[c] : chunk * kMxDecRows + c) * a.N + ch, v);
   }
 }
 
@@ -305,7 +304,7 @@ template <bool GATED>
 cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   constexpr int H = GATED ? 2 : 1;
   auto kern = k_mx_dec<GATED>;
-  constexpr int kSmem = 220 * 1024;
+  constexpr int kSmem = 104 * 1024;
   static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (attr != cudaSuccess) return attr;
   const int stages = mx_stages(a.K), tiles = (a.N + 127) / 128;
@@ -315,15 +314,13 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   while (lsplit < 3 && (2 << lsplit) <= stages && (units << lsplit) <= a.sms) ++lsplit;
   const int split = 1 << lsplit;
   const int per = (stages + split - 1) / split;
-  const int stage = (H * (kMxTileBytes + 1024) + a.bn * 128 + 1024 + 1023) / 1024 * 1024;
-  const int part = H * a.bn * 128 * 4;
+  const int stage = H * (kMxTileBytes + 1024) + kMdXBytes + 1024;
+  const int part = H * kMxDecRows * 128 * 4;
+  // a ring that leaves room for two CTAs on an SM
   const int ring = std::max(1, std::min(std::min(kMdMaxRing, per), (100 * 1024 - part) / stage));
   uint32_t cols = 32;
-  while (cols < (uint32_t)(H * a.bn + 8 * H + 8)) cols *= 2;
-  // no more CTAs on an SM than its tensor memory has columns for
-  int smem = 1024 + ring * stage + part;
-  smem = std::max(smem, (int)(227 * 1024 / (512 / cols + 1)));
-  if (smem > kSmem) return cudaErrorInvalidConfiguration;
+  while (cols < (uint32_t)(H * kMxDecRows + 8 * H + 8)) cols *= 2;
+  const int smem = 1024 + ring * stage + part;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * split));
   cfg.blockDim = dim3(kMdThreads);
