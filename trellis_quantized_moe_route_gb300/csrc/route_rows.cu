@@ -52,10 +52,10 @@ constexpr int kCbChunk = 8;  // routes whose dot products a block holds at once
 // One block per token; a thread takes eight columns at a time, the chunk's
 // loads all in flight.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_combine_routes_bwd(const T* __restrict__ rows, const float* __restrict__ w,
+__global__ void __launch_bounds__(512) k_combine_routes_bwd(const T* __restrict__ rows, const float* __restrict__ w,
                                                             const float* __restrict__ gout, int k, int H,
                                                             T* __restrict__ grows, float* __restrict__ gw) {
-  __shared__ float s_dot[8][kCbChunk];
+  __shared__ float s_dot[16][kCbChunk];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const size_t t = blockIdx.x;
   for (int j0 = 0; j0 < k; j0 += kCbChunk) {
@@ -165,8 +165,9 @@ tm_status trellis_moe_combine_backward(const void* rows, int32_t dtype, const fl
     return status_fail(TM_EINVAL, "grad_rows must be aligned to its elements");
   const int es = dtype_bytes(dtype);
   const bool vec = eights(rows, H, H, es) && eights(grad_out, H, H, 4) && eights(grad_rows, H, H, es);
-  // (as many threads as have a column group, whole warps)
-  const int threads = std::min(256, (H + 255) / 256 * 32);
+  // whole warps, as few passes over the columns as 512 threads need, evenly filled
+  const int groups = (H + 7) / 8, passes = (groups + 511) / 512;
+  const int threads = ((groups + passes - 1) / passes + 31) / 32 * 32;
   auto go = [&](auto elem, auto v) {
     using E = decltype(elem);
     k_combine_routes_bwd<E, decltype(v)::value><<<T, threads, 0, (cudaStream_t)stream>>>(
