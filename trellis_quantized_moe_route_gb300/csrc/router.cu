@@ -18,7 +18,7 @@
 // bytes. Each logit becomes a 32-bit key that is unique in the row and orders
 // like (logit, then lower expert): 16-bit logits have their expert in the low
 // half; fp32 logits give up their lowest 8 bits for it, and a token in which two
-// of the k + 1 largest agree in the other 24 (one in some hundred, or equal
+// of the k + 1 largest agree in the other 24 (one in a few hundred, or equal
 // logits) is selected again on the whole values. A lane sorts its keys once
 // (min / max only, nothing carried along); each of the k rounds is then one
 // warp-wide maximum of the lanes' first keys, and the lane that held it moves up.
@@ -27,9 +27,13 @@
 // the CTA's warps and the cluster's CTAs in shared memory and over the clusters
 // by a second kernel (with up to 128 tokens there is one cluster and no second
 // kernel), always in the same order; counts are integers. So the same bits every
-// time. The
-// backward pass reads the logits again and rebuilds p from lse, which costs less
-// than storing p (T E fp32).
+// time. The backward pass reads the logits again and rebuilds p from lse, which
+// costs less than storing p (T E fp32).
+//
+// 65536 tokens x 160 bf16 logits, k = 8, masked: forward 27 us (360 instructions
+// a token, 65% of the issue slots, the integer pipe 62% busy; its bytes take
+// 4 us), finishing sums 5 us, backward 17 us (220 instructions a token; its
+// bytes take 7 us). 8 tokens x 128: one launch, 4 us.
 #include <algorithm>
 
 #include "elem.cuh"
