@@ -186,30 +186,31 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
 
   if (warp == 4) {
-    if (lane == 0) {
-      const int wrow = m.expert * H * a.N + tile * 128;
-      const size_t wsf = ((size_t)m.expert * H * tiles + tile) * stages * 1024;
-      MxRing r;
-      int it = 0;
-      for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
-        if (it >= ring && !mbar_wait_abort(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
-        unsigned char* st = smem + (size_t)r.slot * kStage;
-        uint64_t* bar = &bars.full[r.slot];
-        mbar_arrive_expect_tx(bar, H * (kMxTileBytes + 1024));
+    const bool lead = mx_elect();
+    const uint32_t base = smem_u32(smem), bar0 = smem_u32(&bars.full[0]);
+    const int wrow = m.expert * H * a.N + tile * 128;
+    const uint8_t* wsf = a.wscale + ((size_t)m.expert * H * tiles + tile) * stages * 1024;
+    const uint8_t* usf = wsf + (size_t)tiles * stages * 1024;
+    MxRing r;
+    int it = 0;
+    for (int s = s_lo; s < s_hi; ++s, ++it, r.next(ring)) {
+      if (it >= ring && !mx_wait_warp(&bars.empty[r.slot], r.phase ^ 1, abort, limit)) break;
+      const uint32_t st = base + (uint32_t)r.slot * kStage, sf = st + H * kMxTileBytes + kMdXBytes;
+      const uint32_t bar = bar0 + (uint32_t)r.slot * 8;
+      if (lead) {
+        mx_expect(bar, H * (kMxTileBytes + 1024));
         mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
         if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
-        unsigned char* sf = st + H * kMxTileBytes + kMdXBytes;
-        bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
-        if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)tiles * stages + s) * 1024, 1024, bar);
+        mx_bulk(sf, wsf + s * 1024, 1024, bar);
+        if (GATED) mx_bulk(sf + 1024, usf + s * 1024, 1024, bar);
       }
-      // (after an abort, full[] also counts the quantisers' arrivals; they
-      // arrive for every stage they reach, and a copy in flight lands within
-      // the limit)
-      if (*abort) {
-        int never = 0;
-        for (int i = max(0, it - ring); i < it; ++i)
-          mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs / kMdMaxRing);
-      }
+    }
+    // (after an abort, full[] also counts the quantisers' arrivals; they arrive
+    // for every stage they reach, and a copy in flight lands within the limit)
+    if (*abort) {
+      int never = 0;
+      for (int i = max(0, it - ring); i < it; ++i)
+        mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs / kMdMaxRing);
     }
   } else if (warp == 5) {
     const bool lead = mx_elect();

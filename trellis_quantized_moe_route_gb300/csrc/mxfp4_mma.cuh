@@ -35,9 +35,19 @@ __device__ __forceinline__ void mx_prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
 }
 
-__device__ __forceinline__ void mx_tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
+// The copies of a stage take shared addresses, which a converged warp keeps in
+// uniform registers (from one thread's own branch, issuing a stage's copies took
+// 280-400 cycles).
+__device__ __forceinline__ void mx_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mx_tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
-               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar)) : "memory");
+               ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mx_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 // 512 bytes of scales (32 rows of 16 bytes, rows 16 bytes apart) to four

@@ -9,9 +9,9 @@
 // rows of the same 128 channels against one x operand, and the same thread
 // holds both.
 //
-// Persistent, one CTA per SM: a loader thread (TMA boxes of 256 columns = one
+// Persistent, one CTA per SM: a loader warp (TMA boxes of 256 columns = one
 // 128-byte swizzle span of codes, bulk copies of the scale chunks), an issuer
-// thread (scales to tensor memory with tcgen05.cp, then one MMA per 64
+// warp (scales to tensor memory with tcgen05.cp, then one MMA per 64
 // columns), and sixteen epilogue warps that drain one accumulator buffer while
 // the next unit fills the other. 240 columns twice, plus 24 columns of scales,
 // is what 512 columns of tensor memory hold; that is why a block ends at 240
@@ -112,6 +112,9 @@ __device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring, FastDiv t
 template <bool GATED, bool EXPERTS>
 __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
                           uint64_t limit) {
+  const bool lead = mx_elect();
+  const uint32_t base = smem_u32(smem), bar0 = smem_u32(&B.full[0]);
+  const uint32_t bytes = g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes;
   MxRing r;
   int it = 0;
   bool ok = true;
@@ -120,23 +123,25 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
     const MxUnit m = next;
     next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
     const int wrow = m.expert * (GATED ? 2 * a.N : a.N) + m.tile * 128;
-    const size_t wsf = ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles.d + m.tile) * g.stages * 1024;
-    const size_t xsf = (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
+    const uint8_t* wsf = a.wscale + ((size_t)m.expert * (GATED ? 2 : 1) * g.tiles.d + m.tile) * g.stages * 1024;
+    const uint8_t* usf = wsf + (size_t)g.tiles.d * g.stages * 1024;
+    const uint8_t* xsf = a.xscale + (size_t)(m.slot0 / a.bn) * g.stages * g.sfb_bytes;
     for (int s = 0; s < g.stages; ++s, ++it, r.next(g.ring)) {
-      if (it >= g.ring && !mbar_wait_abort(&B.empty[r.slot], r.phase ^ 1, abort, limit)) {
+      if (it >= g.ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, limit)) {
         ok = false;
         break;
       }
-      unsigned char* st = smem + (size_t)r.slot * g.stage_bytes;
-      uint64_t* bar = &B.full[r.slot];
-      mbar_arrive_expect_tx(bar, g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes);
-      mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
-      if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
-      mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
-      unsigned char* sf = st + g.a_bytes + g.b_bytes;
-      bulk_g2s(sf, a.wscale + wsf + (size_t)s * 1024, 1024, bar);
-      if (GATED) bulk_g2s(sf + 1024, a.wscale + wsf + ((size_t)g.tiles.d * g.stages + s) * 1024, 1024, bar);
-      bulk_g2s(sf + g.sfa_bytes, a.xscale + xsf + (size_t)s * g.sfb_bytes, g.sfb_bytes, bar);
+      const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes, sf = st + g.a_bytes + g.b_bytes;
+      const uint32_t bar = bar0 + (uint32_t)r.slot * 8;
+      if (lead) {
+        mx_expect(bar, bytes);
+        mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
+        if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
+        mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
+        mx_bulk(sf, wsf + s * 1024, 1024, bar);
+        if (GATED) mx_bulk(sf + 1024, usf + s * 1024, 1024, bar);
+        mx_bulk(sf + g.sfa_bytes, xsf + (uint32_t)s * g.sfb_bytes, g.sfb_bytes, bar);
+      }
     }
   }
   if (*abort) {  // let the copies in flight land before the CTA goes
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
     // (every route was dropped)
   } else if (warp < kMxEpiWarps) {
     mx_epilogue<GATED, EXPERTS, T>(a, g, bars, tmem, smem + (size_t)ring * g.stage_bytes, abort, limit);
-  } else if (threadIdx.x == kMxEpiWarps * 32) {
+  } else if (warp == kMxEpiWarps) {
     mx_loader<GATED, EXPERTS>(a, g, bars, smem, abort, limit);
   } else if (warp == kMxEpiWarps + 1) {
     if (a.nrb == 1)
