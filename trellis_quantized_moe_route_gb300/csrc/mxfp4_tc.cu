@@ -115,10 +115,32 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(&B.full[0]);
   const uint32_t bytes = g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes;
+  // W's part of a stage: the copies of the codes and scales
+  auto load_w = [&](int s, uint32_t st, uint32_t bar, int wrow, const uint8_t* wsf, const uint8_t* usf) {
+    const uint32_t sf = st + g.a_bytes + g.b_bytes;
+    if (lead) {
+      mx_expect(bar, bytes);
+      mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
+      if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
+      mx_bulk(sf, wsf + s * 1024, 1024, bar);
+      if (GATED) mx_bulk(sf + 1024, usf + s * 1024, 1024, bar);
+    }
+  };
   MxRing r;
-  int it = 0;
+  int it = 0, ahead = 0;
   bool ok = true;
   MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
+  if (!EXPERTS) {
+    // Dense: the kernel before this one quantises x, and lets this one start
+    // only after it has itself waited for what came before; so W may be read
+    // while x is being quantised.
+    if ((int)blockIdx.x < g.units) ahead = min(g.ring, g.stages);
+    const uint8_t* wsf = a.wscale + (size_t)next.tile * g.stages * 1024;
+    for (int s = 0; s < ahead; ++s)
+      load_w(s, base + (uint32_t)s * g.stage_bytes, bar0 + s * 8, next.tile * 128, wsf,
+             wsf + (size_t)g.tiles.d * g.stages * 1024);
+    mx_grid_wait();
+  }
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
     const MxUnit m = next;
     next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
@@ -131,16 +153,11 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
         ok = false;
         break;
       }
-      const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes, sf = st + g.a_bytes + g.b_bytes;
-      const uint32_t bar = bar0 + (uint32_t)r.slot * 8;
+      const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
+      if (EXPERTS || it >= ahead) load_w(s, st, bar, wrow, wsf, usf);
       if (lead) {
-        mx_expect(bar, bytes);
-        mx_tma_2d(st, &a.wmap, s * 128, wrow, bar);
-        if (GATED) mx_tma_2d(st + kMxTileBytes, &a.wmap, s * 128, wrow + a.N, bar);
         mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
-        mx_bulk(sf, wsf + s * 1024, 1024, bar);
-        if (GATED) mx_bulk(sf + 1024, usf + s * 1024, 1024, bar);
-        mx_bulk(sf + g.sfa_bytes, xsf + (uint32_t)s * g.sfb_bytes, g.sfb_bytes, bar);
+        mx_bulk(st + g.a_bytes + g.b_bytes + g.sfa_bytes, xsf + (uint32_t)s * g.sfb_bytes, g.sfb_bytes, bar);
       }
     }
   }
@@ -328,7 +345,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  mx_grid_wait();
+  if (EXPERTS || warp != kMxEpiWarps) mx_grid_wait();  // (the dense loader waits by itself)
   mx_grid_launch();
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &s_abort;
