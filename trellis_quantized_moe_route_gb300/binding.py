@@ -478,18 +478,32 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _launch(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current; raises on an error status. The
-    marshalling of the small calls costs more than their kernels, so the guard
-    is entered only when another device is current."""
-    torch = _torch()
-    index = device.index
-    if index == torch.cuda.current_device():
-        raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-        status = fn(*args, raw)
+# torch.float32 and others, and the current device's and stream's numbers without
+# their objects: the marshalling of a small call costs more than its kernel, so
+# the calls below look nothing up twice and check their usual arguments in one
+# expression, going through the checks that name a fault only when one is there.
+_f32 = _i32 = _u8 = _device_now = _stream_of = _empty = None
+
+
+def _start():
+    """Loads the library and fills in the names above (every call begins with it)."""
+    global _f32, _i32, _u8, _device_now, _stream_of, _empty
+    if _f32 is None:
+        torch = _torch()
+        _dtype_code(torch.float32)
+        torch.cuda.init()
+        _f32, _i32, _u8, _empty = torch.float32, torch.int32, torch.uint8, torch.empty
+        _device_now, _stream_of = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return load_library()
+
+
+def _launch(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current; raises on an error status."""
+    if index == _device_now():
+        status = fn(*args, _stream_of(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(stream))
+        with _torch().cuda.device(index):
+            status = fn(*args, _stream_of(index) if stream is None else stream.cuda_stream)
     if status != TM_OK:
         _check(status)
 
@@ -512,11 +526,12 @@ def _on_device(name, t, dtype=None, shape=None, contiguous=True):
 def _rows_2d(name, t):
     """A matrix whose rows may lie apart (last dimension contiguous); returns
     its rows, columns and row stride."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must have two dimensions, not %d" % (name, len(shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 2:
-        raise ValueError("%s must have two dimensions, not %d" % (name, t.dim()))
-    rows, cols = t.shape
+    rows, cols = shape
     if t.is_contiguous():
         return rows, cols, cols
     ld, step = t.stride()
@@ -557,117 +572,114 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
     """Router with load statistics and losses on device logits [T, E] (float32,
     bfloat16 or float16; rows may lie apart); mask: bool or uint8 [T], false
     for padding."""
-    torch = _torch()
-    lib = load_library()
+    lib = _start()
     T, E, ld = _rows_2d("logits", logits)
-    mp = _mask(mask, T)
     dev, k = logits.device, int(k)
     kk = max(k, 0)
-    f32, i32, empty = torch.float32, torch.int32, torch.empty
-    out = RouterOut(empty((T, kk), dtype=i32, device=dev), empty((T, kk), dtype=f32, device=dev),
-                    empty(T, dtype=f32, device=dev), empty(E, dtype=i32, device=dev), empty(E, dtype=f32, device=dev),
-                    empty(2, dtype=f32, device=dev), empty(1, dtype=i32, device=dev))
-    wsb = lib.trellis_moe_router_workspace_size(T, E)
-    ws = empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    ids, w, lse, counts, prob, losses, tokens = out
-    _launch(lib.trellis_moe_router_forward, dev, stream, logits.data_ptr(), _dtype_code(logits.dtype), ld, mp, T, E, k,
-            ids.data_ptr(), w.data_ptr(), lse.data_ptr(), counts.data_ptr(), prob.data_ptr(), losses.data_ptr(),
-            tokens.data_ptr(), _opt(ws), wsb)
-    return out
+    wsb = lib.trellis_moe_router_workspace_size(T, E) if T > 128 else 0
+    ws = _empty(wsb, dtype=_u8, device=dev) if wsb else None
+    ids, counts, tokens = _empty((T, kk), dtype=_i32, device=dev), _empty(E, dtype=_i32, device=dev), _empty(1, dtype=_i32, device=dev)
+    w, lse = _empty((T, kk), dtype=_f32, device=dev), _empty(T, dtype=_f32, device=dev)
+    prob, losses = _empty(E, dtype=_f32, device=dev), _empty(2, dtype=_f32, device=dev)
+    _launch(lib.trellis_moe_router_forward, logits.get_device(), stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+            None if mask is None else _mask(mask, T), T, E, k, ids.data_ptr(), w.data_ptr(), lse.data_ptr(),
+            counts.data_ptr(), prob.data_ptr(), losses.data_ptr(), tokens.data_ptr(), _opt(ws), wsb)
+    return RouterOut(ids, w, lse, counts, prob, losses, tokens)
 
 
 def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=None, out=None, stream=None):
     """Gradient of the logits from grad_w [T, k] and grad_losses [2] (float32,
     on the device, either may be None); fwd and mask as in the forward call."""
-    torch = _torch()
-    lib = load_library()
+    lib = _start()
     T, E, ld = _rows_2d("logits", logits)
     k = fwd.ids.shape[1]
-    f32, i32 = torch.float32, torch.int32
-    _on_device("ids", fwd.ids, i32, (T, k))
-    _on_device("w", fwd.w, f32, (T, k))
-    _on_device("lse", fwd.lse, f32, (T,))
-    _on_device("counts", fwd.counts, i32, (E,))
-    _on_device("tokens", fwd.tokens, i32, (1,))
-    _on_device("grad_w", grad_w, f32, (T, k))
-    _on_device("grad_losses", grad_losses, f32, (2,))
+    _on_device("ids", fwd.ids, _i32, (T, k))
+    _on_device("w", fwd.w, _f32, (T, k))
+    _on_device("lse", fwd.lse, _f32, (T,))
+    _on_device("counts", fwd.counts, _i32, (E,))
+    _on_device("tokens", fwd.tokens, _i32, (1,))
+    _on_device("grad_w", grad_w, _f32, (T, k))
+    _on_device("grad_losses", grad_losses, _f32, (2,))
     mp = _mask(mask, T)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out = _empty((T, E), dtype=logits.dtype, device=logits.device)
     else:
         _on_device("out", out, logits.dtype, (T, E))
-    _launch(lib.trellis_moe_router_backward, logits.device, stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+    _launch(lib.trellis_moe_router_backward, logits.get_device(), stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
             mp, T, E, k, fwd.ids.data_ptr(), fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(),
             fwd.tokens.data_ptr(), _opt(grad_w), _opt(grad_losses), out.data_ptr())
     return out
 
 
 def _route_rows(rows, w):
-    _on_device("w", w, _torch().float32)
-    if w.dim() != 2:
-        raise ValueError("w must have two dimensions, not %d" % w.dim())
-    T, k = w.shape
+    ws, rs = w.shape, rows.shape
+    if (len(ws) == 2 and len(rs) == 2 and rs[0] == ws[0] * ws[1] and w.dtype is _f32 and w.is_cuda and rows.is_cuda and
+            w.is_contiguous() and rows.is_contiguous()):
+        return ws[0], ws[1], rs[1]
+    _on_device("w", w, _f32)
+    if len(ws) != 2:
+        raise ValueError("w must have two dimensions, not %d" % len(ws))
     _on_device("rows", rows)
-    if rows.dim() != 2 or rows.shape[0] != T * k:
-        raise ValueError("rows must have shape [%d, H], not %s" % (T * k, tuple(rows.shape)))
-    return T, k, rows.shape[1]
+    raise ValueError("rows must have shape [%d, H], not %s" % (ws[0] * ws[1], tuple(rs)))
 
 
 def combine(rows, w, out=None, stream=None):
     """out [T, H] float32 = sum_j w[t, j] rows[t * k + j] for rows [T * k, H] in
     route order and w float32 [T, k]."""
-    torch = _torch()
+    lib = _start()
     T, k, H = _route_rows(rows, w)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=rows.device)
+        out = _empty((T, H), dtype=_f32, device=rows.device)
     else:
-        _on_device("out", out, torch.float32, (T, H))
-    _launch(load_library().trellis_moe_combine_forward, rows.device, stream, rows.data_ptr(), _dtype_code(rows.dtype),
+        _on_device("out", out, _f32, (T, H))
+    _launch(lib.trellis_moe_combine_forward, rows.get_device(), stream, rows.data_ptr(), _dtype_code(rows.dtype),
             w.data_ptr(), T, k, H, out.data_ptr())
     return out
 
 
 def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = True, stream=None):
     """(grad_rows of the rows' type, grad_w float32) of combine; None where not wanted."""
-    torch = _torch()
+    lib = _start()
     T, k, H = _route_rows(rows, w)
-    _on_device("grad_out", grad_out, torch.float32, (T, H))
-    grows = torch.empty_like(rows) if want_rows else None
-    gw = torch.empty_like(w) if want_w else None
-    _launch(load_library().trellis_moe_combine_backward, rows.device, stream, rows.data_ptr(),
-            _dtype_code(rows.dtype), w.data_ptr(), grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw))
+    _on_device("grad_out", grad_out, _f32, (T, H))
+    grows = _torch_mod.empty_like(rows) if want_rows else None
+    gw = _torch_mod.empty_like(w) if want_w else None
+    _launch(lib.trellis_moe_combine_backward, rows.get_device(), stream, rows.data_ptr(), _dtype_code(rows.dtype),
+            w.data_ptr(), grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw))
     return grows, gw
 
 
 def mxfp4_quantize(x, stream=None):
     """Rows of x [rows, K] (float32, bfloat16 or float16; rows may lie apart) ->
     (codes uint8 [rows, 16 B], scales uint8 [rows, B]), B = ceil(K / 32)."""
-    torch = _torch()
+    lib = _start()
     rows, K, ld = _rows_2d("x", x)
-    B = (K + 31) // 32
-    codes = torch.empty((rows, 16 * B), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, B), dtype=torch.uint8, device=x.device)
-    _launch(load_library().trellis_moe_mxfp4_quantize, x.device, stream, x.data_ptr(), _dtype_code(x.dtype), ld, rows,
-            K, codes.data_ptr(), scales.data_ptr())
+    B, dev = (K + 31) // 32, x.device
+    codes = _empty((rows, 16 * B), dtype=_u8, device=dev)
+    scales = _empty((rows, B), dtype=_u8, device=dev)
+    _launch(lib.trellis_moe_mxfp4_quantize, x.get_device(), stream, x.data_ptr(), _dtype_code(x.dtype), ld, rows, K,
+            codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
     """Values [rows, K] of MXFP4 codes [rows, 16 B] and scales [rows, B]."""
-    torch = _torch()
-    B = (int(K) + 31) // 32
+    lib = _start()
+    K = int(K)
+    B = (K + 31) // 32
     if codes.dim() != 2:
         raise ValueError("codes must have two dimensions, not %d" % codes.dim())
     rows = codes.shape[0]
-    _on_device("codes", codes, torch.uint8, (rows, 16 * B))
-    _on_device("scales", scales, torch.uint8, (rows, B))
-    dtype = torch.float32 if dtype is None else dtype
+    _on_device("codes", codes, _u8, (rows, 16 * B))
+    _on_device("scales", scales, _u8, (rows, B))
+    dtype = _f32 if dtype is None else dtype
+    code = _dtype_code(dtype)
     if out is None:
-        out = torch.empty((rows, int(K)), dtype=dtype, device=codes.device)
+        out = _empty((rows, K), dtype=dtype, device=codes.device)
     else:
-        _on_device("out", out, dtype, (rows, int(K)))
-    _launch(load_library().trellis_moe_mxfp4_dequantize, codes.device, stream, codes.data_ptr(), scales.data_ptr(),
-            rows, int(K), out.data_ptr(), _dtype_code(dtype))
+        _on_device("out", out, dtype, (rows, K))
+    _launch(lib.trellis_moe_mxfp4_dequantize, codes.get_device(), stream, codes.data_ptr(), scales.data_ptr(), rows, K,
+            out.data_ptr(), code)
     return out
 
 
@@ -677,14 +689,14 @@ class _MxFp4:
 
     def __init__(self, codes, scales, K: int, max_rows: int, gated: bool):
         torch = _torch()
-        self.lib = load_library()
+        self.lib = _start()
         B = (int(K) + 31) // 32
         E, R = int(codes.shape[0]), int(codes.shape[1])
         _on_device("codes", codes, torch.uint8, (E, R, 16 * B))
         _on_device("scales", scales, torch.uint8, (E, R, B))
         if gated and R % 2:
             raise ValueError("a gated matrix has gate and up rows: %d rows are odd" % R)
-        self.device = codes.device
+        self.device, self.index = codes.device, codes.get_device()
         self.codes, self.scales = codes, scales
         self.E, self.N, self.K, self.gated = E, R // 2 if gated else R, int(K), bool(gated)
         d = MxFp4Desc(E, self.N, self.K, 1 if gated else 0, int(max_rows), codes.data_ptr(), scales.data_ptr())
@@ -725,17 +737,18 @@ class _MxFp4:
         _check(self.lib.trellis_moe_mxfp4_set_wait_test(self.handle, int(wait_limit_ns), 1 if stall_issuer else 0))
 
     def _output(self, rows, x, out, out_dtype):
-        torch = _torch()
-        dtype = out.dtype if out is not None else (torch.float32 if out_dtype is None else out_dtype)
-        if out_dtype is not None and dtype != out_dtype:
-            raise ValueError("out is %s, out_dtype %s" % (dtype, out_dtype))
-        if x.device != self.device:
+        """The result tensor, and its dtype's number."""
+        if x.get_device() != self.index:
             raise ValueError("x is on %s, the weights on %s" % (x.device, self.device))
         if x.shape[1] != self.K:
             raise ValueError("x must have %d columns, not %d" % (self.K, x.shape[1]))
         if out is None:
-            return torch.empty((rows, self.N), dtype=dtype, device=self.device)
-        return _on_device("out", out, dtype, (rows, self.N))
+            dtype = _f32 if out_dtype is None else out_dtype
+            code = _dtype_code(dtype)
+            return _empty((rows, self.N), dtype=dtype, device=self.device), code
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        return _on_device("out", out, None, (rows, self.N)), _dtype_code(out.dtype)
 
 
 class MxFp4Linear(_MxFp4):
@@ -749,10 +762,9 @@ class MxFp4Linear(_MxFp4):
         """x [T, K] (float32, bfloat16 or float16; rows may lie apart) -> [T, N]
         of out_dtype (default float32)."""
         T, _, ld = _rows_2d("x", x)
-        out = self._output(T, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward, self.device, stream, self.handle, x.data_ptr(),
-                _dtype_code(x.dtype), ld, T, out.data_ptr(), _dtype_code(out.dtype), self.workspace_ptr,
-                self.workspace_bytes)
+        out, code = self._output(T, x, out, out_dtype)
+        _launch(self.lib.trellis_moe_mxfp4_forward, self.index, stream, self.handle, x.data_ptr(), _dtype_code(x.dtype),
+                ld, T, out.data_ptr(), code, self.workspace_ptr, self.workspace_bytes)
         return out
 
 
@@ -768,13 +780,13 @@ class MxFp4Experts(_MxFp4):
         """x [T, K] (per_route: [T * topk, K]) and ids int32 [T, topk] -> rows
         [T * topk, N] in route order, of out_dtype (default float32)."""
         rows, _, ld = _rows_2d("x", x)
-        T = ids.shape[0]
-        _on_device("ids", ids, _torch().int32, (T, self.topk))
-        need = T * self.topk if per_route else T
+        T, topk = ids.shape[0], self.topk
+        _on_device("ids", ids, _i32, (T, topk))
+        need = T * topk if per_route else T
         if rows != need:
             raise ValueError("x must have %d rows, not %d" % (need, rows))
-        out = self._output(T * self.topk, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.device, stream, self.handle, x.data_ptr(),
-                _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T, self.topk, out.data_ptr(),
-                _dtype_code(out.dtype), self.workspace_ptr, self.workspace_bytes)
+        out, code = self._output(T * topk, x, out, out_dtype)
+        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.index, stream, self.handle, x.data_ptr(),
+                _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T, topk, out.data_ptr(), code,
+                self.workspace_ptr, self.workspace_bytes)
         return out
