@@ -77,7 +77,7 @@ __device__ __forceinline__ MxUnit mx_unit(const MxTcArgs& a, int u, int units, F
   m.tile = v - b * (int)tiles.d;
   m.slot0 = b * a.bn;
   if (EXPERTS) {
-    const int2 i = __ldg(a.block_info + b);  // (of an earlier kernel: complete before mx_grid_wait returns)
+    const int2 i = __ldg(a.block_info + b);  // (the map's, complete before this kernel starts)
     m.expert = i.x;
     m.rows = i.y;
   } else {
@@ -130,15 +130,15 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
   int it = 0, ahead = 0;
   bool ok = true;
   MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
-  if (!EXPERTS) {
-    // Dense: the kernel before this one quantises x, and lets this one start
-    // only after it has itself waited for what came before; so W may be read
-    // while x is being quantised.
+  {
+    // The kernel before this one quantises x, and lets this one start only after
+    // it has itself waited for what came before it (by expert, the route map):
+    // the first stages' W is read while x is being quantised and stored.
     if ((int)blockIdx.x < g.units) ahead = min(g.ring, g.stages);
-    const uint8_t* wsf = a.wscale + (size_t)next.tile * g.stages * 1024;
+    const uint8_t* wsf = a.wscale + ((size_t)next.expert * (GATED ? 2 : 1) * g.tiles.d + next.tile) * g.stages * 1024;
     for (int s = 0; s < ahead; ++s)
-      load_w(s, base + (uint32_t)s * g.stage_bytes, bar0 + s * 8, next.tile * 128, wsf,
-             wsf + (size_t)g.tiles.d * g.stages * 1024);
+      load_w(s, base + (uint32_t)s * g.stage_bytes, bar0 + s * 8,
+             next.expert * (GATED ? 2 * a.N : a.N) + next.tile * 128, wsf, wsf + (size_t)g.tiles.d * g.stages * 1024);
     mx_grid_wait();
   }
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
@@ -154,7 +154,7 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
         break;
       }
       const uint32_t st = base + (uint32_t)r.slot * g.stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
-      if (EXPERTS || it >= ahead) load_w(s, st, bar, wrow, wsf, usf);
+      if (it >= ahead) load_w(s, st, bar, wrow, wsf, usf);
       if (lead) {
         mx_tma_2d(st + g.a_bytes, &a.xmap, s * 128, m.slot0, bar);
         mx_bulk(st + g.a_bytes + g.b_bytes + g.sfa_bytes, xsf + (uint32_t)s * g.sfb_bytes, g.sfb_bytes, bar);
@@ -345,14 +345,15 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (EXPERTS || warp != kMxEpiWarps) mx_grid_wait();  // (the dense loader waits by itself)
+  // (the loader alone waits for the kernel before this one: what the others read
+  // and write hangs on its copies of x, and the map was complete before)
   mx_grid_launch();
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
   const MxGeom g = mx_geom<GATED, EXPERTS>(a, ring, tiles);
   if (g.units == 0) {
-    // (every route was dropped)
+    mx_grid_wait();  // (every route was dropped; this kernel still ends after the one before it)
   } else if (warp < kMxEpiWarps) {
     mx_epilogue<GATED, EXPERTS, T>(a, g, bars, tmem, smem + (size_t)ring * g.stage_bytes, abort, limit);
   } else if (warp == kMxEpiWarps) {
@@ -462,15 +463,10 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
                                                           FastDiv bn, int items) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
-  if (!a.slot_of_route) {
-    mx_grid_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
-  }
-  mx_grid_launch();
-  if (i >= items) {
-    if (a.slot_of_route) mx_grid_wait();
-    return;
-  }
+  if (!a.slot_of_route || i >= items) mx_grid_wait();
+  if (!a.slot_of_route && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
+  if (!a.slot_of_route || i >= items) mx_grid_launch();
+  if (i >= items) return;
   const int nb = mx_blocks(a.K);
   const int row = (int)segs.div(i), s0 = (i - row * (int)segs.d) * per, n = min(per, stages - s0);
   const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ld + s0 * 256 + lane * 8;
@@ -487,7 +483,10 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
       q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
     }
   }
-  if (a.slot_of_route) mx_grid_wait();
+  if (a.slot_of_route) {
+    mx_grid_wait();
+    mx_grid_launch();  // (only now: the products' kernel relies on the map when it starts)
+  }
   for (int j = 0; j < a.topk; ++j) {
     const int r = row * a.topk + j;
     const int slot = a.slot_of_route ? a.slot_of_route[r] : r;
