@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
     s_abort = 0;
     mbar_fence_init();
   }
-  mx_grid_wait();
-  mx_grid_launch();
+  grid_wait();
+  grid_launch();
   MdChunk m{0, min(kMxDecRows, a.rows - chunk * kMxDecRows), false};
   if (a.ids) {
     m = md_find(a, chunk, warp == 0 ? s_row : nullptr);

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "pdl.cuh"
 #include "tc.cuh"
 
 namespace tmoe {
@@ -12,12 +13,6 @@ namespace tmoe {
 constexpr uint64_t kMxWaitNs = 2000000000ull;   // limit of a pipeline wait
 constexpr uint64_t kMxDrainNs = 500000000ull;   // of a wait for copies in flight after one gave up
 constexpr int kMxTileBytes = 128 * 128;         // 128 rows of W, 256 columns
-
-// Programmatic dependent launch: a kernel may start while the one before it in
-// the stream still runs; before it touches global memory it waits for that one
-// to end, and it lets the next one start as soon as all its own CTAs run.
-__device__ __forceinline__ void mx_grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void mx_grid_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // silu(g) = g / (1 + exp(-g)) with the hardware's exp2 and reciprocal (each a
 // few ulp). Subnormals flush: an exp(-g) that small leaves 1, and a reciprocal

@@ -9,6 +9,7 @@
 
 #include "elem.cuh"
 #include "mxfp4.cuh"
+#include "pdl.cuh"
 #include "status.h"
 
 namespace tmoe {
@@ -29,6 +30,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ x, int64_t ld, uint32_t total, FastDiv per,
                                                         int K, uint32_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales) {
+  grid_wait();
+  grid_launch();
   const uint32_t tile = blockIdx.x * kQuTile + threadIdx.x;
   Eight<T, VEC> e[kQuUnroll];
 #pragma unroll
@@ -55,6 +58,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_mxfp4_dequantize(const uint32_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales, uint32_t total,
                                                           FastDiv per, int K, T* __restrict__ out) {
+  grid_wait();
+  grid_launch();
   const uint32_t tile = blockIdx.x * kQuTile + threadIdx.x;
   uint32_t c[kQuUnroll], b[kQuUnroll];
 #pragma unroll
@@ -99,10 +104,9 @@ cudaError_t mxfp4_quantize(const void* x, int dtype, int64_t ld, long rows, int 
     using T = decltype(elem);
     return by_rows(rows, per, [&](long r, long n) {
       const uint32_t total = (uint32_t)(n * per);
-      k_mxfp4_quantize<T, decltype(vec)::value><<<quant_ctas(total), 256, 0, st>>>(
-          static_cast<const T*>(x) + r * ld, ld, total, FastDiv(per), K, reinterpret_cast<uint32_t*>(codes) + r * per,
-          scales + r * nb);
-      return cudaGetLastError();
+      return launch_after(k_mxfp4_quantize<T, decltype(vec)::value>, dim3(quant_ctas(total)), 256, 0, st,
+                             static_cast<const T*>(x) + r * ld, ld, total, FastDiv(per), K,
+                             reinterpret_cast<uint32_t*>(codes) + r * per, scales + r * nb);
     });
   };
   return TM_BY_DTYPE_VEC(dtype, eights(x, ld, K, es), go);
@@ -115,10 +119,9 @@ cudaError_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long r
     using T = decltype(elem);
     return by_rows(rows, per, [&](long r, long n) {
       const uint32_t total = (uint32_t)(n * per);
-      k_mxfp4_dequantize<T, decltype(vec)::value><<<quant_ctas(total), 256, 0, st>>>(
-          reinterpret_cast<const uint32_t*>(codes) + r * per, scales + r * nb, total, FastDiv(per), K,
-          static_cast<T*>(out) + r * K);
-      return cudaGetLastError();
+      return launch_after(k_mxfp4_dequantize<T, decltype(vec)::value>, dim3(quant_ctas(total)), 256, 0, st,
+                             reinterpret_cast<const uint32_t*>(codes) + r * per, scales + r * nb, total, FastDiv(per), K,
+                             static_cast<T*>(out) + r * K);
     });
   };
   return TM_BY_DTYPE_VEC(dtype, eights(out, K, K, es), go);

@@ -139,7 +139,7 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
     for (int s = 0; s < ahead; ++s)
       load_w(s, base + (uint32_t)s * g.stage_bytes, bar0 + s * 8,
              next.expert * (GATED ? 2 * a.N : a.N) + next.tile * 128, wsf, wsf + (size_t)g.tiles.d * g.stages * 1024);
-    mx_grid_wait();
+    grid_wait();
   }
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x) {
     const MxUnit m = next;
@@ -347,13 +347,13 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   tc_fence_after();
   // (the loader alone waits for the kernel before this one: what the others read
   // and write hangs on its copies of x, and the map was complete before)
-  mx_grid_launch();
+  grid_launch();
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
   const MxGeom g = mx_geom<GATED, EXPERTS>(a, ring, tiles);
   if (g.units == 0) {
-    mx_grid_wait();  // (every route was dropped; this kernel still ends after the one before it)
+    grid_wait();  // (every route was dropped; this kernel still ends after the one before it)
   } else if (warp < kMxEpiWarps) {
     mx_epilogue<GATED, EXPERTS, T>(a, g, bars, tmem, smem + (size_t)ring * g.stage_bytes, abort, limit);
   } else if (warp == kMxEpiWarps) {
@@ -400,22 +400,6 @@ cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// A launch that may start while the kernel before it ends.
-template <typename... P, typename... A>
-cudaError_t mx_launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <bool GATED, bool EXPERTS, typename T>
 cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
   auto kern = k_mx_tc<GATED, EXPERTS, T>;
@@ -427,7 +411,7 @@ cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
   const int ring = (int)std::min<uint32_t>(kMxMaxStages, (kMxSmem - 1024 - store) / stage_bytes);
   const long units = (long)a.max_blocks * ((a.N + 127) / 128);
   const int grid = (int)std::max<long>(1, std::min<long>(units, a.sms));
-  return mx_launch_after(kern, dim3(grid), kMxThreads, 1024 + ring * stage_bytes + store, st, a, ring,
+  return launch_after(kern, dim3(grid), kMxThreads, 1024 + ring * stage_bytes + store, st, a, ring,
                          FastDiv((a.N + 127) / 128));
 }
 
@@ -463,9 +447,9 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
                                                           FastDiv bn, int items) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
-  if (!a.slot_of_route || i >= items) mx_grid_wait();
+  if (!a.slot_of_route || i >= items) grid_wait();
   if (!a.slot_of_route && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
-  if (!a.slot_of_route || i >= items) mx_grid_launch();
+  if (!a.slot_of_route || i >= items) grid_launch();
   if (i >= items) return;
   const int nb = mx_blocks(a.K);
   const int row = (int)segs.div(i), s0 = (i - row * (int)segs.d) * per, n = min(per, stages - s0);
@@ -484,8 +468,8 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
     }
   }
   if (a.slot_of_route) {
-    mx_grid_wait();
-    mx_grid_launch();  // (only now: the products' kernel relies on the map when it starts)
+    grid_wait();
+    grid_launch();  // (only now: the products' kernel relies on the map when it starts)
   }
   for (int j = 0; j < a.topk; ++j) {
     const int r = row * a.topk + j;
@@ -548,8 +532,8 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
   for (int e = tid; e < kMaxExperts; e += kMapThreads) s_cnt[e] = 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  mx_grid_wait();
-  mx_grid_launch();
+  grid_wait();
+  grid_launch();
   const int part = (a.R + kMapCtas - 1) / kMapCtas, lo = (int)rank * part, hi = min(a.R, lo + part);
   const bool held = part <= kMapHeld * kMapThreads;
   int e[kMapHeld], at[kMapHeld];
@@ -654,7 +638,7 @@ cudaError_t launch_mx_tc(MxTcArgs& a, const uint8_t* codes_x, long slots, int ou
 }
 
 cudaError_t launch_mx_map(const MxMapArgs& a, cudaStream_t st) {
-  return mx_launch_after(k_mx_map, dim3(kMapCtas), kMapThreads, 0, st, a);
+  return launch_after(k_mx_map, dim3(kMapCtas), kMapThreads, 0, st, a);
 }
 
 cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_t st) {
@@ -662,7 +646,7 @@ cudaError_t launch_mx_rows_quantize(const MxQuantArgs& a, int dtype, cudaStream_
   const int stages = mx_stages(a.K), segs = (stages + kRqUnroll - 1) / kRqUnroll, per = (stages + segs - 1) / segs;
   const int items = a.x_rows * segs;
   auto go = [&](auto elem, auto vec) {
-    return mx_launch_after(k_mx_rows_quantize<decltype(elem), decltype(vec)::value>, dim3((items + 7) / 8), 256, 0, st, a,
+    return launch_after(k_mx_rows_quantize<decltype(elem), decltype(vec)::value>, dim3((items + 7) / 8), 256, 0, st, a,
                            stages, per, FastDiv(segs), FastDiv(a.bn), items);
   };
   return TM_BY_DTYPE_VEC(dtype, eights(a.x, a.ld, a.K, es), go);

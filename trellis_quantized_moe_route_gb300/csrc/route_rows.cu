@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "elem.cuh"
+#include "pdl.cuh"
 #include "status.h"
 
 namespace tmoe {
@@ -20,6 +21,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_combine_routes(const T* __restrict__ rows, const float* __restrict__ w,
                                                         uint32_t total, FastDiv per, int k, int H,
                                                         float* __restrict__ out) {
+  grid_wait();
+  grid_launch();
   const uint32_t n = blockIdx.x * 256 + threadIdx.x;
   if (n >= total) return;
   const size_t t = per.div(n);
@@ -59,6 +62,8 @@ __global__ void __launch_bounds__(512) k_combine_routes_bwd(const T* __restrict_
   __shared__ float s_dot[16][kCbChunk];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const size_t t = blockIdx.x;
+  grid_wait();
+  grid_launch();
   for (int j0 = 0; j0 < k; j0 += kCbChunk) {
     float dot[kCbChunk] = {}, wj[kCbChunk];
 #pragma unroll
@@ -143,9 +148,8 @@ tm_status trellis_moe_combine_forward(const void* rows, int32_t dtype, const flo
   const uint32_t items = (uint32_t)T * per;
   auto go = [&](auto elem, auto vec) {
     using E = decltype(elem);
-    k_combine_routes<E, decltype(vec)::value><<<(items + 255) / 256, 256, 0, (cudaStream_t)stream>>>(
-        static_cast<const E*>(rows), w, items, FastDiv(per), k, H, out);
-    return cudaGetLastError();
+    return launch_after(k_combine_routes<E, decltype(vec)::value>, dim3((items + 255) / 256), 256, 0,
+                           (cudaStream_t)stream, static_cast<const E*>(rows), w, items, FastDiv(per), k, H, out);
   };
   const bool vec = eights(rows, H, H, dtype_bytes(dtype)) && eights(out, H, H, 4);
   const cudaError_t e = TM_BY_DTYPE_VEC(dtype, vec, go);
@@ -171,9 +175,8 @@ tm_status trellis_moe_combine_backward(const void* rows, int32_t dtype, const fl
   const int threads = ((groups + passes - 1) / passes + 31) / 32 * 32;
   auto go = [&](auto elem, auto v) {
     using E = decltype(elem);
-    k_combine_routes_bwd<E, decltype(v)::value><<<T, threads, 0, (cudaStream_t)stream>>>(
-        static_cast<const E*>(rows), w, grad_out, k, H, static_cast<E*>(grad_rows), grad_w);
-    return cudaGetLastError();
+    return launch_after(k_combine_routes_bwd<E, decltype(v)::value>, dim3(T), threads, 0, (cudaStream_t)stream,
+                           static_cast<const E*>(rows), w, grad_out, k, H, static_cast<E*>(grad_rows), grad_w);
   };
   const cudaError_t e = TM_BY_DTYPE_VEC(dtype, vec, go);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "combine backward");

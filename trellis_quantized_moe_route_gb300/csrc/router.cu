@@ -37,6 +37,7 @@
 #include <algorithm>
 
 #include "elem.cuh"
+#include "pdl.cuh"
 #include "status.h"
 
 namespace tmoe {
@@ -84,8 +85,6 @@ struct Order<__half> : Order16 {
   }
 };
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -252,7 +251,8 @@ __global__ void __cluster_dims__(kFinCtas, 1, 1) __launch_bounds__(kMaxExperts) 
   __shared__ float s_p[kMaxExperts], s_z;
   __shared__ int s_c[kMaxExperts], s_n;
   const int e = threadIdx.x, q = (int)cluster_rank();
-  griddep_wait();
+  grid_wait();
+  grid_launch();
   float p[kEach], z[kEach];
   int c[kEach], n[kEach];
 #pragma unroll
@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, in
   __shared__ int s_nv[kRtWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = csize > 1 ? (int)cluster_rank() : 0;
-  griddep_launch();
+  grid_wait();
+  grid_launch();
   for (int e = threadIdx.x; e < V * 32; e += blockDim.x) s_cnt[e] = 0;
   __syncthreads();
   const T* logits = static_cast<const T*>(a.logits);
@@ -499,6 +500,8 @@ __global__ void __launch_bounds__(256, kRtBwdCtas) k_router_bwd(RouterBwd a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* logits = static_cast<const T*>(a.logits);
   T* grad = static_cast<T*>(a.grad_logits);
+  grid_wait();
+  grid_launch();
   const int n = *a.tokens;
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.0f;
   const float gb = a.grad_losses ? a.grad_losses[0] * (float)a.E * inv_n : 0.0f;
@@ -672,27 +675,24 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   a.part_counts = reinterpret_cast<int32_t*>(a.part_prob + (size_t)clusters * E);
   a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)clusters * E);
   a.part_n = reinterpret_cast<int32_t*>(a.part_z + clusters);
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * csize));
   cfg.blockDim = dim3(32 * kRtWarps);
   cfg.stream = st;
   cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 1 : 0;
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)csize, 1, 1};
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)csize, 1, 1};
   cudaError_t e = by_pairs(dtype, E, logits, ld, nullptr, [&](auto elem, auto pair) {
     return by_width(E, [&](auto v) {
       return cudaLaunchKernelEx(&cfg, k_router_fwd<decltype(v)::value, decltype(elem), decltype(pair)::value>, a, csize);
     });
   });
   if (e == cudaSuccess && clusters > 1) {
-    cfg.gridDim = dim3(kFinCtas);
-    cfg.blockDim = dim3(kMaxExperts);
-    cfg.numAttrs = 1;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    e = cudaLaunchKernelEx(&cfg, k_router_finish, a, clusters);
+    e = launch_after(k_router_finish, dim3(kFinCtas), kMaxExperts, 0, st, a, clusters);
   }
   return e == cudaSuccess ? TM_OK : status_cuda(e, "router with losses");
 }
@@ -715,8 +715,7 @@ tm_status trellis_moe_router_backward(const void* logits, int32_t dtype, int64_t
   const int ctas = std::min(152 * kRtBwdCtas, (T + 7) / 8);
   const cudaError_t e = by_pairs(dtype, E, logits, ld, grad_logits, [&](auto elem, auto pair) {
     return by_width(E, [&](auto v) {
-      k_router_bwd<decltype(v)::value, decltype(elem), decltype(pair)::value><<<ctas, 256, 0, st>>>(a);
-      return cudaGetLastError();
+      return launch_after(k_router_bwd<decltype(v)::value, decltype(elem), decltype(pair)::value>, dim3(ctas), 256, 0, st, a);
     });
   });
   return e == cudaSuccess ? TM_OK : status_cuda(e, "router backward");
