@@ -77,6 +77,13 @@ struct MxDecArgs {
   CUtensorMap wmap;
 };
 cudaError_t launch_mx_dec(const MxDecArgs& a, int chunks, cudaStream_t st);
+// log2 of the CTAs of a cluster, among which the stages are split: as many parts
+// as there are stages and SMs (two CTAs on some), at most a portable cluster.
+inline int mx_dec_split(long units, int stages, int sms) {
+  int l = 0;
+  while (l < 3 && (2 << l) <= stages && (units << l) <= sms) ++l;
+  return l;
+}
 
 // Rows of x to MXFP4 in block order: row r's codes at slot s, its scales at
 // [s / bn][...][(s % bn) / 128]. dense: s = r; by expert: slot_of_route of its

@@ -316,9 +316,7 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   if (attr != cudaSuccess) return attr;
   const int stages = mx_stages(a.K), tiles = (a.N + 127) / 128;
   const int units = chunks * tiles;
-  // as many parts as there are stages and idle SMs (two CTAs each), at most a portable cluster
-  int lsplit = 0;
-  while (lsplit < 3 && (2 << lsplit) <= stages && (units << lsplit) <= a.sms) ++lsplit;
+  const int lsplit = mx_dec_split(units, stages, a.sms);
   const int split = 1 << lsplit;
   const int per = (stages + split - 1) / split;
   const int stage = H * (kMxTileBytes + 1024) + kMdXBytes + 1024;
