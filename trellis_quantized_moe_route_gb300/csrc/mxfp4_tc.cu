@@ -467,13 +467,15 @@ __global__ void __launch_bounds__(256) k_mx_rows_quantize(const MxQuantArgs a, i
       q[u] = mxfp4_codes(v, e[u].block_amax_bits(), byte[u]);
     }
   }
+  int mine = row;  // lane j: the slot of the row's route j (at most 32)
   if (a.slot_of_route) {
     grid_wait();
     grid_launch();  // (only now: the products' kernel relies on the map when it starts)
+    mine = lane < a.topk ? a.slot_of_route[row * a.topk + lane] : -1;
   }
   for (int j = 0; j < a.topk; ++j) {
     const int r = row * a.topk + j;
-    const int slot = a.slot_of_route ? a.slot_of_route[r] : r;
+    const int slot = __shfl_sync(0xFFFFFFFFu, mine, j);
     if (slot < 0) {
       if (s0 == 0) {
         char* o = static_cast<char*>(a.out) + (size_t)r * a.out_row_bytes;
