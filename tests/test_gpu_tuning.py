@@ -155,6 +155,41 @@ def test_router_agrees_with_the_layers_router(binding):
     assert torch.equal(ids, r.ids) and torch.allclose(w, r.w, rtol=64 * U, atol=0)
 
 
+# (many tokens of 16-bit logits, at most eight experts a token: a lane takes a token)
+@pytest.mark.parametrize("T,E,k,dtype,masked,neg", [
+    (32768, 160, 8, "bf16", True, True), (32845, 64, 6, "f16", False, True), (40001, 8, 3, "bf16", True, False),
+    (33000, 256, 8, "f16", True, True), (32769, 128, 1, "bf16", False, False)])
+def test_router_many_tokens(binding, T, E, k, dtype, masked, neg):
+    mask = (gen(T).random(T) < 0.8) if masked else None
+    check_router(binding, router_inputs(T, E, dtype, T + E, neg=neg), k, mask, T)
+
+
+def test_router_many_tokens_strided_masked_and_repeated(binding):
+    """Rows with a stride, equal calls, and NaN or infinities in masked tokens, with a warp and with a lane a token."""
+    T, E, k = 33333, 40, 5
+    wide = router_inputs(T, 56, "bf16", 11)
+    mask = np.ones(T, dtype=bool)
+    mask[[3, 29, T - 1]] = False
+    wide[3] = float("nan")
+    wide[29, 5 + 8] = float("inf")
+    wide[T - 1] = -np.inf
+    view, md = wide.cuda()[:, 8:8 + E], torch.from_numpy(mask).cuda()
+    a = binding.router_forward(view, k, mask=md)
+    for b in (binding.router_forward(view.contiguous(), k, mask=md), binding.router_forward(view, k, mask=md)):
+        for x, y in zip(a[1:], b[1:]):
+            assert torch.equal(torch.nan_to_num(x.double(), nan=-7.0), torch.nan_to_num(y.double(), nan=-7.0))
+        assert torch.equal(a[0], b[0])
+    odd = torch.zeros(T, E + 9, dtype=torch.bfloat16, device="cuda")[:, 1:1 + E].copy_(view)  # (rows not in 16-byte pieces)
+    c = binding.router_forward(odd, k, mask=md)
+    assert torch.equal(a.ids, c.ids) and torch.equal(a.counts, c.counts) and int(a.tokens) == int(c.tokens) == T - 3
+    assert torch.isfinite(a.losses).all() and torch.isfinite(a.prob).all()
+    rel = 40 * U
+    assert torch.allclose(a.prob, c.prob, rtol=rel + T * U, atol=0)
+    assert torch.allclose(a.losses, c.losses, rtol=4 * rel + T * U, atol=0)
+    ok = md.clone()
+    assert torch.allclose(a.w[ok], c.w[ok], rtol=rel, atol=0) and torch.allclose(a.lse[ok], c.lse[ok], rtol=rel, atol=rel)
+
+
 # ----------------------------------------------------------------- combine
 @pytest.mark.parametrize("T,k,H,dtype", [(1, 1, 1, "f32"), (8, 8, 1024, "bf16"), (3, 10, 333, "f16"), (17, 32, 64, "f32"),
                                          (40, 9, 2560, "bf16"), (5, 2, 7, "bf16"), (300, 3, 40, "f32")])

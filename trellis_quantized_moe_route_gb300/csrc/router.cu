@@ -14,7 +14,7 @@
 // All of it in fp32 whatever the logits' type; only dl is rounded to it.
 //
 // One warp takes a token, V logits a lane, and reads the next token's row while
-// it works on this one. What bounds it is the selection's instructions, not the
+// it works on this one (many tokens of 16-bit logits: a lane a token, below). What bounds it is the selection's instructions, not the
 // bytes. Each logit becomes a 32-bit key that is unique in the row and orders
 // like (logit, then lower expert): 16-bit logits have their expert in the low
 // half; fp32 logits give up their lowest 8 bits for it, and a token in which two
@@ -30,10 +30,10 @@
 // time. The backward pass reads the logits again and rebuilds p from lse, which
 // costs less than storing p (T E fp32).
 //
-// 65536 tokens x 160 bf16 logits, k = 8, masked: forward 27 us (360 instructions
-// a token, 65% of the issue slots, the integer pipe 62% busy; its bytes take
-// 4 us), finishing sums 5 us, backward 17 us (220 instructions a token; its
-// bytes take 7 us). 8 tokens x 128: one launch, 4 us.
+// 65536 tokens x 160 bf16 logits, k = 8, masked: forward 17 us with a lane a token
+// (its bytes take 4 us; with a warp a token 24: 360 instructions a token, the
+// integer pipe 62% busy), finishing sums 5 us, backward 17 us (220 instructions a
+// token; its bytes take 7 us). 8 tokens x 128: one launch, 4 us.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -355,6 +355,65 @@ __device__ __noinline__ uint32_t router_select_exact(const float* __restrict__ r
   return mine;
 }
 
+// Adds up a CTA's statistics (s_acc: its warps' probability sums, `width` floats
+// apart; s_z, s_nv: theirs too; s_cnt: the CTA's), then its cluster's of csize
+// CTAs. With one cluster the results are written here, with more its part.
+__device__ __forceinline__ void router_stats(const RouterFwd& a, int csize, int rank, int warps, float* s_acc,
+                                             int width, int* s_cnt, float* s_z, int* s_nv) {
+  // the CTA's sums, in warp order
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    float p = 0.0f;
+    for (int u = 0; u < warps; ++u) p += s_acc[u * width + e];
+    s_acc[e] = p;
+  }
+  if (threadIdx.x == 0) {
+    for (int u = 1; u < warps; ++u) {
+      s_z[0] += s_z[u];
+      s_nv[0] += s_nv[u];
+    }
+  }
+  // the cluster's, in rank order, by its first CTA
+  float p = 0.0f, zs = 0.0f;
+  int c = 0, ns = 0;
+  const int e = threadIdx.x;
+  if (csize > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      for (int u = 0; u < csize; ++u) {
+        if (e < a.E) {
+          p += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_acc[e]), u));
+          c += cluster_peer(&s_cnt[e], u);
+        }
+        zs += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_z[0]), u));
+        ns += cluster_peer(&s_nv[0], u);
+      }
+    }
+    cluster_sync();  // no CTA leaves while its sums are read
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+    if (e < a.E) {
+      p = s_acc[e];
+      c = s_cnt[e];
+    }
+    zs = s_z[0];
+    ns = s_nv[0];
+  }
+  if ((int)gridDim.x == csize) {
+    router_write(a, p, c, zs, ns);
+  } else {
+    const int part = blockIdx.x / csize;
+    if (e < a.E) {
+      a.part_prob[part * a.E + e] = p;
+      a.part_counts[part * a.E + e] = c;
+    }
+    if (e == 0) {
+      a.part_z[part] = zs;
+      a.part_n[part] = ns;
+    }
+  }
+}
+
 // A warp's tokens are warp, warp + W, ... (W: warps of the grid). With one
 // cluster (of csize CTAs) the statistics are finished here.
 template <int V, typename T, bool PAIR>
@@ -424,58 +483,192 @@ __global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, in
     s_nv[warp] = n;
   }
   __syncthreads();
-  // the CTA's sums, in warp order
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    float p = 0.0f;
-    for (int u = 0; u < warps; ++u) p += s_acc[u][e];
-    s_acc[0][e] = p;
-  }
-  if (threadIdx.x == 0) {
-    for (int u = 1; u < warps; ++u) {
-      s_z[0] += s_z[u];
-      s_nv[0] += s_nv[u];
+  router_stats(a, csize, rank, warps, &s_acc[0][0], V * 32, s_cnt, s_z, s_nv);
+}
+
+// The same for many tokens of 16-bit logits and k <= 8, a lane a token: a warp
+// brings 32 rows to shared memory, and each lane finds the k largest of one of
+// them with a list of the eight largest so far, eight keys at a time: sorted by
+// a network of 19 exchanges, merged by eight maxima and 12 exchanges more.
+// Probabilities are made with a warp's lanes over the experts again, since their
+// sums go over the tokens. Rows lie an odd number of 16 bytes apart, so that
+// neither way of reading meets bank conflicts. 160 instructions a token with 160
+// experts, where a warp a token takes 360. At 65536 tokens an SM has 13.5 of
+// these groups of 32, and a quarter of it (one scheduler) 3 or 4: of the 17 us,
+// 3.3 for each of the four, bound by the integer pipe, and the rest is the rows'
+// way from memory and the statistics.
+constexpr int kRtLaneWarps = 8;
+
+__device__ __forceinline__ void exchange(int32_t& a, int32_t& b) {
+  const int32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+
+template <int V, typename T>
+__global__ void __launch_bounds__(kRtLaneWarps * 32, 2) k_router_fwd_lanes(RouterFwd a, int csize, FastDiv units) {
+  using Row = RowRegs<V, T, true>;
+  extern __shared__ uint4 s_rows[];
+  __shared__ int s_cnt[V * 32];
+  __shared__ float s_z[kRtLaneWarps];
+  __shared__ int s_nv[kRtLaneWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = csize > 1 ? (int)cluster_rank() : 0;
+  const int nu = (int)units.d, pitch = nu | 1;
+  uint4* rows = s_rows + (size_t)warp * 32 * pitch;
+  grid_wait();
+  grid_launch();
+  for (int e = threadIdx.x; e < V * 32; e += blockDim.x) s_cnt[e] = 0;
+  __syncthreads();
+  const T* logits = static_cast<const T*>(a.logits);
+  float acc[V] = {};
+  float z = 0.0f;
+  int n = 0;
+  const int groups = (a.T + 31) / 32;
+  for (int g = warp * (int)gridDim.x + (int)blockIdx.x; g < groups; g += (int)gridDim.x * kRtLaneWarps) {
+    const int t0 = g * 32, count = min(32, a.T - t0);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(rows);
+    for (int i = lane; i < count * nu; i += 32) {
+      const int r = (int)units.div(i), c = i - r * nu;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + (uint32_t)(r * pitch + c) * 16u),
+                   "l"(logits + (size_t)(t0 + r) * a.ld + c * 8)
+                   : "memory");
     }
-  }
-  // the cluster's, in rank order, by its first CTA
-  float p = 0.0f, zs = 0.0f;
-  int c = 0, ns = 0;
-  const int e = threadIdx.x;
-  if (csize > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      for (int u = 0; u < csize; ++u) {
-        if (e < a.E) {
-          p += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_acc[0][e]), u));
-          c += cluster_peer(&s_cnt[e], u);
+    const bool in = lane < count;
+    const bool on = in && (a.mask == nullptr || a.mask[t0 + lane] != 0);
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncwarp();
+    // keys as above, in signed order; `low` has the experts' part for two of them
+    uint32_t low[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) low[i] = (0xFFFFu - 2u * i) | (0xFFFEu - 2u * i) << 16;
+    auto read = [&](int c, int32_t(&key)[8]) {
+      const uint4 q = rows[lane * pitch + c];
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v = Row::add_zero(w[i]), sign;
+        asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(sign) : "r"(v));  // each half's sign in all its bits
+        v ^= sign & 0x7FFF7FFFu;
+        key[2 * i] = (int32_t)__byte_perm(v, low[i], 0x1054);
+        key[2 * i + 1] = (int32_t)__byte_perm(v, low[i], 0x3276);
+        low[i] -= 0x00080008u;
+      }
+      exchange(key[0], key[1]), exchange(key[2], key[3]), exchange(key[4], key[5]), exchange(key[6], key[7]);
+      exchange(key[0], key[2]), exchange(key[1], key[3]), exchange(key[4], key[6]), exchange(key[5], key[7]);
+      exchange(key[1], key[2]), exchange(key[5], key[6]);
+      exchange(key[0], key[4]), exchange(key[1], key[5]), exchange(key[2], key[6]), exchange(key[3], key[7]);
+      exchange(key[2], key[4]), exchange(key[3], key[5]);
+      exchange(key[1], key[2]), exchange(key[3], key[4]), exchange(key[5], key[6]);
+    };
+    int32_t top[8];
+    read(0, top);
+#pragma unroll 2
+    for (int c = 1; c < nu; ++c) {
+      int32_t key[8];
+      read(c, key);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = max(top[i], key[7 - i]);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(i & d)) exchange(top[i], top[i + d]);
+    }
+    const auto value = [](int32_t key) { return Order<T>::value(((uint32_t)key ^ 0x80000000u) & Order<T>::kMask); };
+    const bool some = ((uint32_t)top[0] ^ 0x80000000u) > Order<T>::kNone;
+    const float m = value(top[0]);
+    const bool valid = on && some;
+    {
+      float we[8], sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        we[j] = j < a.k ? exp_fast(value(top[j]) - m) : 0.0f;
+        sum += we[j];
+      }
+      int32_t* ids = a.ids + (size_t)(t0 + lane) * a.k;
+      float* w = a.w + (size_t)(t0 + lane) * a.k;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < a.k && in) {
+          const int id = 0xFFFF - (top[j] & 0xFFFF);
+          ids[j] = id;
+          w[j] = some ? __fdividef(we[j], sum) : 0.0f;
+          if (valid && value(top[j]) != -INFINITY) atomicAdd(&s_cnt[id], 1);
         }
-        zs += __int_as_float(cluster_peer(reinterpret_cast<const int*>(&s_z[0]), u));
-        ns += cluster_peer(&s_nv[0], u);
       }
     }
-    cluster_sync();  // no CTA leaves while its sums are read
-    if (rank != 0) return;
-  } else {
-    __syncthreads();
-    if (e < a.E) {
-      p = s_acc[0][e];
-      c = s_cnt[e];
+    const uint32_t valids = __ballot_sync(0xFFFFFFFFu, valid);
+    // Four tokens at a time: their sums over the lanes are folded into one value,
+    // the lanes' upper two bits saying whose it is.
+    float mine = 0.0f;
+    const bool hi = lane & 16, mid = lane & 8;
+#pragma unroll 1
+    for (int t = 0; t < count; t += 4) {  // (rows past the last are there, too, and count for nothing)
+      float p[4][V], total[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Row row;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(rows + (t + j) * pitch);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const uint32_t none = 0xFFFFu & ~Row::kInf16;
+          row.raw[i] = none | none << 16;
+          if (Row::expert(2 * i) < a.E) row.raw[i] = words[lane + 32 * i];
+        }
+        const float mt = __shfl_sync(0xFFFFFFFFu, m, t + j);
+        total[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[j][i] = exp_fast(row.get(i) - mt);
+          total[j] += p[j][i];
+        }
+      }
+      const float x0 = __shfl_xor_sync(0xFFFFFFFFu, hi ? total[0] : total[2], 16);
+      const float x1 = __shfl_xor_sync(0xFFFFFFFFu, hi ? total[1] : total[3], 16);
+      const float u0 = (hi ? total[2] : total[0]) + x0, u1 = (hi ? total[3] : total[1]) + x1;
+      float v = (mid ? u1 : u0) + __shfl_xor_sync(0xFFFFFFFFu, mid ? u0 : u1, 8);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      const float of = __shfl_sync(0xFFFFFFFFu, v, (lane & 3) * 8);
+      if (lane >> 2 == t >> 2) mine = of;
+      const float inv = __fdividef(1.0f, v);
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = __shfl_sync(0xFFFFFFFFu, inv, j * 8);
+      const uint32_t four = valids >> t & 15;
+      if (four == 15) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += p[j][i] * f[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (four >> j & 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += p[j][i] * f[j];
+      }
     }
-    zs = s_z[0];
-    ns = s_nv[0];
+    if (in) {
+      const float lse = m + __logf(mine);
+      a.lse[t0 + lane] = some ? lse : -INFINITY;
+      if (valid) z += lse * lse;
+    }
+    n += __popc(valids);
+    __syncwarp();  // (the rows are read before the next ones come)
   }
-  if ((int)gridDim.x == csize) {
-    router_write(a, p, c, zs, ns);
-  } else {
-    const int part = blockIdx.x / csize;
-    if (e < a.E) {
-      a.part_prob[part * a.E + e] = p;
-      a.part_counts[part * a.E + e] = c;
-    }
-    if (e == 0) {
-      a.part_z[part] = zs;
-      a.part_n[part] = ns;
-    }
+  z = warp_sum(z);
+  __syncthreads();
+  float* s_acc = reinterpret_cast<float*>(s_rows);  // (at least as large: 16 bytes a lane and unit)
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_acc[warp * V * 32 + Row::expert(i)] = acc[i];
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_nv[warp] = n;
   }
+  __syncthreads();
+  router_stats(a, csize, rank, kRtLaneWarps, s_acc, V * 32, s_cnt, s_z, s_nv);
 }
 
 struct RouterBwd {
@@ -620,6 +813,32 @@ RouterGrid router_grid(int T) {
   return {2, std::min(kRtMaxClusters, (ctas + 1) / 2)};
 }
 
+// Whether a call takes a lane a token: 16-bit logits in whole 16-byte pieces, at
+// most the eight of its list, and tokens enough for the SMs' warps, 32 to each.
+// us a forward call (bf16, masked), a warp / a lane a token:
+//   128 experts, k = 8   20480: 12.9 / 14.4   32768: 16.1 / 15.0   65536: 25.2 / 21.6   200000: 63 / 49
+//   128 experts, k = 1   20480: 10.9 / 13.8   32768: 13.4 / 13.9   65536: 19.7 / 20.5   200000: 47 / 45
+//   160 experts, k = 8   20480: 14.5 / 14.4   32768: 18.6 / 15.0   65536: 28.9 / 21.6   200000: 75 / 49
+//   256 experts, k = 8   20480: 16.4 / 16.8   32768: 21.6 / 18.2   65536: 34.5 / 29.9   200000: 92 / 78
+//   64 experts, k = 8    20480: 11.9 / 11.9   32768: 14.5 / 12.8   65536: 21.7 / 17.0   200000: 53 / 37
+constexpr int kRtLaneTokens = 32768;
+
+bool router_lanes(const RouterFwd& a, int32_t dtype) {
+  return dtype != TM_F32 && a.k <= 8 && a.T >= kRtLaneTokens && a.E % 8 == 0 && a.ld % 8 == 0 &&
+         ((uintptr_t)a.logits) % 16 == 0;
+}
+
+template <int V, typename T>
+cudaError_t router_lanes_launch(const RouterFwd& a, cudaLaunchConfig_t cfg, int csize) {
+  auto kern = k_router_fwd_lanes<V, T>;
+  constexpr int kMost = kRtLaneWarps * 32 * 16 * (kMaxExperts / 8 | 1);
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (attr != cudaSuccess) return attr;
+  cfg.blockDim = dim3(32 * kRtLaneWarps);
+  cfg.dynamicSmemBytes = (size_t)kRtLaneWarps * 32 * 16 * (a.E / 8 | 1);
+  return cudaLaunchKernelEx(&cfg, kern, a, csize, FastDiv((uint32_t)(a.E / 8)));
+}
+
 size_t router_ws_bytes(int T, int E) {
   const int n = router_grid(T).clusters;
   return n > 1 ? (size_t)n * ((size_t)E * 8 + 8) : 0;
@@ -670,7 +889,11 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   }
   cudaStream_t st = (cudaStream_t)stream;
   RouterFwd a{logits, ld, mask, T, E, k, ids, w, lse, counts, prob, losses, tokens, nullptr, nullptr, nullptr, nullptr};
-  const int clusters = router_grid(T).clusters, csize = router_grid(T).csize;
+  const bool lanes = router_lanes(a, dtype);
+  const int csize = router_grid(T).csize;
+  int clusters = router_grid(T).clusters;
+  // (32 tokens a warp, spread over the CTAs; rows of more than 208 experts leave room for one CTA an SM)
+  if (lanes) clusters = std::min(std::min(clusters, E > 208 ? kRtMaxClusters / 2 : kRtMaxClusters), ((T + 31) / 32 + 1) / 2);
   a.part_prob = static_cast<float*>(workspace);
   a.part_counts = reinterpret_cast<int32_t*>(a.part_prob + (size_t)clusters * E);
   a.part_z = reinterpret_cast<float*>(a.part_counts + (size_t)clusters * E);
@@ -687,7 +910,9 @@ tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t 
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim = {(unsigned)csize, 1, 1};
   cudaError_t e = by_pairs(dtype, E, logits, ld, nullptr, [&](auto elem, auto pair) {
+    using T16 = std::conditional_t<std::is_same<decltype(elem), __half>::value, __half, __nv_bfloat16>;
     return by_width(E, [&](auto v) {
+      if (lanes) return router_lanes_launch<decltype(v)::value, T16>(a, cfg, csize);
       return cudaLaunchKernelEx(&cfg, k_router_fwd<decltype(v)::value, decltype(elem), decltype(pair)::value>, a, csize);
     });
   });
