@@ -91,10 +91,10 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
 //   dense 4096 x 4096   T = 1: 6.8 / 7.8   4: 7.3 / 7.8   8: 9.4 / 7.8   16: 12.4 / 7.8
 //   dense 1024 x 1024   T = 1: 3.8 / 5.2   4: 4.2 / 5.2   8: 5.3 / 5.2   16: 6.8 / 5.2
 //   dense 5120 x 1536   T = 1: 5.2 / 5.8   4: 5.8 / 5.8   8: 8.2 / 5.8
-//   128 experts, gated 1024 -> 512    64 routes: 7.7 / 12.5   128: 10.9 / 14.4   192: 13.9 / 14.4   256: 17.0 / 14.5
-//   128 experts, 512 -> 1024          64 routes: 7.3 / 10.8   128: 11.2 / 12.4   192: 17.0 / 13.4
+//   128 experts, gated 1024 -> 512    64 routes: 7.1 / 10.9   128: 10.9 / 12.4   192: 13.9 / 12.4   256: 17.0 / 12.4
+//   128 experts, 512 -> 1024          64 routes: 7.3 / 8.9    128: 11.2 / 10.8   192: 17.0 / 11.8
 //   8 experts, gated 1024 -> 1024     16 routes: 7.3 / 8.8    32: 10.3 / 8.8
-//   160 experts, 1536 -> 5120         16 routes: 13.9 / 18.0  32: 26.1 / 26.0    64: 47.8 / 40.7
+//   160 experts, 1536 -> 5120         16 routes: 14.0 / 16.0  32: 26.1 / 24.2    64: 47.8 / 40.2
 // Hence, dense, up to 8 pieces (rows times stages) for a CTA to quantise, where
 // the times are equal and the second launch's cost to the host is saved; by
 // expert few rows each on average, and no more CTAs than a few waves.

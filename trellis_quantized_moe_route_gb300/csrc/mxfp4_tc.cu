@@ -18,16 +18,16 @@
 // (gated: 4 x 112).
 //
 // Measured on one GB300 (bf16 in and out, whole call with quantisation and map):
-//   2048 x 4096 x 4096 dense        23 us   2.98 PFLOP/s over the call. The
+//   2048 x 4096 x 4096 dense        20 us   3.4 PFLOP/s over the call. The
 //     issuer spends 503 cycles on a stage (four 128 x 240 x 64 MMAs, 15.6 K
 //     multiply-adds a cycle), which is what the tensor pipe takes; while an
 //     epilogue reads the other buffer a stage takes 1100. Quantisation and
-//     launches are 9 us of the call, the pipeline's start and last drain 3 us.
-//   2048 tokens x 8 of 128 experts, gated 1024 -> 512, Zipf   31 us: map and
-//     quantisation 13 us, then 49 KB a stage at 55-65 bytes a cycle and SM from
+//     launches are 7 us of the call, the pipeline's start and last drain 3 us.
+//   2048 tokens x 8 of 128 experts, gated 1024 -> 512, Zipf   26 us: map and
+//     quantisation 7 us, then 49 KB a stage at 55-65 bytes a cycle and SM from
 //     L2 and an epilogue of the same length (silu: two special-function
 //     instructions a value).
-//   4096 tokens x 8 of 160 experts, 1536 -> 5120   190 us: 1.03 GB of weights and
+//   4096 tokens x 8 of 160 experts, 1536 -> 5120   189.5 us: 1.03 GB of weights and
 //     results in 155 us = 6.6 TB/s in the products, at the memory's rate.
 // Timing copies without the MMAs, the stores or the loads each take as long or
 // 2-3 us less in the first two: the three overlap.
@@ -439,13 +439,13 @@ __global__ void __launch_bounds__(256) k_mx_weight_scales(const uint8_t* __restr
 // thread clears the error word. By expert: the route map is the kernel before
 // this one in the stream, and it lets this one start only after it has itself
 // waited for all that came before it, so x may be read, and quantised, while
-// the map is being made; only the slots wait for it.
+// the map is being made; only the slots wait for it. 2048 x 4096 bf16: 4 us;
+// 32768 x 1536: 24 us = 5.3 TB/s, bound by its instructions and the memory alike.
 constexpr int kRqUnroll = 4;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, VEC && sizeof(T) == 2 ? 8 : 5)
-    k_mx_rows_quantize(const MxQuantArgs a, int stages, int per, FastDiv segs,
-                                                          FastDiv bn, int items) {
+    k_mx_rows_quantize(const MxQuantArgs a, int stages, int per, FastDiv segs, FastDiv bn, int items) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
   if (!a.slot_of_route || i >= items) grid_wait();
@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(256, VEC && sizeof(T) == 2 ? 8 : 5)
   static_assert(kRqUnroll == 4, "a lane of four for a stage");
   {
     const bool odd = lane & 1, high = lane & 2;
-    uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? q[0] : q[1], 1), x1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? q[2] : q[3], 1);
+    uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? q[0] : q[1], 1);
+    uint32_t x1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? q[2] : q[3], 1);
     (odd ? q[0] : q[1]) = x0;
     (odd ? q[2] : q[3]) = x1;
     x0 = __shfl_xor_sync(0xFFFFFFFFu, high ? q[0] : q[2], 2);
@@ -519,13 +520,11 @@ __global__ void __launch_bounds__(256, VEC && sizeof(T) == 2 ? 8 : 5)
       *reinterpret_cast<uint4*>(a.codes + ((size_t)slot * nb + s0 * 8 + lane) * 16) =
           make_uint4(q[0], q[1], q[2], q[3]);
     if (scale_on)
-      *reinterpret_cast<uint32_t*>(a.scales + ((((size_t)b * stages + s0 + (lane & 3)) * 2 + (lane >> 4)) * a.nrb + (t >> 7)) * 512 +
-                                   (t & 31) * 16 + ((t & 127) >> 5) * 4) = word;
+      *reinterpret_cast<uint32_t*>(
+          a.scales + ((((size_t)b * stages + s0 + (lane & 3)) * 2 + (lane >> 4)) * a.nrb + (t >> 7)) * 512 +
+          (t & 31) * 16 + ((t & 127) >> 5) * 4) = word;
   }
 }
-
-// 2048 x 4096 bf16: 4 us; 32768 x 1536: 23 us = 5.6 TB/s, bound by its
-// instructions and the memory alike.
 
 // Route map for the block kernel, by one cluster of kMapCtas CTAs: every CTA
 // counts its part of the routes by expert in shared memory, reads the others'
