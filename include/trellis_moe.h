@@ -378,8 +378,8 @@ typedef enum { TM_F32 = 0, TM_BF16 = 1, TM_F16 = 2 } tm_dtype;
  * The mask keeps padding out of the statistics and losses; it does not change
  * the token's own ids, w and lse. A token whose logits are all -inf gets ids
  * 0..k-1, w 0 and lse -inf. logits: row t at logits + t * ld elements, ld >= E;
- * 1 <= E <= 256, 1 <= k <= min(E, 32). Nothing is summed by atomics: equal
- * inputs give equal bits. workspace: trellis_moe_router_workspace_size bytes
+ * T <= 2^30, 1 <= E <= 256, 1 <= k <= min(E, 32). Sums are taken in a fixed
+ * order: equal calls give equal bits. workspace: trellis_moe_router_workspace_size bytes
  * (0 for few tokens: then NULL will do), 16-byte aligned, contents ignored. T = 0 writes the statistics of no tokens. */
 size_t trellis_moe_router_workspace_size(int32_t T, int32_t E);
 tm_status trellis_moe_router_forward(const void* logits, int32_t dtype, int64_t ld, const uint8_t* mask, int32_t T,
@@ -399,7 +399,8 @@ tm_status trellis_moe_router_backward(const void* logits, int32_t dtype, int64_t
 /* ------------------------------------------------------------------------
  * Weighted combine of rows in route order (r = t * k + j, as
  * trellis_moe_mxfp4_forward_experts writes them): out[t] = sum_j w[t, j]
- * rows[t * k + j], fp32, in order j; a route of weight 0 is left out. 1 <= k <= 32. */
+ * rows[t * k + j], fp32, in order j; a route of weight 0 is left out. 1 <= k <= 32,
+ * 1 <= H <= 2^30. */
 tm_status trellis_moe_combine_forward(const void* rows, int32_t dtype, const float* w, int32_t T, int32_t k,
                                       int32_t H, float* out, void* stream);
 

@@ -134,3 +134,17 @@ def test_tuning_entry_points_validate_without_gpu(lib):
     assert lib.trellis_moe_mxfp4_set_wait_test(None, 0, 0) == -1
     assert lib.trellis_moe_mxfp4_workspace_size(None, 4) == 0
     lib.trellis_moe_mxfp4_destroy(None)
+
+
+def test_tuning_sizes_end_below_32_bits(lib):
+    """Sizes at which an index of 32 bits could pass its end are refused before any launch."""
+    P = ctypes.c_void_p
+    err = lib.trellis_moe_last_error
+    for T in ((1 << 30) + 1, (1 << 31) - 1):
+        assert lib.trellis_moe_router_forward(P(16), 0, 8, None, T, 8, 2, P(16), P(16), P(16), P(16), P(16), P(16), P(16),
+                                              P(16), 1 << 40, None) == -2 and b"T=" in err()
+        assert lib.trellis_moe_router_backward(P(16), 0, 8, None, T, 8, 2, None, None, P(16), P(16), P(16), None, None,
+                                               P(16), None) == -2
+    for H in ((1 << 30) + 1, (1 << 31) - 1):
+        assert lib.trellis_moe_combine_forward(P(16), 0, P(16), 1, 1, H, P(16), None) == -2 and b"H=" in err()
+        assert lib.trellis_moe_combine_backward(P(16), 0, P(16), P(16), 1, 1, H, P(16), P(16), None) == -2

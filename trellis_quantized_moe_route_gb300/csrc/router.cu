@@ -848,6 +848,7 @@ tm_status router_check(const char* what, const void* logits, int32_t dtype, int6
                        int32_t k) {
   if (!dtype_ok(dtype)) return status_fail(TM_EINVAL, "%s: dtype=%d is not a tm_dtype", what, dtype);
   if (T < 0) return status_fail(TM_EINVAL, "%s: T=%d < 0", what, T);
+  if (T > 1 << 30) return status_fail(TM_EUNSUPPORTED, "%s: T=%d is more than %d", what, T, 1 << 30);
   if (E < 1 || E > kMaxExperts) return status_fail(TM_EUNSUPPORTED, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
   if (k < 1 || k > 32 || k > E) return status_fail(TM_EINVAL, "%s: k=%d outside 1..min(E,32)", what, k);
   if (ld < E) return status_fail(TM_EINVAL, "%s: ld=%lld is less than E=%d", what, (long long)ld, E);
@@ -866,7 +867,7 @@ using namespace tmoe;
 extern "C" {
 
 size_t trellis_moe_router_workspace_size(int32_t T, int32_t E) {
-  if (T < 0 || E < 1 || E > kMaxExperts) return 0;
+  if (T < 0 || T > 1 << 30 || E < 1 || E > kMaxExperts) return 0;
   return router_ws_bytes(T, E);
 }
 
