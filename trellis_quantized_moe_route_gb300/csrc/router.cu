@@ -170,6 +170,16 @@ struct RowRegs {
     const uint16_t h = (uint16_t)(raw[i >> 1] >> (16 * (i & 1)));
     return to_f32(*reinterpret_cast<const T*>(&h));
   }
+  // The row's largest logit, NaN if there is one (fp32). Beside the selection, so
+  // that the probabilities need not wait for it: with the first selected one read
+  // again in its place, 8 x 128 takes 3.3 us instead of 3.1, and 65536 x 160
+  // 34.5 instead of 35.0.
+  __device__ __forceinline__ float largest() const {
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) k = max(k, Order<float>::key(__uint_as_float(raw[i])));
+    return Order<float>::value(__reduce_max_sync(0xFFFFFFFFu, k));
+  }
   // Unique keys: the logit's order, then the lower expert.
   __device__ __forceinline__ void keys(uint32_t (&key)[V]) const {
     if (sizeof(T) == 4) {
@@ -447,9 +457,10 @@ __global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, in
     uint32_t id = ~Order<T>::kMask - (mine & ~Order<T>::kMask);
     const T* src = logits + (size_t)t * a.ld;
     if (sizeof(T) == 4 && !sure) id = router_select_exact<V>(reinterpret_cast<const float*>(src), a.k, a.E);
-    // any value near the largest serves as the softmax's offset: fp32's lacks its low bits
+    // The softmax's offset is the row's largest logit to the last bit: fp32's key
+    // lacks the low ones, which are worth thousands where logits are of 1e9.
     const bool some = first > Order<T>::kNone;
-    const float m = Order<T>::value(first & Order<T>::kMask);
+    const float m = sizeof(T) == 4 ? now.largest() : Order<T>::value(first & Order<T>::kMask);
     float my_l = 0.0f;
     if (lane < a.k) my_l = sizeof(T) == 4 ? to_f32(src[id]) : Order<T>::value(mine & Order<T>::kMask);
     float p[V], total = 0.0f;
