@@ -71,7 +71,8 @@ def backward(logits, k: int, mask, fwd, grad_w, grad_losses):
         if fwd["lse"][t] == -np.inf:
             continue
         if mask is None or mask[t]:
-            p = np.exp(l[t] - fwd["lse"][t])
+            p = np.exp(l[t] - l[t].max())       # (not through lse, which 1e30 leaves without its fraction)
+            p /= p.sum()
             a, b = grad_losses[0] * E / n, 2 * grad_losses[1] / n * fwd["lse"][t]
             d[t] += p * (a * (f - np.sum(f * p)) + b)
             mag[t] += p * (abs(a) * (f + np.sum(f * p)) + abs(b))

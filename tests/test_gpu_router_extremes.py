@@ -83,3 +83,27 @@ def test_large_logits_in_masked_tokens_stay_there(binding, dtype):
     assert torch.allclose(r.prob, clean.prob, rtol=REL, atol=0) and torch.allclose(r.losses, clean.losses, rtol=4 * REL, atol=0)
     f = router.forward(host(l), 6, None)
     assert np.array_equal(host(r.ids), f["ids"]) and (np.abs(host(r.w) - f["w"]) <= REL * f["w"] + 1e-37).all()
+
+
+@pytest.mark.parametrize("E,k,dtype", CASES)
+def test_large_logits_backward(binding, E, k, dtype):
+    """Both losses and the weights; lse alone, rounded to fp32, does not give the probabilities here."""
+    l = large_logits(E, dtype, E + k)
+    T = l.shape[0]
+    f = router.forward(host(l), k, None)
+    r = binding.router_forward(l.cuda(), k)
+    gw = np.random.default_rng(k).standard_normal((T, k)).astype(np.float32)
+    for gl in ((0.7, 0.0), (0.7, 1e-6)):
+        want, mag = router.backward(host(l), k, None, f, gw, gl)
+        got = host(binding.router_backward(l.cuda(), r, torch.from_numpy(gw).cuda(), torch.tensor(gl, device="cuda")))
+        assert (np.abs(got - want) <= 4 * REL * mag + HALF_ULP[dtype] * np.abs(want) + SMALLEST[dtype]).all()
+
+
+def test_balance_gradient_of_equal_logits_sums_to_zero(binding):
+    """p (f - sum f p) over the experts, for rows whose log k is lost in lse."""
+    for v in (0.0, 1e5, -1e9, 1e30):
+        l = torch.full((8, 16), v, device="cuda")
+        g = binding.router_backward(l, binding.router_forward(l, 4), None, torch.tensor([1.0, 0.0], device="cuda"))
+        # per token 16 / 8 * (1 / 16) (f_e - 1 / 16) with f = 1 / 4 for the first four
+        want = torch.tensor([0.125 * 3 / 16] * 4 + [-0.125 / 16] * 12, device="cuda")
+        assert torch.allclose(g, want.expand(8, 16), rtol=4 * REL, atol=0)

@@ -752,6 +752,22 @@ __global__ void __launch_bounds__(256, kRtBwdCtas) k_router_bwd(RouterBwd a) {
       s += f[i] * p[i];
     }
     s = warp_sum(s);
+    // lse is rounded, which makes all of p wrong by one factor: up to 1 + |lse|
+    // 2^-24, and as much as the number of the logits where these are so large that
+    // its logarithm is lost in lse. Their sum, which should be 1, takes it out
+    // where that is above the exponents' own rounding (fp32) or an eighth of the
+    // result's (16 bits: lse is within 2^-15 up to 1024). 65536 x 160 bf16: 15.5
+    // us, with the sum for every token 16.9, and with the warp not known to agree
+    // (no vote) 15.9.
+    if (__any_sync(0xFFFFFFFFu, on && fabsf(in.lse) > (sizeof(T) == 4 ? 16.0f : 1024.0f))) {
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) total += p[i];
+      const float r = __fdividef(1.0f, warp_sum(total));
+      s *= r;
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] *= r;
+    }
     const int id = in.id >= 0 && in.id < a.E ? in.id : -1;
     if (a.grad_w) {
       // (a weight of zero gets no gradient whatever comes from above, and a
