@@ -107,3 +107,48 @@ def test_balance_gradient_of_equal_logits_sums_to_zero(binding):
         # per token 16 / 8 * (1 / 16) (f_e - 1 / 16) with f = 1 / 4 for the first four
         want = torch.tensor([0.125 * 3 / 16] * 4 + [-0.125 / 16] * 12, device="cuda")
         assert torch.allclose(g, want.expand(8, 16), rtol=4 * REL, atol=0)
+
+
+NAN = {"f32": (np.uint32, [0x7FC00000, 0xFFC00000, 0xFFFFFFFF, 0xFF800001]), "bf16": (np.uint16, [0x7FC0, 0xFFC0, 0xFFFF, 0xFF81]),
+       "f16": (np.uint16, [0x7E00, 0xFE00, 0xFFFF, 0xFC01])}
+
+
+def from_bits(bits, dtype):
+    return torch.from_numpy(bits.view(np.int32 if bits.itemsize == 4 else np.int16)).view(DT[dtype])
+
+
+@pytest.mark.parametrize("E,k", [(40, 40 - 8), (96, 32), (7, 7)])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_nan_of_either_sign(binding, E, k, dtype):
+    """Selected before all numbers, by expert, whatever their sign; in masked tokens they stay there."""
+    rng = np.random.default_rng(E)
+    kind, nans = NAN[dtype]
+    T = 60
+    bits = (1.5 * torch.randn(T, E)).to(DT[dtype]).view(torch.int32 if kind is np.uint32 else torch.int16).numpy().view(kind)
+    is_nan = rng.random((T, E)) < 0.3
+    is_nan[T - 5:] = True                            # (whole rows, the matrix's last one among them)
+    bits = np.where(is_nan, rng.choice(np.array(nans, dtype=kind), (T, E)), bits)
+    bits[T - 1] = nans[1]
+    l = from_bits(np.ascontiguousarray(bits), dtype)
+    l[0] = torch.from_numpy(1.5 * rng.standard_normal(E)).to(DT[dtype])
+    is_nan[0] = False
+    mask = torch.from_numpy(~is_nan.any(1)).cuda()
+    assert int(mask.sum()) >= 1
+    r = binding.router_forward(l.cuda(), k, mask=mask)
+    ids = host(r.ids)
+    key = np.where(is_nan, np.inf, host(torch.nan_to_num(l.float())))
+    assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
+    clean = binding.router_forward(l.cuda()[mask], k)
+    assert torch.equal(r.counts, clean.counts) and torch.equal(r.tokens, clean.tokens)
+    assert torch.allclose(r.prob, clean.prob, rtol=REL, atol=0) and torch.allclose(r.losses, clean.losses, rtol=4 * REL, atol=0)
+
+
+def test_nan_of_either_sign_with_many_tokens(binding):
+    T, E, k = 32800, 40, 8
+    nans = np.array(NAN["bf16"][1], dtype=np.uint16)
+    l = torch.randn(T, E).bfloat16()
+    l[T - 3:] = from_bits(np.random.default_rng(0).choice(nans, (3, E)), "bf16")
+    mask = torch.arange(T) < T - 3
+    r, clean = binding.router_forward(l.cuda(), k, mask=mask.cuda()), binding.router_forward(l[: T - 3].cuda(), k)
+    assert torch.equal(r.ids[T - 3:].cpu(), torch.arange(k, dtype=torch.int32).expand(3, k))
+    assert torch.equal(r.counts, clean.counts) and torch.isfinite(r.losses).all()

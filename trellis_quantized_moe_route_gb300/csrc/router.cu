@@ -49,7 +49,10 @@ constexpr int kRtBwdCtas = 5;         // CTAs of 256 threads that an SM holds of
 constexpr int kRtMaxClusters = 152;  // of two CTAs each: two CTAs of 512 threads on each of 152 SMs
 
 // Orderable bits of a logit (larger value, larger bits; -0 as +0), in the upper
-// kBits of a word, and back. kNone: the largest such word for -inf.
+// bits of a word, and back. kNone: the largest such word for -inf. Every key is
+// made after an addition of +0, here or in add_zero: it turns -0 into +0 and a
+// NaN of either sign into the positive one, whose key is above all others. So
+// nothing in a row lies below -inf, and no absent expert before a real one.
 template <typename T>
 struct Order;
 template <>
@@ -195,7 +198,7 @@ struct RowRegs {
       }
     }
   }
-  // -0 becomes +0
+  // -0 becomes +0, a NaN the positive one (see Order)
   static __device__ __forceinline__ uint32_t add_zero(uint32_t w) {
     if (std::is_same<T, __nv_bfloat16>::value) {
       const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.0f));
