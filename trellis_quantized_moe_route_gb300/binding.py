@@ -464,6 +464,10 @@ class TrellisLinear:
 
 # ---------------------------------------------------------------------------
 # Router losses, route combine and MXFP4 (device tensors in, device tensors out)
+#
+# A call runs on the current stream, or on its `stream` argument, and its results
+# are allocated there. As anywhere in torch, a tensor that another stream brings
+# or takes has to be complete there first, and not freed before.
 # ---------------------------------------------------------------------------
 _dtype_codes: dict = {}
 
@@ -497,15 +501,25 @@ def _start():
     return load_library()
 
 
-def _launch(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current; raises on an error status."""
+def _launch(fn, index, *args):
+    """fn(*args, current stream) with device `index` current; raises on an error status."""
     if index == _device_now():
-        status = fn(*args, _stream_of(index) if stream is None else stream.cuda_stream)
+        status = fn(*args, _stream_of(index))
     else:
         with _torch().cuda.device(index):
-            status = fn(*args, _stream_of(index) if stream is None else stream.cuda_stream)
+            status = fn(*args, _stream_of(index))
     if status != TM_OK:
         _check(status)
+
+
+def _given(stream, name, t):
+    """Makes a call's `stream` argument the current stream, for its launches
+    and for what it allocates: memory of another stream's pool could still be in
+    use there, or be handed out again there while the call runs."""
+    torch = _torch()
+    if stream.device != t.device:
+        raise ValueError("stream is on %s, %s on %s" % (stream.device, name, t.device))
+    return torch.cuda.stream(stream)
 
 
 def _on_device(name, t, dtype=None, shape=None, contiguous=True):
@@ -572,6 +586,9 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
     """Router with load statistics and losses on device logits [T, E] (float32,
     bfloat16 or float16; rows may lie apart); mask: bool or uint8 [T], false
     for padding."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return router_forward(logits, k, mask)
     lib = _start()
     T, E, ld = _rows_2d("logits", logits)
     dev, k = logits.device, int(k)
@@ -581,7 +598,7 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
     ids, counts, tokens = _empty((T, kk), dtype=_i32, device=dev), _empty(E, dtype=_i32, device=dev), _empty(1, dtype=_i32, device=dev)
     w, lse = _empty((T, kk), dtype=_f32, device=dev), _empty(T, dtype=_f32, device=dev)
     prob, losses = _empty(E, dtype=_f32, device=dev), _empty(2, dtype=_f32, device=dev)
-    _launch(lib.trellis_moe_router_forward, logits.get_device(), stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+    _launch(lib.trellis_moe_router_forward, logits.get_device(), logits.data_ptr(), _dtype_code(logits.dtype), ld,
             None if mask is None else _mask(mask, T), T, E, k, ids.data_ptr(), w.data_ptr(), lse.data_ptr(),
             counts.data_ptr(), prob.data_ptr(), losses.data_ptr(), tokens.data_ptr(), _opt(ws), wsb)
     return RouterOut(ids, w, lse, counts, prob, losses, tokens)
@@ -590,6 +607,9 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
 def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=None, out=None, stream=None):
     """Gradient of the logits from grad_w [T, k] and grad_losses [2] (float32,
     on the device, either may be None); fwd and mask as in the forward call."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return router_backward(logits, fwd, grad_w, grad_losses, mask, out)
     lib = _start()
     T, E, ld = _rows_2d("logits", logits)
     k = fwd.ids.shape[1]
@@ -605,7 +625,7 @@ def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=
         out = _empty((T, E), dtype=logits.dtype, device=logits.device)
     else:
         _on_device("out", out, logits.dtype, (T, E))
-    _launch(lib.trellis_moe_router_backward, logits.get_device(), stream, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+    _launch(lib.trellis_moe_router_backward, logits.get_device(), logits.data_ptr(), _dtype_code(logits.dtype), ld,
             mp, T, E, k, fwd.ids.data_ptr(), fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(),
             fwd.tokens.data_ptr(), _opt(grad_w), _opt(grad_losses), out.data_ptr())
     return out
@@ -626,25 +646,31 @@ def _route_rows(rows, w):
 def combine(rows, w, out=None, stream=None):
     """out [T, H] float32 = sum_j w[t, j] rows[t * k + j] for rows [T * k, H] in
     route order and w float32 [T, k]."""
+    if stream is not None:
+        with _given(stream, "rows", rows):
+            return combine(rows, w, out)
     lib = _start()
     T, k, H = _route_rows(rows, w)
     if out is None:
         out = _empty((T, H), dtype=_f32, device=rows.device)
     else:
         _on_device("out", out, _f32, (T, H))
-    _launch(lib.trellis_moe_combine_forward, rows.get_device(), stream, rows.data_ptr(), _dtype_code(rows.dtype),
+    _launch(lib.trellis_moe_combine_forward, rows.get_device(), rows.data_ptr(), _dtype_code(rows.dtype),
             w.data_ptr(), T, k, H, out.data_ptr())
     return out
 
 
 def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = True, stream=None):
     """(grad_rows of the rows' type, grad_w float32) of combine; None where not wanted."""
+    if stream is not None:
+        with _given(stream, "rows", rows):
+            return combine_backward(rows, w, grad_out, want_rows, want_w)
     lib = _start()
     T, k, H = _route_rows(rows, w)
     _on_device("grad_out", grad_out, _f32, (T, H))
     grows = _torch_mod.empty_like(rows) if want_rows else None
     gw = _torch_mod.empty_like(w) if want_w else None
-    _launch(lib.trellis_moe_combine_backward, rows.get_device(), stream, rows.data_ptr(), _dtype_code(rows.dtype),
+    _launch(lib.trellis_moe_combine_backward, rows.get_device(), rows.data_ptr(), _dtype_code(rows.dtype),
             w.data_ptr(), grad_out.data_ptr(), T, k, H, _opt(grows), _opt(gw))
     return grows, gw
 
@@ -652,18 +678,24 @@ def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = T
 def mxfp4_quantize(x, stream=None):
     """Rows of x [rows, K] (float32, bfloat16 or float16; rows may lie apart) ->
     (codes uint8 [rows, 16 B], scales uint8 [rows, B]), B = ceil(K / 32)."""
+    if stream is not None:
+        with _given(stream, "x", x):
+            return mxfp4_quantize(x)
     lib = _start()
     rows, K, ld = _rows_2d("x", x)
     B, dev = (K + 31) // 32, x.device
     codes = _empty((rows, 16 * B), dtype=_u8, device=dev)
     scales = _empty((rows, B), dtype=_u8, device=dev)
-    _launch(lib.trellis_moe_mxfp4_quantize, x.get_device(), stream, x.data_ptr(), _dtype_code(x.dtype), ld, rows, K,
+    _launch(lib.trellis_moe_mxfp4_quantize, x.get_device(), x.data_ptr(), _dtype_code(x.dtype), ld, rows, K,
             codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
     """Values [rows, K] of MXFP4 codes [rows, 16 B] and scales [rows, B]."""
+    if stream is not None:
+        with _given(stream, "codes", codes):
+            return mxfp4_dequantize(codes, scales, K, dtype, out)
     lib = _start()
     K = int(K)
     B = (K + 31) // 32
@@ -678,7 +710,7 @@ def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
         out = _empty((rows, K), dtype=dtype, device=codes.device)
     else:
         _on_device("out", out, dtype, (rows, K))
-    _launch(lib.trellis_moe_mxfp4_dequantize, codes.get_device(), stream, codes.data_ptr(), scales.data_ptr(), rows, K,
+    _launch(lib.trellis_moe_mxfp4_dequantize, codes.get_device(), codes.data_ptr(), scales.data_ptr(), rows, K,
             out.data_ptr(), code)
     return out
 
@@ -761,9 +793,12 @@ class MxFp4Linear(_MxFp4):
     def forward(self, x, out=None, out_dtype=None, stream=None):
         """x [T, K] (float32, bfloat16 or float16; rows may lie apart) -> [T, N]
         of out_dtype (default float32)."""
+        if stream is not None:
+            with _given(stream, "x", x):
+                return self.forward(x, out, out_dtype)
         T, _, ld = _rows_2d("x", x)
         out, code = self._output(T, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward, self.index, stream, self.handle, x.data_ptr(), _dtype_code(x.dtype),
+        _launch(self.lib.trellis_moe_mxfp4_forward, self.index, self.handle, x.data_ptr(), _dtype_code(x.dtype),
                 ld, T, out.data_ptr(), code, self.workspace_ptr, self.workspace_bytes)
         return out
 
@@ -779,6 +814,9 @@ class MxFp4Experts(_MxFp4):
     def forward(self, x, ids, per_route: bool = False, out=None, out_dtype=None, stream=None):
         """x [T, K] (per_route: [T * topk, K]) and ids int32 [T, topk] -> rows
         [T * topk, N] in route order, of out_dtype (default float32)."""
+        if stream is not None:
+            with _given(stream, "x", x):
+                return self.forward(x, ids, per_route, out, out_dtype)
         rows, _, ld = _rows_2d("x", x)
         T, topk = ids.shape[0], self.topk
         _on_device("ids", ids, _i32, (T, topk))
@@ -786,7 +824,7 @@ class MxFp4Experts(_MxFp4):
         if rows != need:
             raise ValueError("x must have %d rows, not %d" % (need, rows))
         out, code = self._output(T * topk, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.index, stream, self.handle, x.data_ptr(),
+        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.index, self.handle, x.data_ptr(),
                 _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T, topk, out.data_ptr(), code,
                 self.workspace_ptr, self.workspace_bytes)
         return out
