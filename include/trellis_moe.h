@@ -34,6 +34,9 @@
  *     the current CUDA device, owned by the caller, never freed by the library.
  *   - "fp16" / "bf16" arrays are passed as uint16_t bit patterns.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
+ *   - Calls that share a workspace must not overlap on the GPU: order them on
+ *     one stream or by events, and let no two threads issue them at once (a call
+ *     is several launches).
  *   - Every argument is validated on the host before any launch; a call that
  *     returns an error has launched nothing and written nothing.
  *   - Errors: a negative tm_status; trellis_moe_last_error() gives a message

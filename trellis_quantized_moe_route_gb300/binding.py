@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Any, NamedTuple, Optional
 
 import numpy as np
@@ -717,7 +718,11 @@ def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
 
 class _MxFp4:
     """One prepared set of MXFP4 matrices: codes uint8 [E, R, 16 B] and scales
-    uint8 [E, R, B] on the device (kept alive here)."""
+    uint8 [E, R, B] on the device (kept alive here), with one workspace. Calls
+    that share it run one after the other: one on another stream than the last
+    waits for that one, and threads take turns. Handles of their own let calls
+    overlap. Of calls captured in a CUDA graph only the capture is seen here: a
+    replay has to be ordered with the handle's other calls by its user."""
 
     def __init__(self, codes, scales, K: int, max_rows: int, gated: bool):
         torch = _torch()
@@ -742,6 +747,26 @@ class _MxFp4:
         off = (-self.workspace.data_ptr()) % 256
         self.workspace = self.workspace[off:off + self.workspace_bytes]
         self.workspace_ptr = self.workspace.data_ptr()
+        self._lock = threading.Lock()
+        self._stream = torch.cuda.current_stream(self.device)  # of the last call
+        self._raw = self._stream.cuda_stream
+
+    def _follow(self):
+        """Makes the current stream wait for the last call's, if that is another one."""
+        torch = _torch()
+        now, last = torch.cuda.current_stream(self.device), self._stream
+        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(last):
+            same = torch.cuda.is_current_stream_capturing() == capturing
+        if same:  # (a capture cannot wait for what runs outside it, nor what runs for a capture)
+            now.wait_stream(last)
+        self._stream, self._raw = now, now.cuda_stream
+
+    def _run(self, fn, *args):
+        with self._lock:
+            if _stream_of(self.index) != self._raw:
+                self._follow()
+            _launch(fn, self.index, self.handle, *args, self.workspace_ptr, self.workspace_bytes)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -755,10 +780,15 @@ class _MxFp4:
             pass
 
     def poll_error(self, stream=None) -> int:
+        if stream is not None:
+            with _given(stream, "the weights", self):
+                return self.poll_error()
         flags = ctypes.c_uint32(0)
-        with _torch().cuda.device(self.device):
-            st = self.lib.trellis_moe_mxfp4_poll_error(self.handle, _ptr(self.workspace), ctypes.byref(flags),
-                                                       _raw_stream(stream))
+        with self._lock, _torch().cuda.device(self.device):
+            if _stream_of(self.index) != self._raw:
+                self._follow()
+            st = self.lib.trellis_moe_mxfp4_poll_error(self.handle, self.workspace_ptr, ctypes.byref(flags),
+                                                       _stream_of(self.index))
         if st not in (TM_OK, -5):
             _check(st)
         return int(flags.value)
@@ -798,8 +828,7 @@ class MxFp4Linear(_MxFp4):
                 return self.forward(x, out, out_dtype)
         T, _, ld = _rows_2d("x", x)
         out, code = self._output(T, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward, self.index, self.handle, x.data_ptr(), _dtype_code(x.dtype),
-                ld, T, out.data_ptr(), code, self.workspace_ptr, self.workspace_bytes)
+        self._run(self.lib.trellis_moe_mxfp4_forward, x.data_ptr(), _dtype_code(x.dtype), ld, T, out.data_ptr(), code)
         return out
 
 
@@ -824,7 +853,6 @@ class MxFp4Experts(_MxFp4):
         if rows != need:
             raise ValueError("x must have %d rows, not %d" % (need, rows))
         out, code = self._output(T * topk, x, out, out_dtype)
-        _launch(self.lib.trellis_moe_mxfp4_forward_experts, self.index, self.handle, x.data_ptr(),
-                _dtype_code(x.dtype), ld, 1 if per_route else 0, ids.data_ptr(), T, topk, out.data_ptr(), code,
-                self.workspace_ptr, self.workspace_bytes)
+        self._run(self.lib.trellis_moe_mxfp4_forward_experts, x.data_ptr(), _dtype_code(x.dtype), ld,
+                  1 if per_route else 0, ids.data_ptr(), T, topk, out.data_ptr(), code)
         return out
