@@ -523,12 +523,15 @@ def _given(stream, name, t):
     return torch.cuda.stream(stream)
 
 
-def _on_device(name, t, dtype=None, shape=None, contiguous=True):
-    """Checks one tensor argument; returns it (None passes)."""
+def _on_device(name, t, index, dtype=None, shape=None, contiguous=True):
+    """Checks one tensor argument, on CUDA device `index` (None: any); returns
+    it (None passes)."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    if index is not None and t.get_device() != index:
+        raise ValueError("%s is on cuda:%d, the call's first argument on cuda:%d" % (name, t.get_device(), index))
     if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if shape is not None and t.shape != shape:
@@ -559,10 +562,10 @@ def _rows_2d(name, t):
     return rows, cols, ld
 
 
-def _mask(mask, T):
+def _mask(mask, index, T):
     if mask is None:
         return None
-    _on_device("mask", mask, shape=(T,))
+    _on_device("mask", mask, index, shape=(T,))
     if mask.dtype not in (_torch_mod.bool, _torch_mod.uint8):
         raise ValueError("mask must be bool or uint8, not %s" % mask.dtype)
     return mask.data_ptr()
@@ -592,15 +595,15 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
             return router_forward(logits, k, mask)
     lib = _start()
     T, E, ld = _rows_2d("logits", logits)
-    dev, k = logits.device, int(k)
+    dev, index, k = logits.device, logits.get_device(), int(k)
     kk = max(k, 0)
     wsb = lib.trellis_moe_router_workspace_size(T, E) if T > 128 else 0
     ws = _empty(wsb, dtype=_u8, device=dev) if wsb else None
     ids, counts, tokens = _empty((T, kk), dtype=_i32, device=dev), _empty(E, dtype=_i32, device=dev), _empty(1, dtype=_i32, device=dev)
     w, lse = _empty((T, kk), dtype=_f32, device=dev), _empty(T, dtype=_f32, device=dev)
     prob, losses = _empty(E, dtype=_f32, device=dev), _empty(2, dtype=_f32, device=dev)
-    _launch(lib.trellis_moe_router_forward, logits.get_device(), logits.data_ptr(), _dtype_code(logits.dtype), ld,
-            None if mask is None else _mask(mask, T), T, E, k, ids.data_ptr(), w.data_ptr(), lse.data_ptr(),
+    _launch(lib.trellis_moe_router_forward, index, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+            None if mask is None else _mask(mask, index, T), T, E, k, ids.data_ptr(), w.data_ptr(), lse.data_ptr(),
             counts.data_ptr(), prob.data_ptr(), losses.data_ptr(), tokens.data_ptr(), _opt(ws), wsb)
     return RouterOut(ids, w, lse, counts, prob, losses, tokens)
 
@@ -613,20 +616,20 @@ def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=
             return router_backward(logits, fwd, grad_w, grad_losses, mask, out)
     lib = _start()
     T, E, ld = _rows_2d("logits", logits)
-    k = fwd.ids.shape[1]
-    _on_device("ids", fwd.ids, _i32, (T, k))
-    _on_device("w", fwd.w, _f32, (T, k))
-    _on_device("lse", fwd.lse, _f32, (T,))
-    _on_device("counts", fwd.counts, _i32, (E,))
-    _on_device("tokens", fwd.tokens, _i32, (1,))
-    _on_device("grad_w", grad_w, _f32, (T, k))
-    _on_device("grad_losses", grad_losses, _f32, (2,))
-    mp = _mask(mask, T)
+    index, k = logits.get_device(), fwd.ids.shape[1]
+    _on_device("ids", fwd.ids, index, _i32, (T, k))
+    _on_device("w", fwd.w, index, _f32, (T, k))
+    _on_device("lse", fwd.lse, index, _f32, (T,))
+    _on_device("counts", fwd.counts, index, _i32, (E,))
+    _on_device("tokens", fwd.tokens, index, _i32, (1,))
+    _on_device("grad_w", grad_w, index, _f32, (T, k))
+    _on_device("grad_losses", grad_losses, index, _f32, (2,))
+    mp = _mask(mask, index, T)
     if out is None:
         out = _empty((T, E), dtype=logits.dtype, device=logits.device)
     else:
-        _on_device("out", out, logits.dtype, (T, E))
-    _launch(lib.trellis_moe_router_backward, logits.get_device(), logits.data_ptr(), _dtype_code(logits.dtype), ld,
+        _on_device("out", out, index, logits.dtype, (T, E))
+    _launch(lib.trellis_moe_router_backward, index, logits.data_ptr(), _dtype_code(logits.dtype), ld,
             mp, T, E, k, fwd.ids.data_ptr(), fwd.w.data_ptr(), fwd.lse.data_ptr(), fwd.counts.data_ptr(),
             fwd.tokens.data_ptr(), _opt(grad_w), _opt(grad_losses), out.data_ptr())
     return out
@@ -635,12 +638,12 @@ def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=
 def _route_rows(rows, w):
     ws, rs = w.shape, rows.shape
     if (len(ws) == 2 and len(rs) == 2 and rs[0] == ws[0] * ws[1] and w.dtype is _f32 and w.is_cuda and rows.is_cuda and
-            w.is_contiguous() and rows.is_contiguous()):
+            w.is_contiguous() and rows.is_contiguous() and w.get_device() == rows.get_device()):
         return ws[0], ws[1], rs[1]
-    _on_device("w", w, _f32)
+    _on_device("rows", rows, None)
+    _on_device("w", w, rows.get_device(), _f32)
     if len(ws) != 2:
         raise ValueError("w must have two dimensions, not %d" % len(ws))
-    _on_device("rows", rows)
     raise ValueError("rows must have shape [%d, H], not %s" % (ws[0] * ws[1], tuple(rs)))
 
 
@@ -655,7 +658,7 @@ def combine(rows, w, out=None, stream=None):
     if out is None:
         out = _empty((T, H), dtype=_f32, device=rows.device)
     else:
-        _on_device("out", out, _f32, (T, H))
+        _on_device("out", out, rows.get_device(), _f32, (T, H))
     _launch(lib.trellis_moe_combine_forward, rows.get_device(), rows.data_ptr(), _dtype_code(rows.dtype),
             w.data_ptr(), T, k, H, out.data_ptr())
     return out
@@ -668,7 +671,7 @@ def combine_backward(rows, w, grad_out, want_rows: bool = True, want_w: bool = T
             return combine_backward(rows, w, grad_out, want_rows, want_w)
     lib = _start()
     T, k, H = _route_rows(rows, w)
-    _on_device("grad_out", grad_out, _f32, (T, H))
+    _on_device("grad_out", grad_out, rows.get_device(), _f32, (T, H))
     grows = _torch_mod.empty_like(rows) if want_rows else None
     gw = _torch_mod.empty_like(w) if want_w else None
     _launch(lib.trellis_moe_combine_backward, rows.get_device(), rows.data_ptr(), _dtype_code(rows.dtype),
@@ -703,14 +706,14 @@ def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
     if codes.dim() != 2:
         raise ValueError("codes must have two dimensions, not %d" % codes.dim())
     rows = codes.shape[0]
-    _on_device("codes", codes, _u8, (rows, 16 * B))
-    _on_device("scales", scales, _u8, (rows, B))
+    _on_device("codes", codes, None, _u8, (rows, 16 * B))
+    _on_device("scales", scales, codes.get_device(), _u8, (rows, B))
     dtype = _f32 if dtype is None else dtype
     code = _dtype_code(dtype)
     if out is None:
         out = _empty((rows, K), dtype=dtype, device=codes.device)
     else:
-        _on_device("out", out, dtype, (rows, K))
+        _on_device("out", out, codes.get_device(), dtype, (rows, K))
     _launch(lib.trellis_moe_mxfp4_dequantize, codes.get_device(), codes.data_ptr(), scales.data_ptr(), rows, K,
             out.data_ptr(), code)
     return out
@@ -729,8 +732,8 @@ class _MxFp4:
         self.lib = _start()
         B = (int(K) + 31) // 32
         E, R = int(codes.shape[0]), int(codes.shape[1])
-        _on_device("codes", codes, torch.uint8, (E, R, 16 * B))
-        _on_device("scales", scales, torch.uint8, (E, R, B))
+        _on_device("codes", codes, None, torch.uint8, (E, R, 16 * B))
+        _on_device("scales", scales, codes.get_device(), torch.uint8, (E, R, B))
         if gated and R % 2:
             raise ValueError("a gated matrix has gate and up rows: %d rows are odd" % R)
         self.device, self.index = codes.device, codes.get_device()
@@ -810,7 +813,7 @@ class _MxFp4:
             return _empty((rows, self.N), dtype=dtype, device=self.device), code
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
-        return _on_device("out", out, None, (rows, self.N)), _dtype_code(out.dtype)
+        return _on_device("out", out, self.index, None, (rows, self.N)), _dtype_code(out.dtype)
 
 
 class MxFp4Linear(_MxFp4):
@@ -848,7 +851,7 @@ class MxFp4Experts(_MxFp4):
                 return self.forward(x, ids, per_route, out, out_dtype)
         rows, _, ld = _rows_2d("x", x)
         T, topk = ids.shape[0], self.topk
-        _on_device("ids", ids, _i32, (T, topk))
+        _on_device("ids", ids, self.index, _i32, (T, topk))
         need = T * topk if per_route else T
         if rows != need:
             raise ValueError("x must have %d rows, not %d" % (need, rows))
