@@ -110,3 +110,37 @@ def test_weights_and_scales_of_two_devices_are_refused(launched, monkeypatch):
     monkeypatch.setattr(binding, "_torch", lambda: torch)
     with pytest.raises(ValueError, match="cuda:1"):
         binding.MxFp4Linear(Tensor(16, 32, dtype=U8), Tensor(16, 2, dtype=U8, index=1), 64, max_tokens=4)
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: binding.router_forward(Tensor(4, 8), n + 2), lambda n: binding.router_forward(Tensor(n + 4, 1), 1),
+    lambda n: binding.router_forward(Tensor(4, n + 8), 2),
+    lambda n: binding.combine(Tensor(2 * (n + 4), 1), Tensor(n + 4, 2)), lambda n: binding.combine(Tensor(4, n + 1), Tensor(4, 1)),
+    lambda n: binding.combine_backward(Tensor(n + 1, 1), Tensor(1, n + 1), Tensor(1, 1)),
+    lambda n: binding.mxfp4_quantize(Tensor(1, n + 32)),
+    lambda n: binding.mxfp4_dequantize(Tensor(1, (n + 32) // 2, dtype=U8), Tensor(1, (n + 32) // 32, dtype=U8), n + 32),
+    lambda n: binding.MxFp4Linear(Tensor(16, 32, dtype=U8), Tensor(16, 2, dtype=U8), 64, max_tokens=n + 4),
+    lambda n: binding.MxFp4Linear(Tensor(n + 16, 32, dtype=U8), Tensor(n + 16, 2, dtype=U8), 64, max_tokens=4),
+    lambda n: binding.MxFp4Experts(Tensor(2, 16, 32, dtype=U8), Tensor(2, 16, 2, dtype=U8), 64, topk=n + 1, max_tokens=1),
+    lambda n: handle(binding.MxFp4Linear, 1, 16, 64).forward(Tensor(n + 4, 64)),
+    lambda n: handle(binding.MxFp4Experts, 4, 16, 64, topk=1).forward(Tensor(n + 4, 64), Tensor(n + 4, 1, dtype=I32))])
+def test_sizes_past_32_bits_are_refused(launched, monkeypatch, call):
+    """2^32 + a small size must not be taken for the small size."""
+    monkeypatch.setattr(binding, "_torch", lambda: torch)
+    with pytest.raises(ValueError, match="too large|32 bits"):
+        call(2 ** 32)
+    assert not launched
+
+
+def test_quantisation_of_more_rows_than_32_bits_hold(launched):
+    binding.mxfp4_quantize(Tensor(2 ** 32 + 1, 32))
+    assert launched[0][2][3] == 2 ** 32 + 1
+
+
+def test_router_allocates_no_more_than_it_may_use(launched, monkeypatch):
+    """k past E is refused by the C call; until then it costs no memory."""
+    sizes, empty = [], binding._empty
+    monkeypatch.setattr(binding, "_empty", lambda shape, **kw: sizes.append(shape) or empty(shape, **kw))
+    binding.router_forward(Tensor(4, 8), 2 ** 30)
+    assert launched[0][2][6] == 2 ** 30
+    assert all(torch.Size((s,) if isinstance(s, int) else s).numel() <= 32 for s in sizes)

@@ -541,7 +541,18 @@ def _on_device(name, t, index, dtype=None, shape=None, contiguous=True):
     return t
 
 
-def _rows_2d(name, t):
+_MOST = 2 ** 31 - 1
+
+
+def _size(name, v):
+    """v as a size that the C calls take in 32 bits (ctypes would cut off the rest)."""
+    v = int(v)
+    if not -_MOST <= v <= _MOST:
+        raise ValueError("%s=%d is more than 32 bits hold" % (name, v))
+    return v
+
+
+def _rows_2d(name, t, most_rows=_MOST):
     """A matrix whose rows may lie apart (last dimension contiguous); returns
     its rows, columns and row stride."""
     shape = t.shape
@@ -550,6 +561,8 @@ def _rows_2d(name, t):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     rows, cols = shape
+    if rows > most_rows or cols > _MOST:
+        raise ValueError("%s: %d x %d is too large" % (name, rows, cols))
     if t.is_contiguous():
         return rows, cols, cols
     ld, step = t.stride()
@@ -595,8 +608,8 @@ def router_forward(logits, k: int, mask=None, stream=None) -> RouterOut:
             return router_forward(logits, k, mask)
     lib = _start()
     T, E, ld = _rows_2d("logits", logits)
-    dev, index, k = logits.device, logits.get_device(), int(k)
-    kk = max(k, 0)
+    dev, index, k = logits.device, logits.get_device(), _size("k", k)
+    kk = min(max(k, 0), E)  # (what is out of range is refused below)
     wsb = lib.trellis_moe_router_workspace_size(T, E) if T > 128 else 0
     ws = _empty(wsb, dtype=_u8, device=dev) if wsb else None
     ids, counts, tokens = _empty((T, kk), dtype=_i32, device=dev), _empty(E, dtype=_i32, device=dev), _empty(1, dtype=_i32, device=dev)
@@ -638,12 +651,15 @@ def router_backward(logits, fwd: RouterOut, grad_w=None, grad_losses=None, mask=
 def _route_rows(rows, w):
     ws, rs = w.shape, rows.shape
     if (len(ws) == 2 and len(rs) == 2 and rs[0] == ws[0] * ws[1] and w.dtype is _f32 and w.is_cuda and rows.is_cuda and
-            w.is_contiguous() and rows.is_contiguous() and w.get_device() == rows.get_device()):
+            w.is_contiguous() and rows.is_contiguous() and w.get_device() == rows.get_device() and
+            ws[0] <= _MOST and ws[1] <= _MOST and rs[1] <= _MOST):
         return ws[0], ws[1], rs[1]
     _on_device("rows", rows, None)
     _on_device("w", w, rows.get_device(), _f32)
     if len(ws) != 2:
         raise ValueError("w must have two dimensions, not %d" % len(ws))
+    if max(ws) > _MOST or max(rs) > _MOST:
+        raise ValueError("rows %s and w %s are too large" % (tuple(rs), tuple(ws)))
     raise ValueError("rows must have shape [%d, H], not %s" % (ws[0] * ws[1], tuple(rs)))
 
 
@@ -686,7 +702,7 @@ def mxfp4_quantize(x, stream=None):
         with _given(stream, "x", x):
             return mxfp4_quantize(x)
     lib = _start()
-    rows, K, ld = _rows_2d("x", x)
+    rows, K, ld = _rows_2d("x", x, 2 ** 63 - 1)
     B, dev = (K + 31) // 32, x.device
     codes = _empty((rows, 16 * B), dtype=_u8, device=dev)
     scales = _empty((rows, B), dtype=_u8, device=dev)
@@ -701,7 +717,7 @@ def mxfp4_dequantize(codes, scales, K: int, dtype=None, out=None, stream=None):
         with _given(stream, "codes", codes):
             return mxfp4_dequantize(codes, scales, K, dtype, out)
     lib = _start()
-    K = int(K)
+    K = _size("K", K)
     B = (K + 31) // 32
     if codes.dim() != 2:
         raise ValueError("codes must have two dimensions, not %d" % codes.dim())
@@ -730,16 +746,17 @@ class _MxFp4:
     def __init__(self, codes, scales, K: int, max_rows: int, gated: bool):
         torch = _torch()
         self.lib = _start()
-        B = (int(K) + 31) // 32
-        E, R = int(codes.shape[0]), int(codes.shape[1])
+        K, max_rows = _size("K", K), _size("rows of a call", max_rows)
+        B = (K + 31) // 32
+        E, R = _size("E", codes.shape[0]), _size("R", codes.shape[1])
         _on_device("codes", codes, None, torch.uint8, (E, R, 16 * B))
         _on_device("scales", scales, codes.get_device(), torch.uint8, (E, R, B))
         if gated and R % 2:
             raise ValueError("a gated matrix has gate and up rows: %d rows are odd" % R)
         self.device, self.index = codes.device, codes.get_device()
         self.codes, self.scales = codes, scales
-        self.E, self.N, self.K, self.gated = E, R // 2 if gated else R, int(K), bool(gated)
-        d = MxFp4Desc(E, self.N, self.K, 1 if gated else 0, int(max_rows), codes.data_ptr(), scales.data_ptr())
+        self.E, self.N, self.K, self.gated = E, R // 2 if gated else R, K, bool(gated)
+        d = MxFp4Desc(E, self.N, self.K, 1 if gated else 0, max_rows, codes.data_ptr(), scales.data_ptr())
         handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
         with torch.cuda.device(self.device):
             torch.cuda.current_stream().synchronize()  # prepare reads the scales on a stream of its own
