@@ -477,10 +477,12 @@ tm_status trellis_moe_mxfp4_forward_experts(tm_mxfp4* h, const void* x, int32_t 
 tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* flags, void* stream);
 
 /* Test hook, as trellis_moe_set_wait_test: the limit of the kernels' pipeline
- * waits in ns (0: 2 s) and whether the MMA issuer first waits for an arrival
- * that never comes. Later calls with the handle give up after the limit, set
- * bit 1 of the error word and leave `out` undefined. */
-tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, int32_t stall_issuer);
+ * waits in ns (0: 2 s) and which wait is for an arrival that never comes: none
+ * (stall 0), the MMA issuer's before its first MMA (1), or one epilogue warp's
+ * for its accumulators, which the other warps see complete (2). Later calls
+ * with the handle give up after the limit, set bit 1 of the error word and
+ * leave `out` undefined. */
+tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, int32_t stall);
 
 void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
 

@@ -813,10 +813,11 @@ class _MxFp4:
             _check(st)
         return int(flags.value)
 
-    def set_wait_test(self, wait_limit_ns: int = 0, stall_issuer: bool = False):
-        """Limit of the kernels' pipeline waits, and the stalled issuer used to
-        test that they give up (see the C header)."""
-        _check(self.lib.trellis_moe_mxfp4_set_wait_test(self.handle, int(wait_limit_ns), 1 if stall_issuer else 0))
+    def set_wait_test(self, wait_limit_ns: int = 0, stall_issuer: bool = False, stall_epilogue: bool = False):
+        """Limit of the kernels' pipeline waits, and the stalled issuer or
+        epilogue warp used to test that they give up (see the C header)."""
+        _check(self.lib.trellis_moe_mxfp4_set_wait_test(self.handle, int(wait_limit_ns),
+                                                        1 if stall_issuer else 2 if stall_epilogue else 0))
 
     def _output(self, rows, x, out, out_dtype):
         """The result tensor, and its dtype's number."""

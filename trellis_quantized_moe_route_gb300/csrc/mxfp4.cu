@@ -13,7 +13,7 @@ struct tm_mxfp4 {
   uint8_t* d_scales;  // the weights' scales as the tensor cores read them
   int sms;
   uint64_t wait_ns;   // trellis_moe_mxfp4_set_wait_test
-  int stall_issuer;
+  int stall;          // 0, or which wait of the kernels never ends by itself (same)
   CUtensorMap wmap;
 };
 
@@ -130,7 +130,8 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
     a.out_dtype = c.out_dtype;
     a.err = static_cast<uint32_t*>(c.ws);
     a.wait_ns = h->wait_ns;
-    a.stall_issuer = h->stall_issuer;
+    a.stall_issuer = h->stall == 1;
+    a.stall_epilogue = h->stall == 2;
     a.wmap = h->wmap;
     const int chunks = c.ids ? c.rows : 1;
     return launch_mx_dec(a, chunks, st);
@@ -154,7 +155,8 @@ cudaError_t mx_run(tm_mxfp4* h, const MxCall& c, cudaStream_t st) {
   a.err = err;
   a.sms = h->sms;
   a.wait_ns = h->wait_ns;
-  a.stall_issuer = h->stall_issuer;
+  a.stall_issuer = h->stall == 1;
+  a.stall_epilogue = h->stall == 2;
   a.wmap = h->wmap;
   a.max_blocks = (c.rows + a.bn - 1) / a.bn;
   if (c.ids) {
@@ -218,7 +220,7 @@ tm_status trellis_moe_mxfp4_prepare(const tm_mxfp4_desc* desc, tm_mxfp4** out, s
   h->desc = d;
   h->d_scales = nullptr;
   h->wait_ns = 0;
-  h->stall_issuer = 0;
+  h->stall = 0;
   const int halves = d.gated ? 2 : 1;
   cudaError_t e;
   int dev = 0;
@@ -291,12 +293,12 @@ tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* f
   return TM_OK;
 }
 
-tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, int32_t stall_issuer) {
+tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, int32_t stall) {
   set_last_error("");
   if (!h) return status_fail(TM_EINVAL, "handle is NULL");
-  if (stall_issuer != 0 && stall_issuer != 1) return status_fail(TM_EINVAL, "stall_issuer=%d must be 0 or 1", stall_issuer);
+  if (stall < 0 || stall > 2) return status_fail(TM_EINVAL, "stall=%d must be 0, 1 or 2", stall);
   h->wait_ns = wait_limit_ns;
-  h->stall_issuer = stall_issuer;
+  h->stall = stall;
   return TM_OK;
 }
 

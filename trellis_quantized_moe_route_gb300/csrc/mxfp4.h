@@ -35,7 +35,8 @@ struct MxTcArgs {
   uint32_t* err;
   int sms;
   uint64_t wait_ns;              // limit of a pipeline wait (0: 2 s)
-  int stall_issuer;              // test of the bounded waits: the issuer first waits for what never comes
+  int stall_issuer;              // test of the bounded waits: the issuer first waits for what never comes,
+  int stall_epilogue;            // or the first epilogue warp does so for every accumulator
   CUtensorMap wmap;              // codes of W as [E * R][16 B] bytes, box 128 x 128 bytes
   CUtensorMap xmap;              // codes of x as [blocks * bn][16 B] bytes, box bn x 128 bytes
 };
@@ -73,7 +74,7 @@ struct MxDecArgs {
   int out_dtype;
   uint32_t* err;
   uint64_t wait_ns;     // as in MxTcArgs
-  int stall_issuer;
+  int stall_issuer, stall_epilogue;
   CUtensorMap wmap;
 };
 cudaError_t launch_mx_dec(const MxDecArgs& a, int chunks, cudaStream_t st);

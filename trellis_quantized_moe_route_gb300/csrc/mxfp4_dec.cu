@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   if (split > 1) md_cluster_wait();  // every CTA of the cluster has started
   const int own = kMxDecRows >> lsplit;      // rows that a CTA of the cluster may own: c = rank, rank + split, ...
   if (warp < 4 && s_hi > s_lo) {
-    const bool ok = mx_wait_warp(&bars.acc, 0, abort, limit);
+    const bool ok = mx_wait_warp(a.stall_epilogue && warp == 0 ? &bars.never : &bars.acc, 0, abort, limit);
     tc_fence_after();
     if (ok) {
       const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);

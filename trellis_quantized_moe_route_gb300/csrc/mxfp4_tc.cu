@@ -260,6 +260,16 @@ __device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __rest
   }
 }
 
+// Whether all four warps of a part say yes, by its named barrier.
+__device__ __forceinline__ bool mx_vote_part(bool yes, int bar) {
+  uint32_t all;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(all)
+               : "r"((uint32_t)yes), "r"(bar)
+               : "memory");
+  return all != 0;
+}
+
 template <bool GATED, bool EXPERTS, typename T>
 __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, unsigned char* stage,
                             volatile int* abort, uint64_t limit) {
@@ -287,7 +297,12 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
     next = mx_unit<EXPERTS>(a, u + gridDim.x, g.units, g.tiles);
     const int buf = nu & 1;
     const int n = m.tile * 128 + quarter * 32 + lane;
-    if (!mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, limit)) return;
+    const bool test = a.stall_epilogue && warp == 0;
+    const bool full = mx_wait_warp(test ? &B.never : &B.acc_full[buf], test ? 0 : (nu >> 1) & 1, abort, limit);
+    // The four warps of a part meet at its barrier while they store: they go on
+    // together or not at all. (One may give up on the abort flag just before the
+    // accumulator that its neighbours then find complete.)
+    if (!mx_vote_part(full, 1 + part)) return;
     tc_fence_after();
     const uint32_t d = tmem + lane_base + (uint32_t)(buf * (GATED ? 2 : 1) * a.bn);
 #pragma unroll
