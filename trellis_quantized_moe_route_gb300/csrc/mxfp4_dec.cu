@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   const uint32_t tsfa = tmem + (uint32_t)(H * kMxDecRows);
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
+  int loaded = 0;  // stages, in the loading warp
 
   if (warp == 4) {
     const bool lead = mx_elect();
@@ -205,13 +206,7 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
         if (GATED) mx_bulk(sf + 1024, usf + s * 1024, 1024, bar);
       }
     }
-    // (after an abort, full[] also counts the quantisers' arrivals; they arrive
-    // for every stage they reach, and a copy in flight lands within the limit)
-    if (*abort) {
-      int never = 0;
-      for (int i = max(0, it - ring); i < it; ++i)
-        mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs / kMdMaxRing);
-    }
+    loaded = it;
   } else if (warp == 5) {
     const bool lead = mx_elect();
     const uint32_t base = smem_u32(smem), idesc = mx_idesc(kMxDecRows);
@@ -226,10 +221,6 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
       if (lead) tc_commit(&bars.empty[r.slot]);
     }
     if (lead) tc_commit(&bars.acc);
-    if (*abort) {  // what was issued ends before the tensor memory goes
-      int never = 0;
-      mx_wait_warp(&bars.acc, 0, &never, kMxDrainNs);
-    }
   } else {
     MxRing r;
     int it = 0, item = 0;
@@ -284,7 +275,19 @@ __global__ void __launch_bounds__(kMdThreads) k_mx_dec(const __grid_constant__ M
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *abort) atomicOr(a.err, 2u);
+  if (*abort) {  // (nobody sets it any more: the same for all)
+    // What is in flight ends before shared and tensor memory go. Here, since any
+    // warp may give up after the loader and the issuer are done. (full[] also
+    // counts the quantisers' arrivals, one for every stage they reach; a copy
+    // in flight lands within the limit.)
+    int never = 0;
+    for (int i = max(0, loaded - ring); i < loaded; ++i)
+      mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs / kMdMaxRing);
+    never = 0;
+    if (warp == 5) mx_wait_warp(&bars.acc, 0, &never, kMxDrainNs);
+    if (tid == 0) atomicOr(a.err, 2u);
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 5) tmem_dealloc(tmem, cols);
   if (split > 1) {

@@ -109,9 +109,10 @@ __device__ __forceinline__ MxGeom mx_geom(const MxTcArgs& a, int ring, FastDiv t
   return g;
 }
 
+// (returns the stages it loaded)
 template <bool GATED, bool EXPERTS>
-__device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
-                          uint64_t limit) {
+__device__ int mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, volatile int* abort,
+                         uint64_t limit) {
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(&B.full[0]);
   const uint32_t bytes = g.a_bytes + g.b_bytes + g.sfa_bytes + g.sfb_bytes;
@@ -161,22 +162,33 @@ __device__ void mx_loader(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
       }
     }
   }
-  if (*abort) {  // let the copies in flight land before the CTA goes
-    int never = 0;
-    for (int i = max(0, it - g.ring); i < it; ++i) mbar_wait_abort(&B.full[i % g.ring], (i / g.ring) & 1, &never, kMxDrainNs);
-  }
+  return it;
 }
 
+// What a CTA that gave up still has in flight ends before its shared and tensor
+// memory go: the copies of the last stages loaded, and the MMAs of the last one
+// issued. Called when all its warps are done, since any of them may give up
+// after the loader and the issuer have left.
+__device__ __forceinline__ void mx_drain_copies(MxBars& B, int ring, int loaded) {
+  int never = 0;
+  for (int i = max(0, loaded - ring); i < loaded; ++i) mbar_wait_abort(&B.full[i % ring], (i / ring) & 1, &never, kMxDrainNs);
+}
+__device__ __forceinline__ void mx_drain_mmas(MxBars& B, int ring, int issued) {
+  int never = 0;
+  if (issued > 0) mbar_wait_abort(&B.empty[(issued - 1) % ring], ((issued - 1) / ring) & 1, &never, kMxDrainNs);
+}
+
+// (returns the stages whose MMAs it issued)
 template <bool GATED, bool EXPERTS, int NRB>
-__device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
-                          volatile int* abort, uint64_t limit) {
+__device__ int mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned char* smem, uint32_t tmem,
+                         volatile int* abort, uint64_t limit) {
   MxRing r;
   int it = 0, nu = 0;
   bool ok = true;
   constexpr int H = GATED ? 2 : 1;
   const bool lead = mx_elect();
   const uint32_t base = smem_u32(smem);
-  if (a.stall_issuer && !mx_wait_warp(&B.never, 0, abort, limit)) return;
+  if (a.stall_issuer && !mx_wait_warp(&B.never, 0, abort, limit)) return 0;
   MxUnit next = mx_unit<EXPERTS>(a, blockIdx.x, g.units, g.tiles);
   for (int u = blockIdx.x; u < g.units && ok; u += gridDim.x, ++nu) {
     const MxUnit m = next;
@@ -202,10 +214,7 @@ __device__ void mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigne
     }
     if (ok && lead) tc_commit(&B.acc_full[buf]);
   }
-  if (*abort && it > 0) {
-    int never = 0;
-    mbar_wait_abort(&B.empty[(it - 1) % g.ring], ((it - 1) / g.ring) & 1, &never, kMxDrainNs);
-  }
+  return it;
 }
 
 // 32 columns (rows of y) of a thread's channel, as T: y[c] for row `row` of
@@ -367,21 +376,27 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   volatile int* abort = &s_abort;
   const uint64_t limit = a.wait_ns ? a.wait_ns : kMxWaitNs;
   const MxGeom g = mx_geom<GATED, EXPERTS>(a, ring, tiles);
+  int loaded = 0, issued = 0;  // stages, in the warp that did it
   if (g.units == 0) {
     grid_wait();  // (every route was dropped; this kernel still ends after the one before it)
   } else if (warp < kMxEpiWarps) {
     mx_epilogue<GATED, EXPERTS, T>(a, g, bars, tmem, smem + (size_t)ring * g.stage_bytes, abort, limit);
   } else if (warp == kMxEpiWarps) {
-    mx_loader<GATED, EXPERTS>(a, g, bars, smem, abort, limit);
+    loaded = mx_loader<GATED, EXPERTS>(a, g, bars, smem, abort, limit);
   } else if (warp == kMxEpiWarps + 1) {
     if (a.nrb == 1)
-      mx_issuer<GATED, EXPERTS, 1>(a, g, bars, smem, tmem, abort, limit);
+      issued = mx_issuer<GATED, EXPERTS, 1>(a, g, bars, smem, tmem, abort, limit);
     else
-      mx_issuer<GATED, EXPERTS, 2>(a, g, bars, smem, tmem, abort, limit);
+      issued = mx_issuer<GATED, EXPERTS, 2>(a, g, bars, smem, tmem, abort, limit);
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort) atomicOr(a.err, 2u);
+  if (*abort) {  // (nobody sets it any more: the same for all)
+    mx_drain_copies(bars, ring, loaded);
+    mx_drain_mmas(bars, ring, issued);
+    if (threadIdx.x == 0) atomicOr(a.err, 2u);
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
