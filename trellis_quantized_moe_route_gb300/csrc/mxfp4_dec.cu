@@ -315,8 +315,9 @@ cudaError_t md_launch(const MxDecArgs& a, int chunks, cudaStream_t st) {
   constexpr int H = GATED ? 2 : 1;
   auto kern = k_mx_dec<GATED>;
   constexpr int kSmem = 104 * 1024;
-  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess) return attr;
+  static OncePerDevice done;
+  const cudaError_t limit = allow_smem(done, kern, kSmem);
+  if (limit != cudaSuccess) return limit;
   const int stages = mx_stages(a.K), tiles = (a.N + 127) / 128;
   const int units = chunks * tiles;
   const int lsplit = mx_dec_split(units, stages, a.sms);

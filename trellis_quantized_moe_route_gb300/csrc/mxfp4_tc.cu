@@ -433,8 +433,9 @@ cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, 
 template <bool GATED, bool EXPERTS, typename T>
 cudaError_t mx_launch(const MxTcArgs& a, cudaStream_t st) {
   auto kern = k_mx_tc<GATED, EXPERTS, T>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
-  if (attr != cudaSuccess) return attr;
+  static OncePerDevice done;
+  const cudaError_t limit = allow_smem(done, kern, (int)kMxSmem);
+  if (limit != cudaSuccess) return limit;
   const uint32_t stage = (uint32_t)(GATED ? 2 : 1) * (kMxTileBytes + 1024) + (uint32_t)a.bn * 128 + (uint32_t)a.nrb * 1024;
   const uint32_t stage_bytes = (stage + 1023) / 1024 * 1024;
   const uint32_t store = kMxEpiWarps / 4 * kMxStoreBytes;

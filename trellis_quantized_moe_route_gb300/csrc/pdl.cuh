@@ -1,7 +1,9 @@
-// Programmatic dependent launch.
+// Launching: programmatic dependent launches, and the shared memory of large CTAs.
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include "per_device.h"
 
 namespace tmoe {
 
@@ -25,6 +27,16 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Lets `kern` have `bytes` of dynamic shared memory on the current device. (The
+// limit belongs to a device's copy of the kernel; `done`: one for each kernel.)
+template <typename... P>
+cudaError_t allow_smem(OncePerDevice& done, void (*kern)(P...), int bytes) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return done(dev, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
 }  // namespace tmoe

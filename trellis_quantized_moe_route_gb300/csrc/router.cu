@@ -862,8 +862,9 @@ template <int V, typename T>
 cudaError_t router_lanes_launch(const RouterFwd& a, cudaLaunchConfig_t cfg, int csize) {
   auto kern = k_router_fwd_lanes<V, T>;
   constexpr int kMost = kRtLaneWarps * 32 * 16 * (kMaxExperts / 8 | 1);
-  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (attr != cudaSuccess) return attr;
+  static OncePerDevice done;
+  const cudaError_t limit = allow_smem(done, kern, kMost);
+  if (limit != cudaSuccess) return limit;
   cfg.blockDim = dim3(32 * kRtLaneWarps);
   cfg.dynamicSmemBytes = (size_t)kRtLaneWarps * 32 * 16 * (a.E / 8 | 1);
   return cudaLaunchKernelEx(&cfg, kern, a, csize, FastDiv((uint32_t)(a.E / 8)));
