@@ -4,13 +4,36 @@ What tuning the router of a layer with frozen experts needs: the gradient goes
 from the layer's output through ``combine`` to the route weights, and with the
 losses' own through ``route`` to the logits. The experts' rows are constants
 here (``binding.MxFp4Experts`` has no backward pass); ``combine`` does return
-their gradient to a caller whose rows want one.
+their gradient to a caller whose rows want one. Gradients are of first order: a
+second derivative through either is refused.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding
+
+
+class _FirstOrder(torch.autograd.Function):
+    """A gradient as it is, that refuses to be differentiated in turn."""
+
+    @staticmethod
+    def forward(ctx, grad, *sources):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("route and combine have first-order gradients only")
+
+
+def _first_order(grad, *sources):
+    """`grad`, made by a kernel from `sources`. Where a graph of the backward
+    pass is being built (create_graph) it depends on all of them, though no
+    operation shows it: also where the incoming gradient is a constant, which is
+    all that once_differentiable looks at."""
+    if grad is not None and torch.is_grad_enabled() and any(s is not None and s.requires_grad for s in sources):
+        return _FirstOrder.apply(grad, *sources)
+    return grad
 
 
 class _Route(torch.autograd.Function):
@@ -26,7 +49,8 @@ class _Route(torch.autograd.Function):
         logits, mask, *r = ctx.saved_tensors
         grad_w = None if grad_w is None else grad_w.contiguous()
         grad_losses = None if grad_losses is None else grad_losses.contiguous()
-        return binding.router_backward(logits, binding.RouterOut(*r), grad_w, grad_losses, mask=mask), None, None
+        grad = binding.router_backward(logits, binding.RouterOut(*r), grad_w, grad_losses, mask=mask)
+        return _first_order(grad, logits, grad_w, grad_losses), None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -39,7 +63,9 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, grad_out):
         rows, w = ctx.saved_tensors
         want_rows, want_w = ctx.needs_input_grad
-        return binding.combine_backward(rows, w, grad_out.contiguous(), want_rows, want_w)
+        grad_out = grad_out.contiguous()
+        grad_rows, grad_w = binding.combine_backward(rows, w, grad_out, want_rows, want_w)
+        return _first_order(grad_rows, w, grad_out), _first_order(grad_w, rows, grad_out)
 
 
 def route(logits, k: int, mask=None) -> binding.RouterOut:
