@@ -459,7 +459,8 @@ size_t trellis_moe_mxfp4_workspace_size(const tm_mxfp4* h, int32_t rows);
 
 /* Dense form (E = 1): x [T, K], row t at x + t * ld elements; out [T, N],
  * written. workspace 256-byte aligned, contents on entry ignored; its first
- * 4 bytes are the device error word. T = 0 is a no-op. */
+ * 4 bytes are the device error word, which every call starts anew. T = 0 is a
+ * no-op and leaves the error word as it is. */
 tm_status trellis_moe_mxfp4_forward(tm_mxfp4* h, const void* x, int32_t x_dtype, int64_t ld, int32_t T, void* out,
                                     int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -471,9 +472,9 @@ tm_status trellis_moe_mxfp4_forward_experts(tm_mxfp4* h, const void* x, int32_t 
                                             int32_t per_route, const int32_t* ids, int32_t T, int32_t topk, void* out,
                                             int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Read and clear the error word of `workspace` (synchronises `stream`). Returns
- * TM_EDEVICE if any flag was set (bit 0: expert id out of range; bit 1: a
- * pipeline wait gave up). */
+/* Read and clear the error word of `workspace` (synchronises `stream`): the
+ * flags of the last call with that workspace. Returns TM_EDEVICE if any was set
+ * (bit 0: expert id out of range; bit 1: a pipeline wait gave up). */
 tm_status trellis_moe_mxfp4_poll_error(tm_mxfp4* h, void* workspace, uint32_t* flags, void* stream);
 
 /* Test hook, as trellis_moe_set_wait_test: the limit of the kernels' pipeline

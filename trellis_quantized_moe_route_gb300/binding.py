@@ -767,6 +767,7 @@ class _MxFp4:
         off = (-self.workspace.data_ptr()) % 256
         self.workspace = self.workspace[off:off + self.workspace_bytes]
         self.workspace_ptr = self.workspace.data_ptr()
+        self.workspace[:4].zero_()  # the error word, until the first call writes it
         self._lock = threading.Lock()
         self._stream = torch.cuda.current_stream(self.device)  # of the last call
         self._raw = self._stream.cuda_stream
@@ -800,6 +801,9 @@ class _MxFp4:
             pass
 
     def poll_error(self, stream=None) -> int:
+        """The last call's error flags (0: none; every call starts them anew),
+        and clears them: bit 0 an expert id out of range, bit 1 a wait that gave
+        up. Waits for the stream."""
         if stream is not None:
             with _given(stream, "the weights", self):
                 return self.poll_error()
