@@ -33,7 +33,12 @@ class FrozenExperts:
     def rows(self, x, ids):
         """The experts' outputs in route order, bf16 [T * topk, H]."""
         z = self.up.forward(x, ids, out_dtype=torch.bfloat16)
-        return self.down.forward(z, ids, per_route=True, out_dtype=torch.bfloat16)
+        y = self.down.forward(z, ids, per_route=True, out_dtype=torch.bfloat16)
+        for name, e in (("up", self.up), ("down", self.down)):  # (the flags are the last call's alone; this waits for it)
+            flags = e.poll_error()
+            if flags:
+                raise RuntimeError("device error flags 0x%x in the %s projections" % (flags, name))
+        return y
 
 
 def layer(x, weight, experts, topk, mask=None):
@@ -67,8 +72,6 @@ def tune(steps=100, tokens=2048, E=32, H=512, I=256, topk=4, seed=0, balance=0.0
             log("step %4d  task %.5f  balance %.3f  z %.2f  busiest expert %d of %d routes" %
                 (step, history[-1], *r.losses.tolist(), int(r.counts.max()), int(r.tokens) * topk))
     for e in (experts.up, experts.down):
-        if e.poll_error():
-            raise RuntimeError("device error flags set")
         e.close()
     return history
 

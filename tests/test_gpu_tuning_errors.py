@@ -53,3 +53,23 @@ def test_flags_are_the_last_calls(binding, T):
     ex.forward(x[:0], ids[:0])
     assert ex.poll_error() == 1
     ex.close()
+
+
+@pytest.mark.parametrize("which,call", [("up", 1), ("down", 2), ("up", 6)])
+def test_example_sees_an_error_of_any_step(binding, monkeypatch, which, call):
+    """One call's wait gives up (after 1 ms, for an arrival that never comes), and later ones run well."""
+    import tune_router
+    calls = {"n": 0}
+    cls = binding.MxFp4Experts
+    forward = cls.forward
+
+    def one_stalls(self, *args, **kw):
+        if self.gated == (which == "up"):
+            calls["n"] += 1
+            self.set_wait_test(1000000 if calls["n"] == call else 0, stall_issuer=calls["n"] == call)
+        return forward(self, *args, **kw)
+
+    monkeypatch.setattr(cls, "forward", one_stalls)
+    with pytest.raises(RuntimeError, match="flags 0x2 in the %s" % which):
+        tune_router.tune(steps=5, tokens=512, E=16, H=256, I=128, topk=2, log=lambda *_: None)
+    assert calls["n"] == call
