@@ -144,13 +144,20 @@ tm_status trellis_moe_combine_forward(const void* rows, int32_t dtype, const flo
   if (s != TM_OK) return s;
   if (T == 0) return TM_OK;
   if (!out || ((uintptr_t)out) % 4) return status_fail(TM_EINVAL, "out must be non-NULL and 4-byte aligned");
-  const int per = (H + 7) / 8;
-  if ((long)T * per > (1L << 30)) return status_fail(TM_EUNSUPPORTED, "T=%d rows of H=%d are too large", T, H);
-  const uint32_t items = (uint32_t)T * per;
+  // pieces of at most 2^30 eighths of a row, so that the kernel's items stay in 32 bits
+  const int per = (H + 7) / 8, most = (1 << 30) / per;
   auto go = [&](auto elem, auto vec) {
     using E = decltype(elem);
-    return launch_after(k_combine_routes<E, decltype(vec)::value>, dim3((items + 255) / 256), 256, 0,
-                           (cudaStream_t)stream, static_cast<const E*>(rows), w, items, FastDiv(per), k, H, out);
+    for (int t = 0; t < T;) {
+      const int n = std::min(most, T - t);
+      const uint32_t items = (uint32_t)n * per;
+      const cudaError_t e = launch_after(k_combine_routes<E, decltype(vec)::value>, dim3((items + 255) / 256), 256, 0,
+                                         (cudaStream_t)stream, static_cast<const E*>(rows) + (size_t)t * k * H,
+                                         w + (size_t)t * k, items, FastDiv(per), k, H, out + (size_t)t * H);
+      if (e != cudaSuccess) return e;
+      t += n;  // (at most T: no overflow)
+    }
+    return cudaSuccess;
   };
   const bool vec = eights(rows, H, H, dtype_bytes(dtype)) && eights(out, H, H, 4);
   const cudaError_t e = TM_BY_DTYPE_VEC(dtype, vec, go);
