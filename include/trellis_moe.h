@@ -363,7 +363,10 @@ void trellis_linear_destroy(tm_linear* lin);
 
 /* ------------------------------------------------------------------------
  * Element types of the entry points below. All of them compute in fp32 and
- * round once where they store. */
+ * round once where they store. exp, log and the quotients of softmax and silu
+ * are the hardware's approximations (about 2 ulp; that of the log is absolute,
+ * some 2^-21, so that an lse near 0 has fewer right bits; subnormal results
+ * flush to 0, so that silu(g) is 0 below g = -87). */
 typedef enum { TM_F32 = 0, TM_BF16 = 1, TM_F16 = 2 } tm_dtype;
 
 /* ------------------------------------------------------------------------

@@ -92,10 +92,14 @@ MxLayout mx_layout(const tm_mxfp4_desc& d, long rows) {
 //   dense 1024 x 1024   T = 1: 3.8 / 5.2   4: 4.2 / 5.2   8: 5.3 / 5.2   16: 6.8 / 5.2
 //   dense 5120 x 1536   T = 1: 5.2 / 5.8   4: 5.8 / 5.8   8: 8.2 / 5.8
 //   128 experts, gated 1024 -> 512    64 routes: 7.1 / 10.9   128: 10.9 / 12.4   192: 13.9 / 12.4   256: 17.0 / 12.4
-//   128 experts, 512 -> 1024          64 routes: 7.3 / 8.9    128: 11.2 / 10.8   192: 17.0 / 11.8
-//   8 experts, gated 1024 -> 1024     16 routes: 7.3 / 8.8    32: 10.3 / 8.8
-//   160 experts, 1536 -> 5120         16 routes: 14.0 / 16.0  32: 26.1 / 24.2    64: 47.8 / 40.2
-// Hence, dense, up to 8 pieces (rows times stages) for a CTA to quantise, where
+//   128 experts, 512 -> 1024          64 routes: 7.3 / 9.3    128: 10.3-11.2 / 10.8   192: 16.6 / 11.8
+//   256 experts, gated 2048 -> 256    64 routes: 8.2 / 10.8   128: 9.3 / 13.4    256: 17.5 / 16.9
+//   64 experts, gated 2560 -> 320     32 routes: 8.7 / 10.8   64: 13.4 / 11.4    96: 11.7 / 11.3
+//   32 experts, 512 -> 2048           32 routes: 7.2 / 8.7    64: 9.2 / 8.8
+//   16 experts, 4096 -> 768           16 routes: 8.2 / 10.3   32: 15.5 / 10.3
+//   8 experts, gated 1024 -> 1024     16 routes: 5.7-7.3 / 8.8   32: 7.2-10.3 / 8.8
+//   160 experts, 1536 -> 5120         16 routes: 12.3-14.0 / 15.4   32: 26.1 / 24.2-25.5    64: 42.6-47.8 / 40.2
+// (Of these the rule errs by most, 18%, at 64 routes of 64 experts.) Hence, dense, up to 8 pieces (rows times stages) for a CTA to quantise, where
 // the times are equal and the second launch's cost to the host is saved; by
 // expert few rows each on average, and no more CTAs than a few waves.
 bool mx_few_rows(const tm_mxfp4* h, const MxCall& c) {

@@ -17,10 +17,13 @@
 // is what 512 columns of tensor memory hold; that is why a block ends at 240
 // (gated: 4 x 112).
 //
-// Measured on one GB300 (bf16 in and out, whole call with quantisation and map):
+// Measured on one GB300 (bf16 in and out, with quantisation and map, replayed from
+// a CUDA graph; a call through the Python binding takes 1-5 us more where the
+// host is the longer side):
 //   2048 x 4096 x 4096 dense        20 us   3.4 PFLOP/s over the call. The
-//     issuer spends 503 cycles on a stage (four 128 x 240 x 64 MMAs, 15.6 K
-//     multiply-adds a cycle), which is what the tensor pipe takes; while an
+//     issuer spends 503 cycles on a stage of four 128 x 240 x 64 MMAs: 96 waiting
+//     for data, 257 on the scales' copies and the MMAs, 26 on the commit and 124 in
+//     its loop; the tensor pipe is active in 35% of the kernel's cycles. While an
 //     epilogue reads the other buffer a stage takes 1100. Quantisation and
 //     launches are 7 us of the call, the pipeline's start and last drain 3 us.
 //   2048 tokens x 8 of 128 experts, gated 1024 -> 512, Zipf   26 us: map and

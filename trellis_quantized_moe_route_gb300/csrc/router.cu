@@ -14,8 +14,9 @@
 // All of it in fp32 whatever the logits' type; only dl is rounded to it.
 //
 // One warp takes a token, V logits a lane, and reads the next token's row while
-// it works on this one (many tokens of 16-bit logits: a lane a token, below). What bounds it is the selection's instructions, not the
-// bytes. Each logit becomes a 32-bit key that is unique in the row and orders
+// it works on this one (many tokens of 16-bit logits: a lane a token, below).
+// The selection's instructions and their latency bound it, not the bytes. Each
+// logit becomes a 32-bit key that is unique in the row and orders
 // like (logit, then lower expert): 16-bit logits have their expert in the low
 // half; fp32 logits give up their lowest 8 bits for it, and a token in which two
 // of the k + 1 largest agree in the other 24 (one in a few hundred, or equal
@@ -30,10 +31,19 @@
 // time. The backward pass reads the logits again and rebuilds p from lse, which
 // costs less than storing p (T E fp32).
 //
-// 65536 tokens x 160 bf16 logits, k = 8, masked: forward 17 us with a lane a token
-// (its bytes take 4 us; with a warp a token 24: 360 instructions a token, the
-// integer pipe 62% busy), finishing sums 5 us, backward 17 us (220 instructions a
-// token; its bytes take 7 us). 8 tokens x 128: one launch, 4 us.
+// Exponentials, the logarithm and the quotients are the hardware's approximations
+// of 2 ulp or so: beside the arguments' rounding in fp32 they add little (w, prob
+// and lse are off by 1e-7 of themselves); the logarithm's error is absolute, so
+// that an lse near 0 has fewer right bits.
+//
+// 65536 tokens x 160 bf16 logits, k = 8, masked: forward 16 us with a lane a token
+// (160 instructions a token; its bytes take 4 us; with a warp a token 24: 360
+// instructions), finishing sums 5 us, backward 15.4 us (220 instructions a token;
+// its bytes take 7 us). Both are bound by latency: the forward kernel issues in
+// 36% of its cycles (integer pipe 41% busy, DRAM 12%), since a group's rows are
+// waited for with nothing of the next one under way; the backward kernel in 52%
+// (42%, 16%), with 4 bytes a lane and load. fp32 logits, all a warp a token:
+// forward 35 us, backward 18.6 us. 8 tokens x 128: one launch, 3.1 us.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -508,9 +518,9 @@ __global__ void __launch_bounds__(kRtWarps * 32, 2) k_router_fwd(RouterFwd a, in
 // sums go over the tokens. Rows lie an odd number of 16 bytes apart, so that
 // neither way of reading meets bank conflicts. 160 instructions a token with 160
 // experts, where a warp a token takes 360. At 65536 tokens an SM has 13.5 of
-// these groups of 32, and a quarter of it (one scheduler) 3 or 4: of the 17 us,
-// 3.3 for each of the four, bound by the integer pipe, and the rest is the rows'
-// way from memory and the statistics.
+// these groups of 32, and a quarter of it (one scheduler) 3 or 4, each of which
+// waits for its own rows before it starts: of the 16 us, 3.3 for each of the four,
+// and the rest is the statistics.
 constexpr int kRtLaneWarps = 8;
 
 __device__ __forceinline__ void exchange(int32_t& a, int32_t& b) {
@@ -846,11 +856,21 @@ RouterGrid router_grid(int T) {
 // Whether a call takes a lane a token: 16-bit logits in whole 16-byte pieces, at
 // most the eight of its list, and tokens enough for the SMs' warps, 32 to each.
 // us a forward call (bf16, masked), a warp / a lane a token:
-//   128 experts, k = 8   20480: 12.9 / 14.4   32768: 16.1 / 15.0   65536: 25.2 / 21.6   200000: 63 / 49
-//   128 experts, k = 1   20480: 10.9 / 13.8   32768: 13.4 / 13.9   65536: 19.7 / 20.5   200000: 47 / 45
-//   160 experts, k = 8   20480: 14.5 / 14.4   32768: 18.6 / 15.0   65536: 28.9 / 21.6   200000: 75 / 49
-//   256 experts, k = 8   20480: 16.4 / 16.8   32768: 21.6 / 18.2   65536: 34.5 / 29.9   200000: 92 / 78
-//   64 experts, k = 8    20480: 11.9 / 11.9   32768: 14.5 / 12.8   65536: 21.7 / 17.0   200000: 53 / 37
+//   tokens               20480         32768         49152         65536         200000
+//   8 experts, k = 1     9.8 / 9.3     11.9 / 9.2    14.4 / 10.3   16.9 / 10.8   38 / 19
+//   8 experts, k = 8     11.3 / 10.3   14.4 / 11.3   18.0 / 13.8   21.6 / 15.4   54 / 30
+//   64 experts, k = 1    9.8 / 11.3    11.9 / 11.8   14.4 / 13.8   16.8 / 14.5   37 / 29
+//   64 experts, k = 8    11.8 / 11.4   14.4 / 12.3   18.2 / 14.9   21.6 / 16.4   53 / 36
+//   128 experts, k = 1   10.8 / 14.4   13.4 / 14.5   16.7 / 19.0   19.6 / 20.5   47 / 45
+//   128 experts, k = 4   11.8 / 14.2   14.4 / 14.4   18.0 / 19.1   21.6 / 20.6   53 / 46
+//   128 experts, k = 8   13.0 / 14.9   16.3 / 14.9   20.6 / 19.5   25.2 / 21.6   63 / 50
+//   160 experts, k = 1   12.8 / 13.9   15.0 / 14.4   19.5 / 19.4   23.5 / 20.0   58 / 44
+//   160 experts, k = 8   14.4 / 14.4   18.5 / 14.9   24.0 / 20.1   29.0 / 21.6   74 / 49
+//   256 experts, k = 1   13.9 / 16.4   18.0 / 16.9   23.1 / 24.1   27.9 / 27.7   72 / 70
+//   256 experts, k = 8   16.1 / 17.0   21.6 / 18.0   28.2 / 26.4   34.4 / 29.9   92 / 79
+// The one limit on tokens is where most of these are even or better; with 128
+// experts and k below 8 it comes too early (14% at the worst, 49152 tokens, k = 1),
+// and a limit that moved with k would lose as much with 8, 64 and 160 experts.
 constexpr int kRtLaneTokens = 32768;
 
 bool router_lanes(const RouterFwd& a, int32_t dtype) {
