@@ -739,9 +739,10 @@ class _MxFp4:
     """One prepared set of MXFP4 matrices: codes uint8 [E, R, 16 B] and scales
     uint8 [E, R, B] on the device (kept alive here), with one workspace. Calls
     that share it run one after the other: one on another stream than the last
-    waits for that one, and threads take turns. Handles of their own let calls
-    overlap. Of calls captured in a CUDA graph only the capture is seen here: a
-    replay has to be ordered with the handle's other calls by its user."""
+    waits for that stream (which must still exist), and threads take turns.
+    Handles of their own let calls overlap. Of calls captured in a CUDA graph
+    only the capture is seen here: a replay has to be ordered with the handle's
+    other calls by its user."""
 
     def __init__(self, codes, scales, K: int, max_rows: int, gated: bool):
         torch = _torch()
@@ -776,10 +777,13 @@ class _MxFp4:
         """Makes the current stream wait for the last call's, if that is another one."""
         torch = _torch()
         now, last = torch.cuda.current_stream(self.device), self._stream
-        capturing = torch.cuda.is_current_stream_capturing()
-        with torch.cuda.stream(last):
-            same = torch.cuda.is_current_stream_capturing() == capturing
-        if same:  # (a capture cannot wait for what runs outside it, nor what runs for a capture)
+
+        def capturing(stream):  # (the default stream is in no capture, and may not be asked beside one)
+            with torch.cuda.stream(stream):
+                return stream.cuda_stream != 0 and torch.cuda.is_current_stream_capturing()
+
+        # (a capture cannot wait for what runs outside it, nor what runs for a capture)
+        if capturing(now) == capturing(last):
             now.wait_stream(last)
         self._stream, self._raw = now, now.cuda_stream
 
