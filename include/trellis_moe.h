@@ -490,6 +490,108 @@ tm_status trellis_moe_mxfp4_set_wait_test(tm_mxfp4* h, uint64_t wait_limit_ns, i
 
 void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
 
+/* ------------------------------------------------------------------------
+ * Products by expert with 16-bit weights (bf16 or fp16 throughout), with both
+ * gradients. Route r = t * topk + j goes to expert ids[r] and reads row s(r) of
+ * x: t (per_route 0) or r (per_route 1):
+ *   y_r  = W_e x_s(r)                       W_e [N, K]
+ *   dx_s = sum of W_e^T dy_r over the routes r that read row s
+ *   dW_e = sum of dy_r x_s(r)^T over the expert's routes
+ * Sums are in fp32 and in an order that depends on the arguments alone: equal
+ * calls give equal bits. 1 <= E <= 256, 1 <= topk <= 32, T * topk <= 2^22,
+ * N and K <= 2^20.
+ *
+ * The plan: order [R] holds the R routes by expert, in ascending order within
+ * one, those whose id is outside 0..E-1 last; offsets [E + 1] where each group
+ * begins. flags [1] is the error word, started anew: bit 0 is set if an id was
+ * outside 0..E-1; the products set bit 1 if a pipeline wait gave up. Made once
+ * for a routing, it serves any number of products. R = 0 is a plan of no routes. */
+tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int32_t* order, int32_t* offsets,
+                                  uint32_t* flags, void* stream);
+
+/* out [T * topk, N] in route order, of out_dtype; a route of no expert gives a
+ * row of zeros. x: row s at x + s * ldx elements; w: row n of expert e at
+ * w + e * lde + n * ldw elements. T = 0 is a no-op. */
+tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx, int32_t per_route, const void* w,
+                                      int64_t ldw, int64_t lde, const int32_t* order, const int32_t* offsets, int32_t T,
+                                      int32_t topk, int32_t E, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                                      uint32_t* flags, void* stream);
+
+/* grad_x [T, K] (per_route: [T * topk, K]), contiguous, of `dtype`, from
+ * grad_out [T * topk, N] in route order, row r at grad_out + r * ldg elements.
+ * A token's routes are summed in fp32, in order j, through the workspace
+ * (16-byte aligned, contents ignored; size 0 with per_route: NULL will do). */
+size_t trellis_moe_experts_grad_x_workspace_size(int32_t T, int32_t topk, int32_t K, int32_t per_route);
+tm_status trellis_moe_experts_grad_x(const void* grad_out, int32_t dtype, int64_t ldg, int32_t per_route, const void* w,
+                                     int64_t ldw, int64_t lde, const int32_t* order, const int32_t* offsets, int32_t T,
+                                     int32_t topk, int32_t E, int32_t N, int32_t K, void* grad_x, uint32_t* flags,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_w [E, N, K], contiguous, of grad_dtype; an expert without routes gets
+ * zeros (T = 0: all do). */
+tm_status trellis_moe_experts_grad_w(const void* x, int32_t dtype, int64_t ldx, int32_t per_route, const void* grad_out,
+                                     int64_t ldg, const int32_t* order, const int32_t* offsets, int32_t T, int32_t topk,
+                                     int32_t E, int32_t N, int32_t K, void* grad_w, int32_t grad_dtype, uint32_t* flags,
+                                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens. For a row l of V logits (row t at
+ * logits + t * ld elements) and u = l / temperature:
+ *   logprob [T]       u_y - lse(u) of the row's target y; 0 where y is outside 0..V-1 (no target)
+ *   entropy [T]       -sum p ln p, p = softmax(u)
+ *   stats [T, 2]      max l, and ln sum exp((l - max l) / temperature): lse(u) = max l / temperature + the second
+ *   top_ids, top_logprobs [T, top]   the `top` largest, descending, ties to the lowest id
+ * targets: int32 or int64 (target_bytes 4 or 8), [T]. Logits of -inf have
+ * probability 0. A row that is -inf throughout: stats (0, -inf), logprob and
+ * top_logprobs -inf, entropy 0, and no probability in the gradient. A row with a
+ * NaN or +inf: logprob, entropy and top_logprobs NaN; NaN (of either sign)
+ * counts as the largest. 1 <= V <= 2^30, 0 <= top <= min(V, 32). T = 0 is a
+ * no-op. Sums are taken in a fixed order: equal calls give equal bits. */
+tm_status trellis_moe_token_logprobs(const void* logits, int32_t dtype, int64_t ld, const void* targets,
+                                     int32_t target_bytes, int32_t T, int32_t V, float temperature, int32_t top,
+                                     float* logprob, float* entropy, float* stats, int32_t* top_ids, float* top_logprobs,
+                                     void* stream);
+
+/* grad_logits (of the logits' type, written; row t at grad_logits + t * grad_ld
+ * elements) from the forward call's inputs and entropy and stats, and
+ * grad_logprob [T] and grad_entropy [T] (either may be NULL: none). grad_logits
+ * may be logits itself, with grad_ld = ld; otherwise the two must not overlap. */
+tm_status trellis_moe_token_logprobs_backward(const void* logits, int32_t dtype, int64_t ld, const void* targets,
+                                              int32_t target_bytes, int32_t T, int32_t V, float temperature,
+                                              const float* entropy, const float* stats, const float* grad_logprob,
+                                              const float* grad_entropy, void* grad_logits, int64_t grad_ld, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's largest logits: its values v_j [T, n] at tokens
+ * i_j [T, n] (ids int32 or int64, id_bytes 4 or 8; values of any tm_dtype).
+ * Entries whose id is outside 0..V-1 count as absent, so lists may differ in
+ * length; the same id twice counts twice. With p = softmax(logits / temperature):
+ *   q = softmax(v / temperature) over the row's entries, or, with teacher_lse [T]
+ *       (the teacher's log-sum-exp of its logits / temperature), q_j =
+ *       exp(v_j / temperature - teacher_lse): the teacher's own probabilities,
+ *       which add up to less than 1
+ *   loss [T] = sum_j q_j (ln q_j - ln p_(i_j))          (terms of q_j = 0 are 0)
+ *   gradient = grad_loss / temperature (p_i sum_j q_j - sum_(j: i_j = i) q_j)
+ * mask [T] (NULL: all true): a row where it is 0 has loss and gradient 0, and
+ * its logits are not read. stats as above (a masked row's are 0). Rows with -inf,
+ * NaN or +inf as above. 1 <= n <= 256. The gradient's place as above.
+ * loss_grad is both at once, the logits read once, for a caller who knows
+ * grad_loss beforehand (1/T for a mean). */
+tm_status trellis_moe_distill_forward(const void* logits, int32_t dtype, int64_t ld, const void* ids, int32_t id_bytes,
+                                      const void* values, int32_t values_dtype, int32_t n, const uint8_t* mask,
+                                      const float* teacher_lse, int32_t T, int32_t V, float temperature, float* loss,
+                                      float* stats, void* stream);
+tm_status trellis_moe_distill_backward(const void* logits, int32_t dtype, int64_t ld, const void* ids, int32_t id_bytes,
+                                       const void* values, int32_t values_dtype, int32_t n, const uint8_t* mask,
+                                       const float* teacher_lse, int32_t T, int32_t V, float temperature,
+                                       const float* stats, const float* grad_loss, void* grad_logits, int64_t grad_ld,
+                                       void* stream);
+tm_status trellis_moe_distill_loss_grad(const void* logits, int32_t dtype, int64_t ld, const void* ids, int32_t id_bytes,
+                                        const void* values, int32_t values_dtype, int32_t n, const uint8_t* mask,
+                                        const float* teacher_lse, int32_t T, int32_t V, float temperature,
+                                        const float* grad_loss, float* loss, void* grad_logits, int64_t grad_ld,
+                                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

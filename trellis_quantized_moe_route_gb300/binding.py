@@ -40,6 +40,10 @@ EXPORTED = [
     "trellis_moe_mxfp4_quantize", "trellis_moe_mxfp4_dequantize", "trellis_moe_mxfp4_prepare",
     "trellis_moe_mxfp4_workspace_size", "trellis_moe_mxfp4_forward", "trellis_moe_mxfp4_forward_experts",
     "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_set_wait_test", "trellis_moe_mxfp4_destroy",
+    "trellis_moe_expert_plan", "trellis_moe_experts_forward", "trellis_moe_experts_grad_x_workspace_size",
+    "trellis_moe_experts_grad_x", "trellis_moe_experts_grad_w",
+    "trellis_moe_token_logprobs", "trellis_moe_token_logprobs_backward",
+    "trellis_moe_distill_forward", "trellis_moe_distill_backward", "trellis_moe_distill_loss_grad",
 ]
 
 
@@ -88,7 +92,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError("libtrellis_moe.so is not built (%s); run __graft_entry__.build()" % path)
     lib = ctypes.CDLL(path)
-    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    distill = [P, I32, I64, P, I32, P, I32, I32, P, P, I32, I32, F32]  # up to the temperature
     sig = {
         "trellis_moe_prepare": (I32, [ctypes.POINTER(LayerDesc), ctypes.POINTER(P), ctypes.POINTER(SZ)]),
         "trellis_moe_workspace_size": (SZ, [P, I32]),
@@ -126,6 +131,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "trellis_moe_mxfp4_poll_error": (I32, [P, P, ctypes.POINTER(ctypes.c_uint32), P]),
         "trellis_moe_mxfp4_set_wait_test": (I32, [P, ctypes.c_uint64, I32]),
         "trellis_moe_mxfp4_destroy": (None, [P]),
+        "trellis_moe_expert_plan": (I32, [P, I32, I32, P, P, P, P]),
+        "trellis_moe_experts_forward": (I32, [P, I32, I64, I32, P, I64, I64, P, P, I32, I32, I32, I32, I32, P, I32, P, P]),
+        "trellis_moe_experts_grad_x_workspace_size": (SZ, [I32, I32, I32, I32]),
+        "trellis_moe_experts_grad_x": (I32, [P, I32, I64, I32, P, I64, I64, P, P, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
+        "trellis_moe_experts_grad_w": (I32, [P, I32, I64, I32, P, I64, P, P, I32, I32, I32, I32, I32, P, I32, P, P]),
+        "trellis_moe_token_logprobs": (I32, [P, I32, I64, P, I32, I32, I32, F32, I32, P, P, P, P, P, P]),
+        "trellis_moe_token_logprobs_backward": (I32, [P, I32, I64, P, I32, I32, I32, F32, P, P, P, P, P, I64, P]),
+        "trellis_moe_distill_forward": (I32, distill + [P, P, P]),
+        "trellis_moe_distill_backward": (I32, distill + [P, P, P, I64, P]),
+        "trellis_moe_distill_loss_grad": (I32, distill + [P, P, P, I64, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -885,3 +900,296 @@ class MxFp4Experts(_MxFp4):
         self._run(self.lib.trellis_moe_mxfp4_forward_experts, x.data_ptr(), _dtype_code(x.dtype), ld,
                   1 if per_route else 0, ids.data_ptr(), T, topk, out.data_ptr(), code)
         return out
+
+
+# ---------------------------------------------------------------------------
+# Products by expert with 16-bit weights, log probabilities of given tokens and
+# distillation (device tensors in, device tensors out; streams as above)
+# ---------------------------------------------------------------------------
+class ExpertPlan:
+    """Where each expert's routes are (see trellis_moe_expert_plan), made by
+    expert_plan once for a routing and used by any number of products."""
+
+    __slots__ = ("T", "topk", "E", "index", "device", "words", "order_ptr", "offsets_ptr", "flags_ptr")
+
+    def __init__(self, T: int, topk: int, E: int, words):
+        # one allocation: flags, three words of padding, offsets, order
+        self.T, self.topk, self.E, self.words = T, topk, E, words
+        self.index, self.device = words.get_device(), words.device
+        self.flags_ptr = words.data_ptr()
+        self.offsets_ptr = self.flags_ptr + 16
+        self.order_ptr = self.offsets_ptr + 4 * (E + 1)
+
+    @property
+    def offsets(self):
+        """int32 [E + 1]: the place of each expert's first route in `order`."""
+        return self.words[4:5 + self.E]
+
+    @property
+    def order(self):
+        """int32 [T * topk]: routes by expert; those of no expert last."""
+        return self.words[5 + self.E:]
+
+    def poll_error(self, stream=None) -> int:
+        """The error flags of the plan and of the products made with it, and
+        clears them: bit 0 an expert id out of range, bit 1 a wait that gave up.
+        Waits for the stream."""
+        if stream is not None:
+            with _given(stream, "the plan", self):
+                return self.poll_error()
+        flags = int(self.words[0])
+        self.words[0].zero_()
+        return flags
+
+
+def expert_plan(ids, E: int, stream=None) -> ExpertPlan:
+    """Plan of a routing: ids int32 [T, topk] on the device, E experts."""
+    if stream is not None:
+        with _given(stream, "ids", ids):
+            return expert_plan(ids, E)
+    lib = _start()
+    _on_device("ids", ids, None, _i32)
+    if len(ids.shape) != 2:
+        raise ValueError("ids must have two dimensions, not %d" % len(ids.shape))
+    T, topk = ids.shape
+    R, E = _size("routes", T * topk), _size("E", E)
+    plan = ExpertPlan(T, topk, E, _empty(5 + max(E, 0) + R, dtype=_i32, device=ids.device))
+    _launch(lib.trellis_moe_expert_plan, plan.index, ids.data_ptr(), R, E, plan.order_ptr, plan.offsets_ptr, plan.flags_ptr)
+    return plan
+
+
+def _half(name, dtype) -> int:
+    code = _dtype_code(dtype)
+    if code == 0:
+        raise ValueError("%s must be bfloat16 or float16, not %s" % (name, dtype))
+    return code
+
+
+def _expert_weights(w, plan, dtype):
+    """N, K and the strides of w [E, N, K], whose rows and experts may lie apart."""
+    shape = w.shape
+    if len(shape) != 3 or shape[0] != plan.E:
+        raise ValueError("w must have shape [%d, N, K], not %s" % (plan.E, tuple(shape)))
+    _on_device("w", w, plan.index, dtype, contiguous=False)
+    _, N, K = shape
+    if N > _MOST or K > _MOST:
+        raise ValueError("w %s is too large" % (tuple(shape),))
+    if w.is_contiguous():
+        return N, K, K, N * K
+    lde, ldw, step = w.stride()
+    if K > 1 and step != 1:
+        raise ValueError("w: the last dimension must be contiguous")
+    if N <= 1:
+        ldw = K
+    if plan.E <= 1:
+        lde = N * ldw
+    if ldw < K or lde < 0:
+        raise ValueError("w: rows overlap (strides %s)" % (w.stride(),))
+    return N, K, ldw, lde
+
+
+def _expert_rows(name, t, plan, rows, cols, dtype):
+    """The row stride of x or grad_out."""
+    n, c, ld = _rows_2d(name, t)
+    if n != rows or c != cols:
+        raise ValueError("%s must have shape [%d, %d], not [%d, %d]" % (name, rows, cols, n, c))
+    _on_device(name, t, plan.index, dtype, contiguous=False)
+    return ld
+
+
+def experts_forward(x, w, plan: ExpertPlan, per_route: bool = False, out=None, out_dtype=None, stream=None):
+    """Rows [T * topk, N] in route order: the route's expert's w [E, N, K] times
+    row t of x [T, K] (per_route: row r of x [T * topk, K]), bfloat16 or
+    float16, of out_dtype (default x's)."""
+    if stream is not None:
+        with _given(stream, "x", x):
+            return experts_forward(x, w, plan, per_route, out, out_dtype)
+    lib = _start()
+    dtype = x.dtype
+    code, R = _half("x", dtype), plan.T * plan.topk
+    N, K, ldw, lde = _expert_weights(w, plan, dtype)
+    ldx = _expert_rows("x", x, plan, R if per_route else plan.T, K, dtype)
+    if out is None:
+        out_dtype = dtype if out_dtype is None else out_dtype
+        out_code = _dtype_code(out_dtype)
+        out = _empty((R, N), dtype=out_dtype, device=x.device)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        out_code = _dtype_code(_on_device("out", out, plan.index, None, (R, N)).dtype)
+    _launch(lib.trellis_moe_experts_forward, plan.index, x.data_ptr(), code, ldx, 1 if per_route else 0, w.data_ptr(), ldw,
+            lde, plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, out.data_ptr(), out_code, plan.flags_ptr)
+    return out
+
+
+def experts_backward(x, w, plan: ExpertPlan, grad_out, per_route: bool = False, want_x: bool = True, want_w: bool = True,
+                     grad_w_dtype=None, stream=None):
+    """(grad_x of x's shape, grad_w of w's shape, both contiguous) of
+    experts_forward from grad_out [T * topk, N] of x's type; None where not
+    wanted. grad_w is of grad_w_dtype (default w's; float32 for sums over
+    several batches)."""
+    if stream is not None:
+        with _given(stream, "x", x):
+            return experts_backward(x, w, plan, grad_out, per_route, want_x, want_w, grad_w_dtype)
+    lib = _start()
+    dtype, flag = x.dtype, 1 if per_route else 0
+    code, R = _half("x", dtype), plan.T * plan.topk
+    N, K, ldw, lde = _expert_weights(w, plan, dtype)
+    ldx = _expert_rows("x", x, plan, R if per_route else plan.T, K, dtype)
+    ldg = _expert_rows("grad_out", grad_out, plan, R, N, dtype)
+    gx = gw = None
+    if want_x:
+        gx = _empty((x.shape[0], K), dtype=dtype, device=x.device)
+        wsb = lib.trellis_moe_experts_grad_x_workspace_size(plan.T, plan.topk, K, flag)
+        ws = _empty(wsb, dtype=_u8, device=x.device) if wsb else None
+        _launch(lib.trellis_moe_experts_grad_x, plan.index, grad_out.data_ptr(), code, ldg, flag, w.data_ptr(), ldw, lde,
+                plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, gx.data_ptr(), plan.flags_ptr, _opt(ws),
+                wsb)
+    if want_w:
+        grad_w_dtype = dtype if grad_w_dtype is None else grad_w_dtype
+        gcode = _dtype_code(grad_w_dtype)
+        gw = _empty((plan.E, N, K), dtype=grad_w_dtype, device=x.device)
+        _launch(lib.trellis_moe_experts_grad_w, plan.index, x.data_ptr(), code, ldx, flag, grad_out.data_ptr(), ldg,
+                plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, gw.data_ptr(), gcode, plan.flags_ptr)
+    return gx, gw
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs (see trellis_moe_token_logprobs)."""
+    logprob: Any       # float32 [T]
+    entropy: Any       # float32 [T]
+    top_ids: Any       # int32 [T, top]
+    top_logprobs: Any  # float32 [T, top]
+    stats: Any         # float32 [T, 2]
+
+
+def _index_bytes(name, t, index, shape) -> int:
+    _on_device(name, t, index, None, shape)
+    if t.dtype is _i32:
+        return 4
+    if t.dtype is _torch_mod.int64:
+        return 8
+    raise ValueError("%s must be int32 or int64, not %s" % (name, t.dtype))
+
+
+def _grad_place(out, logits, T, V):
+    """The tensor for a gradient of logits [T, V], and its row stride."""
+    if out is None:
+        return _empty((T, V), dtype=logits.dtype, device=logits.device), V
+    rows, cols, ld = _rows_2d("out", out)
+    _on_device("out", out, logits.get_device(), logits.dtype, (T, V), contiguous=False)
+    return out, ld
+
+
+def token_logprobs(logits, targets, top: int = 0, temperature: float = 1.0, stream=None) -> TokenLogprobs:
+    """Log probability of each row's target (int32 or int64 [T]; outside 0..V-1:
+    none), entropy, and the `top` largest, of softmax(logits / temperature);
+    logits [T, V] float32, bfloat16 or float16, rows may lie apart."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return token_logprobs(logits, targets, top, temperature)
+    lib = _start()
+    T, V, ld = _rows_2d("logits", logits)
+    dev, index, top = logits.device, logits.get_device(), _size("top", top)
+    width = _index_bytes("targets", targets, index, (T,))
+    kk = min(max(top, 0), V)  # (what is out of range is refused below)
+    logprob, entropy = _empty(T, dtype=_f32, device=dev), _empty(T, dtype=_f32, device=dev)
+    stats = _empty((T, 2), dtype=_f32, device=dev)
+    ids, lp = _empty((T, kk), dtype=_i32, device=dev), _empty((T, kk), dtype=_f32, device=dev)
+    _launch(lib.trellis_moe_token_logprobs, index, logits.data_ptr(), _dtype_code(logits.dtype), ld, targets.data_ptr(), width,
+            T, V, temperature, top, logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), ids.data_ptr(), lp.data_ptr())
+    return TokenLogprobs(logprob, entropy, ids, lp, stats)
+
+
+def token_logprobs_backward(logits, targets, fwd: TokenLogprobs, grad_logprob=None, grad_entropy=None,
+                            temperature: float = 1.0, out=None, stream=None):
+    """Gradient of the logits from grad_logprob and grad_entropy (float32 [T],
+    either may be None); fwd, targets and temperature as in the forward call.
+    out may be logits itself."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return token_logprobs_backward(logits, targets, fwd, grad_logprob, grad_entropy, temperature, out)
+    lib = _start()
+    T, V, ld = _rows_2d("logits", logits)
+    index = logits.get_device()
+    width = _index_bytes("targets", targets, index, (T,))
+    _on_device("entropy", fwd.entropy, index, _f32, (T,))
+    _on_device("stats", fwd.stats, index, _f32, (T, 2))
+    _on_device("grad_logprob", grad_logprob, index, _f32, (T,))
+    _on_device("grad_entropy", grad_entropy, index, _f32, (T,))
+    out, gld = _grad_place(out, logits, T, V)
+    _launch(lib.trellis_moe_token_logprobs_backward, index, logits.data_ptr(), _dtype_code(logits.dtype), ld,
+            targets.data_ptr(), width, T, V, temperature, fwd.entropy.data_ptr(), fwd.stats.data_ptr(), _opt(grad_logprob),
+            _opt(grad_entropy), out.data_ptr(), gld)
+    return out
+
+
+class DistillOut(NamedTuple):
+    """Results of distill_forward (see trellis_moe_distill_forward)."""
+    loss: Any   # float32 [T]
+    stats: Any  # float32 [T, 2]
+
+
+def _teacher(logits, ids, values, temperature, mask, teacher_lse):
+    """Checks a distillation call's inputs; returns T, V, the device's index and
+    the C call's arguments up to the temperature."""
+    T, V, ld = _rows_2d("logits", logits)
+    index = logits.get_device()
+    if len(ids.shape) != 2:
+        raise ValueError("ids must have two dimensions, not %d" % len(ids.shape))
+    n = ids.shape[1]
+    width = _index_bytes("ids", ids, index, (T, n))
+    _on_device("values", values, index, None, (T, n))
+    _on_device("teacher_lse", teacher_lse, index, _f32, (T,))
+    return T, V, index, (logits.data_ptr(), _dtype_code(logits.dtype), ld, ids.data_ptr(), width, values.data_ptr(),
+                         _dtype_code(values.dtype), _size("n", n), _mask(mask, index, T), _opt(teacher_lse), T, V,
+                         temperature)
+
+
+def distill_forward(logits, ids, values, temperature: float = 1.0, mask=None, teacher_lse=None, stream=None) -> DistillOut:
+    """Loss of each row against a teacher's largest logits: values [T, n]
+    (float32, bfloat16 or float16) at ids [T, n] (int32 or int64; outside
+    0..V-1: absent), over the listed tokens, or with the teacher's own
+    log-sum-exp teacher_lse (float32 [T], of its logits / temperature). mask: bool
+    or uint8 [T], false for rows without a loss."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return distill_forward(logits, ids, values, temperature, mask, teacher_lse)
+    lib = _start()
+    T, _, index, args = _teacher(logits, ids, values, temperature, mask, teacher_lse)
+    loss, stats = _empty(T, dtype=_f32, device=logits.device), _empty((T, 2), dtype=_f32, device=logits.device)
+    _launch(lib.trellis_moe_distill_forward, index, *args, loss.data_ptr(), stats.data_ptr())
+    return DistillOut(loss, stats)
+
+
+def distill_backward(logits, ids, values, fwd: DistillOut, grad_loss, temperature: float = 1.0, mask=None, teacher_lse=None,
+                     out=None, stream=None):
+    """Gradient of the logits from grad_loss (float32 [T]); the rest as in the
+    forward call. out may be logits itself."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return distill_backward(logits, ids, values, fwd, grad_loss, temperature, mask, teacher_lse, out)
+    lib = _start()
+    T, V, index, args = _teacher(logits, ids, values, temperature, mask, teacher_lse)
+    _on_device("stats", fwd.stats, index, _f32, (T, 2))
+    _on_device("grad_loss", grad_loss, index, _f32, (T,))
+    out, gld = _grad_place(out, logits, T, V)
+    _launch(lib.trellis_moe_distill_backward, index, *args, fwd.stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), gld)
+    return out
+
+
+def distill_loss_grad(logits, ids, values, grad_loss, temperature: float = 1.0, mask=None, teacher_lse=None, out=None,
+                      stream=None):
+    """(loss [T], gradient of the logits) of distill_forward and
+    distill_backward in one pass over the logits, for a grad_loss (float32 [T])
+    that is known beforehand. out may be logits itself."""
+    if stream is not None:
+        with _given(stream, "logits", logits):
+            return distill_loss_grad(logits, ids, values, grad_loss, temperature, mask, teacher_lse, out)
+    lib = _start()
+    T, V, index, args = _teacher(logits, ids, values, temperature, mask, teacher_lse)
+    _on_device("grad_loss", grad_loss, index, _f32, (T,))
+    loss = _empty(T, dtype=_f32, device=logits.device)
+    out, gld = _grad_place(out, logits, T, V)
+    _launch(lib.trellis_moe_distill_loss_grad, index, *args, grad_loss.data_ptr(), loss.data_ptr(), out.data_ptr(), gld)
+    return loss, out
