@@ -328,6 +328,14 @@ cudaError_t launch_ex_general(const ExArgs& a, cudaStream_t st) {
 
 namespace {
 
+cudaError_t ex_product(const ExArgs& a, cudaStream_t st) {
+  if (!ex_tc_ok(a)) return launch_ex_general(a, st);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? launch_ex_tc(a, sms, st) : e;
+}
+
 tm_status ex_check(const ExArgs& a) {
   if (a.dtype != TM_BF16 && a.dtype != TM_F16) return status_fail(TM_EINVAL, "dtype=%d is not TM_BF16 or TM_F16", a.dtype);
   if (!dtype_ok(a.out_dtype)) return status_fail(TM_EINVAL, "out_dtype=%d is not a tm_dtype", a.out_dtype);
@@ -382,7 +390,7 @@ tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx,
   a.out = out, a.flags = flags;
   const tm_status s = ex_check(a);
   if (s != TM_OK || T == 0) return s;
-  const cudaError_t e = launch_ex_general(a, (cudaStream_t)stream);
+  const cudaError_t e = ex_product(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products");
 }
 
@@ -408,7 +416,7 @@ tm_status trellis_moe_experts_grad_x(const void* grad_out, int32_t dtype, int64_
       return status_fail(TM_EWORKSPACE, "workspace of %zu bytes is too small", workspace_bytes);
     if ((long)T * ((K + 7) / 8) >= 1L << 31) return status_fail(TM_EUNSUPPORTED, "T=%d rows of K=%d are too many", T, K);
   }
-  cudaError_t e = launch_ex_general(a, (cudaStream_t)stream);
+  cudaError_t e = ex_product(a, (cudaStream_t)stream);
   if (e == cudaSuccess && !per_route)
     e = launch_ex_sum(static_cast<const float*>(workspace), T, topk, K, grad_x, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products' gradient of x");
@@ -425,7 +433,7 @@ tm_status trellis_moe_experts_grad_w(const void* x, int32_t dtype, int64_t ldx, 
   a.out = grad_w, a.flags = flags;
   const tm_status s = ex_check(a);
   if (s != TM_OK) return s;
-  const cudaError_t e = launch_ex_general(a, (cudaStream_t)stream);
+  const cudaError_t e = ex_product(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products' gradient of w");
 }
 

@@ -38,8 +38,6 @@
 // Every wait is bounded (2 s): one that runs out raises bit 1 of the error
 // word, lets the copies and MMAs in flight finish, frees the tensor memory and
 // returns.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 
 #include "elem.cuh"
@@ -47,6 +45,8 @@
 #include "mxfp4.h"
 #include "mxfp4_mma.cuh"
 #include "status.h"
+#include "tensor_map.h"
+#include "tile_store.cuh"
 
 namespace tmoe {
 
@@ -220,68 +220,6 @@ __device__ int mx_issuer(const MxTcArgs& a, const MxGeom& g, MxBars& B, unsigned
   return it;
 }
 
-// 32 columns (rows of y) of a thread's channel, as T: y[c] for row `row` of
-// lane c, `rows` of them.
-template <typename T>
-__device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__ out, int row, int rows, int n, int N) {
-  T* o = out + n;
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const int r = __shfl_sync(0xFFFFFFFFu, row, c);
-    if (n < N && c < rows) o[(size_t)r * N] = from_f32<T>(y[c]);
-  }
-}
-
-// The same for 16-bit types where rows of y are whole 16-byte words: the four
-// warps of a piece (128 channels) put 16 rows at a time into shared memory and
-// store them from there in 16-byte words, a whole row's 256 bytes by 16 lanes
-// (as single elements a warp's store covered 64 bytes, and storing a piece of
-// 32 rows took 1400 cycles). Neighbouring lanes first swap halves, so that the
-// even one holds both channels of an even row and the odd one of the next; the
-// 64-byte halves of odd rows change places, which keeps the two apart in banks.
-template <typename T>
-__device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __restrict__ out, int row, int rows, int tile,
-                                                 int N, unsigned char* stage, int bar) {
-  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, odd = lane & 1;
-  const uint32_t pick = odd ? 0x3276u : 0x5410u;
-  const int t = quarter * 32 + lane, chunk = t & 15;
-  const bool in = tile * 128 + chunk * 8 < N;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (h * 16 >= rows) break;
-#pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      uint32_t p;
-      T* e = reinterpret_cast<T*>(&p);
-      e[0] = from_f32<T>(y[h * 16 + c]);
-      e[1] = from_f32<T>(y[h * 16 + c + 1]);
-      const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
-      const int word = (quarter * 16 + (lane >> 1)) ^ (odd << 4);
-      *reinterpret_cast<uint32_t*>(stage + (c + odd) * 256 + word * 4) = __byte_perm(p, q, pick);
-    }
-    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = k * 8 + (t >> 4);
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((chunk * 16) ^ ((r & 1) << 6)));
-      const int to = __shfl_sync(0xFFFFFFFFu, row, h * 16 + r);
-      if (in && h * 16 + r < rows)
-        *reinterpret_cast<uint4*>(out + (size_t)to * N + tile * 128 + chunk * 8) = v;
-    }
-    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
-  }
-}
-
-// Whether all four warps of a part say yes, by its named barrier.
-__device__ __forceinline__ bool mx_vote_part(bool yes, int bar) {
-  uint32_t all;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-               : "=r"(all)
-               : "r"((uint32_t)yes), "r"(bar)
-               : "memory");
-  return all != 0;
-}
-
 template <bool GATED, bool EXPERTS, typename T>
 __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint32_t tmem, unsigned char* stage,
                             volatile int* abort, uint64_t limit) {
@@ -404,23 +342,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 mx_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-  }();
-  return fn;
-}
-
 // Rows of codes as bytes, boxes of 128 bytes (256 values) x `box` rows. Box
 // starts are multiples of 128 bytes, rows of 16; what lies past a row or the
 // last row reads as 0.
 cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, int box) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
+  const auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t bytes = (cuuint64_t)mx_blocks(K) * 16;
   cuuint64_t dims[2] = {bytes, (cuuint64_t)rows};
