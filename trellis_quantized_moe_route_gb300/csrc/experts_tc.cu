@@ -8,9 +8,12 @@
 //   grad_w   D[n, k]  A = dy^T (M contiguous)  B = x^T (N contiguous)     contraction over the expert's routes
 // With the routes as columns, a block of them may have any multiple of 16 rows,
 // so that experts with few routes waste little, and the weights, which bound
-// these products by their bytes, are read by every block once. Rows are fetched
-// where they lie, by the plan's order (gather copies of four rows): there is no
-// sorted copy of x or dy, and results go straight to route order.
+// these products by their bytes, are read by every block once. Rows of x and dy
+// are fetched where they lie, by the plan's order: there is no sorted copy of
+// them, and results go straight to route order. Eight warps fetch them (16 bytes
+// a lane, written in the swizzled layout); the weights come by TMA. (TMA's gather
+// of four rows, issued lane by lane, took 65-73 cycles each: 1.8 us for a stage
+// of 208 rows, of which the MMAs need 0.2.)
 #include <algorithm>
 
 #include "elem.cuh"
@@ -25,7 +28,8 @@ namespace tmoe {
 namespace {
 
 constexpr int kEtEpiWarps = 8;
-constexpr int kEtThreads = (kEtEpiWarps + 2) * 32;
+constexpr int kEtRowWarps = 8;
+constexpr int kEtThreads = (kEtEpiWarps + kEtRowWarps + 2) * 32;
 constexpr int kEtMaxRing = 12;
 constexpr uint32_t kEtSmem = 224 * 1024;
 constexpr uint32_t kEtABytes = 128 * 128;      // 128 rows of 64 elements, or 64 of 128
@@ -34,7 +38,9 @@ constexpr uint32_t kEtStoreBytes = 16 * 256;   // for four epilogue warps
 constexpr int kEtMaxGroups = 257 + 1;
 
 struct EtArgs {
-  CUtensorMap amap, bmap;
+  CUtensorMap wmap;         // forward, grad_x
+  const void *x, *g;
+  int64_t ldx, ldg;         // elements
   int E, R, M, depth;       // M: output channels; depth: contraction (forward, grad_x)
   int cols;                 // grad_w: columns of dW
   int bn;                   // most columns of a unit
@@ -45,7 +51,8 @@ struct EtArgs {
 };
 
 struct EtBars {
-  uint64_t full[kEtMaxRing], empty[kEtMaxRing];
+  uint64_t full[kEtMaxRing], wfull[kEtMaxRing];  // the rows' part of a stage, the weights' part
+  uint64_t empty[kEtMaxRing];
   uint64_t acc_full[2], acc_empty[2];
 };
 
@@ -90,13 +97,10 @@ __device__ __forceinline__ void et_tma_3d(uint32_t dst, const CUtensorMap* map, 
   asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
                ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-// Four rows of 64 elements, from column x.
-__device__ __forceinline__ void et_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n"
-      ::"r"(dst), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar) : "memory");
+// 16 bytes to shared memory, of which the last 16 - `bytes` are zeros.
+__device__ __forceinline__ void et_copy(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-
 // Descriptor of an operand that is contiguous along M or N, 128-byte swizzled:
 // 64 of those by 8 of the contraction are an atom of 1024 bytes; atoms follow each
 // other along the contraction, and groups of 64 along M or N are kEtGroup apart. A step
@@ -113,79 +117,131 @@ __device__ __forceinline__ uint32_t et_idesc(int bf16, int n) {
          ((MODE == kExGradW ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// (returns the stages it loaded)
+// The weights' part of the stages. (Returns the stages it loaded.)
 template <int MODE>
 __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
-                         FastDiv tiles, FastDiv ctiles, FastDiv topk, volatile int* abort) {
-  const int lane = threadIdx.x & 31;
+                         FastDiv tiles, FastDiv ctiles, volatile int* abort) {
   const bool lead = mx_elect();
-  const uint32_t bar0 = smem_u32(&B.full[0]);
+  const uint32_t bar0 = smem_u32(&B.wfull[0]);
   MxRing r;
   int it = 0;
-  auto source = [&](int route) { return a.per_route ? route : (int)topk.div((uint32_t)route); };
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64;
-    if (stages == 0) continue;
-    int q[2][4];
-    if (MODE != kExGradW) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int route = __ldg(a.order + m.slot0 + min((lane + 32 * h) * 4 + i, m.rows - 1));  // (past the last row: any)
-          q[h][i] = MODE == kExForward ? source(route) : route;
-        }
-    }
-    const int quads = et_up16(m.rows) / 4;
-    auto routes = [&](int s, int (&to)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[i] = __ldg(a.order + m.slot0 + min(s * 64 + (lane & 15) * 4 + i, m.depth - 1));
-    };
-    if (MODE == kExGradW) routes(0, q[0]);
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
       if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
       const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
-      if (MODE == kExGradW) {
-        const int n = et_up16(min(64, m.depth - s * 64)), groups = (m.rows + 63) / 64;
-        const int agroups = a.M - m.tile * 128 > 64 ? 2 : 1;  // (what lies past the last channel is not stored)
-        if (lead) mx_expect(bar, (uint32_t)(n * 128 * (agroups + groups)));
-        __syncwarp();
-        int x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = source(q[0][i]);
-        const int quad = lane & 15, half = lane >> 4;
-        if (quad * 4 < n) {
-          if (half < agroups) et_gather4(st + half * kEtGroup + quad * 512, &a.amap, m.tile * 128 + half * 64, q[0], bar);
-          for (int c = half; c < groups; c += 2)
-            et_gather4(st + kEtABytes + c * kEtGroup + quad * 512, &a.bmap, m.col0 + c * 64, x, bar);
+      if (lead) {
+        mx_expect(bar, kEtABytes);
+        if (MODE == kExForward) {
+          et_tma_3d(st, &a.wmap, s * 64, m.tile * 128, m.expert, bar);
+        } else {
+          et_tma_3d(st, &a.wmap, m.tile * 128, s * 64, m.expert, bar);
+          et_tma_3d(st + kEtGroup, &a.wmap, m.tile * 128 + 64, s * 64, m.expert, bar);
         }
-        if (s + 1 < stages) routes(s + 1, q[0]);
-      } else {
-        if (lead) {
-          mx_expect(bar, kEtABytes + (uint32_t)quads * 512);
-          if (MODE == kExForward) {
-            et_tma_3d(st, &a.amap, s * 64, m.tile * 128, m.expert, bar);
-          } else {
-            et_tma_3d(st, &a.amap, m.tile * 128, s * 64, m.expert, bar);
-            et_tma_3d(st + kEtGroup, &a.amap, m.tile * 128 + 64, s * 64, m.expert, bar);
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (lane + 32 * h < quads) et_gather4(st + kEtABytes + (uint32_t)(lane + 32 * h) * 512, &a.bmap, s * 64, q[h], bar);
       }
     }
   }
   return it;
 }
 
+// The rows' part. A lane copies 16 bytes of every 32nd row, and arrives at the
+// stage's barrier when they have landed. (They are written by the generic proxy;
+// the issuer's fence, behind that barrier, shows them to the tensor cores.)
+template <int MODE>
+__device__ void et_rows(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
+                        FastDiv tiles, FastDiv ctiles, FastDiv topk, volatile int* abort) {
+  const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - kEtEpiWarps;
+  const int chunk = lane & 7, row = warp * 4 + (lane >> 3);  // of each 32 rows
+  const uint32_t at = (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
+  const uint16_t *x = static_cast<const uint16_t*>(a.x), *dy = static_cast<const uint16_t*>(a.g);
+  auto source = [&](int route) { return a.per_route ? route : (int)topk.div((uint32_t)route); };
+  MxRing r;
+  int it = 0;
+  auto stage = [&](auto copy) {  // one stage's copies
+    if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return false;
+    copy(base + (uint32_t)r.slot * stage_bytes + at);
+    cp_async_mbar_arrive(&B.full[r.slot]);
+    ++it;
+    r.next(ring);
+    return true;
+  };
+  bool ok = true;
+  if (MODE == kExGradW) {
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+      const int stages = (m.depth + 63) / 64, groups = (m.rows + 63) / 64;
+      int route[2];
+      auto routes = [&](int s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = s * 64 + h * 32 + row;
+          route[h] = i < m.depth ? __ldg(a.order + m.slot0 + i) : -1;
+        }
+      };
+      if (stages) routes(0);
+      const int n0 = m.tile * 128 + chunk * 8, k0 = m.col0 + chunk * 8;
+      for (int s = 0; s < stages && ok; ++s) {
+        ok = stage([&](uint32_t to) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h * 32 >= et_up16(m.depth - s * 64)) break;
+            const bool in = route[h] >= 0;  // (rows past the last route: zeros)
+            const uint16_t* p = dy + (in ? (size_t)route[h] * a.ldg : 0);
+            const uint16_t* q = x + (in ? (size_t)source(route[h]) * a.ldx : 0);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int bytes = in ? min(16, max(0, (a.M - n0 - c * 64) * 2)) : 0;
+              et_copy(to + c * kEtGroup + h * 4096, bytes ? p + n0 + c * 64 : dy, bytes);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c >= groups) break;
+              const int bytes = in ? min(16, max(0, (a.cols - k0 - c * 64) * 2)) : 0;
+              et_copy(to + kEtABytes + c * kEtGroup + h * 4096, bytes ? q + k0 + c * 64 : x, bytes);
+            }
+          }
+        });
+        if (s + 1 < stages) routes(s + 1);
+      }
+    }
+  } else {
+    const uint16_t* src = MODE == kExForward ? x : dy;
+    const int64_t ld = MODE == kExForward ? a.ldx : a.ldg;
+    // a unit's rows are looked up while the one before it is copied
+    auto find = [&](int u, int (&to)[8], EtUnit& m) {
+      m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // (past the last row: any)
+        to[j] = j * 32 < m.rows ? __ldg(a.order + m.slot0 + min(j * 32 + row, m.rows - 1)) : 0;
+    };
+    int next[8];
+    EtUnit m, ahead;
+    if ((int)blockIdx.x < units) find(blockIdx.x, next, ahead);
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      m = ahead;
+      const uint16_t* p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = src + (size_t)(MODE == kExForward ? source(next[j]) : next[j]) * ld + chunk * 8;
+      if (u + (int)gridDim.x < units) find(u + gridDim.x, next, ahead);
+      const int stages = (m.depth + 63) / 64, rows = et_up16(m.rows);
+      for (int s = 0; s < stages && ok; ++s) {
+        const int left = (m.depth - s * 64 - chunk * 8) * 2, bytes = min(16, max(0, left));
+        ok = stage([&](uint32_t to) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j * 32 + row < rows) et_copy(to + kEtABytes + j * 4096, bytes ? p[j] + s * 64 : src, bytes);
+        });
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+}
+
 // (returns the stages whose MMAs it issued)
 template <int MODE>
 __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
                          FastDiv tiles, FastDiv ctiles, uint32_t tmem, volatile int* abort) {
-  const int lane = threadIdx.x & 31;
   const bool lead = mx_elect();
   MxRing r;
   int it = 0, nu = 0;
@@ -199,19 +255,11 @@ __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
     tc_fence_after();
     const uint32_t idesc = et_idesc<MODE>(a.bf16, et_up16(m.rows)), d = tmem + (uint32_t)(buf * a.bn);
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
+      if (MODE != kExGradW && !mx_wait_warp(&B.wfull[r.slot], r.phase, abort, kMxWaitNs)) return it;
       if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, kMxWaitNs)) return it;
+      fence_proxy_async();
       const uint32_t st = base + (uint32_t)r.slot * stage_bytes;
-      const int left = min(64, m.depth - s * 64), steps = (left + 15) / 16;
-      if (MODE == kExGradW && (left & 15)) {
-        // rows past the last route, which the copies filled with some row, become zeros in both operands
-        const int groups = 2 + (m.rows + 63) / 64, n = (et_up16(left) - left) * 8;
-        for (int i = lane; i < groups * n; i += 32) {
-          const int c = i / n, w = i - c * n;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(st + c * kEtGroup + left * 128 + w * 16), "r"(0) : "memory");
-        }
-        fence_proxy_async();
-        __syncwarp();
-      }
+      const int steps = (min(64, m.depth - s * 64) + 15) / 16;
       tc_fence_after();
       const uint64_t ad = MODE == kExForward ? smem_desc_sw128(st) : et_desc_mn(st);
       const uint64_t bd = MODE == kExGradW ? et_desc_mn(st + kEtABytes) : smem_desc_sw128(st + kEtABytes);
@@ -253,10 +301,18 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
   const int quarter = warp & 3, part = warp >> 2;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   O* out = static_cast<O*>(a.out);
-  constexpr int kStep = kEtEpiWarps / 4 * 32;
+  constexpr int kStep = kEtEpiWarps / 4 * 32, kPieces = 256 / kStep;  // a warp's pieces of 32 columns
   int nu = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+    int row[kPieces] = {};
+    if (MODE != kExGradW) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int c = part * 32 + k * kStep + lane;
+        row[k] = c < m.rows ? __ldg(a.order + m.slot0 + c) : 0;
+      }
+    }
     const bool some = m.depth > 0;
     const int buf = nu & 1, n = m.tile * 128 + quarter * 32 + lane;
     if (some) {
@@ -267,10 +323,11 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
       tc_fence_after();
     }
     const uint32_t d = tmem + lane_base + (uint32_t)(buf * a.bn);
-    for (int c0 = part * 32; c0 < m.rows; c0 += kStep) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c0 = part * 32 + k * kStep;
+      if (c0 >= m.rows) break;
       float y[32];
-      int row = 0;
-      if (MODE != kExGradW) row = __ldg(a.order + m.slot0 + min(c0 + lane, m.rows - 1));
       if (some) {
         uint32_t v[32];
         tmem_ld32(d + c0, v);
@@ -286,9 +343,9 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
         if (n < a.M)
           et_store_row<O>(y, out + ((size_t)m.expert * a.M + n) * a.cols + m.col0 + c0, m.rows - c0, a.vec);
       } else if (sizeof(O) == 2 && a.vec) {
-        mx_store32_words<O>(y, out, row, m.rows - c0, m.tile, a.M, stage + part * kEtStoreBytes, 1 + part);
+        mx_store32_words<O>(y, out, row[k], m.rows - c0, m.tile, a.M, stage + part * kEtStoreBytes, 1 + part);
       } else {
-        mx_store32<O>(y, out, row, m.rows - c0, n, a.M);
+        mx_store32<O>(y, out, row[k], m.rows - c0, n, a.M);
       }
     }
     if (some) {
@@ -311,7 +368,8 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ring; ++i) {
-      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.full[i], kEtRowWarps * 32);
+      mbar_init(&bars.wfull[i], 1);
       mbar_init(&bars.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -321,10 +379,7 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
     s_abort = 0;
     mbar_fence_init();
   }
-  if (threadIdx.x == kEtEpiWarps * 32) {
-    mx_prefetch_map(&a.amap);
-    mx_prefetch_map(&a.bmap);
-  }
+  if (MODE != kExGradW && threadIdx.x == kEtEpiWarps * 32) mx_prefetch_map(&a.wmap);
   if (warp == 0) tmem_alloc(&tmem_slot, 512);
   grid_wait();
   grid_launch();
@@ -356,16 +411,19 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   int loaded = 0, issued = 0;
   if (warp < kEtEpiWarps)
     et_epilogue<MODE, O>(a, groups, bars, units, tiles, ctiles, tmem, smem + (size_t)ring * stage_bytes, abort);
-  else if (warp == kEtEpiWarps)
-    loaded = et_loader<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, topk, abort);
-  else
+  else if (warp < kEtEpiWarps + kEtRowWarps)
+    et_rows<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, topk, abort);
+  else if (warp == kEtEpiWarps + kEtRowWarps) {
+    if (MODE != kExGradW) loaded = et_loader<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, abort);
+  } else
     issued = et_issuer<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, tmem, abort);
   tc_fence_before();
   __syncthreads();
   if (*abort) {  // (nobody sets it any more: the same for all)
-    // what a CTA that gave up has in flight ends before its shared and tensor memory go
+    // what a CTA that gave up has in flight ends before its shared and tensor memory go (the
+    // row warps have waited for their copies)
     int never = 0;
-    for (int i = max(0, loaded - ring); i < loaded; ++i) mbar_wait_abort(&bars.full[i % ring], (i / ring) & 1, &never, kMxDrainNs);
+    for (int i = max(0, loaded - ring); i < loaded; ++i) mbar_wait_abort(&bars.wfull[i % ring], (i / ring) & 1, &never, kMxDrainNs);
     if (issued > 0) mbar_wait_abort(&bars.empty[(issued - 1) % ring], ((issued - 1) / ring) & 1, &never, kMxDrainNs);
     if (threadIdx.x == 0) atomicOr(a.flags, 2u);
     __syncthreads();
@@ -374,16 +432,16 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Boxes of 64 elements by `rows` rows (gathered: one). Box starts are multiples of 64 elements.
-cudaError_t et_map(CUtensorMap* m, int dtype, const void* p, int cols, long rows, int64_t ld, int E, int64_t lde, int box) {
+// Boxes of 64 elements by `box` rows. Box starts are multiples of 64 elements.
+cudaError_t et_weight_map(CUtensorMap* m, const ExArgs& a, int box) {
   const auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)E};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(E > 1 ? lde : ld) * 2};
+  cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
+  cuuint64_t strides[2] = {(cuuint64_t)a.ldw * 2, (cuuint64_t)(a.E > 1 ? a.lde : a.ldw) * 2};
   cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(m, dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, E > 0 ? 3 : 2,
-                         const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = enc(m, a.dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void*>(a.w), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -420,12 +478,10 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   const int R = a.T * a.topk, es = a.out_dtype == TM_F32 ? 4 : 2;
   t.E = a.E, t.R = R, t.bf16 = a.dtype == TM_BF16, t.per_route = a.per_route;
   t.order = a.order, t.offsets = a.offsets, t.out = a.out, t.flags = a.flags;
-  const long xrows = a.per_route ? R : a.T;
-  cudaError_t e;
+  t.x = a.x, t.ldx = a.ldx, t.g = a.g, t.ldg = a.ldg;
+  cudaError_t e = cudaSuccess;
   if (a.mode == kExGradW) {
     t.M = a.N, t.cols = a.K, t.bn = std::min(256, (a.K + 63) / 64 * 64);
-    e = et_map(&t.amap, a.dtype, a.g, a.N, R, a.ldg, 0, 0, 1);
-    if (e == cudaSuccess) e = et_map(&t.bmap, a.dtype, a.x, a.K, xrows, a.ldx, 0, 0, 1);
     t.vec = ((uintptr_t)a.out) % 16 == 0 && (int64_t)a.K * es % 16 == 0;
   } else {
     const bool fwd = a.mode == kExForward;
@@ -433,9 +489,7 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
     // columns of a block: twice the mean number of routes of an expert, so that most experts
     // take one block and a stage holds no more than it needs (shorter stages: more in flight)
     t.bn = std::min(256, std::max(32, (2 * ((R + a.E - 1) / a.E) + 31) / 32 * 32));
-    e = et_map(&t.amap, a.dtype, a.w, a.K, a.N, a.ldw, a.E, a.lde, fwd ? 128 : 64);
-    if (e == cudaSuccess) e = fwd ? et_map(&t.bmap, a.dtype, a.x, a.K, xrows, a.ldx, 0, 0, 1)
-                                  : et_map(&t.bmap, a.dtype, a.g, a.N, R, a.ldg, 0, 0, 1);
+    e = et_weight_map(&t.wmap, a, fwd ? 128 : 64);
     t.vec = ((uintptr_t)a.out) % 16 == 0 && t.M % 8 == 0;
   }
   if (e != cudaSuccess) return e;
