@@ -28,19 +28,18 @@ namespace tmoe {
 namespace {
 
 constexpr int kEtEpiWarps = 8;
-constexpr int kEtRowWarps = 8;
+constexpr int kEtRowWarps = 16;
 constexpr int kEtThreads = (kEtEpiWarps + kEtRowWarps + 2) * 32;
 constexpr int kEtMaxRing = 12;
-constexpr uint32_t kEtSmem = 224 * 1024;
+constexpr uint32_t kEtSmem = 227 * 1024;
 constexpr uint32_t kEtABytes = 128 * 128;      // 128 rows of 64 elements, or 64 of 128
 constexpr uint32_t kEtGroup = 64 * 128;        // 64 rows of 64 elements (contiguous along M or N)
-constexpr uint32_t kEtStoreBytes = 16 * 256;   // for four epilogue warps
+constexpr uint32_t kEtStoreBytes = 16 * 256;   // results on their way: rows' for four epilogue warps, dW's for one
 constexpr int kEtMaxGroups = 257 + 1;
 
 struct EtArgs {
-  CUtensorMap wmap;         // forward, grad_x
-  const void *x, *g;
-  int64_t ldx, ldg;         // elements
+  CUtensorMap map;          // forward, grad_x: the weights; grad_w: the result (if vec)
+  CUtensorMap xmap, gmap;   // rows of x and dy, one at a time
   int E, R, M, depth;       // M: output channels; depth: contraction (forward, grad_x)
   int cols;                 // grad_w: columns of dW
   int bn;                   // most columns of a unit
@@ -51,14 +50,31 @@ struct EtArgs {
 };
 
 struct EtBars {
-  uint64_t full[kEtMaxRing], wfull[kEtMaxRing];  // the rows' part of a stage, the weights' part
-  uint64_t empty[kEtMaxRing];
+  uint64_t full[kEtMaxRing], empty[kEtMaxRing];    // the ring of the rows
+  uint64_t wfull[kEtMaxRing], wempty[kEtMaxRing];  // that of the weights
   uint64_t acc_full[2], acc_empty[2];
 };
 
 // The groups of routes: where each begins, and its first block.
 struct EtGroups {
   int off[kEtMaxGroups], first[kEtMaxGroups];
+};
+
+// Two rings of stages of 64 of the contraction: the weights come from memory and
+// need more of them in flight than the rows, which mostly come from L2. (One ring
+// of both, 4 stages of 48 KB: 58% of the memory's rate at 205 routes an expert.)
+// grad_w has both its operands in the rows' ring.
+struct EtRings {
+  int rows, weights;
+  uint32_t stage;  // bytes of a stage of the rows' ring
+};
+
+// What lies in shared memory behind the rings and the store buffers.
+struct EtShared {
+  EtBars bars;
+  EtGroups groups;
+  uint32_t tmem_slot;
+  int abort;
 };
 
 struct EtUnit {
@@ -97,10 +113,13 @@ __device__ __forceinline__ void et_tma_3d(uint32_t dst, const CUtensorMap* map, 
   asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
                ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-// 16 bytes to shared memory, of which the last 16 - `bytes` are zeros.
-__device__ __forceinline__ void et_copy(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Four rows of 64 elements, from column x.
+__device__ __forceinline__ void et_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n"
+      ::"r"(dst), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar) : "memory");
 }
+
 // Descriptor of an operand that is contiguous along M or N, 128-byte swizzled:
 // 64 of those by 8 of the contraction are an atom of 1024 bytes; atoms follow each
 // other along the contraction, and groups of 64 along M or N are kEtGroup apart. A step
@@ -119,8 +138,8 @@ __device__ __forceinline__ uint32_t et_idesc(int bf16, int n) {
 
 // The weights' part of the stages. (Returns the stages it loaded.)
 template <int MODE>
-__device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
-                         FastDiv tiles, FastDiv ctiles, volatile int* abort) {
+__device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, int ring, int units, FastDiv tiles,
+                         FastDiv ctiles, volatile int* abort) {
   const bool lead = mx_elect();
   const uint32_t bar0 = smem_u32(&B.wfull[0]);
   MxRing r;
@@ -129,15 +148,15 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64;
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
-      if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
-      const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
+      if (it >= ring && !mx_wait_warp(&B.wempty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
+      const uint32_t st = base + (uint32_t)r.slot * kEtABytes, bar = bar0 + (uint32_t)r.slot * 8;
       if (lead) {
         mx_expect(bar, kEtABytes);
         if (MODE == kExForward) {
-          et_tma_3d(st, &a.wmap, s * 64, m.tile * 128, m.expert, bar);
+          et_tma_3d(st, &a.map, s * 64, m.tile * 128, m.expert, bar);
         } else {
-          et_tma_3d(st, &a.wmap, m.tile * 128, s * 64, m.expert, bar);
-          et_tma_3d(st + kEtGroup, &a.wmap, m.tile * 128 + 64, s * 64, m.expert, bar);
+          et_tma_3d(st, &a.map, m.tile * 128, s * 64, m.expert, bar);
+          et_tma_3d(st + kEtGroup, &a.map, m.tile * 128 + 64, s * 64, m.expert, bar);
         }
       }
     }
@@ -145,105 +164,79 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
   return it;
 }
 
-// The rows' part. A lane copies 16 bytes of every 32nd row, and arrives at the
-// stage's barrier when they have landed. (They are written by the generic proxy;
-// the issuer's fence, behind that barrier, shows them to the tensor cores.)
+// The rows' part. A stage's rows are copied four at a time; lanes of all the row
+// warps take a copy each. (Returns the stages it loaded.)
 template <int MODE>
-__device__ void et_rows(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
-                        FastDiv tiles, FastDiv ctiles, FastDiv topk, volatile int* abort) {
+__device__ int et_rows(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
+                       FastDiv tiles, FastDiv ctiles, FastDiv topk, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - kEtEpiWarps;
-  const int chunk = lane & 7, row = warp * 4 + (lane >> 3);  // of each 32 rows
-  const uint32_t at = (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
-  const uint16_t *x = static_cast<const uint16_t*>(a.x), *dy = static_cast<const uint16_t*>(a.g);
   auto source = [&](int route) { return a.per_route ? route : (int)topk.div((uint32_t)route); };
+  const uint32_t bar0 = smem_u32(&B.full[0]);
   MxRing r;
   int it = 0;
-  auto stage = [&](auto copy) {  // one stage's copies
-    if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return false;
-    copy(base + (uint32_t)r.slot * stage_bytes + at);
-    cp_async_mbar_arrive(&B.full[r.slot]);
-    ++it;
-    r.next(ring);
-    return true;
-  };
-  bool ok = true;
   if (MODE == kExGradW) {
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    // warp: four rows of a stage; lanes 0..5: the groups of 64 columns of dy, then x
+    constexpr int kPer = kEtRowWarps / 16;
+    static_assert(kPer == 1, "a warp for each four rows of a stage");
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
-      const int stages = (m.depth + 63) / 64, groups = (m.rows + 63) / 64;
-      int route[2];
-      auto routes = [&](int s) {
+      const int stages = (m.depth + 63) / 64, groups = (m.rows + 63) / 64, agroups = a.M - m.tile * 128 > 64 ? 2 : 1;
+      int q[4];
+      auto look = [&](int s) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = s * 64 + h * 32 + row;
-          route[h] = i < m.depth ? __ldg(a.order + m.slot0 + i) : -1;
-        }
+        for (int i = 0; i < 4; ++i) q[i] = __ldg(a.order + m.slot0 + min(s * 64 + warp * 4 + i, m.depth - 1));
       };
-      if (stages) routes(0);
-      const int n0 = m.tile * 128 + chunk * 8, k0 = m.col0 + chunk * 8;
-      for (int s = 0; s < stages && ok; ++s) {
-        ok = stage([&](uint32_t to) {
+      if (stages) look(0);
+      for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
+        if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
+        const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
+        const bool some = s * 64 + warp * 4 < (m.depth + 15) / 16 * 16;
+        if (lane == 0) mx_expect(bar, some ? (uint32_t)((agroups + groups) * 512) : 0u);
+        __syncwarp();
+        if (some && lane < agroups + groups) {
+          const bool isx = lane >= agroups;
+          const int c = isx ? lane - agroups : lane;
+          int t[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h * 32 >= et_up16(m.depth - s * 64)) break;
-            const bool in = route[h] >= 0;  // (rows past the last route: zeros)
-            const uint16_t* p = dy + (in ? (size_t)route[h] * a.ldg : 0);
-            const uint16_t* q = x + (in ? (size_t)source(route[h]) * a.ldx : 0);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int bytes = in ? min(16, max(0, (a.M - n0 - c * 64) * 2)) : 0;
-              et_copy(to + c * kEtGroup + h * 4096, bytes ? p + n0 + c * 64 : dy, bytes);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c >= groups) break;
-              const int bytes = in ? min(16, max(0, (a.cols - k0 - c * 64) * 2)) : 0;
-              et_copy(to + kEtABytes + c * kEtGroup + h * 4096, bytes ? q + k0 + c * 64 : x, bytes);
-            }
-          }
-        });
-        if (s + 1 < stages) routes(s + 1);
+          for (int i = 0; i < 4; ++i) t[i] = isx ? source(q[i]) : q[i];
+          et_gather4(st + (isx ? kEtABytes : 0) + c * kEtGroup + warp * 512, isx ? &a.xmap : &a.gmap,
+                     (isx ? m.col0 : m.tile * 128) + c * 64, t, bar);
+        }
+        if (s + 1 < stages) look(s + 1);
       }
     }
   } else {
-    const uint16_t* src = MODE == kExForward ? x : dy;
-    const int64_t ld = MODE == kExForward ? a.ldx : a.ldg;
-    // a unit's rows are looked up while the one before it is copied
-    auto find = [&](int u, int (&to)[8], EtUnit& m) {
-      m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+    // lanes 0..3 of a warp: four rows each
+    const int quad = warp + (lane & 3) * kEtRowWarps;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+      const int stages = (m.depth + 63) / 64, quads = et_up16(m.rows) / 4;
+      int q[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // (past the last row: any)
-        to[j] = j * 32 < m.rows ? __ldg(a.order + m.slot0 + min(j * 32 + row, m.rows - 1)) : 0;
-    };
-    int next[8];
-    EtUnit m, ahead;
-    if ((int)blockIdx.x < units) find(blockIdx.x, next, ahead);
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      m = ahead;
-      const uint16_t* p[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = src + (size_t)(MODE == kExForward ? source(next[j]) : next[j]) * ld + chunk * 8;
-      if (u + (int)gridDim.x < units) find(u + gridDim.x, next, ahead);
-      const int stages = (m.depth + 63) / 64, rows = et_up16(m.rows);
-      for (int s = 0; s < stages && ok; ++s) {
-        const int left = (m.depth - s * 64 - chunk * 8) * 2, bytes = min(16, max(0, left));
-        ok = stage([&](uint32_t to) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j * 32 + row < rows) et_copy(to + kEtABytes + j * 4096, bytes ? p[j] + s * 64 : src, bytes);
-        });
+      for (int i = 0; i < 4; ++i) {
+        const int route = __ldg(a.order + m.slot0 + min(quad * 4 + i, m.rows - 1));
+        q[i] = MODE == kExForward ? source(route) : route;
+      }
+      const bool mine = lane < 4 && quad < quads;
+      const uint32_t bytes = 512u * __popc(__ballot_sync(0xFFFFFFFFu, mine));
+      for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
+        if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
+        const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
+        if (lane == 0) mx_expect(bar, bytes);
+        __syncwarp();
+        if (mine) et_gather4(st + (uint32_t)quad * 512, MODE == kExForward ? &a.xmap : &a.gmap, s * 64, q, bar);
       }
     }
   }
-  asm volatile("cp.async.wait_all;\n" ::: "memory");
+  return it;
 }
 
 // (returns the stages whose MMAs it issued)
 template <int MODE>
-__device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
+__device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t wbase, EtRings rings, int units,
                          FastDiv tiles, FastDiv ctiles, uint32_t tmem, volatile int* abort) {
   const bool lead = mx_elect();
-  MxRing r;
+  MxRing r, rw;
   int it = 0, nu = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
@@ -254,43 +247,52 @@ __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
     ++nu;
     tc_fence_after();
     const uint32_t idesc = et_idesc<MODE>(a.bf16, et_up16(m.rows)), d = tmem + (uint32_t)(buf * a.bn);
-    for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
-      if (MODE != kExGradW && !mx_wait_warp(&B.wfull[r.slot], r.phase, abort, kMxWaitNs)) return it;
+    for (int s = 0; s < stages; ++s, ++it, r.next(rings.rows), rw.next(rings.weights)) {
       if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, kMxWaitNs)) return it;
-      fence_proxy_async();
-      const uint32_t st = base + (uint32_t)r.slot * stage_bytes;
-      const int steps = (min(64, m.depth - s * 64) + 15) / 16;
+      if (MODE != kExGradW && !mx_wait_warp(&B.wfull[rw.slot], rw.phase, abort, kMxWaitNs)) return it;
+      const uint32_t st = base + (uint32_t)r.slot * rings.stage, wt = wbase + (uint32_t)rw.slot * kEtABytes;
+      const int left = min(64, m.depth - s * 64), steps = (left + 15) / 16;
+      if (MODE == kExGradW && (left & 15)) {
+        // rows past the last route, which the copies filled with some row, become zeros in both operands
+        const int groups = 2 + (m.rows + 63) / 64, n = (et_up16(left) - left) * 8;
+        for (int i = threadIdx.x & 31; i < groups * n; i += 32) {
+          const int c = i / n, w = i - c * n;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(st + c * kEtGroup + left * 128 + w * 16), "r"(0) : "memory");
+        }
+        fence_proxy_async();
+        __syncwarp();
+      }
       tc_fence_after();
-      const uint64_t ad = MODE == kExForward ? smem_desc_sw128(st) : et_desc_mn(st);
-      const uint64_t bd = MODE == kExGradW ? et_desc_mn(st + kEtABytes) : smem_desc_sw128(st + kEtABytes);
+      const uint64_t ad = MODE == kExForward ? smem_desc_sw128(wt) : et_desc_mn(MODE == kExGradX ? wt : st);
+      const uint64_t bd = MODE == kExGradW ? et_desc_mn(st + kEtABytes) : smem_desc_sw128(st);
       constexpr uint64_t sa = MODE == kExForward ? 2 : 128, sb = MODE == kExGradW ? 128 : 2;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (k < steps && lead) tc_mma_f16(d, ad + k * sa, bd + k * sb, idesc, s > 0 || k > 0 ? 1u : 0u);
       if (lead) tc_commit(&B.empty[r.slot]);
+      if (MODE != kExGradW && lead) tc_commit(&B.wempty[rw.slot]);
     }
     if (lead) tc_commit(&B.acc_full[buf]);
   }
   return it;
 }
 
-// 32 columns of dW of a thread's row.
-template <typename O>
-__device__ __forceinline__ void et_store_row(const float (&y)[32], O* __restrict__ out, int cols, bool vec) {
-  constexpr int n = 16 / (int)sizeof(O);
-  if (vec) {
+// 32 rows by 128 bytes of dW, a lane's row in v, by way of shared memory and one
+// TMA store for the warp. (A lane's own 16-byte stores, each to its row, wrote dW at
+// 2.6 TB/s.) What lies past the last row or column is left out by the copy.
+__device__ __forceinline__ void et_store_tile(const uint4 (&v)[8], unsigned char* stage, const CUtensorMap* map, int x, int y, int z,
+                                              bool on) {
+  const int lane = threadIdx.x & 31;
+  asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");  // (the lane that issued the last one: it has been read)
+  __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 32; c += n) {
-      uint4 q;
-      O* e = reinterpret_cast<O*>(&q);
-#pragma unroll
-      for (int i = 0; i < n; ++i) e[i] = from_f32<O>(y[c + i]);
-      if (c < cols) *reinterpret_cast<uint4*>(out + c) = q;  // (cols is a multiple of n)
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (c < cols) out[c] = from_f32<O>(y[c]);
+  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0 && on) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(smem_u32(stage)) : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
   }
 }
 
@@ -318,13 +320,43 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
     if (some) {
       const bool full = mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, kMxWaitNs);
       // the warps of a part meet at its barrier while they store: they go on together or not at all
-      if (!mx_vote_part(full, 1 + part)) return;
+      if (!mx_vote_part(full, 1 + part)) break;
       ++nu;
       tc_fence_after();
     }
     const uint32_t d = tmem + lane_base + (uint32_t)(buf * a.bn);
+    if (MODE == kExGradW) {
+      constexpr int kCols = 128 / (int)sizeof(O);  // columns of 128 bytes
+      const int n0 = m.tile * 128 + quarter * 32;
+      for (int c0 = part * kCols; c0 < m.rows; c0 += kEtEpiWarps / 4 * kCols) {
+        uint4 q[8];
+        O* e = reinterpret_cast<O*>(q);
+        if (some) {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
+          for (int h = 0; h < kCols; h += 32) {
+            uint32_t v[32];
+            tmem_ld32(d + c0 + h, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) e[h + c] = from_f32<O>(__uint_as_float(v[c]));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) q[c] = make_uint4(0, 0, 0, 0);
+        }
+        if (a.vec) {
+          et_store_tile(q, stage + warp * kEtStoreBytes, &a.map, m.col0 + c0, n0, m.expert, n0 < a.M);
+        } else if (n < a.M) {
+          O* o = out + ((size_t)m.expert * a.M + n) * a.cols + m.col0 + c0;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (c0 + c < m.rows) o[c] = e[c];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < (MODE == kExGradW ? 0 : kPieces); ++k) {
       const int c0 = part * 32 + k * kStep;
       if (c0 >= m.rows) break;
       float y[32];
@@ -339,10 +371,7 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
 #pragma unroll
         for (int c = 0; c < 32; ++c) y[c] = 0.0f;
       }
-      if (MODE == kExGradW) {
-        if (n < a.M)
-          et_store_row<O>(y, out + ((size_t)m.expert * a.M + n) * a.cols + m.col0 + c0, m.rows - c0, a.vec);
-      } else if (sizeof(O) == 2 && a.vec) {
+      if (sizeof(O) == 2 && a.vec) {
         mx_store32_words<O>(y, out, row[k], m.rows - c0, m.tile, a.M, stage + part * kEtStoreBytes, 1 + part);
       } else {
         mx_store32<O>(y, out, row[k], m.rows - c0, n, a.M);
@@ -354,33 +383,40 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
     }
     __syncwarp();
   }
+  if (MODE == kExGradW) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
 }
 
+template <int MODE>
+constexpr uint32_t et_store_bytes() { return (MODE == kExGradW ? kEtEpiWarps : kEtEpiWarps / 4) * kEtStoreBytes; }
+
 template <int MODE, typename O>
-__global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__ EtArgs a, int ring, FastDiv tiles, FastDiv ctiles,
+__global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__ EtArgs a, EtRings rings, FastDiv tiles, FastDiv ctiles,
                                                          FastDiv topk) {
-  extern __shared__ unsigned char et_smem_raw[];
-  __shared__ __align__(8) EtBars bars;
-  __shared__ EtGroups groups;
-  __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort;
-  unsigned char* smem = et_smem_raw + ((1024u - (smem_u32(et_smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t wofs = (uint32_t)rings.rows * rings.stage;
+  unsigned char* store = smem + wofs + (uint32_t)rings.weights * kEtABytes;
+  EtShared& sh = *reinterpret_cast<EtShared*>(store + et_store_bytes<MODE>());
+  EtBars& bars = sh.bars;
+  EtGroups& groups = sh.groups;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ring; ++i) {
-      mbar_init(&bars.full[i], kEtRowWarps * 32);
-      mbar_init(&bars.wfull[i], 1);
+    for (int i = 0; i < rings.rows; ++i) {
+      mbar_init(&bars.full[i], kEtRowWarps);
       mbar_init(&bars.empty[i], 1);
+    }
+    for (int i = 0; i < rings.weights; ++i) {
+      mbar_init(&bars.wfull[i], 1);
+      mbar_init(&bars.wempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], kEtEpiWarps);
     }
-    s_abort = 0;
+    sh.abort = 0;
     mbar_fence_init();
   }
-  if (MODE != kExGradW && threadIdx.x == kEtEpiWarps * 32) mx_prefetch_map(&a.wmap);
-  if (warp == 0) tmem_alloc(&tmem_slot, 512);
+  if (MODE != kExGradW && threadIdx.x == kEtEpiWarps * 32) mx_prefetch_map(&a.map);
+  if (warp == 0) tmem_alloc(&sh.tmem_slot, 512);
   grid_wait();
   grid_launch();
   for (int e = threadIdx.x; e <= a.E; e += kEtThreads) groups.off[e] = a.offsets[e];
@@ -405,26 +441,29 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
     if (lane == 0) groups.first[a.E + 1] = run;
   }
   __syncthreads();
-  const uint32_t tmem = tmem_slot, base = smem_u32(smem), stage_bytes = kEtABytes + (uint32_t)a.bn * 128;
+  const uint32_t tmem = sh.tmem_slot, base = smem_u32(smem);
   const int units = MODE == kExGradW ? a.E * (int)ctiles.d * (int)tiles.d : groups.first[a.E + 1] * (int)tiles.d;
-  volatile int* abort = &s_abort;
-  int loaded = 0, issued = 0;
+  volatile int* abort = &sh.abort;
+  int loaded = 0, rows_loaded = 0, issued = 0;
   if (warp < kEtEpiWarps)
-    et_epilogue<MODE, O>(a, groups, bars, units, tiles, ctiles, tmem, smem + (size_t)ring * stage_bytes, abort);
+    et_epilogue<MODE, O>(a, groups, bars, units, tiles, ctiles, tmem, store, abort);
   else if (warp < kEtEpiWarps + kEtRowWarps)
-    et_rows<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, topk, abort);
+    rows_loaded = et_rows<MODE>(a, groups, bars, base, rings.stage, rings.rows, units, tiles, ctiles, topk, abort);
   else if (warp == kEtEpiWarps + kEtRowWarps) {
-    if (MODE != kExGradW) loaded = et_loader<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, abort);
+    if (MODE != kExGradW) loaded = et_loader<MODE>(a, groups, bars, base + wofs, rings.weights, units, tiles, ctiles, abort);
   } else
-    issued = et_issuer<MODE>(a, groups, bars, base, stage_bytes, ring, units, tiles, ctiles, tmem, abort);
+    issued = et_issuer<MODE>(a, groups, bars, base, base + wofs, rings, units, tiles, ctiles, tmem, abort);
   tc_fence_before();
   __syncthreads();
   if (*abort) {  // (nobody sets it any more: the same for all)
     // what a CTA that gave up has in flight ends before its shared and tensor memory go (the
     // row warps have waited for their copies)
     int never = 0;
-    for (int i = max(0, loaded - ring); i < loaded; ++i) mbar_wait_abort(&bars.wfull[i % ring], (i / ring) & 1, &never, kMxDrainNs);
-    if (issued > 0) mbar_wait_abort(&bars.empty[(issued - 1) % ring], ((issued - 1) / ring) & 1, &never, kMxDrainNs);
+    for (int i = max(0, loaded - rings.weights); i < loaded; ++i)
+      mbar_wait_abort(&bars.wfull[i % rings.weights], (i / rings.weights) & 1, &never, kMxDrainNs);
+    for (int i = max(0, rows_loaded - rings.rows); i < rows_loaded; ++i)
+      mbar_wait_abort(&bars.full[i % rings.rows], (i / rings.rows) & 1, &never, kMxDrainNs);
+    if (issued > 0) mbar_wait_abort(&bars.empty[(issued - 1) % rings.rows], ((issued - 1) / rings.rows) & 1, &never, kMxDrainNs);
     if (threadIdx.x == 0) atomicOr(a.flags, 2u);
     __syncthreads();
   }
@@ -432,16 +471,32 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Boxes of 64 elements by `box` rows. Box starts are multiples of 64 elements.
-cudaError_t et_weight_map(CUtensorMap* m, const ExArgs& a, int box) {
+// [E, N, K] in boxes of `width` elements (128 bytes, as all box starts are multiples of) by `box` rows.
+cudaError_t et_map3(CUtensorMap* m, int dtype, const void* p, const ExArgs& a, int64_t ldw, int64_t lde, int width, int box) {
   const auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
-  cuuint64_t strides[2] = {(cuuint64_t)a.ldw * 2, (cuuint64_t)(a.E > 1 ? a.lde : a.ldw) * 2};
-  cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
+  const cuuint64_t es = dtype_bytes(dtype);
+  cuuint64_t strides[2] = {(cuuint64_t)ldw * es, (cuuint64_t)(a.E > 1 ? lde : ldw) * es};
+  cuuint32_t boxes[3] = {(cuuint32_t)width, (cuuint32_t)box, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(m, a.dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                         const_cast<void*>(a.w), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = enc(m, dtype == TM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                            : dtype == TM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                         3, const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t et_map2(CUtensorMap* m, int dtype, const void* p, int cols, long rows, int64_t ld) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t boxes[2] = {64, 1};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                         const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -452,13 +507,22 @@ cudaError_t et_launch(const EtArgs& a, int topk, int sms, cudaStream_t st) {
   static OncePerDevice done;
   const cudaError_t limit = allow_smem(done, kern, (int)kEtSmem);
   if (limit != cudaSuccess) return limit;
-  const uint32_t stage = kEtABytes + (uint32_t)a.bn * 128, store = MODE == kExGradW ? 0 : kEtEpiWarps / 4 * kEtStoreBytes;
-  const int ring = (int)std::min<uint32_t>(kEtMaxRing, (kEtSmem - 1024 - store) / stage);
+  const uint32_t rest = et_store_bytes<MODE>() + (uint32_t)sizeof(EtShared), room = kEtSmem - rest;
+  EtRings rings;
+  if (MODE == kExGradW) {
+    rings.stage = kEtABytes + (uint32_t)a.bn * 128;
+    rings.rows = (int)std::min<uint32_t>(kEtMaxRing, room / rings.stage);
+    rings.weights = 0;
+  } else {
+    rings.stage = (uint32_t)a.bn * 128;
+    rings.rows = (int)std::min<uint32_t>(8, 96 * 1024 / rings.stage);  // (3 of 256 rows)
+    rings.weights = (int)std::min<uint32_t>(kEtMaxRing, (room - rings.rows * rings.stage) / kEtABytes);
+  }
   const long tiles = (a.M + 127) / 128, ctiles = MODE == kExGradW ? (a.cols + a.bn - 1) / a.bn : 1;
   const long units = MODE == kExGradW ? (long)a.E * tiles * ctiles : ((long)a.R / a.bn + std::min<long>(a.R, a.E + 1)) * tiles;
   if (units >= 1L << 31) return cudaErrorInvalidConfiguration;
   const int grid = (int)std::max<long>(1, std::min<long>(units, sms));
-  return launch_after(kern, dim3(grid), kEtThreads, 1024 + ring * stage + store, st, a, ring, FastDiv((uint32_t)tiles),
+  return launch_after(kern, dim3(grid), kEtThreads, rings.rows * rings.stage + rings.weights * kEtABytes + rest, st, a, rings, FastDiv((uint32_t)tiles),
                       FastDiv((uint32_t)ctiles), FastDiv((uint32_t)topk));
 }
 
@@ -478,18 +542,26 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   const int R = a.T * a.topk, es = a.out_dtype == TM_F32 ? 4 : 2;
   t.E = a.E, t.R = R, t.bf16 = a.dtype == TM_BF16, t.per_route = a.per_route;
   t.order = a.order, t.offsets = a.offsets, t.out = a.out, t.flags = a.flags;
-  t.x = a.x, t.ldx = a.ldx, t.g = a.g, t.ldg = a.ldg;
+  if (a.mode != kExGradX) {
+    const cudaError_t e = et_map2(&t.xmap, a.dtype, a.x, a.K, a.per_route ? R : a.T, a.ldx);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.mode != kExForward) {
+    const cudaError_t e = et_map2(&t.gmap, a.dtype, a.g, a.N, R, a.ldg);
+    if (e != cudaSuccess) return e;
+  }
   cudaError_t e = cudaSuccess;
   if (a.mode == kExGradW) {
     t.M = a.N, t.cols = a.K, t.bn = std::min(256, (a.K + 63) / 64 * 64);
     t.vec = ((uintptr_t)a.out) % 16 == 0 && (int64_t)a.K * es % 16 == 0;
+    if (t.vec) e = et_map3(&t.map, a.out_dtype, a.out, a, a.K, (int64_t)a.N * a.K, 128 / es, 32);
   } else {
     const bool fwd = a.mode == kExForward;
     t.M = fwd ? a.N : a.K, t.depth = fwd ? a.K : a.N;
     // columns of a block: twice the mean number of routes of an expert, so that most experts
     // take one block and a stage holds no more than it needs (shorter stages: more in flight)
     t.bn = std::min(256, std::max(32, (2 * ((R + a.E - 1) / a.E) + 31) / 32 * 32));
-    e = et_weight_map(&t.wmap, a, fwd ? 128 : 64);
+    e = et_map3(&t.map, a.dtype, a.w, a, a.ldw, a.lde, 64, fwd ? 128 : 64);
     t.vec = ((uintptr_t)a.out) % 16 == 0 && t.M % 8 == 0;
   }
   if (e != cudaSuccess) return e;
