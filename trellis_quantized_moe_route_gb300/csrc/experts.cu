@@ -23,10 +23,14 @@ constexpr int kExMaxSide = 1 << 20;  // N and K
 // time: lanes of one expert find each other (match), the lowest adds their
 // number to the warp's count. Counts are summed over the warps and the CTAs of
 // the cluster, and the same walk gives every route its place. Ids outside
-// 0..E-1 form a last group.
-constexpr int kPlanThreads = 512;
+// 0..E-1 form a last group. Bound by latency: one CTA for up to kPlanAlone routes,
+// a cluster beyond; ids of up to kPlanHeld walks stay in registers.
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCtas = 8;
+constexpr int kPlanHeld = 4;
+constexpr int kPlanAlone = 2048;
+constexpr int kPlanGroups = kExMaxExperts + 1;
 
 __device__ __forceinline__ int plan_peer(const int* p, int rank) {
   uint32_t at;
@@ -36,86 +40,100 @@ __device__ __forceinline__ int plan_peer(const int* p, int rank) {
   return v;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanThreads)
     k_ex_plan(const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ order, int32_t* __restrict__ offsets,
               uint32_t* __restrict__ flags) {
-  __shared__ int s_cnt[kPlanWarps][kExMaxExperts + 1];  // counts, then places, by warp
-  __shared__ int s_all[kExMaxExperts + 1];              // the CTA's counts
-  __shared__ int s_total[kExMaxExperts + 1], s_scan[kExMaxExperts + 1];
+  __shared__ int s_cnt[kPlanWarps][kPlanGroups];  // counts, then places, by warp
+  __shared__ int s_all[kPlanGroups];              // the CTA's counts
+  __shared__ int s_scan[kPlanGroups], s_warp[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = E + 1;
-  uint32_t rank;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  for (int i = tid; i < kPlanWarps * (kExMaxExperts + 1); i += kPlanThreads) (&s_cnt[0][0])[i] = 0;
+  uint32_t rank = 0;
+  if (CTAS > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  for (int i = tid; i < kPlanWarps * kPlanGroups; i += kPlanThreads) (&s_cnt[0][0])[i] = 0;
   __syncthreads();
   grid_wait();
   grid_launch();
-  const long per = ((long)R + kPlanCtas * kPlanWarps - 1) / (kPlanCtas * kPlanWarps);
-  const long lo = std::min<long>(R, per * ((long)rank * kPlanWarps + warp)), hi = std::min<long>(R, lo + per);
-  auto group = [&](long r) {
+  const int per = (R + CTAS * kPlanWarps - 1) / (CTAS * kPlanWarps);  // routes of a warp
+  const int lo = min((long)R, (long)per * (rank * kPlanWarps + warp)), hi = min(R, lo + per);
+  auto group = [&](int r) {
     const int e = r < hi ? ids[r] : -2;
     return r < hi ? (e >= 0 && e < E ? e : E) : -1;
   };
-  for (long r = lo; r < hi; r += 32) {
-    const int e = group(r + lane);
+  int held[kPlanHeld];
+#pragma unroll
+  for (int u = 0; u < kPlanHeld; ++u) held[u] = group(lo + u * 32 + lane);
+  auto walk = [&](auto f) {
+#pragma unroll
+    for (int u = 0; u < kPlanHeld; ++u)
+      if (lo + u * 32 < hi) f(lo + u * 32 + lane, held[u]);
+    for (int r = lo + kPlanHeld * 32; r < hi; r += 32) f(r + lane, group(r + lane));
+  };
+  walk([&](int, int e) {
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     if (e >= 0 && lane == __ffs(same) - 1) s_cnt[warp][e] += __popc(same);
     __syncwarp();
-  }
+  });
   __syncthreads();
-  for (int e = tid; e < G; e += kPlanThreads) {
-    int n = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int c = s_cnt[w][e];
-      s_cnt[w][e] = n;
-      n += c;
-    }
-    s_all[e] = n;
-  }
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-  for (int e = tid; e < G; e += kPlanThreads) {
-    int before = 0, total = 0;
-    for (int c = 0; c < kPlanCtas; ++c) {
-      const int v = plan_peer(&s_all[e], c);
-      if (c < (int)rank) before += v;
-      total += v;
-    }
-    s_total[e] = total;
-    s_scan[e] = before;
-  }
-  __syncthreads();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");  // (done with the peers' counts)
-  if (warp == 0) {  // exclusive scan of the totals
-    int run = 0;
-    for (int e0 = 0; e0 < G; e0 += 32) {
-      const int e = e0 + lane, v = e < G ? s_total[e] : 0;
-      int incl = v;
+  int all = 0;
+  if (tid < G) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      if (e < G) {
-        s_scan[e] += run + incl - v;
-        if (rank == 0) offsets[e] = run + incl - v;  // (offsets[E]: where the last group begins)
-      }
-      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int c = s_cnt[w][tid];
+      s_cnt[w][tid] = all;
+      all += c;
     }
-    if (rank == 0 && lane == 0) *flags = s_total[E] ? 1u : 0u;
+  }
+  int before = 0, total = all;
+  if (CTAS > 1) {
+    if (tid < G) s_all[tid] = all;
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    if (tid < G) {
+      int v[CTAS];
+#pragma unroll
+      for (int c = 0; c < CTAS; ++c) v[c] = plan_peer(&s_all[tid], c);
+      total = 0;
+#pragma unroll
+      for (int c = 0; c < CTAS; ++c) {
+        if (c < (int)rank) before += v[c];
+        total += v[c];
+      }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");  // (done with the peers' counts)
+  }
+  // exclusive scan of the totals, one to a thread
+  int incl = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  if (tid < G) {
+    int first = incl - total;
+    for (int w = 0; w < warp; ++w) first += s_warp[w];
+    s_scan[tid] = first + before;
+    if (rank == 0) {
+      offsets[tid] = first;  // (offsets[E]: where the last group begins)
+      if (tid == E) *flags = total ? 1u : 0u;
+    }
   }
   __syncthreads();
-  for (long r = lo; r < hi; r += 32) {
-    const int e = group(r + lane);
+  walk([&](int r, int e) {
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     int at = 0;
     if (e >= 0) at = s_scan[e] + s_cnt[warp][e] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (e >= 0) {
-      order[at] = (int)(r + lane);
+      order[at] = r;
       if (lane == __ffs(same) - 1) s_cnt[warp][e] += __popc(same);
     }
     __syncwarp();
-  }
-  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no CTA leaves while another reads its counts
+  });
+  if (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no CTA leaves while another reads its counts
 }
 
 // ------------------------------------------------------- any sizes and strides
@@ -304,7 +322,20 @@ __global__ void __launch_bounds__(256) k_ex_sum(const float* __restrict__ rows, 
 
 cudaError_t launch_ex_plan(const int32_t* ids, int R, int E, int32_t* order, int32_t* offsets, uint32_t* flags,
                            cudaStream_t st) {
-  return launch_after(k_ex_plan, dim3(kPlanCtas), kPlanThreads, 0, st, ids, R, E, order, offsets, flags);
+  if (R <= kPlanAlone) return launch_after(k_ex_plan<1>, dim3(1), kPlanThreads, 0, st, ids, R, E, order, offsets, flags);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPlanCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = kPlanCtas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_ex_plan<kPlanCtas>, ids, R, E, order, offsets, flags);
 }
 
 cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, int dtype, cudaStream_t st) {

@@ -32,17 +32,20 @@ constexpr int kEtRowWarps = 16;
 constexpr int kEtThreads = (kEtEpiWarps + kEtRowWarps + 2) * 32;
 constexpr int kEtMaxRing = 12;
 constexpr uint32_t kEtSmem = 227 * 1024;
-constexpr uint32_t kEtABytes = 128 * 128;      // 128 rows of 64 elements, or 64 of 128
+constexpr uint32_t kEtABytes = 128 * 128;      // half a tile of A: 128 rows of 64 elements, or 64 of 128
 constexpr uint32_t kEtGroup = 64 * 128;        // 64 rows of 64 elements (contiguous along M or N)
-constexpr uint32_t kEtStoreBytes = 16 * 256;   // results on their way: rows' for four epilogue warps, dW's for one
+constexpr uint32_t kEtStoreBytes = 4096;       // results on their way: rows' for four epilogue warps, dW's for one
 constexpr int kEtMaxGroups = 257 + 1;
 
 struct EtArgs {
   CUtensorMap map;          // forward, grad_x: the weights; grad_w: the result (if vec)
   CUtensorMap xmap, gmap;   // rows of x and dy, one at a time
+  const uint16_t* x;
+  int64_t ldx;              // elements
   int E, R, M, depth;       // M: output channels; depth: contraction (forward, grad_x)
   int cols;                 // grad_w: columns of dW
   int bn;                   // most columns of a unit
+  int bufs;                 // accumulators of a tile that TMEM holds: 1 or 2
   int bf16, per_route, vec; // vec: results can be stored in 16-byte words
   const int32_t *order, *offsets;
   void* out;
@@ -82,6 +85,12 @@ struct EtUnit {
   int col0;
 };
 
+// Halves of 128 channels of a unit's tile of MT * 128.
+template <int MT>
+__device__ __forceinline__ int et_halves(const EtArgs& a, const EtUnit& m) {
+  return MT == 1 || a.M - m.tile * (MT * 128) > 128 ? MT : 1;
+}
+
 template <int MODE>
 __device__ __forceinline__ EtUnit et_unit(const EtArgs& a, const EtGroups& g, int u, int units, FastDiv tiles, FastDiv ctiles) {
   EtUnit m;
@@ -120,6 +129,11 @@ __device__ __forceinline__ void et_gather4(uint32_t dst, const CUtensorMap* map,
       ::"r"(dst), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar) : "memory");
 }
 
+// 16 bytes to shared memory, of which the last 16 - `bytes` are zeros.
+__device__ __forceinline__ void et_copy(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // Descriptor of an operand that is contiguous along M or N, 128-byte swizzled:
 // 64 of those by 8 of the contraction are an atom of 1024 bytes; atoms follow each
 // other along the contraction, and groups of 64 along M or N are kEtGroup apart. A step
@@ -137,7 +151,7 @@ __device__ __forceinline__ uint32_t et_idesc(int bf16, int n) {
 }
 
 // The weights' part of the stages. (Returns the stages it loaded.)
-template <int MODE>
+template <int MODE, int MT>
 __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, int ring, int units, FastDiv tiles,
                          FastDiv ctiles, volatile int* abort) {
   const bool lead = mx_elect();
@@ -146,17 +160,21 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
   int it = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
-    const int stages = (m.depth + 63) / 64;
+    const int stages = (m.depth + 63) / 64, halves = et_halves<MT>(a, m), c0 = m.tile * (MT * 128);
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
       if (it >= ring && !mx_wait_warp(&B.wempty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
-      const uint32_t st = base + (uint32_t)r.slot * kEtABytes, bar = bar0 + (uint32_t)r.slot * 8;
+      const uint32_t st = base + (uint32_t)r.slot * (MT * kEtABytes), bar = bar0 + (uint32_t)r.slot * 8;
       if (lead) {
-        mx_expect(bar, kEtABytes);
-        if (MODE == kExForward) {
-          et_tma_3d(st, &a.map, s * 64, m.tile * 128, m.expert, bar);
-        } else {
-          et_tma_3d(st, &a.map, m.tile * 128, s * 64, m.expert, bar);
-          et_tma_3d(st + kEtGroup, &a.map, m.tile * 128 + 64, s * 64, m.expert, bar);
+        mx_expect(bar, halves * kEtABytes);
+#pragma unroll
+        for (int h = 0; h < MT; ++h) {
+          if (h >= halves) break;
+          if (MODE == kExForward) {
+            et_tma_3d(st + h * kEtABytes, &a.map, s * 64, c0 + h * 128, m.expert, bar);
+          } else {
+            et_tma_3d(st + h * kEtABytes, &a.map, c0 + h * 128, s * 64, m.expert, bar);
+            et_tma_3d(st + h * kEtABytes + kEtGroup, &a.map, c0 + h * 128 + 64, s * 64, m.expert, bar);
+          }
         }
       }
     }
@@ -164,75 +182,152 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
   return it;
 }
 
-// The rows' part. A stage's rows are copied four at a time; lanes of all the row
-// warps take a copy each. (Returns the stages it loaded.)
-template <int MODE>
-__device__ int et_rows(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t stage_bytes, int ring, int units,
-                       FastDiv tiles, FastDiv ctiles, FastDiv topk, volatile int* abort) {
+// The rows' part of the stages, by sixteen warps: TMA copies of four rows (one warp
+// alone took 65-73 cycles to issue each; sixteen together some 9 to 12), and for dW in
+// tiles of 256 x's rows by cp.async, 16 bytes a lane (some 14 cycles for 512 of them).
+// TMA and the load/store unit are different parts of the SM and together move
+// more (large, dW: 745 us by TMA alone, 682 so; forward 478 by TMA, 489 and 526 with
+// half and all of the rows by cp.async). cp.async writes by the generic proxy; the
+// issuer's fence behind the stage's barrier shows it to the tensor cores.
+template <int MODE, int MT>
+struct EtRowPlan {
+  static constexpr int kCopyWarps = MT == 2 && MODE == kExGradW ? 8 : 0;  // by cp.async: the last ones
+  static constexpr int kTmaWarps = kEtRowWarps - kCopyWarps;
+  static constexpr int kArrivals = kTmaWarps + 32 * kCopyWarps;  // of a stage
+};
+
+// What the row warps' walk through units and stages has in common. (Returns the
+// stages.)
+struct EtWalk {
+  EtBars& B;
+  volatile int* abort;
+  uint32_t base, stage_bytes;
+  int ring, it;
+  MxRing r;
+  // waits for the stage's place; its shared address in `st`
+  __device__ __forceinline__ bool next(uint32_t& st) {
+    if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return false;
+    st = base + (uint32_t)r.slot * stage_bytes;
+    return true;
+  }
+  __device__ __forceinline__ void done() {
+    ++it;
+    r.next(ring);
+  }
+};
+
+// By TMA. (Returns the stages it loaded.)
+template <int MODE, int MT>
+__device__ int et_rows_tma(const EtArgs& a, const EtGroups& g, EtWalk k, int units, FastDiv tiles, FastDiv ctiles, FastDiv topk) {
+  constexpr int kWarps = EtRowPlan<MODE, MT>::kTmaWarps;
   const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - kEtEpiWarps;
   auto source = [&](int route) { return a.per_route ? route : (int)topk.div((uint32_t)route); };
-  const uint32_t bar0 = smem_u32(&B.full[0]);
-  MxRing r;
-  int it = 0;
-  if (MODE == kExGradW) {
-    // warp: four rows of a stage; lanes 0..5: the groups of 64 columns of dy, then x
-    constexpr int kPer = kEtRowWarps / 16;
-    static_assert(kPer == 1, "a warp for each four rows of a stage");
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
-      const int stages = (m.depth + 63) / 64, groups = (m.rows + 63) / 64, agroups = a.M - m.tile * 128 > 64 ? 2 : 1;
+  uint32_t st;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+    const int stages = (m.depth + 63) / 64;
+    if constexpr (MODE == kExGradW) {
+      // a lane for a group of 64 columns of four rows: first dy's groups, then (if it has no
+      // warps of its own) x's; eight lanes to four rows
+      constexpr int kQuads = 16 / kWarps;  // of a warp
+      const int quad = warp * kQuads + (lane >> 3), c = lane & 7, c0 = m.tile * (MT * 128);
+      const int agroups = min(2 * MT, (a.M - c0 + 63) / 64), groups = MT == 1 ? (m.rows + 63) / 64 : 0;
       int q[4];
       auto look = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = __ldg(a.order + m.slot0 + min(s * 64 + warp * 4 + i, m.depth - 1));
+        for (int i = 0; i < 4; ++i) q[i] = __ldg(a.order + m.slot0 + min(s * 64 + quad * 4 + i, m.depth - 1));
       };
       if (stages) look(0);
-      for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
-        if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
-        const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
-        const bool some = s * 64 + warp * 4 < (m.depth + 15) / 16 * 16;
-        if (lane == 0) mx_expect(bar, some ? (uint32_t)((agroups + groups) * 512) : 0u);
+      for (int s = 0; s < stages; ++s, k.done()) {
+        if (!k.next(st)) return k.it;
+        const uint32_t bar = smem_u32(&k.B.full[k.r.slot]);
+        const bool some = lane < 8 * kQuads && s * 64 + quad * 4 < (m.depth + 15) / 16 * 16;
+        const bool isg = some && c < agroups, isx = MT == 1 && some && c < groups;
+        const uint32_t bytes = 512u * (__popc(__ballot_sync(0xFFFFFFFFu, isg)) + __popc(__ballot_sync(0xFFFFFFFFu, isx)));
+        if (lane == 0) mx_expect(bar, bytes);
         __syncwarp();
-        if (some && lane < agroups + groups) {
-          const bool isx = lane >= agroups;
-          const int c = isx ? lane - agroups : lane;
-          int t[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[i] = isx ? source(q[i]) : q[i];
-          et_gather4(st + (isx ? kEtABytes : 0) + c * kEtGroup + warp * 512, isx ? &a.xmap : &a.gmap,
-                     (isx ? m.col0 : m.tile * 128) + c * 64, t, bar);
+        if (isg) et_gather4(st + c * kEtGroup + quad * 512, &a.gmap, c0 + c * 64, q, bar);
+        if (MT == 1) {
+          __syncwarp();
+          if (isx) {
+            const int t[4] = {source(q[0]), source(q[1]), source(q[2]), source(q[3])};
+            et_gather4(st + MT * kEtABytes + c * kEtGroup + quad * 512, &a.xmap, m.col0 + c * 64, t, bar);
+          }
         }
+        __syncwarp();
         if (s + 1 < stages) look(s + 1);
       }
-    }
-  } else {
-    // lanes 0..3 of a warp: four rows each
-    const int quad = warp + (lane & 3) * kEtRowWarps;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
-      const int stages = (m.depth + 63) / 64, quads = et_up16(m.rows) / 4;
+    } else {
+      // the first lanes of a warp: four rows each
+      constexpr int kPer = 64 / kWarps;
+      const int quad = warp + (lane % kPer) * kWarps, quads = et_up16(m.rows) / 4;
       int q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int route = __ldg(a.order + m.slot0 + min(quad * 4 + i, m.rows - 1));
         q[i] = MODE == kExForward ? source(route) : route;
       }
-      const bool mine = lane < 4 && quad < quads;
+      const bool mine = lane < kPer && quad < quads;
       const uint32_t bytes = 512u * __popc(__ballot_sync(0xFFFFFFFFu, mine));
-      for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
-        if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
-        const uint32_t st = base + (uint32_t)r.slot * stage_bytes, bar = bar0 + (uint32_t)r.slot * 8;
+      for (int s = 0; s < stages; ++s, k.done()) {
+        if (!k.next(st)) return k.it;
+        const uint32_t bar = smem_u32(&k.B.full[k.r.slot]);
         if (lane == 0) mx_expect(bar, bytes);
         __syncwarp();
         if (mine) et_gather4(st + (uint32_t)quad * 512, MODE == kExForward ? &a.xmap : &a.gmap, s * 64, q, bar);
+        __syncwarp();
       }
     }
   }
-  return it;
+  return k.it;
+}
+
+// x's rows of dW's stages by cp.async; what it copied has landed when it returns.
+template <int MODE, int MT>
+__device__ void et_rows_copy(const EtArgs& a, const EtGroups& g, EtWalk k, int units, FastDiv tiles, FastDiv ctiles, FastDiv topk) {
+  constexpr int kWarps = EtRowPlan<MODE, MT>::kCopyWarps, kSweep = kWarps * 4, kSweeps = 64 / kSweep;  // rows at once
+  const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - kEtEpiWarps - EtRowPlan<MODE, MT>::kTmaWarps;
+  const int chunk = lane & 7, row = warp * 4 + (lane >> 3);
+  const uint32_t at = (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
+  uint32_t st;
+  bool ok = true;
+  for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
+    const int stages = (m.depth + 63) / 64, k0 = m.col0 + chunk * 8, groups = (m.rows + 63) / 64;
+    int route[kSweeps];
+    auto look = [&](int s) {
+#pragma unroll
+      for (int h = 0; h < kSweeps; ++h) {
+        const int i = s * 64 + h * kSweep + row;
+        route[h] = i < m.depth ? __ldg(a.order + m.slot0 + i) : -1;
+      }
+    };
+    if (stages) look(0);
+    for (int s = 0; s < stages; ++s, k.done()) {
+      if (!(ok = k.next(st))) break;
+      const int rows = et_up16(min(64, m.depth - s * 64));
+#pragma unroll
+      for (int h = 0; h < kSweeps; ++h) {
+        if (h * kSweep + row >= rows) break;
+        const bool in = route[h] >= 0;  // (rows past the last route: zeros)
+        const uint16_t* p = a.x + (in ? (size_t)(a.per_route ? route[h] : (int)topk.div((uint32_t)route[h])) * a.ldx + k0 : 0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= groups) break;
+          const int bytes = in ? min(16, max(0, (a.cols - k0 - c * 64) * 2)) : 0;
+          et_copy(st + MT * kEtABytes + c * kEtGroup + h * kSweep * 128 + at, bytes ? p + c * 64 : a.x, bytes);
+        }
+      }
+      cp_async_mbar_arrive(&k.B.full[k.r.slot]);
+      if (s + 1 < stages) look(s + 1);
+    }
+  }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+  __syncwarp();
 }
 
 // (returns the stages whose MMAs it issued)
-template <int MODE>
+template <int MODE, int MT>
 __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t wbase, EtRings rings, int units,
                          FastDiv tiles, FastDiv ctiles, uint32_t tmem, volatile int* abort) {
   const bool lead = mx_elect();
@@ -242,33 +337,42 @@ __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64;
     if (stages == 0) continue;
-    const int buf = nu & 1;
-    if (nu >= 2 && !mx_wait_warp(&B.acc_empty[buf], ((nu >> 1) - 1) & 1, abort, kMxWaitNs)) return it;
+    const int buf = a.bufs == 2 ? nu & 1 : 0, turn = a.bufs == 2 ? nu >> 1 : nu;
+    if (turn >= 1 && !mx_wait_warp(&B.acc_empty[buf], (turn - 1) & 1, abort, kMxWaitNs)) return it;
     ++nu;
     tc_fence_after();
-    const uint32_t idesc = et_idesc<MODE>(a.bf16, et_up16(m.rows)), d = tmem + (uint32_t)(buf * a.bn);
+    const uint32_t idesc = et_idesc<MODE>(a.bf16, et_up16(m.rows)), d = tmem + (uint32_t)(buf * MT * a.bn);
+    const int halves = et_halves<MT>(a, m);
     for (int s = 0; s < stages; ++s, ++it, r.next(rings.rows), rw.next(rings.weights)) {
       if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, kMxWaitNs)) return it;
+      if (EtRowPlan<MODE, MT>::kCopyWarps) fence_proxy_async();
       if (MODE != kExGradW && !mx_wait_warp(&B.wfull[rw.slot], rw.phase, abort, kMxWaitNs)) return it;
-      const uint32_t st = base + (uint32_t)r.slot * rings.stage, wt = wbase + (uint32_t)rw.slot * kEtABytes;
+      const uint32_t st = base + (uint32_t)r.slot * rings.stage, wt = wbase + (uint32_t)rw.slot * (MT * kEtABytes);
       const int left = min(64, m.depth - s * 64), steps = (left + 15) / 16;
       if (MODE == kExGradW && (left & 15)) {
-        // rows past the last route, which the copies filled with some row, become zeros in both operands
-        const int groups = 2 + (m.rows + 63) / 64, n = (et_up16(left) - left) * 8;
-        for (int i = threadIdx.x & 31; i < groups * n; i += 32) {
-          const int c = i / n, w = i - c * n;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(st + c * kEtGroup + left * 128 + w * 16), "r"(0) : "memory");
-        }
+        // Rows past the last route, which the gather filled with some row, become zeros: of both
+        // operands, since zero times infinity is none.
+        const int groups = 2 * MT + (MT == 1 ? (m.rows + 63) / 64 : 0), lane = threadIdx.x & 31;
+        for (int c = 0; c < groups; ++c)
+          for (int i = left + (lane >> 3); i < et_up16(left); i += 4)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(st + c * kEtGroup + i * 128 + (lane & 7) * 16), "r"(0)
+                         : "memory");
         fence_proxy_async();
         __syncwarp();
       }
       tc_fence_after();
       const uint64_t ad = MODE == kExForward ? smem_desc_sw128(wt) : et_desc_mn(MODE == kExGradX ? wt : st);
-      const uint64_t bd = MODE == kExGradW ? et_desc_mn(st + kEtABytes) : smem_desc_sw128(st);
+      const uint64_t bd = MODE == kExGradW ? et_desc_mn(st + MT * kEtABytes) : smem_desc_sw128(st);
       constexpr uint64_t sa = MODE == kExForward ? 2 : 128, sb = MODE == kExGradW ? 128 : 2;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (k < steps && lead) tc_mma_f16(d, ad + k * sa, bd + k * sb, idesc, s > 0 || k > 0 ? 1u : 0u);
+        if (k < steps) {
+#pragma unroll
+          for (int h = 0; h < MT; ++h)
+            if (h < halves && lead)
+              tc_mma_f16(d + (uint32_t)(h * a.bn), ad + (uint64_t)(h * (kEtABytes >> 4)) + k * sa, bd + k * sb, idesc,
+                         s > 0 || k > 0 ? 1u : 0u);
+        }
       if (lead) tc_commit(&B.empty[r.slot]);
       if (MODE != kExGradW && lead) tc_commit(&B.wempty[rw.slot]);
     }
@@ -296,7 +400,7 @@ __device__ __forceinline__ void et_store_tile(const uint4 (&v)[8], unsigned char
   }
 }
 
-template <int MODE, typename O>
+template <int MODE, int MT, typename O>
 __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int units, FastDiv tiles, FastDiv ctiles, uint32_t tmem,
                             unsigned char* stage, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -316,31 +420,43 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
       }
     }
     const bool some = m.depth > 0;
-    const int buf = nu & 1, n = m.tile * 128 + quarter * 32 + lane;
+    const int buf = a.bufs == 2 ? nu & 1 : 0, turn = a.bufs == 2 ? nu >> 1 : nu, halves = et_halves<MT>(a, m);
     if (some) {
-      const bool full = mx_wait_warp(&B.acc_full[buf], (nu >> 1) & 1, abort, kMxWaitNs);
+      const bool full = mx_wait_warp(&B.acc_full[buf], turn & 1, abort, kMxWaitNs);
       // the warps of a part meet at its barrier while they store: they go on together or not at all
       if (!mx_vote_part(full, 1 + part)) break;
       ++nu;
       tc_fence_after();
     }
-    const uint32_t d = tmem + lane_base + (uint32_t)(buf * a.bn);
+    // the accumulators are free when the warp's last piece of them is in registers
+    bool held = some;
+    auto release = [&]() {
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
+      __syncwarp();
+      held = false;
+    };
+    for (int h = 0; h < halves; ++h) {
+    const uint32_t d = tmem + lane_base + (uint32_t)((buf * MT + h) * a.bn);
+    const int tile = m.tile * MT + h, n = tile * 128 + quarter * 32 + lane;  // of 128 channels
+    const bool last = h == halves - 1;
     if (MODE == kExGradW) {
       constexpr int kCols = 128 / (int)sizeof(O);  // columns of 128 bytes
-      const int n0 = m.tile * 128 + quarter * 32;
+      const int n0 = tile * 128 + quarter * 32;
       for (int c0 = part * kCols; c0 < m.rows; c0 += kEtEpiWarps / 4 * kCols) {
         uint4 q[8];
         O* e = reinterpret_cast<O*>(q);
         if (some) {
 #pragma unroll
-          for (int h = 0; h < kCols; h += 32) {
+          for (int i = 0; i < kCols; i += 32) {
             uint32_t v[32];
-            tmem_ld32(d + c0 + h, v);
+            tmem_ld32(d + c0 + i, v);
             tmem_ld_wait();
             reg_fence32(v);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) e[h + c] = from_f32<O>(__uint_as_float(v[c]));
+            for (int c = 0; c < 32; ++c) e[i + c] = from_f32<O>(__uint_as_float(v[c]));
           }
+          if (last && c0 + kEtEpiWarps / 4 * kCols >= m.rows) release();
         } else {
 #pragma unroll
           for (int c = 0; c < 8; ++c) q[c] = make_uint4(0, 0, 0, 0);
@@ -353,6 +469,7 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
           for (int c = 0; c < kCols; ++c)
             if (c0 + c < m.rows) o[c] = e[c];
         }
+        __syncwarp();  // (tcgen05.ld is for a converged warp)
       }
     }
 #pragma unroll
@@ -367,21 +484,19 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
         reg_fence32(v);
 #pragma unroll
         for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(v[c]);
+        if (last && c0 + kStep >= m.rows) release();
       } else {
 #pragma unroll
         for (int c = 0; c < 32; ++c) y[c] = 0.0f;
       }
-      if (sizeof(O) == 2 && a.vec) {
-        mx_store32_words<O>(y, out, row[k], m.rows - c0, m.tile, a.M, stage + part * kEtStoreBytes, 1 + part);
-      } else {
+      if (sizeof(O) == 2 && a.vec)
+        mx_store32_words<O>(y, out, row[k], m.rows - c0, tile, a.M, stage + part * kEtStoreBytes, 1 + part);
+      else
         mx_store32<O>(y, out, row[k], m.rows - c0, n, a.M);
-      }
+      __syncwarp();  // (tcgen05.ld is for a converged warp)
     }
-    if (some) {
-      tc_fence_before();
-      if (lane == 0) mbar_arrive(&B.acc_empty[buf]);
     }
-    __syncwarp();
+    if (held) release();  // (it had no piece)
   }
   if (MODE == kExGradW) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
 }
@@ -389,19 +504,19 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
 template <int MODE>
 constexpr uint32_t et_store_bytes() { return (MODE == kExGradW ? kEtEpiWarps : kEtEpiWarps / 4) * kEtStoreBytes; }
 
-template <int MODE, typename O>
+template <int MODE, int MT, typename O>
 __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__ EtArgs a, EtRings rings, FastDiv tiles, FastDiv ctiles,
                                                          FastDiv topk) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t wofs = (uint32_t)rings.rows * rings.stage;
-  unsigned char* store = smem + wofs + (uint32_t)rings.weights * kEtABytes;
+  unsigned char* store = smem + wofs + (uint32_t)rings.weights * (MT * kEtABytes);
   EtShared& sh = *reinterpret_cast<EtShared*>(store + et_store_bytes<MODE>());
   EtBars& bars = sh.bars;
   EtGroups& groups = sh.groups;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < rings.rows; ++i) {
-      mbar_init(&bars.full[i], kEtRowWarps);
+      mbar_init(&bars.full[i], EtRowPlan<MODE, MT>::kArrivals);
       mbar_init(&bars.empty[i], 1);
     }
     for (int i = 0; i < rings.weights; ++i) {
@@ -416,6 +531,7 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
     mbar_fence_init();
   }
   if (MODE != kExGradW && threadIdx.x == kEtEpiWarps * 32) mx_prefetch_map(&a.map);
+  __syncwarp();
   if (warp == 0) tmem_alloc(&sh.tmem_slot, 512);
   grid_wait();
   grid_launch();
@@ -446,18 +562,23 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   volatile int* abort = &sh.abort;
   int loaded = 0, rows_loaded = 0, issued = 0;
   if (warp < kEtEpiWarps)
-    et_epilogue<MODE, O>(a, groups, bars, units, tiles, ctiles, tmem, store, abort);
-  else if (warp < kEtEpiWarps + kEtRowWarps)
-    rows_loaded = et_rows<MODE>(a, groups, bars, base, rings.stage, rings.rows, units, tiles, ctiles, topk, abort);
-  else if (warp == kEtEpiWarps + kEtRowWarps) {
-    if (MODE != kExGradW) loaded = et_loader<MODE>(a, groups, bars, base + wofs, rings.weights, units, tiles, ctiles, abort);
+    et_epilogue<MODE, MT, O>(a, groups, bars, units, tiles, ctiles, tmem, store, abort);
+  else if (warp < kEtEpiWarps + kEtRowWarps) {
+    const EtWalk walk{bars, abort, base, rings.stage, rings.rows, 0, MxRing()};
+    using Plan = EtRowPlan<MODE, MT>;
+    if (warp < kEtEpiWarps + Plan::kTmaWarps) rows_loaded = et_rows_tma<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
+    if constexpr (Plan::kCopyWarps > 0)
+      if (warp >= kEtEpiWarps + Plan::kTmaWarps) et_rows_copy<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
+  } else if (warp == kEtEpiWarps + kEtRowWarps) {
+    if (MODE != kExGradW) loaded = et_loader<MODE, MT>(a, groups, bars, base + wofs, rings.weights, units, tiles, ctiles, abort);
   } else
-    issued = et_issuer<MODE>(a, groups, bars, base, base + wofs, rings, units, tiles, ctiles, tmem, abort);
+    issued = et_issuer<MODE, MT>(a, groups, bars, base, base + wofs, rings, units, tiles, ctiles, tmem, abort);
   tc_fence_before();
   __syncthreads();
   if (*abort) {  // (nobody sets it any more: the same for all)
-    // what a CTA that gave up has in flight ends before its shared and tensor memory go (the
-    // row warps have waited for their copies)
+    // What a CTA that gave up has in flight ends before its shared and tensor memory go. (A
+    // stage that some warps never filled is waited for until the limit, by when the others'
+    // copies have landed; cp.async's have been waited for.)
     int never = 0;
     for (int i = max(0, loaded - rings.weights); i < loaded; ++i)
       mbar_wait_abort(&bars.wfull[i % rings.weights], (i / rings.weights) & 1, &never, kMxDrainNs);
@@ -468,6 +589,7 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
     __syncthreads();
   }
   tc_fence_after();
+  __syncwarp();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -501,30 +623,40 @@ cudaError_t et_map2(CUtensorMap* m, int dtype, const void* p, int cols, long row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int MODE, typename O>
-cudaError_t et_launch(const EtArgs& a, int topk, int sms, cudaStream_t st) {
-  auto kern = k_ex_tc<MODE, O>;
+template <int MODE, int MT, typename O>
+cudaError_t et_launch(EtArgs a, int topk, int sms, cudaStream_t st) {
+  auto kern = k_ex_tc<MODE, MT, O>;
   static OncePerDevice done;
   const cudaError_t limit = allow_smem(done, kern, (int)kEtSmem);
   if (limit != cudaSuccess) return limit;
   const uint32_t rest = et_store_bytes<MODE>() + (uint32_t)sizeof(EtShared), room = kEtSmem - rest;
   EtRings rings;
   if (MODE == kExGradW) {
-    rings.stage = kEtABytes + (uint32_t)a.bn * 128;
+    rings.stage = MT * kEtABytes + (uint32_t)a.bn * 128;
     rings.rows = (int)std::min<uint32_t>(kEtMaxRing, room / rings.stage);
     rings.weights = 0;
   } else {
     rings.stage = (uint32_t)a.bn * 128;
     rings.rows = (int)std::min<uint32_t>(8, 96 * 1024 / rings.stage);  // (3 of 256 rows)
-    rings.weights = (int)std::min<uint32_t>(kEtMaxRing, (room - rings.rows * rings.stage) / kEtABytes);
+    rings.weights = (int)std::min<uint32_t>(kEtMaxRing, (room - rings.rows * rings.stage) / (MT * kEtABytes));
   }
-  const long tiles = (a.M + 127) / 128, ctiles = MODE == kExGradW ? (a.cols + a.bn - 1) / a.bn : 1;
+  a.bufs = 2 * MT * a.bn <= 512 ? 2 : 1;
+  const long tiles = (a.M + MT * 128 - 1) / (MT * 128), ctiles = MODE == kExGradW ? (a.cols + a.bn - 1) / a.bn : 1;
   const long units = MODE == kExGradW ? (long)a.E * tiles * ctiles : ((long)a.R / a.bn + std::min<long>(a.R, a.E + 1)) * tiles;
   if (units >= 1L << 31) return cudaErrorInvalidConfiguration;
   const int grid = (int)std::max<long>(1, std::min<long>(units, sms));
-  return launch_after(kern, dim3(grid), kEtThreads, rings.rows * rings.stage + rings.weights * kEtABytes + rest, st, a, rings, FastDiv((uint32_t)tiles),
+  return launch_after(kern, dim3(grid), kEtThreads, rings.rows * rings.stage + rings.weights * (MT * kEtABytes) + rest, st, a, rings, FastDiv((uint32_t)tiles),
                       FastDiv((uint32_t)ctiles), FastDiv((uint32_t)topk));
 }
+
+// Whether tiles have 256 channels, not 128: then the rows, which every tile of
+// channels reads anew, are read half as often, and where there are many of them
+// to an expert that counts (large: 205 routes an expert, forward 568 -> 480 us, dx 592
+// -> 462, dW 840 -> 745; uneven: 128, 74 -> 66, 99 -> 89, 103 -> 96). With few, the
+// weights are all that counts, and more, smaller tiles spread better over the SMs
+// (one token: dx 27.1 us with 128 and 31.4 with 256; decode: 23.1 and 23.9; odd, 80
+// routes an expert: 52.7 and 52.1, 67.3 and 66.7, dW 55.5 and 59.7).
+bool et_wide(int R, int E) { return R >= 96L * E; }
 
 bool et_rows_ok(const void* p, int64_t ld) { return ((uintptr_t)p) % 16 == 0 && ld % 8 == 0 && ld < (1LL << 38); }
 
@@ -542,6 +674,7 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   const int R = a.T * a.topk, es = a.out_dtype == TM_F32 ? 4 : 2;
   t.E = a.E, t.R = R, t.bf16 = a.dtype == TM_BF16, t.per_route = a.per_route;
   t.order = a.order, t.offsets = a.offsets, t.out = a.out, t.flags = a.flags;
+  t.x = static_cast<const uint16_t*>(a.x), t.ldx = a.ldx;
   if (a.mode != kExGradX) {
     const cudaError_t e = et_map2(&t.xmap, a.dtype, a.x, a.K, a.per_route ? R : a.T, a.ldx);
     if (e != cudaSuccess) return e;
@@ -565,11 +698,14 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
     t.vec = ((uintptr_t)a.out) % 16 == 0 && t.M % 8 == 0;
   }
   if (e != cudaSuccess) return e;
+  const bool wide = et_wide(R, a.E);
   auto go = [&](auto elem) {
     using O = decltype(elem);
-    return a.mode == kExForward ? et_launch<kExForward, O>(t, a.topk, sms, st)
-         : a.mode == kExGradX   ? et_launch<kExGradX, O>(t, a.topk, sms, st)
-                                : et_launch<kExGradW, O>(t, a.topk, sms, st);
+    if (a.mode == kExForward)
+      return wide ? et_launch<kExForward, 2, O>(t, a.topk, sms, st) : et_launch<kExForward, 1, O>(t, a.topk, sms, st);
+    if (a.mode == kExGradX)
+      return wide ? et_launch<kExGradX, 2, O>(t, a.topk, sms, st) : et_launch<kExGradX, 1, O>(t, a.topk, sms, st);
+    return wide ? et_launch<kExGradW, 2, O>(t, a.topk, sms, st) : et_launch<kExGradW, 1, O>(t, a.topk, sms, st);
   };
   return TM_BY_DTYPE(a.out_dtype, go);
 }
