@@ -20,13 +20,12 @@ constexpr int kExMaxSide = 1 << 20;  // N and K
 // ------------------------------------------------------------------ the plan
 // Routes sorted by expert, stably: their order is that of the sums in dW, which
 // so do not depend on the run. A warp takes a stretch of the routes, 32 at a
-// time: lanes of one expert find each other (match), the lowest adds their
-// number to the warp's count. Counts are summed over the warps and the CTAs of
-// the cluster, and the same walk gives every route its place. Ids outside
-// 0..E-1 form a last group. Bound by latency: one CTA for up to kPlanAlone routes,
-// a cluster beyond; ids of up to kPlanHeld walks stay in registers.
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+// time: lanes of one expert find each other, the lowest adds their number to the
+// warp's count. Counts are summed over the warps and the CTAs of the cluster, and
+// the same walk gives every route its place. Ids outside 0..E-1 form a last
+// group. Bound by latency: one CTA for up to kPlanAlone routes, a cluster beyond;
+// what the first kPlanHeld steps found stays in registers.
+constexpr int kPlanThreads = 1024, kPlanFew = 512;  // of a CTA of the cluster, of the one CTA
 constexpr int kPlanCtas = 8;
 constexpr int kPlanHeld = 4;
 constexpr int kPlanAlone = 2048;
@@ -40,40 +39,57 @@ __device__ __forceinline__ int plan_peer(const int* p, int rank) {
   return v;
 }
 
-template <int CTAS>
-__global__ void __launch_bounds__(kPlanThreads)
+// The lanes with the same group, bit by bit. (match.any serves one warp of an SM
+// at a time, some 70 cycles each: 32768 routes took 14.8 us.)
+__device__ __forceinline__ uint32_t plan_same(int e, int bits) {
+  uint32_t same = 0xFFFFFFFFu;
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
+    same &= e >> b & 1 ? v : ~v;
+  }
+  return same;
+}
+
+template <int CTAS, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     k_ex_plan(const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ order, int32_t* __restrict__ offsets,
               uint32_t* __restrict__ flags) {
+  constexpr int kPlanWarps = THREADS / 32;
   __shared__ int s_cnt[kPlanWarps][kPlanGroups];  // counts, then places, by warp
   __shared__ int s_all[kPlanGroups];              // the CTA's counts
   __shared__ int s_scan[kPlanGroups], s_warp[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = E + 1;
   uint32_t rank = 0;
   if (CTAS > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  for (int i = tid; i < kPlanWarps * kPlanGroups; i += kPlanThreads) (&s_cnt[0][0])[i] = 0;
+  for (int i = tid; i < kPlanWarps * kPlanGroups; i += THREADS) (&s_cnt[0][0])[i] = 0;
   __syncthreads();
   grid_wait();
   grid_launch();
   const int per = (R + CTAS * kPlanWarps - 1) / (CTAS * kPlanWarps);  // routes of a warp
   const int lo = min((long)R, (long)per * (rank * kPlanWarps + warp)), hi = min(R, lo + per);
+  const int bits = 32 - __clz(E + 1);  // (groups 0..E, and E + 1 for no route)
   auto group = [&](int r) {
-    const int e = r < hi ? ids[r] : -2;
-    return r < hi ? (e >= 0 && e < E ? e : E) : -1;
+    const int e = r < hi ? ids[r] : 0;
+    return r < hi ? (e >= 0 && e < E ? e : E) : E + 1;
   };
   int held[kPlanHeld];
+  uint32_t same[kPlanHeld];
 #pragma unroll
   for (int u = 0; u < kPlanHeld; ++u) held[u] = group(lo + u * 32 + lane);
-  auto walk = [&](auto f) {
-#pragma unroll
-    for (int u = 0; u < kPlanHeld; ++u)
-      if (lo + u * 32 < hi) f(lo + u * 32 + lane, held[u]);
-    for (int r = lo + kPlanHeld * 32; r < hi; r += 32) f(r + lane, group(r + lane));
-  };
-  walk([&](int, int e) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) s_cnt[warp][e] += __popc(same);
+  auto count = [&](int e, uint32_t m) {
+    if (e <= E && lane == __ffs(m) - 1) s_cnt[warp][e] += __popc(m);
     __syncwarp();
-  });
+  };
+#pragma unroll
+  for (int u = 0; u < kPlanHeld; ++u)
+    if (lo + u * 32 < hi) {
+      same[u] = plan_same(held[u], bits);
+      count(held[u], same[u]);
+    }
+  for (int r = lo + kPlanHeld * 32; r < hi; r += 32) {
+    const int e = group(r + lane);
+    count(e, plan_same(e, bits));
+  }
   __syncthreads();
   int all = 0;
   if (tid < G) {
@@ -122,17 +138,19 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
   }
   __syncthreads();
-  walk([&](int r, int e) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    int at = 0;
-    if (e >= 0) at = s_scan[e] + s_cnt[warp][e] + __popc(same & ((1u << lane) - 1));
+  auto place = [&](int r, int e, uint32_t m) {
+    if (e <= E) order[s_scan[e] + s_cnt[warp][e] + __popc(m & ((1u << lane) - 1))] = r;
     __syncwarp();
-    if (e >= 0) {
-      order[at] = r;
-      if (lane == __ffs(same) - 1) s_cnt[warp][e] += __popc(same);
-    }
-    __syncwarp();
-  });
+    count(e, m);
+  };
+#pragma unroll
+  for (int u = 0; u < kPlanHeld; ++u)
+    if (lo + u * 32 < hi) place(lo + u * 32 + lane, held[u], same[u]);
+  for (int r = lo + kPlanHeld * 32; r < hi; r += 32) {
+    const int e = group(r + lane);
+    place(r + lane, e, plan_same(e, bits));
+  }
+  __syncwarp();
   if (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no CTA leaves while another reads its counts
 }
 
@@ -322,7 +340,7 @@ __global__ void __launch_bounds__(256) k_ex_sum(const float* __restrict__ rows, 
 
 cudaError_t launch_ex_plan(const int32_t* ids, int R, int E, int32_t* order, int32_t* offsets, uint32_t* flags,
                            cudaStream_t st) {
-  if (R <= kPlanAlone) return launch_after(k_ex_plan<1>, dim3(1), kPlanThreads, 0, st, ids, R, E, order, offsets, flags);
+  if (R <= kPlanAlone) return launch_after(k_ex_plan<1, kPlanFew>, dim3(1), kPlanFew, 0, st, ids, R, E, order, offsets, flags);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kPlanCtas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -335,7 +353,7 @@ cudaError_t launch_ex_plan(const int32_t* ids, int R, int E, int32_t* order, int
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_ex_plan<kPlanCtas>, ids, R, E, order, offsets, flags);
+  return cudaLaunchKernelEx(&cfg, k_ex_plan<kPlanCtas, kPlanThreads>, ids, R, E, order, offsets, flags);
 }
 
 cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, int dtype, cudaStream_t st) {
