@@ -573,7 +573,8 @@ tm_status trellis_moe_token_logprobs_backward(const void* logits, int32_t dtype,
  *   loss [T] = sum_j q_j (ln q_j - ln p_(i_j))          (terms of q_j = 0 are 0)
  *   gradient = grad_loss / temperature (p_i sum_j q_j - sum_(j: i_j = i) q_j)
  * mask [T] (NULL: all true): a row where it is 0 has loss and gradient 0, and
- * its logits are not read. stats as above (a masked row's are 0). Rows with -inf,
+ * its logits are not read. stats [T, 5]: the two above, the teacher's two (v -
+ * third) / temperature - fourth = ln q, and sum q (a masked row's are 0). Rows with -inf,
  * NaN or +inf as above. 1 <= n <= 256. The gradient's place as above.
  * loss_grad is both at once, the logits read once, for a caller who knows
  * grad_loss beforehand (1/T for a mean). */

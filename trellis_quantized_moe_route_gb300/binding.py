@@ -1127,7 +1127,7 @@ def token_logprobs_backward(logits, targets, fwd: TokenLogprobs, grad_logprob=No
 class DistillOut(NamedTuple):
     """Results of distill_forward (see trellis_moe_distill_forward)."""
     loss: Any   # float32 [T]
-    stats: Any  # float32 [T, 2]
+    stats: Any  # float32 [T, 5]
 
 
 def _teacher(logits, ids, values, temperature, mask, teacher_lse):
@@ -1157,7 +1157,7 @@ def distill_forward(logits, ids, values, temperature: float = 1.0, mask=None, te
             return distill_forward(logits, ids, values, temperature, mask, teacher_lse)
     lib = _start()
     T, _, index, args = _teacher(logits, ids, values, temperature, mask, teacher_lse)
-    loss, stats = _empty(T, dtype=_f32, device=logits.device), _empty((T, 2), dtype=_f32, device=logits.device)
+    loss, stats = _empty(T, dtype=_f32, device=logits.device), _empty((T, 5), dtype=_f32, device=logits.device)
     _launch(lib.trellis_moe_distill_forward, index, *args, loss.data_ptr(), stats.data_ptr())
     return DistillOut(loss, stats)
 
@@ -1171,7 +1171,7 @@ def distill_backward(logits, ids, values, fwd: DistillOut, grad_loss, temperatur
             return distill_backward(logits, ids, values, fwd, grad_loss, temperature, mask, teacher_lse, out)
     lib = _start()
     T, V, index, args = _teacher(logits, ids, values, temperature, mask, teacher_lse)
-    _on_device("stats", fwd.stats, index, _f32, (T, 2))
+    _on_device("stats", fwd.stats, index, _f32, (T, 5))
     _on_device("grad_loss", grad_loss, index, _f32, (T,))
     out, gld = _grad_place(out, logits, T, V)
     _launch(lib.trellis_moe_distill_backward, index, *args, fwd.stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), gld)

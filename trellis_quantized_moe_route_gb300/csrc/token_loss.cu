@@ -4,12 +4,15 @@
 //   dl_i    = (g ([i = y] - p_i) - h p_i (log p_i + H)) / tau
 //   loss    = sum_j q_j (ln q_j - log p_(i_j)),   dl_i = g (Q p_i - sum_(j: i_j = i) q_j) / tau
 //
-// Bound by memory: a row is read once (and its gradient written once). A row is
-// cut into the segments of a cluster's CTAs; a CTA keeps its segment in shared
-// memory, so that the pass that writes the gradient, and the search for the
-// largest logits, need not read it again, and fetches the next row's while it
-// works on this one (cp.async: a thread reads only words that it fetched itself,
-// so that no barrier stands between). Longer rows go through in tiles.
+// Bound by memory: a row is read once, and its gradient written once.
+//   k_tl_forward: a CTA goes through a row (few rows: a cluster shares one) in
+//     tiles, the next one fetched while it works on this one. A thread reads only
+//     words that it fetched itself (cp.async) and keeps its own maximum and sums, so
+//     that no barrier stands between tiles; the threads' sums meet at the row's end.
+//   k_tl_once: loss and gradient in one pass; a cluster holds the row in shared
+//     memory between the sums and the gradient. Rows that are longer than that go
+//     through it in tiles twice.
+//   k_tl_backward: one CTA for each piece of a row.
 #include <algorithm>
 #include <cmath>
 
@@ -23,9 +26,8 @@ namespace {
 
 constexpr int kTlMaxTop = 32;
 constexpr int kTlMaxEntries = 256;
-constexpr int kTlWords = 8;      // 16-byte words of a tile that a thread holds
+constexpr int kTlWords = 8;      // 16-byte words of a tile to a thread
 constexpr int kTlCtas = 8;       // most CTAs of a cluster
-constexpr int kTlCandidates = 448;  // (what lets three CTAs share an SM)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -147,56 +149,72 @@ struct TlRow {
   }
 };
 
-// exp2 arguments of a row's elements relative to its maximum M: d = (x - M) c,
-// c = log2(e) / tau. As one fused operation, x c - round(M c), it is off by the
-// residual r = M c - round(M c), the same for all elements, which is put right in
-// what the exponentials are multiplied with: 2^-r. Where M c is so large that r
-// would not be small, the difference is taken first (`far`).
-struct TlShift {
-  float c, m, mc, r;
+// exp2 arguments of elements relative to a reference near their maximum m: with
+// c = log2(e) / tau and the whole number w nearest to m c, d = x c - w is one fused
+// operation with one rounding, and what belongs to different references differs by
+// an exact power of two. Where m c is so large that d would not stay small (`far`),
+// elements are either the maximum itself or so far below it that they do not count.
+struct TlRef {
+  float c, m, w;
   bool far;
-  __device__ __forceinline__ TlShift(float M, float scale) : c(scale), m(M) {
-    mc = M * scale;
-    far = !(fabsf(mc) < 65536.0f);
-    r = far ? 0.0f : fmaf(M, scale, -mc);
+  __device__ __forceinline__ TlRef(float max, float scale) : c(scale) {
+    m = max == -INFINITY ? 0.0f : max;
+    w = rintf(m * scale);
+    far = !(fabsf(w) < 1073741824.0f);
   }
-  template <bool FAR>
-  __device__ __forceinline__ float arg(float x) const {
-    return FAR ? (x - m) * c : fmaf(x, c, -mc);
-  }
+  __device__ __forceinline__ float arg(float x) const { return far ? (x == m ? 0.0f : x < m ? -1000.0f : NAN) : fmaf(x, c, -w); }
+  // m c - w, which the reference is below m
+  __device__ __forceinline__ float above() const { return far ? 0.0f : fmaf(m, c, -w); }
 };
 
-// Largest value, sum of exponentials relative to it and sum of those times their
-// (base 2) arguments, of a part of a row.
+// Largest value, sum of exponentials relative to its reference and sum of those
+// times their (base 2) arguments, of a part of a row.
 struct TlPart {
   float m, s, d;
+  // to the reference of a larger maximum
+  __device__ __forceinline__ void raise(float top, float c) {
+    const TlRef a(m, c), b(top, c);
+    const float u = m == top || m == -INFINITY ? 0.0f : fmaxf(a.far || b.far ? -1000.0f : a.w - b.w, -1000.0f);
+    const float e = tl_ex2(u);
+    d = e * fmaf(s, u, d);
+    s *= e;
+    m = top;
+  }
 };
 
-__device__ __forceinline__ void tl_merge(TlPart& a, float m, float c, float s, float d) {
-  const float top = tl_max_nan(a.m, m);
-  if (top == -INFINITY) return;  // (both empty)
-  const float ua = fmaxf((a.m - top) * c, -1000.0f), ub = fmaxf((m - top) * c, -1000.0f);
-  const float ea = tl_ex2(ua), eb = tl_ex2(ub);
-  a.d = ea * (a.d + a.s * ua) + eb * (d + s * ub);
-  a.s = ea * a.s + eb * s;
-  a.m = top;
+// The parts of a warp's lanes (those of lanes past `n` are not looked at), the same for all lanes.
+__device__ __forceinline__ TlPart tl_warp_merge(TlPart p, float c) {
+  const float top = tl_warp_max(p.m);
+  p.raise(top, c);
+  p.s = tl_warp_sum(p.s);
+  p.d = tl_warp_sum(p.d);
+  return p;
+}
+
+// ln sum exp of a row relative to its maximum, and sum p u' from its part. NaN
+// where the row has a NaN or +inf; -inf where it has nothing.
+__device__ __forceinline__ float tl_log_sum(const TlPart& p, float c) {
+  if (p.m == -INFINITY) return -INFINITY;
+  if (p.m != p.m || p.m == INFINITY) return NAN;
+  return logf(p.s) - TlRef(p.m, c).above() * kLn2;
 }
 
 // ------------------------------------------------------ the teacher's entries
-// Thread j has entry j. What is shared: the warps' largest value and sum, and
-// how many of the CTA's entries are in its segment; then those, in order.
-struct TlTeacher {
-  float m[8], s[8], loss[8];
-  int count[8];
-  int id[kTlMaxEntries];
+// A thread has entries threadIdx.x + j NT, j < EPT.
+constexpr int kTlStats = 5;  // of a distilled row: M, s, the teacher's maximum and its s (with teacher_lse: 0 and that), Q
+
+struct TlTeacherWarps {
+  float m[8], s[8], loss[8];  // by warp
+};
+struct TlTeacher : TlTeacherWarps {
+  int count[2][8];            // by j and warp: entries in the CTA's part of the row
+  int id[kTlMaxEntries];      // those, in their order
   float q[kTlMaxEntries], x[kTlMaxEntries];
 };
 
 struct TlEntry {
-  int id;        // -1: none
-  float v, x;    // value and the student's logit (where it was read)
-  bool mine;     // in this CTA's segment
-  uint32_t warp; // the warp's lanes whose entries are
+  int id;      // -1: none
+  float v, x;  // value and the student's logit (where it was read)
 };
 
 __device__ __forceinline__ float tl_teacher_value(const TlArgs& a, size_t i) {
@@ -205,13 +223,18 @@ __device__ __forceinline__ float tl_teacher_value(const TlArgs& a, size_t i) {
                                      : to_f32(static_cast<const __half*>(a.values)[i]);
 }
 
-__device__ __forceinline__ void tl_entry_load(const TlArgs& a, long t, TlEntry& e) {
-  e.id = -1, e.v = -INFINITY;
-  if ((int)threadIdx.x < a.n) {
-    const size_t i = (size_t)t * a.n + threadIdx.x;
-    const long id = tl_index(a.ids, a.ids64, i);
-    const float v = tl_teacher_value(a, i);
-    if (id >= 0 && id < a.V) e.id = (int)id, e.v = v;
+template <int NT, int EPT>
+__device__ __forceinline__ void tl_entry_load(const TlArgs& a, long t, TlEntry (&e)[EPT]) {
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    e[j].id = -1, e[j].v = -INFINITY, e[j].x = 0.0f;
+    const int k = threadIdx.x + j * NT;
+    if (k < a.n) {
+      const size_t i = (size_t)t * a.n + k;
+      const long id = tl_index(a.ids, a.ids64, i);
+      const float v = tl_teacher_value(a, i);
+      if (id >= 0 && id < a.V) e[j].id = (int)id, e[j].v = v;
+    }
   }
 }
 
@@ -223,81 +246,117 @@ __device__ __forceinline__ bool tl_mine(const TlRow<T>& row, int rank, int w0, i
   return (i >= lo && i < hi) || (rank == 0 && i >= V - row.tail && i < V);
 }
 
-// `all`: read every entry's logit, not only those of this CTA.
-template <typename T>
-__device__ __forceinline__ void tl_entry_start(const TlRow<T>& row, bool mine, bool all, float c, TlTeacher& te, TlEntry& e) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  e.mine = mine;
-  e.x = e.mine || (all && e.id >= 0) ? to_f32(row.p[e.id]) : 0.0f;
-  e.warp = __ballot_sync(0xFFFFFFFFu, e.mine);
-  const float m = tl_warp_max(e.v);
-  const float s = tl_warp_sum(m == -INFINITY ? 0.0f : tl_ex2((e.v - m) * c));
-  if (lane == 0) te.m[warp] = m, te.s[warp] = s, te.count[warp] = __popc(e.warp);
+// What the teacher's distribution takes from each warp; before a barrier.
+template <int NT, int EPT>
+__device__ __forceinline__ void tl_teacher_part(const TlEntry (&e)[EPT], float c, TlTeacherWarps& te) {
+  float m = -INFINITY, s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) m = tl_max_nan(m, e[j].v);
+  m = tl_warp_max(m);
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) s += m == -INFINITY ? 0.0f : tl_ex2((e[j].v - m) * c);
+  s = tl_warp_sum(s);
+  if ((threadIdx.x & 31) == 0) te.m[threadIdx.x >> 5] = m, te.s[threadIdx.x >> 5] = s;
 }
 
-// After a barrier: Q; the entry's q and ln q; this CTA's entries in te.
-__device__ __forceinline__ float tl_entry_share(const TlArgs& a, long t, int warps, float c, TlTeacher& te, const TlEntry& e,
-                                                float& q, float& lnq) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  TlPart p{-INFINITY, 0.0f, 0.0f};
-  int before = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w * 32 >= a.n) break;
-    tl_merge(p, te.m[w], c, te.s[w], 0.0f);
-    if (w < warp) before += te.count[w];
-  }
-  float Q;
-  if (p.m == -INFINITY) {
-    Q = 0.0f, lnq = -INFINITY;
-  } else if (a.teacher_lse) {
+// ln q of an entry is (v - m) / tau - s.
+struct TlTeacherSum {
+  float m, s, Q;
+};
+
+// After the barrier.
+template <int NT>
+__device__ __forceinline__ TlTeacherSum tl_teacher_sum(const TlArgs& a, long t, float c, const TlTeacherWarps& te) {
+  float m = -INFINITY, s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) m = tl_max_nan(m, te.m[w]);
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) s += te.m[w] == -INFINITY ? 0.0f : te.s[w] * tl_ex2((te.m[w] - m) * c);
+  if (m == -INFINITY) return {0.0f, 0.0f, 0.0f};
+  if (a.teacher_lse) {
     const float lse = a.teacher_lse[t];
-    Q = expf(p.m * a.inv_tau - lse) * p.s;
-    lnq = e.v * a.inv_tau - lse;
-  } else {
-    Q = p.s * (1.0f / p.s);  // (1, or NaN)
-    lnq = (e.v - p.m) * a.inv_tau - logf(p.s);
+    return {0.0f, lse, expf(m * a.inv_tau - lse) * s};
   }
-  if (e.v == -INFINITY) lnq = -INFINITY;
-  q = expf(lnq);
-  if (e.mine) {
-    const int i = before + __popc(e.warp & ((1u << lane) - 1));
-    te.id[i] = e.id, te.q[i] = q, te.x[i] = e.x;
+  return {m, logf(s), s * (1.0f / s)};  // (Q: 1, or NaN)
+}
+
+__device__ __forceinline__ float tl_ln_q(const TlEntry& e, const TlTeacherSum& k, float inv_tau) {
+  return e.v == -INFINITY ? -INFINITY : (e.v - k.m) * inv_tau - k.s;
+}
+
+// This CTA's entries in te, in order: their numbers before a barrier ...
+template <int EPT>
+__device__ __forceinline__ void tl_entry_count(const bool (&mine)[EPT], TlTeacher& te, uint32_t (&lanes)[EPT]) {
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    lanes[j] = __ballot_sync(0xFFFFFFFFu, mine[j]);
+    if ((threadIdx.x & 31) == 0) te.count[j][threadIdx.x >> 5] = __popc(lanes[j]);
   }
-  return Q;
+}
+// ... and after it themselves; returns how many.
+template <int NT, int EPT>
+__device__ __forceinline__ int tl_entry_share(const TlEntry (&e)[EPT], const bool (&mine)[EPT], const uint32_t (&lanes)[EPT],
+                                              const TlTeacherSum& k, float inv_tau, TlTeacher& te) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int all = 0;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    int at = all;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const int n = te.count[j][w];
+      at += w < warp ? n : 0;
+      all += n;
+    }
+    if (mine[j]) {
+      at += __popc(lanes[j] & ((1u << lane) - 1));
+      te.id[at] = e[j].id, te.q[at] = expf(tl_ln_q(e[j], k, inv_tau)), te.x[at] = e[j].x;
+    }
+  }
+  return all;
 }
 
 // The gradient at this CTA's entries: the same token's q add up in their order.
-template <typename T, typename P>
+template <int NT, typename T, typename P>
 __device__ __forceinline__ void tl_entry_grad(const TlTeacher& te, int count, float g, float Q, T* out, P prob) {
-  const int i = threadIdx.x;
-  if (i >= count) return;
-  const int id = te.id[i];
-  float q = 0.0f;
-  bool first = true;
-  for (int x = 0; x < count; ++x)
-    if (te.id[x] == id) {
-      first = first && x >= i;
-      q += te.q[x];
-    }
-  if (first) out[id] = from_f32<T>(g * (Q * prob(te.x[i]) - q));
+  for (int i = threadIdx.x; i < count; i += NT) {
+    const int id = te.id[i];
+    float q = 0.0f;
+    bool first = true;
+    for (int x = 0; x < count; ++x)
+      if (te.id[x] == id) {
+        first = first && x >= i;
+        q += te.q[x];
+      }
+    if (first) out[id] = from_f32<T>(g * (Q * prob(te.x[i]) - q));
+  }
 }
 
 // ------------------------------------------------------------- gradient pass
 // out = e (A + B d), e = 2^d: with B = 0 the multiple A of the probability.
-template <typename T, bool ENTROPY>
-__device__ __forceinline__ float tl_grad_value(float x, const TlShift& sh, float A, float B) {
-  float d = sh.far ? sh.arg<true>(x) : sh.arg<false>(x);
+template <bool ENTROPY>
+__device__ __forceinline__ float tl_grad_value(float x, const TlRef& r, float A, float B) {
+  float d = r.arg(x);
   if (ENTROPY) d = fmaxf(d, -1000.0f);  // (0 times infinity)
   return tl_ex2(d) * (ENTROPY ? fmaf(B, d, A) : A);
 }
 
 template <typename T, bool ENTROPY>
-__device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool vec, const TlShift& sh, float A, float B) {
+__device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool vec, const TlRef& r, float A, float B) {
   constexpr int n = TlWord<T>::kN;
   float v[n];
   w.to(v);
+  if (!r.far) {
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = tl_grad_value<T, ENTROPY>(v[i], sh, A, B);
+    for (int i = 0; i < n; ++i) {
+      float d = fmaf(v[i], r.c, -r.w);
+      if (ENTROPY) d = fmaxf(d, -1000.0f);
+      v[i] = tl_ex2(d) * (ENTROPY ? fmaf(B, d, A) : A);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = tl_grad_value<ENTROPY>(v[i], r, A, B);
+  }
   TlWord<T> o;
   o.from(v);
   if (vec) {
@@ -309,21 +368,30 @@ __device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool ve
   }
 }
 
-// ------------------------------------------------------ the largest of a tile
-// Threads of one lane number form 32 groups, over which neighbouring words are
-// spread. The `top`-th largest of the groups' maxima is a bound that at least
-// `top` elements reach. Those above it are collected (some 4 top of them for
-// random data) and ranked by counting; if they are fewer than `top`, the first
-// of those equal to it follow.
+// p = 2^d unit
+__device__ __forceinline__ float tl_unit(const TlRef& r, float log_sum) {
+  return log_sum == -INFINITY ? 0.0f : expf(-log_sum) * tl_ex2(-r.above());
+}
+
+// ------------------------------------------------------ the largest logits
+// 64 groups of threads, over which neighbouring words are spread, keep their
+// largest so far. The `top`-th largest of those is a bound that `top` elements
+// reach; what reaches it is collected as the row goes by (some top log(tiles) of
+// random values), and in the end ranked by counting. Where that is too many (equal
+// values, or rows that rise), or fewer than `top` are above -inf, the row is
+// gone through again.
 template <int NT>
 struct TlTop {
-  uint32_t group[NT];
-  unsigned long long cand[kTlCandidates], list[kTlMaxTop], best[NT / 32];
-  int n, warp[NT / 32];
+  static constexpr int kPer = NT == 32 ? 8 : 4, kRoom = kPer * NT;
+  uint32_t group[64];
+  unsigned long long cand[kRoom], list[kTlMaxTop], best[NT / 32];
+  int n, left, warp[NT / 32];
 };
 
-// The k-th largest (k = 1..32) of the warp's values.
-__device__ __forceinline__ uint32_t tl_kth(uint32_t v, int k) {
+constexpr uint32_t kTlOrderNone = 0x007FFFFFu;  // tl_order(-inf)
+
+// The warp's values in descending order.
+__device__ __forceinline__ uint32_t tl_sort(uint32_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int size = 2; size <= 32; size *= 2)
@@ -333,72 +401,83 @@ __device__ __forceinline__ uint32_t tl_kth(uint32_t v, int k) {
       const bool down = (lane & size) == 0 || size == 32, low = (lane & o) == 0;
       v = (low == down) ? max(u, v) : min(u, v);
     }
+  return v;
+}
+
+// The k-th largest (k = 1..32) of 64 values.
+__device__ __forceinline__ uint32_t tl_kth(const uint32_t* g, int k) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t x = tl_sort(g[lane]), y = tl_sort(g[lane + 32]);
+  uint32_t v = max(x, __shfl_sync(0xFFFFFFFFu, y, 31 - lane));  // the 32 largest, rising then falling
+#pragma unroll
+  for (int o = 16; o; o /= 2) {
+    const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = (lane & o) == 0 ? max(u, v) : min(u, v);
+  }
   return __shfl_sync(0xFFFFFFFFu, v, k - 1);
 }
 
-// Merges the tile's largest into to.list (sorted, 0 where there are fewer). The
-// thread's elements: its words, and the single one of value xs where `single` is
-// not -1; `mine`: the order of the largest (0: none). Ends without a barrier:
-// to.list may be read after the next one.
+template <int NT>
+__device__ __forceinline__ void tl_put(TlTop<NT>& to, uint32_t order, int i) {
+  const int at = atomicAdd(&to.n, 1);
+  if (at < TlTop<NT>::kRoom) to.cand[at] = tl_key(order, i);
+}
+
+// to.list: the largest of the n candidates. Needs a barrier before and after.
+template <int NT>
+__device__ __forceinline__ void tl_rank(TlTop<NT>& to, int n, int top) {
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const unsigned long long k = to.cand[i];
+    int rank = 0;
+    for (int x = 0; x < n; ++x) rank += to.cand[x] > k;
+    if (rank < top) to.list[rank] = k;
+  }
+}
+
+// The same from the row itself, words [w0, w0 + wn) and the threads' single
+// elements (`single` -1: none): the candidates above `bound`, of which at least
+// `top` reach it, and the first of those equal to it.
 template <typename T, int NT>
-__device__ void tl_tile_top(TlTop<NT>& to, int top, bool first, const uint4* tile, int w0, int wn, const TlRow<T>& row,
-                            int single, float xs, uint32_t mine) {
+__device__ __noinline__ int tl_top_again(TlTop<NT>& to, int top, const TlRow<T> row, int w0, int wn, int single, float xs,
+                                         uint32_t bound) {
   constexpr int N = TlWord<T>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  to.group[tid] = mine;
+  const uint4* words = reinterpret_cast<const uint4*>(row.p + row.head) + w0;
+  const int first = row.head + w0 * N;
+  __syncthreads();
   if (tid == 0) to.n = 0;
   __syncthreads();
-  uint32_t g = 0;
+  for (int i = tid; i < wn; i += NT) {
+    const TlWord<T> w{words[i]};
+    if (tl_order(tl_word_max(w)) > bound) {
+      float v[N];
+      w.to(v);
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) g = max(g, to.group[w * 32 + lane]);
-  uint32_t bound = tl_kth(g, top);
-  const unsigned long long last = first ? 0ull : to.list[top - 1];
-  const bool full = last != 0 && (uint32_t)(last >> 32) >= bound;  // (equals of a later tile come after those)
-  if (full) bound = (uint32_t)(last >> 32);
-  // words of the thread, in order: f(word's place in the tile, first index)
-  auto words = [&](auto f) {
-#pragma unroll 1
-    for (int u = 0; u < kTlWords; ++u) {
-      const int i = u * NT + tid;
-      if (i < wn) f(i, row.head + (w0 + i) * N);
+      for (int x = 0; x < N; ++x)
+        if (tl_order(v[x]) > bound) tl_put(to, tl_order(v[x]), first + i * N + x);
     }
-  };
-  auto put = [&](uint32_t o, int i) {
-    const int at = atomicAdd(&to.n, 1);
-    if (at < kTlCandidates) to.cand[at] = tl_key(o, i);
-  };
-  if (mine > bound) {
-    words([&](int i, int at) {
-      TlWord<T> w{tile[i]};
-      if (tl_order(tl_word_max(w)) > bound) {
-        const T* e = reinterpret_cast<const T*>(&tile[i]);
-#pragma unroll 1
-        for (int x = 0; x < N; ++x) {
-          const uint32_t o = tl_order(to_f32(e[x]));
-          if (o > bound) put(o, at + x);
-        }
-      }
-    });
-    if (single >= 0 && tl_order(xs) > bound) put(tl_order(xs), single);
   }
+  if (single >= 0 && tl_order(xs) > bound) tl_put(to, tl_order(xs), single);
   __syncthreads();
   int n = to.n;
-  if (n > kTlCandidates - kTlMaxTop) {
+  if (n > TlTop<NT>::kRoom - top) {
     // more than there is room for: the largest key below the last one, `top` times
     unsigned long long below = ~0ull;
-    __syncthreads();
     for (n = 0; n < top; ++n) {
       unsigned long long best = 0;
-      auto look = [&](uint32_t o, int i) {
-        const unsigned long long k = tl_key(o, i);
+      auto look = [&](float v, int i) {
+        const unsigned long long k = tl_key(tl_order(v), i);
         if (k < below && k > best) best = k;
       };
-      words([&](int i, int at) {
-        const T* e = reinterpret_cast<const T*>(&tile[i]);
-#pragma unroll 1
-        for (int x = 0; x < N; ++x) look(tl_order(to_f32(e[x])), at + x);
-      });
-      if (single >= 0) look(tl_order(xs), single);
+      for (int i = tid; i < wn; i += NT) {
+        const TlWord<T> w{words[i]};
+        if (tl_order(tl_word_max(w)) < (uint32_t)(best >> 32)) continue;
+        float v[N];
+        w.to(v);
+#pragma unroll
+        for (int x = 0; x < N; ++x) look(v[x], first + i * N + x);
+      }
+      if (single >= 0) look(xs, single);
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         const unsigned long long b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -411,20 +490,22 @@ __device__ void tl_tile_top(TlTop<NT>& to, int top, bool first, const uint4* til
       if (tid == 0) to.cand[n] = best;
       below = best;
     }
-    __syncthreads();
-  } else if (n < top && !full && bound != 0) {
-    // the first of the elements equal to the bound: the head's, the words' row by row, the tail's
+  } else {
+    // the first of the elements equal to the bound: the head's, the words' in order, the tail's
     int need = top - n;
-    for (int u = -1; u <= kTlWords && need > 0; ++u) {
+    const int rounds = (wn + NT - 1) / NT;
+    for (int u = -1; u <= rounds && need > 0; ++u) {
       uint32_t same = 0;  // bits of the thread's elements
       int at = 0;
-      if (u < 0 || u == kTlWords) {
+      if (u < 0 || u == rounds) {
         if (single >= 0 && (u < 0) == (tid < 16) && tl_order(xs) == bound) same = 1, at = single;
       } else if (u * NT + tid < wn) {
-        at = row.head + (w0 + u * NT + tid) * N;
-        const T* e = reinterpret_cast<const T*>(&tile[u * NT + tid]);
+        at = first + (u * NT + tid) * N;
+        const TlWord<T> w{words[u * NT + tid]};
+        float v[N];
+        w.to(v);
 #pragma unroll
-        for (int x = 0; x < N; ++x) same |= (uint32_t)(tl_order(to_f32(e[x])) == bound) << x;
+        for (int x = 0; x < N; ++x) same |= (uint32_t)(tl_order(v[x]) == bound) << x;
       }
       int incl = __popc(same);
 #pragma unroll
@@ -449,22 +530,38 @@ __device__ void tl_tile_top(TlTop<NT>& to, int top, bool first, const uint4* til
       __syncthreads();
     }
   }
-  // the earlier tiles' list, then ranks
-  if (!first) {
-    if (tid < top && to.list[tid]) to.cand[n + tid] = to.list[tid];
-    int have = 0;
-    for (int i = 0; i < top; ++i) have += to.list[i] != 0;
-    n += have;
-    __syncthreads();
-  }
-  if (tid < top) to.list[tid] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += NT) {
-    const unsigned long long k = to.cand[i];
-    int rank = 0;
-    for (int x = 0; x < n; ++x) rank += to.cand[x] > k;
-    if (rank < top) to.list[rank] = k;
+  return n;
+}
+
+// At the end of a row (of the CTA's words of it): to.list. Leaves `to` as the
+// next row needs it. Needs a barrier after it.
+template <typename T, int NT>
+__device__ __forceinline__ void tl_top_finish(TlTop<NT>& to, int top, const TlRow<T>& row, int w0, int wn, int single, float xs) {
+  constexpr int kPer = TlTop<NT>::kPer;
+  const int tid = threadIdx.x;
+  __syncthreads();
+  const int n = to.n;
+  const uint32_t bound = tl_kth(to.group, top);
+  unsigned long long k[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) k[j] = tid + j * NT < n ? to.cand[tid + j * NT] : 0ull;
+  if (tid == 0) to.left = 0;
+  __syncthreads();
+  if (tid == 0) to.n = 0;
+  for (int i = tid; i < 64; i += NT) to.group[i] = 0;
+  int left = 0;
+  if (n <= TlTop<NT>::kRoom) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (k[j] != 0 && (uint32_t)(k[j] >> 32) >= bound) to.cand[atomicAdd(&to.left, 1)] = k[j];
+    __syncthreads();
+    left = to.left;
   }
+  if (n > TlTop<NT>::kRoom || left < top) left = tl_top_again<T, NT>(to, top, row, w0, wn, single, xs, bound);
+  tl_rank(to, left, top);
+  // (tl_top_again has counted in to.n)
+  if (tid == 0) to.n = 0;
 }
 
 __device__ __forceinline__ uint32_t tl_map(const void* p, int rank) {
@@ -472,8 +569,18 @@ __device__ __forceinline__ uint32_t tl_map(const void* p, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return at;
 }
+__device__ __forceinline__ void tl_push(void* p, int rank, const TlPart& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(tl_map(p, rank)), "f"(v.m), "f"(v.s), "f"(v.d), "f"(0.0f)
+               : "memory");
+}
+template <bool CLUSTER>
 __device__ __forceinline__ void tl_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  if (CLUSTER) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  } else {
+    __syncthreads();
+  }
 }
 
 // (with their order among the reads of shared memory)
@@ -486,20 +593,80 @@ __device__ __forceinline__ void tl_copy_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-enum { kTlLogprobs = 0, kTlDistill = 1, kTlDistillGrad = 2 };
+// Takes W words (of which the thread has those below n, NT apart) and a single
+// element (-inf: none) into a thread's part; returns their maximum.
+template <typename T, int NT, int W, bool ENTROPY>
+__device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, float single, float c) {
+  constexpr int N = TlWord<T>::kN;
+  TlWord<T> w[W];
+  float m = single;
+#pragma unroll
+  for (int u = 0; u < W; ++u)
+    if (u * NT + (int)threadIdx.x < n) {
+      w[u].q = tile[u * NT + threadIdx.x];
+      m = tl_max_nan(m, tl_word_max(w[u]));
+    }
+  const float top = tl_max_nan(p.m, m);
+  if (!(top == p.m)) p.raise(top, c);
+  const TlRef r(p.m, c);
+  float s = p.s, dot = p.d;
+  auto add = [&](float d) {
+    if (ENTROPY) d = fmaxf(d, -1000.0f);  // (0 times infinity)
+    const float e = tl_ex2(d);
+    s += e;
+    if (ENTROPY) dot = fmaf(e, d, dot);
+  };
+  auto all = [&](auto arg) {
+#pragma unroll
+    for (int u = 0; u < W; ++u)
+      if (u * NT + (int)threadIdx.x < n) {
+        float v[N];
+        w[u].to(v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) add(arg(v[i]));
+      }
+  };
+  if (!r.far)
+    all([&](float x) { return fmaf(x, r.c, -r.w); });
+  else
+    all([&](float x) { return r.arg(x); });
+  if (single != -INFINITY) add(r.arg(single));
+  p.s = s, p.d = dot;
+  return m;
+}
 
-template <typename T, int NT, int MODE>
-__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 10) k_tl_rows(const TlArgs a) {
+// The warps' parts of a row, by a warp: the same bits for every warp that merges them.
+__device__ __forceinline__ TlPart tl_merge_parts(const float4* parts, int n, float c) {
+  TlPart p{-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const float4 v = parts[i];
+    TlPart x{v.x, v.y, v.z};
+    const float top = tl_max_nan(p.m, x.m);
+    if (!(top == p.m)) p.raise(top, c);
+    if (!(top == x.m)) x.raise(top, c);
+    p.s += x.s, p.d += x.d;
+  }
+  return tl_warp_merge(p, c);
+}
+
+// ------------------------------------------------------------------- forward
+// CLUSTER: a row for each cluster; else a row for each CTA, and the next after it.
+template <typename T, int NT, int EPT, bool CLUSTER, bool LOGPROBS>
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_forward(const TlArgs a) {
   constexpr int N = TlWord<T>::kN, W = kTlWords, TW = NT * W, NW = NT / 32;
-  constexpr bool kEntropy = MODE == kTlLogprobs, kGrad = MODE == kTlDistillGrad;
   extern __shared__ uint4 tl_buf[];  // two tiles
-  __shared__ __align__(16) float4 s_part[2][kTlCtas * NW];
-  __shared__ unsigned long long s_lists[MODE == kTlLogprobs ? 2 * kTlCtas * kTlMaxTop : 1];
-  __shared__ typename std::conditional<MODE == kTlLogprobs, TlTop<NT>, TlTeacher>::type sh;
+  __shared__ __align__(16) float4 s_part[2][CLUSTER ? kTlCtas * NW : NW];
+  __shared__ unsigned long long s_lists[LOGPROBS && CLUSTER ? kTlCtas * kTlMaxTop : 1];
+  __shared__ typename std::conditional<LOGPROBS, TlTop<NT>, TlTeacherWarps>::type sh[LOGPROBS ? 1 : 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = a.ctas == 1 ? 0 : (int)(blockIdx.x % a.ctas);
-  const long step = gridDim.x / a.ctas;
+  const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)(blockIdx.x % a.ctas) : 0;
+  const long step = gridDim.x / ctas;
   const float c = a.inv_tau * kLog2e;
+  if constexpr (LOGPROBS) {
+    for (int i = tid; i < 64; i += NT) sh[0].group[i] = 0;
+    if (tid == 0) sh[0].n = 0;
+    __syncthreads();
+  }
   grid_wait();
   grid_launch();
 
@@ -508,8 +675,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 10) k_tl_rows(const TlArgs
     w0 = rank * a.seg + p * TW;
     return max(0, min(min(row.words, (rank + 1) * a.seg) - w0, TW));
   };
+  auto masked = [&](long t) { return !LOGPROBS && a.mask && !a.mask[t]; };
   auto fetch = [&](long t, int p, int buf) {
-    if (t < a.T && !(MODE != kTlLogprobs && a.mask && !a.mask[t])) {
+    if (t < a.T && !masked(t)) {
       const TlRow<T> row(a.logits, a.ld, t, a.V);
       int w0;
       const int n = tile_words(row, p, w0);
@@ -521,71 +689,53 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 10) k_tl_rows(const TlArgs
     tl_copy_commit();
   };
   // what a row needs besides, one row ahead
-  TlEntry entry;
+  TlEntry entry[EPT];
   long y = 0;
   float xs = 0.0f;
   auto ahead = [&](long t) {
-    if (t >= a.T) return;
-    if constexpr (MODE == kTlLogprobs)
+    if (t >= a.T || masked(t)) return;
+    if constexpr (LOGPROBS)
       y = tl_index(a.targets, a.target64, t);
     else
-      tl_entry_load(a, t, entry);
+      tl_entry_load<NT>(a, t, entry);
     const TlRow<T> row(a.logits, a.ld, t, a.V);
     const int i = row.single(rank, a.V);
     xs = i >= 0 ? to_f32(row.p[i]) : -INFINITY;
   };
 
-  const int steps = a.tiles * (kGrad && a.tiles > 1 ? 2 : 1);  // tiles of a row that go through the buffers
-  long t = blockIdx.x / a.ctas;
+  long t = blockIdx.x / ctas;
   int buf = 0, parity = 0;
   fetch(t, 0, 0);
   ahead(t);
   for (; t < a.T; t += step) {
-    const bool masked = MODE != kTlLogprobs && a.mask && !a.mask[t];
+    if (masked(t)) {  // (the same for the cluster)
+      fetch(t + step, 0, buf ^= 1);
+      ahead(t + step);
+      if (rank == 0 && tid == 0) a.loss[t] = 0.0f;
+      if (rank == 0 && tid < kTlStats) a.stats[t * kTlStats + tid] = 0.0f;
+      continue;
+    }
     const TlRow<T> row(a.logits, a.ld, t, a.V);
     const int single = row.single(rank, a.V);
     const float x1 = xs;
-    const TlEntry e0 = entry;
     const long target = y;
-    T* out = kGrad ? static_cast<T*>(a.grad) + t * a.grad_ld : nullptr;
-    if (masked) {  // (the same for the cluster)
-      fetch(t + step, 0, buf ^ 1);
-      ahead(t + step);
-      buf ^= 1;
-      if (kGrad) {
-        TlWord<T> z;
-        z.q = make_uint4(0, 0, 0, 0);
-        for (int p = 0; p < a.tiles; ++p) {
-          int w0;
-          const int n = tile_words(row, p, w0);
-          for (int i = tid; i < n; i += NT) {
-            T* o = out + row.head + (size_t)(w0 + i) * N;
-            if (a.vec_out)
-              *reinterpret_cast<uint4*>(o) = z.q;
-            else
-              for (int x = 0; x < N; ++x) o[x] = from_f32<T>(0.0f);
-          }
-        }
-        if (single >= 0) out[single] = from_f32<T>(0.0f);
-      }
-      if (rank == 0 && tid == 0) {
-        a.loss[t] = 0.0f;
-        if (a.stats) a.stats[2 * t] = a.stats[2 * t + 1] = 0.0f;
-      }
-      continue;
-    }
-    TlEntry e = e0;
+    TlEntry e[EPT];
     float xy = 0.0f;
-    if constexpr (MODE == kTlLogprobs) {
+    if constexpr (LOGPROBS) {
       if (rank == 0 && tid == 0 && target >= 0 && target < a.V) xy = to_f32(row.p[target]);
     } else {
-      tl_entry_start(row, tl_mine(row, rank, rank * a.seg, (rank + 1) * a.seg, e.id, a.V), rank == 0, c, sh, e);
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        e[j] = entry[j];
+        if (rank == 0 && e[j].id >= 0) e[j].x = to_f32(row.p[e[j].id]);
+      }
+      tl_teacher_part<NT>(e, c, sh[parity]);
     }
     TlPart part{-INFINITY, 0.0f, 0.0f};
-    const int held = buf;  // (the row's only tile stays there)
+    uint32_t most = 0, bound = 0;
     for (int p = 0; p < a.tiles; ++p) {
-      if (p + 1 < steps)
-        fetch(t, (p + 1) % a.tiles, buf ^ 1);
+      if (p + 1 < a.tiles)
+        fetch(t, p + 1, buf ^ 1);
       else
         fetch(t + step, 0, buf ^ 1);
       tl_copy_wait<1>();
@@ -593,177 +743,240 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 10) k_tl_rows(const TlArgs
       const int n = tile_words(row, p, w0);
       const uint4* tile = tl_buf + buf * TW;
       buf ^= 1;
-      TlWord<T> w[W];
-      // (the head's single elements go with the first tile, the tail's with the last: tiles are in the row's order)
-      const bool here = single >= 0 && p == (tid < 16 ? 0 : a.tiles - 1);
-      const float xh = here ? x1 : -INFINITY;
-      float m = xh;
-#pragma unroll
-      for (int u = 0; u < W; ++u)
-        if (u * NT + tid < n) {
-          w[u].q = tile[u * NT + tid];
-          m = tl_max_nan(m, tl_word_max(w[u]));
-        }
-      const float wm = tl_warp_max(m);
-      const TlShift shift(wm == -INFINITY ? 0.0f : wm, c);
-      float s = 0.0f, dot = 0.0f;
-      auto sums = [&](auto far) {
-        auto add = [&](float x) {
-          float d = shift.arg<decltype(far)::value>(x);
-          if (kEntropy) d = fmaxf(d, -1000.0f);
-          const float v = tl_ex2(d);
-          s += v;
-          if (kEntropy) dot = fmaf(v, d, dot);
-        };
-#pragma unroll
-        for (int u = 0; u < W; ++u)
-          if (u * NT + tid < n) {
-            float v[N];
-            w[u].to(v);
-#pragma unroll
-            for (int i = 0; i < N; ++i) add(v[i]);
+      const bool here = single >= 0 && p == 0;
+      const float m = tl_take<T, NT, W, LOGPROBS>(part, tile, n, here ? x1 : -INFINITY, c);
+      if constexpr (LOGPROBS) {
+        if (a.top) {
+          TlTop<NT>& to = sh[0];
+          const uint32_t o = tid < n || here ? tl_order(m) : 0u;
+          if (o > most) atomicMax(&to.group[tid & 63], most = o);
+          if (p == 0) __syncthreads();
+          // (later, whatever the other warps have found so far: any bound of this row's will do)
+          if ((p & (p - 1)) == 0) bound = tl_kth(to.group, a.top);
+          const uint32_t least = max(bound, kTlOrderNone + 1);
+          if (o >= least) {
+#pragma unroll 1
+            for (int u = 0; u * NT + tid < n; ++u) {
+              const TlWord<T> w{tile[u * NT + tid]};
+              if (tl_order(tl_word_max(w)) < least) continue;
+              const T* v = reinterpret_cast<const T*>(&tile[u * NT + tid]);
+#pragma unroll 1
+              for (int x = 0; x < N; ++x) {
+                const uint32_t k = tl_order(to_f32(v[x]));
+                if (k >= least) tl_put(to, k, row.head + (w0 + u * NT + tid) * N + x);
+              }
+            }
+            if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
           }
-        add(xh);
-      };
-      if (shift.far)
-        sums(std::true_type());
-      else
-        sums(std::false_type());
-      // relative to the exact maximum
-      if (kEntropy) dot -= shift.r * s;
-      const float back = tl_ex2(-shift.r);
-      tl_merge(part, wm, c, tl_warp_sum(s) * back, kEntropy ? tl_warp_sum(dot) * back : 0.0f);
-      if constexpr (MODE == kTlLogprobs) {
-        if (a.top)
-          tl_tile_top<T, NT>(sh, a.top, p == 0, tile, w0, n, row, here ? single : -1, xh,
-                             tid < n || here ? tl_order(m) : 0u);
+          __syncwarp();
+        }
       }
     }
     ahead(t + step);
-    // every warp's part goes to all CTAs of the row
-    __syncwarp();
-    if (lane < a.ctas) {
-      const uint32_t to = tl_map(&s_part[parity][rank * NW + warp], lane);
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "f"(part.m), "f"(part.s), "f"(part.d),
-                   "f"(0.0f) : "memory");
+    part = tl_warp_merge(part, c);
+    if (lane == 0) {
+      if (CLUSTER)
+        tl_push(&s_part[parity][rank * NW + warp], 0, part);
+      else
+        s_part[parity][warp] = make_float4(part.m, part.s, part.d, 0.0f);
     }
-    if constexpr (MODE == kTlLogprobs) {
+    if constexpr (LOGPROBS) {
       if (a.top) {
-        __syncthreads();
-        if (tid < a.top) {
-          const uint32_t to = tl_map(&s_lists[(parity * kTlCtas + rank) * a.top + tid], 0);
-          asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(to), "l"(sh.list[tid]) : "memory");
+        const int w0 = rank * a.seg, wn = max(0, min(row.words, w0 + a.seg) - w0);
+        tl_top_finish<T, NT>(sh[0], a.top, row, w0, wn, single, x1);
+        if (CLUSTER) {
+          __syncthreads();
+          if (tid < a.top)
+            asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(tl_map(&s_lists[rank * a.top + tid], 0)), "l"(sh[0].list[tid])
+                         : "memory");
         }
       }
     }
-    __syncwarp();
-    tl_meet();
-    TlPart all{-INFINITY, 0.0f, 0.0f};
-    if (kGrad || rank == 0) {
-      // (the same order for every warp of every CTA: lanes, then the tree)
-      for (int i = lane; i < a.ctas * NW; i += 32) {
-        const float4 v = s_part[parity][i];
-        tl_merge(all, v.x, c, v.y, v.z);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float m = __shfl_xor_sync(0xFFFFFFFFu, all.m, o), s = __shfl_xor_sync(0xFFFFFFFFu, all.s, o);
-        const float d = __shfl_xor_sync(0xFFFFFFFFu, all.d, o);
-        const bool low = (lane & o) == 0;  // (both lanes of a pair add in the same order)
-        TlPart x{low ? all.m : m, low ? all.s : s, low ? all.d : d};
-        tl_merge(x, low ? m : all.m, c, low ? s : all.s, low ? d : all.d);
-        all = x;
-      }
-    }
-    const bool none = all.m == -INFINITY;
-    const float M = none ? 0.0f : all.m;
-    const float lns = none ? -INFINITY : (all.m != all.m || all.m == INFINITY ? NAN : logf(all.s));
-    auto logp = [&](float x) { return none ? -INFINITY : (x - M) * a.inv_tau - lns; };
-    if constexpr (MODE == kTlLogprobs) {
-      if (rank == 0 && tid == 0) {
-        a.logprob[t] = target >= 0 && target < a.V ? logp(xy) : 0.0f;
-        a.entropy[t] = none ? 0.0f : lns - all.d * kLn2 / all.s;
-        a.stats[2 * t] = M;
-        a.stats[2 * t + 1] = lns;
-      }
-      if (a.top && rank == 0) {
-        const unsigned long long* l = s_lists + parity * kTlCtas * a.top;
-        const int n = a.ctas * a.top;
-        for (int i = tid; i < n; i += NT) {
-          const unsigned long long k = l[i];
-          int r = k ? 0 : kTlMaxTop;
-          for (int x = 0; x < n; ++x) r += l[x] > k;
-          if (r < a.top) {
-            a.top_ids[t * a.top + r] = (int)~(uint32_t)k;
-            a.top_logprobs[t * a.top + r] = logp(tl_value_of((uint32_t)(k >> 32)));
-          }
-        }
-      }
-    } else {
-      float q, lnq;
-      const float Q = tl_entry_share(a, t, NW, c, sh, e, q, lnq);
-      if (rank == 0) {
-        const float term = tl_warp_sum(e.id >= 0 && !(q == 0.0f) ? q * (lnq - logp(e.x)) : 0.0f);
-        if (lane == 0) sh.loss[warp] = term;
-      }
-      const float g = kGrad ? a.grad_loss[t] * a.inv_tau : 0.0f;
-      const TlShift shift(M, c);
-      const float unit = none ? 0.0f : expf(-lns) * tl_ex2(-shift.r);  // p = 2^d unit
-      if (kGrad) {
-        const float A = g * Q * unit;
-        for (int p = 0; p < a.tiles; ++p) {
-          int at = held;
-          if (a.tiles > 1) {
-            if (p + 1 < a.tiles)
-              fetch(t, p + 1, buf ^ 1);
-            else
-              fetch(t + step, 0, buf ^ 1);
-            tl_copy_wait<1>();
-            at = buf;
-            buf ^= 1;
-          }
-          int w0;
-          const int n = tile_words(row, p, w0);
-#pragma unroll
-          for (int u = 0; u < W; ++u)
-            if (u * NT + tid < n) {
-              TlWord<T> w{tl_buf[at * TW + u * NT + tid]};
-              tl_grad_word<T, false>(w, out + row.head + (size_t)(w0 + u * NT + tid) * N, a.vec_out, shift, A, 0.0f);
-            }
-        }
-        if (single >= 0) out[single] = from_f32<T>(tl_grad_value<T, false>(x1, shift, A, 0.0f));
-      }
-      int count = 0;  // (read here: after the barrier a warp may already be at the next row's)
-      for (int w = 0; w < NW; ++w) count += w * 32 < a.n ? sh.count[w] : 0;
-      __syncthreads();
-      if (kGrad) {
-        auto prob = [&](float x) { return unit * tl_ex2(shift.far ? shift.arg<true>(x) : shift.arg<false>(x)); };
-        tl_entry_grad<T>(sh, count, g, Q, out, prob);
-      }
-      if (rank == 0 && tid == 0) {
-        float loss = 0.0f;
-        for (int w = 0; w < NW; ++w) loss += w * 32 < a.n ? sh.loss[w] : 0.0f;
-        a.loss[t] = loss;
-        if (a.stats) {
+    tl_meet<CLUSTER>();
+    if (rank == 0) {
+      const TlPart all = tl_merge_parts(s_part[parity], ctas * NW, c);
+      const bool none = all.m == -INFINITY;
+      const float M = none ? 0.0f : all.m, lns = tl_log_sum(all, c);
+      auto logp = [&](float x) { return none ? -INFINITY : (x - M) * a.inv_tau - lns; };
+      if constexpr (LOGPROBS) {
+        if (tid == 0) {
+          a.logprob[t] = target >= 0 && target < a.V ? logp(xy) : 0.0f;
+          // H = s - sum p u', u' = (d - (M c - w)) ln 2
+          a.entropy[t] = none ? 0.0f : lns - (all.d / all.s - TlRef(M, c).above()) * kLn2;
           a.stats[2 * t] = M;
           a.stats[2 * t + 1] = lns;
+        }
+        if (a.top) {
+          auto store = [&](int r, unsigned long long k) {
+            a.top_ids[t * a.top + r] = (int)~(uint32_t)k;
+            a.top_logprobs[t * a.top + r] = logp(tl_value_of((uint32_t)(k >> 32)));
+          };
+          if (CLUSTER) {
+            const int n = ctas * a.top;
+            for (int i = tid; i < n; i += NT) {
+              const unsigned long long k = s_lists[i];
+              int r = 0;
+              for (int x = 0; x < n; ++x) r += s_lists[x] > k;
+              if (r < a.top) store(r, k);
+            }
+          } else if (tid < a.top) {
+            store(tid, sh[0].list[tid]);
+          }
+        }
+      } else {
+        const TlTeacherSum k = tl_teacher_sum<NT>(a, t, c, sh[parity]);
+        float term = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+          const float lnq = tl_ln_q(e[j], k, a.inv_tau), q = expf(lnq);
+          if (e[j].id >= 0 && !(q == 0.0f)) term += q * (lnq - logp(e[j].x));
+        }
+        term = tl_warp_sum(term);
+        if (lane == 0) sh[parity].loss[warp] = term;
+        __syncthreads();
+        if (tid == 0) {
+          float loss = 0.0f;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) loss += sh[parity].loss[w];
+          a.loss[t] = loss;
+          float* st = a.stats + t * kTlStats;
+          st[0] = M, st[1] = lns, st[2] = k.m, st[3] = k.s, st[4] = k.Q;
         }
       }
     }
     parity ^= 1;
   }
   tl_copy_wait<0>();
-  __syncwarp();
-  tl_meet();  // no CTA leaves while another may still write to it
+}
+
+// ------------------------------------------------------------------- one pass
+template <typename T, int NT, int W, int EPT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_once(const TlArgs a) {
+  constexpr int N = TlWord<T>::kN, TW = NT * W, NW = NT / 32, kPart = 8;  // words of a thread taken at once
+  extern __shared__ uint4 tl_buf[];  // one tile
+  __shared__ __align__(16) float4 s_part[kTlCtas * NW];
+  __shared__ TlTeacher te;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % a.ctas);
+  const long t = blockIdx.x / a.ctas;
+  const float c = a.inv_tau * kLog2e;
+  grid_wait();
+  grid_launch();
+  const TlRow<T> row(a.logits, a.ld, t, a.V);
+  const int single = row.single(rank, a.V);
+  T* out = static_cast<T*>(a.grad) + t * a.grad_ld;
+  auto tile_words = [&](int p, int& w0) {
+    w0 = rank * a.seg + p * TW;
+    return max(0, min(min(row.words, (rank + 1) * a.seg) - w0, TW));
+  };
+  if (a.mask && !a.mask[t]) {  // (the same for the cluster)
+    for (int p = 0; p < a.tiles; ++p) {
+      int w0;
+      const int n = tile_words(p, w0);
+      for (int i = tid; i < n; i += NT) {
+        T* o = out + row.head + (size_t)(w0 + i) * N;
+        if (a.vec_out)
+          *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
+        else
+          for (int x = 0; x < N; ++x) o[x] = from_f32<T>(0.0f);
+      }
+    }
+    if (single >= 0) out[single] = from_f32<T>(0.0f);
+    if (rank == 0 && tid == 0) a.loss[t] = 0.0f;
+    return;
+  }
+  auto fetch = [&](int p) {
+    int w0;
+    const int n = tile_words(p, w0);
+    const T* src = row.p + row.head + (size_t)(w0 + tid) * N;
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      if (u * NT + tid < n) tl_copy16(tl_buf + u * NT + tid, src + (size_t)u * NT * N);
+      if (u % kPart == kPart - 1) tl_copy_commit();
+    }
+    return n;
+  };
+  int n = fetch(0);
+  TlEntry e[EPT];
+  tl_entry_load<NT>(a, t, e);
+  const float x1 = single >= 0 ? to_f32(row.p[single]) : -INFINITY;
+  const float grad_loss = a.grad_loss[t];
+  bool mine[EPT];
+  uint32_t lanes[EPT];
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    mine[j] = tl_mine(row, rank, rank * a.seg, (rank + 1) * a.seg, e[j].id, a.V);
+    if (mine[j] || (rank == 0 && e[j].id >= 0)) e[j].x = to_f32(row.p[e[j].id]);
+  }
+  tl_entry_count(mine, te, lanes);
+  tl_teacher_part<NT>(e, c, te);
+  TlPart part{-INFINITY, 0.0f, 0.0f};
+  for (int p = 0; p < a.tiles; ++p) {
+    if (p) n = fetch(p);
+    const float xh = p == 0 ? x1 : -INFINITY;
+    static_assert(W == kPart || W == 2 * kPart, "one or two parts");
+    if (W == 2 * kPart) {
+      tl_copy_wait<1>();
+      tl_take<T, NT, kPart, false>(part, tl_buf, n, xh, c);
+    }
+    tl_copy_wait<0>();
+    constexpr int kLast = W - kPart;
+    tl_take<T, NT, kPart, false>(part, tl_buf + kLast * NT, n - kLast * NT, kLast ? -INFINITY : xh, c);
+  }
+  part = tl_warp_merge(part, c);
+  if (lane < a.ctas) tl_push(&s_part[rank * NW + warp], lane, part);
+  if (a.ctas > 1)
+    tl_meet<true>();
+  else
+    tl_meet<false>();
+  const TlPart all = tl_merge_parts(s_part, a.ctas * NW, c);
+  const bool none = all.m == -INFINITY;
+  const float M = none ? 0.0f : all.m, lns = tl_log_sum(all, c);
+  const TlTeacherSum k = tl_teacher_sum<NT>(a, t, c, te);
+  const int count = tl_entry_share<NT>(e, mine, lanes, k, a.inv_tau, te);
+  if (rank == 0) {
+    float term = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const float lnq = tl_ln_q(e[j], k, a.inv_tau), q = expf(lnq);
+      if (e[j].id >= 0 && !(q == 0.0f)) term += q * (lnq - (none ? -INFINITY : (e[j].x - M) * a.inv_tau - lns));
+    }
+    term = tl_warp_sum(term);
+    if (lane == 0) te.loss[warp] = term;
+  }
+  const float g = grad_loss * a.inv_tau;
+  const TlRef ref(M, c);
+  const float unit = tl_unit(ref, lns), A = g * k.Q * unit;
+  for (int p = a.tiles - 1; p >= 0; --p) {  // (the last tile is still here)
+    if (p < a.tiles - 1) {
+      fetch(p);
+      tl_copy_wait<0>();
+    }
+    int w0;
+    const int m = tile_words(p, w0);
+#pragma unroll 8
+    for (int u = 0; u < W; ++u)
+      if (u * NT + tid < m)
+        tl_grad_word<T, false>(TlWord<T>{tl_buf[u * NT + tid]}, out + row.head + (size_t)(w0 + u * NT + tid) * N, a.vec_out, ref, A, 0.0f);
+  }
+  if (single >= 0) out[single] = from_f32<T>(tl_grad_value<false>(x1, ref, A, 0.0f));
+  __syncthreads();
+  tl_entry_grad<NT>(te, count, g, k.Q, out, [&](float x) { return unit * tl_ex2(ref.arg(x)); });
+  if (rank == 0 && tid == 0) {
+    float loss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) loss += te.loss[w];
+    a.loss[t] = loss;
+  }
 }
 
 // ------------------------------------------------------------------ backward
 // One CTA for each NT * 8 words of a row.
-template <typename T, int NT, bool ENTROPY, bool TEACHER>
-__global__ void __launch_bounds__(NT) k_tl_backward(const TlArgs a) {
-  constexpr int N = TlWord<T>::kN, W = kTlWords, NW = NT / 32;
+template <typename T, int NT, int EPT, bool ENTROPY, bool TEACHER>
+__global__ void __launch_bounds__(NT, NT == 256 ? 4 : 16) k_tl_backward(const TlArgs a) {
+  constexpr int N = TlWord<T>::kN, W = kTlWords;
   __shared__ typename std::conditional<TEACHER, TlTeacher, int>::type sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int rank = (int)(blockIdx.x % a.ctas);
   const long t = blockIdx.x / a.ctas;
   const float c = a.inv_tau * kLog2e;
@@ -780,103 +993,143 @@ __global__ void __launch_bounds__(NT) k_tl_backward(const TlArgs a) {
     if (u * NT + tid < n && !masked)
       w[u].q = *reinterpret_cast<const uint4*>(row.p + row.head + (size_t)(w0 + u * NT + tid) * N);
   const float x1 = single >= 0 && !masked ? to_f32(row.p[single]) : 0.0f;
-  const float lns = masked ? 0.0f : a.stats[2 * t + 1];
-  const TlShift shift(masked ? 0.0f : a.stats[2 * t], c);
-  const float unit = masked || lns == -INFINITY ? 0.0f : expf(-lns) * tl_ex2(-shift.r);  // p = 2^d unit
-  auto prob = [&](float x) { return unit * tl_ex2(shift.far ? shift.arg<true>(x) : shift.arg<false>(x)); };
   auto mine = [&](int i) { return tl_mine(row, rank, w0, w0 + NT * W, i, a.V); };
-  float A = 0.0f, B = 0.0f, g, Q = 0.0f, xy = 0.0f;
+  const float* st = a.stats + t * (TEACHER ? kTlStats : 2);
+  const float lns = masked ? 0.0f : st[1];
+  const TlRef ref(masked ? 0.0f : st[0], c);
+  const float unit = masked ? 0.0f : tl_unit(ref, lns);
+  float A = 0.0f, B = 0.0f, g = 0.0f, Q = 0.0f, xy = 0.0f;
   long y = -1;
+  int count = 0;
   if constexpr (TEACHER) {
+    TlEntry e[EPT];
+    bool own[EPT];
+    uint32_t lanes[EPT];
     if (!masked) {
-      TlEntry e;
-      tl_entry_load(a, t, e);
-      tl_entry_start(row, mine(e.id), false, c, sh, e);
-      __syncthreads();
-      float q, lnq;
-      Q = tl_entry_share(a, t, NW, c, sh, e, q, lnq);
+      tl_entry_load<NT>(a, t, e);
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        own[j] = mine(e[j].id);
+        if (own[j]) e[j].x = to_f32(row.p[e[j].id]);
+      }
+      tl_entry_count(own, sh, lanes);
+    }
+    __syncthreads();  // (and the entries' logits are read before anybody writes there)
+    if (!masked) {
+      const TlTeacherSum k{st[2], st[3], st[4]};
+      Q = k.Q;
+      count = tl_entry_share<NT>(e, own, lanes, k, a.inv_tau, sh);
       g = a.grad_loss[t] * a.inv_tau;
       A = g * Q * unit;
     }
   } else {
     y = tl_index(a.targets, a.target64, t);
-    const bool has = y >= 0 && y < a.V;
-    g = has && a.grad_logprob ? a.grad_logprob[t] * a.inv_tau : 0.0f;
-    const float h = ENTROPY && a.grad_entropy ? a.grad_entropy[t] * a.inv_tau : 0.0f;
-    if (tid == 0 && has && mine((int)y)) xy = to_f32(row.p[y]);
-    // -g p - h p (ln p + H), ln p = ln 2 (d - r) - ln s
-    A = -(g + h * ((-shift.r * kLn2 - lns) + (ENTROPY ? a.entropy[t] : 0.0f))) * unit;
-    B = -h * kLn2 * unit;
+    const bool has = y >= 0 && y < a.V && a.grad_logprob;
+    g = has ? a.grad_logprob[t] * a.inv_tau : 0.0f;
+    const float h = ENTROPY ? a.grad_entropy[t] * a.inv_tau : 0.0f;
+    if (!has || !mine((int)y)) y = -1;
+    if (tid == 0 && y >= 0) xy = to_f32(row.p[y]);
+    // -g p - h p (ln p + H), ln p = ln 2 (d - above) - ln s
+    A = -g * unit;
+    if (ENTROPY) {
+      A = -(g + h * ((-ref.above() * kLn2 - lns) + a.entropy[t])) * unit;
+      B = -h * kLn2 * unit;
+    }
     if (lns == -INFINITY) A = 0.0f;
-    if (!has || !a.grad_logprob) y = -1;
     __syncthreads();  // (the target's logit is read before anybody writes there)
   }
 #pragma unroll
   for (int u = 0; u < W; ++u)
     if (u * NT + tid < n) {
       if (masked) w[u].q = make_uint4(0, 0, 0, 0);
-      tl_grad_word<T, ENTROPY>(w[u], out + row.head + (size_t)(w0 + u * NT + tid) * N, a.vec_out, shift, A, B);
+      tl_grad_word<T, ENTROPY>(w[u], out + row.head + (size_t)(w0 + u * NT + tid) * N, a.vec_out, ref, A, B);
     }
-  if (single >= 0) out[single] = from_f32<T>(tl_grad_value<T, ENTROPY>(x1, shift, A, B));
+  if (single >= 0) out[single] = from_f32<T>(tl_grad_value<ENTROPY>(x1, ref, A, B));
   __syncthreads();
   if constexpr (TEACHER) {
-    if (!masked) {
-      int count = 0;
-      for (int i = 0; i < NW; ++i) count += i * 32 < a.n ? sh.count[i] : 0;
-      tl_entry_grad<T>(sh, count, g, Q, out, prob);
-    }
-  } else if (tid == 0 && y >= 0 && mine((int)y)) {
-    out[y] = from_f32<T>(g + tl_grad_value<T, ENTROPY>(xy, shift, A, B));
+    tl_entry_grad<NT>(sh, count, g, Q, out, [&](float x) { return unit * tl_ex2(ref.arg(x)); });
+  } else if (tid == 0 && y >= 0) {
+    out[y] = from_f32<T>(g + tl_grad_value<ENTROPY>(xy, ref, A, B));
   }
 }
 
-// CTAs of a row, threads and tiles. A short row takes one small CTA; a longer one
-// as many as it takes to hold it, and with few rows as many as keep 8 KB each.
-template <int NT>
-void tl_shape(TlArgs& a, int es) {
-  const long words = ((long)a.V * es + 15) / 16;
-  int ctas = 1;
-  while (ctas < kTlCtas && (words > (long)ctas * NT * kTlWords || ((long)a.T * ctas * 2 <= 152 && words / (2 * ctas) >= 512))) ctas *= 2;
-  if (NT < 256) ctas = 1;
+// ------------------------------------------------------------------ launches
+long tl_words(const TlArgs& a, int es) { return ((long)a.V * es + 15) / 16; }
+
+void tl_shape(TlArgs& a, int es, int ctas, int tile) {
   a.ctas = ctas;
-  a.seg = (int)((words + ctas - 1) / ctas);
-  a.tiles = (a.seg + NT * kTlWords - 1) / (NT * kTlWords);
+  a.seg = (int)((tl_words(a, es) + ctas - 1) / ctas);
+  a.tiles = std::max(1, (a.seg + tile - 1) / tile);
 }
 
-bool tl_small(const TlArgs& a, int es) {
-  return ((long)a.V * es + 15) / 16 <= 64 * kTlWords && a.n <= 64;
-}
-
-template <typename T, int NT, int MODE>
-cudaError_t tl_rows_launch(TlArgs a, cudaStream_t st) {
-  auto kern = k_tl_rows<T, NT, MODE>;
-  tl_shape<NT>(a, (int)sizeof(T));
-  constexpr int smem = 2 * NT * kTlWords * 16;
-  static OncePerDevice done;
-  cudaError_t e = allow_smem(done, kern, smem);
-  if (e != cudaSuccess) return e;
-  const long most = 152L * (NT == 256 ? 3 : 10) / a.ctas;
+template <typename... P>
+cudaError_t tl_launch(void (*kern)(P...), long ctas, int cluster, int threads, int smem, const TlArgs& a, cudaStream_t st) {
+  if (ctas >= 1L << 31) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(std::min<long>(a.T, most) * a.ctas));
-  cfg.blockDim = dim3(NT);
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)a.ctas;
+  at[1].val.clusterDim.x = (unsigned)cluster;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int MODE>
-cudaError_t tl_rows(const TlArgs& a, int dtype, cudaStream_t st) {
+template <typename T, int NT, int EPT, bool CLUSTER, bool LOGPROBS>
+cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
+  auto kern = k_tl_forward<T, NT, EPT, CLUSTER, LOGPROBS>;
+  constexpr int smem = 2 * NT * kTlWords * 16, resident = NT == 256 ? 2 : NT == 128 ? 6 : 18;
+  static OncePerDevice done;
+  const cudaError_t e = allow_smem(done, kern, smem);
+  if (e != cudaSuccess) return e;
+  tl_shape(a, (int)sizeof(T), ctas, NT * kTlWords);
+  return tl_launch(kern, CLUSTER ? (long)a.T * ctas : std::min<long>(a.T, 152L * resident), ctas, NT, smem, a, st);
+}
+
+// A warp for a row where rows are short and there are many; a cluster of large
+// CTAs for a row where there are few, so that they still fill the SMs; else a CTA of
+// 128 threads for a row, six of which share an SM.
+template <bool LOGPROBS>
+cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
   auto go = [&](auto elem) {
     using T = decltype(elem);
-    return tl_small(a, sizeof(T)) ? tl_rows_launch<T, 64, MODE>(a, st) : tl_rows_launch<T, 256, MODE>(a, st);
+    const long words = tl_words(a, (int)sizeof(T));
+    if (a.n <= 64 && (words <= 256 || (words <= 1024 && a.T >= 2000)))
+      return tl_forward_launch<T, 32, 2, false, LOGPROBS>(a, 1, st);
+    int ctas = 1;
+    while (ctas < kTlCtas && (long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512) ctas *= 2;
+    if (ctas > 1) return tl_forward_launch<T, 256, 1, true, LOGPROBS>(a, ctas, st);
+    return tl_forward_launch<T, 128, 2, false, LOGPROBS>(a, 1, st);
+  };
+  return TM_BY_DTYPE(dtype, go);
+}
+
+template <typename T, int NT, int W, int EPT>
+cudaError_t tl_once_launch(TlArgs a, int ctas, cudaStream_t st) {
+  auto kern = k_tl_once<T, NT, W, EPT>;
+  constexpr int smem = NT * W * 16;
+  static OncePerDevice done;
+  const cudaError_t e = allow_smem(done, kern, smem);
+  if (e != cudaSuccess) return e;
+  tl_shape(a, (int)sizeof(T), ctas, NT * W);
+  return tl_launch(kern, (long)a.T * ctas, ctas, NT, smem, a, st);
+}
+
+cudaError_t tl_once(const TlArgs& a, int dtype, cudaStream_t st) {
+  auto go = [&](auto elem) {
+    using T = decltype(elem);
+    const long words = tl_words(a, (int)sizeof(T));
+    if (a.n <= 64 && words <= 512) return tl_once_launch<T, 32, 16, 2>(a, 1, st);
+    if (words <= 2048 && (long)a.T * 2 > 304) return tl_once_launch<T, 128, 16, 2>(a, 1, st);
+    int ctas = 1;
+    while (ctas < kTlCtas && (words > (long)ctas * 4096 || ((long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512))) ctas *= 2;
+    return tl_once_launch<T, 256, 16, 1>(a, ctas, st);
   };
   return TM_BY_DTYPE(dtype, go);
 }
@@ -885,13 +1138,14 @@ template <bool ENTROPY, bool TEACHER>
 cudaError_t tl_backward(TlArgs a, int dtype, cudaStream_t st) {
   auto go = [&](auto elem) {
     using T = decltype(elem);
-    const bool small = tl_small(a, sizeof(T));
-    const long words = ((long)a.V * (long)sizeof(T) + 15) / 16, per = (small ? 64 : 256) * kTlWords;
-    a.ctas = (int)((words + per - 1) / per);
+    const long words = tl_words(a, (int)sizeof(T));
+    const bool small = words <= 64 * kTlWords && a.n <= 128;
+    const long per = (small ? 64 : 256) * kTlWords;
+    a.ctas = std::max(1, (int)((words + per - 1) / per));
     const long ctas = (long)a.T * a.ctas;
     if (ctas >= 1L << 31) return cudaErrorInvalidConfiguration;
-    if (small) return launch_after(k_tl_backward<T, 64, ENTROPY, TEACHER>, dim3((unsigned)ctas), 64, 0, st, a);
-    return launch_after(k_tl_backward<T, 256, ENTROPY, TEACHER>, dim3((unsigned)ctas), 256, 0, st, a);
+    if (small) return launch_after(k_tl_backward<T, 64, 2, ENTROPY, TEACHER>, dim3((unsigned)ctas), 64, 0, st, a);
+    return launch_after(k_tl_backward<T, 256, 1, ENTROPY, TEACHER>, dim3((unsigned)ctas), 256, 0, st, a);
   };
   return TM_BY_DTYPE(dtype, go);
 }
@@ -973,7 +1227,7 @@ tm_status trellis_moe_token_logprobs(const void* logits, int32_t dtype, int64_t 
   a.logits = logits, a.ld = ld, a.T = T, a.V = V, a.inv_tau = 1.0f / temperature;
   a.targets = targets, a.target64 = target_bytes == 8, a.top = top;
   a.logprob = logprob, a.entropy = entropy, a.stats = stats, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
-  const cudaError_t e = tl_rows<kTlLogprobs>(a, dtype, (cudaStream_t)stream);
+  const cudaError_t e = tl_forward<true>(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "token log probabilities");
 }
 
@@ -1012,7 +1266,7 @@ tm_status trellis_moe_distill_forward(const void* logits, int32_t dtype, int64_t
   if (T > 0 && (!loss || !stats)) return status_fail(TM_EINVAL, "loss and stats must be non-NULL");
   if (T == 0) return TM_OK;
   a.loss = loss, a.stats = stats;
-  const cudaError_t e = tl_rows<kTlDistill>(a, dtype, (cudaStream_t)stream);
+  const cudaError_t e = tl_forward<false>(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "distillation");
 }
 
@@ -1050,7 +1304,7 @@ tm_status trellis_moe_distill_loss_grad(const void* logits, int32_t dtype, int64
   if (T == 0) return TM_OK;
   a.loss = loss, a.grad_loss = grad_loss;
   tl_grad_args(a, dtype, grad_logits, grad_ld);
-  const cudaError_t e = tl_rows<kTlDistillGrad>(a, dtype, (cudaStream_t)stream);
+  const cudaError_t e = tl_once(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "distillation");
 }
 
