@@ -95,20 +95,75 @@ __device__ __forceinline__ float tl_warp_sum(float v) {
   return v;
 }
 
+// Two fp32 values that one instruction works on: the sums and gradients below are
+// bound by their instructions, half as many with pairs.
+struct TlPair {
+  uint64_t v;
+  __device__ __forceinline__ TlPair() {}
+  __device__ __forceinline__ TlPair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+  __device__ __forceinline__ float sum() const {
+    float a, b;
+    get(a, b);
+    return a + b;
+  }
+  __device__ __forceinline__ TlPair ex2() const {
+    float a, b;
+    get(a, b);
+    return TlPair(tl_ex2(a), tl_ex2(b));
+  }
+};
+__device__ __forceinline__ TlPair tl_fma(TlPair a, TlPair b, TlPair c) {
+  TlPair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ TlPair tl_add(TlPair a, TlPair b) {
+  TlPair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ TlPair tl_mul(TlPair a, TlPair b) {
+  TlPair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // 16 bytes of a row.
 template <typename T>
 struct TlWord {
   static constexpr int kN = 16 / (int)sizeof(T);
   uint4 q;
   __device__ __forceinline__ void to(float (&v)[kN]) const {
-    const T* t = reinterpret_cast<const T*>(&q);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = to_f32(t[i]);
+    for (int i = 0; i < kN; i += 2) pair(i / 2).get(v[i], v[i + 1]);
   }
-  __device__ __forceinline__ void from(const float (&v)[kN]) {
-    T* t = reinterpret_cast<T*>(&q);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) t[i] = from_f32<T>(v[i]);
+  __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
+  // elements 2 i and 2 i + 1
+  __device__ __forceinline__ TlPair pair(int i) const {
+    if constexpr (sizeof(T) == 4) return TlPair(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+    const uint32_t w = word(i);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return TlPair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return TlPair(f.x, f.y);
+  }
+  __device__ __forceinline__ void set(int i, TlPair p) {
+    float a, b;
+    p.get(a, b);
+    uint32_t* w = reinterpret_cast<uint32_t*>(&q);
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  __device__ __forceinline__ static TlWord none() {  // -inf throughout
+    const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __nv_bfloat16>::value ? 0xFF80FF80u : 0xFC00FC00u;
+    return TlWord{make_uint4(w, w, w, w)};
   }
 };
 __device__ __forceinline__ float tl_word_max(const TlWord<float>& w) {
@@ -344,21 +399,27 @@ __device__ __forceinline__ float tl_grad_value(float x, const TlRef& r, float A,
 template <typename T, bool ENTROPY>
 __device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool vec, const TlRef& r, float A, float B) {
   constexpr int n = TlWord<T>::kN;
-  float v[n];
-  w.to(v);
+  TlWord<T> o;
   if (!r.far) {
+    const TlPair c(r.c, r.c), shift(-r.w, -r.w), a2(A, A), b2(B, B);
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      float d = fmaf(v[i], r.c, -r.w);
-      if (ENTROPY) d = fmaxf(d, -1000.0f);
-      v[i] = tl_ex2(d) * (ENTROPY ? fmaf(B, d, A) : A);
+    for (int i = 0; i < n / 2; ++i) {
+      TlPair d = tl_fma(w.pair(i), c, shift);
+      if (ENTROPY) {
+        float x, y;
+        d.get(x, y);
+        d = TlPair(fmaxf(x, -1000.0f), fmaxf(y, -1000.0f));
+      }
+      o.set(i, tl_mul(d.ex2(), ENTROPY ? tl_fma(b2, d, a2) : a2));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = tl_grad_value<ENTROPY>(v[i], r, A, B);
+    for (int i = 0; i < n / 2; ++i) {
+      float x, y;
+      w.pair(i).get(x, y);
+      o.set(i, TlPair(tl_grad_value<ENTROPY>(x, r, A, B), tl_grad_value<ENTROPY>(y, r, A, B)));
+    }
   }
-  TlWord<T> o;
-  o.from(v);
   if (vec) {
     *reinterpret_cast<uint4*>(out) = o.q;
   } else {
@@ -390,31 +451,17 @@ struct TlTop {
 
 constexpr uint32_t kTlOrderNone = 0x007FFFFFu;  // tl_order(-inf)
 
-// The warp's values in descending order.
-__device__ __forceinline__ uint32_t tl_sort(uint32_t v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-    for (int o = size / 2; o; o /= 2) {
-      const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      const bool down = (lane & size) == 0 || size == 32, low = (lane & o) == 0;
-      v = (low == down) ? max(u, v) : min(u, v);
-    }
-  return v;
-}
-
-// The k-th largest (k = 1..32) of 64 values.
+// The k-th largest (k = 1..32) of 64 values, the largest taken away until k are.
 __device__ __forceinline__ uint32_t tl_kth(const uint32_t* g, int k) {
   const int lane = threadIdx.x & 31;
-  const uint32_t x = tl_sort(g[lane]), y = tl_sort(g[lane + 32]);
-  uint32_t v = max(x, __shfl_sync(0xFFFFFFFFu, y, 31 - lane));  // the 32 largest, rising then falling
-#pragma unroll
-  for (int o = 16; o; o /= 2) {
-    const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = (lane & o) == 0 ? max(u, v) : min(u, v);
+  uint32_t x = g[lane], y = g[lane + 32], m;
+  for (;;) {
+    m = __reduce_max_sync(0xFFFFFFFFu, max(x, y));
+    k -= __popc(__ballot_sync(0xFFFFFFFFu, x == m)) + __popc(__ballot_sync(0xFFFFFFFFu, y == m));
+    if (k <= 0 || m == 0) return m;
+    x = x == m ? 0 : x;
+    y = y == m ? 0 : y;
   }
-  return __shfl_sync(0xFFFFFFFFu, v, k - 1);
 }
 
 template <int NT>
@@ -593,45 +640,74 @@ __device__ __forceinline__ void tl_copy_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
+// A tile's words and a single element into a thread's part where the row's values
+// are so large that exponents need care.
+template <typename T, int NT, int W, bool ENTROPY>
+__device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, float single, float c) {
+  constexpr int N = TlWord<T>::kN;
+  const TlRef r(p.m, c);
+  auto add = [&](float x) {
+    const float d = fmaxf(r.arg(x), -1000.0f), e = tl_ex2(d);  // (not 0 times infinity; a NaN shows in the maximum)
+    p.s += e;
+    if (ENTROPY) p.d = fmaf(e, d, p.d);
+  };
+  for (int u = threadIdx.x; u < min(n, W * NT); u += NT) {
+    const TlWord<T> w{tile[u]};
+    float v[N];
+    w.to(v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(v[i]);
+  }
+  if (single != -INFINITY) add(single);
+  return p;
+}
+
 // Takes W words (of which the thread has those below n, NT apart) and a single
 // element (-inf: none) into a thread's part; returns their maximum.
 template <typename T, int NT, int W, bool ENTROPY>
 __device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, float single, float c) {
   constexpr int N = TlWord<T>::kN;
+  const int tid = threadIdx.x;
   TlWord<T> w[W];
+  if (n >= NT * W) {
+#pragma unroll
+    for (int u = 0; u < W; ++u) w[u].q = tile[u * NT + tid];
+  } else {
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      w[u] = TlWord<T>::none();
+      if (u * NT + tid < n) w[u].q = tile[u * NT + tid];
+    }
+  }
   float m = single;
 #pragma unroll
-  for (int u = 0; u < W; ++u)
-    if (u * NT + (int)threadIdx.x < n) {
-      w[u].q = tile[u * NT + threadIdx.x];
-      m = tl_max_nan(m, tl_word_max(w[u]));
-    }
+  for (int u = 0; u < W; ++u) m = tl_max_nan(m, tl_word_max(w[u]));
   const float top = tl_max_nan(p.m, m);
   if (!(top == p.m)) p.raise(top, c);
   const TlRef r(p.m, c);
-  float s = p.s, dot = p.d;
-  auto add = [&](float d) {
-    if (ENTROPY) d = fmaxf(d, -1000.0f);  // (0 times infinity)
-    const float e = tl_ex2(d);
-    s += e;
-    if (ENTROPY) dot = fmaf(e, d, dot);
+  if (r.far) {
+    p = tl_take_far<T, NT, W, ENTROPY>(p, tile, n, single, c);
+    return m;
+  }
+  const TlPair c2(r.c, r.c), shift(-r.w, -r.w);
+  TlPair s(p.s, 0.0f), dot(p.d, 0.0f);
+  auto add = [&](TlPair x) {
+    TlPair d = tl_fma(x, c2, shift);
+    if (ENTROPY) {  // (not 0 times infinity)
+      float a, b;
+      d.get(a, b);
+      d = TlPair(fmaxf(a, -1000.0f), fmaxf(b, -1000.0f));
+    }
+    const TlPair e = d.ex2();
+    s = tl_add(s, e);
+    if (ENTROPY) dot = tl_fma(e, d, dot);
   };
-  auto all = [&](auto arg) {
 #pragma unroll
-    for (int u = 0; u < W; ++u)
-      if (u * NT + (int)threadIdx.x < n) {
-        float v[N];
-        w[u].to(v);
+  for (int u = 0; u < W; ++u)
 #pragma unroll
-        for (int i = 0; i < N; ++i) add(arg(v[i]));
-      }
-  };
-  if (!r.far)
-    all([&](float x) { return fmaf(x, r.c, -r.w); });
-  else
-    all([&](float x) { return r.arg(x); });
-  if (single != -INFINITY) add(r.arg(single));
-  p.s = s, p.d = dot;
+    for (int i = 0; i < N / 2; ++i) add(w[u].pair(i));
+  if (single != -INFINITY) add(TlPair(single, -INFINITY));
+  p.s = s.sum(), p.d = dot.sum();
   return m;
 }
 
