@@ -28,14 +28,28 @@ constexpr int kTlMaxTop = 32;
 constexpr int kTlMaxEntries = 256;
 constexpr int kTlWords = 8;      // 16-byte words of a tile to a thread
 constexpr int kTlCtas = 8;       // most CTAs of a cluster
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// log2(e) / tau is c, rounded down, and lo > 0 (so that -inf times either is
+// -inf). The sums of the distillation's forward pass take both; those of the log
+// probabilities take c and are put right by the arguments' mean, which they have;
+// gradients take c (with both they took a tenth longer), which moves a p at
+// 2^-10 of the largest by 2^-21.
+struct TlScale {
+  float c, lo, rest;  // rest: lo / c
+  float tau, inv;     // inv: 1 / tau, rounded
+  // x / tau to the last bit or its neighbour (a tenth of a division's instructions)
+  __device__ __forceinline__ float div(float x) const {
+    const float q = x * inv;
+    return fabsf(q) < INFINITY ? fmaf(fmaf(-q, tau, x), inv, q) : q;
+  }
+};
 
 struct TlArgs {
   const void* logits;
   int64_t ld;
   int T, V;
-  float inv_tau;
+  TlScale c;
   // given tokens
   const void* targets;
   int target64, top;
@@ -207,19 +221,23 @@ struct TlRow {
 // exp2 arguments of elements relative to a reference near their maximum m: with
 // c = log2(e) / tau and the whole number w nearest to m c, d = x c - w is one fused
 // operation with one rounding, and what belongs to different references differs by
-// an exact power of two. Where m c is so large that d would not stay small (`far`),
-// elements are either the maximum itself or so far below it that they do not count.
+// an exact power of two. Where m c is so large that d would not stay small (`far`), elements are
+// either the maximum itself or so far below it that they do not count.
 struct TlRef {
-  float c, m, w;
+  TlScale c;
+  float m, w;
   bool far;
-  __device__ __forceinline__ TlRef(float max, float scale) : c(scale) {
+  __device__ __forceinline__ TlRef(float max, const TlScale& scale) : c(scale) {
     m = max == -INFINITY ? 0.0f : max;
-    w = rintf(m * scale);
+    w = rintf(m * scale.c);
     far = !(fabsf(w) < 1073741824.0f);
   }
-  __device__ __forceinline__ float arg(float x) const { return far ? (x == m ? 0.0f : x < m ? -1000.0f : NAN) : fmaf(x, c, -w); }
-  // m c - w, which the reference is below m
-  __device__ __forceinline__ float above() const { return far ? 0.0f : fmaf(m, c, -w); }
+  __device__ __forceinline__ float arg(float x) const { return far ? (x == m ? 0.0f : x < m ? -1000.0f : NAN) : fmaf(x, c.c, -w); }
+  // m c - w, which the reference is below m (BOTH: of c + lo)
+  template <bool BOTH = false>
+  __device__ __forceinline__ float above() const {
+    return far ? 0.0f : BOTH ? fmaf(m, c.lo, fmaf(m, c.c, -w)) : fmaf(m, c.c, -w);
+  }
 };
 
 // Largest value, sum of exponentials relative to its reference and sum of those
@@ -227,7 +245,7 @@ struct TlRef {
 struct TlPart {
   float m, s, d;
   // to the reference of a larger maximum
-  __device__ __forceinline__ void raise(float top, float c) {
+  __device__ __forceinline__ void raise(float top, const TlScale& c) {
     const TlRef a(m, c), b(top, c);
     const float u = m == top || m == -INFINITY ? 0.0f : fmaxf(a.far || b.far ? -1000.0f : a.w - b.w, -1000.0f);
     const float e = tl_ex2(u);
@@ -238,7 +256,7 @@ struct TlPart {
 };
 
 // The parts of a warp's lanes (those of lanes past `n` are not looked at), the same for all lanes.
-__device__ __forceinline__ TlPart tl_warp_merge(TlPart p, float c) {
+__device__ __forceinline__ TlPart tl_warp_merge(TlPart p, const TlScale& c) {
   const float top = tl_warp_max(p.m);
   p.raise(top, c);
   p.s = tl_warp_sum(p.s);
@@ -248,10 +266,11 @@ __device__ __forceinline__ TlPart tl_warp_merge(TlPart p, float c) {
 
 // ln sum exp of a row relative to its maximum, and sum p u' from its part. NaN
 // where the row has a NaN or +inf; -inf where it has nothing.
-__device__ __forceinline__ float tl_log_sum(const TlPart& p, float c) {
+template <bool BOTH>
+__device__ __forceinline__ float tl_log_sum(const TlPart& p, const TlScale& c) {
   if (p.m == -INFINITY) return -INFINITY;
   if (p.m != p.m || p.m == INFINITY) return NAN;
-  return logf(p.s) - TlRef(p.m, c).above() * kLn2;
+  return logf(p.s) - TlRef(p.m, c).above<BOTH>() * kLn2;
 }
 
 // ------------------------------------------------------ the teacher's entries
@@ -303,14 +322,16 @@ __device__ __forceinline__ bool tl_mine(const TlRow<T>& row, int rank, int w0, i
 
 // What the teacher's distribution takes from each warp; before a barrier.
 template <int NT, int EPT>
-__device__ __forceinline__ void tl_teacher_part(const TlEntry (&e)[EPT], float c, TlTeacherWarps& te) {
+__device__ __forceinline__ void tl_teacher_part(const TlEntry (&e)[EPT], const TlScale& c, TlTeacherWarps& te) {
   float m = -INFINITY, s = 0.0f;
 #pragma unroll
   for (int j = 0; j < EPT; ++j) m = tl_max_nan(m, e[j].v);
   m = tl_warp_max(m);
+  if (m != -INFINITY) {  // (most warps have no entries)
 #pragma unroll
-  for (int j = 0; j < EPT; ++j) s += m == -INFINITY ? 0.0f : tl_ex2((e[j].v - m) * c);
-  s = tl_warp_sum(s);
+    for (int j = 0; j < EPT; ++j) s += expf(c.div(e[j].v - m));
+    s = tl_warp_sum(s);
+  }
   if ((threadIdx.x & 31) == 0) te.m[threadIdx.x >> 5] = m, te.s[threadIdx.x >> 5] = s;
 }
 
@@ -321,22 +342,26 @@ struct TlTeacherSum {
 
 // After the barrier.
 template <int NT>
-__device__ __forceinline__ TlTeacherSum tl_teacher_sum(const TlArgs& a, long t, float c, const TlTeacherWarps& te) {
-  float m = -INFINITY, s = 0.0f;
+__device__ __forceinline__ TlTeacherSum tl_teacher_sum(const TlArgs& a, long t, const TlTeacherWarps& te) {
+  // (a lane for a warp's part, the same in every eight lanes)
+  const int w = threadIdx.x & 7;
+  const float wm = w < NT / 32 ? te.m[w] : -INFINITY;
+  float m = wm;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) m = tl_max_nan(m, te.m[w]);
+  for (int o = 4; o; o >>= 1) m = tl_max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float s = wm == -INFINITY ? 0.0f : te.s[w] * expf(a.c.div(wm - m));
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) s += te.m[w] == -INFINITY ? 0.0f : te.s[w] * tl_ex2((te.m[w] - m) * c);
+  for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (m == -INFINITY) return {0.0f, 0.0f, 0.0f};
   if (a.teacher_lse) {
     const float lse = a.teacher_lse[t];
-    return {0.0f, lse, expf(m * a.inv_tau - lse) * s};
+    return {0.0f, lse, expf(a.c.div(m) - lse) * s};
   }
   return {m, logf(s), s * (1.0f / s)};  // (Q: 1, or NaN)
 }
 
-__device__ __forceinline__ float tl_ln_q(const TlEntry& e, const TlTeacherSum& k, float inv_tau) {
-  return e.v == -INFINITY ? -INFINITY : (e.v - k.m) * inv_tau - k.s;
+__device__ __forceinline__ float tl_ln_q(const TlEntry& e, const TlTeacherSum& k, const TlScale& c) {
+  return e.v == -INFINITY ? -INFINITY : c.div(e.v - k.m) - k.s;
 }
 
 // This CTA's entries in te, in order: their numbers before a barrier ...
@@ -351,7 +376,7 @@ __device__ __forceinline__ void tl_entry_count(const bool (&mine)[EPT], TlTeache
 // ... and after it themselves; returns how many.
 template <int NT, int EPT>
 __device__ __forceinline__ int tl_entry_share(const TlEntry (&e)[EPT], const bool (&mine)[EPT], const uint32_t (&lanes)[EPT],
-                                              const TlTeacherSum& k, float inv_tau, TlTeacher& te) {
+                                              const TlTeacherSum& k, const TlScale& c, TlTeacher& te) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int all = 0;
 #pragma unroll
@@ -365,7 +390,7 @@ __device__ __forceinline__ int tl_entry_share(const TlEntry (&e)[EPT], const boo
     }
     if (mine[j]) {
       at += __popc(lanes[j] & ((1u << lane) - 1));
-      te.id[at] = e[j].id, te.q[at] = expf(tl_ln_q(e[j], k, inv_tau)), te.x[at] = e[j].x;
+      te.id[at] = e[j].id, te.q[at] = expf(tl_ln_q(e[j], k, c)), te.x[at] = e[j].x;
     }
   }
   return all;
@@ -401,7 +426,7 @@ __device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool ve
   constexpr int n = TlWord<T>::kN;
   TlWord<T> o;
   if (!r.far) {
-    const TlPair c(r.c, r.c), shift(-r.w, -r.w), a2(A, A), b2(B, B);
+    const TlPair c(r.c.c, r.c.c), shift(-r.w, -r.w), a2(A, A), b2(B, B);
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
       TlPair d = tl_fma(w.pair(i), c, shift);
@@ -476,6 +501,7 @@ __device__ __forceinline__ void tl_rank(TlTop<NT>& to, int n, int top) {
   for (int i = threadIdx.x; i < n; i += NT) {
     const unsigned long long k = to.cand[i];
     int rank = 0;
+#pragma unroll 8
     for (int x = 0; x < n; ++x) rank += to.cand[x] > k;
     if (rank < top) to.list[rank] = k;
   }
@@ -581,34 +607,37 @@ __device__ __noinline__ int tl_top_again(TlTop<NT>& to, int top, const TlRow<T> 
   return n;
 }
 
-// At the end of a row (of the CTA's words of it): to.list. Leaves `to` as the
-// next row needs it. Needs a barrier after it.
+// At the end of a row (of the CTA's words of it): to.list, complete when this
+// returns. Leaves `to` as the next row needs it behind a barrier.
 template <typename T, int NT>
 __device__ __forceinline__ void tl_top_finish(TlTop<NT>& to, int top, const TlRow<T>& row, int w0, int wn, int single, float xs) {
-  constexpr int kPer = TlTop<NT>::kPer;
+  constexpr int kPer = TlTop<NT>::kPer, kFew = 96;
   const int tid = threadIdx.x;
   __syncthreads();
   const int n = to.n;
-  const uint32_t bound = tl_kth(to.group, top);
-  unsigned long long k[kPer];
+  int left = n;
+  if (n > kFew || n < top) {
+    // those that reach the final bound
+    const uint32_t bound = tl_kth(to.group, top);
+    unsigned long long k[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) k[j] = tid + j * NT < n ? to.cand[tid + j * NT] : 0ull;
-  if (tid == 0) to.left = 0;
+    for (int j = 0; j < kPer; ++j) k[j] = tid + j * NT < n ? to.cand[tid + j * NT] : 0ull;
+    if (tid == 0) to.left = 0;
+    __syncthreads();
+    left = 0;
+    if (n <= TlTop<NT>::kRoom) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (k[j] != 0 && (uint32_t)(k[j] >> 32) >= bound) to.cand[atomicAdd(&to.left, 1)] = k[j];
+      __syncthreads();
+      left = to.left;
+    }
+    if (n > TlTop<NT>::kRoom || left < top) left = tl_top_again<T, NT>(to, top, row, w0, wn, single, xs, bound);
+  }
+  tl_rank(to, left, top);
   __syncthreads();
   if (tid == 0) to.n = 0;
   for (int i = tid; i < 64; i += NT) to.group[i] = 0;
-  int left = 0;
-  if (n <= TlTop<NT>::kRoom) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (k[j] != 0 && (uint32_t)(k[j] >> 32) >= bound) to.cand[atomicAdd(&to.left, 1)] = k[j];
-    __syncthreads();
-    left = to.left;
-  }
-  if (n > TlTop<NT>::kRoom || left < top) left = tl_top_again<T, NT>(to, top, row, w0, wn, single, xs, bound);
-  tl_rank(to, left, top);
-  // (tl_top_again has counted in to.n)
-  if (tid == 0) to.n = 0;
 }
 
 __device__ __forceinline__ uint32_t tl_map(const void* p, int rank) {
@@ -643,7 +672,7 @@ __device__ __forceinline__ void tl_copy_wait() {
 // A tile's words and a single element into a thread's part where the row's values
 // are so large that exponents need care.
 template <typename T, int NT, int W, bool ENTROPY>
-__device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, float single, float c) {
+__device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, float single, const TlScale& c) {
   constexpr int N = TlWord<T>::kN;
   const TlRef r(p.m, c);
   auto add = [&](float x) {
@@ -665,7 +694,7 @@ __device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, f
 // Takes W words (of which the thread has those below n, NT apart) and a single
 // element (-inf: none) into a thread's part; returns their maximum.
 template <typename T, int NT, int W, bool ENTROPY>
-__device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, float single, float c) {
+__device__ __forceinline__ float tl_take_words(TlPart& p, const uint4* tile, int n, float single, const TlScale& c) {
   constexpr int N = TlWord<T>::kN;
   const int tid = threadIdx.x;
   TlWord<T> w[W];
@@ -689,10 +718,11 @@ __device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, fl
     p = tl_take_far<T, NT, W, ENTROPY>(p, tile, n, single, c);
     return m;
   }
-  const TlPair c2(r.c, r.c), shift(-r.w, -r.w);
-  TlPair s(p.s, 0.0f), dot(p.d, 0.0f);
+  const TlPair c2(r.c.c, r.c.c), lo(r.c.lo, r.c.lo), shift(-r.w, -r.w);
+  TlPair s(0.0f, 0.0f), dot(0.0f, 0.0f);  // (of this tile: short sums round less)
   auto add = [&](TlPair x) {
     TlPair d = tl_fma(x, c2, shift);
+    if (!ENTROPY) d = tl_fma(x, lo, d);
     if (ENTROPY) {  // (not 0 times infinity)
       float a, b;
       d.get(a, b);
@@ -707,12 +737,19 @@ __device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, fl
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) add(w[u].pair(i));
   if (single != -INFINITY) add(TlPair(single, -INFINITY));
-  p.s = s.sum(), p.d = dot.sum();
+  p.s += s.sum(), p.d += dot.sum();
   return m;
 }
 
+// (half the work where half of the words are not there)
+template <typename T, int NT, int W, bool ENTROPY>
+__device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, float single, const TlScale& c) {
+  return n > NT * W / 2 ? tl_take_words<T, NT, W, ENTROPY>(p, tile, n, single, c)
+                        : tl_take_words<T, NT, W / 2, ENTROPY>(p, tile, n, single, c);
+}
+
 // The warps' parts of a row, by a warp: the same bits for every warp that merges them.
-__device__ __forceinline__ TlPart tl_merge_parts(const float4* parts, int n, float c) {
+__device__ __forceinline__ TlPart tl_merge_parts(const float4* parts, int n, const TlScale& c) {
   TlPart p{-INFINITY, 0.0f, 0.0f};
   for (int i = threadIdx.x & 31; i < n; i += 32) {
     const float4 v = parts[i];
@@ -737,7 +774,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)(blockIdx.x % a.ctas) : 0;
   const long step = gridDim.x / ctas;
-  const float c = a.inv_tau * kLog2e;
+  const TlScale c = a.c;
   if constexpr (LOGPROBS) {
     for (int i = tid; i < 64; i += NT) sh[0].group[i] = 0;
     if (tid == 0) sh[0].n = 0;
@@ -827,23 +864,34 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
           const uint32_t o = tid < n || here ? tl_order(m) : 0u;
           if (o > most) atomicMax(&to.group[tid & 63], most = o);
           if (p == 0) __syncthreads();
-          // (later, whatever the other warps have found so far: any bound of this row's will do)
+          // (later, with whatever the other warps have found so far: any bound of this row's will do)
           if ((p & (p - 1)) == 0) bound = tl_kth(to.group, a.top);
           const uint32_t least = max(bound, kTlOrderNone + 1);
-          if (o >= least) {
-#pragma unroll 1
-            for (int u = 0; u * NT + tid < n; ++u) {
-              const TlWord<T> w{tile[u * NT + tid]};
-              if (tl_order(tl_word_max(w)) < least) continue;
-              const T* v = reinterpret_cast<const T*>(&tile[u * NT + tid]);
-#pragma unroll 1
-              for (int x = 0; x < N; ++x) {
-                const uint32_t k = tl_order(to_f32(v[x]));
-                if (k >= least) tl_put(to, k, row.head + (w0 + u * NT + tid) * N + x);
+          // lane by lane of those that have something, by the whole warp: a lane's 32 4-byte words
+          for (uint32_t hit = __ballot_sync(0xFFFFFFFFu, o >= least); hit; hit &= hit - 1) {
+            const int src = (tid & ~31) + __ffs(hit) - 1, i = (lane >> 2) * NT + src;
+            uint32_t k0 = 0, k1 = 0;  // orders of the lane's one or two elements
+            if (i < n) {
+              const uint32_t v = reinterpret_cast<const uint32_t*>(tile + i)[lane & 3];
+              if constexpr (sizeof(T) == 4) {
+                k0 = tl_order(__uint_as_float(v));
+              } else {
+                const T* h = reinterpret_cast<const T*>(&v);
+                k0 = tl_order(to_f32(h[0])), k1 = tl_order(to_f32(h[1]));
               }
             }
-            if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
+            const bool one = k0 >= least, two = k1 >= least;
+            const uint32_t b1 = __ballot_sync(0xFFFFFFFFu, one), b2 = __ballot_sync(0xFFFFFFFFu, two);
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&to.n, __popc(b1) + __popc(b2));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0);
+            const uint32_t before = (1u << lane) - 1;
+            const int x = row.head + (w0 + i) * N + (lane & 3) * (4 / (int)sizeof(T));
+            const int p1 = at + __popc(b1 & before), p2 = at + __popc(b1) + __popc(b2 & before);
+            if (one && p1 < TlTop<NT>::kRoom) to.cand[p1] = tl_key(k0, x);
+            if (two && p2 < TlTop<NT>::kRoom) to.cand[p2] = tl_key(k1, x + 1);
           }
+          if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
           __syncwarp();
         }
       }
@@ -861,7 +909,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
         const int w0 = rank * a.seg, wn = max(0, min(row.words, w0 + a.seg) - w0);
         tl_top_finish<T, NT>(sh[0], a.top, row, w0, wn, single, x1);
         if (CLUSTER) {
-          __syncthreads();
           if (tid < a.top)
             asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(tl_map(&s_lists[rank * a.top + tid], 0)), "l"(sh[0].list[tid])
                          : "memory");
@@ -872,13 +919,15 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
     if (rank == 0) {
       const TlPart all = tl_merge_parts(s_part[parity], ctas * NW, c);
       const bool none = all.m == -INFINITY;
-      const float M = none ? 0.0f : all.m, lns = tl_log_sum(all, c);
-      auto logp = [&](float x) { return none ? -INFINITY : (x - M) * a.inv_tau - lns; };
+      const float M = none ? 0.0f : all.m, raw = tl_log_sum<!LOGPROBS>(all, c);
+      // the mean of ln 2 (x - M) c, by which the sum grows with c
+      const float mean = LOGPROBS && !none ? (all.d / all.s - TlRef(M, c).above()) * kLn2 : 0.0f;
+      const float lns = LOGPROBS && !none ? fmaf(c.rest, mean, raw) : raw;
+      auto logp = [&](float x) { return none ? -INFINITY : c.div(x - M) - lns; };
       if constexpr (LOGPROBS) {
         if (tid == 0) {
           a.logprob[t] = target >= 0 && target < a.V ? logp(xy) : 0.0f;
-          // H = s - sum p u', u' = (d - (M c - w)) ln 2
-          a.entropy[t] = none ? 0.0f : lns - (all.d / all.s - TlRef(M, c).above()) * kLn2;
+          a.entropy[t] = none ? 0.0f : raw - mean;  // (c's rounding moves both alike)
           a.stats[2 * t] = M;
           a.stats[2 * t + 1] = lns;
         }
@@ -892,6 +941,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
             for (int i = tid; i < n; i += NT) {
               const unsigned long long k = s_lists[i];
               int r = 0;
+#pragma unroll 8
               for (int x = 0; x < n; ++x) r += s_lists[x] > k;
               if (r < a.top) store(r, k);
             }
@@ -900,13 +950,14 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
           }
         }
       } else {
-        const TlTeacherSum k = tl_teacher_sum<NT>(a, t, c, sh[parity]);
+        const TlTeacherSum k = tl_teacher_sum<NT>(a, t, sh[parity]);
         float term = 0.0f;
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-          const float lnq = tl_ln_q(e[j], k, a.inv_tau), q = expf(lnq);
-          if (e[j].id >= 0 && !(q == 0.0f)) term += q * (lnq - logp(e[j].x));
-        }
+        for (int j = 0; j < EPT; ++j)
+          if (e[j].id >= 0) {
+            const float lnq = tl_ln_q(e[j], k, c), q = expf(lnq);
+            if (!(q == 0.0f)) term += q * (lnq - logp(e[j].x));
+          }
         term = tl_warp_sum(term);
         if (lane == 0) sh[parity].loss[warp] = term;
         __syncthreads();
@@ -935,7 +986,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % a.ctas);
   const long t = blockIdx.x / a.ctas;
-  const float c = a.inv_tau * kLog2e;
+  const TlScale c = a.c;
   grid_wait();
   grid_launch();
   const TlRow<T> row(a.logits, a.ld, t, a.V);
@@ -990,14 +1041,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
   for (int p = 0; p < a.tiles; ++p) {
     if (p) n = fetch(p);
     const float xh = p == 0 ? x1 : -INFINITY;
-    static_assert(W == kPart || W == 2 * kPart, "one or two parts");
-    if (W == 2 * kPart) {
-      tl_copy_wait<1>();
-      tl_take<T, NT, kPart, false>(part, tl_buf, n, xh, c);
-    }
+    static_assert(W == 2 * kPart, "two parts");
+    tl_copy_wait<1>();
+    tl_take<T, NT, kPart, false>(part, tl_buf, n, xh, c);
     tl_copy_wait<0>();
-    constexpr int kLast = W - kPart;
-    tl_take<T, NT, kPart, false>(part, tl_buf + kLast * NT, n - kLast * NT, kLast ? -INFINITY : xh, c);
+    if (n > kPart * NT) tl_take<T, NT, kPart, false>(part, tl_buf + kPart * NT, n - kPart * NT, -INFINITY, c);
   }
   part = tl_warp_merge(part, c);
   if (lane < a.ctas) tl_push(&s_part[rank * NW + warp], lane, part);
@@ -1007,20 +1055,21 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
     tl_meet<false>();
   const TlPart all = tl_merge_parts(s_part, a.ctas * NW, c);
   const bool none = all.m == -INFINITY;
-  const float M = none ? 0.0f : all.m, lns = tl_log_sum(all, c);
-  const TlTeacherSum k = tl_teacher_sum<NT>(a, t, c, te);
-  const int count = tl_entry_share<NT>(e, mine, lanes, k, a.inv_tau, te);
+  const float M = none ? 0.0f : all.m, lns = tl_log_sum<true>(all, c);
+  const TlTeacherSum k = tl_teacher_sum<NT>(a, t, te);
+  const int count = tl_entry_share<NT>(e, mine, lanes, k, c, te);
   if (rank == 0) {
     float term = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-      const float lnq = tl_ln_q(e[j], k, a.inv_tau), q = expf(lnq);
-      if (e[j].id >= 0 && !(q == 0.0f)) term += q * (lnq - (none ? -INFINITY : (e[j].x - M) * a.inv_tau - lns));
-    }
+    for (int j = 0; j < EPT; ++j)
+      if (e[j].id >= 0) {
+        const float lnq = tl_ln_q(e[j], k, c), q = expf(lnq);
+        if (!(q == 0.0f)) term += q * (lnq - (none ? -INFINITY : c.div(e[j].x - M) - lns));
+      }
     term = tl_warp_sum(term);
     if (lane == 0) te.loss[warp] = term;
   }
-  const float g = grad_loss * a.inv_tau;
+  const float g = grad_loss * c.inv;
   const TlRef ref(M, c);
   const float unit = tl_unit(ref, lns), A = g * k.Q * unit;
   for (int p = a.tiles - 1; p >= 0; --p) {  // (the last tile is still here)
@@ -1055,7 +1104,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 16) k_tl_backward(const Tl
   const int tid = threadIdx.x;
   const int rank = (int)(blockIdx.x % a.ctas);
   const long t = blockIdx.x / a.ctas;
-  const float c = a.inv_tau * kLog2e;
+  const TlScale c = a.c;
   grid_wait();
   grid_launch();
   const TlRow<T> row(a.logits, a.ld, t, a.V);
@@ -1094,15 +1143,15 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 16) k_tl_backward(const Tl
     if (!masked) {
       const TlTeacherSum k{st[2], st[3], st[4]};
       Q = k.Q;
-      count = tl_entry_share<NT>(e, own, lanes, k, a.inv_tau, sh);
-      g = a.grad_loss[t] * a.inv_tau;
+      count = tl_entry_share<NT>(e, own, lanes, k, c, sh);
+      g = a.grad_loss[t] * c.inv;
       A = g * Q * unit;
     }
   } else {
     y = tl_index(a.targets, a.target64, t);
     const bool has = y >= 0 && y < a.V && a.grad_logprob;
-    g = has ? a.grad_logprob[t] * a.inv_tau : 0.0f;
-    const float h = ENTROPY ? a.grad_entropy[t] * a.inv_tau : 0.0f;
+    g = has ? a.grad_logprob[t] * c.inv : 0.0f;
+    const float h = ENTROPY ? a.grad_entropy[t] * c.inv : 0.0f;
     if (!has || !mine((int)y)) y = -1;
     if (tid == 0 && y >= 0) xy = to_f32(row.p[y]);
     // -g p - h p (ln p + H), ln p = ln 2 (d - above) - ln s
@@ -1157,12 +1206,25 @@ cudaError_t tl_launch(void (*kern)(P...), long ctas, int cluster, int threads, i
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// Lets a kernel have `smem` bytes, and its SM as much shared memory as there is:
+// how many CTAs share one is what keeps the memory busy.
+template <typename... P>
+cudaError_t tl_allow(OncePerDevice& done, void (*kern)(P...), int smem) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return done(dev, [&] {
+    const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return f == cudaSuccess ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : f;
+  });
+}
+
 template <typename T, int NT, int EPT, bool CLUSTER, bool LOGPROBS>
 cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
   auto kern = k_tl_forward<T, NT, EPT, CLUSTER, LOGPROBS>;
   constexpr int smem = 2 * NT * kTlWords * 16, resident = NT == 256 ? 2 : NT == 128 ? 6 : 18;
   static OncePerDevice done;
-  const cudaError_t e = allow_smem(done, kern, smem);
+  const cudaError_t e = tl_allow(done, kern, smem);
   if (e != cudaSuccess) return e;
   tl_shape(a, (int)sizeof(T), ctas, NT * kTlWords);
   return tl_launch(kern, CLUSTER ? (long)a.T * ctas : std::min<long>(a.T, 152L * resident), ctas, NT, smem, a, st);
@@ -1191,7 +1253,7 @@ cudaError_t tl_once_launch(TlArgs a, int ctas, cudaStream_t st) {
   auto kern = k_tl_once<T, NT, W, EPT>;
   constexpr int smem = NT * W * 16;
   static OncePerDevice done;
-  const cudaError_t e = allow_smem(done, kern, smem);
+  const cudaError_t e = tl_allow(done, kern, smem);
   if (e != cudaSuccess) return e;
   tl_shape(a, (int)sizeof(T), ctas, NT * W);
   return tl_launch(kern, (long)a.T * ctas, ctas, NT, smem, a, st);
@@ -1224,6 +1286,16 @@ cudaError_t tl_backward(TlArgs a, int dtype, cudaStream_t st) {
     return launch_after(k_tl_backward<T, 256, 1, ENTROPY, TEACHER>, dim3((unsigned)ctas), 256, 0, st, a);
   };
   return TM_BY_DTYPE(dtype, go);
+}
+
+void tl_temperature(TlArgs& a, float tau) {
+  const double c = 1.4426950408889634 / tau;
+  a.c.tau = tau;
+  a.c.inv = 1.0f / tau;
+  a.c.c = (float)c;
+  if ((double)a.c.c > c) a.c.c = nextafterf(a.c.c, 0.0f);
+  a.c.lo = std::max((float)(c - a.c.c), 1e-30f);
+  a.c.rest = a.c.lo / a.c.c;
 }
 
 tm_status tl_check(const void* logits, int32_t dtype, int64_t ld, int32_t T, int32_t V, float temperature) {
@@ -1272,7 +1344,8 @@ TlArgs tl_teacher_args(const void* logits, int64_t ld, const void* ids, int32_t 
                        int32_t values_dtype, int32_t n, const uint8_t* mask, const float* teacher_lse, int32_t T, int32_t V,
                        float temperature) {
   TlArgs a{};
-  a.logits = logits, a.ld = ld, a.T = T, a.V = V, a.inv_tau = 1.0f / temperature;
+  a.logits = logits, a.ld = ld, a.T = T, a.V = V;
+  tl_temperature(a, temperature);
   a.ids = ids, a.ids64 = id_bytes == 8, a.values = values, a.values_dtype = values_dtype, a.n = n;
   a.mask = mask, a.teacher_lse = teacher_lse;
   return a;
@@ -1300,7 +1373,8 @@ tm_status trellis_moe_token_logprobs(const void* logits, int32_t dtype, int64_t 
   if (!targets || !logprob || !entropy || !stats) return status_fail(TM_EINVAL, "targets, logprob, entropy and stats must be non-NULL");
   if (top > 0 && (!top_ids || !top_logprobs)) return status_fail(TM_EINVAL, "top_ids and top_logprobs must be non-NULL");
   TlArgs a{};
-  a.logits = logits, a.ld = ld, a.T = T, a.V = V, a.inv_tau = 1.0f / temperature;
+  a.logits = logits, a.ld = ld, a.T = T, a.V = V;
+  tl_temperature(a, temperature);
   a.targets = targets, a.target64 = target_bytes == 8, a.top = top;
   a.logprob = logprob, a.entropy = entropy, a.stats = stats, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
   const cudaError_t e = tl_forward<true>(a, dtype, (cudaStream_t)stream);
@@ -1320,7 +1394,8 @@ tm_status trellis_moe_token_logprobs_backward(const void* logits, int32_t dtype,
   if (T == 0) return TM_OK;
   if (!targets || !entropy || !stats) return status_fail(TM_EINVAL, "targets, entropy and stats must be non-NULL");
   TlArgs a{};
-  a.logits = logits, a.ld = ld, a.T = T, a.V = V, a.inv_tau = 1.0f / temperature;
+  a.logits = logits, a.ld = ld, a.T = T, a.V = V;
+  tl_temperature(a, temperature);
   a.targets = targets, a.target64 = target_bytes == 8;
   a.entropy = const_cast<float*>(entropy), a.stats = const_cast<float*>(stats);
   a.grad_logprob = grad_logprob, a.grad_entropy = grad_entropy;
