@@ -1230,15 +1230,19 @@ cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
   return tl_launch(kern, CLUSTER ? (long)a.T * ctas : std::min<long>(a.T, 152L * resident), ctas, NT, smem, a, st);
 }
 
-// A warp for a row where rows are short and there are many; a cluster of large
-// CTAs for a row where there are few, so that they still fill the SMs; else a CTA of
-// 128 threads for a row, six of which share an SM.
+// Rows of up to 4 KB take a warp each (16384 x 1000 bf16: forward 34 us, with 128
+// threads 56; x 2048: 37 and 56; x 4096 would be 54 and 56, but 101 and 82 with the
+// five largest, and 90 and 74 for the distillation).
+bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256; }
+
+// Few rows take a cluster of large CTAs each, so that they still fill the SMs; the
+// others a CTA of 128 threads, six of which share an SM.
 template <bool LOGPROBS>
 cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
   auto go = [&](auto elem) {
     using T = decltype(elem);
     const long words = tl_words(a, (int)sizeof(T));
-    if (a.n <= 64 && (words <= 256 || (words <= 1024 && a.T >= 2000)))
+    if (tl_short(a, words))
       return tl_forward_launch<T, 32, 2, false, LOGPROBS>(a, 1, st);
     int ctas = 1;
     while (ctas < kTlCtas && (long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512) ctas *= 2;
@@ -1263,7 +1267,7 @@ cudaError_t tl_once(const TlArgs& a, int dtype, cudaStream_t st) {
   auto go = [&](auto elem) {
     using T = decltype(elem);
     const long words = tl_words(a, (int)sizeof(T));
-    if (a.n <= 64 && words <= 512) return tl_once_launch<T, 32, 16, 2>(a, 1, st);
+    if (tl_short(a, words)) return tl_once_launch<T, 32, 16, 2>(a, 1, st);
     if (words <= 2048 && (long)a.T * 2 > 304) return tl_once_launch<T, 128, 16, 2>(a, 1, st);
     int ctas = 1;
     while (ctas < kTlCtas && (words > (long)ctas * 4096 || ((long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512))) ctas *= 2;

@@ -1,11 +1,13 @@
-"""Autograd forms of the router losses and of the route combine.
+"""Autograd forms of the router losses, the route combine, the products by
+expert, the distillation loss and the token log probabilities.
 
 What tuning the router of a layer with frozen experts needs: the gradient goes
 from the layer's output through ``combine`` to the route weights, and with the
-losses' own through ``route`` to the logits. The experts' rows are constants
-here (``binding.MxFp4Experts`` has no backward pass); ``combine`` does return
-their gradient to a caller whose rows want one. Gradients are of first order: a
-second derivative through either is refused.
+losses' own through ``route`` to the logits. Frozen experts' rows are constants
+(``binding.MxFp4Experts`` has no backward pass); experts in 16 bits take part
+through ``experts``, which has the gradients of its rows and weights. ``distill``
+and ``token_logprobs`` are the losses at the head. Gradients are of first order:
+a second derivative through any of them is refused.
 """
 from __future__ import annotations
 
@@ -23,7 +25,7 @@ class _FirstOrder(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, _):
-        raise RuntimeError("route and combine have first-order gradients only")
+        raise RuntimeError("route, combine, experts, distill and token_logprobs have first-order gradients only")
 
 
 def _first_order(grad, *sources):
@@ -76,3 +78,74 @@ def route(logits, k: int, mask=None) -> binding.RouterOut:
 def combine(rows, w):
     """binding.combine with a gradient through ``rows`` and ``w``."""
     return _Combine.apply(rows, w)
+
+
+class _Experts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, plan, per_route):
+        ctx.save_for_backward(x, w)
+        ctx.plan, ctx.per_route = plan, per_route
+        return binding.experts_forward(x, w, plan, per_route=per_route)
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        x, w = ctx.saved_tensors
+        want_x, want_w = ctx.needs_input_grad[:2]
+        grad_out = grad_out.contiguous()
+        grad_x, grad_w = binding.experts_backward(x, w, ctx.plan, grad_out, ctx.per_route, want_x, want_w)
+        return _first_order(grad_x, w, grad_out), _first_order(grad_w, x, grad_out), None, None
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, values, temperature, mask, teacher_lse):
+        r = binding.distill_forward(logits, ids, values, temperature, mask, teacher_lse)
+        ctx.save_for_backward(logits, ids, values, mask, teacher_lse, r.stats)
+        ctx.temperature = temperature
+        return r.loss
+
+    @staticmethod
+    def backward(ctx, grad_loss):
+        logits, ids, values, mask, teacher_lse, stats = ctx.saved_tensors
+        grad_loss = grad_loss.contiguous()
+        grad = binding.distill_backward(logits, ids, values, binding.DistillOut(None, stats), grad_loss, ctx.temperature,
+                                        mask, teacher_lse)
+        return _first_order(grad, logits, grad_loss), None, None, None, None, None
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, top, temperature):
+        r = binding.token_logprobs(logits, targets, top, temperature)
+        ctx.save_for_backward(logits, targets, r.entropy, r.stats)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(r.top_ids, r.top_logprobs, r.stats)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, grad_logprob, grad_entropy, _ids, _logprobs, _stats):
+        logits, targets, entropy, stats = ctx.saved_tensors
+        grad_logprob = None if grad_logprob is None else grad_logprob.contiguous()
+        grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
+        fwd = binding.TokenLogprobs(None, entropy, None, None, stats)
+        grad = binding.token_logprobs_backward(logits, targets, fwd, grad_logprob, grad_entropy, ctx.temperature)
+        return _first_order(grad, logits, grad_logprob, grad_entropy), None, None, None
+
+
+def experts(x, w, plan: binding.ExpertPlan, per_route: bool = False):
+    """binding.experts_forward with a gradient through ``x`` and ``w``."""
+    return _Experts.apply(x, w, plan, per_route)
+
+
+def distill(logits, ids, values, temperature: float = 1.0, mask=None, teacher_lse=None):
+    """The losses [T] of binding.distill_forward with a gradient through
+    ``logits``; the teacher is a constant."""
+    for name, t in (("values", values), ("teacher_lse", teacher_lse)):
+        if t is not None and t.requires_grad:
+            raise ValueError("%s requires a gradient: the teacher is a constant of the loss" % name)
+    return _Distill.apply(logits, ids, values, temperature, mask, teacher_lse)
+
+
+def token_logprobs(logits, targets, top: int = 0, temperature: float = 1.0) -> binding.TokenLogprobs:
+    """binding.token_logprobs with a gradient through ``logprob`` and ``entropy``."""
+    return binding.TokenLogprobs(*_TokenLogprobs.apply(logits, targets, top, temperature))
