@@ -10,10 +10,27 @@
 // so that experts with few routes waste little, and the weights, which bound
 // these products by their bytes, are read by every block once. Rows of x and dy
 // are fetched where they lie, by the plan's order: there is no sorted copy of
-// them, and results go straight to route order. Eight warps fetch them (16 bytes
-// a lane, written in the swizzled layout); the weights come by TMA. (TMA's gather
-// of four rows, issued lane by lane, took 65-73 cycles each: 1.8 us for a stage
-// of 208 rows, of which the MMAs need 0.2.)
+// them, and results go straight to route order.
+//
+// Persistent, one CTA per SM: eight epilogue warps, sixteen that fetch rows, one for
+// the weights, one that issues the MMAs.
+//
+// Measured on one GB300, us (floor: each operand once at the memory's copy rate):
+//   160 experts 1536 -> 5120, 32768 routes   forward 476, dx 461, dW 655 (434 each). The
+//     products run at the memory's rate but for a last round of units (5%) and, in
+//     dW, for tiles that are drained and then filled in turn: an SM writes one in 2.7
+//     to 3.1 us (26 bytes a cycle, also where dW stays in L2), each 64 routes add 0.63
+//     (the MMAs alone 0.54), and two accumulators of 256 x 256 do not fit tensor memory.
+//     128 x 256 with two of them is slower (876): rows come from L2 at 42 bytes a cycle
+//     and SM, by TMA or cp.async or both, and those tiles need half as many again.
+//   128 experts 1024 -> 1024, 16384 routes, uneven   66, 87 with the tokens' sums, 90 (45)
+//   64 experts 2560 -> 640, 5120 routes   53, 67 with the sums, 53 (32): 320 units on 152 SMs
+//   8 tokens x 8 of 128 experts, 1024 -> 1024   23 (bytes 15)
+// Measured and not kept: dW's stages of 32 routes with two store buffers a warp (708 us;
+// with 64 and room for two stages 742; two buffers of half the size 674), stores of dW from registers after exchanging
+// pieces between four lanes (734), the routes of dW's stages looked up two stages
+// ahead (656), forward's and dx's results stored from registers after such an exchange
+// (501 and 469 us; through shared memory 480 and 462).
 #include <algorithm>
 
 #include "elem.cuh"

@@ -13,6 +13,9 @@
 //     memory between the sums and the gradient. Rows that are longer than that go
 //     through it in tiles twice.
 //   k_tl_backward: one CTA for each piece of a row.
+// 4096 x 131072 bf16 (1.07 GB): log probabilities 174 us = 6.2 TB/s (five largest
+// 180, twenty 236), distillation forward 174, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
+// loss and gradient in one pass 398 = 5.4. 8 rows: 6.4 us, with twenty largest 10.5.
 #include <algorithm>
 #include <cmath>
 
