@@ -156,39 +156,86 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // ------------------------------------------------------- any sizes and strides
-// C[i, j] = sum_k A(i, k) B(j, k) in 64 x 64 tiles by mma.sync, 32 of k at a
-// time, operands read element by element and laid out k-major in shared memory.
+// C[i, j] = sum_k A(i, k) B(j, k) in 128 x 128 tiles by mma.sync, 32 of k at a time.
+//   forward  i: the expert's routes   j: n          k: k                     both stored along k
+//   grad_x   i: the expert's routes   j: k          k: n                     B stored along j
+//   grad_w   i: n                     j: k          k: the expert's routes   both stored along i, j
 // For rows that do not begin on 16 bytes (an odd K or N without padding, a column
-// range at an odd place), which TMA cannot read. 25 to 30 TFLOP/s, bound by
-// its loads of two bytes a lane.
-//   forward  i: the expert's routes   j: n          k: k
-//   grad_x   i: the expert's routes   j: k          k: n
-//   grad_w   i: n                     j: k          k: the expert's routes
-constexpr int kGenTile = 64, kGenStep = 32, kGenPad = 8, kGenThreads = 128;
+// range at an odd place), which TMA cannot read: eight elements come as the one or
+// two aligned words of 16 bytes that hold them, shifted into place, and lie in
+// shared memory as they do in memory; ldmatrix turns those stored along i or j. The
+// next step's loads are under way while one is multiplied. Forward, dx, dW in us: 5120
+// routes of 64 experts, 2559 -> 641, 429, 316, 398 (39 to 53 TFLOP/s); 8192 of 4 experts,
+// 2049 -> 2047, 592, 597, 562 (116 to 122); element by element, in tiles of 64, it was 25
+// to 30 TFLOP/s. Bound by the latency of those loads: two CTAs an SM, each one step
+// ahead. One CTA an SM that holds raw words in registers: 353, 303, 491 and 646, 614,
+// 696; the words by cp.async three steps ahead: 373, 308, 519 and 727, 691, 779.
+constexpr int kGenTile = 128, kGenStep = 32, kGenThreads = 256;
+constexpr int kGenAlong = kGenStep + 8, kGenAcross = kGenTile + 8;  // elements between rows in shared memory
+constexpr int kGenBytes = kGenTile * kGenAlong * 2;                 // (the larger of the two layouts)
 
-template <typename T>
-__device__ __forceinline__ void gen_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void gen_mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void gen_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <>
-__device__ __forceinline__ void gen_mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void gen_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+template <bool TRANS>
+__device__ __forceinline__ void gen_ldmatrix(uint32_t (&r)[4], uint32_t at) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+// The memory that a tensor's rows and what lies between them take.
+struct GenSpan {
+  uintptr_t lo, hi;
+};
+
+// n (at most eight, none if below 1) elements of 16 bits at p, then zeros.
+__device__ __forceinline__ uint4 gen_load8(const uint16_t* p, int n, GenSpan in) {
+  uint4 q = make_uint4(0, 0, 0, 0);
+  if (n <= 0) return q;
+  const uintptr_t at = (uintptr_t)p, w0 = at & ~(uintptr_t)15;
+  const int off = (int)(at & 15);
+  const bool two = off + 2 * n > 16 && off;
+  if (w0 >= in.lo && w0 + (two ? 32 : 16) <= in.hi) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(w0));
+    const uint4 y = two ? __ldg(reinterpret_cast<const uint4*>(w0) + 1) : make_uint4(0, 0, 0, 0);
+    // the eight words from byte `off` on, by 8, 4 and 2 bytes
+    const bool e = off & 8, f = off & 4;
+    const uint32_t a0 = e ? x.z : x.x, a1 = e ? x.w : x.y, a2 = e ? y.x : x.z, a3 = e ? y.y : x.w, a4 = e ? y.z : y.x, a5 = e ? y.w : y.y;
+    const uint32_t b0 = f ? a1 : a0, b1 = f ? a2 : a1, b2 = f ? a3 : a2, b3 = f ? a4 : a3, b4 = f ? a5 : a4;
+    const int s = (off & 2) * 8;
+    q = make_uint4(__funnelshift_r(b0, b1, s), __funnelshift_r(b1, b2, s), __funnelshift_r(b2, b3, s), __funnelshift_r(b3, b4, s));
+    if (n < 8) {
+      auto keep = [&](uint32_t w, int i) { return n >= 2 * i + 2 ? w : n == 2 * i + 1 ? w & 0xFFFFu : 0u; };
+      q = make_uint4(keep(q.x, 0), keep(q.y, 1), keep(q.z, 2), keep(q.w, 3));
+    }
+  } else {  // (the tensor's first and last words)
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return q;
+}
 
 template <typename T, typename O, int MODE>
-__global__ void __launch_bounds__(kGenThreads) k_ex_general(const ExArgs a) {
-  __shared__ __align__(16) T sa[kGenTile][kGenStep + kGenPad];
-  __shared__ __align__(16) T sb[kGenTile][kGenStep + kGenPad];
-  __shared__ int s_off[kExMaxExperts + 2], s_first[kExMaxExperts + 2];
-  __shared__ int s_row[kGenTile], s_src[kGenTile];
+__global__ void __launch_bounds__(kGenThreads, 2) k_ex_general(const ExArgs a) {
+  __shared__ __align__(16) unsigned char s_tile[2][2][kGenBytes];  // by step, operand
+  __shared__ int s_off[kExMaxExperts + 2], s_first[kExMaxExperts + 2], s_row[kGenTile];
+  constexpr bool kAcrossA = MODE == kExGradW, kAcrossB = MODE != kExForward;  // stored along i, j
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.T * a.topk, E = a.E;
   for (int e = tid; e <= E; e += kGenThreads) s_off[e] = a.offsets[e];
@@ -217,84 +264,118 @@ __global__ void __launch_bounds__(kGenThreads) k_ex_general(const ExArgs a) {
     I = s_off[expert + 1] - s_off[expert];
     J = MODE == kExForward ? a.N : a.K;
     depth = expert == E ? 0 : (MODE == kExForward ? a.K : a.N);  // (routes of no expert: zeros)
+    if (tid < kGenTile) s_row[tid] = i0 + tid < I ? a.order[s_off[expert] + i0 + tid] : -1;
+    __syncthreads();
   }
   const int j0 = blockIdx.y * kGenTile, base = s_off[expert];
-  if (MODE != kExGradW) {
-    if (tid < kGenTile) s_row[tid] = i0 + tid < I ? a.order[base + i0 + tid] : -1;
-    __syncthreads();
-  }
-  const T* x = static_cast<const T*>(a.x);
-  const T* g = static_cast<const T*>(a.g);
-  const T* w = static_cast<const T*>(a.w) + (size_t)(expert < E ? expert : 0) * a.lde;
-  const T zero = from_f32<T>(0.0f);
-  float acc[4][4][4] = {};  // [row pair of 16][column 8] of the warp's 32 x 32... (two row tiles, four column tiles)
-  const int wi = (warp >> 1) * 32, wj = (warp & 1) * 32;
-  for (int k0 = 0; k0 < depth; k0 += kGenStep) {
-    __syncthreads();
-    if (MODE == kExGradW && tid < kGenStep) {
-      const int r = k0 + tid < depth ? a.order[base + k0 + tid] : -1;
-      s_row[tid] = r;
-      s_src[tid] = r < 0 || a.per_route ? r : r / a.topk;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  const uint16_t* g = static_cast<const uint16_t*>(a.g);
+  const uint16_t* wall = static_cast<const uint16_t*>(a.w);
+  const uint16_t* w = wall + (size_t)(expert < E ? expert : 0) * a.lde;
+  auto span = [](const uint16_t* p, int64_t last, int64_t ld, int cols) {
+    return GenSpan{(uintptr_t)p, (uintptr_t)(p + last * ld + cols)};
+  };
+  const GenSpan xs = span(x, (a.per_route ? R : a.T) - 1, a.ldx, a.K), gs = span(g, R - 1, a.ldg, a.N);
+  const GenSpan ws{(uintptr_t)wall, (uintptr_t)(wall + (int64_t)(E - 1) * a.lde + (int64_t)(a.N - 1) * a.ldw + a.K)};
+  auto source = [&](int route) { return a.per_route ? route : route / a.topk; };
+  // a thread's two pieces of each operand: along k, rows tid / 4 and 64 more, piece tid % 4;
+  // across, steps tid / 16 and 16 more, piece tid % 16
+  const int ar = tid >> 2, ac = (tid & 3) * 8, br = tid >> 4, bc = (tid & 15) * 8;
+  uint4 qa[2], qb[2];
+  int route[2];  // grad_w: of the step to be loaded
+  auto look = [&](int k0) {
+    if (MODE == kExGradW) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) route[u] = k0 + br + 16 * u < depth ? __ldg(a.order + base + k0 + br + 16 * u) : -1;
     }
-    if (MODE == kExGradW) __syncthreads();
-    for (int q = tid; q < kGenTile * kGenStep; q += kGenThreads) {
-      if (MODE == kExGradW) {  // neighbouring threads along the rows' columns
-        const int i = q % kGenTile, k = q / kGenTile;
-        const bool in = s_row[k] >= 0;
-        sa[i][k] = in && i0 + i < I ? g[(size_t)s_row[k] * a.ldg + i0 + i] : zero;
-        sb[i][k] = in && j0 + i < J ? x[(size_t)s_src[k] * a.ldx + j0 + i] : zero;
+  };
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (MODE == kExGradW) {
+        const bool in = route[u] >= 0;
+        qa[u] = gen_load8(g + (in ? (size_t)route[u] * a.ldg + i0 + bc : 0), in ? min(8, I - i0 - bc) : 0, gs);
+        qb[u] = gen_load8(x + (in ? (size_t)source(route[u]) * a.ldx + j0 + bc : 0), in ? min(8, J - j0 - bc) : 0, xs);
       } else {
-        const int i = q / kGenStep, k = q % kGenStep;
-        const int r = s_row[i];
-        const bool in = r >= 0 && k0 + k < depth;
-        if (MODE == kExForward)
-          sa[i][k] = in ? x[(size_t)(a.per_route ? r : r / a.topk) * a.ldx + k0 + k] : zero;
-        else
-          sa[i][k] = in ? g[(size_t)r * a.ldg + k0 + k] : zero;
+        const int r = s_row[ar + 64 * u], n = min(8, depth - k0 - ac), j = j0 + ar + 64 * u;
         if (MODE == kExForward) {
-          sb[i][k] = j0 + i < J && k0 + k < depth ? w[(size_t)(j0 + i) * a.ldw + k0 + k] : zero;
+          qa[u] = gen_load8(x + (r >= 0 ? (size_t)source(r) * a.ldx + k0 + ac : 0), r >= 0 ? n : 0, xs);
+          qb[u] = gen_load8(w + (j < J ? (size_t)j * a.ldw + k0 + ac : 0), j < J ? n : 0, ws);
         } else {
-          const int j = q % kGenTile, n = q / kGenTile;
-          sb[j][n] = j0 + j < J && k0 + n < depth ? w[(size_t)(k0 + n) * a.ldw + j0 + j] : zero;
+          const int k = k0 + br + 16 * u;
+          qa[u] = gen_load8(g + (r >= 0 ? (size_t)r * a.ldg + k0 + ac : 0), r >= 0 ? n : 0, gs);
+          qb[u] = gen_load8(w + (k < depth ? (size_t)k * a.ldw + j0 + bc : 0), k < depth ? min(8, J - j0 - bc) : 0, ws);
         }
       }
     }
-    __syncthreads();
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int along = ((ar + 64 * u) * kGenAlong + ac) * 2, across = ((br + 16 * u) * kGenAcross + bc) * 2;
+      *reinterpret_cast<uint4*>(s_tile[buf][0] + (kAcrossA ? across : along)) = qa[u];
+      *reinterpret_cast<uint4*>(s_tile[buf][1] + (kAcrossB ? across : along)) = qb[u];
+    }
+  };
+  float acc[4][4][4] = {};  // the warp's 64 x 32: rows of 16, columns of 8
+  const int wi = (warp >> 2) * 64, wj = (warp & 3) * 32;
+  const int steps = (depth + kGenStep - 1) / kGenStep;
+  if (steps > 0) {
+    look(0);
+    load(0);
+    look(kGenStep);
+    put(0);
+  }
+  __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    if (s + 1 < steps) {
+      load((s + 1) * kGenStep);
+      look((s + 2) * kGenStep);
+    }
+    const uint32_t ta = (uint32_t)__cvta_generic_to_shared(s_tile[s & 1][0]), tb = (uint32_t)__cvta_generic_to_shared(s_tile[s & 1][1]);
 #pragma unroll
     for (int kk = 0; kk < kGenStep; kk += 16) {
-      const int r = lane >> 2, c = kk + (lane & 3) * 2;
-      uint32_t fa[2][4], fb[4][2];
+      uint32_t fa[4][4], fb[2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int i = wi + m * 16 + r;
-        fa[m][0] = *reinterpret_cast<const uint32_t*>(&sa[i][c]);
-        fa[m][1] = *reinterpret_cast<const uint32_t*>(&sa[i + 8][c]);
-        fa[m][2] = *reinterpret_cast<const uint32_t*>(&sa[i][c + 8]);
-        fa[m][3] = *reinterpret_cast<const uint32_t*>(&sa[i + 8][c + 8]);
+      for (int m = 0; m < 4; ++m) {
+        const int i = wi + m * 16;
+        if (kAcrossA)
+          gen_ldmatrix<true>(fa[m], ta + ((kk + (lane & 7) + ((lane >> 4) << 3)) * kGenAcross + i + ((lane >> 3) & 1) * 8) * 2);
+        else
+          gen_ldmatrix<false>(fa[m], ta + ((i + (lane & 15)) * kGenAlong + kk + (lane >> 4) * 8) * 2);
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        fb[n][0] = *reinterpret_cast<const uint32_t*>(&sb[wj + n * 8 + r][c]);
-        fb[n][1] = *reinterpret_cast<const uint32_t*>(&sb[wj + n * 8 + r][c + 8]);
+      for (int n = 0; n < 2; ++n) {
+        const int j = wj + n * 16;
+        if (kAcrossB)
+          gen_ldmatrix<true>(fb[n], tb + ((kk + (lane & 15)) * kGenAcross + j + (lane >> 4) * 8) * 2);
+        else
+          gen_ldmatrix<false>(fb[n], tb + ((j + (lane & 7) + ((lane >> 4) << 3)) * kGenAlong + kk + ((lane >> 3) & 1) * 8) * 2);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) gen_mma<T>(acc[m][n], fa[m], fb[n][0], fb[n][1]);
+        for (int n = 0; n < 4; ++n) gen_mma(acc[m][n], fa[m], fb[n >> 1][(n & 1) * 2], fb[n >> 1][(n & 1) * 2 + 1], T());
     }
+    if (s + 1 < steps) put((s + 1) & 1);
+    __syncthreads();
   }
   O* out = static_cast<O*>(a.out);
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int h = 0; h < 2; ++h) {
+      const int i = wi + m * 16 + (lane >> 2) + h * 8;
+      if (i0 + i >= I) continue;
+      O* row = out + (MODE == kExGradW ? (size_t)expert * a.N + i0 + i : (size_t)s_row[i]) * J;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int i = wi + m * 16 + (lane >> 2) + (v >> 1) * 8, j = j0 + wj + n * 8 + (lane & 3) * 2 + (v & 1);
-        if (i0 + i >= I || j >= J) continue;
-        const size_t row = MODE == kExGradW ? (size_t)expert * a.N + i0 + i : (size_t)s_row[i];
-        out[row * J + j] = from_f32<O>(acc[m][n][v]);
-      }
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int j = j0 + wj + n * 8 + (lane & 3) * 2 + v;
+          if (j < J) row[j] = from_f32<O>(acc[m][n][2 * h + v]);
+        }
+    }
 }
 
 template <typename T, typename O>
