@@ -168,3 +168,17 @@ def test_in_one_captured_graph(example):
         torch.cuda.synchronize()
         for out in outs:
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_no_entropy_term_no_entropy_gradient(example, monkeypatch):
+    """A loss of the log probabilities alone takes the gradient without the entropy's part."""
+    binding, tuning = example.binding, example.tuning
+    given = []
+    plain = binding.token_logprobs_backward
+    monkeypatch.setattr(binding, "token_logprobs_backward", lambda *a, **k: given.append(a[3:5]) or plain(*a, **k))
+    logits = torch.randn(6, 77, device="cuda", requires_grad=True)
+    t, g = torch.randint(0, 77, (6,), device="cuda"), torch.randn(6, device="cuda")
+    (tuning.token_logprobs(logits, t, top=3).logprob * g).sum().backward()
+    assert given[0][0] is not None and given[0][1] is None
+    f = binding.token_logprobs(logits.detach(), t)
+    assert torch.equal(logits.grad, plain(logits.detach(), t, f, g))

@@ -652,11 +652,19 @@ __device__ __forceinline__ void tl_push(void* p, int rank, const TlPart& v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(tl_map(p, rank)), "f"(v.m), "f"(v.s), "f"(v.d), "f"(0.0f)
                : "memory");
 }
+__device__ __forceinline__ void tl_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tl_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
 template <bool CLUSTER>
 __device__ __forceinline__ void tl_meet() {
   if (CLUSTER) {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    tl_arrive();
+    tl_wait();
   } else {
     __syncthreads();
   }
@@ -783,6 +791,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
     if (tid == 0) sh[0].n = 0;
     __syncthreads();
   }
+  if (CLUSTER) tl_arrive();
   grid_wait();
   grid_launch();
 
@@ -823,6 +832,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
   int buf = 0, parity = 0;
   fetch(t, 0, 0);
   ahead(t);
+  if (CLUSTER) tl_wait();  // (the first CTA runs: its shared memory may be written)
   for (; t < a.T; t += step) {
     if (masked(t)) {  // (the same for the cluster)
       fetch(t + step, 0, buf ^= 1);
@@ -990,6 +1000,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
   const int rank = (int)(blockIdx.x % a.ctas);
   const long t = blockIdx.x / a.ctas;
   const TlScale c = a.c;
+  if (a.ctas > 1) tl_arrive();
   grid_wait();
   grid_launch();
   const TlRow<T> row(a.logits, a.ld, t, a.V);
@@ -1000,6 +1011,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
     return max(0, min(min(row.words, (rank + 1) * a.seg) - w0, TW));
   };
   if (a.mask && !a.mask[t]) {  // (the same for the cluster)
+    if (a.ctas > 1) tl_wait();
     for (int p = 0; p < a.tiles; ++p) {
       int w0;
       const int n = tile_words(p, w0);
@@ -1051,6 +1063,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_o
     if (n > kPart * NT) tl_take<T, NT, kPart, false>(part, tl_buf + kPart * NT, n - kPart * NT, -INFINITY, c);
   }
   part = tl_warp_merge(part, c);
+  if (a.ctas > 1) tl_wait();  // (all CTAs run: their shared memory may be written)
   if (lane < a.ctas) tl_push(&s_part[rank * NW + warp], lane, part);
   if (a.ctas > 1)
     tl_meet<true>();

@@ -120,10 +120,13 @@ class _TokenLogprobs(torch.autograd.Function):
         ctx.save_for_backward(logits, targets, r.entropy, r.stats)
         ctx.temperature = temperature
         ctx.mark_non_differentiable(r.top_ids, r.top_logprobs, r.stats)
+        ctx.set_materialize_grads(False)  # (a loss of the log probabilities alone: no entropy term)
         return tuple(r)
 
     @staticmethod
     def backward(ctx, grad_logprob, grad_entropy, _ids, _logprobs, _stats):
+        if grad_logprob is None and grad_entropy is None:
+            return None, None, None, None
         logits, targets, entropy, stats = ctx.saved_tensors
         grad_logprob = None if grad_logprob is None else grad_logprob.contiguous()
         grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
