@@ -24,7 +24,7 @@
 //     128 x 256 with two of them is slower (876): rows come from L2 at 42 bytes a cycle
 //     and SM, by TMA or cp.async or both, and those tiles need half as many again.
 //   128 experts 1024 -> 1024, 16384 routes, uneven   66, 87 with the tokens' sums, 90 (45)
-//   64 experts 2560 -> 640, 5120 routes   53, 67 with the sums, 53 (32): 320 units on 152 SMs
+//   64 experts 2560 -> 640, 5120 routes   46, 67 with the sums, 53 (32)
 //   8 tokens x 8 of 128 experts, 1024 -> 1024   23 (bytes 15)
 // Measured and not kept: dW's stages of 32 routes with two store buffers a warp (708 us;
 // with 64 and room for two stages 742; two buffers of half the size 674), stores of dW from registers after exchanging
@@ -53,6 +53,8 @@ constexpr uint32_t kEtABytes = 128 * 128;      // half a tile of A: 128 rows of 
 constexpr uint32_t kEtGroup = 64 * 128;        // 64 rows of 64 elements (contiguous along M or N)
 constexpr uint32_t kEtStoreBytes = 4096;       // results on their way: rows' for four epilogue warps, dW's for one
 constexpr int kEtMaxGroups = 257 + 1;
+constexpr int kEtHeights = 3;                  // that a tile of forward's weights may have: 128, 96 or 64 channels
+constexpr int kEtBox = 32;                     // rows of its TMA copies
 
 struct EtArgs {
   CUtensorMap map;          // forward, grad_x: the weights; grad_w: the result (if vec)
@@ -87,6 +89,30 @@ struct EtGroups {
 struct EtRings {
   int rows, weights;
   uint32_t stage;  // bytes of a stage of the rows' ring
+};
+
+// Channels of a tile, and tiles of that size.
+struct EtTiles {
+  int high;
+  FastDiv tiles;
+};
+
+// Of forward's heights the one whose rounds of units take least. A unit's time
+// goes by its weights; kEtUnit is what it takes besides, in channels. (320 units of
+// 128 channels are three rounds on 152 SMs, 448 of 96 as well: odd 53 -> 46 us.)
+constexpr int kEtUnit = 8;
+struct EtChoice {
+  EtTiles of[kEtHeights];
+  __device__ __forceinline__ EtTiles pick(int blocks) const {
+    EtTiles best = of[0];
+    int least = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < kEtHeights; ++i) {
+      const int units = blocks * (int)of[i].tiles.d, cost = (units + (int)gridDim.x - 1) / (int)gridDim.x * (of[i].high + kEtUnit);
+      if (cost < least) least = cost, best = of[i];
+    }
+    return best;
+  }
 };
 
 // What lies in shared memory behind the rings and the store buffers.
@@ -169,19 +195,24 @@ __device__ __forceinline__ uint32_t et_idesc(int bf16, int n) {
 
 // The weights' part of the stages. (Returns the stages it loaded.)
 template <int MODE, int MT>
-__device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, int ring, int units, FastDiv tiles,
-                         FastDiv ctiles, volatile int* abort) {
+__device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, int ring, int units, int high,
+                         FastDiv tiles, FastDiv ctiles, volatile int* abort) {
   const bool lead = mx_elect();
   const uint32_t bar0 = smem_u32(&B.wfull[0]);
   MxRing r;
   int it = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
-    const int stages = (m.depth + 63) / 64, halves = et_halves<MT>(a, m), c0 = m.tile * (MT * 128);
+    const int stages = (m.depth + 63) / 64, halves = et_halves<MT>(a, m), c0 = m.tile * high;
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
       if (it >= ring && !mx_wait_warp(&B.wempty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
       const uint32_t st = base + (uint32_t)r.slot * (MT * kEtABytes), bar = bar0 + (uint32_t)r.slot * 8;
-      if (lead) {
+      if (lead && MODE == kExForward && MT == 1) {
+        mx_expect(bar, high * 128);
+#pragma unroll
+        for (int i = 0; i < 128; i += kEtBox)
+          if (i < high) et_tma_3d(st + i * 128, &a.map, s * 64, c0 + i, m.expert, bar);
+      } else if (lead) {
         mx_expect(bar, halves * kEtABytes);
 #pragma unroll
         for (int h = 0; h < MT; ++h) {
@@ -418,8 +449,8 @@ __device__ __forceinline__ void et_store_tile(const uint4 (&v)[8], unsigned char
 }
 
 template <int MODE, int MT, typename O>
-__device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int units, FastDiv tiles, FastDiv ctiles, uint32_t tmem,
-                            unsigned char* stage, volatile int* abort) {
+__device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int units, int high, FastDiv tiles, FastDiv ctiles,
+                            uint32_t tmem, unsigned char* stage, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quarter = warp & 3, part = warp >> 2;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -455,11 +486,11 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
     };
     for (int h = 0; h < halves; ++h) {
     const uint32_t d = tmem + lane_base + (uint32_t)((buf * MT + h) * a.bn);
-    const int tile = m.tile * MT + h, n = tile * 128 + quarter * 32 + lane;  // of 128 channels
+    const int first = m.tile * high + h * 128, end = min(a.M, first + min(128, high)), n = first + quarter * 32 + lane;
     const bool last = h == halves - 1;
     if (MODE == kExGradW) {
       constexpr int kCols = 128 / (int)sizeof(O);  // columns of 128 bytes
-      const int n0 = tile * 128 + quarter * 32;
+      const int n0 = first + quarter * 32;
       for (int c0 = part * kCols; c0 < m.rows; c0 += kEtEpiWarps / 4 * kCols) {
         uint4 q[8];
         O* e = reinterpret_cast<O*>(q);
@@ -507,9 +538,9 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
         for (int c = 0; c < 32; ++c) y[c] = 0.0f;
       }
       if (sizeof(O) == 2 && a.vec)
-        mx_store32_words<O>(y, out, row[k], m.rows - c0, tile, a.M, stage + part * kEtStoreBytes, 1 + part);
+        mx_store32_words<O>(y, out, row[k], m.rows - c0, first, end, a.M, stage + part * kEtStoreBytes, 1 + part);
       else
-        mx_store32<O>(y, out, row[k], m.rows - c0, n, a.M);
+        mx_store32<O>(y, out, row[k], m.rows - c0, n < end ? n : a.M, a.M);
       __syncwarp();  // (tcgen05.ld is for a converged warp)
     }
     }
@@ -522,7 +553,7 @@ template <int MODE>
 constexpr uint32_t et_store_bytes() { return (MODE == kExGradW ? kEtEpiWarps : kEtEpiWarps / 4) * kEtStoreBytes; }
 
 template <int MODE, int MT, typename O>
-__global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__ EtArgs a, EtRings rings, FastDiv tiles, FastDiv ctiles,
+__global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__ EtArgs a, EtRings rings, EtChoice choice, FastDiv ctiles,
                                                          FastDiv topk) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t wofs = (uint32_t)rings.rows * rings.stage;
@@ -575,11 +606,13 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   }
   __syncthreads();
   const uint32_t tmem = sh.tmem_slot, base = smem_u32(smem);
+  const EtTiles shape = MODE == kExForward && MT == 1 ? choice.pick(groups.first[a.E + 1]) : choice.of[0];
+  const FastDiv tiles = shape.tiles;
   const int units = MODE == kExGradW ? a.E * (int)ctiles.d * (int)tiles.d : groups.first[a.E + 1] * (int)tiles.d;
   volatile int* abort = &sh.abort;
   int loaded = 0, rows_loaded = 0, issued = 0;
   if (warp < kEtEpiWarps)
-    et_epilogue<MODE, MT, O>(a, groups, bars, units, tiles, ctiles, tmem, store, abort);
+    et_epilogue<MODE, MT, O>(a, groups, bars, units, shape.high, tiles, ctiles, tmem, store, abort);
   else if (warp < kEtEpiWarps + kEtRowWarps) {
     const EtWalk walk{bars, abort, base, rings.stage, rings.rows, 0, MxRing()};
     using Plan = EtRowPlan<MODE, MT>;
@@ -587,7 +620,7 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
     if constexpr (Plan::kCopyWarps > 0)
       if (warp >= kEtEpiWarps + Plan::kTmaWarps) et_rows_copy<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
   } else if (warp == kEtEpiWarps + kEtRowWarps) {
-    if (MODE != kExGradW) loaded = et_loader<MODE, MT>(a, groups, bars, base + wofs, rings.weights, units, tiles, ctiles, abort);
+    if (MODE != kExGradW) loaded = et_loader<MODE, MT>(a, groups, bars, base + wofs, rings.weights, units, shape.high, tiles, ctiles, abort);
   } else
     issued = et_issuer<MODE, MT>(a, groups, bars, base, base + wofs, rings, units, tiles, ctiles, tmem, abort);
   tc_fence_before();
@@ -658,11 +691,14 @@ cudaError_t et_launch(EtArgs a, int topk, int sms, cudaStream_t st) {
     rings.weights = (int)std::min<uint32_t>(kEtMaxRing, (room - rings.rows * rings.stage) / (MT * kEtABytes));
   }
   a.bufs = 2 * MT * a.bn <= 512 ? 2 : 1;
-  const long tiles = (a.M + MT * 128 - 1) / (MT * 128), ctiles = MODE == kExGradW ? (a.cols + a.bn - 1) / a.bn : 1;
+  auto of = [&](int high) { return EtTiles{high, FastDiv((uint32_t)((a.M + high - 1) / high))}; };
+  constexpr bool kChoose = MODE == kExForward && MT == 1;
+  const EtChoice choice{{of(MT * 128), of(kChoose ? 96 : MT * 128), of(kChoose ? 64 : MT * 128)}};
+  const long tiles = choice.of[2].tiles.d, ctiles = MODE == kExGradW ? (a.cols + a.bn - 1) / a.bn : 1;
   const long units = MODE == kExGradW ? (long)a.E * tiles * ctiles : ((long)a.R / a.bn + std::min<long>(a.R, a.E + 1)) * tiles;
   if (units >= 1L << 31) return cudaErrorInvalidConfiguration;
   const int grid = (int)std::max<long>(1, std::min<long>(units, sms));
-  return launch_after(kern, dim3(grid), kEtThreads, rings.rows * rings.stage + rings.weights * (MT * kEtABytes) + rest, st, a, rings, FastDiv((uint32_t)tiles),
+  return launch_after(kern, dim3(grid), kEtThreads, rings.rows * rings.stage + rings.weights * (MT * kEtABytes) + rest, st, a, rings, choice,
                       FastDiv((uint32_t)ctiles), FastDiv((uint32_t)topk));
 }
 
@@ -689,6 +725,7 @@ bool ex_tc_ok(const ExArgs& a) {
 cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   EtArgs t{};
   const int R = a.T * a.topk, es = a.out_dtype == TM_F32 ? 4 : 2;
+  const bool wide = et_wide(R, a.E);
   t.E = a.E, t.R = R, t.bf16 = a.dtype == TM_BF16, t.per_route = a.per_route;
   t.order = a.order, t.offsets = a.offsets, t.out = a.out, t.flags = a.flags;
   t.x = static_cast<const uint16_t*>(a.x), t.ldx = a.ldx;
@@ -711,11 +748,10 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
     // columns of a block: twice the mean number of routes of an expert, so that most experts
     // take one block and a stage holds no more than it needs (shorter stages: more in flight)
     t.bn = std::min(256, std::max(32, (2 * ((R + a.E - 1) / a.E) + 31) / 32 * 32));
-    e = et_map3(&t.map, a.dtype, a.w, a, a.ldw, a.lde, 64, fwd ? 128 : 64);
+    e = et_map3(&t.map, a.dtype, a.w, a, a.ldw, a.lde, 64, !fwd ? 64 : wide ? 128 : kEtBox);
     t.vec = ((uintptr_t)a.out) % 16 == 0 && t.M % 8 == 0;
   }
   if (e != cudaSuccess) return e;
-  const bool wide = et_wide(R, a.E);
   auto go = [&](auto elem) {
     using O = decltype(elem);
     if (a.mode == kExForward)

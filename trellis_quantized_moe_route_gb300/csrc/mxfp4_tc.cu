@@ -270,7 +270,7 @@ __device__ void mx_epilogue(const MxTcArgs& a, const MxGeom& g, MxBars& B, uint3
       for (int c = 0; c < 32; ++c)
         y[c] = GATED ? mx_silu(__uint_as_float(v[c])) * __uint_as_float(w[c]) : __uint_as_float(v[c]);
       if (words)
-        mx_store32_words<T>(y, out, row[k], m.rows - c0, m.tile, a.N, stage + part * kMxStoreBytes, 1 + part);
+        mx_store32_words<T>(y, out, row[k], m.rows - c0, m.tile * 128, a.N, a.N, stage + part * kMxStoreBytes, 1 + part);
       else
         mx_store32<T>(y, out, row[k], m.rows - c0, n, a.N);
     }

@@ -20,20 +20,20 @@ __device__ __forceinline__ void mx_store32(const float (&y)[32], T* __restrict__
   }
 }
 
-// The same for 16-bit types where rows of y are whole 16-byte words: the four
-// warps of a piece (128 channels) put 16 rows at a time into shared memory and
+// The same for 16-bit types where rows of y are whole 16-byte words, channels
+// `first` to `end` (at most 128): the four warps of a piece put 16 rows at a time into shared memory and
 // store them from there in 16-byte words, a whole row's 256 bytes by 16 lanes
 // (as single elements a warp's store covered 64 bytes, and storing a piece of
 // 32 rows took 1400 cycles). Neighbouring lanes first swap halves, so that the
 // even one holds both channels of an even row and the odd one of the next; the
 // 64-byte halves of odd rows change places, which keeps the two apart in banks.
 template <typename T>
-__device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __restrict__ out, int row, int rows, int tile,
-                                                 int N, unsigned char* stage, int bar) {
+__device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __restrict__ out, int row, int rows, int first,
+                                                 int end, int N, unsigned char* stage, int bar) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, odd = lane & 1;
   const uint32_t pick = odd ? 0x3276u : 0x5410u;
   const int t = quarter * 32 + lane, chunk = t & 15;
-  const bool in = tile * 128 + chunk * 8 < N;
+  const bool in = first + chunk * 8 < end;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h * 16 >= rows) break;
@@ -54,7 +54,7 @@ __device__ __forceinline__ void mx_store32_words(const float (&y)[32], T* __rest
       const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((chunk * 16) ^ ((r & 1) << 6)));
       const int to = __shfl_sync(0xFFFFFFFFu, row, h * 16 + r);
       if (in && h * 16 + r < rows)
-        *reinterpret_cast<uint4*>(out + (size_t)to * N + tile * 128 + chunk * 8) = v;
+        *reinterpret_cast<uint4*>(out + (size_t)to * N + first + chunk * 8) = v;
     }
     asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
   }
