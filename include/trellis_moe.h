@@ -509,9 +509,21 @@ void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
 tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int32_t* order, int32_t* offsets,
                                   uint32_t* flags, void* stream);
 
+/* Copies of those of x [x_rows, K], grad_out [g_rows, N] and w [E, N, K] whose
+ * rows do not begin on 16 bytes (the address, or twice a stride, is no multiple of
+ * 16; or lde is 0), as the products below need them: to x_to [x_rows, K'], g_to
+ * [g_rows, N'] and w_to [E, N, K'], K' and N' being the next multiples of eight, each
+ * 16-byte aligned, or NULL: none. Strides in elements of 16 bits, as below. Of w only
+ * experts that have routes by the plan's offsets are copied. What lies behind a copy's
+ * K or N elements of a row is left undefined, and no product reads it. */
+tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, const void* grad_out, int64_t ldg,
+                                    int32_t g_rows, const void* w, int64_t ldw, int64_t lde, const int32_t* offsets, int32_t E,
+                                    int32_t N, int32_t K, void* x_to, void* g_to, void* w_to, void* stream);
+
 /* out [T * topk, N] in route order, of out_dtype; a route of no expert gives a
  * row of zeros. x: row s at x + s * ldx elements; w: row n of expert e at
- * w + e * lde + n * ldw elements. T = 0 is a no-op. */
+ * w + e * lde + n * ldw elements. Rows of x, w and (below) grad_out begin on 16
+ * bytes; results lie anywhere. T = 0 is a no-op. */
 tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx, int32_t per_route, const void* w,
                                       int64_t ldw, int64_t lde, const int32_t* order, const int32_t* offsets, int32_t T,
                                       int32_t topk, int32_t E, int32_t N, int32_t K, void* out, int32_t out_dtype,

@@ -70,6 +70,32 @@ def test_products(lib, name, ok):
     assert lib.trellis_moe_experts_grad_x_workspace_size(1 << 21, 2, 1 << 20, 0) == (1 << 22) * (1 << 20) * 4
 
 
+ALIGN = dict(x=A + 2, ldx=65, x_rows=4, g=A + 2, ldg=33, g_rows=8, w=A + 2, ldw=65, lde=65 * 32, offsets=A, E=4, N=32, K=64, x_to=A,
+             g_to=A, w_to=A, stream=None)
+
+
+def test_aligned_copies(lib):
+    for status, part, changed in (
+            (EUNSUPPORTED, "E=0", dict(E=0)), (EUNSUPPORTED, "E=257", dict(E=257)), (EINVAL, "N=0", dict(N=0)),
+            (EINVAL, "K=", dict(K=(1 << 20) + 1)), (EINVAL, "x_rows=0", dict(x_rows=0)), (EINVAL, "g_rows=-1", dict(g_rows=-1)),
+            (EINVAL, "ldx=63", dict(ldx=63)), (EINVAL, "ldg=31", dict(ldg=31)), (EINVAL, "ldw=63", dict(ldw=63)),
+            (EINVAL, "lde=-1", dict(lde=-1)), (EINVAL, "non-NULL", dict(x=None)), (EINVAL, "non-NULL", dict(g=None)),
+            (EINVAL, "non-NULL", dict(w=None)), (EINVAL, "non-NULL", dict(offsets=None)), (EINVAL, "elements", dict(x=A + 1)),
+            (EINVAL, "elements", dict(g=A + 1)), (EINVAL, "elements", dict(w=A + 1)), (EINVAL, "16-byte", dict(x_to=A + 8)),
+            (EINVAL, "16-byte", dict(g_to=A + 8)), (EINVAL, "16-byte", dict(w_to=A + 8)),
+            (EUNSUPPORTED, "2^34", dict(N=1 << 20, K=1 << 14, ldw=1 << 14, ldg=1 << 20, ldx=1 << 14))):
+        refused(lib, "trellis_moe_experts_align", ALIGN, status, part, **changed)
+    nothing = dict(ALIGN, x=None, g=None, w=None, offsets=None, x_to=None, g_to=None, w_to=None)
+    assert lib.trellis_moe_experts_align(*nothing.values()) == OK
+
+
+@pytest.mark.parametrize("name,ok", [("forward", FWD), ("grad_x", GX), ("grad_w", GW)])
+def test_products_need_aligned_rows(lib, name, ok):
+    for key, value in (("x", A + 8), ("ldx", 68), ("g", A + 8), ("ldg", 36), ("w", A + 8), ("ldw", 68), ("lde", 64 * 32 + 4), ("lde", 0)):
+        if key in ok:
+            refused(lib, "trellis_moe_experts_" + name, ok, EINVAL, "16 bytes", **{key: value})
+
+
 LP = dict(l=A, dtype=BF16, ld=100, targets=A, tb=8, T=4, V=100, tau=1.0, top=3, lp=A, ent=A, st=A, ids=A, tlp=A, stream=None)
 LPB = dict(l=A, dtype=BF16, ld=100, targets=A, tb=4, T=4, V=100, tau=1.0, ent=A, st=A, gl=A, ge=None, out=2 * A, gld=100,
            stream=None)

@@ -50,6 +50,22 @@ def test_calls_that_are_right(lib):
     assert grad.count("trellis_moe_experts_grad_x") == 1 and grad.count("trellis_moe_experts_grad_w") == 1
 
 
+def test_copies_of_what_is_not_aligned(lib):
+    """One call copies the inputs whose rows do not begin on 16 bytes, and those alone; the products read the copies."""
+    wide = Apart(4, 16, dtype=BF16, strides=(41, 1))
+    w, g = Tensor(3, 8, 16, dtype=BF16), Tensor(8, 8, dtype=BF16)
+    binding.experts_forward(wide, w, plan())
+    binding.experts_backward(wide, w, plan(), g)
+    binding.experts_backward(wide, w, plan(), g, want_w=False)          # (x is not read)
+    binding.experts_forward(Tensor(4, 16, dtype=BF16), Apart(3, 8, 16, dtype=BF16, strides=(0, 16, 1)), plan())
+    calls = [(n, a) for n, _, a in lib if n not in ("trellis_moe_experts_grad_x_workspace_size",)]
+    names = [n.replace("trellis_moe_experts_", "") for n, _ in calls]
+    assert names == ["align", "forward", "align", "grad_x", "grad_w", "grad_x", "align", "forward"]
+    for i, has in ((0, (True, False, False)), (2, (True, False, False)), (6, (False, False, True))):
+        assert tuple(bool(to) for to in calls[i][1][13:16]) == has
+    assert calls[1][1][2] == calls[4][1][2] == 16 and calls[7][1][5:7] == (16, 128)
+
+
 @pytest.mark.parametrize("name", ["x", "w", "g", "plan", "out"])
 def test_other_devices(lib, name):
     forward, backward = experts(lambda n: 1 if n == name else 0)

@@ -114,6 +114,35 @@ def test_fp32_results_and_strides(binding, dtype, per_route):
         check(binding, ids, E, x, w, g, per_route, dtype, "f32", "f32")
 
 
+@pytest.mark.parametrize("T,E,k,N,K,dtype", [(600, 3, 2, 300, 531, "bf16"), (600, 3, 2, 265, 1030, "f16"), (17, 40, 4, 515, 129, "bf16"),
+                                             (200, 2, 1, 1, 700, "f16"), (200, 2, 1, 700, 1, "bf16"), (1, 3, 1, 77, 1001, "f16")])
+@pytest.mark.parametrize("out", [None, "f32"])
+def test_odd_sizes_in_several_tiles(binding, T, E, k, N, K, dtype, out):
+    """Rows of no whole 16-byte words, in tiles of 128 and 256 channels, read and written; values between them stay."""
+    rng = np.random.default_rng(N)
+    ids = routing(rng, T, E, k, outside=T > 2)
+    x, w, g = device(rng, dtype, T, K), device(rng, dtype, E, N, K), device(rng, dtype, T * k, N)
+    y, gx, gw = check(binding, ids, E, x, w, g, False, dtype, out, out)
+    # the same values in rows that are aligned: the same bits
+    pad = lambda t: torch.nn.functional.pad(t, (0, -t.shape[-1] % 8), value=float("nan"))[..., :t.shape[-1]]  # noqa: E731
+    plan = binding.expert_plan(torch.from_numpy(ids).cuda(), E)
+    dt = None if out is None else DT[out]
+    assert torch.equal(y, binding.experts_forward(pad(x), pad(w), plan, out_dtype=dt))
+    again = binding.experts_backward(pad(x), pad(w), plan, pad(g), grad_w_dtype=dt)
+    assert torch.equal(gx, again[0]) and torch.equal(gw, again[1])
+    store = torch.full((T * k * N + 16,), 9.0, dtype=y.dtype, device="cuda")
+    binding.experts_forward(x, w, plan, out=store[3:3 + T * k * N].view(T * k, N))
+    assert torch.equal(store[3:3 + T * k * N].view(T * k, N), y) and (store[:3] == 9).all() and (store[3 + T * k * N:] == 9).all()
+
+
+def test_one_matrix_for_all_experts(binding):
+    """w expanded over the experts."""
+    rng = np.random.default_rng(12)
+    ids = routing(rng, 30, 5, 2)
+    w = device(rng, "bf16", 1, 48, 64).expand(5, 48, 64)
+    check(binding, ids, 5, device(rng, "bf16", 30, 64), w, device(rng, "bf16", 60, 48), False, "bf16")
+
+
 def test_the_same_expert_twice(binding):
     """A token may list an expert more than once: its routes all count."""
     rng = np.random.default_rng(8)

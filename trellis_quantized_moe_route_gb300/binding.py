@@ -40,7 +40,7 @@ EXPORTED = [
     "trellis_moe_mxfp4_quantize", "trellis_moe_mxfp4_dequantize", "trellis_moe_mxfp4_prepare",
     "trellis_moe_mxfp4_workspace_size", "trellis_moe_mxfp4_forward", "trellis_moe_mxfp4_forward_experts",
     "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_set_wait_test", "trellis_moe_mxfp4_destroy",
-    "trellis_moe_expert_plan", "trellis_moe_experts_forward", "trellis_moe_experts_grad_x_workspace_size",
+    "trellis_moe_expert_plan", "trellis_moe_experts_align", "trellis_moe_experts_forward", "trellis_moe_experts_grad_x_workspace_size",
     "trellis_moe_experts_grad_x", "trellis_moe_experts_grad_w",
     "trellis_moe_token_logprobs", "trellis_moe_token_logprobs_backward",
     "trellis_moe_distill_forward", "trellis_moe_distill_backward", "trellis_moe_distill_loss_grad",
@@ -132,6 +132,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "trellis_moe_mxfp4_set_wait_test": (I32, [P, ctypes.c_uint64, I32]),
         "trellis_moe_mxfp4_destroy": (None, [P]),
         "trellis_moe_expert_plan": (I32, [P, I32, I32, P, P, P, P]),
+        "trellis_moe_experts_align": (I32, [P, I64, I32, P, I64, I32, P, I64, I64, P, I32, I32, I32, P, P, P, P]),
         "trellis_moe_experts_forward": (I32, [P, I32, I64, I32, P, I64, I64, P, P, I32, I32, I32, I32, I32, P, I32, P, P]),
         "trellis_moe_experts_grad_x_workspace_size": (SZ, [I32, I32, I32, I32]),
         "trellis_moe_experts_grad_x": (I32, [P, I32, I64, I32, P, I64, I64, P, P, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
@@ -997,10 +998,38 @@ def _expert_rows(name, t, plan, rows, cols, dtype):
     return ld
 
 
+def _experts_align(lib, plan, N, K, x, g, w):
+    """The address and strides of x (x, ld), grad_out (g, ld) and w (w, ldw, lde),
+    or of copies of those whose rows do not begin on 16 bytes; and what holds the
+    copies (None: nothing), which has to live until the last launch."""
+    xp, gp, wp = (0 if t is None else t[0].data_ptr() for t in (x, g, w))
+    ldx, ldg, ldw, lde = x[1] if x else 0, g[1] if g else 0, w[1] if w else 0, w[2] if w else 0
+    if not ((xp | gp | wp | 2 * (ldx | ldg | ldw | lde)) & 15) and (lde or w is None or plan.E == 1) or plan.T == 0:
+        return xp, ldx, gp, ldg, wp, ldw, lde, None
+    K8, N8, R = (K + 7) // 8 * 8, (N + 7) // 8 * 8, plan.T * plan.topk
+    xr = x[0].shape[0] if x and (xp | 2 * ldx) & 15 else 0
+    gr = R if g and (gp | 2 * ldg) & 15 else 0
+    we = plan.E if w and ((wp | 2 * (ldw | lde)) & 15 or (lde == 0 and plan.E > 1)) else 0
+    copies = _empty(xr * K8 + gr * N8 + we * N * K8, dtype=_torch_mod.int16, device=plan.device)
+    to = copies.data_ptr()
+    tx, tg, tw = (to if xr else None, to + 2 * xr * K8 if gr else None, to + 2 * (xr * K8 + gr * N8) if we else None)
+    _launch(lib.trellis_moe_experts_align, plan.index, xp, ldx, xr, gp, ldg, gr, wp, ldw, lde, plan.offsets_ptr, plan.E, N, K,
+            tx, tg, tw)
+    if xr:
+        xp, ldx = tx, K8
+    if gr:
+        gp, ldg = tg, N8
+    if we:
+        wp, ldw, lde = tw, K8, N * K8
+    return xp, ldx, gp, ldg, wp, ldw, lde, copies
+
+
 def experts_forward(x, w, plan: ExpertPlan, per_route: bool = False, out=None, out_dtype=None, stream=None):
     """Rows [T * topk, N] in route order: the route's expert's w [E, N, K] times
     row t of x [T, K] (per_route: row r of x [T * topk, K]), bfloat16 or
-    float16, of out_dtype (default x's)."""
+    float16, of out_dtype (default x's). Of inputs whose rows do not begin on 16
+    bytes (K no multiple of eight, say) it makes copies first, of w for each call:
+    weights that are padded, w[:, :, :K] of a wider tensor, save that."""
     if stream is not None:
         with _given(stream, "x", x):
             return experts_forward(x, w, plan, per_route, out, out_dtype)
@@ -1017,8 +1046,8 @@ def experts_forward(x, w, plan: ExpertPlan, per_route: bool = False, out=None, o
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
         out_code = _dtype_code(_on_device("out", out, plan.index, None, (R, N)).dtype)
-    _launch(lib.trellis_moe_experts_forward, plan.index, x.data_ptr(), code, ldx, 1 if per_route else 0, w.data_ptr(), ldw,
-            lde, plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, out.data_ptr(), out_code, plan.flags_ptr)
+    xp, ldx, _, _, wp, ldw, lde, _copies = _experts_align(lib, plan, N, K, (x, ldx), None, (w, ldw, lde))
+    _launch(lib.trellis_moe_experts_forward, plan.index, xp, code, ldx, 1 if per_route else 0, wp, ldw, lde, plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, out.data_ptr(), out_code, plan.flags_ptr)
     return out
 
 
@@ -1038,18 +1067,21 @@ def experts_backward(x, w, plan: ExpertPlan, grad_out, per_route: bool = False, 
     ldx = _expert_rows("x", x, plan, R if per_route else plan.T, K, dtype)
     ldg = _expert_rows("grad_out", grad_out, plan, R, N, dtype)
     gx = gw = None
+    xp, ldx, gp, ldg, wp, ldw, lde, _copies = _experts_align(lib, plan, N, K, (x, ldx) if want_w else None,
+                                                            (grad_out, ldg) if want_x or want_w else None,
+                                                            (w, ldw, lde) if want_x else None)
     if want_x:
         gx = _empty((x.shape[0], K), dtype=dtype, device=x.device)
         wsb = lib.trellis_moe_experts_grad_x_workspace_size(plan.T, plan.topk, K, flag)
         ws = _empty(wsb, dtype=_u8, device=x.device) if wsb else None
-        _launch(lib.trellis_moe_experts_grad_x, plan.index, grad_out.data_ptr(), code, ldg, flag, w.data_ptr(), ldw, lde,
+        _launch(lib.trellis_moe_experts_grad_x, plan.index, gp, code, ldg, flag, wp, ldw, lde,
                 plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, gx.data_ptr(), plan.flags_ptr, _opt(ws),
                 wsb)
     if want_w:
         grad_w_dtype = dtype if grad_w_dtype is None else grad_w_dtype
         gcode = _dtype_code(grad_w_dtype)
         gw = _empty((plan.E, N, K), dtype=grad_w_dtype, device=x.device)
-        _launch(lib.trellis_moe_experts_grad_w, plan.index, x.data_ptr(), code, ldx, flag, grad_out.data_ptr(), ldg,
+        _launch(lib.trellis_moe_experts_grad_w, plan.index, xp, code, ldx, flag, gp, ldg,
                 plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, gw.data_ptr(), gcode, plan.flags_ptr)
     return gx, gw
 

@@ -1,5 +1,5 @@
 // Products by expert with 16-bit weights (sm_103a): entry points, the plan, the
-// sum over a token's routes, and the kernel that takes any sizes and strides.
+// sum over a token's routes, and copies of rows that TMA cannot read.
 //   y_r = W_e x_s(r),   dx_s = sum of W_e^T dy_r over the routes r that read row s,
 //   dW_e = sum of dy_r x_s(r)^T over the expert's routes, in order.
 #include "experts.h"
@@ -155,241 +155,76 @@ __global__ void __launch_bounds__(THREADS)
   if (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");  // no CTA leaves while another reads its counts
 }
 
-// ------------------------------------------------------- any sizes and strides
-// C[i, j] = sum_k A(i, k) B(j, k) in 128 x 128 tiles by mma.sync, 32 of k at a time.
-//   forward  i: the expert's routes   j: n          k: k                     both stored along k
-//   grad_x   i: the expert's routes   j: k          k: n                     B stored along j
-//   grad_w   i: n                     j: k          k: the expert's routes   both stored along i, j
-// For rows that do not begin on 16 bytes (an odd K or N without padding, a column
-// range at an odd place), which TMA cannot read: eight elements come as the one or
-// two aligned words of 16 bytes that hold them, shifted into place, and lie in
-// shared memory as they do in memory; ldmatrix turns those stored along i or j. The
-// next step's loads are under way while one is multiplied. Forward, dx, dW in us: 5120
-// routes of 64 experts, 2559 -> 641, 429, 316, 398 (39 to 53 TFLOP/s); 8192 of 4 experts,
-// 2049 -> 2047, 592, 597, 562 (116 to 122); element by element, in tiles of 64, it was 25
-// to 30 TFLOP/s. Bound by the latency of those loads: two CTAs an SM, each one step
-// ahead. One CTA an SM that holds raw words in registers: 353, 303, 491 and 646, 614,
-// 696; the words by cp.async three steps ahead: 373, 308, 519 and 727, 691, 779.
-constexpr int kGenTile = 128, kGenStep = 32, kGenThreads = 256;
-constexpr int kGenAlong = kGenStep + 8, kGenAcross = kGenTile + 8;  // elements between rows in shared memory
-constexpr int kGenBytes = kGenTile * kGenAlong * 2;                 // (the larger of the two layouts)
+// ------------------------------------------------------------ aligned copies
+// Rows that do not begin on 16 bytes (an odd N or K without padding, a column range
+// at an odd place) cannot be read by TMA; copies of them can. Eight elements come
+// as the one or two aligned words of 16 bytes that hold them, shifted into place.
+// Bound by memory: some 5.7 TB/s read and written. Products with their copies,
+// forward, dx, dW in us: 5120 routes of 64 experts, 2559 -> 641, 120, 149, 114 (aligned
+// 46, 67, 53; by mma.sync in tiles of 128, with the shifting in its loads, 429, 316, 398);
+// 8192 of 4 experts, 2049 -> 2047, 88, 119, 93 (592, 597, 562); 64 of 128 experts, 1025 ->
+// 1023, 77, 84, 118 (138, 139, 315).
+constexpr int kAlignThreads = 256, kAlignWords = 4;  // of a thread
 
-__device__ __forceinline__ void gen_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void gen_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <bool TRANS>
-__device__ __forceinline__ void gen_ldmatrix(uint32_t (&r)[4], uint32_t at) {
-  if (TRANS)
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-  else
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-
-// The memory that a tensor's rows and what lies between them take.
-struct GenSpan {
-  uintptr_t lo, hi;
+struct ExAlignJob {
+  const uint16_t* src;
+  uintptr_t lo, hi;    // the memory that src's rows and what lies between them take
+  int64_t ld, lde;     // elements between rows and between matrices
+  FastDiv words;       // 16-byte words of a row of the copy
+  uint32_t total;      // words of a matrix
+  int cols;
+  uint4* dst;
 };
 
-// n (at most eight, none if below 1) elements of 16 bits at p, then zeros.
-__device__ __forceinline__ uint4 gen_load8(const uint16_t* p, int n, GenSpan in) {
-  uint4 q = make_uint4(0, 0, 0, 0);
-  if (n <= 0) return q;
+struct ExAlignArgs {
+  ExAlignJob w, x, g;  // E matrices, one and one
+  int experts;         // E, 0 without w
+  const int32_t* offsets;
+};
+
+// n (at most eight) elements of 16 bits at p, then zeros.
+__device__ __forceinline__ uint4 align_load(const uint16_t* p, int n, uintptr_t lo, uintptr_t hi) {
   const uintptr_t at = (uintptr_t)p, w0 = at & ~(uintptr_t)15;
   const int off = (int)(at & 15);
-  const bool two = off + 2 * n > 16 && off;
-  if (w0 >= in.lo && w0 + (two ? 32 : 16) <= in.hi) {
+  const bool two = off + 2 * n > 16;
+  if (w0 >= lo && w0 + (two ? 32 : 16) <= hi) {
     const uint4 x = __ldg(reinterpret_cast<const uint4*>(w0));
     const uint4 y = two ? __ldg(reinterpret_cast<const uint4*>(w0) + 1) : make_uint4(0, 0, 0, 0);
-    // the eight words from byte `off` on, by 8, 4 and 2 bytes
+    // the words from byte `off` on, by 8, 4 and 2 bytes
     const bool e = off & 8, f = off & 4;
     const uint32_t a0 = e ? x.z : x.x, a1 = e ? x.w : x.y, a2 = e ? y.x : x.z, a3 = e ? y.y : x.w, a4 = e ? y.z : y.x, a5 = e ? y.w : y.y;
     const uint32_t b0 = f ? a1 : a0, b1 = f ? a2 : a1, b2 = f ? a3 : a2, b3 = f ? a4 : a3, b4 = f ? a5 : a4;
     const int s = (off & 2) * 8;
-    q = make_uint4(__funnelshift_r(b0, b1, s), __funnelshift_r(b1, b2, s), __funnelshift_r(b2, b3, s), __funnelshift_r(b3, b4, s));
-    if (n < 8) {
-      auto keep = [&](uint32_t w, int i) { return n >= 2 * i + 2 ? w : n == 2 * i + 1 ? w & 0xFFFFu : 0u; };
-      q = make_uint4(keep(q.x, 0), keep(q.y, 1), keep(q.z, 2), keep(q.w, 3));
-    }
-  } else {  // (the tensor's first and last words)
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
-    q = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(__funnelshift_r(b0, b1, s), __funnelshift_r(b1, b2, s), __funnelshift_r(b2, b3, s), __funnelshift_r(b3, b4, s));
   }
-  return q;
+  uint32_t w[4] = {};  // (the tensor's first and last words)
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, typename O, int MODE>
-__global__ void __launch_bounds__(kGenThreads, 2) k_ex_general(const ExArgs a) {
-  __shared__ __align__(16) unsigned char s_tile[2][2][kGenBytes];  // by step, operand
-  __shared__ int s_off[kExMaxExperts + 2], s_first[kExMaxExperts + 2], s_row[kGenTile];
-  constexpr bool kAcrossA = MODE == kExGradW, kAcrossB = MODE != kExForward;  // stored along i, j
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int R = a.T * a.topk, E = a.E;
-  for (int e = tid; e <= E; e += kGenThreads) s_off[e] = a.offsets[e];
-  if (tid == 0) s_off[E + 1] = R;
-  __syncthreads();
-  int expert, i0, I, J, depth;
-  if (MODE == kExGradW) {
-    expert = blockIdx.z;
-    i0 = blockIdx.x * kGenTile;
-    I = a.N, J = a.K, depth = s_off[expert + 1] - s_off[expert];
-  } else {
-    if (tid == 0) {
-      int run = 0;
-      for (int e = 0; e <= E; ++e) {
-        s_first[e] = run;
-        run += (s_off[e + 1] - s_off[e] + kGenTile - 1) / kGenTile;
-      }
-      s_first[E + 1] = run;
+__global__ void __launch_bounds__(kAlignThreads) k_ex_align(const __grid_constant__ ExAlignArgs a) {
+  grid_wait();
+  grid_launch();
+  const int y = blockIdx.y, e = y < a.experts ? y : 0;
+  if (y < a.experts && a.offsets[e] == a.offsets[e + 1]) return;  // (nobody reads it)
+  const ExAlignJob& j = y < a.experts ? a.w : y == a.experts && a.x.total ? a.x : a.g;
+  const uint16_t* src = j.src + (size_t)e * j.lde;
+  uint4* dst = j.dst + (size_t)e * j.total;
+  const uint32_t n0 = blockIdx.x * (kAlignThreads * kAlignWords) + threadIdx.x;
+  uint4 q[kAlignWords];
+#pragma unroll
+  for (int u = 0; u < kAlignWords; ++u) {
+    const uint32_t n = n0 + u * kAlignThreads;
+    if (n < j.total) {
+      const uint32_t row = j.words.div(n), c = (n - row * j.words.d) * 8;
+      q[u] = align_load(src + (size_t)row * j.ld + c, min(8, j.cols - (int)c), j.lo, j.hi);
     }
-    __syncthreads();
-    const int b = blockIdx.x;
-    if (b >= s_first[E + 1]) return;
-    expert = 0;
-    while (s_first[expert + 1] <= b) ++expert;
-    i0 = (b - s_first[expert]) * kGenTile;
-    I = s_off[expert + 1] - s_off[expert];
-    J = MODE == kExForward ? a.N : a.K;
-    depth = expert == E ? 0 : (MODE == kExForward ? a.K : a.N);  // (routes of no expert: zeros)
-    if (tid < kGenTile) s_row[tid] = i0 + tid < I ? a.order[s_off[expert] + i0 + tid] : -1;
-    __syncthreads();
   }
-  const int j0 = blockIdx.y * kGenTile, base = s_off[expert];
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* g = static_cast<const uint16_t*>(a.g);
-  const uint16_t* wall = static_cast<const uint16_t*>(a.w);
-  const uint16_t* w = wall + (size_t)(expert < E ? expert : 0) * a.lde;
-  auto span = [](const uint16_t* p, int64_t last, int64_t ld, int cols) {
-    return GenSpan{(uintptr_t)p, (uintptr_t)(p + last * ld + cols)};
-  };
-  const GenSpan xs = span(x, (a.per_route ? R : a.T) - 1, a.ldx, a.K), gs = span(g, R - 1, a.ldg, a.N);
-  const GenSpan ws{(uintptr_t)wall, (uintptr_t)(wall + (int64_t)(E - 1) * a.lde + (int64_t)(a.N - 1) * a.ldw + a.K)};
-  auto source = [&](int route) { return a.per_route ? route : route / a.topk; };
-  // a thread's two pieces of each operand: along k, rows tid / 4 and 64 more, piece tid % 4;
-  // across, steps tid / 16 and 16 more, piece tid % 16
-  const int ar = tid >> 2, ac = (tid & 3) * 8, br = tid >> 4, bc = (tid & 15) * 8;
-  uint4 qa[2], qb[2];
-  int route[2];  // grad_w: of the step to be loaded
-  auto look = [&](int k0) {
-    if (MODE == kExGradW) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) route[u] = k0 + br + 16 * u < depth ? __ldg(a.order + base + k0 + br + 16 * u) : -1;
-    }
-  };
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (MODE == kExGradW) {
-        const bool in = route[u] >= 0;
-        qa[u] = gen_load8(g + (in ? (size_t)route[u] * a.ldg + i0 + bc : 0), in ? min(8, I - i0 - bc) : 0, gs);
-        qb[u] = gen_load8(x + (in ? (size_t)source(route[u]) * a.ldx + j0 + bc : 0), in ? min(8, J - j0 - bc) : 0, xs);
-      } else {
-        const int r = s_row[ar + 64 * u], n = min(8, depth - k0 - ac), j = j0 + ar + 64 * u;
-        if (MODE == kExForward) {
-          qa[u] = gen_load8(x + (r >= 0 ? (size_t)source(r) * a.ldx + k0 + ac : 0), r >= 0 ? n : 0, xs);
-          qb[u] = gen_load8(w + (j < J ? (size_t)j * a.ldw + k0 + ac : 0), j < J ? n : 0, ws);
-        } else {
-          const int k = k0 + br + 16 * u;
-          qa[u] = gen_load8(g + (r >= 0 ? (size_t)r * a.ldg + k0 + ac : 0), r >= 0 ? n : 0, gs);
-          qb[u] = gen_load8(w + (k < depth ? (size_t)k * a.ldw + j0 + bc : 0), k < depth ? min(8, J - j0 - bc) : 0, ws);
-        }
-      }
-    }
-  };
-  auto put = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int along = ((ar + 64 * u) * kGenAlong + ac) * 2, across = ((br + 16 * u) * kGenAcross + bc) * 2;
-      *reinterpret_cast<uint4*>(s_tile[buf][0] + (kAcrossA ? across : along)) = qa[u];
-      *reinterpret_cast<uint4*>(s_tile[buf][1] + (kAcrossB ? across : along)) = qb[u];
-    }
-  };
-  float acc[4][4][4] = {};  // the warp's 64 x 32: rows of 16, columns of 8
-  const int wi = (warp >> 2) * 64, wj = (warp & 3) * 32;
-  const int steps = (depth + kGenStep - 1) / kGenStep;
-  if (steps > 0) {
-    look(0);
-    load(0);
-    look(kGenStep);
-    put(0);
-  }
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) {
-      load((s + 1) * kGenStep);
-      look((s + 2) * kGenStep);
-    }
-    const uint32_t ta = (uint32_t)__cvta_generic_to_shared(s_tile[s & 1][0]), tb = (uint32_t)__cvta_generic_to_shared(s_tile[s & 1][1]);
-#pragma unroll
-    for (int kk = 0; kk < kGenStep; kk += 16) {
-      uint32_t fa[4][4], fb[2][4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int i = wi + m * 16;
-        if (kAcrossA)
-          gen_ldmatrix<true>(fa[m], ta + ((kk + (lane & 7) + ((lane >> 4) << 3)) * kGenAcross + i + ((lane >> 3) & 1) * 8) * 2);
-        else
-          gen_ldmatrix<false>(fa[m], ta + ((i + (lane & 15)) * kGenAlong + kk + (lane >> 4) * 8) * 2);
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int j = wj + n * 16;
-        if (kAcrossB)
-          gen_ldmatrix<true>(fb[n], tb + ((kk + (lane & 15)) * kGenAcross + j + (lane >> 4) * 8) * 2);
-        else
-          gen_ldmatrix<false>(fb[n], tb + ((j + (lane & 7) + ((lane >> 4) << 3)) * kGenAlong + kk + ((lane >> 3) & 1) * 8) * 2);
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) gen_mma(acc[m][n], fa[m], fb[n >> 1][(n & 1) * 2], fb[n >> 1][(n & 1) * 2 + 1], T());
-    }
-    if (s + 1 < steps) put((s + 1) & 1);
-    __syncthreads();
-  }
-  O* out = static_cast<O*>(a.out);
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = wi + m * 16 + (lane >> 2) + h * 8;
-      if (i0 + i >= I) continue;
-      O* row = out + (MODE == kExGradW ? (size_t)expert * a.N + i0 + i : (size_t)s_row[i]) * J;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int j = j0 + wj + n * 8 + (lane & 3) * 2 + v;
-          if (j < J) row[j] = from_f32<O>(acc[m][n][2 * h + v]);
-        }
-    }
-}
-
-template <typename T, typename O>
-cudaError_t gen_launch(const ExArgs& a, cudaStream_t st) {
-  const long R = (long)a.T * a.topk;
-  const unsigned blocks = (unsigned)(R / kGenTile + std::min<long>(R, a.E + 1));  // (at least as many as there are)
-  auto tiles = [](int n) { return (unsigned)((n + kGenTile - 1) / kGenTile); };
-  if (a.mode == kExForward)
-    k_ex_general<T, O, kExForward><<<dim3(blocks, tiles(a.N)), kGenThreads, 0, st>>>(a);
-  else if (a.mode == kExGradX)
-    k_ex_general<T, O, kExGradX><<<dim3(blocks, tiles(a.K)), kGenThreads, 0, st>>>(a);
-  else
-    k_ex_general<T, O, kExGradW><<<dim3(tiles(a.N), tiles(a.K), a.E), kGenThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  for (int u = 0; u < kAlignWords; ++u)
+    if (n0 + u * kAlignThreads < j.total) dst[n0 + u * kAlignThreads] = q[u];
 }
 
 // A thread takes eight columns of a token. The routes' rows are in fp32, so that a
@@ -453,18 +288,11 @@ cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, 
   return TM_BY_DTYPE_VEC(dtype, eights(rows, K, K, 4) && eights(out, K, K, dtype_bytes(dtype)), go);
 }
 
-cudaError_t launch_ex_general(const ExArgs& a, cudaStream_t st) {
-  auto go = [&](auto elem) {
-    using O = decltype(elem);
-    return a.dtype == TM_BF16 ? gen_launch<__nv_bfloat16, O>(a, st) : gen_launch<__half, O>(a, st);
-  };
-  return TM_BY_DTYPE(a.out_dtype, go);
-}
-
 namespace {
 
 cudaError_t ex_product(const ExArgs& a, cudaStream_t st) {
-  if (!ex_tc_ok(a)) return launch_ex_general(a, st);
+  if (a.T == 0)  // (grad_w of no tokens)
+    return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * dtype_bytes(a.out_dtype), st);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -493,7 +321,22 @@ tm_status ex_check(const ExArgs& a) {
   for (const void* q : p)
     if (((uintptr_t)q) % 2) return status_fail(TM_EINVAL, "x, w and grad_out must be aligned to their elements");
   if (((uintptr_t)a.out) % dtype_bytes(a.out_dtype)) return status_fail(TM_EINVAL, "the result must be aligned to its elements");
+  auto rows_ok = [](const void* q, int64_t ld) { return ((uintptr_t)q) % 16 == 0 && ld % 8 == 0 && ld < (1LL << 38); };
+  if (a.T > 0 && ((a.mode != kExGradX && !rows_ok(a.x, a.ldx)) || (a.mode != kExForward && !rows_ok(a.g, a.ldg)) ||
+                  (a.mode != kExGradW && (!rows_ok(a.w, a.ldw) || (a.E > 1 && (!rows_ok(a.w, a.lde) || a.lde == 0))))))
+    return status_fail(TM_EINVAL, "rows of x, w and grad_out must begin on 16 bytes (trellis_moe_experts_align copies them so)");
   return TM_OK;
+}
+
+// One tensor of an aligned copy: E matrices of `rows` rows; false if it is too large.
+bool ex_align_job(ExAlignJob& j, const void* src, int64_t ld, int64_t lde, int E, int rows, int cols, void* dst) {
+  const int words = (cols + 7) / 8;
+  const long total = (long)rows * words;
+  j.src = static_cast<const uint16_t*>(src), j.ld = ld, j.lde = lde, j.cols = cols, j.dst = static_cast<uint4*>(dst);
+  j.words = FastDiv((uint32_t)words), j.total = (uint32_t)total;
+  j.lo = (uintptr_t)src;
+  j.hi = (uintptr_t)(j.src + (int64_t)(E - 1) * lde + (int64_t)(rows - 1) * ld + cols);
+  return total < 1L << 31;
 }
 
 }  // namespace
@@ -512,6 +355,35 @@ tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int3
   if ((R > 0 && (!ids || !order)) || !offsets || !flags) return status_fail(TM_EINVAL, "ids, order, offsets and flags must be non-NULL");
   const cudaError_t e = launch_ex_plan(ids, R, E, order, offsets, flags, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert plan");
+}
+
+tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, const void* grad_out, int64_t ldg,
+                                    int32_t g_rows, const void* w, int64_t ldw, int64_t lde, const int32_t* offsets, int32_t E,
+                                    int32_t N, int32_t K, void* x_to, void* g_to, void* w_to, void* stream) {
+  set_last_error("");
+  if (E < 1 || E > kExMaxExperts) return status_fail(TM_EUNSUPPORTED, "E=%d outside 1..%d", E, kExMaxExperts);
+  if (N < 1 || N > kExMaxSide) return status_fail(TM_EINVAL, "N=%d outside 1..%d", N, kExMaxSide);
+  if (K < 1 || K > kExMaxSide) return status_fail(TM_EINVAL, "K=%d outside 1..%d", K, kExMaxSide);
+  if ((x_to && x_rows < 1) || (g_to && g_rows < 1)) return status_fail(TM_EINVAL, "x_rows=%d, g_rows=%d: less than 1", x_rows, g_rows);
+  if (x_to && ldx < K) return status_fail(TM_EINVAL, "ldx=%lld is less than K=%d", (long long)ldx, K);
+  if (g_to && ldg < N) return status_fail(TM_EINVAL, "ldg=%lld is less than N=%d", (long long)ldg, N);
+  if (w_to && (ldw < K || lde < 0))
+    return status_fail(TM_EINVAL, "ldw=%lld, lde=%lld: rows of w must not overlap", (long long)ldw, (long long)lde);
+  if ((x_to && !x) || (g_to && !grad_out) || (w_to && (!w || !offsets))) return status_fail(TM_EINVAL, "arguments must be non-NULL");
+  for (const void* q : {x_to ? x : nullptr, g_to ? grad_out : nullptr, w_to ? w : nullptr})
+    if (((uintptr_t)q) % 2) return status_fail(TM_EINVAL, "x, w and grad_out must be aligned to their elements");
+  for (const void* q : {x_to, g_to, w_to})
+    if (((uintptr_t)q) % 16) return status_fail(TM_EINVAL, "the copies must be 16-byte aligned");
+  ExAlignArgs a{ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, w_to ? E : 0, offsets};
+  const bool ok = (!x_to || ex_align_job(a.x, x, ldx, 0, 1, x_rows, K, x_to)) &&
+                  (!g_to || ex_align_job(a.g, grad_out, ldg, 0, 1, g_rows, N, g_to)) &&
+                  (!w_to || ex_align_job(a.w, w, ldw, lde, E, N, K, w_to));
+  if (!ok) return status_fail(TM_EUNSUPPORTED, "a matrix of 2^34 elements or more cannot be copied");
+  const uint32_t most = std::max({a.x.total, a.g.total, a.w.total}), per = kAlignThreads * kAlignWords;
+  const unsigned grid_y = (unsigned)(a.experts + (x_to != nullptr) + (g_to != nullptr));
+  if (grid_y == 0) return TM_OK;
+  const cudaError_t e = launch_after(k_ex_align, dim3((most + per - 1) / per, grid_y), kAlignThreads, 0, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? TM_OK : status_cuda(e, "aligned copies");
 }
 
 tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx, int32_t per_route, const void* w,

@@ -29,10 +29,7 @@ cudaError_t launch_ex_plan(const int32_t* ids, int R, int E, int32_t* order, int
                            cudaStream_t st);
 // dx of a token: the sum of its routes' fp32 rows, in order.
 cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, int dtype, cudaStream_t st);
-// On the tensor cores' own path, for addresses and strides that TMA can read.
-bool ex_tc_ok(const ExArgs& a);
+// One of the products; some token, addresses and strides of 16 bytes.
 cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st);
-// Any sizes and strides.
-cudaError_t launch_ex_general(const ExArgs& a, cudaStream_t st);
 
 }  // namespace tmoe

@@ -448,6 +448,26 @@ __device__ __forceinline__ void et_store_tile(const uint4 (&v)[8], unsigned char
   }
 }
 
+// The same where dW's rows are not whole 16-byte words: element by element, lanes
+// along a row; `rows` and `cols` of them are there.
+template <typename O>
+__device__ __forceinline__ void et_store_elements(const uint4 (&v)[8], unsigned char* stage, O* out, int ld, int rows, int cols) {
+  constexpr int kCols = 128 / (int)sizeof(O);
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+  __syncwarp();
+  const int n = min(rows, 32);
+#pragma unroll 4
+  for (int r = 0; r < n; ++r)
+#pragma unroll
+    for (int c = lane; c < kCols; c += 32) {
+      const int b = c * (int)sizeof(O);
+      if (c < cols) out[(size_t)r * ld + c] = *reinterpret_cast<const O*>(stage + r * 128 + ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
+    }
+}
+
 template <int MODE, int MT, typename O>
 __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int units, int high, FastDiv tiles, FastDiv ctiles,
                             uint32_t tmem, unsigned char* stage, volatile int* abort) {
@@ -511,11 +531,9 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
         }
         if (a.vec) {
           et_store_tile(q, stage + warp * kEtStoreBytes, &a.map, m.col0 + c0, n0, m.expert, n0 < a.M);
-        } else if (n < a.M) {
-          O* o = out + ((size_t)m.expert * a.M + n) * a.cols + m.col0 + c0;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c0 + c < m.rows) o[c] = e[c];
+        } else {
+          et_store_elements<O>(q, stage + warp * kEtStoreBytes, out + ((size_t)m.expert * a.M + n0) * a.cols + m.col0 + c0, a.cols,
+                               a.M - n0, m.rows - c0);
         }
         __syncwarp();  // (tcgen05.ld is for a converged warp)
       }
@@ -711,16 +729,7 @@ cudaError_t et_launch(EtArgs a, int topk, int sms, cudaStream_t st) {
 // routes an expert: 52.7 and 52.1, 67.3 and 66.7, dW 55.5 and 59.7).
 bool et_wide(int R, int E) { return R >= 96L * E; }
 
-bool et_rows_ok(const void* p, int64_t ld) { return ((uintptr_t)p) % 16 == 0 && ld % 8 == 0 && ld < (1LL << 38); }
-
 }  // namespace
-
-bool ex_tc_ok(const ExArgs& a) {
-  if (a.T == 0) return false;
-  if (a.mode != kExGradX && !et_rows_ok(a.x, a.ldx)) return false;
-  if (a.mode != kExForward && !et_rows_ok(a.g, a.ldg)) return false;
-  return a.mode == kExGradW || (et_rows_ok(a.w, a.ldw) && (a.E == 1 || (et_rows_ok(a.w, a.lde) && a.lde > 0)));
-}
 
 cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   EtArgs t{};
