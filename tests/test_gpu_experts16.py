@@ -135,6 +135,15 @@ def test_odd_sizes_in_several_tiles(binding, T, E, k, N, K, dtype, out):
     assert torch.equal(store[3:3 + T * k * N].view(T * k, N), y) and (store[:3] == 9).all() and (store[3 + T * k * N:] == 9).all()
 
 
+@pytest.mark.parametrize("E,k,N,K", [(30, 1, 136, 264), (256, 2, 520, 72), (3, 1, 300, 600)])
+def test_most_routes_to_few_experts(binding, E, k, N, K):
+    """Experts in the order of their routes: equal numbers, none, and far more than the others; more tiles than SMs."""
+    rng = np.random.default_rng(E)
+    ids = rng.choice(E, size=(700, k), p=np.where(np.arange(E) == E // 2, 0.7, 0.3 / (E - 1))).astype(np.int32)
+    ids[ids == E - 1] = 0
+    check(binding, ids, E, device(rng, "f16", 700, K), device(rng, "f16", E, N, K), device(rng, "f16", 700 * k, N), False, "f16")
+
+
 def test_one_matrix_for_all_experts(binding):
     """w expanded over the experts."""
     rng = np.random.default_rng(12)

@@ -23,7 +23,7 @@
 //     (the MMAs alone 0.54), and two accumulators of 256 x 256 do not fit tensor memory.
 //     128 x 256 with two of them is slower (876): rows come from L2 at 42 bytes a cycle
 //     and SM, by TMA or cp.async or both, and those tiles need half as many again.
-//   128 experts 1024 -> 1024, 16384 routes, uneven   66, 87 with the tokens' sums, 90 (45)
+//   128 experts 1024 -> 1024, 16384 routes, uneven   66, 88 with the tokens' sums, 82 (45)
 //   64 experts 2560 -> 640, 5120 routes   46, 67 with the sums, 53 (32)
 //   8 tokens x 8 of 128 experts, 1024 -> 1024   23 (bytes 15)
 // Measured and not kept: dW's stages of 32 routes with two store buffers a warp (708 us;
@@ -77,10 +77,22 @@ struct EtBars {
   uint64_t acc_full[2], acc_empty[2];
 };
 
-// The groups of routes: where each begins, and its first block.
+// The groups of routes: where each begins; forward, grad_x: its first block; grad_w:
+// the experts in the order in which they are taken.
 struct EtGroups {
   int off[kEtMaxGroups], first[kEtMaxGroups];
+  bool uneven;
 };
+
+// The CTA's unit of a round. grad_w's units last as long as their experts have routes:
+// where that differs much, those with most routes come first, and rounds go to and
+// fro, so that who has a long unit in one has a shorter one in the next (uneven: 90 -> 82
+// us; large, where it hardly differs, would take 669 and not 660).
+template <int MODE>
+__device__ __forceinline__ int et_turn(const EtGroups& g, int round) {
+  const int n = (int)gridDim.x;
+  return round * n + (MODE == kExGradW && g.uneven && (round & 1) ? n - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
 
 // Two rings of stages of 64 of the contraction: the weights come from memory and
 // need more of them in flight than the rows, which mostly come from L2. (One ring
@@ -141,8 +153,9 @@ __device__ __forceinline__ EtUnit et_unit(const EtArgs& a, const EtGroups& g, in
   int b = (int)tiles.div((uint32_t)v);
   m.tile = v - b * (int)tiles.d;
   if (MODE == kExGradW) {
-    m.expert = (int)ctiles.div((uint32_t)b);
-    m.col0 = (b - m.expert * (int)ctiles.d) * a.bn;
+    const int p = (int)ctiles.div((uint32_t)b);
+    m.expert = g.first[p];
+    m.col0 = (b - p * (int)ctiles.d) * a.bn;
     m.rows = min(a.bn, a.cols - m.col0);
     m.slot0 = g.off[m.expert];
     m.depth = g.off[m.expert + 1] - m.slot0;
@@ -201,7 +214,7 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
   const uint32_t bar0 = smem_u32(&B.wfull[0]);
   MxRing r;
   int it = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64, halves = et_halves<MT>(a, m), c0 = m.tile * high;
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
@@ -271,7 +284,7 @@ __device__ int et_rows_tma(const EtArgs& a, const EtGroups& g, EtWalk k, int uni
   const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - kEtEpiWarps;
   auto source = [&](int route) { return a.per_route ? route : (int)topk.div((uint32_t)route); };
   uint32_t st;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64;
     if constexpr (MODE == kExGradW) {
@@ -339,7 +352,7 @@ __device__ void et_rows_copy(const EtArgs& a, const EtGroups& g, EtWalk k, int u
   const uint32_t at = (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
   uint32_t st;
   bool ok = true;
-  for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+  for (int round = 0, u; ok && (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64, k0 = m.col0 + chunk * 8, groups = (m.rows + 63) / 64;
     int route[kSweeps];
@@ -381,7 +394,7 @@ __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
   const bool lead = mx_elect();
   MxRing r, rw;
   int it = 0, nu = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64;
     if (stages == 0) continue;
@@ -477,7 +490,7 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
   O* out = static_cast<O*>(a.out);
   constexpr int kStep = kEtEpiWarps / 4 * 32, kPieces = 256 / kStep;  // a warp's pieces of 32 columns
   int nu = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     int row[kPieces] = {};
     if (MODE != kExGradW) {
@@ -606,6 +619,23 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (MODE == kExGradW) {
+    int count[8], most = 0;  // of experts lane + 32 i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) count[i] = lane + 32 * i < a.E ? groups.off[lane + 32 * i + 1] - groups.off[lane + 32 * i] : -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, count[i]);
+    const bool uneven = __reduce_max_sync(0xFFFFFFFFu, most) > 2 * (a.R / a.E) + 64;  // (64: a stage)
+    if (threadIdx.x == 0) groups.uneven = uneven;
+    for (int e = warp; e < a.E; e += kEtThreads / 32) {
+      const int n = groups.off[e + 1] - groups.off[e];
+      int before = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) before += count[i] > n || (count[i] == n && lane + 32 * i < e);
+      before = __reduce_add_sync(0xFFFFFFFFu, before);
+      if (lane == 0) groups.first[uneven ? before : e] = e;
+    }
+  }
   if (MODE != kExGradW && warp == 0) {  // blocks before each group
     int run = 0;
     for (int e0 = 0; e0 <= a.E; e0 += 32) {
