@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
 
 // ------------------------------------------------------------------- one pass
 template <typename T, int NT, int W, int EPT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 3 : NT == 128 ? 6 : 20) k_tl_once(const TlArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 4 : NT == 128 ? 8 : 20) k_tl_once(const TlArgs a) {
   constexpr int N = TlWord<T>::kN, TW = NT * W, NW = NT / 32, kPart = 8;  // words of a thread taken at once
   extern __shared__ uint4 tl_buf[];  // one tile
   __shared__ __align__(16) float4 s_part[kTlCtas * NW];
@@ -1276,7 +1276,9 @@ cudaError_t tl_once_launch(TlArgs a, int ctas, cudaStream_t st) {
   const cudaError_t e = tl_allow(done, kern, smem);
   if (e != cudaSuccess) return e;
   tl_shape(a, (int)sizeof(T), ctas, NT * W);
-  return tl_launch(kern, (long)a.T * ctas, ctas, NT, smem, a, st);
+  // (no more than the segment has: up to four CTAs share an SM, not three. 4096 rows of
+  // 20000: 90.5 -> 80 us, of 50021: 200 -> 182, of 131072, which fill it: 412 and 415)
+  return tl_launch(kern, (long)a.T * ctas, ctas, NT, std::min(smem, a.seg * 16), a, st);
 }
 
 cudaError_t tl_once(const TlArgs& a, int dtype, cudaStream_t st) {
