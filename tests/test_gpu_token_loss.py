@@ -154,6 +154,14 @@ def test_number_of_alternatives(binding, top):
     check_logprobs(binding, l, rng.integers(0, 5003, 4), top, 1.5)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V,top,dtype", [(32, 32, "bf16"), (450, 20, "f32"), (1804, 20, "f16"), (1804, 21, "f16"), (2040, 32, "bf16")])
+def test_many_alternatives_of_short_rows(binding, kind, V, top, dtype):
+    rng = np.random.default_rng(V + top)
+    l = make_logits(rng, 9, V, dtype, 1.0, kind)
+    check_logprobs(binding, l, rng.integers(0, V, 9), top, 1.0)
+
+
 @pytest.mark.parametrize("T", [63, 700])
 def test_many_rows(binding, T):
     rng = np.random.default_rng(T)

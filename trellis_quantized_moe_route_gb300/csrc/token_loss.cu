@@ -1249,7 +1249,9 @@ cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
 // Rows of up to 4 KB take a warp each (16384 x 1000 bf16: forward 34 us, with 128
 // threads 56; x 2048: 37 and 56; x 4096 would be 54 and 56, but 101 and 82 with the
 // five largest, and 90 and 74 for the distillation).
-bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256; }
+// Of more than 20 largest a warp's 32 groups give no useful bound (16384 x 1000, 20
+// largest: 134 us, with 128 threads 131; 32 largest: 316 and 176).
+bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256 && a.top <= 20; }
 
 // Few rows take a cluster of large CTAs each, so that they still fill the SMs; the
 // others a CTA of 128 threads, six of which share an SM.
