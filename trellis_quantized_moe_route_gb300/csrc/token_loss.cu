@@ -13,9 +13,9 @@
 //     memory between the sums and the gradient. Rows that are longer than that go
 //     through it in tiles twice.
 //   k_tl_backward: one CTA for each piece of a row.
-// 4096 x 131072 bf16 (1.07 GB): log probabilities 174 us = 6.2 TB/s (five largest
-// 180, twenty 236), distillation forward 174, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
-// loss and gradient in one pass 398 = 5.4. 8 rows: 6.4 us, with twenty largest 10.5.
+// 4096 x 131072 bf16 (1.07 GB): log probabilities 157 us = 6.8 TB/s (five largest
+// 182, twenty 237), distillation forward 174, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
+// loss and gradient in one pass 398 to 412 = 5.4 to 5.2. 8 rows: 6.3 us, with twenty largest 10.6.
 #include <algorithm>
 #include <cmath>
 
@@ -498,6 +498,76 @@ __device__ __forceinline__ void tl_put(TlTop<NT>& to, uint32_t order, int i) {
   if (at < TlTop<NT>::kRoom) to.cand[at] = tl_key(order, i);
 }
 
+// A tile's elements that reach `least`, the n words of which a warp's lanes have NT
+// apart, `first` the index of the first: lane by lane of the `hits` that have some, by
+// the whole warp, a lane's 32 4-byte words at once (some 40 instructions a hit) ...
+constexpr int kTlFewHits = 4;
+template <typename T, int NT>
+__device__ __forceinline__ void tl_collect_warp(TlTop<NT>& to, uint32_t hits, const uint4* tile, int n, uint32_t least, int first) {
+  constexpr int N = TlWord<T>::kN;
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (uint32_t hit = hits; hit; hit &= hit - 1) {
+    const int src = (tid & ~31) + __ffs(hit) - 1, i = (lane >> 2) * NT + src;
+    uint32_t k0 = 0, k1 = 0;  // orders of the lane's one or two elements
+    if (i < n) {
+      const uint32_t v = reinterpret_cast<const uint32_t*>(tile + i)[lane & 3];
+      if constexpr (sizeof(T) == 4) {
+        k0 = tl_order(__uint_as_float(v));
+      } else {
+        const T* h = reinterpret_cast<const T*>(&v);
+        k0 = tl_order(to_f32(h[0])), k1 = tl_order(to_f32(h[1]));
+      }
+    }
+    const bool one = k0 >= least, two = k1 >= least;
+    const uint32_t b1 = __ballot_sync(0xFFFFFFFFu, one), b2 = __ballot_sync(0xFFFFFFFFu, two);
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&to.n, __popc(b1) + __popc(b2));
+    at = __shfl_sync(0xFFFFFFFFu, at, 0);
+    const uint32_t before = (1u << lane) - 1;
+    const int x = first + i * N + (lane & 3) * (4 / (int)sizeof(T));
+    const int p1 = at + __popc(b1 & before), p2 = at + __popc(b1) + __popc(b2 & before);
+    if (one && p1 < TlTop<NT>::kRoom) to.cand[p1] = tl_key(k0, x);
+    if (two && p2 < TlTop<NT>::kRoom) to.cand[p2] = tl_key(k1, x + 1);
+  }
+}
+
+// ... or, where most lanes have some, each lane its own words, of which it looks into those whose maximum does.
+template <typename T, int NT, int W>
+__device__ __noinline__ void tl_collect_lanes(TlTop<NT>& to, const uint4* tile, int n, uint32_t least, int first) {
+  constexpr int N = TlWord<T>::kN;
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t words = 0;  // bits of those
+#pragma unroll
+  for (int u = 0; u < W; ++u)
+    if (u * NT + tid < n) words |= (uint32_t)(tl_order(tl_word_max(TlWord<T>{tile[u * NT + tid]})) >= least) << u;
+  while (__any_sync(0xFFFFFFFFu, words != 0)) {
+    const int i = (__ffs(words) - 1) * NT + tid;
+    uint32_t k[N], some = 0;
+    if (words) {
+      float v[N];
+      TlWord<T>{tile[i]}.to(v);
+#pragma unroll
+      for (int x = 0; x < N; ++x) some |= (uint32_t)((k[x] = tl_order(v[x])) >= least) << x;
+    }
+    words &= words - 1;
+    int incl = __popc(some);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int at = 0;
+    if (lane == 31) at = atomicAdd(&to.n, incl);
+    at = __shfl_sync(0xFFFFFFFFu, at, 31) + incl - __popc(some);
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+      if (some >> x & 1) {
+        if (at < TlTop<NT>::kRoom) to.cand[at] = tl_key(k[x], first + i * N + x);
+        ++at;
+      }
+  }
+}
+
 // to.list: the largest of the n candidates. Needs a barrier before and after.
 template <int NT>
 __device__ __forceinline__ void tl_rank(TlTop<NT>& to, int n, int top) {
@@ -775,18 +845,22 @@ __device__ __forceinline__ TlPart tl_merge_parts(const float4* parts, int n, con
 
 // ------------------------------------------------------------------- forward
 // CLUSTER: a row for each cluster; else a row for each CTA, and the next after it.
-template <typename T, int NT, int EPT, bool CLUSTER, bool LOGPROBS>
+// KIND: distillation, log probabilities, or those and the largest (one kernel for the
+// latter two took 170 us for 4096 x 131072 without any, not 157).
+enum { kTlDistill = 0, kTlLogprobs = 1, kTlLargest = 2 };
+template <typename T, int NT, int EPT, bool CLUSTER, int KIND>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_forward(const TlArgs a) {
   constexpr int N = TlWord<T>::kN, W = kTlWords, TW = NT * W, NW = NT / 32;
   extern __shared__ uint4 tl_buf[];  // two tiles
   __shared__ __align__(16) float4 s_part[2][CLUSTER ? kTlCtas * NW : NW];
-  __shared__ unsigned long long s_lists[LOGPROBS && CLUSTER ? kTlCtas * kTlMaxTop : 1];
-  __shared__ typename std::conditional<LOGPROBS, TlTop<NT>, TlTeacherWarps>::type sh[LOGPROBS ? 1 : 2];
+  constexpr bool LOGPROBS = KIND != kTlDistill, TOP = KIND == kTlLargest;
+  __shared__ unsigned long long s_lists[TOP && CLUSTER ? kTlCtas * kTlMaxTop : 1];
+  __shared__ typename std::conditional<TOP, TlTop<NT>, TlTeacherWarps>::type sh[LOGPROBS ? 1 : 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)(blockIdx.x % a.ctas) : 0;
   const long step = gridDim.x / ctas;
   const TlScale c = a.c;
-  if constexpr (LOGPROBS) {
+  if constexpr (TOP) {
     for (int i = tid; i < 64; i += NT) sh[0].group[i] = 0;
     if (tid == 0) sh[0].n = 0;
     __syncthreads();
@@ -871,42 +945,21 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
       buf ^= 1;
       const bool here = single >= 0 && p == 0;
       const float m = tl_take<T, NT, W, LOGPROBS>(part, tile, n, here ? x1 : -INFINITY, c);
-      if constexpr (LOGPROBS) {
-        if (a.top) {
-          TlTop<NT>& to = sh[0];
-          const uint32_t o = tid < n || here ? tl_order(m) : 0u;
-          if (o > most) atomicMax(&to.group[tid & 63], most = o);
-          if (p == 0) __syncthreads();
-          // (later, with whatever the other warps have found so far: any bound of this row's will do)
-          if ((p & (p - 1)) == 0) bound = tl_kth(to.group, a.top);
-          const uint32_t least = max(bound, kTlOrderNone + 1);
-          // lane by lane of those that have something, by the whole warp: a lane's 32 4-byte words
-          for (uint32_t hit = __ballot_sync(0xFFFFFFFFu, o >= least); hit; hit &= hit - 1) {
-            const int src = (tid & ~31) + __ffs(hit) - 1, i = (lane >> 2) * NT + src;
-            uint32_t k0 = 0, k1 = 0;  // orders of the lane's one or two elements
-            if (i < n) {
-              const uint32_t v = reinterpret_cast<const uint32_t*>(tile + i)[lane & 3];
-              if constexpr (sizeof(T) == 4) {
-                k0 = tl_order(__uint_as_float(v));
-              } else {
-                const T* h = reinterpret_cast<const T*>(&v);
-                k0 = tl_order(to_f32(h[0])), k1 = tl_order(to_f32(h[1]));
-              }
-            }
-            const bool one = k0 >= least, two = k1 >= least;
-            const uint32_t b1 = __ballot_sync(0xFFFFFFFFu, one), b2 = __ballot_sync(0xFFFFFFFFu, two);
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&to.n, __popc(b1) + __popc(b2));
-            at = __shfl_sync(0xFFFFFFFFu, at, 0);
-            const uint32_t before = (1u << lane) - 1;
-            const int x = row.head + (w0 + i) * N + (lane & 3) * (4 / (int)sizeof(T));
-            const int p1 = at + __popc(b1 & before), p2 = at + __popc(b1) + __popc(b2 & before);
-            if (one && p1 < TlTop<NT>::kRoom) to.cand[p1] = tl_key(k0, x);
-            if (two && p2 < TlTop<NT>::kRoom) to.cand[p2] = tl_key(k1, x + 1);
-          }
-          if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
-          __syncwarp();
-        }
+      if constexpr (TOP) {
+        TlTop<NT>& to = sh[0];
+        const uint32_t o = tid < n || here ? tl_order(m) : 0u;
+        if (o > most) atomicMax(&to.group[tid & 63], most = o);
+        if (p == 0) __syncthreads();
+        // (later, with whatever the other warps have found so far: any bound of this row's will do)
+        if ((p & (p - 1)) == 0) bound = tl_kth(to.group, a.top);
+        const uint32_t least = max(bound, kTlOrderNone + 1);
+        const uint32_t hits = __ballot_sync(0xFFFFFFFFu, o >= least);
+        if (__popc(hits) > kTlFewHits)
+          tl_collect_lanes<T, NT, W>(to, tile, n, least, row.head + w0 * N);
+        else
+          tl_collect_warp<T, NT>(to, hits, tile, n, least, row.head + w0 * N);
+        if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
+        __syncwarp();
       }
     }
     ahead(t + step);
@@ -917,15 +970,13 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
       else
         s_part[parity][warp] = make_float4(part.m, part.s, part.d, 0.0f);
     }
-    if constexpr (LOGPROBS) {
-      if (a.top) {
-        const int w0 = rank * a.seg, wn = max(0, min(row.words, w0 + a.seg) - w0);
-        tl_top_finish<T, NT>(sh[0], a.top, row, w0, wn, single, x1);
-        if (CLUSTER) {
-          if (tid < a.top)
-            asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(tl_map(&s_lists[rank * a.top + tid], 0)), "l"(sh[0].list[tid])
-                         : "memory");
-        }
+    if constexpr (TOP) {
+      const int w0 = rank * a.seg, wn = max(0, min(row.words, w0 + a.seg) - w0);
+      tl_top_finish<T, NT>(sh[0], a.top, row, w0, wn, single, x1);
+      if (CLUSTER) {
+        if (tid < a.top)
+          asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(tl_map(&s_lists[rank * a.top + tid], 0)), "l"(sh[0].list[tid])
+                       : "memory");
       }
     }
     tl_meet<CLUSTER>();
@@ -944,7 +995,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
           a.stats[2 * t] = M;
           a.stats[2 * t + 1] = lns;
         }
-        if (a.top) {
+        if constexpr (TOP) {
           auto store = [&](int r, unsigned long long k) {
             a.top_ids[t * a.top + r] = (int)~(uint32_t)k;
             a.top_logprobs[t * a.top + r] = logp(tl_value_of((uint32_t)(k >> 32)));
@@ -1235,9 +1286,9 @@ cudaError_t tl_allow(OncePerDevice& done, void (*kern)(P...), int smem) {
   });
 }
 
-template <typename T, int NT, int EPT, bool CLUSTER, bool LOGPROBS>
+template <typename T, int NT, int EPT, bool CLUSTER, int KIND>
 cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
-  auto kern = k_tl_forward<T, NT, EPT, CLUSTER, LOGPROBS>;
+  auto kern = k_tl_forward<T, NT, EPT, CLUSTER, KIND>;
   constexpr int smem = 2 * NT * kTlWords * 16, resident = NT == 256 ? 2 : NT == 128 ? 6 : 18;
   static OncePerDevice done;
   const cudaError_t e = tl_allow(done, kern, smem);
@@ -1249,23 +1300,23 @@ cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
 // Rows of up to 4 KB take a warp each (16384 x 1000 bf16: forward 34 us, with 128
 // threads 56; x 2048: 37 and 56; x 4096 would be 54 and 56, but 101 and 82 with the
 // five largest, and 90 and 74 for the distillation).
-// Of more than 20 largest a warp's 32 groups give no useful bound (16384 x 1000, 20
-// largest: 134 us, with 128 threads 131; 32 largest: 316 and 176).
-bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256 && a.top <= 20; }
+// Of more than 24 largest a warp's 32 groups give no useful bound (16384 x 1000, 24
+// largest: 117 us, with 128 threads 123; 32 largest: 249 and 139).
+bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256 && a.top <= 24; }
 
 // Few rows take a cluster of large CTAs each, so that they still fill the SMs; the
 // others a CTA of 128 threads, six of which share an SM.
-template <bool LOGPROBS>
+template <int KIND>
 cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
   auto go = [&](auto elem) {
     using T = decltype(elem);
     const long words = tl_words(a, (int)sizeof(T));
     if (tl_short(a, words))
-      return tl_forward_launch<T, 32, 2, false, LOGPROBS>(a, 1, st);
+      return tl_forward_launch<T, 32, 2, false, KIND>(a, 1, st);
     int ctas = 1;
     while (ctas < kTlCtas && (long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512) ctas *= 2;
-    if (ctas > 1) return tl_forward_launch<T, 256, 1, true, LOGPROBS>(a, ctas, st);
-    return tl_forward_launch<T, 128, 2, false, LOGPROBS>(a, 1, st);
+    if (ctas > 1) return tl_forward_launch<T, 256, 1, true, KIND>(a, ctas, st);
+    return tl_forward_launch<T, 128, 2, false, KIND>(a, 1, st);
   };
   return TM_BY_DTYPE(dtype, go);
 }
@@ -1401,7 +1452,8 @@ tm_status trellis_moe_token_logprobs(const void* logits, int32_t dtype, int64_t 
   tl_temperature(a, temperature);
   a.targets = targets, a.target64 = target_bytes == 8, a.top = top;
   a.logprob = logprob, a.entropy = entropy, a.stats = stats, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
-  const cudaError_t e = tl_forward<true>(a, dtype, (cudaStream_t)stream);
+  const cudaError_t e = top > 0 ? tl_forward<kTlLargest>(a, dtype, (cudaStream_t)stream)
+                                : tl_forward<kTlLogprobs>(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "token log probabilities");
 }
 
@@ -1441,7 +1493,7 @@ tm_status trellis_moe_distill_forward(const void* logits, int32_t dtype, int64_t
   if (T > 0 && (!loss || !stats)) return status_fail(TM_EINVAL, "loss and stats must be non-NULL");
   if (T == 0) return TM_OK;
   a.loss = loss, a.stats = stats;
-  const cudaError_t e = tl_forward<false>(a, dtype, (cudaStream_t)stream);
+  const cudaError_t e = tl_forward<kTlDistill>(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "distillation");
 }
 
