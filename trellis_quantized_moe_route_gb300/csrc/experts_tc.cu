@@ -17,12 +17,12 @@
 //
 // Measured on one GB300, us (floor: each operand once at the memory's copy rate):
 //   160 experts 1536 -> 5120, 32768 routes   forward 476, dx 461, dW 655 (434 each). The
-//     products run at the memory's rate but for a last round of units (5%) and, in
-//     dW, for tiles that are drained and then filled in turn: an SM writes one in 2.7
-//     to 3.1 us (26 bytes a cycle, also where dW stays in L2), each 64 routes add 0.63
-//     (the MMAs alone 0.54), and two accumulators of 256 x 256 do not fit tensor memory.
-//     128 x 256 with two of them is slower (876): rows come from L2 at 42 bytes a cycle
-//     and SM, by TMA or cp.async or both, and those tiles need half as many again.
+//     products run at the memory's rate but for a last round of units (5%). dW is bound by
+//     what an SM exchanges with L2: for a tile of 256 x 256 and its 205 routes, 205 KB
+//     come at 42 bytes a cycle (by TMA or cp.async or both) and 131 KB leave at 26
+//     (also where dW stays in L2), some 5 us in all, and the two add up: half a tile
+//     filled while the other half is drained takes 667. Tiles of 128 x 256 need half as many rows
+//     again (876).
 //   128 experts 1024 -> 1024, 16384 routes, uneven   66, 88 with the tokens' sums, 82 (45)
 //   64 experts 2560 -> 640, 5120 routes   46, 67 with the sums, 53 (32)
 //   8 tokens x 8 of 128 experts, 1024 -> 1024   23 (bytes 15)
