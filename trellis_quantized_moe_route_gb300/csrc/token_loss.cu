@@ -14,7 +14,7 @@
 //     through it in tiles twice.
 //   k_tl_backward: one CTA for each piece of a row.
 // 4096 x 131072 bf16 (1.07 GB): log probabilities 157 us = 6.8 TB/s (five largest
-// 182, twenty 237), distillation forward 174, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
+// 182, twenty 237), distillation forward 171, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
 // loss and gradient in one pass 398 to 412 = 5.4 to 5.2. 8 rows: 6.3 us, with twenty largest 10.6.
 #include <algorithm>
 #include <cmath>
@@ -904,6 +904,19 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
 
   long t = blockIdx.x / ctas;
   int buf = 0, parity = 0;
+  // distillation: the warps' terms of a row are added up behind the next row's barrier, or after
+  // the last one (with a barrier for each row's, 4096 x 131072 took 173 us)
+  long open = -1;
+  auto close = [&]() {
+    if constexpr (!LOGPROBS) {
+      if (tid == 0 && open >= 0) {
+        float loss = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) loss += sh[parity ^ 1].loss[w];
+        a.loss[open] = loss;
+      }
+    }
+  };
   fetch(t, 0, 0);
   ahead(t);
   if (CLUSTER) tl_wait();  // (the first CTA runs: its shared memory may be written)
@@ -980,6 +993,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
       }
     }
     tl_meet<CLUSTER>();
+    close();
     if (rank == 0) {
       const TlPart all = tl_merge_parts(s_part[parity], ctas * NW, c);
       const bool none = all.m == -INFINITY;
@@ -1024,18 +1038,18 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
           }
         term = tl_warp_sum(term);
         if (lane == 0) sh[parity].loss[warp] = term;
-        __syncthreads();
+        open = t;
         if (tid == 0) {
-          float loss = 0.0f;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) loss += sh[parity].loss[w];
-          a.loss[t] = loss;
           float* st = a.stats + t * kTlStats;
           st[0] = M, st[1] = lns, st[2] = k.m, st[3] = k.s, st[4] = k.Q;
         }
       }
     }
     parity ^= 1;
+  }
+  if (!LOGPROBS && open >= 0) {
+    __syncthreads();
+    close();
   }
   tl_copy_wait<0>();
 }
