@@ -40,8 +40,8 @@ EXPORTED = [
     "trellis_moe_mxfp4_quantize", "trellis_moe_mxfp4_dequantize", "trellis_moe_mxfp4_prepare",
     "trellis_moe_mxfp4_workspace_size", "trellis_moe_mxfp4_forward", "trellis_moe_mxfp4_forward_experts",
     "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_set_wait_test", "trellis_moe_mxfp4_destroy",
-    "trellis_moe_expert_plan", "trellis_moe_experts_align", "trellis_moe_experts_forward", "trellis_moe_experts_grad_x_workspace_size",
-    "trellis_moe_experts_grad_x", "trellis_moe_experts_grad_w",
+    "trellis_moe_expert_plan", "trellis_moe_experts_align", "trellis_moe_experts_forward",
+    "trellis_moe_experts_grad_x_workspace_size", "trellis_moe_experts_grad_x", "trellis_moe_experts_grad_w",
     "trellis_moe_token_logprobs", "trellis_moe_token_logprobs_backward",
     "trellis_moe_distill_forward", "trellis_moe_distill_backward", "trellis_moe_distill_loss_grad",
 ]
@@ -1047,7 +1047,8 @@ def experts_forward(x, w, plan: ExpertPlan, per_route: bool = False, out=None, o
             raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
         out_code = _dtype_code(_on_device("out", out, plan.index, None, (R, N)).dtype)
     xp, ldx, _, _, wp, ldw, lde, _copies = _experts_align(lib, plan, N, K, (x, ldx), None, (w, ldw, lde))
-    _launch(lib.trellis_moe_experts_forward, plan.index, xp, code, ldx, 1 if per_route else 0, wp, ldw, lde, plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, out.data_ptr(), out_code, plan.flags_ptr)
+    _launch(lib.trellis_moe_experts_forward, plan.index, xp, code, ldx, 1 if per_route else 0, wp, ldw, lde, plan.order_ptr,
+            plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, out.data_ptr(), out_code, plan.flags_ptr)
     return out
 
 
@@ -1056,7 +1057,7 @@ def experts_backward(x, w, plan: ExpertPlan, grad_out, per_route: bool = False, 
     """(grad_x of x's shape, grad_w of w's shape, both contiguous) of
     experts_forward from grad_out [T * topk, N] of x's type; None where not
     wanted. grad_w is of grad_w_dtype (default w's; float32 for sums over
-    several batches)."""
+    several batches). Copies are made as in the forward call, once for both."""
     if stream is not None:
         with _given(stream, "x", x):
             return experts_backward(x, w, plan, grad_out, per_route, want_x, want_w, grad_w_dtype)
