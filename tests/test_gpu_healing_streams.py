@@ -117,3 +117,38 @@ def test_calls_from_threads_at_once(binding):
     for t in threads:
         t.join()
     assert not bad
+
+
+def test_aligned_copies_on_streams_and_in_graphs(binding):
+    """Rows that are copied first: on four threads' streams at once, and in a graph whose weights change between replays."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, E, k, N, K = 200, 6, 2, 77, 333
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda").int()
+    x, w, dy = (torch.randn(s, generator=g, device="cuda").half() for s in ((T, K), (E, N, K), (T * k, N)))
+
+    def run(stream=None):
+        plan = binding.expert_plan(ids, E, stream=stream)
+        return (binding.experts_forward(x, w, plan, stream=stream), *binding.experts_backward(x, w, plan, dy, stream=stream))
+
+    want = run()
+    torch.cuda.synchronize()
+    got = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            out = run(s)
+            s.synchronize()
+            got.append(all(torch.equal(a, b) for a, b in zip(out, want)))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(got) == 80 and all(got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for scale in (1.0, 0.5, 2.0):
+        w.mul_(scale)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, run()))
