@@ -224,23 +224,27 @@ struct TlRow {
 // exp2 arguments of elements relative to a reference near their maximum m: with
 // c = log2(e) / tau and the whole number w nearest to m c, d = x c - w is one fused
 // operation with one rounding, and what belongs to different references differs by
-// an exact power of two. Where m c is so large that d would not stay small (`far`), elements are
-// either the maximum itself or so far below it that they do not count.
+// an exact power of two. BOTH: the same with c + lo, whose m lo, up to 128, belongs into w, or
+// the maximum's own 2^d would be 0 or infinite. |w| below 2^30 is at most 32 (half a step of
+// fp32 there) from the product, which is how large d gets at the maximum; beyond (`far`) the
+// next value below it is 64 or more away: elements are either the maximum or do not count.
+template <bool BOTH>
 struct TlRef {
   TlScale c;
   float m, w;
   bool far;
   __device__ __forceinline__ TlRef(float max, const TlScale& scale) : c(scale) {
     m = max == -INFINITY ? 0.0f : max;
-    w = rintf(m * scale.c);
+    w = rintf(BOTH ? fmaf(m, scale.c, m * scale.lo) : m * scale.c);
     far = !(fabsf(w) < 1073741824.0f);
   }
-  __device__ __forceinline__ float arg(float x) const { return far ? (x == m ? 0.0f : x < m ? -1000.0f : NAN) : fmaf(x, c.c, -w); }
-  // m c - w, which the reference is below m (BOTH: of c + lo)
-  template <bool BOTH = false>
-  __device__ __forceinline__ float above() const {
-    return far ? 0.0f : BOTH ? fmaf(m, c.lo, fmaf(m, c.c, -w)) : fmaf(m, c.c, -w);
+  __device__ __forceinline__ float near(float x) const {
+    const float d = fmaf(x, c.c, -w);
+    return BOTH ? fmaf(x, c.lo, d) : d;
   }
+  __device__ __forceinline__ float arg(float x) const { return far ? (x == m ? 0.0f : x < m ? -1000.0f : NAN) : near(x); }
+  // what the reference is below m
+  __device__ __forceinline__ float above() const { return far ? 0.0f : near(m); }
 };
 
 // Largest value, sum of exponentials relative to its reference and sum of those
@@ -248,8 +252,9 @@ struct TlRef {
 struct TlPart {
   float m, s, d;
   // to the reference of a larger maximum
+  template <bool BOTH>
   __device__ __forceinline__ void raise(float top, const TlScale& c) {
-    const TlRef a(m, c), b(top, c);
+    const TlRef<BOTH> a(m, c), b(top, c);
     const float u = m == top || m == -INFINITY ? 0.0f : fmaxf(a.far || b.far ? -1000.0f : a.w - b.w, -1000.0f);
     const float e = tl_ex2(u);
     d = e * fmaf(s, u, d);
@@ -259,9 +264,10 @@ struct TlPart {
 };
 
 // The parts of a warp's lanes (those of lanes past `n` are not looked at), the same for all lanes.
+template <bool BOTH>
 __device__ __forceinline__ TlPart tl_warp_merge(TlPart p, const TlScale& c) {
   const float top = tl_warp_max(p.m);
-  p.raise(top, c);
+  p.raise<BOTH>(top, c);
   p.s = tl_warp_sum(p.s);
   p.d = tl_warp_sum(p.d);
   return p;
@@ -273,7 +279,7 @@ template <bool BOTH>
 __device__ __forceinline__ float tl_log_sum(const TlPart& p, const TlScale& c) {
   if (p.m == -INFINITY) return -INFINITY;
   if (p.m != p.m || p.m == INFINITY) return NAN;
-  return logf(p.s) - TlRef(p.m, c).above<BOTH>() * kLn2;
+  return logf(p.s) - TlRef<BOTH>(p.m, c).above() * kLn2;
 }
 
 // ------------------------------------------------------ the teacher's entries
@@ -418,14 +424,14 @@ __device__ __forceinline__ void tl_entry_grad(const TlTeacher& te, int count, fl
 // ------------------------------------------------------------- gradient pass
 // out = e (A + B d), e = 2^d: with B = 0 the multiple A of the probability.
 template <bool ENTROPY>
-__device__ __forceinline__ float tl_grad_value(float x, const TlRef& r, float A, float B) {
+__device__ __forceinline__ float tl_grad_value(float x, const TlRef<false>& r, float A, float B) {
   float d = r.arg(x);
   if (ENTROPY) d = fmaxf(d, -1000.0f);  // (0 times infinity)
   return tl_ex2(d) * (ENTROPY ? fmaf(B, d, A) : A);
 }
 
 template <typename T, bool ENTROPY>
-__device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool vec, const TlRef& r, float A, float B) {
+__device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool vec, const TlRef<false>& r, float A, float B) {
   constexpr int n = TlWord<T>::kN;
   TlWord<T> o;
   if (!r.far) {
@@ -458,7 +464,7 @@ __device__ __forceinline__ void tl_grad_word(const TlWord<T>& w, T* out, bool ve
 }
 
 // p = 2^d unit
-__device__ __forceinline__ float tl_unit(const TlRef& r, float log_sum) {
+__device__ __forceinline__ float tl_unit(const TlRef<false>& r, float log_sum) {
   return log_sum == -INFINITY ? 0.0f : expf(-log_sum) * tl_ex2(-r.above());
 }
 
@@ -755,7 +761,7 @@ __device__ __forceinline__ void tl_copy_wait() {
 template <typename T, int NT, int W, bool ENTROPY>
 __device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, float single, const TlScale& c) {
   constexpr int N = TlWord<T>::kN;
-  const TlRef r(p.m, c);
+  const TlRef<!ENTROPY> r(p.m, c);
   auto add = [&](float x) {
     const float d = fmaxf(r.arg(x), -1000.0f), e = tl_ex2(d);  // (not 0 times infinity; a NaN shows in the maximum)
     p.s += e;
@@ -772,6 +778,7 @@ __device__ __noinline__ TlPart tl_take_far(TlPart p, const uint4* tile, int n, f
   return p;
 }
 
+// (The distillation's sums, without ENTROPY, take c and lo, the others c.)
 // Takes W words (of which the thread has those below n, NT apart) and a single
 // element (-inf: none) into a thread's part; returns their maximum.
 template <typename T, int NT, int W, bool ENTROPY>
@@ -793,8 +800,8 @@ __device__ __forceinline__ float tl_take_words(TlPart& p, const uint4* tile, int
 #pragma unroll
   for (int u = 0; u < W; ++u) m = tl_max_nan(m, tl_word_max(w[u]));
   const float top = tl_max_nan(p.m, m);
-  if (!(top == p.m)) p.raise(top, c);
-  const TlRef r(p.m, c);
+  if (!(top == p.m)) p.raise<!ENTROPY>(top, c);
+  const TlRef<!ENTROPY> r(p.m, c);
   if (r.far) {
     p = tl_take_far<T, NT, W, ENTROPY>(p, tile, n, single, c);
     return m;
@@ -830,17 +837,18 @@ __device__ __forceinline__ float tl_take(TlPart& p, const uint4* tile, int n, fl
 }
 
 // The warps' parts of a row, by a warp: the same bits for every warp that merges them.
+template <bool BOTH>
 __device__ __forceinline__ TlPart tl_merge_parts(const float4* parts, int n, const TlScale& c) {
   TlPart p{-INFINITY, 0.0f, 0.0f};
   for (int i = threadIdx.x & 31; i < n; i += 32) {
     const float4 v = parts[i];
     TlPart x{v.x, v.y, v.z};
     const float top = tl_max_nan(p.m, x.m);
-    if (!(top == p.m)) p.raise(top, c);
-    if (!(top == x.m)) x.raise(top, c);
+    if (!(top == p.m)) p.raise<BOTH>(top, c);
+    if (!(top == x.m)) x.raise<BOTH>(top, c);
     p.s += x.s, p.d += x.d;
   }
-  return tl_warp_merge(p, c);
+  return tl_warp_merge<BOTH>(p, c);
 }
 
 // ------------------------------------------------------------------- forward
@@ -976,7 +984,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
       }
     }
     ahead(t + step);
-    part = tl_warp_merge(part, c);
+    part = tl_warp_merge<!LOGPROBS>(part, c);
     if (lane == 0) {
       if (CLUSTER)
         tl_push(&s_part[parity][rank * NW + warp], 0, part);
@@ -995,11 +1003,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
     tl_meet<CLUSTER>();
     close();
     if (rank == 0) {
-      const TlPart all = tl_merge_parts(s_part[parity], ctas * NW, c);
+      const TlPart all = tl_merge_parts<!LOGPROBS>(s_part[parity], ctas * NW, c);
       const bool none = all.m == -INFINITY;
       const float M = none ? 0.0f : all.m, raw = tl_log_sum<!LOGPROBS>(all, c);
       // the mean of ln 2 (x - M) c, by which the sum grows with c
-      const float mean = LOGPROBS && !none ? (all.d / all.s - TlRef(M, c).above()) * kLn2 : 0.0f;
+      const float mean = LOGPROBS && !none ? (all.d / all.s - TlRef<false>(M, c).above()) * kLn2 : 0.0f;
       const float lns = LOGPROBS && !none ? fmaf(c.rest, mean, raw) : raw;
       auto logp = [&](float x) { return none ? -INFINITY : c.div(x - M) - lns; };
       if constexpr (LOGPROBS) {
@@ -1127,14 +1135,14 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : NT == 128 ? 8 : 20) k_tl_o
     tl_copy_wait<0>();
     if (n > kPart * NT) tl_take<T, NT, kPart, false>(part, tl_buf + kPart * NT, n - kPart * NT, -INFINITY, c);
   }
-  part = tl_warp_merge(part, c);
+  part = tl_warp_merge<true>(part, c);
   if (a.ctas > 1) tl_wait();  // (all CTAs run: their shared memory may be written)
   if (lane < a.ctas) tl_push(&s_part[rank * NW + warp], lane, part);
   if (a.ctas > 1)
     tl_meet<true>();
   else
     tl_meet<false>();
-  const TlPart all = tl_merge_parts(s_part, a.ctas * NW, c);
+  const TlPart all = tl_merge_parts<true>(s_part, a.ctas * NW, c);
   const bool none = all.m == -INFINITY;
   const float M = none ? 0.0f : all.m, lns = tl_log_sum<true>(all, c);
   const TlTeacherSum k = tl_teacher_sum<NT>(a, t, te);
@@ -1151,7 +1159,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : NT == 128 ? 8 : 20) k_tl_o
     if (lane == 0) te.loss[warp] = term;
   }
   const float g = grad_loss * c.inv;
-  const TlRef ref(M, c);
+  const TlRef<false> ref(M, c);
   const float unit = tl_unit(ref, lns), A = g * k.Q * unit;
   for (int p = a.tiles - 1; p >= 0; --p) {  // (the last tile is still here)
     if (p < a.tiles - 1) {
@@ -1202,7 +1210,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 16) k_tl_backward(const Tl
   auto mine = [&](int i) { return tl_mine(row, rank, w0, w0 + NT * W, i, a.V); };
   const float* st = a.stats + t * (TEACHER ? kTlStats : 2);
   const float lns = masked ? 0.0f : st[1];
-  const TlRef ref(masked ? 0.0f : st[0], c);
+  const TlRef<false> ref(masked ? 0.0f : st[0], c);
   const float unit = masked ? 0.0f : tl_unit(ref, lns);
   float A = 0.0f, B = 0.0f, g = 0.0f, Q = 0.0f, xy = 0.0f;
   long y = -1;
