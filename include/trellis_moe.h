@@ -515,7 +515,8 @@ tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int3
  * [g_rows, N'] and w_to [E, N, K'], K' and N' being the next multiples of eight, each
  * 16-byte aligned, or NULL: none. Strides in elements of 16 bits, as below. Of w only
  * experts that have routes by the plan's offsets are copied. What lies behind a copy's
- * K or N elements of a row is left undefined, and no product reads it. */
+ * K or N elements of a row is left undefined, and no product reads it. The copies must
+ * not overlap what is copied, or one another (TM_EINVAL). */
 tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, const void* grad_out, int64_t ldg,
                                     int32_t g_rows, const void* w, int64_t ldw, int64_t lde, const int32_t* offsets, int32_t E,
                                     int32_t N, int32_t K, void* x_to, void* g_to, void* w_to, void* stream);
@@ -523,7 +524,9 @@ tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, 
 /* out [T * topk, N] in route order, of out_dtype; a route of no expert gives a
  * row of zeros. x: row s at x + s * ldx elements; w: row n of expert e at
  * w + e * lde + n * ldw elements. Rows of x, w and (below) grad_out begin on 16
- * bytes; results lie anywhere. T = 0 is a no-op. */
+ * bytes. A result of this and the next two, and the workspace, lies at any address
+ * of its type, but must not overlap what its product reads: rows of x, w or
+ * grad_out, or the plan (TM_EINVAL); rows may lie around it. T = 0 is a no-op. */
 tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx, int32_t per_route, const void* w,
                                       int64_t ldw, int64_t lde, const int32_t* order, const int32_t* offsets, int32_t T,
                                       int32_t topk, int32_t E, int32_t N, int32_t K, void* out, int32_t out_dtype,
@@ -532,7 +535,8 @@ tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx,
 /* grad_x [T, K] (per_route: [T * topk, K]), contiguous, of `dtype`, from
  * grad_out [T * topk, N] in route order, row r at grad_out + r * ldg elements.
  * A token's routes are summed in fp32, in order j, through the workspace
- * (16-byte aligned, contents ignored; size 0 with per_route: NULL will do). */
+ * (16-byte aligned, contents ignored; size 0 with per_route: NULL will do). Such a
+ * sum is written when the products are done: over grad_out if wanted. */
 size_t trellis_moe_experts_grad_x_workspace_size(int32_t T, int32_t topk, int32_t K, int32_t per_route);
 tm_status trellis_moe_experts_grad_x(const void* grad_out, int32_t dtype, int64_t ldg, int32_t per_route, const void* w,
                                      int64_t ldw, int64_t lde, const int32_t* order, const int32_t* offsets, int32_t T,

@@ -1027,9 +1027,10 @@ def _experts_align(lib, plan, N, K, x, g, w):
 def experts_forward(x, w, plan: ExpertPlan, per_route: bool = False, out=None, out_dtype=None, stream=None):
     """Rows [T * topk, N] in route order: the route's expert's w [E, N, K] times
     row t of x [T, K] (per_route: row r of x [T * topk, K]), bfloat16 or
-    float16, of out_dtype (default x's). Of inputs whose rows do not begin on 16
-    bytes (K no multiple of eight, say) it makes copies first, of w for each call:
-    weights that are padded, w[:, :, :K] of a wider tensor, save that."""
+    float16, of out_dtype (default x's). out must not overlap x, w or the plan.
+    Of inputs whose rows do not begin on 16 bytes (K no multiple of eight, say)
+    it makes copies first, of w for each call: weights that are padded,
+    w[:, :, :K] of a wider tensor, save that."""
     if stream is not None:
         with _given(stream, "x", x):
             return experts_forward(x, w, plan, per_route, out, out_dtype)

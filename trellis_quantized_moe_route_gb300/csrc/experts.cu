@@ -328,6 +328,37 @@ tm_status ex_check(const ExArgs& a) {
   return TM_OK;
 }
 
+// Whether [lo, hi) touches any of E matrices, lde elements of 16 bits apart, of
+// `rows` rows of `cols` elements, ld apart. (It may lie between the rows.)
+bool ex_touch(uintptr_t lo, uintptr_t hi, const void* src, int64_t ld, int64_t lde, int E, int64_t rows, int64_t cols) {
+  const uintptr_t p = (uintptr_t)src, row = (uintptr_t)cols * 2, step = (uintptr_t)ld * 2;
+  if (!src || lo >= hi || p >= hi || p + ((uintptr_t)(E - 1) * lde + (uintptr_t)(rows - 1) * ld) * 2 + row <= lo) return false;
+  for (int e = 0; e < E; ++e) {
+    const uintptr_t q = p + (uintptr_t)e * lde * 2;
+    const uintptr_t r = lo < q + row ? 0 : (lo - q - row) / step + 1;  // the first row that ends behind lo
+    if (r < (uintptr_t)rows && q + r * step < hi) return true;
+  }
+  return false;
+}
+
+bool ex_meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return a_bytes && b_bytes && (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
+
+// A product's CTAs store rows while others still read theirs.
+tm_status ex_check_apart(const ExArgs& a) {
+  const int64_t R = (int64_t)a.T * a.topk, xrows = a.per_route ? R : a.T;
+  const size_t rows = a.mode == kExGradW ? (size_t)a.E * a.N : (size_t)R, cols = a.mode == kExForward ? a.N : a.K;
+  const size_t bytes = rows * cols * dtype_bytes(a.out_dtype);
+  const uintptr_t lo = (uintptr_t)a.out, hi = lo + bytes;
+  const bool meets = (a.mode != kExGradX && ex_touch(lo, hi, a.x, a.ldx, 0, 1, xrows, a.K)) ||
+                     (a.mode != kExForward && ex_touch(lo, hi, a.g, a.ldg, 0, 1, R, a.N)) ||
+                     (a.mode != kExGradW && ex_touch(lo, hi, a.w, a.ldw, a.lde, a.E, a.N, a.K)) ||
+                     ex_meet(a.out, bytes, a.order, (size_t)R * 4) || ex_meet(a.out, bytes, a.offsets, (size_t)(a.E + 1) * 4) ||
+                     ex_meet(a.out, bytes, a.flags, 4);
+  return meets ? status_fail(TM_EINVAL, "the result (or workspace) must not overlap x, w, grad_out or the plan") : TM_OK;
+}
+
 // One tensor of an aligned copy: E matrices of `rows` rows; false if it is too large.
 bool ex_align_job(ExAlignJob& j, const void* src, int64_t ld, int64_t lde, int E, int rows, int cols, void* dst) {
   const int words = (cols + 7) / 8;
@@ -353,6 +384,10 @@ tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int3
   if (R < 0 || R > (1 << 22)) return status_fail(TM_EUNSUPPORTED, "%d routes: outside 0..%d", R, 1 << 22);
   if (E < 1 || E > kExMaxExperts) return status_fail(TM_EUNSUPPORTED, "E=%d outside 1..%d", E, kExMaxExperts);
   if ((R > 0 && (!ids || !order)) || !offsets || !flags) return status_fail(TM_EINVAL, "ids, order, offsets and flags must be non-NULL");
+  const size_t rb = (size_t)R * 4, ob = (size_t)(E + 1) * 4;
+  if (ex_meet(ids, rb, order, rb) || ex_meet(ids, rb, offsets, ob) || ex_meet(ids, rb, flags, 4) || ex_meet(order, rb, offsets, ob) ||
+      ex_meet(order, rb, flags, 4) || ex_meet(offsets, ob, flags, 4))
+    return status_fail(TM_EINVAL, "ids, order, offsets and flags must not overlap");
   const cudaError_t e = launch_ex_plan(ids, R, E, order, offsets, flags, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert plan");
 }
@@ -378,6 +413,19 @@ tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, 
   const bool ok = (!x_to || ex_align_job(a.x, x, ldx, 0, 1, x_rows, K, x_to)) &&
                   (!g_to || ex_align_job(a.g, grad_out, ldg, 0, 1, g_rows, N, g_to)) &&
                   (!w_to || ex_align_job(a.w, w, ldw, lde, E, N, K, w_to));
+  const struct {
+    const void* p;
+    size_t bytes;
+  } to[3] = {{x_to, (size_t)a.x.total * 16}, {g_to, (size_t)a.g.total * 16}, {w_to, (size_t)a.w.total * 16 * E}};
+  bool meets = false;
+  for (int i = 0; ok && i < 3; ++i) {
+    if (!to[i].p) continue;
+    const uintptr_t lo = (uintptr_t)to[i].p, hi = lo + to[i].bytes;
+    meets = meets || (x_to && ex_touch(lo, hi, x, ldx, 0, 1, x_rows, K)) || (g_to && ex_touch(lo, hi, grad_out, ldg, 0, 1, g_rows, N)) ||
+            (w_to && (ex_touch(lo, hi, w, ldw, lde, E, N, K) || ex_meet(to[i].p, to[i].bytes, offsets, (size_t)(E + 1) * 4)));
+    for (int j = 0; j < i; ++j) meets = meets || (to[j].p && ex_meet(to[i].p, to[i].bytes, to[j].p, to[j].bytes));
+  }
+  if (meets) return status_fail(TM_EINVAL, "the copies must not overlap what is copied, or one another");
   if (!ok) return status_fail(TM_EUNSUPPORTED, "a matrix of 2^34 elements or more cannot be copied");
   const uint32_t most = std::max({a.x.total, a.g.total, a.w.total}), per = kAlignThreads * kAlignWords;
   const unsigned grid_y = (unsigned)(a.experts + (x_to != nullptr) + (g_to != nullptr));
@@ -395,8 +443,9 @@ tm_status trellis_moe_experts_forward(const void* x, int32_t dtype, int64_t ldx,
   a.mode = kExForward, a.dtype = dtype, a.out_dtype = out_dtype, a.T = T, a.topk = topk, a.E = E, a.N = N, a.K = K;
   a.per_route = per_route, a.x = x, a.ldx = ldx, a.w = w, a.ldw = ldw, a.lde = lde, a.order = order, a.offsets = offsets;
   a.out = out, a.flags = flags;
-  const tm_status s = ex_check(a);
+  tm_status s = ex_check(a);
   if (s != TM_OK || T == 0) return s;
+  if ((s = ex_check_apart(a)) != TM_OK) return s;
   const cudaError_t e = ex_product(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products");
 }
@@ -414,7 +463,7 @@ tm_status trellis_moe_experts_grad_x(const void* grad_out, int32_t dtype, int64_
   a.mode = kExGradX, a.dtype = dtype, a.out_dtype = per_route ? dtype : TM_F32, a.T = T, a.topk = topk, a.E = E, a.N = N, a.K = K;
   a.per_route = per_route, a.g = grad_out, a.ldg = ldg, a.w = w, a.ldw = ldw, a.lde = lde, a.order = order, a.offsets = offsets;
   a.out = per_route ? grad_x : workspace, a.flags = flags;
-  const tm_status s = ex_check(a);
+  tm_status s = ex_check(a);
   if (s != TM_OK || T == 0) return s;
   if (!per_route) {
     if (!grad_x || ((uintptr_t)grad_x) % 2) return status_fail(TM_EINVAL, "grad_x must be non-NULL and aligned to its elements");
@@ -422,7 +471,13 @@ tm_status trellis_moe_experts_grad_x(const void* grad_out, int32_t dtype, int64_
     if (workspace_bytes < trellis_moe_experts_grad_x_workspace_size(T, topk, K, per_route))
       return status_fail(TM_EWORKSPACE, "workspace of %zu bytes is too small", workspace_bytes);
     if ((long)T * ((K + 7) / 8) >= 1L << 31) return status_fail(TM_EUNSUPPORTED, "T=%d rows of K=%d are too many", T, K);
+    // (written when the products are done; the plan stays whole for the next one)
+    const size_t gb = (size_t)T * K * 2, rb = (size_t)T * topk * 4;
+    if (ex_meet(grad_x, gb, workspace, rb * K) || ex_meet(grad_x, gb, order, rb) || ex_meet(grad_x, gb, offsets, (size_t)(E + 1) * 4) ||
+        ex_meet(grad_x, gb, flags, 4))
+      return status_fail(TM_EINVAL, "grad_x must not overlap the workspace or the plan");
   }
+  if ((s = ex_check_apart(a)) != TM_OK) return s;
   cudaError_t e = ex_product(a, (cudaStream_t)stream);
   if (e == cudaSuccess && !per_route)
     e = launch_ex_sum(static_cast<const float*>(workspace), T, topk, K, grad_x, dtype, (cudaStream_t)stream);
@@ -438,7 +493,8 @@ tm_status trellis_moe_experts_grad_w(const void* x, int32_t dtype, int64_t ldx, 
   a.mode = kExGradW, a.dtype = dtype, a.out_dtype = grad_dtype, a.T = T, a.topk = topk, a.E = E, a.N = N, a.K = K;
   a.per_route = per_route, a.x = x, a.ldx = ldx, a.g = grad_out, a.ldg = ldg, a.order = order, a.offsets = offsets;
   a.out = grad_w, a.flags = flags;
-  const tm_status s = ex_check(a);
+  tm_status s = ex_check(a);
+  if (s == TM_OK && T > 0) s = ex_check_apart(a);
   if (s != TM_OK) return s;
   const cudaError_t e = ex_product(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products' gradient of w");
