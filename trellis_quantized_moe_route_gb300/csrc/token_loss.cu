@@ -9,6 +9,8 @@
 //     tiles, the next one fetched while it works on this one. A thread reads only
 //     words that it fetched itself (cp.async) and keeps its own maximum and sums, so
 //     that no barrier stands between tiles; the threads' sums meet at the row's end.
+//     (Words that may be among the largest are looked at by the whole warp, behind a
+//     __syncwarp.)
 //   k_tl_once: loss and gradient in one pass; a cluster holds the row in shared
 //     memory between the sums and the gradient. Rows that are longer than that go
 //     through it in tiles twice.
@@ -975,10 +977,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NT == 128 ? 6 : 18) k_tl_f
         if ((p & (p - 1)) == 0) bound = tl_kth(to.group, a.top);
         const uint32_t least = max(bound, kTlOrderNone + 1);
         const uint32_t hits = __ballot_sync(0xFFFFFFFFu, o >= least);
-        if (__popc(hits) > kTlFewHits)
+        if (__popc(hits) > kTlFewHits) {
           tl_collect_lanes<T, NT, W>(to, tile, n, least, row.head + w0 * N);
-        else
+        } else if (hits) {
+          __syncwarp();  // (each lane has waited for its own copies: now all may read them)
           tl_collect_warp<T, NT>(to, hits, tile, n, least, row.head + w0 * N);
+        }
         if (here && tl_order(x1) >= least) tl_put(to, tl_order(x1), single);
         __syncwarp();
       }
