@@ -172,13 +172,18 @@ struct ExAlignJob {
   int64_t ld, lde;     // elements between rows and between matrices
   FastDiv words;       // 16-byte words of a row of the copy
   uint32_t total;      // words of a matrix
+  uint32_t ctas;       // that copy a matrix
   int cols;
   uint4* dst;
 };
 
+// CTAs in a list: each expert's w's, then x's, then g's. (As many for each expert as
+// the largest tensor needs, 32768 rows and 160 experts, 2559 -> 641, were 1650000 CTAs, of which
+// 42000 had work: 1.86 ms for the forward call, 0.37 so.)
 struct ExAlignArgs {
-  ExAlignJob w, x, g;  // E matrices, one and one
-  int experts;         // E, 0 without w
+  ExAlignJob w, x, g;  // E matrices, one and one; those that are not copied: no CTAs
+  uint32_t w_ctas;     // of all experts
+  FastDiv per_expert;
   const int32_t* offsets;
 };
 
@@ -207,12 +212,21 @@ __device__ __forceinline__ uint4 align_load(const uint16_t* p, int n, uintptr_t 
 __global__ void __launch_bounds__(kAlignThreads) k_ex_align(const __grid_constant__ ExAlignArgs a) {
   grid_wait();
   grid_launch();
-  const int y = blockIdx.y, e = y < a.experts ? y : 0;
-  if (y < a.experts && a.offsets[e] == a.offsets[e + 1]) return;  // (nobody reads it)
-  const ExAlignJob& j = y < a.experts ? a.w : y == a.experts && a.x.total ? a.x : a.g;
+  uint32_t b = blockIdx.x, e = 0;
+  const bool w = b < a.w_ctas;
+  if (w) {
+    e = a.per_expert.div(b);
+    b -= e * a.per_expert.d;
+    if (a.offsets[e] == a.offsets[e + 1]) return;  // (nobody reads it)
+  } else {
+    b -= a.w_ctas;
+  }
+  const bool x = !w && b < a.x.ctas;
+  if (!w && !x) b -= a.x.ctas;
+  const ExAlignJob& j = w ? a.w : x ? a.x : a.g;
   const uint16_t* src = j.src + (size_t)e * j.lde;
   uint4* dst = j.dst + (size_t)e * j.total;
-  const uint32_t n0 = blockIdx.x * (kAlignThreads * kAlignWords) + threadIdx.x;
+  const uint32_t n0 = b * (kAlignThreads * kAlignWords) + threadIdx.x;
   uint4 q[kAlignWords];
 #pragma unroll
   for (int u = 0; u < kAlignWords; ++u) {
@@ -365,6 +379,7 @@ bool ex_align_job(ExAlignJob& j, const void* src, int64_t ld, int64_t lde, int E
   const long total = (long)rows * words;
   j.src = static_cast<const uint16_t*>(src), j.ld = ld, j.lde = lde, j.cols = cols, j.dst = static_cast<uint4*>(dst);
   j.words = FastDiv((uint32_t)words), j.total = (uint32_t)total;
+  j.ctas = (uint32_t)((total + kAlignThreads * kAlignWords - 1) / (kAlignThreads * kAlignWords));  // (below 2^21)
   j.lo = (uintptr_t)src;
   j.hi = (uintptr_t)(j.src + (int64_t)(E - 1) * lde + (int64_t)(rows - 1) * ld + cols);
   return total < 1L << 31;
@@ -409,7 +424,7 @@ tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, 
     if (((uintptr_t)q) % 2) return status_fail(TM_EINVAL, "x, w and grad_out must be aligned to their elements");
   for (const void* q : {x_to, g_to, w_to})
     if (((uintptr_t)q) % 16) return status_fail(TM_EINVAL, "the copies must be 16-byte aligned");
-  ExAlignArgs a{ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, w_to ? E : 0, offsets};
+  ExAlignArgs a{ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, ExAlignJob{.words = FastDiv(1)}, 0, FastDiv(1), offsets};
   const bool ok = (!x_to || ex_align_job(a.x, x, ldx, 0, 1, x_rows, K, x_to)) &&
                   (!g_to || ex_align_job(a.g, grad_out, ldg, 0, 1, g_rows, N, g_to)) &&
                   (!w_to || ex_align_job(a.w, w, ldw, lde, E, N, K, w_to));
@@ -427,10 +442,10 @@ tm_status trellis_moe_experts_align(const void* x, int64_t ldx, int32_t x_rows, 
   }
   if (meets) return status_fail(TM_EINVAL, "the copies must not overlap what is copied, or one another");
   if (!ok) return status_fail(TM_EUNSUPPORTED, "a matrix of 2^34 elements or more cannot be copied");
-  const uint32_t most = std::max({a.x.total, a.g.total, a.w.total}), per = kAlignThreads * kAlignWords;
-  const unsigned grid_y = (unsigned)(a.experts + (x_to != nullptr) + (g_to != nullptr));
-  if (grid_y == 0) return TM_OK;
-  const cudaError_t e = launch_after(k_ex_align, dim3((most + per - 1) / per, grid_y), kAlignThreads, 0, (cudaStream_t)stream, a);
+  if (w_to) a.w_ctas = a.w.ctas * (uint32_t)E, a.per_expert = FastDiv(a.w.ctas);
+  const uint32_t ctas = a.w_ctas + a.x.ctas + a.g.ctas;  // (below 2^30)
+  if (ctas == 0) return TM_OK;
+  const cudaError_t e = launch_after(k_ex_align, dim3(ctas), kAlignThreads, 0, (cudaStream_t)stream, a);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "aligned copies");
 }
 
