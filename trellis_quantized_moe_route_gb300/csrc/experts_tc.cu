@@ -693,32 +693,23 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
 
 // [E, N, K] in boxes of `width` elements (128 bytes, as all box starts are multiples of) by `box` rows.
 cudaError_t et_map3(CUtensorMap* m, int dtype, const void* p, const ExArgs& a, int64_t ldw, int64_t lde, int width, int box) {
-  const auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
+  const cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
   const cuuint64_t es = dtype_bytes(dtype);
-  cuuint64_t strides[2] = {(cuuint64_t)ldw * es, (cuuint64_t)(a.E > 1 ? lde : ldw) * es};
-  cuuint32_t boxes[3] = {(cuuint32_t)width, (cuuint32_t)box, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(m, dtype == TM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                            : dtype == TM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                         3, const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t strides[2] = {(cuuint64_t)ldw * es, (cuuint64_t)(a.E > 1 ? lde : ldw) * es};
+  const cuuint32_t boxes[3] = {(cuuint32_t)width, (cuuint32_t)box, 1};
+  return tensor_map_encode(m,
+                           dtype == TM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                           : dtype == TM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                           3, p, dims, strides, boxes);
 }
 
 cudaError_t et_map2(CUtensorMap* m, int dtype, const void* p, int cols, long rows, int64_t ld) {
-  const auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t boxes[2] = {64, 1};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                         const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t boxes[2] = {64, 1};
+  return tensor_map_encode(m, dtype == TM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, dims,
+                           strides, boxes);
 }
 
 template <int MODE, int MT, typename O>

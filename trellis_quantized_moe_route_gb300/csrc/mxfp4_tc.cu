@@ -346,17 +346,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) k_mx_tc(const __grid_constant__
 // starts are multiples of 128 bytes, rows of 16; what lies past a row or the
 // last row reads as 0.
 cudaError_t mx_code_map(CUtensorMap* m, const uint8_t* codes, long rows, int K, int box) {
-  const auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
   const cuuint64_t bytes = (cuuint64_t)mx_blocks(K) * 16;
-  cuuint64_t dims[2] = {bytes, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {bytes};
-  cuuint32_t boxes[2] = {128, (cuuint32_t)box};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, boxes, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {bytes};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box};
+  return tensor_map_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, boxes);
 }
 
 template <bool GATED, bool EXPERTS, typename T>

@@ -19,4 +19,24 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// A map with 128-byte swizzle; outside the tensor is 0. The encoder wants the device's context
+// current, which a thread's first runtime call makes it, and a thread whose first call this
+// is has none: it sets its device and encodes again.
+inline cudaError_t tensor_map_encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* p, const cuuint64_t* dims,
+                                     const cuuint64_t* strides, const cuuint32_t* boxes) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  auto go = [&] {
+    return enc(m, type, (cuuint32_t)rank, const_cast<void*>(p), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (go() == CUDA_SUCCESS) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return go() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace tmoe
