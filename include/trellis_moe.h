@@ -550,6 +550,15 @@ tm_status trellis_moe_experts_grad_w(const void* x, int32_t dtype, int64_t ldx, 
                                      int32_t E, int32_t N, int32_t K, void* grad_w, int32_t grad_dtype, uint32_t* flags,
                                      void* stream);
 
+/* Test hook, as trellis_moe_set_wait_test, for the products that the calling thread
+ * starts from now on: the limit of their pipeline waits (0: 2 s), and which of them
+ * waits for what never comes: none (stall 0), the MMA issuer before its first MMA (1),
+ * one epilogue warp for every accumulator (2), the first (3) or the last (4) of the
+ * warps that fetch rows, or the one that fetches weights (5; grad_w has none). Such a
+ * product gives up after the limit and some 0.5 s for its copies in flight, sets
+ * bit 1 of the error word and leaves its result undefined. */
+tm_status trellis_moe_experts_set_wait_test(uint64_t wait_limit_ns, int32_t stall);
+
 /* ------------------------------------------------------------------------
  * Log probabilities of given tokens. For a row l of V logits (row t at
  * logits + t * ld elements) and u = l / temperature:

@@ -42,6 +42,7 @@ EXPORTED = [
     "trellis_moe_mxfp4_poll_error", "trellis_moe_mxfp4_set_wait_test", "trellis_moe_mxfp4_destroy",
     "trellis_moe_expert_plan", "trellis_moe_experts_align", "trellis_moe_experts_forward",
     "trellis_moe_experts_grad_x_workspace_size", "trellis_moe_experts_grad_x", "trellis_moe_experts_grad_w",
+    "trellis_moe_experts_set_wait_test",
     "trellis_moe_token_logprobs", "trellis_moe_token_logprobs_backward",
     "trellis_moe_distill_forward", "trellis_moe_distill_backward", "trellis_moe_distill_loss_grad",
 ]
@@ -137,6 +138,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "trellis_moe_experts_grad_x_workspace_size": (SZ, [I32, I32, I32, I32]),
         "trellis_moe_experts_grad_x": (I32, [P, I32, I64, I32, P, I64, I64, P, P, I32, I32, I32, I32, I32, P, P, P, SZ, P]),
         "trellis_moe_experts_grad_w": (I32, [P, I32, I64, I32, P, I64, P, P, I32, I32, I32, I32, I32, P, I32, P, P]),
+        "trellis_moe_experts_set_wait_test": (I32, [ctypes.c_uint64, I32]),
         "trellis_moe_token_logprobs": (I32, [P, I32, I64, P, I32, I32, I32, F32, I32, P, P, P, P, P, P]),
         "trellis_moe_token_logprobs_backward": (I32, [P, I32, I64, P, I32, I32, I32, F32, P, P, P, P, P, I64, P]),
         "trellis_moe_distill_forward": (I32, distill + [P, P, P]),
@@ -1086,6 +1088,12 @@ def experts_backward(x, w, plan: ExpertPlan, grad_out, per_route: bool = False, 
         _launch(lib.trellis_moe_experts_grad_w, plan.index, xp, code, ldx, flag, gp, ldg,
                 plan.order_ptr, plan.offsets_ptr, plan.T, plan.topk, plan.E, N, K, gw.data_ptr(), gcode, plan.flags_ptr)
     return gx, gw
+
+
+def experts_set_wait_test(wait_limit_ns: int = 0, stall: int = 0):
+    """Test hook of the products that this thread starts from now on (see
+    trellis_moe_experts_set_wait_test); without arguments, back to normal."""
+    _check(_start().trellis_moe_experts_set_wait_test(wait_limit_ns, stall))
 
 
 class TokenLogprobs(NamedTuple):

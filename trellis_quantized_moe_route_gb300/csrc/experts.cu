@@ -304,7 +304,15 @@ cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, 
 
 namespace {
 
-cudaError_t ex_product(const ExArgs& a, cudaStream_t st) {
+// trellis_moe_experts_set_wait_test, by thread (there is no handle that could hold it).
+struct ExWaitTest {
+  uint64_t wait_ns;
+  int stall;
+};
+thread_local ExWaitTest ex_wait_test;
+
+cudaError_t ex_product(ExArgs a, cudaStream_t st) {
+  a.wait_ns = ex_wait_test.wait_ns, a.stall = ex_wait_test.stall;
   if (a.T == 0)  // (grad_w of no tokens)
     return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * dtype_bytes(a.out_dtype), st);
   int dev = 0, sms = 0;
@@ -513,6 +521,13 @@ tm_status trellis_moe_experts_grad_w(const void* x, int32_t dtype, int64_t ldx, 
   if (s != TM_OK) return s;
   const cudaError_t e = ex_product(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TM_OK : status_cuda(e, "expert products' gradient of w");
+}
+
+tm_status trellis_moe_experts_set_wait_test(uint64_t wait_limit_ns, int32_t stall) {
+  set_last_error("");
+  if (stall < 0 || stall > 5) return status_fail(TM_EINVAL, "stall=%d outside 0..5", stall);
+  ex_wait_test = {wait_limit_ns, stall};
+  return TM_OK;
 }
 
 }  // extern "C"

@@ -23,6 +23,8 @@ struct ExArgs {
   const int32_t* offsets;      // [E + 1]
   void* out;                   // y [R, N], dx by route [R, K], or dW [E, N, K]
   uint32_t* flags;
+  uint64_t wait_ns;            // limit of a wait (0: 2 s) and which one never ends: trellis_moe_experts_set_wait_test
+  int stall;
 };
 
 cudaError_t launch_ex_plan(const int32_t* ids, int R, int E, int32_t* order, int32_t* offsets, uint32_t* flags,

@@ -69,13 +69,20 @@ struct EtArgs {
   const int32_t *order, *offsets;
   void* out;
   uint32_t* flags;
+  uint64_t wait_ns;         // limit of a wait
+  int stall;                // test of the bounded waits: which one never ends (kEtStall*, or 0)
 };
 
 struct EtBars {
   uint64_t full[kEtMaxRing], empty[kEtMaxRing];    // the ring of the rows
   uint64_t wfull[kEtMaxRing], wempty[kEtMaxRing];  // that of the weights
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t never;                                  // nothing arrives here
 };
+
+// Which wait runs out in a test: the issuer's before its first MMA, an epilogue warp's for every
+// accumulator, that of the first or the last of the rows' warps before its first stage, the weights'.
+enum { kEtStallIssuer = 1, kEtStallEpilogue, kEtStallFirstRows, kEtStallLastRows, kEtStallWeights };
 
 // The groups of routes: where each begins; forward, grad_x: its first block; grad_w:
 // the experts in the order in which they are taken.
@@ -212,13 +219,14 @@ __device__ int et_loader(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
                          FastDiv tiles, FastDiv ctiles, volatile int* abort) {
   const bool lead = mx_elect();
   const uint32_t bar0 = smem_u32(&B.wfull[0]);
+  if (a.stall == kEtStallWeights && !mx_wait_warp(&B.never, 0, abort, a.wait_ns)) return 0;
   MxRing r;
   int it = 0;
   for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
     const EtUnit m = et_unit<MODE>(a, g, u, units, tiles, ctiles);
     const int stages = (m.depth + 63) / 64, halves = et_halves<MT>(a, m), c0 = m.tile * high;
     for (int s = 0; s < stages; ++s, ++it, r.next(ring)) {
-      if (it >= ring && !mx_wait_warp(&B.wempty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return it;
+      if (it >= ring && !mx_wait_warp(&B.wempty[r.slot], r.phase ^ 1, abort, a.wait_ns)) return it;
       const uint32_t st = base + (uint32_t)r.slot * (MT * kEtABytes), bar = bar0 + (uint32_t)r.slot * 8;
       if (lead && MODE == kExForward && MT == 1) {
         mx_expect(bar, high * 128);
@@ -262,12 +270,13 @@ struct EtRowPlan {
 struct EtWalk {
   EtBars& B;
   volatile int* abort;
+  uint64_t wait_ns;
   uint32_t base, stage_bytes;
   int ring, it;
   MxRing r;
   // waits for the stage's place; its shared address in `st`
   __device__ __forceinline__ bool next(uint32_t& st) {
-    if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, kMxWaitNs)) return false;
+    if (it >= ring && !mx_wait_warp(&B.empty[r.slot], r.phase ^ 1, abort, wait_ns)) return false;
     st = base + (uint32_t)r.slot * stage_bytes;
     return true;
   }
@@ -392,6 +401,7 @@ template <int MODE, int MT>
 __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t base, uint32_t wbase, EtRings rings, int units,
                          FastDiv tiles, FastDiv ctiles, uint32_t tmem, volatile int* abort) {
   const bool lead = mx_elect();
+  if (a.stall == kEtStallIssuer && !mx_wait_warp(&B.never, 0, abort, a.wait_ns)) return 0;
   MxRing r, rw;
   int it = 0, nu = 0;
   for (int round = 0, u; (u = et_turn<MODE>(g, round)) < units; ++round) {
@@ -399,15 +409,15 @@ __device__ int et_issuer(const EtArgs& a, const EtGroups& g, EtBars& B, uint32_t
     const int stages = (m.depth + 63) / 64;
     if (stages == 0) continue;
     const int buf = a.bufs == 2 ? nu & 1 : 0, turn = a.bufs == 2 ? nu >> 1 : nu;
-    if (turn >= 1 && !mx_wait_warp(&B.acc_empty[buf], (turn - 1) & 1, abort, kMxWaitNs)) return it;
+    if (turn >= 1 && !mx_wait_warp(&B.acc_empty[buf], (turn - 1) & 1, abort, a.wait_ns)) return it;
     ++nu;
     tc_fence_after();
     const uint32_t idesc = et_idesc<MODE>(a.bf16, et_up16(m.rows)), d = tmem + (uint32_t)(buf * MT * a.bn);
     const int halves = et_halves<MT>(a, m);
     for (int s = 0; s < stages; ++s, ++it, r.next(rings.rows), rw.next(rings.weights)) {
-      if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, kMxWaitNs)) return it;
+      if (!mx_wait_warp(&B.full[r.slot], r.phase, abort, a.wait_ns)) return it;
       if (EtRowPlan<MODE, MT>::kCopyWarps) fence_proxy_async();
-      if (MODE != kExGradW && !mx_wait_warp(&B.wfull[rw.slot], rw.phase, abort, kMxWaitNs)) return it;
+      if (MODE != kExGradW && !mx_wait_warp(&B.wfull[rw.slot], rw.phase, abort, a.wait_ns)) return it;
       const uint32_t st = base + (uint32_t)r.slot * rings.stage, wt = wbase + (uint32_t)rw.slot * (MT * kEtABytes);
       const int left = min(64, m.depth - s * 64), steps = (left + 15) / 16;
       if (MODE == kExGradW && (left & 15)) {
@@ -503,7 +513,8 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
     const bool some = m.depth > 0;
     const int buf = a.bufs == 2 ? nu & 1 : 0, turn = a.bufs == 2 ? nu >> 1 : nu, halves = et_halves<MT>(a, m);
     if (some) {
-      const bool full = mx_wait_warp(&B.acc_full[buf], turn & 1, abort, kMxWaitNs);
+      const bool test = a.stall == kEtStallEpilogue && warp == 0;
+      const bool full = mx_wait_warp(test ? &B.never : &B.acc_full[buf], test ? 0 : turn & 1, abort, a.wait_ns);
       // the warps of a part meet at its barrier while they store: they go on together or not at all
       if (!mx_vote_part(full, 1 + part)) break;
       ++nu;
@@ -606,6 +617,7 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], kEtEpiWarps);
     }
+    mbar_init(&bars.never, 1);
     sh.abort = 0;
     mbar_fence_init();
   }
@@ -662,11 +674,15 @@ __global__ void __launch_bounds__(kEtThreads, 1) k_ex_tc(const __grid_constant__
   if (warp < kEtEpiWarps)
     et_epilogue<MODE, MT, O>(a, groups, bars, units, shape.high, tiles, ctiles, tmem, store, abort);
   else if (warp < kEtEpiWarps + kEtRowWarps) {
-    const EtWalk walk{bars, abort, base, rings.stage, rings.rows, 0, MxRing()};
+    const EtWalk walk{bars, abort, a.wait_ns, base, rings.stage, rings.rows, 0, MxRing()};
     using Plan = EtRowPlan<MODE, MT>;
-    if (warp < kEtEpiWarps + Plan::kTmaWarps) rows_loaded = et_rows_tma<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
-    if constexpr (Plan::kCopyWarps > 0)
-      if (warp >= kEtEpiWarps + Plan::kTmaWarps) et_rows_copy<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
+    const bool test = (a.stall == kEtStallFirstRows && warp == kEtEpiWarps) ||
+                      (a.stall == kEtStallLastRows && warp == kEtEpiWarps + kEtRowWarps - 1);
+    if (!test || mx_wait_warp(&bars.never, 0, abort, a.wait_ns)) {
+      if (warp < kEtEpiWarps + Plan::kTmaWarps) rows_loaded = et_rows_tma<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
+      if constexpr (Plan::kCopyWarps > 0)
+        if (warp >= kEtEpiWarps + Plan::kTmaWarps) et_rows_copy<MODE, MT>(a, groups, walk, units, tiles, ctiles, topk);
+    }
   } else if (warp == kEtEpiWarps + kEtRowWarps) {
     if (MODE != kExGradW) loaded = et_loader<MODE, MT>(a, groups, bars, base + wofs, rings.weights, units, shape.high, tiles, ctiles, abort);
   } else
@@ -771,6 +787,7 @@ cudaError_t launch_ex_tc(const ExArgs& a, int sms, cudaStream_t st) {
   };
   t.E = a.E, t.R = R, t.bf16 = a.dtype == TM_BF16, t.per_route = a.per_route;
   t.order = a.order, t.offsets = a.offsets, t.out = a.out, t.flags = a.flags;
+  t.wait_ns = a.wait_ns ? a.wait_ns : kMxWaitNs, t.stall = a.stall;
   t.x = static_cast<const uint16_t*>(a.x), t.ldx = a.ldx;
   if (a.mode != kExGradX) {
     const cudaError_t e = et_map2(&t.xmap, a.dtype, a.x, a.K, a.per_route ? R : a.T, a.ldx);
