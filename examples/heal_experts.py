@@ -34,10 +34,13 @@ def rounded(w):
     return binding.mxfp4_dequantize(*binding.mxfp4_quantize(flat), w.shape[-1]).view_as(w)
 
 
-def layer(x, w, topk):
-    """Logits bf16 [T, V] and the routing; x bf16 [T, H], w as `weights` has them."""
+def layer(x, w, topk, plans=None):
+    """Logits bf16 [T, V] and the routing; x bf16 [T, H], w as `weights` has them. The
+    plan, whose error flags tell whether its products are right, goes to the list `plans`."""
     r = tuning.route(x.float() @ w["router"], topk)
     plan = binding.expert_plan(r.ids, w["up"].shape[0])
+    if plans is not None:
+        plans.append(plan)
     gate, up = tuning.experts(x, w["up"].to(BF16), plan).chunk(2, dim=1)
     z = torch.nn.functional.silu(gate) * up
     rows = tuning.experts(z, w["down"].to(BF16), plan, per_route=True)
@@ -57,12 +60,17 @@ def heal(steps=60, tokens=1024, E=16, H=256, I=128, V=8192, topk=2, n=32, seed=0
     for step in range(steps):
         x = torch.randn(tokens, H, generator=g, device="cuda").to(BF16)
         mask = torch.rand(tokens, generator=g, device="cuda") < 0.9  # (padding)
+        plans = []
         with torch.no_grad():
-            values, ids = torch.topk(layer(x, teacher, topk)[0], n, dim=1)
-        logits, r = layer(x, student, topk)
+            values, ids = torch.topk(layer(x, teacher, topk, plans)[0], n, dim=1)
+        logits, r = layer(x, student, topk, plans)
         loss = tuning.distill(logits, ids, values, mask=mask).sum() / mask.sum()
         optimizer.zero_grad()
         (loss + balance * r.losses[0]).backward()
+        for name, plan in zip(("teacher", "student"), plans):  # (of the products and their gradients; this waits for them)
+            flags = plan.poll_error()
+            if flags:
+                raise RuntimeError("device error flags 0x%x in the %s's products" % (flags, name))
         optimizer.step()
         history.append(float(loss.detach()))
         if step % 20 == 0 or step == steps - 1:

@@ -136,7 +136,9 @@ class _TokenLogprobs(torch.autograd.Function):
 
 
 def experts(x, w, plan: binding.ExpertPlan, per_route: bool = False):
-    """binding.experts_forward with a gradient through ``x`` and ``w``."""
+    """binding.experts_forward with a gradient through ``x`` and ``w``. Whether the
+    products and gradients are right is in the plan's error word: a training loop asks
+    ``plan.poll_error()``, which waits for the stream, after its backward pass."""
     return _Experts.apply(x, w, plan, per_route)
 
 
