@@ -368,7 +368,7 @@ __device__ __forceinline__ TlTeacherSum tl_teacher_sum(const TlArgs& a, long t, 
     const float lse = a.teacher_lse[t];
     return {0.0f, lse, expf(a.c.div(m) - lse) * s};
   }
-  return {m, logf(s), s * (1.0f / s)};  // (Q: 1, or NaN)
+  return {m, logf(s), s == s ? 1.0f : s};  // (Q: 1, or NaN)
 }
 
 __device__ __forceinline__ float tl_ln_q(const TlEntry& e, const TlTeacherSum& k, const TlScale& c) {
