@@ -315,9 +315,8 @@ cudaError_t ex_product(ExArgs a, cudaStream_t st) {
   a.wait_ns = ex_wait_test.wait_ns, a.stall = ex_wait_test.stall;
   if (a.T == 0)  // (grad_w of no tokens)
     return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * dtype_bytes(a.out_dtype), st);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t e = current_sms(sms);
   return e == cudaSuccess ? launch_ex_tc(a, sms, st) : e;
 }
 

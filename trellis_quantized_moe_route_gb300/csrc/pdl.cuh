@@ -29,6 +29,13 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// SMs of the current device.
+inline cudaError_t current_sms(int& sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
 // Lets `kern` have `bytes` of dynamic shared memory on the current device. (The
 // limit belongs to a device's copy of the kernel; `done`: one for each kernel.)
 template <typename... P>

@@ -1313,14 +1313,14 @@ cudaError_t tl_allow(OncePerDevice& done, void (*kern)(P...), int smem) {
 }
 
 template <typename T, int NT, int EPT, bool CLUSTER, int KIND>
-cudaError_t tl_forward_launch(TlArgs a, int ctas, cudaStream_t st) {
+cudaError_t tl_forward_launch(TlArgs a, int ctas, int sms, cudaStream_t st) {
   auto kern = k_tl_forward<T, NT, EPT, CLUSTER, KIND>;
   constexpr int smem = 2 * NT * kTlWords * 16, resident = NT == 256 ? 2 : NT == 128 ? 6 : 18;
   static OncePerDevice done;
   const cudaError_t e = tl_allow(done, kern, smem);
   if (e != cudaSuccess) return e;
   tl_shape(a, (int)sizeof(T), ctas, NT * kTlWords);
-  return tl_launch(kern, CLUSTER ? (long)a.T * ctas : std::min<long>(a.T, 152L * resident), ctas, NT, smem, a, st);
+  return tl_launch(kern, CLUSTER ? (long)a.T * ctas : std::min<long>(a.T, (long)sms * resident), ctas, NT, smem, a, st);
 }
 
 // Rows of up to 4 KB take a warp each (16384 x 1000 bf16: forward 34 us, with 128
@@ -1334,15 +1334,18 @@ bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256 &&
 // others a CTA of 128 threads, six of which share an SM.
 template <int KIND>
 cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = current_sms(sms);
+  if (e != cudaSuccess) return e;
   auto go = [&](auto elem) {
     using T = decltype(elem);
     const long words = tl_words(a, (int)sizeof(T));
     if (tl_short(a, words))
-      return tl_forward_launch<T, 32, 2, false, KIND>(a, 1, st);
+      return tl_forward_launch<T, 32, 2, false, KIND>(a, 1, sms, st);
     int ctas = 1;
-    while (ctas < kTlCtas && (long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512) ctas *= 2;
-    if (ctas > 1) return tl_forward_launch<T, 256, 1, true, KIND>(a, ctas, st);
-    return tl_forward_launch<T, 128, 2, false, KIND>(a, 1, st);
+    while (ctas < kTlCtas && (long)a.T * ctas <= sms && words / (2 * ctas) >= 512) ctas *= 2;
+    if (ctas > 1) return tl_forward_launch<T, 256, 1, true, KIND>(a, ctas, sms, st);
+    return tl_forward_launch<T, 128, 2, false, KIND>(a, 1, sms, st);
   };
   return TM_BY_DTYPE(dtype, go);
 }
@@ -1361,13 +1364,16 @@ cudaError_t tl_once_launch(TlArgs a, int ctas, cudaStream_t st) {
 }
 
 cudaError_t tl_once(const TlArgs& a, int dtype, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = current_sms(sms);
+  if (e != cudaSuccess) return e;
   auto go = [&](auto elem) {
     using T = decltype(elem);
     const long words = tl_words(a, (int)sizeof(T));
     if (tl_short(a, words)) return tl_once_launch<T, 32, 16, 2>(a, 1, st);
-    if (words <= 2048 && (long)a.T * 2 > 304) return tl_once_launch<T, 128, 16, 2>(a, 1, st);
+    if (words <= 2048 && a.T > sms) return tl_once_launch<T, 128, 16, 2>(a, 1, st);
     int ctas = 1;
-    while (ctas < kTlCtas && (words > (long)ctas * 4096 || ((long)a.T * ctas * 2 <= 304 && words / (2 * ctas) >= 512))) ctas *= 2;
+    while (ctas < kTlCtas && (words > (long)ctas * 4096 || ((long)a.T * ctas <= sms && words / (2 * ctas) >= 512))) ctas *= 2;
     return tl_once_launch<T, 256, 16, 1>(a, ctas, st);
   };
   return TM_BY_DTYPE(dtype, go);
