@@ -1330,8 +1330,23 @@ cudaError_t tl_forward_launch(TlArgs a, int ctas, int sms, cudaStream_t st) {
 // largest: 117 us, with 128 threads 123; 32 largest: 249 and 139).
 bool tl_short(const TlArgs& a, long words) { return a.n <= 64 && words <= 256 && a.top <= 24; }
 
-// Few rows take a cluster of large CTAs each, so that they still fill the SMs; the
-// others a CTA of 128 threads, six of which share an SM.
+// Few rows take a cluster of CTAs of 256 threads each, twice as many of them as long as all
+// clusters find a place at once: two CTAs an SM of clusters of two, three for two SMs of four, one
+// of eight. log probabilities of 131072 bf16 and 20000, us:
+//   16 rows   clusters of 8: 4.0, 3.4    of 4: 4.0, 2.9    (8 rows: 3.4, 3.1 and 4.0, 2.9; 16 x 200003: 5.5 and 6.0)
+//   38        of 8: 7.0, 6.0             of 4: 5.1, 3.5
+//   54        of 4: 5.2, 3.5             of 2: 5.7, 3.2    (54 x 200003: 8.1 and 8.9)
+//   76        of 4: 8.0, 5.6             of 2: 5.7, 3.2
+//   152       of 2: 8.3, 4.0             a row to a CTA of 128 threads: 11.2, 3.8
+//   153       of 2: 12.0, 6.5            128 threads: 14.1, 4.3    (153 x 50021: 8.8 and 7.6)
+//   304       of 2: 15.5, 7.9            128 threads: 14.5, 4.5
+// Loss and gradient in one pass: 38 rows of 32768 7.4 with eight and 5.6 with four, 76 7.3 with four and 5.9 with two.
+bool tl_more_ctas(const TlArgs& a, long words, int ctas, int sms) {
+  const int halves = ctas == 1 ? 4 : ctas == 2 ? 3 : 2;  // CTAs for two SMs
+  return 2L * ctas * a.T * 2 <= (long)sms * halves && words / (2 * ctas) >= 512;
+}
+
+// More rows: a CTA of 128 threads each, six of which share an SM.
 template <int KIND>
 cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
   int sms = 0;
@@ -1343,7 +1358,7 @@ cudaError_t tl_forward(const TlArgs& a, int dtype, cudaStream_t st) {
     if (tl_short(a, words))
       return tl_forward_launch<T, 32, 2, false, KIND>(a, 1, sms, st);
     int ctas = 1;
-    while (ctas < kTlCtas && (long)a.T * ctas <= sms && words / (2 * ctas) >= 512) ctas *= 2;
+    while (ctas < kTlCtas && tl_more_ctas(a, words, ctas, sms)) ctas *= 2;
     if (ctas > 1) return tl_forward_launch<T, 256, 1, true, KIND>(a, ctas, sms, st);
     return tl_forward_launch<T, 128, 2, false, KIND>(a, 1, sms, st);
   };
@@ -1373,7 +1388,7 @@ cudaError_t tl_once(const TlArgs& a, int dtype, cudaStream_t st) {
     if (tl_short(a, words)) return tl_once_launch<T, 32, 16, 2>(a, 1, st);
     if (words <= 2048 && a.T > sms) return tl_once_launch<T, 128, 16, 2>(a, 1, st);
     int ctas = 1;
-    while (ctas < kTlCtas && (words > (long)ctas * 4096 || ((long)a.T * ctas <= sms && words / (2 * ctas) >= 512))) ctas *= 2;
+    while (ctas < kTlCtas && (words > (long)ctas * 4096 || tl_more_ctas(a, words, ctas, sms))) ctas *= 2;
     return tl_once_launch<T, 256, 16, 1>(a, ctas, st);
   };
   return TM_BY_DTYPE(dtype, go);
