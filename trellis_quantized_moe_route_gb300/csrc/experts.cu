@@ -299,7 +299,9 @@ cudaError_t launch_ex_sum(const float* rows, int T, int topk, int K, void* out, 
     return launch_after(k_ex_sum<O, decltype(vec)::value>, dim3((unsigned)((total + 255) / 256)), 256, 0, st, rows,
                         (uint32_t)total, FastDiv(per), topk, K, static_cast<O*>(out));
   };
-  return TM_BY_DTYPE_VEC(dtype, eights(rows, K, K, 4) && eights(out, K, K, dtype_bytes(dtype)), go);
+  const bool vec = eights(rows, K, K, 4) && eights(out, K, K, 2);  // (dx is of 16 bits)
+  auto with = [&](auto elem) { return vec ? go(elem, std::true_type()) : go(elem, std::false_type()); };
+  return dtype == TM_BF16 ? with(__nv_bfloat16()) : with(__half());
 }
 
 namespace {
