@@ -529,62 +529,62 @@ __device__ void et_epilogue(const EtArgs& a, const EtGroups& g, EtBars& B, int u
       held = false;
     };
     for (int h = 0; h < halves; ++h) {
-    const uint32_t d = tmem + lane_base + (uint32_t)((buf * MT + h) * a.bn);
-    const int first = m.tile * high + h * 128, end = min(a.M, first + min(128, high)), n = first + quarter * 32 + lane;
-    const bool last = h == halves - 1;
-    if (MODE == kExGradW) {
-      constexpr int kCols = 128 / (int)sizeof(O);  // columns of 128 bytes
-      const int n0 = first + quarter * 32;
-      for (int c0 = part * kCols; c0 < m.rows; c0 += kEtEpiWarps / 4 * kCols) {
-        uint4 q[8];
-        O* e = reinterpret_cast<O*>(q);
-        if (some) {
+      const uint32_t d = tmem + lane_base + (uint32_t)((buf * MT + h) * a.bn);
+      const int first = m.tile * high + h * 128, end = min(a.M, first + min(128, high)), n = first + quarter * 32 + lane;
+      const bool last = h == halves - 1;
+      if (MODE == kExGradW) {
+        constexpr int kCols = 128 / (int)sizeof(O);  // columns of 128 bytes
+        const int n0 = first + quarter * 32;
+        for (int c0 = part * kCols; c0 < m.rows; c0 += kEtEpiWarps / 4 * kCols) {
+          uint4 q[8];
+          O* e = reinterpret_cast<O*>(q);
+          if (some) {
 #pragma unroll
-          for (int i = 0; i < kCols; i += 32) {
-            uint32_t v[32];
-            tmem_ld32(d + c0 + i, v);
-            tmem_ld_wait();
-            reg_fence32(v);
+            for (int i = 0; i < kCols; i += 32) {
+              uint32_t v[32];
+              tmem_ld32(d + c0 + i, v);
+              tmem_ld_wait();
+              reg_fence32(v);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) e[i + c] = from_f32<O>(__uint_as_float(v[c]));
+              for (int c = 0; c < 32; ++c) e[i + c] = from_f32<O>(__uint_as_float(v[c]));
+            }
+            if (last && c0 + kEtEpiWarps / 4 * kCols >= m.rows) release();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) q[c] = make_uint4(0, 0, 0, 0);
           }
-          if (last && c0 + kEtEpiWarps / 4 * kCols >= m.rows) release();
+          if (a.vec) {
+            et_store_tile(q, stage + warp * kEtStoreBytes, &a.map, m.col0 + c0, n0, m.expert, n0 < a.M);
+          } else {
+            et_store_elements<O>(q, stage + warp * kEtStoreBytes, out + ((size_t)m.expert * a.M + n0) * a.cols + m.col0 + c0, a.cols,
+                                 a.M - n0, m.rows - c0);
+          }
+          __syncwarp();  // (tcgen05.ld is for a converged warp)
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < (MODE == kExGradW ? 0 : kPieces); ++k) {
+        const int c0 = part * 32 + k * kStep;
+        if (c0 >= m.rows) break;
+        float y[32];
+        if (some) {
+          uint32_t v[32];
+          tmem_ld32(d + c0, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(v[c]);
+          if (last && c0 + kStep >= m.rows) release();
         } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) q[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 32; ++c) y[c] = 0.0f;
         }
-        if (a.vec) {
-          et_store_tile(q, stage + warp * kEtStoreBytes, &a.map, m.col0 + c0, n0, m.expert, n0 < a.M);
-        } else {
-          et_store_elements<O>(q, stage + warp * kEtStoreBytes, out + ((size_t)m.expert * a.M + n0) * a.cols + m.col0 + c0, a.cols,
-                               a.M - n0, m.rows - c0);
-        }
+        if (sizeof(O) == 2 && a.vec)
+          mx_store32_words<O>(y, out, row[k], m.rows - c0, first, end, a.M, stage + part * kEtStoreBytes, 1 + part);
+        else
+          mx_store32<O>(y, out, row[k], m.rows - c0, n < end ? n : a.M, a.M);
         __syncwarp();  // (tcgen05.ld is for a converged warp)
       }
-    }
-#pragma unroll
-    for (int k = 0; k < (MODE == kExGradW ? 0 : kPieces); ++k) {
-      const int c0 = part * 32 + k * kStep;
-      if (c0 >= m.rows) break;
-      float y[32];
-      if (some) {
-        uint32_t v[32];
-        tmem_ld32(d + c0, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(v[c]);
-        if (last && c0 + kStep >= m.rows) release();
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) y[c] = 0.0f;
-      }
-      if (sizeof(O) == 2 && a.vec)
-        mx_store32_words<O>(y, out, row[k], m.rows - c0, first, end, a.M, stage + part * kEtStoreBytes, 1 + part);
-      else
-        mx_store32<O>(y, out, row[k], m.rows - c0, n < end ? n : a.M, a.M);
-      __syncwarp();  // (tcgen05.ld is for a converged warp)
-    }
     }
     if (held) release();  // (it had no piece)
   }

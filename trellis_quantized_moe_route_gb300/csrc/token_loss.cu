@@ -38,8 +38,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // log2(e) / tau is c, rounded down, and lo > 0 (so that -inf times either is
 // -inf). The sums of the distillation's forward pass take both; those of the log
 // probabilities take c and are put right by the arguments' mean, which they have;
-// gradients take c (with both they took a tenth longer), which moves a p at
-// 2^-10 of the largest by 2^-21.
+// gradients take c (with both they took a tenth longer), which, c being off by
+// less than 2^-23 of it, moves a p at 2^-10 of the largest by up to 2^-20 of it.
 struct TlScale {
   float c, lo, rest;  // rest: lo / c
   float tau, inv;     // inv: 1 / tau, rounded
