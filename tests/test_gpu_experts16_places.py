@@ -40,3 +40,18 @@ def test_out_between_rows_and_over_them(binding):
     with pytest.raises(binding.TrellisMoEError, match="overlap"):
         binding.experts_forward(x, we, plan, per_route=True, out=apart.view(-1)[N * K - 8:N * K - 8 + R * N].view(R, N))
     assert plan.poll_error() == 0
+
+
+@pytest.mark.parametrize("N,K", [(64, 128), (33, 77)])
+def test_experts_row_by_row(binding, N, K):
+    """w stored as [N, E, K]: an expert's rows lie further apart than the experts do."""
+    T, E, k = 90, 5, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    randn = lambda *s: torch.randn(s, generator=g, device="cuda").half()  # noqa: E731
+    plan = binding.expert_plan(torch.randint(0, E, (T, k), generator=g, device="cuda").int(), E)
+    x, w, dy = randn(T, K), randn(E, N, K), randn(T * k, N)
+    rows = w.transpose(0, 1).contiguous().transpose(0, 1)
+    assert rows.stride(0) < rows.stride(1) and torch.equal(rows, w)
+    assert torch.equal(binding.experts_forward(x, rows, plan), binding.experts_forward(x, w, plan))
+    for a, b in zip(binding.experts_backward(x, rows, plan, dy), binding.experts_backward(x, w, plan, dy)):
+        assert torch.equal(a, b)
