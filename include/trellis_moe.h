@@ -498,7 +498,10 @@ void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
  *   dx_s = sum of W_e^T dy_r over the routes r that read row s
  *   dW_e = sum of dy_r x_s(r)^T over the expert's routes
  * Sums are in fp32 and in an order that depends on the arguments alone: equal
- * calls give equal bits. 1 <= E <= 256, 1 <= topk <= 32, T * topk <= 2^22,
+ * calls give equal bits. The tensor cores add sixteen products at a time to an
+ * accumulator that they truncate: a sum of D products is off by at most about D / 16
+ * steps of 2^-23 of its largest part, towards zero (5.6e-6 of the results' root mean
+ * square at D = 5120, where sums that round have 7e-7). 1 <= E <= 256, 1 <= topk <= 32, T * topk <= 2^22,
  * N and K <= 2^20.
  *
  * The plan: order [R] holds the R routes by expert, in ascending order within

@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(THREADS)
 // at an odd place) cannot be read by TMA; copies of them can. Eight elements come
 // as the one or two aligned words of 16 bytes that hold them, shifted into place.
 // Bound by memory: some 5.7 TB/s read and written. Products with their copies,
-// forward, dx, dW in us: 5120 routes of 64 experts, 2559 -> 641, 120, 149, 114 (aligned
-// 46, 67, 53; by mma.sync in tiles of 128, with the shifting in its loads, 429, 316, 398);
-// 8192 of 4 experts, 2049 -> 2047, 88, 119, 93 (592, 597, 562); 64 of 128 experts, 1025 ->
-// 1023, 77, 84, 118 (138, 139, 315).
+// forward, dx, dW in us: 5120 routes of 64 experts, 2559 -> 641, 112, 138, 112 (aligned
+// 42, 64, 50; by mma.sync in tiles of 128, with the shifting in its loads, 429, 316, 398);
+// 8192 of 4 experts, 2049 -> 2047, 89, 123 to 131, 94 (592, 597, 562); 64 of 128 experts, 1025 ->
+// 1023, 64 to 73, 67 to 77, 118 (138, 139, 315).
 constexpr int kAlignThreads = 256, kAlignWords = 4;  // of a thread
 
 struct ExAlignJob {

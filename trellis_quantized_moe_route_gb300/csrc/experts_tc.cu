@@ -16,16 +16,17 @@
 // the weights, one that issues the MMAs.
 //
 // Measured on one GB300, us (floor: each operand once at the memory's copy rate):
-//   160 experts 1536 -> 5120, 32768 routes   forward 476, dx 461, dW 655 (434 each). The
+//   160 experts 1536 -> 5120, 32768 routes   forward 466 to 476, dx 453 to 461, dW 640 to 655 (434 each). The
 //     products run at the memory's rate but for a last round of units (5%). dW is bound by
 //     what an SM exchanges with L2: for a tile of 256 x 256 and its 205 routes, 205 KB
 //     come at 42 bytes a cycle (by TMA or cp.async or both) and 131 KB leave at 26
 //     (also where dW stays in L2), some 5 us in all, and the two add up: half a tile
 //     filled while the other half is drained takes 667. Tiles of 128 x 256 need half as many rows
 //     again (876).
-//   128 experts 1024 -> 1024, 16384 routes, uneven   66, 88 with the tokens' sums, 82 (45)
-//   64 experts 2560 -> 640, 5120 routes   46, 67 with the sums, 53 (32)
-//   8 tokens x 8 of 128 experts, 1024 -> 1024   23 (bytes 15)
+//   128 experts 1024 -> 1024, 16384 routes, uneven   62 to 66, 84 to 88 with the tokens' sums, 76 to 82 (45)
+//   64 experts 2560 -> 640, 5120 routes   42 to 46, 64 to 67 with the sums, 50 to 53 (32)
+//   8 tokens x 8 of 128 experts, 1024 -> 1024   19 to 23 (bytes 15)
+//   (The first figure: ten calls in a CUDA graph.)
 // Measured and not kept: dW's stages of 32 routes with two store buffers a warp (708 us;
 // with 64 and room for two stages 742; two buffers of half the size 674), stores of dW from registers after exchanging
 // pieces between four lanes (734), the routes of dW's stages looked up two stages

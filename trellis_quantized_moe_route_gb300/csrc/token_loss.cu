@@ -15,9 +15,9 @@
 //     memory between the sums and the gradient. Rows that are longer than that go
 //     through it in tiles twice.
 //   k_tl_backward: one CTA for each piece of a row.
-// 4096 x 131072 bf16 (1.07 GB): log probabilities 157 us = 6.8 TB/s (five largest
-// 182, twenty 237), distillation forward 171, gradients 318 and 339 us = 6.8 and 6.3 TB/s,
-// loss and gradient in one pass 398 to 412 = 5.4 to 5.2. 8 rows: 6.3 us, with twenty largest 10.6.
+// 4096 x 131072 bf16 (1.07 GB): log probabilities 157 to 165 us = 6.8 to 6.5 TB/s (five largest
+// 182, twenty 237 to 242), distillation forward 172, gradients 314 and 334 to 342 us = 6.8 and 6.3 TB/s,
+// loss and gradient in one pass 413 = 5.2. 8 rows: 3.4 us, with twenty largest 8.3.
 #include <algorithm>
 #include <cmath>
 
@@ -1374,7 +1374,7 @@ cudaError_t tl_once_launch(TlArgs a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   tl_shape(a, (int)sizeof(T), ctas, NT * W);
   // (no more than the segment has: up to four CTAs share an SM, not three. 4096 rows of
-  // 20000: 90.5 -> 80 us, of 50021: 200 -> 182, of 131072, which fill it: 412 and 415)
+  // 20000: 90.5 -> 80 us, of 50021: 200 -> 182, of 131072, which fill it: 413)
   return tl_launch(kern, (long)a.T * ctas, ctas, NT, std::min(smem, a.seg * 16), a, st);
 }
 
