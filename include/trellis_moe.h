@@ -498,17 +498,18 @@ void trellis_moe_mxfp4_destroy(tm_mxfp4* h);
  *   dx_s = sum of W_e^T dy_r over the routes r that read row s
  *   dW_e = sum of dy_r x_s(r)^T over the expert's routes
  * Sums are in fp32 and in an order that depends on the arguments alone: equal
- * calls give equal bits. The tensor cores add sixteen products at a time to an
- * accumulator that they truncate: a sum of D products is off by at most about D / 16
- * steps of 2^-23 of its largest part, towards zero (5.6e-6 of the results' root mean
- * square at D = 5120, where sums that round have 7e-7). 1 <= E <= 256, 1 <= topk <= 32, T * topk <= 2^22,
- * N and K <= 2^20.
+ * calls give equal bits. The tensor cores add some sixteen products at a time to an
+ * accumulator that they truncate, each time by less than 2^-23 of it: results are
+ * off towards zero by 1.5e-6 of their root mean square for sums of 1536 products and
+ * 5.6e-6 for 5120 (fp32 sums that round: 3e-7 and 7e-7). 1 <= E <= 256,
+ * 1 <= topk <= 32, T * topk <= 2^22, N and K <= 2^20.
  *
  * The plan: order [R] holds the R routes by expert, in ascending order within
  * one, those whose id is outside 0..E-1 last; offsets [E + 1] where each group
  * begins. flags [1] is the error word, started anew: bit 0 is set if an id was
  * outside 0..E-1; the products set bit 1 if a pipeline wait gave up. Made once
- * for a routing, it serves any number of products. R = 0 is a plan of no routes. */
+ * for a routing, it serves any number of products. R = 0 is a plan of no routes. The
+ * four arrays must not overlap (TM_EINVAL). */
 tm_status trellis_moe_expert_plan(const int32_t* ids, int32_t R, int32_t E, int32_t* order, int32_t* offsets,
                                   uint32_t* flags, void* stream);
 
